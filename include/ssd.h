@@ -418,6 +418,128 @@ ssd_status ssd_complex_fwd(const ssd_complex_problem *prob, const void *x, const
                            float *y_imag, void *final_states, void *workspace, size_t workspace_bytes,
                            void *stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Selective scan: the state-space scan with a decay rate per channel and state, forward and
+ * backward (the scan above has one rate per head).  Per sequence, channel d of B/C group
+ * g = d / (channels / ngroups) and state n < dstate:
+ *
+ *   dt_t    = softplus(dt_raw_t[d] + dt_bias[d])
+ *   h_t[n]  = exp(dt_t * A[d][n]) * h_{t-1}[n] + dt_t * x_t[d] * B_t[g][n]
+ *   y_t[d]  = (sum_n C_t[g][n] * h_t[n] + D[d] * x_t[d]) * silu(z_t[d])      (gate only when z is given)
+ *
+ * It takes the scan's argument structs, with these layouts (element strides, outermost first,
+ * innermost stride 1; no alignment beyond the element's own is asked for):
+ *   x, z, y, dy, dx, dz : [batch, seqlen, channels]                  bf16 or f32
+ *   dt, ddt             : [batch, seqlen, channels]                  f32, or x's type; ddt as dt
+ *   B, C, dB, dC        : [batch, seqlen, ngroups, dstate]           x's type
+ *   A, dA               : [channels][dstate], contiguous             f32
+ *   D, dt_bias, dD, ddt_bias : [channels], contiguous                f32
+ *   initial/final/dinitial/dfinal states : [nstate][channels][dstate], contiguous, f32 or bf16
+ *                         each (nstate = batch, or nseqs with cu_seqlens), carried in f32
+ *   cu_seqlens          : int32 [nseqs + 1], device, batch 1, as above.  Its contents are not
+ *                         validated: bad ones give unspecified values, yet every access stays
+ *                         inside the tensors described here.
+ * A sequence without tokens has final state = initial state (zero without one), and passes
+ * dfinal on to dinitial.  dstate 1..128 (else SSD_ERR_UNSUPPORTED); all arithmetic in fp32.
+ *
+ * chunk_states (optional): a device buffer of ssd_selective_chunk_states_size bytes, 16-byte
+ * aligned, into which the forward writes the state entering every 32nd token of each sequence
+ * (f32, dstate padded to 16, 32, 64 or 128); the backward, given the same buffer, starts from
+ * them instead of running the forward again.  The forward needs no workspace.  Gradient
+ * reductions run in a fixed order (bitwise reproducible); D, z, dt_bias and initial_states may
+ * be absent, and then so is their gradient.
+ */
+typedef struct {
+    int64_t batch, seqlen, channels, ngroups, dstate, nseqs;   /* nseqs: packed sequences (cu_seqlens), else 0 */
+} ssd_selective_problem;
+
+ssd_status ssd_selective_chunk_states_size(const ssd_selective_problem *prob, size_t *bytes);
+ssd_status ssd_selective_fwd(const ssd_selective_problem *prob, const ssd_fwd_args *args, void *stream);
+/* Workspace: at least *bytes bytes of device memory, 256-byte aligned; contents need not be
+ * initialised.  Its size depends on whether args->fwd.chunk_states is given. */
+ssd_status ssd_selective_bwd_workspace_size(const ssd_selective_problem *prob, const ssd_bwd_args *args, size_t *bytes);
+ssd_status ssd_selective_bwd(const ssd_selective_problem *prob, const ssd_bwd_args *args, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Decoding: one token for each of `batch` requests whose states lie in a pool.
+ *
+ * ssd_step          the scan at the top of this file, one token: state [nslots][nheads][headdim]
+ *                   [dstate], A, D, dt_bias f32 [nheads], dt f32 [batch][nheads]
+ * ssd_selective_step  the selective scan, one token: nheads = channels, headdim = 1, state
+ *                   [nslots][channels][dstate], A f32 [channels][dstate], D, dt_bias f32
+ *                   [channels], dt [batch][channels] f32 or x's type
+ * x, z, y [batch][nheads * headdim] and B, C [batch][ngroups * dstate] of `dtype`, rows
+ * contiguous at the given element strides; D, z, dt_bias may be NULL.  Request i's state is slot
+ * state_indices[i] (int32, device; NULL: slot i), updated in place; slots lie slot_stride
+ * elements apart, each contiguous.  A request whose slot is outside [0, nslots) is padding:
+ * its y is zero and no state is touched.  The slots of one call must differ (two requests on one
+ * slot would race).  state_dtype f32 or bf16 is a storage type: the step computes in fp32
+ * and y is read out of the state before it is rounded.  dstate 1..256, else SSD_ERR_UNSUPPORTED.
+ */
+typedef struct {
+    int64_t batch, nslots, nheads, headdim, ngroups, dstate;
+    int64_t slot_stride, x_stride, dt_stride, z_stride, b_stride, c_stride, y_stride;
+    int32_t dtype, dt_dtype, state_dtype, reserved;            /* ssd_dtype; reserved must be 0 */
+} ssd_step_problem;
+
+ssd_status ssd_step(const ssd_step_problem *prob, void *state, const int32_t *state_indices, const void *x,
+                    const void *dt, const float *A, const void *B, const void *C, const float *D, const void *z,
+                    const float *dt_bias, void *y, void *stream);
+ssd_status ssd_selective_step(const ssd_step_problem *prob, void *state, const int32_t *state_indices, const void *x,
+                              const void *dt, const float *A, const void *B, const void *C, const float *D,
+                              const void *z, const float *dt_bias, void *y, void *stream);
+
+/*
+ * The causal convolution with a carried window: ssd_conv1d_fwd whose sequences go on from the last
+ * width - 1 inputs of their last call instead of from zero.  conv_states [nslots][width - 1]
+ * [channels] of the problem's dtype, oldest row first, each slot contiguous at slot_stride
+ * elements, holds them; sequence s (a batch row, or a packed sequence of cu_seqlens) reads slot
+ * state_indices[s] (NULL: slot s) as the rows before its first token and leaves its own last
+ * width - 1 rows there (a shorter sequence shifts the old ones).  has_initial (uint8 per
+ * sequence, device; NULL: all 1): where it is 0 the sequence starts from zeros and the slot's old
+ * contents are not read.  A slot outside [0, nslots) is padding: the sequence starts from
+ * zeros and leaves nothing.  The slots of one call must differ.  Other arguments and rules as
+ * ssd_conv1d_fwd's, and conv_states 16-byte aligned with slot_stride a multiple of 8; a
+ * sequence without tokens leaves its window as it is (zeros where has_initial is 0).
+ * ssd_conv1d_step is the same for one token per request: prob->batch requests, seqlen 1, u and
+ * out [batch][channels] at the given row strides; a padding request's window counts as zeros.
+ */
+ssd_status ssd_conv1d_prompt(const ssd_conv_problem *prob, const void *u, int64_t u_batch_stride,
+                             int64_t u_token_stride, const float *weight, const float *bias,
+                             const int32_t *cu_seqlens, void *conv_states, int64_t nslots, int64_t slot_stride,
+                             const int32_t *state_indices, const uint8_t *has_initial, void *out,
+                             int64_t out_batch_stride, int64_t out_token_stride, void *stream);
+ssd_status ssd_conv1d_step(const ssd_conv_problem *prob, const void *u, int64_t u_stride, const float *weight,
+                           const float *bias, void *conv_states, int64_t nslots, int64_t slot_stride,
+                           const int32_t *state_indices, void *out, int64_t out_stride, void *stream);
+
+/*
+ * State snapshots in 8 bits: `count` states of a pool put aside and taken up again (a prefix that
+ * requests share, a request that is preempted).  A state is `rows` rows of `dstate` values; a row
+ * is kept as int8 values and one f32 scale:
+ *
+ *   m = max_n |h[n]|,  q[n] = round_half_even(h[n] * (127 / m)),  scale = m / 127      (store)
+ *   h[n] = q[n] * scale                                                                (load)
+ *
+ * so a value is off by half a scale at most.  A row with m < 1e-30 is kept as zeros with scale 0;
+ * one that holds an infinity or a NaN is kept as zeros with scale NaN, and reads back as NaN.
+ * states [nslots][rows][dstate] f32 or bf16 at slot stride state_stride (rows contiguous);
+ * snapshots int8 [nsnapshots][rows][dstate] and scales f32 [nsnapshots][rows], contiguous.
+ * State state_indices[i] (NULL: i) goes to, or comes from, snapshot slots[i] (NULL: i); a pair
+ * with either index out of range is skipped.  Destinations of one call must differ.
+ * dstate 1..1024, else SSD_ERR_UNSUPPORTED.
+ */
+typedef struct {
+    int64_t count, rows, dstate, nslots, nsnapshots, state_stride;
+    int32_t state_dtype, reserved;                             /* ssd_dtype; reserved must be 0 */
+} ssd_snapshot_problem;
+
+ssd_status ssd_snapshot_store(const ssd_snapshot_problem *prob, const void *states, const int32_t *state_indices,
+                              int8_t *snapshots, float *scales, const int32_t *slots, void *stream);
+ssd_status ssd_snapshot_load(const ssd_snapshot_problem *prob, const int8_t *snapshots, const float *scales,
+                             const int32_t *slots, void *states, const int32_t *state_indices, void *stream);
+
 /*
  * ssd_fwd_debug_layout
  * Byte offsets, inside an ssd_fwd workspace, of the intermediates the STAGED

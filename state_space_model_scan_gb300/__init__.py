@@ -7,3 +7,5 @@ build script (``build``).  Importing the package does not load the library; the
 first call does, and raises if it has not been built.
 """
 from .api import ssd_forward, ssd_backward, Workspace  # noqa: F401
+from .api import (selective_scan_forward, selective_scan_backward, SelectiveScanFunction, ssd_step,  # noqa: F401
+                  selective_scan_step, conv1d_prompt, conv1d_step, snapshot_store, snapshot_load)

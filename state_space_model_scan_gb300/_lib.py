@@ -25,7 +25,10 @@ EXPORTS = ["ssd_fwd_workspace_size", "ssd_fwd", "ssd_bwd_workspace_size", "ssd_b
            "ssd_selftest_bounded_wait", "ssd_chunk_states_size", "ssd_noalloc_query_status", "ssd_varlen_metadata",
            "ssd_gated_norm_fwd", "ssd_gated_norm_bwd_workspace_size", "ssd_gated_norm_bwd",
            "ssd_conv1d_fwd", "ssd_conv1d_bwd_workspace_size", "ssd_conv1d_bwd",
-           "ssd_complex_fwd_workspace_size", "ssd_complex_fwd"]
+           "ssd_complex_fwd_workspace_size", "ssd_complex_fwd",
+           "ssd_selective_chunk_states_size", "ssd_selective_fwd", "ssd_selective_bwd_workspace_size",
+           "ssd_selective_bwd", "ssd_step", "ssd_selective_step", "ssd_conv1d_prompt", "ssd_conv1d_step",
+           "ssd_snapshot_store", "ssd_snapshot_load"]
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -77,6 +80,22 @@ class ComplexProblem(ctypes.Structure):
                 ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64), ("chunk_size", ctypes.c_int64)]
 
 
+class SelectiveProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "channels", "ngroups", "dstate", "nseqs")]
+
+
+class StepProblem(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("batch", "nslots", "nheads", "headdim", "ngroups", "dstate",
+                                               "slot_stride", "x_stride", "dt_stride", "z_stride", "b_stride",
+                                               "c_stride", "y_stride")] +
+                [(n, ctypes.c_int32) for n in ("dtype", "dt_dtype", "state_dtype", "reserved")])
+
+
+class SnapshotProblem(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("count", "rows", "dstate", "nslots", "nsnapshots", "state_stride")] +
+                [("state_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)])
+
+
 class DebugLayout(ctypes.Structure):
     _fields_ = [("meta_counts", ctypes.c_int64), ("chunk_info", ctypes.c_int64), ("dt", ctypes.c_int64),
                 ("cs", ctypes.c_int64), ("states", ctypes.c_int64), ("units", ctypes.c_int64),
@@ -122,12 +141,23 @@ def load(path: str = LIB_PATH):
                                    ctypes.c_size_t, V]
     lib.ssd_complex_fwd_workspace_size.argtypes = [P(ComplexProblem), P(ctypes.c_size_t)]
     lib.ssd_complex_fwd.argtypes = [P(ComplexProblem), V, V, V, V, V, V, V, V, V, V, ctypes.c_size_t, V]
+    S = ctypes.c_size_t
+    lib.ssd_selective_chunk_states_size.argtypes = [P(SelectiveProblem), P(S)]
+    lib.ssd_selective_fwd.argtypes = [P(SelectiveProblem), P(FwdArgs), V]
+    lib.ssd_selective_bwd_workspace_size.argtypes = [P(SelectiveProblem), P(BwdArgs), P(S)]
+    lib.ssd_selective_bwd.argtypes = [P(SelectiveProblem), P(BwdArgs), V, S, V]
+    lib.ssd_step.argtypes = lib.ssd_selective_step.argtypes = [P(StepProblem)] + [V] * 12
+    lib.ssd_conv1d_prompt.argtypes = [P(ConvProblem), V, I64, I64, V, V, V, V, I64, I64, V, V, V, I64, I64, V]
+    lib.ssd_conv1d_step.argtypes = [P(ConvProblem), V, I64, V, V, V, I64, I64, V, V, I64, V]
+    lib.ssd_snapshot_store.argtypes = lib.ssd_snapshot_load.argtypes = [P(SnapshotProblem)] + [V] * 6
     for f in ("ssd_fwd_workspace_size", "ssd_fwd", "ssd_bwd_workspace_size", "ssd_bwd", "ssd_query_status",
               "ssd_fwd_debug_layout", "ssd_fwd_noalloc", "ssd_selftest_bounded_wait", "ssd_chunk_states_size",
               "ssd_noalloc_query_status", "ssd_varlen_metadata", "ssd_gated_norm_fwd",
               "ssd_gated_norm_bwd_workspace_size", "ssd_gated_norm_bwd", "ssd_conv1d_fwd",
               "ssd_conv1d_bwd_workspace_size", "ssd_conv1d_bwd", "ssd_complex_fwd_workspace_size",
-              "ssd_complex_fwd"):
+              "ssd_complex_fwd", "ssd_selective_chunk_states_size", "ssd_selective_fwd",
+              "ssd_selective_bwd_workspace_size", "ssd_selective_bwd", "ssd_step", "ssd_selective_step",
+              "ssd_conv1d_prompt", "ssd_conv1d_step", "ssd_snapshot_store", "ssd_snapshot_load"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -360,3 +390,60 @@ def complex_fwd(prob, x, dt, A, B, C, init, y_re, y_im, final, workspace, stream
                                       _ptr(y_re), _ptr(y_im), _ptr(final), _ptr(workspace),
                                       ctypes.c_size_t(workspace.numel() * workspace.element_size()),
                                       _stream_handle(stream)))
+
+
+# The entry points of decoding take addresses as plain integers: a call's own time is mostly this binding's.
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def selective_chunk_states_size(prob):
+    n = ctypes.c_size_t(0)
+    check(load().ssd_selective_chunk_states_size(ctypes.byref(prob), ctypes.byref(n)), "ssd_selective_chunk_states_size")
+    return int(n.value)
+
+
+def selective_fwd(prob, args, stream=None):
+    return int(load().ssd_selective_fwd(ctypes.byref(prob), ctypes.byref(args), _raw_stream(stream)))
+
+
+def selective_bwd_workspace_size(prob, args):
+    n = ctypes.c_size_t(0)
+    check(load().ssd_selective_bwd_workspace_size(ctypes.byref(prob), ctypes.byref(args), ctypes.byref(n)),
+          "ssd_selective_bwd_workspace_size")
+    return int(n.value)
+
+
+def selective_bwd(prob, args, workspace, stream=None):
+    return int(load().ssd_selective_bwd(ctypes.byref(prob), ctypes.byref(args), workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), _raw_stream(stream)))
+
+
+def step(selective, prob, state, idx, x, dt, A, B, C, D, z, dt_bias, y, stream=None):
+    f = load().ssd_selective_step if selective else load().ssd_step
+    return f(prob, state.data_ptr(), _addr(idx), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
+             _addr(D), _addr(z), _addr(dt_bias), y.data_ptr(), _raw_stream(stream))
+
+
+def conv1d_prompt(prob, u, weight, bias, cu_seqlens, states, idx, has, out, stream=None):
+    return load().ssd_conv1d_prompt(prob, u.data_ptr(), u.stride(0), u.stride(1), weight.data_ptr(), _addr(bias),
+                                    _addr(cu_seqlens), states.data_ptr(), states.shape[0], states.stride(0), _addr(idx),
+                                    _addr(has), out.data_ptr(), out.stride(0), out.stride(1), _raw_stream(stream))
+
+
+def conv1d_step(prob, u, weight, bias, states, idx, out, stream=None):
+    return load().ssd_conv1d_step(prob, u.data_ptr(), u.stride(0), weight.data_ptr(), _addr(bias), states.data_ptr(),
+                                  states.shape[0], states.stride(0), _addr(idx), out.data_ptr(), out.stride(0),
+                                  _raw_stream(stream))
+
+
+def snapshot(store, prob, states, idx, q, scales, slots, stream=None):
+    if store:
+        return load().ssd_snapshot_store(prob, states.data_ptr(), _addr(idx), q.data_ptr(), scales.data_ptr(),
+                                         _addr(slots), _raw_stream(stream))
+    return load().ssd_snapshot_load(prob, q.data_ptr(), scales.data_ptr(), _addr(slots), states.data_ptr(), _addr(idx),
+                                    _raw_stream(stream))

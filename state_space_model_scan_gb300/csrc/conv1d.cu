@@ -64,6 +64,11 @@ struct ConvArgs {
     int64_t so_b, so_l, sdu_b, sdu_l;
     float *partials;              // [tiles][Cn][K + 1]: dw shares, then the dbias share
     int64_t tiles_per_row;
+    // carried windows: [nslots][K - 1][Cn] at slot stride sw, slot[s] of sequence s (or s), fresh where has[s] is 0
+    void *win;
+    int64_t nslots, sw;
+    const int32_t *slot;
+    const uint8_t *has;
 };
 
 // Sequence bookkeeping along a sweep: the start of the current token's sequence and the
@@ -220,7 +225,58 @@ __device__ __forceinline__ void stage_taps(const float *w, const float *bias, in
         ws[K * CB + c] = (bias != nullptr && c < nch) ? bias[cbase + c] : 0.f;
 }
 
-template <typename T, int K, int W>   // W channels per thread (8: 256 threads, 4: 512 threads)
+// The carried window of sequence s (its rows are K - 1 back to 1 before the first token), or NULL for padding.
+template <typename T>
+__device__ __forceinline__ T *window(const ConvArgs &a, int64_t s, int K) {
+    const int64_t k = a.slot ? a.slot[s] : s;
+    if (K == 1 || k < 0 || k >= a.nslots) return nullptr;
+    return static_cast<T *>(a.win) + k * a.sw;
+}
+
+// With carried windows, a sequence's first K - 1 outputs and its new window come from the same
+// thread, which reads the old window before it writes (other blocks never touch windows): thread
+// (piece j, group) takes 8 channels of one sequence.
+template <typename T, int K>
+__device__ void conv_edge(const ConvArgs &a, int64_t s, int64_t c0, const float *ws, int j) {
+    const int64_t b = a.cu ? 0 : s;
+    const int64_t t0 = a.cu ? min(max((int64_t)a.cu[s], (int64_t)0), a.L) : 0;
+    const int64_t t1 = a.cu ? min(max((int64_t)a.cu[s + 1], t0), a.L) : a.L;
+    T *win = window<T>(a, s, K);
+    const bool old = win != nullptr && (a.has == nullptr || a.has[s] != 0);
+    const T *u = static_cast<const T *>(a.u) + b * a.su_b + c0;
+    T *o = static_cast<T *>(a.out) + b * a.so_b + c0;
+    const int n = (int)min(t1 - t0, (int64_t)(K - 1));
+    for (int i = 0; i < n; ++i) {
+        float acc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = ws[K * CB + 8 * j + e];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int r = i + k - (K - 1);   // row of tap k from the first token; below 0: in the window
+            if (r < 0 && !old) continue;
+            float v[8];
+            ld8(r < 0 ? win + (K - 1 + r) * a.Cn + c0 : u + (t0 + r) * a.su_l, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(ws[k * CB + 8 * j + e], v[e], acc[e]);
+        }
+        if (a.silu) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] *= sig_t<T>(acc[e]);
+        }
+        st8(o + (t0 + i) * a.so_l, acc);
+    }
+    if (win == nullptr) return;
+    for (int k = 0; k < K - 1; ++k) {   // new row k is K - 1 - k before the end: a token, or old row n + k >= k
+        const int64_t t = t1 - (K - 1) + k;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (t >= t0) ld8(u + t * a.su_l, v);
+        else if (old) ld8(win + (n + k) * a.Cn + c0, v);
+        st8(win + k * a.Cn + c0, v);
+    }
+}
+
+// CARRY: sequences go on from carried windows; blocks past the token tiles do their edges.
+template <typename T, int K, int W, bool CARRY>   // W channels per thread (8: 256 threads, 4: 512 threads)
 __global__ void __launch_bounds__(CT * 8 / W, 4)   // four blocks per SM (64 registers) measured 2-3% faster than three
 k_conv_fwd(const ConvArgs a) {
     constexpr int NPC = CB / W;        // channel pieces per row
@@ -232,6 +288,16 @@ k_conv_fwd(const ConvArgs a) {
     const int64_t b = blockIdx.x / a.tiles_per_row, t0 = (blockIdx.x % a.tiles_per_row) * TT;
     const int64_t tb = t0 - (K - 1);
     stage_taps<K>(a.w, a.bias, cbase, a.Cn, ws);
+    if (CARRY) {
+        static_assert(!CARRY || W == 8, "conv_edge takes 8 channels a thread");
+        const int64_t tiles = a.B * a.tiles_per_row;
+        if (blockIdx.x >= tiles) {
+            __syncthreads();
+            const int64_t s = (blockIdx.x - tiles) * (CT / 32) + grp, ns = a.cu ? a.S : a.B;
+            if (s < ns && c0 < a.Cn) conv_edge<T, K>(a, s, c0, ws, j);
+            return;
+        }
+    }
     stage_rows(static_cast<const T *>(a.u) + b * a.su_b, a.su_l, tb, TT + K - 1, a.L, cbase, a.Cn, tile);
     __syncthreads();
     if (c0 >= a.Cn) return;
@@ -277,6 +343,7 @@ k_conv_fwd(const ConvArgs a) {
     }
     for (int64_t t = s0; t < s1; ++t) {
         cur.advance(a, t);
+        if (CARRY && t - (K - 1) < cur.start) continue;   // conv_edge's
         float acc[W];
 #pragma unroll
         for (int e = 0; e < W; ++e) acc[e] = bias[e];
@@ -538,6 +605,49 @@ __global__ void __launch_bounds__(256) k_conv_dw(const float *partials, int64_t 
     }
 }
 
+// One token for each of a batch of requests: thread (request, 8 channels) reads the window's K - 1
+// rows and the new one, and writes the window one row on.
+template <typename T, int K>
+__global__ void __launch_bounds__(128) k_conv_step(const ConvArgs a) {
+    const int64_t c0 = ((int64_t)blockIdx.x * 128 + threadIdx.x) * 8, b = blockIdx.y;
+    if (c0 >= a.Cn) return;
+    T *win = window<T>(a, b, K);
+    float rows[K][8], w[8 * K];
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) {
+        if (win) ld8(win + k * a.Cn + c0, rows[k]);
+        else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) rows[k][e] = 0.f;
+        }
+    }
+    ld8(static_cast<const T *>(a.u) + b * a.su_b + c0, rows[K - 1]);
+    const float *wp = a.w + c0 * K;   // the 8 channels' taps are contiguous
+    if ((uintptr_t)a.w % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < 2 * K; ++i) {
+            const float4 v = reinterpret_cast<const float4 *>(wp)[i];
+            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8 * K; ++i) w[i] = wp[i];
+    }
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        acc[e] = a.bias ? a.bias[c0 + e] : 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) acc[e] = fmaf(w[e * K + k], rows[k][e], acc[e]);
+        if (a.silu) acc[e] *= sig_t<T>(acc[e]);
+    }
+    st8(static_cast<T *>(a.out) + b * a.so_b + c0, acc);
+    if (win) {
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) st8(win + k * a.Cn + c0, rows[k + 1]);
+    }
+}
+
 template <typename T, int K>
 size_t fwd_smem() { return TAPS_BYTES(K) + (size_t)(TT + K - 1) * 256 * sizeof(T); }
 template <typename T, int K>
@@ -547,13 +657,13 @@ size_t bwd_smem() {
     return TAPS_BYTES(K) + (stage > red ? stage : red);
 }
 constexpr int kFwdW = CONV_FWD_W;   // channels per thread of the forward sweep
-template <typename T, int K>
+template <typename T, int K, bool CARRY>
 cudaError_t launch_fwd_k(const ConvArgs &a, dim3 grid, cudaStream_t st) {
     static int attr[64] = {0};
     const size_t sm = fwd_smem<T, K>();
-    cudaError_t e = ensure_smem_attr(k_conv_fwd<T, K, kFwdW>, (int)sm, attr);
+    cudaError_t e = ensure_smem_attr(k_conv_fwd<T, K, kFwdW, CARRY>, (int)sm, attr);
     if (e != cudaSuccess) return e;
-    k_conv_fwd<T, K, kFwdW><<<grid, CT * 8 / kFwdW, sm, st>>>(a);
+    k_conv_fwd<T, K, kFwdW, CARRY><<<grid, CT * 8 / kFwdW, sm, st>>>(a);
     return cudaGetLastError();
 }
 constexpr int kBwdW = CONV_BWD_W;   // channels per thread of the backward sweep
@@ -567,17 +677,17 @@ cudaError_t launch_bwd_k(const ConvArgs &a, dim3 grid, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, bool CARRY>
 cudaError_t launch_fwd(const ConvArgs &a, dim3 grid, cudaStream_t st) {
     switch (a.K) {
-        case 1: return launch_fwd_k<T, 1>(a, grid, st);
-        case 2: return launch_fwd_k<T, 2>(a, grid, st);
-        case 3: return launch_fwd_k<T, 3>(a, grid, st);
-        case 4: return launch_fwd_k<T, 4>(a, grid, st);
-        case 5: return launch_fwd_k<T, 5>(a, grid, st);
-        case 6: return launch_fwd_k<T, 6>(a, grid, st);
-        case 7: return launch_fwd_k<T, 7>(a, grid, st);
-        default: return launch_fwd_k<T, 8>(a, grid, st);
+        case 1: return launch_fwd_k<T, 1, CARRY>(a, grid, st);
+        case 2: return launch_fwd_k<T, 2, CARRY>(a, grid, st);
+        case 3: return launch_fwd_k<T, 3, CARRY>(a, grid, st);
+        case 4: return launch_fwd_k<T, 4, CARRY>(a, grid, st);
+        case 5: return launch_fwd_k<T, 5, CARRY>(a, grid, st);
+        case 6: return launch_fwd_k<T, 6, CARRY>(a, grid, st);
+        case 7: return launch_fwd_k<T, 7, CARRY>(a, grid, st);
+        default: return launch_fwd_k<T, 8, CARRY>(a, grid, st);
     }
 }
 template <typename T>
@@ -592,6 +702,22 @@ cudaError_t launch_bwd(const ConvArgs &a, dim3 grid, cudaStream_t st) {
         case 7: return launch_bwd_k<T, 7>(a, grid, st);
         default: return launch_bwd_k<T, 8>(a, grid, st);
     }
+}
+
+template <typename T>
+cudaError_t launch_step(const ConvArgs &a, cudaStream_t st) {
+    const dim3 grid((unsigned)((a.Cn / 8 + 127) / 128), (unsigned)a.B);
+    switch (a.K) {
+        case 1: k_conv_step<T, 1><<<grid, 128, 0, st>>>(a); break;
+        case 2: k_conv_step<T, 2><<<grid, 128, 0, st>>>(a); break;
+        case 3: k_conv_step<T, 3><<<grid, 128, 0, st>>>(a); break;
+        case 4: k_conv_step<T, 4><<<grid, 128, 0, st>>>(a); break;
+        case 5: k_conv_step<T, 5><<<grid, 128, 0, st>>>(a); break;
+        case 6: k_conv_step<T, 6><<<grid, 128, 0, st>>>(a); break;
+        case 7: k_conv_step<T, 7><<<grid, 128, 0, st>>>(a); break;
+        default: k_conv_step<T, 8><<<grid, 128, 0, st>>>(a);
+    }
+    return cudaGetLastError();
 }
 
 bool al16(const void *p) { return ((uintptr_t)p) % 16 == 0; }
@@ -616,6 +742,14 @@ ssd_status check_tok(const ssd_conv_problem *p, const void *t, int64_t sb, int64
     if (sl < p->channels || (p->batch > 1 && sb < sl * p->seqlen)) return SSD_ERR_INVALID_ARGUMENT;
     if (!al16(t) || sl % 8 != 0 || sb % 8 != 0) return SSD_ERR_MISALIGNED;
     return SSD_OK;
+}
+
+ssd_status check_win(const ssd_conv_problem *p, const void *win, int64_t nslots, int64_t stride, const int32_t *slot) {
+    if (nslots < 0) return SSD_ERR_INVALID_ARGUMENT;
+    if ((uintptr_t)slot % 4 != 0) return SSD_ERR_MISALIGNED;
+    if (nslots == 0 || p->width == 1) return SSD_OK;
+    if (win == nullptr || (nslots > 1 && stride < (p->width - 1) * p->channels)) return SSD_ERR_INVALID_ARGUMENT;
+    return al16(win) && (nslots == 1 || stride % 8 == 0) ? SSD_OK : SSD_ERR_MISALIGNED;
 }
 
 #define CONV_TRY(expr)                 \
@@ -652,7 +786,45 @@ ssd_status ssd_conv1d_fwd(const ssd_conv_problem *p, const void *x, int64_t x_sb
     a.u = x; a.su_b = x_sb; a.su_l = x_sl; a.out = out; a.so_b = out_sb; a.so_l = out_sl;
     const dim3 grid((unsigned)(a.B * a.tiles_per_row), (unsigned)((a.Cn + CB - 1) / CB));
     cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = p->dtype == SSD_BF16 ? launch_fwd<__nv_bfloat16>(a, grid, st) : launch_fwd<float>(a, grid, st);
+    const cudaError_t e = p->dtype == SSD_BF16 ? launch_fwd<__nv_bfloat16, false>(a, grid, st) : launch_fwd<float, false>(a, grid, st);
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+ssd_status ssd_conv1d_prompt(const ssd_conv_problem *p, const void *x, int64_t x_sb, int64_t x_sl, const float *weight,
+                             const float *bias, const int32_t *cu_seqlens, void *conv_states, int64_t nslots,
+                             int64_t slot_stride, const int32_t *state_indices, const uint8_t *has_initial, void *out,
+                             int64_t out_sb, int64_t out_sl, void *stream) {
+    CONV_TRY(check_conv(p, cu_seqlens != nullptr));
+    CONV_TRY(check_tok(p, x, x_sb, x_sl));
+    CONV_TRY(check_tok(p, out, out_sb, out_sl));
+    if (weight == nullptr) return SSD_ERR_INVALID_ARGUMENT;
+    CONV_TRY(check_win(p, conv_states, nslots, slot_stride, state_indices));
+    ConvArgs a = make_args(p, weight, bias, cu_seqlens);
+    a.u = x; a.su_b = x_sb; a.su_l = x_sl; a.out = out; a.so_b = out_sb; a.so_l = out_sl;
+    a.win = conv_states; a.nslots = nslots; a.sw = slot_stride; a.slot = state_indices; a.has = has_initial;
+    const int64_t ns = cu_seqlens ? a.S : a.B, blocks = a.B * a.tiles_per_row + (ns + CT / 32 - 1) / (CT / 32);
+    if (blocks > ((int64_t)1 << 31) - 1) return SSD_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)blocks, (unsigned)((a.Cn + CB - 1) / CB));
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = p->dtype == SSD_BF16 ? launch_fwd<__nv_bfloat16, true>(a, grid, st) : launch_fwd<float, true>(a, grid, st);
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+ssd_status ssd_conv1d_step(const ssd_conv_problem *p, const void *x, int64_t x_stride, const float *weight,
+                           const float *bias, void *conv_states, int64_t nslots, int64_t slot_stride,
+                           const int32_t *state_indices, void *out, int64_t out_stride, void *stream) {
+    CONV_TRY(check_conv(p, false));
+    if (p->seqlen != 1) return SSD_ERR_INVALID_ARGUMENT;
+    if (p->batch > 65535) return SSD_ERR_UNSUPPORTED;
+    CONV_TRY(check_tok(p, x, x_stride, p->channels));
+    CONV_TRY(check_tok(p, out, out_stride, p->channels));
+    if (weight == nullptr) return SSD_ERR_INVALID_ARGUMENT;
+    CONV_TRY(check_win(p, conv_states, nslots, slot_stride, state_indices));
+    ConvArgs a = make_args(p, weight, bias, nullptr);
+    a.u = x; a.su_b = x_stride; a.out = out; a.so_b = out_stride;
+    a.win = conv_states; a.nslots = nslots; a.sw = slot_stride; a.slot = state_indices;
+    const cudaError_t e = p->dtype == SSD_BF16 ? launch_step<__nv_bfloat16>(a, (cudaStream_t)stream)
+                                               : launch_step<float>(a, (cudaStream_t)stream);
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 

@@ -1,0 +1,278 @@
+"""The selective scan (a decay rate per channel and state) on the GPU, forward and backward, against the float64
+oracle: types, state sizes and channel counts that fill no tile, groups, chunk edges, packed sequences down
+to none, strided inputs, long decays, differences, reproducibility and refusals.
+
+Tolerances (relative 2-norm).  bf16 outputs are rounded once to 8 bits: at most 2^-9 each, 2^-8 allowed.  fp32:
+a decay has a relative error near 2^-22 and a state remembers some 1 / (dt |A|) <= 100 tokens at these inputs'
+typical rates, so 100 x 2^-22 = 2.4e-5; twice that is allowed."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import selective as osel
+from state_space_model_scan_gb300 import _lib
+from state_space_model_scan_gb300.api import SelectiveScanFunction, selective_scan_backward, selective_scan_forward
+from helpers import rel_l2
+
+pytestmark = pytest.mark.gpu
+TD = {"bf16": torch.bfloat16, "f32": torch.float32}
+TOL = {torch.bfloat16: 2.0 ** -8, torch.float32: 5e-5}
+
+
+def make(Bt=1, L=33, Dm=33, G=1, N=16, dtype="f32", dt_dtype=None, z=True, D=True, bias=True, init=True, lens=None, seed=0,
+         state_dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    if lens is not None:
+        Bt, L = 1, sum(lens)
+    S = Bt if lens is None else len(lens)
+    td = TD[dtype]
+
+    def n(*s):
+        return torch.randn(*s, generator=g, dtype=torch.float64)
+    i = dict(x=n(Bt, L, Dm).to(td), dt=(0.5 * n(Bt, L, Dm)).to(TD[dt_dtype or dtype]),
+             A=(-torch.arange(1, N + 1, dtype=torch.float64) * torch.exp(0.2 * n(Dm, N))).float(),
+             B=n(Bt, L, G, N).to(td), C=n(Bt, L, G, N).to(td), D=n(Dm).float() if D else None,
+             z=n(Bt, L, Dm).to(td) if z else None,
+             dt_bias=torch.log(torch.expm1(torch.exp(np.log(1e-3) + torch.rand(Dm, generator=g, dtype=torch.float64) * np.log(100)))).float()
+             if bias else None, init=(0.3 * n(S, Dm, N)).to(state_dtype) if init else None,
+             cu=torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32) if lens is not None else None)
+    i["dy"] = n(Bt, L, Dm).to(td)
+    i["dfinal"] = n(S, Dm, N).to(state_dtype)
+    return i
+
+
+def dev(i):
+    return {k: None if v is None else v.cuda() for k, v in i.items()}
+
+
+def h(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def oracle(i):
+    """Forward and backward over all rows, in the tensors' shapes."""
+    keys = ("x", "dt", "B", "C", "z", "dy")
+    o = {k: h(v) for k, v in i.items() if k != "cu"}
+    cu = None if i["cu"] is None else i["cu"].numpy()
+    res = {}
+    for b in range(i["x"].shape[0]):
+        r = {k: None if o[k] is None else o[k][b] for k in keys}
+        sts = slice(None) if cu is not None else slice(b, b + 1)
+        init = None if o["init"] is None else o["init"][sts]
+        y, fin = osel.forward(r["x"], r["dt"], o["A"], r["B"], r["C"], o["D"], r["z"], o["dt_bias"], init, cu)
+        g = osel.backward(r["x"], r["dt"], o["A"], r["B"], r["C"], r["dy"], o["D"], r["z"], o["dt_bias"], init,
+                          o["dfinal"][sts], cu)
+        for k, v in dict(g, y=y[None], final=fin).items():
+            if k in ("dx", "ddt", "dB", "dC", "dz"):
+                v = v[None]
+            if k in ("dA", "dD", "ddt_bias"):
+                res[k] = res.get(k, 0) + v
+            else:
+                res.setdefault(k, []).append(v)
+    return {k: np.concatenate(v) if isinstance(v, list) else v for k, v in res.items()}
+
+
+def kw(d):
+    return dict(D=d["D"], z=d["z"], dt_bias=d["dt_bias"], initial_states=d["init"], cu_seqlens=d["cu"])
+
+
+def gpu(i, keep=True):
+    d = dev(i)
+    a = (d["x"], d["dt"], d["A"], d["B"], d["C"])
+    y, final, kept = selective_scan_forward(*a, keep_chunk_states=True, **kw(d))
+    g = selective_scan_backward(*a, d["dy"], dfinal_states=d["dfinal"], chunk_states=kept if keep else None, **kw(d))
+    torch.cuda.synchronize()
+    return dict(g, y=y, final=final)
+
+
+def check(i, keep=True):
+    got, want = gpu(i, keep), oracle(i)
+    for k, v in got.items():
+        assert torch.isfinite(v).all(), k
+        assert rel_l2(h(v), want[k]) <= TOL[v.dtype], (k, rel_l2(h(v), want[k]))
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [1, 2, 31, 32, 33, 127, 129, 300])
+def test_lengths(dtype, L):
+    check(make(Bt=2, L=L, Dm=40, dtype=dtype, seed=L))
+
+
+@pytest.mark.parametrize("N", [1, 4, 13, 16, 17, 32, 40, 64, 65, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_state_sizes(N, dtype):
+    check(make(L=70, Dm=37, N=N, dtype=dtype, seed=N))
+
+
+@pytest.mark.parametrize("Dm,G", [(1, 1), (31, 1), (64, 2), (66, 3), (257, 1), (600, 2)])
+def test_channels_and_groups(Dm, G):
+    check(make(Bt=2, L=45, Dm=Dm, G=G, seed=Dm))
+
+
+@pytest.mark.parametrize("drop", ["z", "D", "bias", "init"])
+def test_absent_inputs(drop):
+    i = make(L=65, Dm=34, **{drop: False})
+    got = check(i)
+    for name, out in (("z", "dz"), ("D", "dD"), ("bias", "ddt_bias"), ("init", "dinitial_states")):
+        assert (out in got) == (name != drop)
+
+
+def test_wide_batches_take_the_same_values():
+    """Many channels in flight (no split over time) and few (split): one batch row against itself alone."""
+    i = make(Bt=24, L=200, Dm=512, dtype="bf16", seed=3)
+    d = dev(i)
+    y, fin = selective_scan_forward(d["x"], d["dt"], d["A"], d["B"], d["C"], **kw(d))
+    one = {k: (v[5:6] if k in ("x", "dt", "B", "C", "z", "init") else v) for k, v in d.items()}
+    y1, fin1 = selective_scan_forward(one["x"], one["dt"], one["A"], one["B"], one["C"], **kw(one))
+    assert rel_l2(h(y[5:6]), h(y1)) <= TOL[torch.bfloat16]
+    assert rel_l2(h(fin[5:6]), h(fin1)) <= TOL[torch.float32]
+
+
+@pytest.mark.parametrize("dtype,dt_dtype", [("bf16", "f32"), ("bf16", "bf16")])
+def test_dt_types(dtype, dt_dtype):
+    got = check(make(L=90, Dm=48, dtype=dtype, dt_dtype=dt_dtype))
+    assert got["ddt"].dtype == TD[dt_dtype]
+
+
+@pytest.mark.parametrize("lens", [[5], [1, 1, 1], [0, 3, 0, 64, 200, 0], [33, 31, 32, 1, 95], [300, 2, 129]])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_packed_sequences(lens, dtype):
+    check(make(lens=lens, Dm=35, G=1, N=16, dtype=dtype, seed=len(lens)))
+
+
+def test_packed_is_separate_and_poison_stays_in_its_sequence():
+    i = make(lens=[40, 37, 64], Dm=33, N=16, z=True)
+    clean = gpu(i)
+    for k in ("x", "B", "dt", "z", "dy"):
+        i[k][:, 40:77] = float("nan")
+    i["init"][1] = float("inf")
+    bad = gpu(i)
+    for k in ("y", "dx", "ddt", "dB", "dC", "dz"):
+        assert torch.equal(bad[k][:, :40], clean[k][:, :40]) and torch.equal(bad[k][:, 77:], clean[k][:, 77:]), k
+    assert torch.equal(bad["final"][0], clean["final"][0]) and torch.equal(bad["final"][2], clean["final"][2])
+    assert torch.isnan(bad["y"][:, 40:77]).all()
+
+
+def test_no_tokens():
+    i = make(Bt=2, L=0, Dm=33)
+    got = gpu(i)
+    assert torch.equal(got["final"].cpu(), i["init"]) and torch.equal(got["dinitial_states"].cpu(), i["dfinal"])
+    assert got["dA"].abs().max() == 0 and got["dD"].abs().max() == 0 and got["ddt_bias"].abs().max() == 0
+    i = make(lens=[0, 0], Dm=33, init=False)
+    assert gpu(i)["final"].abs().max() == 0
+
+
+def test_states_in_16_bits():
+    i = make(L=70, Dm=40, state_dtype=torch.bfloat16)
+    got = check(i)
+    assert got["final"].dtype == got["dinitial_states"].dtype == torch.bfloat16
+
+
+def test_backward_without_kept_states_is_the_same():
+    for i in (make(L=150, Dm=70, dtype="bf16"), make(lens=[70, 0, 129], Dm=40)):
+        a, b = gpu(i), gpu(i, keep=False)
+        for k in a:
+            assert torch.equal(a[k], b[k]), k
+
+
+def test_runs_repeat_bit_for_bit():
+    i = make(Bt=2, L=333, Dm=300, G=2, dtype="bf16")
+    a, b = gpu(i), gpu(i)
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+
+
+def test_strided_views():
+    """x, z side by side in one buffer, B and C in another, an odd element offset, dy a slice."""
+    i = make(Bt=2, L=77, Dm=31, N=13, dtype="bf16")
+    d = dev(i)
+    want = gpu(i)
+    xz = torch.empty(2, 77, 63, dtype=torch.bfloat16, device="cuda")
+    xz[..., 1:32], xz[..., 32:] = d["x"], d["z"]
+    bc = torch.empty(2, 77, 1, 27, dtype=torch.bfloat16, device="cuda")
+    bc[..., :13], bc[..., 14:] = d["B"], d["C"]
+    d.update(x=xz[..., 1:32], z=xz[..., 32:], B=bc[..., :13], C=bc[..., 14:])
+    big = torch.zeros(2, 80, 40, dtype=torch.bfloat16, device="cuda")
+    big[:, 2:79, 5:36] = d["dy"]
+    a = (d["x"], d["dt"], d["A"], d["B"], d["C"])
+    y, fin = selective_scan_forward(*a, **kw(d))
+    g = selective_scan_backward(*a, big[:, 2:79, 5:36], dfinal_states=d["dfinal"], **kw(d))
+    for k, v in dict(g, y=y, final=fin).items():
+        assert torch.equal(v, want[k]), k
+
+
+def test_extreme_steps():
+    """Steps whose softplus is its argument, vanishing steps, and decays that underflow to zero."""
+    i = make(L=64, Dm=48)
+    i["dt"][:, ::3] = 30.0
+    i["dt"][:, 1::3] = -40.0
+    check(i)
+
+
+def test_autograd_and_another_stream():
+    i = make(Bt=2, L=50, Dm=33, dtype="f32")
+    d = dev(i)
+    want = gpu(i)
+    names = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "init")
+    v = {k: d[k].clone().requires_grad_() for k in names}
+    y, fin = SelectiveScanFunction.apply(*(v[k] for k in names), None)
+    ((y * d["dy"]).sum() + (fin * d["dfinal"]).sum()).backward()
+    for k in names:
+        assert torch.equal(v[k].grad, want["d" + {"init": "initial_states"}.get(k, k)]), k
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    a = (d["x"], d["dt"], d["A"], d["B"], d["C"])
+    y2, fin2 = selective_scan_forward(*a, stream=s, **kw(d))
+    g2 = selective_scan_backward(*a, d["dy"], dfinal_states=d["dfinal"], stream=s, **kw(d))
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(y2, want["y"]) and torch.equal(fin2, want["final"]) and torch.equal(g2["dA"], want["dA"])
+
+
+@pytest.mark.parametrize("name", ["x", "dt", "A", "B", "C", "D", "z", "dt_bias", "init"])
+def test_gradients_against_differences(name):
+    """The derivative along a random direction, from two forwards.  The loss sums some 4000 products with fp32 errors
+    near 1e-6 of their size, the step is 2^-6 of the inputs' spread: noise / (2 step) near 1e-3 of the
+    derivative's scale, curvature as much; 2% allowed."""
+    i = make(L=60, Dm=33, N=16, seed=5)
+    d = dev(i)
+    g = gpu(i)["d" + {"init": "initial_states"}.get(name, name)].double()
+    v = torch.randn(d[name].shape, generator=torch.Generator().manual_seed(1)).cuda()
+    v = v * (d[name].abs() if name == "A" else 1.0)
+    step = 2.0 ** -6
+
+    def loss(sign):
+        e = dict(d)
+        e[name] = (d[name] + sign * step * v).contiguous()
+        y, fin = selective_scan_forward(e["x"], e["dt"], e["A"], e["B"], e["C"], **kw(e))
+        return float((y.double() * d["dy"].double()).sum() + (fin.double() * d["dfinal"].double()).sum())
+    num = (loss(1) - loss(-1)) / (2 * step)
+    ana = float((g * v.double()).sum())
+    size = float((g * v.double()).norm())
+    assert abs(num - ana) <= 0.02 * max(abs(ana), size), (num, ana)
+
+
+def test_refusals():
+    i = dev(make(L=10, Dm=32))
+    a = [i["x"], i["dt"], i["A"], i["B"], i["C"]]
+    for k, bad in ((1, i["dt"].double()), (1, i["dt"][:, :5]), (2, i["A"][:, :3]), (2, i["A"].t().contiguous().t()),
+                   (3, i["B"].bfloat16()), (3, i["B"][0]), (4, i["C"].cpu()), (0, i["x"].half()),
+                   (0, i["x"].transpose(1, 2).contiguous().transpose(1, 2))):
+        b = list(a)
+        b[k] = bad
+        with pytest.raises(ValueError):
+            selective_scan_forward(*b)
+    with pytest.raises(ValueError):
+        selective_scan_forward(*a, initial_states=i["init"][:, :4])
+    with pytest.raises(ValueError):
+        selective_scan_forward(*a, cu_seqlens=torch.tensor([0, 10], device="cuda"))       # int64
+    with pytest.raises(ValueError):
+        selective_scan_backward(*a, i["dy"], chunk_states=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(_lib.SSDError) as e:                                              # 33 % 2 != 0
+        selective_scan_forward(i["x"], i["dt"], i["A"], i["B"].expand(1, 10, 3, 16).contiguous(),
+                               i["C"].expand(1, 10, 3, 16).contiguous())
+    assert e.value.code == 1
+    j = dev(make(L=10, Dm=32, N=129))
+    with pytest.raises(_lib.SSDError) as e:
+        selective_scan_forward(j["x"], j["dt"], j["A"], j["B"], j["C"])
+    assert e.value.code == 2
