@@ -241,7 +241,8 @@ def complex_ssd_forward(x, A, B, C, dt, initial_states=None, chunk_size=64, retu
 # The selective scan, the convolution with a carried window, single-token steps and 8-bit
 # snapshots of states.  The library sees addresses and strides; that the tensors behind them have
 # the shapes, types and devices it assumes is checked here.
-_CODE = {torch.float32: _lib.SSD_F32, torch.bfloat16: _lib.SSD_BF16}
+_F32 = (torch.float32,)
+_ST = (torch.float32, torch.bfloat16)
 
 
 def _need(ok, what):
@@ -250,28 +251,31 @@ def _need(ok, what):
 
 
 def _like(name, t, shape, dtypes, device, inner=0):
-    """t has this shape, one of these types and this device, and its last `inner` dimensions are contiguous."""
+    """t has this shape, one of these types and this device (its index), and its last `inner` dimensions are
+    contiguous."""
+    if t.shape == shape and t.dtype in dtypes and t.get_device() == device and t.is_contiguous():
+        return
     if t.shape != shape:
         raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
     if t.dtype not in dtypes:
         raise ValueError("%s is %s, not %s" % (name, t.dtype, " or ".join(str(d) for d in dtypes)))
-    if t.device != device:
-        raise ValueError("%s is on %s, not %s" % (name, t.device, device))
-    if inner:
-        st, sh, n = t.stride(), t.shape, 1
-        for k in range(len(sh) - 1, len(sh) - 1 - inner, -1):
-            if sh[k] != 1 and st[k] != n:
-                raise ValueError("%s: its last %d dimensions must be contiguous" % (name, inner))
-            n *= sh[k]
+    if t.get_device() != device:
+        raise ValueError("%s is on %s, not on GPU %d" % (name, t.device, device))
+    st, sh, n = t.stride(), t.shape, 1
+    for k in range(len(sh) - 1, len(sh) - 1 - inner, -1):
+        if sh[k] != 1 and st[k] != n:
+            raise ValueError("%s: its last %d dimensions must be contiguous" % (name, inner))
+        n *= sh[k]
 
 
-_F32 = (torch.float32,)
-_ST = (torch.float32, torch.bfloat16)
-
-
-def _index(name, t, n, device):
-    if t is not None:
-        _like(name, t, (n,), (torch.int32,), device, 1)
+def _on_gpu(name, t):
+    """Index of the GPU that t is on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("%s is not on a GPU" % name)
+    if t.dtype not in _ST:
+        raise ValueError("%s is %s, not float32 or bfloat16" % (name, t.dtype))
+    return dev
 
 
 def _on(stream, *tensors):
@@ -282,55 +286,41 @@ def _on(stream, *tensors):
                 t.record_stream(stream)
 
 
-def _dense(t, inner):
-    """An unset size-1 dimension may carry any stride; the library wants the contiguous ones."""
-    st, n = list(t.stride()), 1
-    for k in range(t.dim() - 1, t.dim() - 1 - inner, -1):
-        st[k] = n
-        n *= t.shape[k]
-    out = _lib.tensor(t)
-    for i, v in enumerate(st[:4]):
-        out.stride[i] = v
-    return out
+def _last_is_one(f, k):
+    """The stride of dimension k in packed fields, set to 1: a dimension of size 1 may have noted any."""
+    return f if f[3 + k] == 1 else f[:3 + k] + (1,) + f[4 + k:]
 
 
-def _selective_args(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens, chunk_states):
-    Bt, L, Dm = x.shape
-    _need(B.dim() == 4, "B has shape [batch, seqlen, ngroups, dstate]")
+def _selective_args(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens):
+    """The problem, the packed fields of the inputs (x .. initial_states) and the number of sequences."""
+    _need(x.dim() == 3 and B.dim() == 4, "x has shape [batch, seqlen, channels], B [batch, seqlen, ngroups, dstate]")
+    shape = x.shape
+    Bt, L, Dm = shape
     G, N = B.shape[2:]
-    dev, own = x.device, (x.dtype,)
-    _need(x.is_cuda, "x is not on a GPU")
-    _need(x.dtype in _ST, "x is %s, not float32 or bfloat16" % x.dtype)
+    dev, own = _on_gpu("x", x), (x.dtype,)
     S = Bt
     if cu_seqlens is not None:
         S = cu_seqlens.numel() - 1
         _need(S >= 1, "cu_seqlens holds no sequence")
-        _index("cu_seqlens", cu_seqlens, S + 1, dev)
-    _like("x", x, x.shape, own, dev, 1)
-    _like("dt", dt, x.shape, (torch.float32, x.dtype), dev, 1)
+        _like("cu_seqlens", cu_seqlens, (S + 1,), (torch.int32,), dev, 1)
+    _like("x", x, shape, own, dev, 1)
+    _like("dt", dt, shape, (torch.float32, x.dtype), dev, 1)
     _like("A", A, (Dm, N), _F32, dev, 2)
     _like("B", B, (Bt, L, G, N), own, dev, 1)
     _like("C", C, (Bt, L, G, N), own, dev, 1)
-    a = _lib.FwdArgs()
-    a.x, a.dt, a.B, a.C, a.A = _dense(x, 1), _dense(dt, 1), _dense(B, 1), _dense(C, 1), _dense(A, 2)
-    for name, t in (("D", D), ("dt_bias", dt_bias)):
-        if t is not None:
-            _like(name, t, (Dm,), _F32, dev, 1)
-            setattr(a, name, _dense(t, 1))
+    if D is not None:
+        _like("D", D, (Dm,), _F32, dev, 1)
+    if dt_bias is not None:
+        _like("dt_bias", dt_bias, (Dm,), _F32, dev, 1)
     if z is not None:
-        _like("z", z, x.shape, own, dev, 1)
-        a.z = _dense(z, 1)
+        _like("z", z, shape, own, dev, 1)
     if initial_states is not None:
         _like("initial_states", initial_states, (S, Dm, N), _ST, dev, 3)
-        a.initial_states = _dense(initial_states, 3)
-    a.cu_seqlens = None if cu_seqlens is None else cu_seqlens.data_ptr()
-    prob = _lib.SelectiveProblem(Bt, L, Dm, G, N, S if cu_seqlens is not None else 0)
-    if chunk_states is not None:
-        need = _lib.selective_chunk_states_size(prob)
-        _need(chunk_states.device == dev and chunk_states.is_contiguous(), "chunk_states: a contiguous buffer on x's device")
-        _need(chunk_states.numel() * chunk_states.element_size() >= need, "chunk_states is smaller than %d bytes" % need)
-        a.chunk_states = chunk_states.data_ptr()
-    return prob, a, S
+    pk = _lib.packed
+    fields = (_last_is_one(pk(x), 2) + _last_is_one(pk(dt), 2) + pk(A, True) + _last_is_one(pk(B), 3) +
+              _last_is_one(pk(C), 3) + pk(D, True) + (_lib._ABSENT if z is None else _last_is_one(pk(z), 2)) +
+              pk(dt_bias, True) + pk(initial_states, True))
+    return _lib.SelectiveProblem(Bt, L, Dm, G, N, S if cu_seqlens is not None else 0), fields, S
 
 
 def selective_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, initial_states=None, cu_seqlens=None,
@@ -344,20 +334,19 @@ def selective_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, initial
     float32 or bfloat16; cu_seqlens: int32 [S + 1] (batch 1).  state_dtype: of the final states (default:
     that of initial_states, else float32).  keep_chunk_states: also return the buffer that
     selective_scan_backward(chunk_states=...) starts from."""
-    prob, a, S = _selective_args(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens, None)
+    prob, fields, S = _selective_args(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens)
     y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    a.y = _dense(y, 1)
     final = kept = None
     if return_final_states:
         sdt = state_dtype or (initial_states.dtype if initial_states is not None else torch.float32)
         _need(sdt in _ST, "state_dtype is float32 or bfloat16")
-        final = torch.empty(S, x.shape[2], B.shape[3], dtype=sdt, device=x.device)
-        a.final_states = _dense(final, 3)
+        final = torch.empty((S, x.shape[2], B.shape[3]), dtype=sdt, device=x.device)
     if keep_chunk_states:
         kept = torch.empty(_lib.selective_chunk_states_size(prob), dtype=torch.uint8, device=x.device)
-        a.chunk_states = kept.data_ptr()
     _on(stream, y, final, kept)
-    _lib.check(_lib.selective_fwd(prob, a, stream), "ssd_selective_fwd")
+    pk = _lib.packed
+    fields += pk(y, True) + pk(final, True) + (_lib._addr(cu_seqlens) or 0, _lib._addr(kept) or 0)
+    _lib.check(_lib.selective_fwd(prob, fields, x, stream), "ssd_selective_fwd")
     return (y, final, kept) if keep_chunk_states else (y, final)
 
 
@@ -367,33 +356,36 @@ def selective_scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, in
     the matching input is given, dD, dz, ddt_bias, dinitial_states.  chunk_states: the buffer that
     selective_scan_forward(keep_chunk_states=True) returned for the same inputs (without it the
     forward's states are computed again)."""
-    prob, f, S = _selective_args(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens, chunk_states)
-    _like("dy", dy, x.shape, (x.dtype,), x.device, 1)
-    dev = x.device
+    prob, fields, S = _selective_args(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens)
+    dev, gpu = x.device, x.get_device()
+    _like("dy", dy, x.shape, (x.dtype,), gpu, 1)
+    if dfinal_states is not None:
+        _like("dfinal_states", dfinal_states, (S, x.shape[2], B.shape[3]), _ST, gpu, 3)
+    if chunk_states is not None:
+        need = _lib.selective_chunk_states_size(prob)
+        _need(chunk_states.get_device() == gpu and chunk_states.is_contiguous(), "chunk_states: a contiguous buffer on x's GPU")
+        _need(chunk_states.numel() * chunk_states.element_size() >= need, "chunk_states is smaller than %d bytes" % need)
     g = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=dev), ddt=torch.empty(dt.shape, dtype=dt.dtype, device=dev),
              dA=torch.empty(A.shape, dtype=torch.float32, device=dev),
              dB=torch.empty(B.shape, dtype=B.dtype, device=dev), dC=torch.empty(C.shape, dtype=C.dtype, device=dev))
-    b = _lib.BwdArgs()
-    b.fwd = f
-    b.dy, b.dx, b.ddt, b.dA = _dense(dy, 1), _dense(g["dx"], 1), _dense(g["ddt"], 1), _dense(g["dA"], 2)
-    b.dB, b.dC = _dense(g["dB"], 1), _dense(g["dC"], 1)
-    for name, t in (("D", D), ("dt_bias", dt_bias)):
-        if t is not None:
-            g["d" + name] = torch.empty(t.shape, dtype=torch.float32, device=dev)
-            setattr(b, "d" + name, _dense(g["d" + name], 1))
+    if D is not None:
+        g["dD"] = torch.empty(D.shape, dtype=torch.float32, device=dev)
+    if dt_bias is not None:
+        g["ddt_bias"] = torch.empty(dt_bias.shape, dtype=torch.float32, device=dev)
     if z is not None:
         g["dz"] = torch.empty(z.shape, dtype=z.dtype, device=dev)
-        b.dz = _dense(g["dz"], 1)
-    if dfinal_states is not None:
-        _like("dfinal_states", dfinal_states, (S, x.shape[2], B.shape[3]), _ST, dev, 3)
-        b.dfinal_states = _dense(dfinal_states, 3)
     if initial_states is not None:   # in the initial states' storage type
         g["dinitial_states"] = torch.empty(initial_states.shape, dtype=initial_states.dtype, device=dev)
-        b.dinitial_states = _dense(g["dinitial_states"], 3)
-    nbytes = _lib.selective_bwd_workspace_size(prob, b)
+    pk = _lib.packed
+    fields += _lib._ABSENT * 2 + (_lib._addr(cu_seqlens) or 0, _lib._addr(chunk_states) or 0)
+    fields += _last_is_one(pk(dy), 2) + pk(dfinal_states, True)
+    for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dinitial_states"):
+        fields += pk(g.get(k), True)
+    args = _lib._BWD.pack(*fields)
+    nbytes = _lib.selective_bwd_workspace_size(prob, args)
     ws = workspace.get(nbytes) if workspace is not None else torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
     _on(stream, ws, *g.values())
-    _lib.check(_lib.selective_bwd(prob, b, ws, stream), "ssd_selective_bwd")
+    _lib.check(_lib.selective_bwd(prob, args, ws, stream), "ssd_selective_bwd")
     return g
 
 
@@ -418,34 +410,39 @@ class SelectiveScanFunction(torch.autograd.Function):
 
 
 def _step(selective, state, x, dt, A, B, C, D, z, dt_bias, state_indices, stream):
-    n, dev, own = x.shape[0], x.device, (x.dtype,)
-    _need(x.is_cuda, "x is not on a GPU")
-    _need(x.dtype in _ST, "x is %s, not float32 or bfloat16" % x.dtype)
     _need(B.dim() == 3, "B has shape [batch, ngroups, dstate]")
+    dev, own, shape, slots = _on_gpu("x", x), (x.dtype,), x.shape, state.shape[0]
     G, N = B.shape[1:]
-    H = x.shape[1]
-    P = 1 if selective else x.shape[2]
-    inner = x.dim() - 1
-    _like("x", x, x.shape, own, dev, inner)
-    _like("dt", dt, (n, H), (torch.float32, x.dtype) if selective else _F32, dev, 1)
-    _like("A", A, (H, N) if selective else (H,), _F32, dev, 2 if selective else 1)
-    _like("B", B, B.shape, own, dev, 2)
-    _like("C", C, B.shape, own, dev, 2)
-    _like("state", state, (state.shape[0], H, N) if selective else (state.shape[0], H, P, N), _ST, dev, inner + 1)
+    if selective:
+        n, H = shape
+        P, inner = 1, 1
+        _like("state", state, (slots, H, N), _ST, dev, 2)
+        _like("A", A, (H, N), _F32, dev, 2)
+        _like("dt", dt, (n, H), (torch.float32, x.dtype), dev, 1)
+    else:
+        n, H, P = shape
+        inner = 2
+        _like("state", state, (slots, H, P, N), _ST, dev, 3)
+        _like("A", A, (H,), _F32, dev, 1)
+        _like("dt", dt, (n, H), _F32, dev, 1)
+    _like("x", x, shape, own, dev, inner)
+    _like("B", B, (n, G, N), own, dev, 2)
+    _like("C", C, (n, G, N), own, dev, 2)
     if D is not None:
         _like("D", D, (H,), _F32, dev, 1)
     if z is not None:
-        _like("z", z, x.shape, own, dev, inner)
+        _like("z", z, shape, own, dev, inner)
     if dt_bias is not None:
         _like("dt_bias", dt_bias, (H,), _F32, dev, 1)
     if state_indices is None:
-        _need(state.shape[0] >= n, "the state pool has fewer slots than there are requests")
+        _need(slots >= n, "the state pool has fewer slots than there are requests")
     else:
-        _index("state_indices", state_indices, n, dev)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    prob = _lib.StepProblem(n, state.shape[0], H, P, G, N, state.stride(0), x.stride(0), dt.stride(0),
+        _like("state_indices", state_indices, (n,), (torch.int32,), dev, 1)
+    y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    code = _lib._CODES
+    prob = _lib.StepProblem(n, slots, H, P, G, N, state.stride(0), x.stride(0), dt.stride(0),
                             0 if z is None else z.stride(0), B.stride(0), C.stride(0), H * P,
-                            _CODE[x.dtype], _CODE[dt.dtype], _CODE[state.dtype], 0)
+                            code[x.dtype], code[dt.dtype], code[state.dtype], 0)
     if stream is not None:
         _on(stream, y)
     _lib.check(_lib.step(selective, prob, state, state_indices, x, dt, A, B, C, D, z, dt_bias, y, stream),
@@ -472,20 +469,21 @@ def selective_scan_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, sta
 
 
 def _conv_check(u, weight, bias, conv_states, state_indices, n):
+    """Checks what both forms share; returns the GPU's index and the width."""
     Cn = u.shape[-1]
-    dev = u.device
-    _need(u.is_cuda, "xbc is not on a GPU")
-    _need(u.dtype in _ST, "xbc is %s, not float32 or bfloat16" % u.dtype)
+    dev = _on_gpu("xbc", u)
     _need(weight.dim() == 2, "weight has shape [channels, width]")
+    K = weight.shape[1]
     _like("xbc", u, u.shape, (u.dtype,), dev, 1)
-    _like("weight", weight, (Cn, weight.shape[1]), _F32, dev, 2)
+    _like("weight", weight, (Cn, K), _F32, dev, 2)
     if bias is not None:
         _like("bias", bias, (Cn,), _F32, dev, 1)
-    _like("conv_states", conv_states, (conv_states.shape[0], weight.shape[1] - 1, Cn), (u.dtype,), dev, 2)
+    _like("conv_states", conv_states, (conv_states.shape[0], K - 1, Cn), (u.dtype,), dev, 2)
     if state_indices is None:
         _need(conv_states.shape[0] >= n, "conv_states has fewer slots than there are sequences")
     else:
-        _index("state_indices", state_indices, n, dev)
+        _like("state_indices", state_indices, (n,), (torch.int32,), dev, 1)
+    return dev, K
 
 
 def conv1d_prompt(xbc, weight, bias, conv_states, cu_seqlens=None, state_indices=None, has_initial=None, silu=True,
@@ -497,14 +495,14 @@ def conv1d_prompt(xbc, weight, bias, conv_states, cu_seqlens=None, state_indices
     _need(xbc.dim() == 3, "xbc has shape [batch, seqlen, channels]")
     Bsz, L, Cn = xbc.shape
     n = Bsz if cu_seqlens is None else cu_seqlens.numel() - 1
-    _conv_check(xbc, weight, bias, conv_states, state_indices, n)
+    dev, K = _conv_check(xbc, weight, bias, conv_states, state_indices, n)
     if cu_seqlens is not None:
         _need(n >= 1, "cu_seqlens holds no sequence")
-        _index("cu_seqlens", cu_seqlens, n + 1, xbc.device)
+        _like("cu_seqlens", cu_seqlens, (n + 1,), (torch.int32,), dev, 1)
     if has_initial is not None:
-        _like("has_initial", has_initial, (n,), (torch.uint8, torch.bool), xbc.device, 1)
-    out = torch.empty(Bsz, L, Cn, dtype=xbc.dtype, device=xbc.device)
-    prob = _lib.conv_problem(Bsz, L, Cn, weight.shape[1], 0 if cu_seqlens is None else n, xbc.dtype, silu)
+        _like("has_initial", has_initial, (n,), (torch.uint8, torch.bool), dev, 1)
+    out = torch.empty((Bsz, L, Cn), dtype=xbc.dtype, device=xbc.device)
+    prob = _lib.ConvProblem(Bsz, L, Cn, K, 0 if cu_seqlens is None else n, _lib._CODES[xbc.dtype], 1 if silu else 0, 0, 0)
     _on(stream, out)
     _lib.check(_lib.conv1d_prompt(prob, xbc, weight, bias, cu_seqlens, conv_states, state_indices, has_initial, out, stream),
                "ssd_conv1d_prompt")
@@ -516,34 +514,35 @@ def conv1d_step(xbc, weight, bias, conv_states, state_indices=None, silu=True, s
     conv1d_prompt (a request whose slot is out of range sees a window of zeros and leaves none)."""
     _need(xbc.dim() == 2, "xbc has shape [batch, channels]")
     n, Cn = xbc.shape
-    _conv_check(xbc, weight, bias, conv_states, state_indices, n)
-    out = torch.empty(n, Cn, dtype=xbc.dtype, device=xbc.device)
+    _, K = _conv_check(xbc, weight, bias, conv_states, state_indices, n)
+    out = torch.empty((n, Cn), dtype=xbc.dtype, device=xbc.device)
     if n == 0:
         return out
-    prob = _lib.ConvProblem(n, 1, Cn, weight.shape[1], 0, _CODE[xbc.dtype], 1 if silu else 0, 0, 0)
+    prob = _lib.ConvProblem(n, 1, Cn, K, 0, _lib._CODES[xbc.dtype], 1 if silu else 0, 0, 0)
     _on(stream, out)
     _lib.check(_lib.conv1d_step(prob, xbc, weight, bias, conv_states, state_indices, out, stream), "ssd_conv1d_step")
     return out
 
 
 def _snapshot(store, states, snapshots, scales, state_indices, slots, stream):
-    dev = states.device
-    _need(states.is_cuda, "states is not on a GPU")
-    _need(states.dim() >= 2, "states has shape [nslots, ..., dstate]")
-    inner = states.dim() - 1
-    _like("states", states, states.shape, _ST, dev, inner)
-    _like("snapshots", snapshots, snapshots.shape[:1] + states.shape[1:], (torch.int8,), dev, inner + 1)
-    _like("scales", scales, snapshots.shape[:-1], _F32, dev, inner)
+    dev, shape, snaps = _on_gpu("states", states), states.shape, snapshots.shape[0]
+    _need(len(shape) >= 2, "states has shape [nslots, ..., dstate]")
+    _like("states", states, shape, _ST, dev, len(shape) - 1)
+    _like("snapshots", snapshots, (snaps,) + shape[1:], (torch.int8,), dev, len(shape))
+    _like("scales", scales, (snaps,) + shape[1:-1], _F32, dev, len(shape) - 1)
     n = (state_indices if state_indices is not None else slots if slots is not None else states).shape[0]
-    _index("state_indices", state_indices, n, dev)
-    _index("slots", slots, n, dev)
-    _need(slots is not None or snapshots.shape[0] >= n, "there are fewer snapshots than states")
-    _need(state_indices is not None or states.shape[0] >= n, "there are fewer states than slots")
-    N = states.shape[-1]
+    if state_indices is None:
+        _need(shape[0] >= n, "there are fewer states than slots")
+    else:
+        _like("state_indices", state_indices, (n,), (torch.int32,), dev, 1)
+    if slots is None:
+        _need(snaps >= n, "there are fewer snapshots than states")
+    else:
+        _like("slots", slots, (n,), (torch.int32,), dev, 1)
     rows = 1
-    for k in states.shape[1:-1]:
+    for k in shape[1:-1]:
         rows *= k
-    prob = _lib.SnapshotProblem(n, rows, N, states.shape[0], snapshots.shape[0], states.stride(0), _CODE[states.dtype], 0)
+    prob = _lib.SnapshotProblem(n, rows, shape[-1], shape[0], snaps, states.stride(0), _lib._CODES[states.dtype], 0)
     _lib.check(_lib.snapshot(store, prob, states, state_indices, snapshots, scales, slots, stream),
                "ssd_snapshot_store" if store else "ssd_snapshot_load")
 
