@@ -41,6 +41,7 @@ ssd_status check_tok(const ssd_selective_problem *p, const ssd_tensor &t, int dt
     if (t.ptr == nullptr || t.dtype != dtype || !type_ok(dtype)) return SSD_ERR_INVALID_ARGUMENT;
     const int64_t inner = grouped ? p->dstate : p->channels;
     if (t.stride[grouped ? 3 : 2] != 1) return SSD_ERR_INVALID_ARGUMENT;
+    if (p->seqlen > 1 && t.stride[1] >= ((int64_t)1 << 28)) return SSD_ERR_UNSUPPORTED;   // a token's bytes fit 31 bits
     if (grouped && p->ngroups > 1 && t.stride[2] < inner) return SSD_ERR_INVALID_ARGUMENT;
     const int64_t row = grouped ? (p->ngroups > 1 ? t.stride[2] * (p->ngroups - 1) : 0) + inner : inner;
     if (p->seqlen > 1 && t.stride[1] < row) return SSD_ERR_INVALID_ARGUMENT;
@@ -80,6 +81,13 @@ ssd_status check_inputs(const ssd_selective_problem *p, const ssd_fwd_args *a) {
     return SSD_OK;
 }
 
+bool fours(const ssd_tensor &t, int dims) {
+    if (t.ptr == nullptr) return true;
+    for (int i = 0; i < dims; ++i)
+        if (t.stride[i] % 4 != 0) return false;
+    return al(t.ptr, 4 * esize(t.dtype));
+}
+
 SelArgs make_args(const ssd_selective_problem *p, const ssd_fwd_args *f) {
     SelArgs a{};
     a.x = f->x.ptr; a.xb = f->x.stride[0]; a.xt = f->x.stride[1];
@@ -100,6 +108,8 @@ SelArgs make_args(const ssd_selective_problem *p, const ssd_fwd_args *f) {
     a.nseqs = (int)(p->nseqs ? p->nseqs : p->batch);
     a.nslots = (int)chunk_slots(p);
     a.states = static_cast<float *>(f->chunk_states);
+    a.vec = (p->ngroups == 1 || a.dpg % 4 == 0) && fours(f->x, 2) && fours(f->dt, 2) && fours(f->z, 2);
+    a.vecBC = fours(f->B, 3) && fours(f->C, 3);
     return a;
 }
 
@@ -168,6 +178,7 @@ ssd_status ssd_selective_fwd(const ssd_selective_problem *p, const ssd_fwd_args 
     SEL_TRY(check_state(f->final_states, p));
     if (p->seqlen == 0 && f->final_states.ptr == nullptr) return SSD_OK;
     SelArgs a = make_args(p, f);
+    a.vec = a.vec && fours(f->y, 2);
     a.y = f->y.ptr; a.yb = f->y.stride[0]; a.yt = f->y.stride[1];
     a.final = f->final_states.ptr;
     a.final_bf16 = f->final_states.dtype == SSD_BF16;

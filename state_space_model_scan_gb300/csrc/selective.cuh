@@ -19,6 +19,8 @@ struct SelArgs {
     int64_t xb, xt, dtb, dtt, Bb, Bt, Bg, Cb, Ct, Cg, zb, zt, dyb, dyt;   // element strides: batch row, token (, group)
     const float *A, *D, *bias;
     const void *init, *dfinal;
+    // four elements at places divisible by four are aligned to their size, in the channel tensors / in B and C
+    bool vec, vecBC;
     bool dt_f32, init_bf16, final_bf16, dfinal_bf16, dinit_bf16;
     const int32_t *cu;                 // packed sequences (batch 1) or NULL
     int nbatch, seqlen, channels, ngroups, dpg, N, NP, nseqs, nslots;     // dpg: channels per group; nseqs: batch or packed
@@ -98,34 +100,107 @@ __device__ __forceinline__ f32x2 ex2x2(f32x2 v) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+__device__ __forceinline__ float rcpf(float v) {   // 1 / v to about 2^-23
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 // softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1].  log1p(e) = 2 atanh(s) with
-// s = e / (2 + e) <= 1/3, by atanh's power series s + s^3/3 + ... + s^15/15 (the rest is below
-// 2^-27 of the sum); no cancellation, so small steps keep their relative accuracy.
+// s = e / (2 + e) <= 1/3; 2 atanh(s) / s is a polynomial of degree 4 in s^2 there, fitted to
+// its smallest largest relative error, 4e-9.  No cancellation: small steps keep their relative accuracy.
 __device__ __forceinline__ float sel_softplus(float v) {
-    const float e = expf(-fabsf(v));
-    const float s = __fdividef(e, 2.f + e), q = s * s;
-    float p = 1.f / 15.f;
-    p = fmaf(p, q, 1.f / 13.f);
-    p = fmaf(p, q, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
-    p = fmaf(p, q, 1.f);
-    const float r = fmaf(2.f * s, p, fmaxf(v, 0.f));
-    return v == v ? r : v;   // fmaxf would drop a NaN
+    const float e = ex2f(-kLog2e * fabsf(v));
+    const float s = e * rcpf(2.f + e), q = s * s;
+    float p = 0.28178334f;
+    p = fmaf(p, q, 0.27960601f);
+    p = fmaf(p, q, 0.40024909f);
+    p = fmaf(p, q, 0.66666317f);
+    p = fmaf(p, q, 2.f);
+    return fmaf(s, p, fmaxf(v, 0.f));   // a NaN comes through s
 }
 
-// The gate's logistic function: for bf16 data one tanh.approx (relative error 2^-11, below the
-// data's own rounding of 2^-9), for fp32 data the full exponential and divide.
+// v silu(z).  The logistic function is (1 + tanh(z / 2)) / 2: for bf16 data one tanh.approx
+// (relative error 2^-11, below the data's own rounding of 2^-9), for fp32 data the full
+// exponential and divide.
 template <typename T>
-__device__ __forceinline__ float sel_sigmoid(float v) {
+__device__ __forceinline__ float sel_gate(float v, float z) {
     if (sizeof(T) == 2) {
+        const float u = 0.5f * z;
         float t;
-        asm("tanh.approx.f32 %0, %1;" : "=f"(t) : "f"(0.5f * v));
-        return fmaf(0.5f, t, 0.5f);
+        asm("tanh.approx.f32 %0, %1;" : "=f"(t) : "f"(u));
+        return v * fmaf(u, t, u);
     }
-    return 1.f / (1.f + expf(-v));
+    return v * z / (1.f + expf(-z));
+}
+
+// ---- four neighbouring elements: a thread's share of a row in the elementwise steps.  vec: the rows'
+// addresses allow one access for all four; n: how many of them exist.
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// to shared memory in the background (one by one and at once where four do not go)
+template <typename U>
+__device__ __forceinline__ void fetch4(U *dst, const U *src, int n, bool vec) {
+    if (n == 4 && vec) {
+        cp_async_small<4 * sizeof(U)>(dst, src);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) dst[i] = src[i];
+    }
+}
+// as they lie in memory (two bf16 to a register)
+template <typename U>
+struct Raw4;
+template <>
+struct Raw4<float> {
+    float4 v;
+    __device__ __forceinline__ void f(float (&o)[4]) const { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
+    __device__ __forceinline__ void load(const float *p, int n, bool vec) {
+        if (n == 4 && vec) v = *reinterpret_cast<const float4 *>(p);
+        else v = make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
+    }
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ void f(float (&o)[4]) const {
+        o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xffff0000u);
+        o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xffff0000u);
+    }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int n, bool vec) {
+        if (n == 4 && vec) {
+            v = *reinterpret_cast<const uint2 *>(p);
+        } else {
+            const unsigned short *u = reinterpret_cast<const unsigned short *>(p);
+            v.x = (n > 0 ? u[0] : 0u) | (n > 1 ? (uint32_t)u[1] << 16 : 0u);
+            v.y = (n > 2 ? u[2] : 0u) | (n > 3 ? (uint32_t)u[3] << 16 : 0u);
+        }
+    }
+};
+__device__ __forceinline__ void put4(float *p, const float (&v)[4]) { *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ void put4(__nv_bfloat16 *p, const float (&v)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+template <typename U>
+__device__ __forceinline__ void store4(U *p, const float (&v)[4], int n, bool vec) {
+    if (n == 4 && vec) {
+        put4(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = from_f<U>(v[i]);
+    }
+}
+// p moved on by t rows of `bytes` bytes (one wide multiply-add; the library bounds the strides)
+template <typename U>
+__device__ __forceinline__ U *row(U *p, int t, int bytes) {
+    return reinterpret_cast<U *>(reinterpret_cast<uintptr_t>(p) + (int64_t)t * bytes);
 }
 
 __device__ __forceinline__ float ld_dt(const SelArgs &a, int64_t at) {

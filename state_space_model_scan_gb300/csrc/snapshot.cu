@@ -13,7 +13,13 @@ namespace ssd {
 
 namespace {
 
-constexpr int SN_NT = 256, SN_RU = 2;   // threads, rows in flight per lane group
+#ifndef SNAP_RU
+#define SNAP_RU 4
+#endif
+#ifndef SNAP_RL
+#define SNAP_RL 4
+#endif
+constexpr int SN_NT = 256;   // threads
 
 struct SnapArgs {
     void *states;
@@ -22,7 +28,7 @@ struct SnapArgs {
     float *scale;
     int64_t nslots, nsnaps, stride, rows;
     int N, lpr;
-    int64_t nrb;                         // row blocks per state
+    int nrb;                             // row blocks per state
 };
 
 __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
@@ -59,14 +65,14 @@ __device__ __forceinline__ void st4s(__nv_bfloat16 *p, const float (&v)[4]) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
-// Where this thread's rows are: false when either index of its pair is out of range.
-template <typename ST>
+// Where this thread's rows are, RU of them rpw apart: false when either index of its pair is out of range.
+template <int RU, typename ST>
 __device__ __forceinline__ bool place(const SnapArgs &a, int64_t &r0, int &l, int &rpw, ST *&st, int8_t *&q, float *&sc) {
-    const int64_t i = blockIdx.x / a.nrb, rb = blockIdx.x % a.nrb;
+    const int i = blockIdx.x / a.nrb, rb = blockIdx.x % a.nrb;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     l = lane & (a.lpr - 1);
     rpw = 32 / a.lpr;
-    r0 = (rb * (SN_NT / 32) + w) * rpw * SN_RU + lane / a.lpr;
+    r0 = ((int64_t)rb * (SN_NT / 32) + w) * rpw * RU + lane / a.lpr;
     const int64_t s = a.sidx ? a.sidx[i] : i, k = a.qidx ? a.qidx[i] : i;
     if (s < 0 || s >= a.nslots || k < 0 || k >= a.nsnaps) return false;
     st = static_cast<ST *>(a.states) + s * a.stride;
@@ -75,21 +81,21 @@ __device__ __forceinline__ bool place(const SnapArgs &a, int64_t &r0, int &l, in
     return true;
 }
 
-// NV pieces of 4 values a lane in registers; NV = 0: single values, read twice.
-template <typename ST, int NV>
+// NV pieces of 4 values a lane in registers; NV = 0: single values, read twice.  The loads of RU rows
+// are issued before the first is used.
+template <typename ST, int NV, int RU>
 __global__ void __launch_bounds__(SN_NT) k_snap_store(const SnapArgs a) {
     int64_t r0;
     int l, rpw;
     ST *st;
     int8_t *q;
     float *sc;
-    if (!place<ST>(a, r0, l, rpw, st, q, sc)) return;
+    if (!place<RU>(a, r0, l, rpw, st, q, sc)) return;
     const int N = a.N;
-    constexpr int NR = NV > 0 ? NV : 1;
-    float v[SN_RU][NR][4];
+    float v[RU][NV > 0 ? NV : 1][4];
     if (NV > 0) {
 #pragma unroll
-        for (int u = 0; u < SN_RU; ++u)
+        for (int u = 0; u < RU; ++u)
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int n = (k * a.lpr + l) * 4;
@@ -98,7 +104,7 @@ __global__ void __launch_bounds__(SN_NT) k_snap_store(const SnapArgs a) {
             }
     }
 #pragma unroll
-    for (int u = 0; u < SN_RU; ++u) {
+    for (int u = 0; u < RU; ++u) {
         const int64_t r = r0 + u * rpw;
         const bool in = r < a.rows;
         uint32_t m = 0;
@@ -134,33 +140,40 @@ __global__ void __launch_bounds__(SN_NT) k_snap_store(const SnapArgs a) {
     }
 }
 
-template <typename ST, bool VEC>
+template <typename ST, bool VEC, int RU>
 __global__ void __launch_bounds__(SN_NT) k_snap_load(const SnapArgs a) {
     int64_t r0;
     int l, rpw;
     ST *st;
     int8_t *q;
     float *sc;
-    if (!place<ST>(a, r0, l, rpw, st, q, sc)) return;
+    if (!place<RU>(a, r0, l, rpw, st, q, sc)) return;
+    for (int n = l * (VEC ? 4 : 1); n < a.N; n += a.lpr * (VEC ? 4 : 1)) {
+        char4 c[RU];
+        float s[RU];
 #pragma unroll
-    for (int u = 0; u < SN_RU; ++u) {
-        const int64_t r = r0 + u * rpw;
-        if (r >= a.rows) break;
-        const float s = sc[r];
-        if (VEC) {
-            for (int n = l * 4; n < a.N; n += a.lpr * 4) {
-                const char4 c = *reinterpret_cast<const char4 *>(q + r * a.N + n);
-                const float v[4] = {c.x * s, c.y * s, c.z * s, c.w * s};
-                st4s(st + r * a.N + n, v);
+        for (int u = 0; u < RU; ++u) {
+            const int64_t r = r0 + u * rpw;
+            if (r < a.rows) {
+                s[u] = sc[r];
+                if (VEC) c[u] = *reinterpret_cast<const char4 *>(q + r * a.N + n);
+                else c[u].x = q[r * a.N + n];
             }
-        } else {
-            for (int n = l; n < a.N; n += a.lpr) st[r * a.N + n] = from_f<ST>(q[r * a.N + n] * s);
+        }
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+            const int64_t r = r0 + u * rpw;
+            if (r < a.rows) {
+                const float v[4] = {c[u].x * s[u], c[u].y * s[u], c[u].z * s[u], c[u].w * s[u]};
+                if (VEC) st4s(st + r * a.N + n, v);
+                else st[r * a.N + n] = from_f<ST>(v[0]);
+            }
         }
     }
 }
 
 ssd_status make(const ssd_snapshot_problem *p, const void *states, const int32_t *sidx, const int8_t *q,
-                const float *scales, const int32_t *slots, SnapArgs &a, bool &vec, unsigned &grid) {
+                const float *scales, const int32_t *slots, int ru, SnapArgs &a, bool &vec, unsigned &grid) {
     if (p == nullptr || p->count < 0 || p->rows < 1 || p->dstate < 1 || p->nslots < 0 || p->nsnapshots < 0 || p->reserved != 0)
         return SSD_ERR_INVALID_ARGUMENT;
     if (p->state_dtype != SSD_F32 && p->state_dtype != SSD_BF16) return SSD_ERR_INVALID_ARGUMENT;
@@ -177,26 +190,28 @@ ssd_status make(const ssd_snapshot_problem *p, const void *states, const int32_t
     vec = a.N % 4 == 0 && (uintptr_t)states % (4 * es) == 0 && (uintptr_t)q % 4 == 0 && (a.stride % 4 == 0 || a.nslots == 1);
     a.lpr = 1;
     while (a.lpr < 32 && a.lpr * (vec ? 4 : 1) < a.N) a.lpr <<= 1;
-    const int64_t per = (int64_t)(SN_NT / 32) * (32 / a.lpr) * SN_RU;
-    a.nrb = (a.rows + per - 1) / per;
-    if (a.nrb * p->count > ((int64_t)1 << 31) - 1) return SSD_ERR_UNSUPPORTED;
-    grid = (unsigned)(a.nrb * p->count);
+    const int64_t per = (int64_t)(SN_NT / 32) * (32 / a.lpr) * ru, nrb = (a.rows + per - 1) / per;
+    if (nrb * p->count > ((int64_t)1 << 31) - 1) return SSD_ERR_UNSUPPORTED;
+    a.nrb = (int)nrb;
+    grid = (unsigned)(nrb * p->count);
     return SSD_OK;
 }
+
+constexpr int kStoreRows = SNAP_RU, kLoadRows = SNAP_RL;   // rows in flight per lane group
 
 template <typename ST>
 void store(const SnapArgs &a, bool vec, unsigned grid, cudaStream_t st) {
     const int nv = vec ? (a.N + 4 * a.lpr - 1) / (4 * a.lpr) : 0;
-    if (nv == 0) k_snap_store<ST, 0><<<grid, SN_NT, 0, st>>>(a);
-    else if (nv == 1) k_snap_store<ST, 1><<<grid, SN_NT, 0, st>>>(a);
-    else if (nv == 2) k_snap_store<ST, 2><<<grid, SN_NT, 0, st>>>(a);
-    else if (nv <= 4) k_snap_store<ST, 4><<<grid, SN_NT, 0, st>>>(a);
-    else k_snap_store<ST, 8><<<grid, SN_NT, 0, st>>>(a);
+    if (nv == 0) k_snap_store<ST, 0, kStoreRows><<<grid, SN_NT, 0, st>>>(a);
+    else if (nv == 1) k_snap_store<ST, 1, kStoreRows><<<grid, SN_NT, 0, st>>>(a);
+    else if (nv == 2) k_snap_store<ST, 2, kStoreRows><<<grid, SN_NT, 0, st>>>(a);
+    else if (nv <= 4) k_snap_store<ST, 4, kStoreRows><<<grid, SN_NT, 0, st>>>(a);
+    else k_snap_store<ST, 8, kStoreRows><<<grid, SN_NT, 0, st>>>(a);
 }
 template <typename ST>
 void load(const SnapArgs &a, bool vec, unsigned grid, cudaStream_t st) {
-    if (vec) k_snap_load<ST, true><<<grid, SN_NT, 0, st>>>(a);
-    else k_snap_load<ST, false><<<grid, SN_NT, 0, st>>>(a);
+    if (vec) k_snap_load<ST, true, kLoadRows><<<grid, SN_NT, 0, st>>>(a);
+    else k_snap_load<ST, false, kLoadRows><<<grid, SN_NT, 0, st>>>(a);
 }
 
 }  // namespace
@@ -211,7 +226,7 @@ ssd_status ssd_snapshot_store(const ssd_snapshot_problem *p, const void *states,
     SnapArgs a{};
     bool vec = false;
     unsigned grid = 0;
-    const ssd_status s = make(p, states, state_indices, snapshots, scales, slots, a, vec, grid);
+    const ssd_status s = make(p, states, state_indices, snapshots, scales, slots, kStoreRows, a, vec, grid);
     if (s != SSD_OK || grid == 0) return s;
     if (p->state_dtype == SSD_BF16) store<__nv_bfloat16>(a, vec, grid, (cudaStream_t)stream);
     else store<float>(a, vec, grid, (cudaStream_t)stream);
@@ -223,7 +238,7 @@ ssd_status ssd_snapshot_load(const ssd_snapshot_problem *p, const int8_t *snapsh
     SnapArgs a{};
     bool vec = false;
     unsigned grid = 0;
-    const ssd_status s = make(p, states, state_indices, snapshots, scales, slots, a, vec, grid);
+    const ssd_status s = make(p, states, state_indices, snapshots, scales, slots, kLoadRows, a, vec, grid);
     if (s != SSD_OK || grid == 0) return s;
     if (p->state_dtype == SSD_BF16) load<__nv_bfloat16>(a, vec, grid, (cudaStream_t)stream);
     else load<float>(a, vec, grid, (cudaStream_t)stream);

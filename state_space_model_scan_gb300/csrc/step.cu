@@ -7,7 +7,8 @@
 // bounds it.  The state is taken as segments of rows of dstate values: a segment is a head (its
 // rows share A and dt) or a B/C group of the selective form (each row a channel with its own).  A row
 // belongs to LPR lanes, each with NV pieces of V values (16 bytes where rows allow it); a
-// warp issues the loads of RU rows per lane group before it uses the first.
+// warp issues the loads of RU rows per lane group before it uses the first, and sums their outputs
+// over the lanes together.
 #include <algorithm>
 
 #include "selective.cuh"
@@ -16,7 +17,10 @@ namespace ssd {
 
 namespace {
 
-constexpr int ST_NT = 128;
+#ifndef STEP_NT
+#define STEP_NT 128
+#endif
+constexpr int ST_NT = STEP_NT;
 
 struct StepArgs {
     void *state;
@@ -34,7 +38,7 @@ template <int V>
 struct Piece {
     float v[V];
 };
-// A piece is one value, or 16 bytes of state: 4 fp32 or 8 bf16 (and the 8 fp32 of A beside them).
+// A piece is one value, or 16 bytes of state: 4 fp32 or 8 bf16 (and as many values of A, B and C).
 template <int V>
 __device__ __forceinline__ void ldp(const float *p, Piece<V> &o) {
     if constexpr (V == 1) {
@@ -51,6 +55,10 @@ template <int V>
 __device__ __forceinline__ void ldp(const __nv_bfloat16 *p, Piece<V> &o) {
     if constexpr (V == 1) {
         o.v[0] = __bfloat162float(*p);
+    } else if constexpr (V == 4) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        o.v[0] = __uint_as_float(u.x << 16); o.v[1] = __uint_as_float(u.x & 0xffff0000u);
+        o.v[2] = __uint_as_float(u.y << 16); o.v[3] = __uint_as_float(u.y & 0xffff0000u);
     } else {
         const uint4 u = *reinterpret_cast<const uint4 *>(p);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -98,76 +106,94 @@ __global__ void __launch_bounds__(ST_NT) k_step(const StepArgs a) {
         return;
     }
     ST *st = static_cast<ST *>(a.state) + slot * a.slot_stride + first * N;
-    const T *B = static_cast<const T *>(a.B) + b * a.bs + (int64_t)(seg / a.spg) * N;
-    const T *C = static_cast<const T *>(a.C) + b * a.cs + (int64_t)(seg / a.spg) * N;
-    Piece<V> h[RU][NV];
+    const T *x = static_cast<const T *>(a.x) + b * a.xs + first;
+    // every load first: the stores below would hold up later ones
+    Piece<V> h[RU][NV], Av[ROW_A ? RU : 1][NV], Bv[NV], Cv[NV];
+    float xv[RU], dt[ROW_A ? RU : 1];
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
         const int r = r0 + u * rpw;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int n = (k * a.lpr + l) * V;
-            if (r < a.rows && n < N) ldp<V>(st + (int64_t)r * N + n, h[u][k]);
+            if (r < a.rows && n < N) {
+                ldp<V>(st + (int64_t)r * N + n, h[u][k]);
+                if (ROW_A) ldp<V>(a.A + (first + r) * N + n, Av[ROW_A ? u : 0][k]);
+            }
         }
     }
-    Piece<V> Bv[NV], Cv[NV];
+    const T *B = static_cast<const T *>(a.B) + b * a.bs + (int64_t)(seg / a.spg) * N;
+    const T *C = static_cast<const T *>(a.C) + b * a.cs + (int64_t)(seg / a.spg) * N;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int n = (k * a.lpr + l) * V;
         if (n < N) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                Bv[k].v[e] = to_f(B[n + e]);
-                Cv[k].v[e] = to_f(C[n + e]);
-            }
+            ldp<V>(B + n, Bv[k]);
+            ldp<V>(C + n, Cv[k]);
         }
     }
-    float dt = 0.f, decay = 0.f;
-    if (!ROW_A) {
-        dt = sel_softplus((a.dt_f32 ? static_cast<const float *>(a.dt)[b * a.dts + seg]
-                                    : to_f(static_cast<const T *>(a.dt)[b * a.dts + seg])) +
-                          (a.bias ? a.bias[seg] : 0.f));
-        decay = ex2f(dt * a.A[seg] * kLog2e);
-    }
-    const T *x = static_cast<const T *>(a.x) + b * a.xs + first;
-    const T *z = a.z ? static_cast<const T *>(a.z) + b * a.zs + first : nullptr;
+    auto load_dt = [&](int64_t at, int64_t par) {
+        return (a.dt_f32 ? static_cast<const float *>(a.dt)[at] : to_f(static_cast<const T *>(a.dt)[at])) + (a.bias ? a.bias[par] : 0.f);
+    };
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
         const int r = r0 + u * rpw;
-        const bool in = r < a.rows;
-        float acc = 0.f, xv = 0.f;
-        if (in) {
-            xv = to_f(x[r]);
-            if (ROW_A) {
-                const int64_t at = b * a.dts + first + r;
-                dt = sel_softplus((a.dt_f32 ? static_cast<const float *>(a.dt)[at] : to_f(static_cast<const T *>(a.dt)[at])) +
-                                  (a.bias ? a.bias[first + r] : 0.f));
-            }
-            const float dtx = dt * xv, dtl = dt * kLog2e;
+        xv[u] = r < a.rows ? to_f(x[r]) : 0.f;
+        if (ROW_A) dt[ROW_A ? u : 0] = r < a.rows ? load_dt(b * a.dts + first + r, first + r) : 0.f;
+    }
+    if (!ROW_A) dt[0] = load_dt(b * a.dts + seg, seg);
+    // where a row has at least RU lanes, lane u finishes row u; else its first lane every row
+    const bool spread = a.lpr >= RU;
+    const int ru = r0 + (spread ? l : 0) * rpw;
+    const bool fin = (spread ? l < RU : l == 0) && ru < a.rows;
+    float zu = 0.f, xu = 0.f, Du = 0.f;
+    if (spread && fin) {
+        if (a.z) zu = to_f(static_cast<const T *>(a.z)[b * a.zs + first + ru]);
+        if (a.D) {
+            Du = a.D[ROW_A ? first + ru : seg];
+            xu = to_f(x[ru]);
+        }
+    }
+    float acc[RU];
+    const float d0 = ROW_A ? 0.f : sel_softplus(dt[0]), decay = ROW_A ? 0.f : ex2f(d0 * a.A[seg] * kLog2e);
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+        const int r = r0 + u * rpw;
+        acc[u] = 0.f;
+        if (r < a.rows) {
+            const float dv = ROW_A ? sel_softplus(dt[ROW_A ? u : 0]) : d0, dtx = dv * xv[u], dtl = dv * kLog2e;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int n = (k * a.lpr + l) * V;
                 if (n < N) {
-                    Piece<V> Av;
-                    if (ROW_A) ldp<V>(a.A + (first + r) * N + n, Av);
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        const float d = ROW_A ? ex2f(dtl * Av.v[e]) : decay;
+                        const float d = ROW_A ? ex2f(dtl * Av[ROW_A ? u : 0][k].v[e]) : decay;
                         h[u][k].v[e] = fmaf(d, h[u][k].v[e], dtx * Bv[k].v[e]);
-                        acc = fmaf(Cv[k].v[e], h[u][k].v[e], acc);
+                        acc[u] = fmaf(Cv[k].v[e], h[u][k].v[e], acc[u]);
                     }
                     stp<V>(st + (int64_t)r * N + n, h[u][k]);
                 }
             }
         }
-        for (int o = a.lpr >> 1; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-        if (in && l == 0) {
-            if (a.D) acc = fmaf(a.D[ROW_A ? first + r : seg], xv, acc);
-            if (z) {
-                const float zv = to_f(z[r]);
-                acc *= zv * sel_sigmoid<T>(zv);
+    }
+    if (spread) {
+        float v = reduce_scatter<RU>(acc, l & (RU - 1));
+        for (int o = RU; o < a.lpr; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (fin) {
+            v = fmaf(Du, xu, v);
+            y[ru] = from_f<T>(a.z ? sel_gate<T>(v, zu) : v);
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+            for (int o = a.lpr >> 1; o > 0; o >>= 1) acc[u] += __shfl_xor_sync(0xffffffffu, acc[u], o);
+            const int r = r0 + u * rpw;
+            if (l == 0 && r < a.rows) {
+                float v = a.D ? fmaf(a.D[ROW_A ? first + r : seg], xv[u], acc[u]) : acc[u];
+                if (a.z) v = sel_gate<T>(v, to_f(static_cast<const T *>(a.z)[b * a.zs + first + r]));
+                y[r] = from_f<T>(v);
             }
-            y[r] = from_f<T>(acc);
         }
     }
 }
@@ -186,12 +212,16 @@ template <typename T, typename ST, bool ROW_A>
 cudaError_t pick(const StepArgs &a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(ST);
     const bool vec = a.N % V == 0 && (uintptr_t)a.state % 16 == 0 && a.slot_stride % V == 0 &&
-                     (!ROW_A || (uintptr_t)a.A % 16 == 0);
+                     (!ROW_A || (uintptr_t)a.A % 16 == 0) && (uintptr_t)a.B % (V * sizeof(T)) % 16 == 0 &&
+                     (uintptr_t)a.C % (V * sizeof(T)) % 16 == 0 && a.bs % V == 0 && a.cs % V == 0;
     if (!vec) return launch<T, ST, 1, 8, 1, ROW_A>(a, st);
+#ifndef STEP_RU
+#define STEP_RU 4
+#endif
     if constexpr (V == 4) {
         if (a.N > 32 * V) return launch<T, ST, V, 2, 2, ROW_A>(a, st);
     }
-    return launch<T, ST, V, 1, 4, ROW_A>(a, st);
+    return launch<T, ST, V, 1, STEP_RU, ROW_A>(a, st);
 }
 template <bool ROW_A>
 cudaError_t pick_types(const StepArgs &a, bool bf16, bool st_bf16, cudaStream_t st) {
