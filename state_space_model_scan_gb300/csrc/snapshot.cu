@@ -2,9 +2,9 @@
 // q = round_half_even(h 127 / m) and the scale m / 127, m = max |h|.  Bytes bound it: 4 or 2 read
 // and 1 written per value, or the other way round.
 //
-// The maximum is taken over the values' bit patterns without the sign: as integers they are
-// ordered like the magnitudes, with infinity and then every NaN above all finite ones, so that
-// one comparison finds rows that cannot be kept.
+// A row belongs to LPR lanes, each with NV pieces of four values, so that one exchange of the maximum
+// serves 16 values a lane.  The maximum lets a NaN through, so that one comparison finds rows that
+// cannot be kept; q is rounded by adding 1.5 x 2^23, whose last byte then is the integer.
 #include <algorithm>
 
 #include "common.cuh"
@@ -13,13 +13,7 @@ namespace ssd {
 
 namespace {
 
-#ifndef SNAP_RU
-#define SNAP_RU 4
-#endif
-#ifndef SNAP_RL
-#define SNAP_RL 4
-#endif
-constexpr int SN_NT = 256;   // threads
+constexpr int SN_NT = 128;   // threads
 
 struct SnapArgs {
     void *states;
@@ -31,24 +25,29 @@ struct SnapArgs {
     int nrb;                             // row blocks per state
 };
 
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-constexpr uint32_t kInfBits = 0x7f800000u;
+__device__ __forceinline__ float max_nan(float a, float b) {   // a NaN wins
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 constexpr float kTiny = 1e-30f;          // below it 127 / m nears the end of fp32's range
 
-// inverse step and scale of a row with largest magnitude bits m
-__device__ __forceinline__ void row_scale(uint32_t m, float &inv, float &scale) {
-    const float v = __uint_as_float(m);
-    if (m >= kInfBits) {
+// inverse step and scale of a row whose largest magnitude is m
+__device__ __forceinline__ void row_scale(float m, float &inv, float &scale) {
+    if (!(m < __int_as_float(0x7f800000))) {
         inv = 0.f;
-        scale = __uint_as_float(0x7fc00000u);
-    } else if (v < kTiny) {
+        scale = __int_as_float(0x7fc00000);
+    } else if (m < kTiny) {
         inv = scale = 0.f;
     } else {
-        inv = __fdiv_rn(127.f, v);
-        scale = __fdiv_rn(v, 127.f);
+        inv = __fdiv_rn(127.f, m);
+        scale = __fdiv_rn(m, 127.f);
     }
 }
-__device__ __forceinline__ int quant(float h, float inv) { return inv == 0.f ? 0 : __float2int_rn(__fmul_rn(h, inv)); }
+// round_half_even(h inv) in the last byte; |h inv| <= 127 (1 + 2^-23)
+__device__ __forceinline__ uint32_t quant(float h, float inv) {
+    return __float_as_uint(__fadd_rn(__fmul_rn(h, inv), 12582912.f));
+}
 
 __device__ __forceinline__ void ld4s(const float *p, float (&v)[4]) {
     const float4 u = *reinterpret_cast<const float4 *>(p);
@@ -81,8 +80,7 @@ __device__ __forceinline__ bool place(const SnapArgs &a, int64_t &r0, int &l, in
     return true;
 }
 
-// NV pieces of 4 values a lane in registers; NV = 0: single values, read twice.  The loads of RU rows
-// are issued before the first is used.
+// The loads of RU rows of NV pieces a lane are issued before the first is used.
 template <typename ST, int NV, int RU>
 __global__ void __launch_bounds__(SN_NT) k_snap_store(const SnapArgs a) {
     int64_t r0;
@@ -92,55 +90,42 @@ __global__ void __launch_bounds__(SN_NT) k_snap_store(const SnapArgs a) {
     float *sc;
     if (!place<RU>(a, r0, l, rpw, st, q, sc)) return;
     const int N = a.N;
-    float v[RU][NV > 0 ? NV : 1][4];
-    if (NV > 0) {
+    float v[RU][NV][4];
 #pragma unroll
-        for (int u = 0; u < RU; ++u)
+    for (int u = 0; u < RU; ++u) {
+        const int64_t r = r0 + u * rpw;
+        const ST *p = st + r * N + l * 4;
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int n = (k * a.lpr + l) * 4;
-                const int64_t r = r0 + u * rpw;
-                if (r < a.rows && n < N) ld4s(st + r * N + n, v[u][k]);
-            }
+        for (int k = 0; k < NV; ++k) {
+            if (r < a.rows && (k * a.lpr + l) * 4 < N) ld4s(p + k * a.lpr * 4, v[u][k]);
+            else v[u][k][0] = v[u][k][1] = v[u][k][2] = v[u][k][3] = 0.f;
+        }
     }
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
         const int64_t r = r0 + u * rpw;
-        const bool in = r < a.rows;
-        uint32_t m = 0;
-        if (NV > 0) {
+        float m = 0.f;
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-                if (in && (k * a.lpr + l) * 4 < N) {
+        for (int k = 0; k < NV; ++k)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) m = max(m, mag(v[u][k][e]));
-                }
-        } else if (in) {
-            for (int n = l; n < N; n += a.lpr) m = max(m, mag(to_f(st[r * N + n])));
-        }
-        for (int o = a.lpr >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (!in) continue;
+            for (int e = 0; e < 4; ++e) m = max_nan(m, fabsf(v[u][k][e]));
+        for (int o = a.lpr >> 1; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (r >= a.rows) continue;
         float inv, scale;
         row_scale(m, inv, scale);
         if (l == 0) sc[r] = scale;
-        if (NV > 0) {
+        int8_t *o = q + r * N + l * 4;
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int n = (k * a.lpr + l) * 4;
-                if (n < N) {
-                    uint32_t p = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p |= (uint32_t)(quant(v[u][k][e], inv) & 0xff) << (8 * e);
-                    *reinterpret_cast<uint32_t *>(q + r * N + n) = p;
-                }
+        for (int k = 0; k < NV; ++k)
+            if ((k * a.lpr + l) * 4 < N) {
+                const uint32_t lo = __byte_perm(quant(v[u][k][0], inv), quant(v[u][k][1], inv), 0x0040);
+                const uint32_t hi = __byte_perm(quant(v[u][k][2], inv), quant(v[u][k][3], inv), 0x0040);
+                *reinterpret_cast<uint32_t *>(o + k * a.lpr * 4) = inv == 0.f ? 0u : __byte_perm(lo, hi, 0x5410);
             }
-        } else {
-            for (int n = l; n < N; n += a.lpr) q[r * N + n] = (int8_t)quant(to_f(st[r * N + n]), inv);
-        }
     }
 }
 
-template <typename ST, bool VEC, int RU>
+template <typename ST, int NV, int RU>
 __global__ void __launch_bounds__(SN_NT) k_snap_load(const SnapArgs a) {
     int64_t r0;
     int l, rpw;
@@ -148,32 +133,82 @@ __global__ void __launch_bounds__(SN_NT) k_snap_load(const SnapArgs a) {
     int8_t *q;
     float *sc;
     if (!place<RU>(a, r0, l, rpw, st, q, sc)) return;
-    for (int n = l * (VEC ? 4 : 1); n < a.N; n += a.lpr * (VEC ? 4 : 1)) {
-        char4 c[RU];
-        float s[RU];
+    const int N = a.N;
+    char4 c[RU][NV];
+    float s[RU];
 #pragma unroll
-        for (int u = 0; u < RU; ++u) {
-            const int64_t r = r0 + u * rpw;
-            if (r < a.rows) {
-                s[u] = sc[r];
-                if (VEC) c[u] = *reinterpret_cast<const char4 *>(q + r * a.N + n);
-                else c[u].x = q[r * a.N + n];
-            }
+    for (int u = 0; u < RU; ++u) {
+        const int64_t r = r0 + u * rpw;
+        if (r < a.rows) {
+            s[u] = sc[r];
+            const int8_t *p = q + r * N + l * 4;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if ((k * a.lpr + l) * 4 < N) c[u][k] = *reinterpret_cast<const char4 *>(p + k * a.lpr * 4);
         }
+    }
 #pragma unroll
-        for (int u = 0; u < RU; ++u) {
-            const int64_t r = r0 + u * rpw;
-            if (r < a.rows) {
-                const float v[4] = {c[u].x * s[u], c[u].y * s[u], c[u].z * s[u], c[u].w * s[u]};
-                if (VEC) st4s(st + r * a.N + n, v);
-                else st[r * a.N + n] = from_f<ST>(v[0]);
-            }
+    for (int u = 0; u < RU; ++u) {
+        const int64_t r = r0 + u * rpw;
+        if (r < a.rows) {
+            ST *p = st + r * N + l * 4;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if ((k * a.lpr + l) * 4 < N) {
+                    const float v[4] = {c[u][k].x * s[u], c[u][k].y * s[u], c[u][k].z * s[u], c[u][k].w * s[u]};
+                    st4s(p + k * a.lpr * 4, v);
+                }
         }
     }
 }
 
+// Rows that do not allow four values an access: single ones, read twice.
+template <typename ST>
+__global__ void __launch_bounds__(SN_NT) k_snap_store1(const SnapArgs a) {
+    int64_t r;
+    int l, rpw;
+    ST *st;
+    int8_t *q;
+    float *sc;
+    if (!place<1>(a, r, l, rpw, st, q, sc)) return;
+    const bool in = r < a.rows;
+    float m = 0.f;
+    if (in)
+        for (int n = l; n < a.N; n += a.lpr) m = max_nan(m, fabsf(to_f(st[r * a.N + n])));
+    for (int o = a.lpr >> 1; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (!in) return;
+    float inv, scale;
+    row_scale(m, inv, scale);
+    if (l == 0) sc[r] = scale;
+    for (int n = l; n < a.N; n += a.lpr) q[r * a.N + n] = inv == 0.f ? 0 : (int8_t)(quant(to_f(st[r * a.N + n]), inv) & 0xff);
+}
+template <typename ST>
+__global__ void __launch_bounds__(SN_NT) k_snap_load1(const SnapArgs a) {
+    int64_t r;
+    int l, rpw;
+    ST *st;
+    int8_t *q;
+    float *sc;
+    if (!place<1>(a, r, l, rpw, st, q, sc) || r >= a.rows) return;
+    const float s = sc[r];
+    for (int n = l; n < a.N; n += a.lpr) st[r * a.N + n] = from_f<ST>(q[r * a.N + n] * s);
+}
+
+// How a row is cut: pieces a lane and rows in flight (0: single values).  At dstate 64 and above four pieces
+// a lane, so that a row's lanes still read 64 bytes or more at once.  Round trip of 96 states of 4096 rows x 128,
+// fp32: four pieces of one row 86 us, one piece of four rows to store and of eight to load 113 us.
+struct Cut {
+    int nv, ru;
+};
+Cut cut(bool vec, int N) {
+    if (!vec) return {0, 1};
+    if (N > 512) return {8, 1};
+    if (N >= 64) return {4, 1};
+    return {1, 4};
+}
+
 ssd_status make(const ssd_snapshot_problem *p, const void *states, const int32_t *sidx, const int8_t *q,
-                const float *scales, const int32_t *slots, int ru, SnapArgs &a, bool &vec, unsigned &grid) {
+                const float *scales, const int32_t *slots, SnapArgs &a, Cut &how, unsigned &grid) {
     if (p == nullptr || p->count < 0 || p->rows < 1 || p->dstate < 1 || p->nslots < 0 || p->nsnapshots < 0 || p->reserved != 0)
         return SSD_ERR_INVALID_ARGUMENT;
     if (p->state_dtype != SSD_F32 && p->state_dtype != SSD_BF16) return SSD_ERR_INVALID_ARGUMENT;
@@ -187,31 +222,30 @@ ssd_status make(const ssd_snapshot_problem *p, const void *states, const int32_t
     a.states = const_cast<void *>(states); a.sidx = sidx; a.qidx = slots; a.q = const_cast<int8_t *>(q);
     a.scale = const_cast<float *>(scales);
     a.nslots = p->nslots; a.nsnaps = p->nsnapshots; a.stride = p->state_stride; a.rows = p->rows; a.N = (int)p->dstate;
-    vec = a.N % 4 == 0 && (uintptr_t)states % (4 * es) == 0 && (uintptr_t)q % 4 == 0 && (a.stride % 4 == 0 || a.nslots == 1);
+    const bool vec = a.N % 4 == 0 && (uintptr_t)states % (4 * es) == 0 && (uintptr_t)q % 4 == 0 && (a.stride % 4 == 0 || a.nslots == 1);
     a.lpr = 1;
-    while (a.lpr < 32 && a.lpr * (vec ? 4 : 1) < a.N) a.lpr <<= 1;
-    const int64_t per = (int64_t)(SN_NT / 32) * (32 / a.lpr) * ru, nrb = (a.rows + per - 1) / per;
+    how = cut(vec, a.N);
+    while (a.lpr < 32 && a.lpr * (vec ? 4 * how.nv : 1) < a.N) a.lpr <<= 1;
+    const int64_t per = (int64_t)(SN_NT / 32) * (32 / a.lpr) * how.ru, nrb = (a.rows + per - 1) / per;
     if (nrb * p->count > ((int64_t)1 << 31) - 1) return SSD_ERR_UNSUPPORTED;
     a.nrb = (int)nrb;
     grid = (unsigned)(nrb * p->count);
     return SSD_OK;
 }
 
-constexpr int kStoreRows = SNAP_RU, kLoadRows = SNAP_RL;   // rows in flight per lane group
-
 template <typename ST>
-void store(const SnapArgs &a, bool vec, unsigned grid, cudaStream_t st) {
-    const int nv = vec ? (a.N + 4 * a.lpr - 1) / (4 * a.lpr) : 0;
-    if (nv == 0) k_snap_store<ST, 0, kStoreRows><<<grid, SN_NT, 0, st>>>(a);
-    else if (nv == 1) k_snap_store<ST, 1, kStoreRows><<<grid, SN_NT, 0, st>>>(a);
-    else if (nv == 2) k_snap_store<ST, 2, kStoreRows><<<grid, SN_NT, 0, st>>>(a);
-    else if (nv <= 4) k_snap_store<ST, 4, kStoreRows><<<grid, SN_NT, 0, st>>>(a);
-    else k_snap_store<ST, 8, kStoreRows><<<grid, SN_NT, 0, st>>>(a);
+void store(const SnapArgs &a, Cut how, unsigned grid, cudaStream_t st) {
+    if (how.nv == 0) k_snap_store1<ST><<<grid, SN_NT, 0, st>>>(a);
+    else if (how.nv == 1) k_snap_store<ST, 1, 4><<<grid, SN_NT, 0, st>>>(a);
+    else if (how.nv == 4) k_snap_store<ST, 4, 1><<<grid, SN_NT, 0, st>>>(a);
+    else k_snap_store<ST, 8, 1><<<grid, SN_NT, 0, st>>>(a);
 }
 template <typename ST>
-void load(const SnapArgs &a, bool vec, unsigned grid, cudaStream_t st) {
-    if (vec) k_snap_load<ST, true, kLoadRows><<<grid, SN_NT, 0, st>>>(a);
-    else k_snap_load<ST, false, kLoadRows><<<grid, SN_NT, 0, st>>>(a);
+void load(const SnapArgs &a, Cut how, unsigned grid, cudaStream_t st) {
+    if (how.nv == 0) k_snap_load1<ST><<<grid, SN_NT, 0, st>>>(a);
+    else if (how.nv == 1) k_snap_load<ST, 1, 4><<<grid, SN_NT, 0, st>>>(a);
+    else if (how.nv == 4) k_snap_load<ST, 4, 1><<<grid, SN_NT, 0, st>>>(a);
+    else k_snap_load<ST, 8, 1><<<grid, SN_NT, 0, st>>>(a);
 }
 
 }  // namespace
@@ -224,24 +258,24 @@ extern "C" {
 ssd_status ssd_snapshot_store(const ssd_snapshot_problem *p, const void *states, const int32_t *state_indices,
                               int8_t *snapshots, float *scales, const int32_t *slots, void *stream) {
     SnapArgs a{};
-    bool vec = false;
+    Cut how{};
     unsigned grid = 0;
-    const ssd_status s = make(p, states, state_indices, snapshots, scales, slots, kStoreRows, a, vec, grid);
+    const ssd_status s = make(p, states, state_indices, snapshots, scales, slots, a, how, grid);
     if (s != SSD_OK || grid == 0) return s;
-    if (p->state_dtype == SSD_BF16) store<__nv_bfloat16>(a, vec, grid, (cudaStream_t)stream);
-    else store<float>(a, vec, grid, (cudaStream_t)stream);
+    if (p->state_dtype == SSD_BF16) store<__nv_bfloat16>(a, how, grid, (cudaStream_t)stream);
+    else store<float>(a, how, grid, (cudaStream_t)stream);
     return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 ssd_status ssd_snapshot_load(const ssd_snapshot_problem *p, const int8_t *snapshots, const float *scales,
                              const int32_t *slots, void *states, const int32_t *state_indices, void *stream) {
     SnapArgs a{};
-    bool vec = false;
+    Cut how{};
     unsigned grid = 0;
-    const ssd_status s = make(p, states, state_indices, snapshots, scales, slots, kLoadRows, a, vec, grid);
+    const ssd_status s = make(p, states, state_indices, snapshots, scales, slots, a, how, grid);
     if (s != SSD_OK || grid == 0) return s;
-    if (p->state_dtype == SSD_BF16) load<__nv_bfloat16>(a, vec, grid, (cudaStream_t)stream);
-    else load<float>(a, vec, grid, (cudaStream_t)stream);
+    if (p->state_dtype == SSD_BF16) load<__nv_bfloat16>(a, how, grid, (cudaStream_t)stream);
+    else load<float>(a, how, grid, (cudaStream_t)stream);
     return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
