@@ -7,7 +7,6 @@ raise -- there is no fallback.
 """
 import ctypes
 import os
-import struct
 
 import torch
 
@@ -151,12 +150,6 @@ def load(path: str = LIB_PATH):
     lib.ssd_conv1d_prompt.argtypes = [P(ConvProblem), V, I64, I64, V, V, V, V, I64, I64, V, V, V, I64, I64, V]
     lib.ssd_conv1d_step.argtypes = [P(ConvProblem), V, I64, V, V, V, I64, I64, V, V, I64, V]
     lib.ssd_snapshot_store.argtypes = lib.ssd_snapshot_load.argtypes = [P(SnapshotProblem)] + [V] * 6
-    # the same functions for argument structs given as packed bytes
-    E = ctypes.c_int
-    lib.selective_fwd = ctypes.CFUNCTYPE(E, P(SelectiveProblem), V, V)(("ssd_selective_fwd", lib))
-    lib.selective_bwd = ctypes.CFUNCTYPE(E, P(SelectiveProblem), V, V, S, V)(("ssd_selective_bwd", lib))
-    lib.selective_bwd_workspace_size = ctypes.CFUNCTYPE(E, P(SelectiveProblem), V, V)(
-        ("ssd_selective_bwd_workspace_size", lib))
     for f in ("ssd_fwd_workspace_size", "ssd_fwd", "ssd_bwd_workspace_size", "ssd_bwd", "ssd_query_status",
               "ssd_fwd_debug_layout", "ssd_fwd_noalloc", "ssd_selftest_bounded_wait", "ssd_chunk_states_size",
               "ssd_noalloc_query_status", "ssd_varlen_metadata", "ssd_gated_norm_fwd",
@@ -399,89 +392,28 @@ def complex_fwd(prob, x, dt, A, B, C, init, y_re, y_im, final, workspace, stream
                                       _stream_handle(stream)))
 
 
-# The entry points below are called for single tokens, where a call's own time is mostly this binding's: addresses go
-# over as plain integers, and an argument struct is packed in one piece (its layout is FwdArgs', BwdArgs').
-_ABSENT = (0,) * 7
-_FWD = struct.Struct("=" + "Qii4q" * len(_FWD_FIELDS) + "QQ")
-_BWD = struct.Struct("=" + "Qii4q" * len(_FWD_FIELDS) + "QQ" + "Qii4q" * len(_BWD_FIELDS))
-assert _FWD.size == ctypes.sizeof(FwdArgs) and _BWD.size == ctypes.sizeof(BwdArgs)
-_CODES = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
-
-
-def packed(t, contiguous=False):
-    """The fields of an ssd_tensor.  contiguous: with the strides of a contiguous tensor, whatever torch notes for
-    dimensions of size 1."""
-    if t is None:
-        return _ABSENT
-    st = t.stride()
-    if contiguous:
-        st, n = list(st), 1
-        for k in range(len(st) - 1, -1, -1):
-            st[k] = n
-            n *= t.shape[k]
-    n = len(st)
-    if n == 3:
-        return (t.data_ptr(), _CODES[t.dtype], 0, st[0], st[1], st[2], 0)
-    if n == 1:
-        return (t.data_ptr(), _CODES[t.dtype], 0, st[0], 0, 0, 0)
-    if n == 2:
-        return (t.data_ptr(), _CODES[t.dtype], 0, st[0], st[1], 0, 0)
-    return (t.data_ptr(), _CODES[t.dtype], 0, st[0], st[1], st[2], st[3])
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _raw_stream(stream, t):
-    """A stream's handle; by default that of t's device's current stream."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
-
-
 def selective_chunk_states_size(prob):
     n = ctypes.c_size_t(0)
     check(load().ssd_selective_chunk_states_size(ctypes.byref(prob), ctypes.byref(n)), "ssd_selective_chunk_states_size")
     return int(n.value)
 
 
-def selective_fwd(prob, args, x, stream=None):
-    """args: the packed fields of an ssd_fwd_args."""
-    return load().selective_fwd(prob, _FWD.pack(*args), _raw_stream(stream, x))
+# ---- the compiled binding (csrc/binding.cpp) of the entry points that are called for single tokens
+_BINDING_ORDER = ["ssd_step", "ssd_selective_step", "ssd_conv1d_prompt", "ssd_conv1d_step", "ssd_snapshot_store",
+                  "ssd_snapshot_load", "ssd_selective_chunk_states_size", "ssd_selective_fwd",
+                  "ssd_selective_bwd_workspace_size", "ssd_selective_bwd"]
+_fast = None
 
 
-def selective_bwd_workspace_size(prob, args):
-    n = ctypes.c_size_t(0)
-    check(load().selective_bwd_workspace_size(prob, args, ctypes.byref(n)), "ssd_selective_bwd_workspace_size")
-    return int(n.value)
-
-
-def selective_bwd(prob, args, workspace, stream=None):
-    """args: the bytes of an ssd_bwd_args."""
-    return load().selective_bwd(prob, args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                _raw_stream(stream, workspace))
-
-
-def step(selective, prob, state, idx, x, dt, A, B, C, D, z, dt_bias, y, stream=None):
-    f = load().ssd_selective_step if selective else load().ssd_step
-    return f(prob, state.data_ptr(), _addr(idx), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
-             _addr(D), _addr(z), _addr(dt_bias), y.data_ptr(), _raw_stream(stream, x))
-
-
-def conv1d_prompt(prob, u, weight, bias, cu_seqlens, states, idx, has, out, stream=None):
-    return load().ssd_conv1d_prompt(prob, u.data_ptr(), u.stride(0), u.stride(1), weight.data_ptr(), _addr(bias),
-                                    _addr(cu_seqlens), states.data_ptr(), states.shape[0], states.stride(0), _addr(idx),
-                                    _addr(has), out.data_ptr(), out.stride(0), out.stride(1), _raw_stream(stream, u))
-
-
-def conv1d_step(prob, u, weight, bias, states, idx, out, stream=None):
-    return load().ssd_conv1d_step(prob, u.data_ptr(), u.stride(0), weight.data_ptr(), _addr(bias), states.data_ptr(),
-                                  states.shape[0], states.stride(0), _addr(idx), out.data_ptr(), out.stride(0),
-                                  _raw_stream(stream, u))
-
-
-def snapshot(store, prob, states, idx, q, scales, slots, stream=None):
-    if store:
-        return load().ssd_snapshot_store(prob, states.data_ptr(), _addr(idx), q.data_ptr(), scales.data_ptr(),
-                                         _addr(slots), _raw_stream(stream, states))
-    return load().ssd_snapshot_load(prob, q.data_ptr(), scales.data_ptr(), _addr(slots), states.data_ptr(), _addr(idx),
-                                    _raw_stream(stream, states))
+def fast():
+    """The module _binding, given the library's functions (raises if either has not been built)."""
+    global _fast
+    if _fast is None:
+        lib = load()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("the binding is not built: build it with state_space_model_scan_gb300.build.build() (%s)" % e)
+        _binding.init(SSDError, torch.OutOfMemoryError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _BINDING_ORDER))
+        _fast = _binding
+    return _fast

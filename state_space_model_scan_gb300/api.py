@@ -239,88 +239,11 @@ def complex_ssd_forward(x, A, B, C, dt, initial_states=None, chunk_size=64, retu
 
 # ---------------------------------------------------------------------------------------------
 # The selective scan, the convolution with a carried window, single-token steps and 8-bit
-# snapshots of states.  The library sees addresses and strides; that the tensors behind them have
-# the shapes, types and devices it assumes is checked here.
-_F32 = (torch.float32,)
-_ST = (torch.float32, torch.bfloat16)
-
-
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
-def _like(name, t, shape, dtypes, device, inner=0):
-    """t has this shape, one of these types and this device (its index), and its last `inner` dimensions are
-    contiguous."""
-    if t.shape == shape and t.dtype in dtypes and t.get_device() == device and t.is_contiguous():
-        return
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype not in dtypes:
-        raise ValueError("%s is %s, not %s" % (name, t.dtype, " or ".join(str(d) for d in dtypes)))
-    if t.get_device() != device:
-        raise ValueError("%s is on %s, not on GPU %d" % (name, t.device, device))
-    st, sh, n = t.stride(), t.shape, 1
-    for k in range(len(sh) - 1, len(sh) - 1 - inner, -1):
-        if sh[k] != 1 and st[k] != n:
-            raise ValueError("%s: its last %d dimensions must be contiguous" % (name, inner))
-        n *= sh[k]
-
-
-def _on_gpu(name, t):
-    """Index of the GPU that t is on."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError("%s is not on a GPU" % name)
-    if t.dtype not in _ST:
-        raise ValueError("%s is %s, not float32 or bfloat16" % (name, t.dtype))
-    return dev
-
-
-def _on(stream, *tensors):
-    """The caching allocator learns that `stream`, where it is not the current one, uses what was allocated here."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-
-
-def _last_is_one(f, k):
-    """The stride of dimension k in packed fields, set to 1: a dimension of size 1 may have noted any."""
-    return f if f[3 + k] == 1 else f[:3 + k] + (1,) + f[4 + k:]
-
-
-def _selective_args(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens):
-    """The problem, the packed fields of the inputs (x .. initial_states) and the number of sequences."""
-    _need(x.dim() == 3 and B.dim() == 4, "x has shape [batch, seqlen, channels], B [batch, seqlen, ngroups, dstate]")
-    shape = x.shape
-    Bt, L, Dm = shape
-    G, N = B.shape[2:]
-    dev, own = _on_gpu("x", x), (x.dtype,)
-    S = Bt
-    if cu_seqlens is not None:
-        S = cu_seqlens.numel() - 1
-        _need(S >= 1, "cu_seqlens holds no sequence")
-        _like("cu_seqlens", cu_seqlens, (S + 1,), (torch.int32,), dev, 1)
-    _like("x", x, shape, own, dev, 1)
-    _like("dt", dt, shape, (torch.float32, x.dtype), dev, 1)
-    _like("A", A, (Dm, N), _F32, dev, 2)
-    _like("B", B, (Bt, L, G, N), own, dev, 1)
-    _like("C", C, (Bt, L, G, N), own, dev, 1)
-    if D is not None:
-        _like("D", D, (Dm,), _F32, dev, 1)
-    if dt_bias is not None:
-        _like("dt_bias", dt_bias, (Dm,), _F32, dev, 1)
-    if z is not None:
-        _like("z", z, shape, own, dev, 1)
-    if initial_states is not None:
-        _like("initial_states", initial_states, (S, Dm, N), _ST, dev, 3)
-    pk = _lib.packed
-    fields = (_last_is_one(pk(x), 2) + _last_is_one(pk(dt), 2) + pk(A, True) + _last_is_one(pk(B), 3) +
-              _last_is_one(pk(C), 3) + pk(D, True) + (_lib._ABSENT if z is None else _last_is_one(pk(z), 2)) +
-              pk(dt_bias, True) + pk(initial_states, True))
-    return _lib.SelectiveProblem(Bt, L, Dm, G, N, S if cu_seqlens is not None else 0), fields, S
+# snapshots of states.  Checks, allocation and the call are the compiled binding's
+# (csrc/binding.cpp): ValueError for tensors that do not fit together, SSDError for what the
+# library refuses.
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def selective_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, initial_states=None, cu_seqlens=None,
@@ -334,20 +257,11 @@ def selective_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, initial
     float32 or bfloat16; cu_seqlens: int32 [S + 1] (batch 1).  state_dtype: of the final states (default:
     that of initial_states, else float32).  keep_chunk_states: also return the buffer that
     selective_scan_backward(chunk_states=...) starts from."""
-    prob, fields, S = _selective_args(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    final = kept = None
-    if return_final_states:
-        sdt = state_dtype or (initial_states.dtype if initial_states is not None else torch.float32)
-        _need(sdt in _ST, "state_dtype is float32 or bfloat16")
-        final = torch.empty((S, x.shape[2], B.shape[3]), dtype=sdt, device=x.device)
-    if keep_chunk_states:
-        kept = torch.empty(_lib.selective_chunk_states_size(prob), dtype=torch.uint8, device=x.device)
-    _on(stream, y, final, kept)
-    pk = _lib.packed
-    fields += pk(y, True) + pk(final, True) + (_lib._addr(cu_seqlens) or 0, _lib._addr(kept) or 0)
-    _lib.check(_lib.selective_fwd(prob, fields, x, stream), "ssd_selective_fwd")
-    return (y, final, kept) if keep_chunk_states else (y, final)
+    if state_dtype not in (None, torch.float32, torch.bfloat16):
+        raise ValueError("state_dtype is float32 or bfloat16")
+    sd = -1 if state_dtype is None else _lib.SSD_BF16 if state_dtype == torch.bfloat16 else _lib.SSD_F32
+    return _lib.fast().selective_fwd(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens, bool(return_final_states),
+                                     sd, bool(keep_chunk_states), _handle(stream))
 
 
 def selective_scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, initial_states=None, dfinal_states=None,
@@ -356,37 +270,8 @@ def selective_scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, in
     the matching input is given, dD, dz, ddt_bias, dinitial_states.  chunk_states: the buffer that
     selective_scan_forward(keep_chunk_states=True) returned for the same inputs (without it the
     forward's states are computed again)."""
-    prob, fields, S = _selective_args(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens)
-    dev, gpu = x.device, x.get_device()
-    _like("dy", dy, x.shape, (x.dtype,), gpu, 1)
-    if dfinal_states is not None:
-        _like("dfinal_states", dfinal_states, (S, x.shape[2], B.shape[3]), _ST, gpu, 3)
-    if chunk_states is not None:
-        need = _lib.selective_chunk_states_size(prob)
-        _need(chunk_states.get_device() == gpu and chunk_states.is_contiguous(), "chunk_states: a contiguous buffer on x's GPU")
-        _need(chunk_states.numel() * chunk_states.element_size() >= need, "chunk_states is smaller than %d bytes" % need)
-    g = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=dev), ddt=torch.empty(dt.shape, dtype=dt.dtype, device=dev),
-             dA=torch.empty(A.shape, dtype=torch.float32, device=dev),
-             dB=torch.empty(B.shape, dtype=B.dtype, device=dev), dC=torch.empty(C.shape, dtype=C.dtype, device=dev))
-    if D is not None:
-        g["dD"] = torch.empty(D.shape, dtype=torch.float32, device=dev)
-    if dt_bias is not None:
-        g["ddt_bias"] = torch.empty(dt_bias.shape, dtype=torch.float32, device=dev)
-    if z is not None:
-        g["dz"] = torch.empty(z.shape, dtype=z.dtype, device=dev)
-    if initial_states is not None:   # in the initial states' storage type
-        g["dinitial_states"] = torch.empty(initial_states.shape, dtype=initial_states.dtype, device=dev)
-    pk = _lib.packed
-    fields += _lib._ABSENT * 2 + (_lib._addr(cu_seqlens) or 0, _lib._addr(chunk_states) or 0)
-    fields += _last_is_one(pk(dy), 2) + pk(dfinal_states, True)
-    for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dinitial_states"):
-        fields += pk(g.get(k), True)
-    args = _lib._BWD.pack(*fields)
-    nbytes = _lib.selective_bwd_workspace_size(prob, args)
-    ws = workspace.get(nbytes) if workspace is not None else torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-    _on(stream, ws, *g.values())
-    _lib.check(_lib.selective_bwd(prob, args, ws, stream), "ssd_selective_bwd")
-    return g
+    return _lib.fast().selective_bwd(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens, dy, dfinal_states, chunk_states,
+                                     workspace, _handle(stream))
 
 
 class SelectiveScanFunction(torch.autograd.Function):
@@ -409,81 +294,20 @@ class SelectiveScanFunction(torch.autograd.Function):
                 g.get("dinitial_states"), None)
 
 
-def _step(selective, state, x, dt, A, B, C, D, z, dt_bias, state_indices, stream):
-    _need(B.dim() == 3, "B has shape [batch, ngroups, dstate]")
-    dev, own, shape, slots = _on_gpu("x", x), (x.dtype,), x.shape, state.shape[0]
-    G, N = B.shape[1:]
-    if selective:
-        n, H = shape
-        P, inner = 1, 1
-        _like("state", state, (slots, H, N), _ST, dev, 2)
-        _like("A", A, (H, N), _F32, dev, 2)
-        _like("dt", dt, (n, H), (torch.float32, x.dtype), dev, 1)
-    else:
-        n, H, P = shape
-        inner = 2
-        _like("state", state, (slots, H, P, N), _ST, dev, 3)
-        _like("A", A, (H,), _F32, dev, 1)
-        _like("dt", dt, (n, H), _F32, dev, 1)
-    _like("x", x, shape, own, dev, inner)
-    _like("B", B, (n, G, N), own, dev, 2)
-    _like("C", C, (n, G, N), own, dev, 2)
-    if D is not None:
-        _like("D", D, (H,), _F32, dev, 1)
-    if z is not None:
-        _like("z", z, shape, own, dev, inner)
-    if dt_bias is not None:
-        _like("dt_bias", dt_bias, (H,), _F32, dev, 1)
-    if state_indices is None:
-        _need(slots >= n, "the state pool has fewer slots than there are requests")
-    else:
-        _like("state_indices", state_indices, (n,), (torch.int32,), dev, 1)
-    y = torch.empty(shape, dtype=x.dtype, device=x.device)
-    code = _lib._CODES
-    prob = _lib.StepProblem(n, slots, H, P, G, N, state.stride(0), x.stride(0), dt.stride(0),
-                            0 if z is None else z.stride(0), B.stride(0), C.stride(0), H * P,
-                            code[x.dtype], code[dt.dtype], code[state.dtype], 0)
-    if stream is not None:
-        _on(stream, y)
-    _lib.check(_lib.step(selective, prob, state, state_indices, x, dt, A, B, C, D, z, dt_bias, y, stream),
-               "ssd_selective_step" if selective else "ssd_step")
-    return y
-
-
 def ssd_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, state_indices=None, stream=None):
     """y = one token of ssd_forward's recurrence for each request (see include/ssd.h, ssd_step); `state`
     [nslots, nheads, headdim, dstate] float32 or bfloat16 is updated in place at state_indices (int32 [batch];
     default: slot i for request i).  x, z, y: [batch, nheads, headdim]; dt: [batch, nheads] float32; A, D,
     dt_bias: [nheads] float32; B, C: [batch, ngroups, dstate].  A request whose slot is out of range is
     padding: its y is zero.  The slots of one call must differ."""
-    _need(x.dim() == 3 and state.dim() == 4, "x has shape [batch, nheads, headdim], state [nslots, nheads, headdim, dstate]")
-    return _step(False, state, x, dt, A, B, C, D, z, dt_bias, state_indices, stream)
+    return _lib.fast().step(False, state, x, dt, A, B, C, D, z, dt_bias, state_indices, _handle(stream))
 
 
 def selective_scan_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, state_indices=None, stream=None):
     """y = one token of selective_scan_forward's recurrence for each request; `state` [nslots, channels, dstate] is
     updated in place.  x, z, y: [batch, channels]; dt: the same in float32 or x's type; A: [channels, dstate],
     D, dt_bias: [channels] float32; B, C: [batch, ngroups, dstate].  Slots as in ssd_step."""
-    _need(x.dim() == 2 and state.dim() == 3, "x has shape [batch, channels], state [nslots, channels, dstate]")
-    return _step(True, state, x, dt, A, B, C, D, z, dt_bias, state_indices, stream)
-
-
-def _conv_check(u, weight, bias, conv_states, state_indices, n):
-    """Checks what both forms share; returns the GPU's index and the width."""
-    Cn = u.shape[-1]
-    dev = _on_gpu("xbc", u)
-    _need(weight.dim() == 2, "weight has shape [channels, width]")
-    K = weight.shape[1]
-    _like("xbc", u, u.shape, (u.dtype,), dev, 1)
-    _like("weight", weight, (Cn, K), _F32, dev, 2)
-    if bias is not None:
-        _like("bias", bias, (Cn,), _F32, dev, 1)
-    _like("conv_states", conv_states, (conv_states.shape[0], K - 1, Cn), (u.dtype,), dev, 2)
-    if state_indices is None:
-        _need(conv_states.shape[0] >= n, "conv_states has fewer slots than there are sequences")
-    else:
-        _like("state_indices", state_indices, (n,), (torch.int32,), dev, 1)
-    return dev, K
+    return _lib.fast().step(True, state, x, dt, A, B, C, D, z, dt_bias, state_indices, _handle(stream))
 
 
 def conv1d_prompt(xbc, weight, bias, conv_states, cu_seqlens=None, state_indices=None, has_initial=None, silu=True,
@@ -491,69 +315,24 @@ def conv1d_prompt(xbc, weight, bias, conv_states, cu_seqlens=None, state_indices
     """conv1d_forward whose sequences go on from carried windows (see include/ssd.h, ssd_conv1d_prompt): `conv_states`
     [nslots, width - 1, channels] of xbc's type holds the inputs before each sequence's first token and
     is left holding its last ones.  xbc: [batch, seqlen, channels]; state_indices: int32, one slot per
-    sequence (default: slot i); has_initial: uint8 per sequence, 0 where it starts from zeros."""
-    _need(xbc.dim() == 3, "xbc has shape [batch, seqlen, channels]")
-    Bsz, L, Cn = xbc.shape
-    n = Bsz if cu_seqlens is None else cu_seqlens.numel() - 1
-    dev, K = _conv_check(xbc, weight, bias, conv_states, state_indices, n)
-    if cu_seqlens is not None:
-        _need(n >= 1, "cu_seqlens holds no sequence")
-        _like("cu_seqlens", cu_seqlens, (n + 1,), (torch.int32,), dev, 1)
-    if has_initial is not None:
-        _like("has_initial", has_initial, (n,), (torch.uint8, torch.bool), dev, 1)
-    out = torch.empty((Bsz, L, Cn), dtype=xbc.dtype, device=xbc.device)
-    prob = _lib.ConvProblem(Bsz, L, Cn, K, 0 if cu_seqlens is None else n, _lib._CODES[xbc.dtype], 1 if silu else 0, 0, 0)
-    _on(stream, out)
-    _lib.check(_lib.conv1d_prompt(prob, xbc, weight, bias, cu_seqlens, conv_states, state_indices, has_initial, out, stream),
-               "ssd_conv1d_prompt")
-    return out
+    sequence (default: slot i); has_initial: uint8 or bool per sequence, 0 where it starts from zeros."""
+    return _lib.fast().conv1d_prompt(xbc, weight, bias, conv_states, cu_seqlens, state_indices, has_initial, bool(silu),
+                                     _handle(stream))
 
 
 def conv1d_step(xbc, weight, bias, conv_states, state_indices=None, silu=True, stream=None):
     """The convolution of one token per request: xbc [batch, channels]; conv_states and state_indices as in
     conv1d_prompt (a request whose slot is out of range sees a window of zeros and leaves none)."""
-    _need(xbc.dim() == 2, "xbc has shape [batch, channels]")
-    n, Cn = xbc.shape
-    _, K = _conv_check(xbc, weight, bias, conv_states, state_indices, n)
-    out = torch.empty((n, Cn), dtype=xbc.dtype, device=xbc.device)
-    if n == 0:
-        return out
-    prob = _lib.ConvProblem(n, 1, Cn, K, 0, _lib._CODES[xbc.dtype], 1 if silu else 0, 0, 0)
-    _on(stream, out)
-    _lib.check(_lib.conv1d_step(prob, xbc, weight, bias, conv_states, state_indices, out, stream), "ssd_conv1d_step")
-    return out
-
-
-def _snapshot(store, states, snapshots, scales, state_indices, slots, stream):
-    dev, shape, snaps = _on_gpu("states", states), states.shape, snapshots.shape[0]
-    _need(len(shape) >= 2, "states has shape [nslots, ..., dstate]")
-    _like("states", states, shape, _ST, dev, len(shape) - 1)
-    _like("snapshots", snapshots, (snaps,) + shape[1:], (torch.int8,), dev, len(shape))
-    _like("scales", scales, (snaps,) + shape[1:-1], _F32, dev, len(shape) - 1)
-    n = (state_indices if state_indices is not None else slots if slots is not None else states).shape[0]
-    if state_indices is None:
-        _need(shape[0] >= n, "there are fewer states than slots")
-    else:
-        _like("state_indices", state_indices, (n,), (torch.int32,), dev, 1)
-    if slots is None:
-        _need(snaps >= n, "there are fewer snapshots than states")
-    else:
-        _like("slots", slots, (n,), (torch.int32,), dev, 1)
-    rows = 1
-    for k in shape[1:-1]:
-        rows *= k
-    prob = _lib.SnapshotProblem(n, rows, shape[-1], shape[0], snaps, states.stride(0), _lib._CODES[states.dtype], 0)
-    _lib.check(_lib.snapshot(store, prob, states, state_indices, snapshots, scales, slots, stream),
-               "ssd_snapshot_store" if store else "ssd_snapshot_load")
+    return _lib.fast().conv1d_step(xbc, weight, bias, conv_states, state_indices, bool(silu), _handle(stream))
 
 
 def snapshot_store(states, snapshots, scales, state_indices=None, slots=None, stream=None):
     """Puts states aside in 8 bits (see include/ssd.h, ssd_snapshot_store): state state_indices[i] of the pool `states`
     [nslots, ..., dstate] (float32 or bfloat16) goes to snapshots[slots[i]] (int8, the same inner shape)
     and scales[slots[i]] (float32, one per row of dstate values).  Indices are int32 and default to i."""
-    _snapshot(True, states, snapshots, scales, state_indices, slots, stream)
+    _lib.fast().snapshot(True, states, snapshots, scales, state_indices, slots, _handle(stream))
 
 
 def snapshot_load(snapshots, scales, states, slots=None, state_indices=None, stream=None):
     """Takes states up again: snapshot slots[i] is read back into state state_indices[i] of the pool `states`."""
-    _snapshot(False, states, snapshots, scales, state_indices, slots, stream)
+    _lib.fast().snapshot(False, states, snapshots, scales, state_indices, slots, _handle(stream))

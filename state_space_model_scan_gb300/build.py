@@ -1,14 +1,17 @@
-"""Builds libssd.so in-tree with nvcc for sm_103a (GB300).
+"""Builds libssd.so in-tree with nvcc for sm_103a (GB300), and its Python binding.
 
 Each .cu file under csrc/ is compiled in parallel to an object file, then the
 objects are linked into ``state_space_model_scan_gb300/libssd.so``.  No torch
 extension machinery is used: the library has a plain C ABI (include/ssd.h).
+csrc/binding.cpp becomes the extension module ``_binding`` against the installed
+torch's headers (g++).
 """
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -45,9 +48,41 @@ def _compile(src, obj, extra):
     return r.stdout + r.stderr
 
 
+BINDING = os.path.join(PKG, "_binding.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/binding.cpp into the extension module _binding; returns its path."""
+    import torch
+    src, deps = os.path.join(CSRC, "binding.cpp"), [os.path.join(ROOT, "include", "ssd.h")]
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(f) for f in [src] + deps):
+        return BINDING
+    home = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_paths()["include"], os.path.join(home, "include"),
+           os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi()] +
+           [f for i in inc for f in ("-isystem", i)] + [src, "-o", tmp, "-L" + os.path.join(home, "lib"),
+                                                        "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (src, " ".join(cmd), r.stdout + r.stderr))
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile csrc/*.cu and link libssd.so; returns its path."""
+    """Compile csrc/*.cu and link libssd.so; build the binding beside it.  Returns the library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(build_binding, force)
+        lib = _build_lib(force, verbose, extra)
+        binding.result()
+    return lib
+
+
+def _build_lib(force, verbose, extra) -> str:
     srcs = sources()
     hm = _headers_mtime()
     jobs = []
