@@ -443,7 +443,7 @@ ssd_status ssd_complex_fwd(const ssd_complex_problem *prob, const void *x, const
  * dfinal on to dinitial.  dstate 1..128 (else SSD_ERR_UNSUPPORTED); all arithmetic in fp32.
  *
  * chunk_states (optional): a device buffer of ssd_selective_chunk_states_size bytes, 16-byte
- * aligned, into which the forward writes the state entering every 32nd token of each sequence
+ * aligned, into which the forward writes the state entering every 16th token of each sequence
  * (f32, dstate padded to 16, 32, 64 or 128); the backward, given the same buffer, starts from
  * them instead of running the forward again.  The forward needs no workspace.  Gradient
  * reductions run in a fixed order (bitwise reproducible); D, z, dt_bias and initial_states may

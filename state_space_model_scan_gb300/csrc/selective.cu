@@ -221,6 +221,8 @@ ssd_status ssd_selective_bwd(const ssd_selective_problem *p, const ssd_bwd_args 
     a.dz = b->dz.ptr; a.dzb = b->dz.stride[0]; a.dzt = b->dz.stride[1];
     a.dB = b->dB.ptr; a.dBb = b->dB.stride[0]; a.dBt = b->dB.stride[1]; a.dBg = b->dB.stride[2];
     a.dC = b->dC.ptr; a.dCb = b->dC.stride[0]; a.dCt = b->dC.stride[1]; a.dCg = b->dC.stride[2];
+    a.vec = a.vec && fours(b->dy, 2);
+    a.vec_out = (p->ngroups == 1 || a.dpg % 4 == 0) && fours(b->dx, 2) && fours(b->ddt, 2) && fours(b->dz, 2);
     a.dA = static_cast<float *>(b->dA.ptr);
     a.dD = f->D.ptr ? static_cast<float *>(b->dD.ptr) : nullptr;
     a.dbias = f->dt_bias.ptr ? static_cast<float *>(b->ddt_bias.ptr) : nullptr;

@@ -9,7 +9,7 @@ namespace ssd {
 // Chunk of the kept states: the state entering every SEL_Q-th token of a sequence is what the
 // forward keeps and the backward starts from.  Sequence s's chunks lie at slots
 // slot0(s) .. slot0(s) + ceil(len / SEL_Q) - 1.
-constexpr int SEL_Q = 32;
+constexpr int SEL_Q = 16;
 
 // dstate padded to the sizes that the kernels are compiled for.
 __host__ __device__ inline int sel_pad(int64_t n) { return n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128; }
@@ -20,7 +20,7 @@ struct SelArgs {
     const float *A, *D, *bias;
     const void *init, *dfinal;
     // four elements at places divisible by four are aligned to their size, in the channel tensors / in B and C
-    bool vec, vecBC;
+    bool vec, vecBC, vec_out;          // (vec_out: the gradients' channel tensors)
     bool dt_f32, init_bf16, final_bf16, dfinal_bf16, dinit_bf16;
     const int32_t *cu;                 // packed sequences (batch 1) or NULL
     int nbatch, seqlen, channels, ngroups, dpg, N, NP, nseqs, nslots;     // dpg: channels per group; nseqs: batch or packed

@@ -20,6 +20,9 @@
 #include <algorithm>
 
 #include "selective.cuh"
+#ifndef GRAD_OCC
+#define GRAD_OCC 3
+#endif
 
 namespace ssd {
 
@@ -28,141 +31,247 @@ namespace {
 // the gate's logistic function to about 1e-6: dA, dD and the others keep 32 bits
 __device__ __forceinline__ float sigf(float v) { return __fdividef(1.f, 1.f + ex2f(-kLog2e * v)); }
 
-// ---- the adjoint at the chunks' right ends
-template <int S_, int TPC_, int CW_, int TW_, int TK_>
+// ---- the adjoint at the chunks' right ends: the forward's first sweep, backwards.  Warp (w, cw) has the w-th TK
+// tokens of a tile and the cw-th 64 / TPC channels, a thread S states of two channels; the warps' folds are
+// joined from the last to the first while the next tile is on its way.
+template <int S_, int TPC_, int CW_, int TW_, int TK_, int OCC_>
 struct RevCfg {
-    static constexpr int S = S_, TPC = TPC_, CW = CW_, TW = TW_, TK = TK_;
-    static constexpr int NP = S * TPC, CPW = 32 / TPC, CB = CW * CPW, TT = TW * TK, NT = 32 * CW * TW;
-    static constexpr size_t smem = (size_t)TT * CB * 8 + (size_t)TT * NP * 4 + (size_t)(TW + 1) * CB * NP * 4 +
-                                   (size_t)TW * CB * 4;
+    static constexpr int S = S_, TPC = TPC_, CW = CW_, TW = TW_, TK = TK_, OCC = OCC_;
+    static constexpr int NP = S * TPC, CPW = 64 / TPC, CB = CW * CPW, TT = TW * TK, NT = 32 * CW * TW;
+    static constexpr int RX = 128 / CPW, PX = (TK + RX - 1) / RX, RB = NP < 128 ? 128 / NP : 1, PB = (TK + RB - 1) / RB;
+    static_assert(SEL_Q % TK == 0 && TT % SEL_Q == 0 && S % 4 == 0 && CB * NP / 4 <= NT, "tile shape");
+    // bytes a warp keeps: (dt, dyp), C, and the next tile's dt, dy, z and C as they come
+    static constexpr size_t wsmem(size_t ts, size_t ds) {
+        return (size_t)TK * CPW * 8 + (size_t)TK * NP * 4 + (size_t)TK * CPW * (2 * ts + ds) + (size_t)TK * NP * ts;
+    }
+    template <typename T>
+    static size_t smem(bool dt_f32) {
+        return CW * TW * wsmem(sizeof(T), dt_f32 ? 4 : sizeof(T)) + 2 * ((size_t)TW * CB * NP * 4 + (size_t)TW * CB * 4);
+    }
 };
 
 template <typename T, typename F>
-__global__ void __launch_bounds__(F::NT, 2) k_sel_rev(const SelArgs a, int cblocks) {
-    constexpr int S = F::S, TPC = F::TPC, NP = F::NP, CB = F::CB, TT = F::TT, TK = F::TK, TW = F::TW, NT = F::NT;
+__global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int cblocks) {
+    constexpr int S = F::S, TPC = F::TPC, NP = F::NP, CB = F::CB, CPW = F::CPW, TT = F::TT, TK = F::TK, TW = F::TW;
     extern __shared__ __align__(16) uint8_t sel_sm[];
-    float2 *dd = reinterpret_cast<float2 *>(sel_sm);                // [TT][CB]: (dt, dyp)
-    float *Cs = reinterpret_cast<float *>(dd + TT * CB);            // [TT][NP]
-    float *E = Cs + TT * NP;                                        // [TW][CB][NP]: what each warp passes on; then the carry
-    float *Sd = E + (TW + 1) * CB * NP;                             // [TW][CB]: sums of dt
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int w = wid % TW, cw = wid / TW;
-    const int q = lane % TPC, cl = cw * F::CPW + lane / TPC;
+    const size_t wbytes = F::wsmem(sizeof(T), a.dt_f32 ? 4 : sizeof(T));
+    float4 *dd = reinterpret_cast<float4 *>(sel_sm + wid * wbytes);  // [TK][CPW / 2]: (dt, dyp) of two channels
+    float *Cs = reinterpret_cast<float *>(dd + TK * CPW / 2);        // [TK][NP]
+    float *rD = Cs + TK * NP;                                        // dt [TK][CPW], fp32 or T
+    T *rY = reinterpret_cast<T *>(rD + TK * CPW / (a.dt_f32 ? 1 : 4 / (int)sizeof(T)));   // dy, z [TK][CPW]
+    T *rZ = rY + TK * CPW, *rC = rZ + TK * CPW;                      // C [TK][NP]
+    float *E = reinterpret_cast<float *>(sel_sm + F::CW * TW * wbytes);   // two of [TW][NP / 4][CB][4]: what each warp passes on
+    float *Sd = E + 2 * TW * CB * NP;                                // two of [TW][CB]: sums of dt
+    const int q = lane % TPC, cp0 = 2 * (lane / TPC), cl = cw * CPW + cp0;
     const int cb = blockIdx.x % cblocks, s = blockIdx.x / cblocks;
     const int bpg = cblocks / a.ngroups, g = cb / bpg;
     const int d0 = g * a.dpg + (cb % bpg) * CB, dend = (g + 1) * a.dpg, d = d0 + cl;
     const SelSeq sq = sel_seq(a, s);
-    const int N = a.N;
-    const T *dy = static_cast<const T *>(a.dy) + sq.b * a.dyb + sq.t0 * a.dyt;
-    const T *z = a.z ? static_cast<const T *>(a.z) + sq.b * a.zb + sq.t0 * a.zt : nullptr;
-    const T *C = static_cast<const T *>(a.C) + sq.b * a.Cb + sq.t0 * a.Ct + g * a.Cg;
-    const int64_t dt0 = sq.b * a.dtb + sq.t0 * a.dtt;
-    f32x2 A2[S / 2];
+    const int N = a.N, len = sq.len;
+    const int pc = 4 * (lane % (CPW / 4)), pt = lane / (CPW / 4), e0 = d0 + cw * CPW + pc, nc = min(max(dend - e0, 0), 4);
+    const int pn = 4 * (lane % (NP / 4)), pbt = lane / (NP / 4), nn = min(max(N - pn, 0), 4);
+    const bool vec = a.vec, vecBC = a.vecBC, gated = a.z != nullptr;
+    const int es = a.dt_f32 ? 4 : (int)sizeof(T), ds = (int)a.dtt * es;
+    const int ys = (int)a.dyt * (int)sizeof(T), zs = (int)a.zt * (int)sizeof(T), cs = (int)a.Ct * (int)sizeof(T);
+    const T *dy = static_cast<const T *>(a.dy) + sq.b * a.dyb + sq.t0 * a.dyt + e0;
+    const T *z = gated ? static_cast<const T *>(a.z) + sq.b * a.zb + sq.t0 * a.zt + e0 : nullptr;
+    const uint8_t *dtp = static_cast<const uint8_t *>(a.dt) + (sq.b * a.dtb + sq.t0 * a.dtt + e0) * es;
+    const T *C = static_cast<const T *>(a.C) + sq.b * a.Cb + sq.t0 * a.Ct + g * a.Cg + pn;
+    float bias[4];
 #pragma unroll
-    for (int i = 0; i < S / 2; ++i) {
-        float v[2];
+    for (int i = 0; i < 4; ++i) bias[i] = a.bias && i < nc ? a.bias[e0 + i] : 0.f;
+
+    auto fetch = [&](int t0) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int n = q * S + 2 * i + e;
-            v[e] = d < dend && n < N ? a.A[(int64_t)d * N + n] * kLog2e : 0.f;
-        }
-        A2[i] = pk2(v[0], v[1]);
-    }
-    for (int i = tid; i < CB * NP; i += NT) {
-        const int c = i / NP, n = i % NP;
-        E[TW * CB * NP + i] = (a.dfinal && d0 + c < dend && n < N)
-                                  ? ld_st(a.dfinal, a.dfinal_bf16, ((int64_t)s * a.channels + d0 + c) * N + n) : 0.f;
-    }
-    for (int t0 = sq.len > 0 ? (sq.len - 1) / TT * TT : -1; t0 >= 0; t0 -= TT) {
-        __syncthreads();
-        for (int i = tid; i < TT * CB; i += NT) {
-            const int t = t0 + i / CB, dc = d0 + i % CB;
-            float dt = 0.f, v = 0.f;
-            if (t < sq.len && dc < dend) {
-                dt = sel_softplus(ld_dt(a, dt0 + t * a.dtt + dc) + (a.bias ? a.bias[dc] : 0.f));
-                v = to_f(dy[t * a.dyt + dc]);
-                if (z) {
-                    const float zv = to_f(z[t * a.zt + dc]);
-                    v *= zv * sigf(zv);
-                }
+        for (int k = 0; k < F::PX; ++k) {
+            const int tl = pt + k * F::RX, t = t0 + w * TK + tl;
+            if ((F::RX * F::PX == TK || tl < TK) && t < len) {
+                if (a.dt_f32) fetch4(rD + tl * CPW + pc, reinterpret_cast<const float *>(row(dtp, t, ds)), nc, vec);
+                else fetch4(reinterpret_cast<T *>(rD) + tl * CPW + pc, reinterpret_cast<const T *>(row(dtp, t, ds)), nc, vec);
+                fetch4(rY + tl * CPW + pc, row(dy, t, ys), nc, vec);
+                if (gated) fetch4(rZ + tl * CPW + pc, row(z, t, zs), nc, vec);
             }
-            dd[i] = make_float2(dt, v);
         }
-        for (int i = tid; i < TT * NP; i += NT) {
-            const int t = t0 + i / NP, n = i % NP;
-            Cs[i] = t < sq.len && n < N ? to_f(C[t * a.Ct + n]) : 0.f;
+#pragma unroll 4
+        for (int k = 0; k < F::PB; ++k) {
+            const int tl = pbt + k * F::RB, t = t0 + w * TK + tl;
+            if (t < len) fetch4(rC + tl * NP + pn, row(C, t, cs), nn, vecBC);
         }
-        __syncthreads();
-        f32x2 u[S / 2];
-        float sum = 0.f;
+        cp_async_commit();
+    };
+
+    f32x2 A2[2][S / 2];
 #pragma unroll
-        for (int i = 0; i < S / 2; ++i) u[i] = 0;
-        if (t0 + w * TK < sq.len) {
-            const float2 *dp = dd + w * TK * CB + cl;
-            const float *cp = Cs + w * TK * NP + q * S;
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < S / 2; ++i) {
+            float v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int n = q * S + 2 * i + e;
+                v[e] = d + c < dend && n < N ? a.A[(int64_t)(d + c) * N + n] * kLog2e : 0.f;
+            }
+            A2[c][i] = pk2(v[0], v[1]);
+        }
+    const int jc = tid % CB, jn = 4 * (tid / CB);
+    const bool joins = tid < CB * NP / 4;
+    f32x2 jA[2] = {0, 0}, ju[2] = {0, 0};
+    if (joins) {
+        float v[4], uv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool in = d0 + jc < dend && jn + e < N;
+            v[e] = in ? a.A[(int64_t)(d0 + jc) * N + jn + e] * kLog2e : 0.f;
+            uv[e] = in && a.dfinal ? ld_st(a.dfinal, a.dfinal_bf16, ((int64_t)s * a.channels + d0 + jc) * N + jn + e) : 0.f;
+        }
+        jA[0] = pk2(v[0], v[1]); jA[1] = pk2(v[2], v[3]);
+        ju[0] = pk2(uv[0], uv[1]); ju[1] = pk2(uv[2], uv[3]);
+    }
+    const int last = len > 0 ? (len - 1) / TT * TT : -1;
+    if (last >= 0) fetch(last);
+    int buf = 0;
+    for (int t0 = last; t0 >= 0; t0 -= TT, buf ^= 1) {
+        cp_async_wait_all();
+        __syncwarp();
+        const int tw = t0 + w * TK;
+        f32x2 u[2][S / 2];
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < S / 2; ++i) u[0][i] = u[1][i] = 0;
+        if (tw < len) {
+#pragma unroll
+            for (int k = 0; k < F::PX; ++k) {
+                const int tl = pt + k * F::RX;
+                if (F::RX * F::PX != TK && tl >= TK) break;
+                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // past the end: decay 1, no gradient
+                if (tw + tl < len) {
+                    float yv[4], zv[4], r[4];
+                    Raw4<T> r0;
+                    r0.load(rY + tl * CPW + pc, 4, true);
+                    r0.f(yv);
+                    if (a.dt_f32) {
+                        Raw4<float> rd;
+                        rd.load(rD + tl * CPW + pc, 4, true);
+                        rd.f(r);
+                    } else {
+                        Raw4<T> rd;
+                        rd.load(reinterpret_cast<T *>(rD) + tl * CPW + pc, 4, true);
+                        rd.f(r);
+                    }
+                    if (gated) {
+                        r0.load(rZ + tl * CPW + pc, 4, true);
+                        r0.f(zv);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < nc) {
+                            v[2 * i] = sel_softplus(r[i] + bias[i]);
+                            v[2 * i + 1] = gated ? yv[i] * zv[i] * sigf(zv[i]) : yv[i];
+                        }
+                }
+                float4 *o = dd + (tl * CPW + pc) / 2;
+                o[0] = make_float4(v[0], v[1], v[2], v[3]);
+                o[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+#pragma unroll 4
+            for (int k = 0; k < F::PB; ++k) {
+                const int tl = pbt + k * F::RB;
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+                if (tw + tl < len) {
+                    float rc[4];
+                    Raw4<T> r;
+                    r.load(rC + tl * NP + pn, 4, true);
+                    r.f(rc);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < nn) c[i] = rc[i];
+                }
+                put4(Cs + tl * NP + pn, c);
+            }
+        }
+        __syncwarp();
+        if (t0 > 0) fetch(t0 - TT);
+        if (tw < len) {
+            const float4 *dp = dd + cp0 / 2;
+            const float *cp = Cs + q * S;
 #pragma unroll 4
             for (int t = TK - 1; t >= 0; --t) {
-                const float2 v = dp[t * CB];
-                sum += v.x;
-                const f32x2 dt2 = pk2(v.x, v.x), dy2 = pk2(v.y, v.y);
+                const float4 v = dp[t * (CPW / 2)];
+                sum0 += v.x;
+                sum1 += v.z;
+                const f32x2 dt0 = pk2(v.x, v.x), y0 = pk2(v.y, v.y), dt1 = pk2(v.z, v.z), y1 = pk2(v.w, v.w);
                 const ulonglong2 *c = reinterpret_cast<const ulonglong2 *>(cp + t * NP);
 #pragma unroll
                 for (int i = 0; i < S / 4; ++i) {
                     const ulonglong2 cv = c[i];
-                    u[2 * i] = mul2(ex2x2(mul2(dt2, A2[2 * i])), fma2(cv.x, dy2, u[2 * i]));
-                    u[2 * i + 1] = mul2(ex2x2(mul2(dt2, A2[2 * i + 1])), fma2(cv.y, dy2, u[2 * i + 1]));
+                    u[0][2 * i] = mul2(ex2x2(mul2(dt0, A2[0][2 * i])), fma2(cv.x, y0, u[0][2 * i]));
+                    u[1][2 * i] = mul2(ex2x2(mul2(dt1, A2[1][2 * i])), fma2(cv.x, y1, u[1][2 * i]));
+                    u[0][2 * i + 1] = mul2(ex2x2(mul2(dt0, A2[0][2 * i + 1])), fma2(cv.y, y0, u[0][2 * i + 1]));
+                    u[1][2 * i + 1] = mul2(ex2x2(mul2(dt1, A2[1][2 * i + 1])), fma2(cv.y, y1, u[1][2 * i + 1]));
                 }
             }
         }
-        ulonglong2 *ep = reinterpret_cast<ulonglong2 *>(E + (w * CB + cl) * NP + q * S);
+        ulonglong2 *ep = reinterpret_cast<ulonglong2 *>(E) + ((buf * TW + w) * (NP / 4) + q * (S / 4)) * CB + cl;
 #pragma unroll
-        for (int i = 0; i < S / 4; ++i) ep[i] = make_ulonglong2(u[2 * i], u[2 * i + 1]);
-        if (q == 0) Sd[w * CB + cl] = sum;
-        __syncthreads();
-        for (int i = tid; i < CB * NP; i += NT) {
-            const int c = i / NP, n = i % NP, dc = d0 + c;
-            const float An = dc < dend && n < N ? a.A[(int64_t)dc * N + n] * kLog2e : 0.f;
-            float uc = E[TW * CB * NP + i];
+        for (int i = 0; i < S / 4; ++i) {
+            ep[i * CB] = make_ulonglong2(u[0][2 * i], u[0][2 * i + 1]);
+            ep[i * CB + 1] = make_ulonglong2(u[1][2 * i], u[1][2 * i + 1]);
+        }
+        if (q == 0) *reinterpret_cast<float2 *>(Sd + (buf * TW + w) * CB + cl) = make_float2(sum0, sum1);
+        __syncthreads();   // (the other buffer's joining is over: its threads are here)
+        if (joins) {
+            ulonglong2 fold[TW];
+            float sd[TW];
+#pragma unroll
+            for (int k = 0; k < TW; ++k) {
+                fold[k] = *(reinterpret_cast<const ulonglong2 *>(E) + ((buf * TW + k) * (NP / 4) + jn / 4) * CB + jc);
+                sd[k] = Sd[(buf * TW + k) * CB + jc];
+            }
 #pragma unroll
             for (int k = TW - 1; k >= 0; --k) {
                 const int te = t0 + (k + 1) * TK;                   // the k-th warp's tokens end here
-                if (te % SEL_Q == 0 && te - SEL_Q < sq.len && dc < dend) {
+                if (te % SEL_Q == 0 && te - SEL_Q < len && d0 + jc < dend) {
                     const int slot = sq.slot0 + te / SEL_Q - 1;
-                    if (slot < a.nslots) a.adj[((int64_t)slot * a.channels + dc) * NP + n] = uc;
+                    if (slot < a.nslots)
+                        *reinterpret_cast<ulonglong2 *>(a.adj + ((int64_t)slot * a.channels + d0 + jc) * NP + jn) =
+                            make_ulonglong2(ju[0], ju[1]);
                 }
-                uc = fmaf(ex2f(An * Sd[k * CB + c]), uc, E[k * CB * NP + i]);
+                const f32x2 sd2 = pk2(sd[k], sd[k]);
+                ju[0] = fma2(ex2x2(mul2(sd2, jA[0])), ju[0], fold[k].x);
+                ju[1] = fma2(ex2x2(mul2(sd2, jA[1])), ju[1], fold[k].y);
             }
-            E[TW * CB * NP + i] = uc;
         }
     }
-    if (a.dinit == nullptr) return;
-    __syncthreads();
-    for (int i = tid; i < CB * NP; i += NT) {
-        const int c = i / NP, n = i % NP;
-        if (d0 + c < dend && n < N)
-            st_st(a.dinit, a.dinit_bf16, ((int64_t)s * a.channels + d0 + c) * N + n, E[TW * CB * NP + i]);
-    }
+    if (a.dinit == nullptr || !joins || d0 + jc >= dend) return;
+    float v[4];
+    up2(ju[0], v[0], v[1]);
+    up2(ju[1], v[2], v[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (jn + e < N) st_st(a.dinit, a.dinit_bf16, ((int64_t)s * a.channels + d0 + jc) * N + jn + e, v[e]);
 }
 
 // ---- the gradients.  A block takes one chunk of SEL_Q tokens and a set of channels: warp w has the
 // w-th GT tokens, and the block goes through its channels 128 / NP at a time, a thread with four
-// states of one channel.
+// states of one channel.  The thread's B, C, dB and dC (GT tokens x four states of each) stay in registers
+// for the block's life: shared memory hands a thread one value a cycle, and would be the bound.
 constexpr int GT = 4, GW = SEL_Q / GT, GNT = 32 * GW, GC = 32;   // tokens a warp, warps, threads, channels staged at once
 
 template <int NP>
 constexpr size_t grad_smem() {
-    return (size_t)2 * SEL_Q * NP * 4 + (size_t)SEL_Q * GC * 16 + (size_t)3 * SEL_Q * GC * 4 + (size_t)GC * NP * 4 +
-           (size_t)3 * GW * 128 * 4 + (size_t)GW * 32 * 4 + (size_t)GW * GC * 8;
+    return (size_t)SEL_Q * GC * 16 + (size_t)3 * SEL_Q * GC * 4 + (size_t)GC * NP * 4 + (size_t)3 * GW * 128 * 4 +
+           (size_t)GW * 32 * 4 + (size_t)GW * GC * 8;
 }
 
 template <typename T, int NP>
-__global__ void __launch_bounds__(GNT, 2) k_sel_grad(const SelArgs a) {
+__global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
     constexpr int TPC = NP / 4, CPW = 32 / TPC;
+    static_assert(GNT == SEL_Q * GC / 4, "a thread has four channels of one token in the elementwise steps");
     extern __shared__ __align__(16) uint8_t sel_sm[];
-    float4 *sv = reinterpret_cast<float4 *>(sel_sm);                // [SEL_Q][GC]: (dt, dt x, dyp, -)
-    float *Bs = reinterpret_cast<float *>(sv + SEL_Q * GC);         // [SEL_Q][NP]
-    float *Cs = Bs + SEL_Q * NP;                                    // [SEL_Q][NP]
-    float *As = Cs + SEL_Q * NP;                                    // [GC][NP]: A log2(e)
+    float4 *sv = reinterpret_cast<float4 *>(sel_sm);                // [SEL_Q][GC]: dt, dt x, dyp, softplus'
+    float *As = reinterpret_cast<float *>(sv + SEL_Q * GC);         // [GC][NP]: A log2(e)
     float *EX = As + GC * NP;                                       // [2][GW][128]: ends, then entering values
     float *DA = EX + 2 * GW * 128;                                  // [GW][128]: shares of dA
     float *ov = DA + GW * 128;                                      // [3][SEL_Q][GC]: sums over the states
@@ -195,107 +304,137 @@ __global__ void __launch_bounds__(GNT, 2) k_sel_grad(const SelArgs a) {
         return;
     }
     const int64_t r0 = sq.t0 + tb;                                  // the chunk's first token in its row
-    const T *x = static_cast<const T *>(a.x) + sq.b * a.xb + r0 * a.xt;
-    const T *dy = static_cast<const T *>(a.dy) + sq.b * a.dyb + r0 * a.dyt;
-    const T *z = a.z ? static_cast<const T *>(a.z) + sq.b * a.zb + r0 * a.zt : nullptr;
-    const T *B = static_cast<const T *>(a.B) + sq.b * a.Bb + r0 * a.Bt + g * a.Bg;
-    const T *C = static_cast<const T *>(a.C) + sq.b * a.Cb + r0 * a.Ct + g * a.Cg;
-    T *dx = static_cast<T *>(a.dx) + sq.b * a.dxb + r0 * a.dxt;
-    T *dz = a.z ? static_cast<T *>(a.dz) + sq.b * a.dzb + r0 * a.dzt : nullptr;
-    const int64_t dt0 = sq.b * a.dtb + r0 * a.dtt, ddt0 = sq.b * a.ddtb + r0 * a.ddtt;
-    for (int i = tid; i < SEL_Q * NP; i += GNT) {
-        const int t = i / NP, n = i % NP;
-        const bool in = t < n_tok && n < N;
-        Bs[i] = in ? to_f(B[t * a.Bt + n]) : 0.f;
-        Cs[i] = in ? to_f(C[t * a.Ct + n]) : 0.f;
-    }
-    f32x2 aB[GT][2], aC[GT][2];                                     // this thread's dB and dC
+    // the elementwise steps: this thread's token and first channel of those staged
+    const int pt = tid / (GC / 4), pc = 4 * (tid % (GC / 4));
+    const bool tok = pt < n_tok, vec = a.vec;
+    const int64_t rt = r0 + (tok ? pt : 0);
+    const T *x = static_cast<const T *>(a.x) + sq.b * a.xb + rt * a.xt + pc;
+    const T *dy = static_cast<const T *>(a.dy) + sq.b * a.dyb + rt * a.dyt + pc;
+    const T *z = a.z ? static_cast<const T *>(a.z) + sq.b * a.zb + rt * a.zt + pc : nullptr;
+    T *dx = static_cast<T *>(a.dx) + sq.b * a.dxb + rt * a.dxt + pc;
+    T *dz = a.z ? static_cast<T *>(a.dz) + sq.b * a.dzb + rt * a.dzt + pc : nullptr;
+    const int64_t dt0 = sq.b * a.dtb + rt * a.dtt + pc, ddt0 = sq.b * a.ddtb + rt * a.ddtt + pc;
+
+    f32x2 Bv[GT][2], Cv[GT][2], aB[GT][2], aC[GT][2];               // B and C, and this thread's dB and dC
 #pragma unroll
-    for (int t = 0; t < GT; ++t) aB[t][0] = aB[t][1] = aC[t][0] = aC[t][1] = 0;
+    for (int t = 0; t < GT; ++t) {
+        const bool in = w * GT + t < n_tok;
+        const int64_t row = r0 + w * GT + t;
+        float b[4], c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = q * 4 + e;
+            b[e] = in && n < N ? to_f(static_cast<const T *>(a.B)[sq.b * a.Bb + row * a.Bt + g * a.Bg + n]) : 0.f;
+            c[e] = in && n < N ? to_f(static_cast<const T *>(a.C)[sq.b * a.Cb + row * a.Ct + g * a.Cg + n]) : 0.f;
+        }
+        Bv[t][0] = pk2(b[0], b[1]); Bv[t][1] = pk2(b[2], b[3]);
+        Cv[t][0] = pk2(c[0], c[1]); Cv[t][1] = pk2(c[2], c[3]);
+        aB[t][0] = aB[t][1] = aC[t][0] = aC[t][1] = 0;
+    }
 
     for (int cb = c_lo; cb < c_hi; cb += GC) {
-        __syncthreads();
+        const int nc = tok ? min(max(c_hi - cb - pc, 0), 4) : 0;
+        {
+            float4 v[4];
+            float xv[4], yv[4], zv[4], r[4];
+            Raw4<T> r1, r2, r3;
+            r1.load(x + cb, nc, vec);
+            r2.load(dy + cb, nc, vec);
+            if (z) r3.load(z + cb, nc, vec);
+            if (a.dt_f32) {
+                Raw4<float> rd;
+                rd.load(static_cast<const float *>(a.dt) + dt0 + cb, nc, vec);
+                rd.f(r);
+            } else {
+                Raw4<T> rd;
+                rd.load(static_cast<const T *>(a.dt) + dt0 + cb, nc, vec);
+                rd.f(r);
+            }
+            r1.f(xv);
+            r2.f(yv);
+            if (z) r3.f(zv);
 #pragma unroll
-        for (int k = 0; k < SEL_Q * GC / GNT; ++k) {
-            const int i = tid + k * GNT, t = i / GC, c = i % GC, dc = cb + c;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (t < n_tok && dc < c_hi) {
-                v.x = sel_softplus(ld_dt(a, dt0 + t * a.dtt + dc) + (a.bias ? a.bias[dc] : 0.f));
-                v.y = v.x * to_f(x[t * a.xt + dc]);
-                v.z = to_f(dy[t * a.dyt + dc]);
-                if (z) {
-                    const float zv = to_f(z[t * a.zt + dc]);
-                    v.z *= zv * sigf(zv);
+            for (int i = 0; i < 4; ++i) {
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < nc) {
+                    const float raw = r[i] + (a.bias ? a.bias[cb + pc + i] : 0.f);
+                    v[i].x = sel_softplus(raw);
+                    v[i].y = v[i].x * xv[i];
+                    v[i].z = z ? yv[i] * zv[i] * sigf(zv[i]) : yv[i];
+                    v[i].w = sigf(raw);
                 }
             }
-            sv[i] = v;
+            __syncthreads();                                        // the last channels are done with
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sv[pt * GC + pc + i] = v[i];
         }
         for (int i = tid; i < GC * NP; i += GNT) {
             const int c = i / NP, n = i % NP;
             As[i] = cb + c < c_hi && n < N ? a.A[(int64_t)(cb + c) * N + n] * kLog2e : 0.f;
         }
         __syncthreads();
+#pragma unroll 1
         for (int it = 0; it < TPC; ++it) {                          // CPW channels at a time
             const int c = it * CPW + cw;
-            // what enters the chunk, for the joining below: threads 0..127 the state, 128..255 the adjoint
-            const int dir = tid >> 7, p = tid & 127, pc = it * CPW + p / NP, pn = p % NP;
-            const bool pin = cb + pc < c_hi;
-            const float *src = dir ? a.adj : a.states;
-            float carry = pin ? src[((int64_t)slot * a.channels + cb + pc) * NP + pn] : 0.f;
+            // what enters the chunk, for the joining below: warp 0 the state, warp 1 the adjoint, four states a lane
+            ulonglong2 carry = make_ulonglong2(0, 0);
+            const int64_t at = ((int64_t)slot * a.channels + cb + c) * NP + q * 4;
+            if (w < 2 && cb + c < c_hi) carry = *reinterpret_cast<const ulonglong2 *>((w ? a.adj : a.states) + at);
 
             const ulonglong2 av = *reinterpret_cast<const ulonglong2 *>(As + c * NP + q * 4);
             const float4 *vp = sv + w * GT * GC + c;
-            const float *bp = Bs + w * GT * NP + q * 4, *cp = Cs + w * GT * NP + q * 4;
             f32x2 al[GT][2], h[GT + 1][2], u[2];
             h[0][0] = h[0][1] = u[0] = u[1] = 0;
             float sum = 0.f;
 #pragma unroll
             for (int t = 0; t < GT; ++t) {
-                const float4 v = vp[t * GC];
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(bp + t * NP);
+                const float2 v = *reinterpret_cast<const float2 *>(vp + t * GC);
                 const f32x2 dt2 = pk2(v.x, v.x), dx2 = pk2(v.y, v.y);
                 sum += v.x;
                 al[t][0] = ex2x2(mul2(dt2, av.x));
                 al[t][1] = ex2x2(mul2(dt2, av.y));
-                h[0][0] = fma2(al[t][0], h[0][0], mul2(dx2, b.x));
-                h[0][1] = fma2(al[t][1], h[0][1], mul2(dx2, b.y));
+                h[0][0] = fma2(al[t][0], h[0][0], mul2(dx2, Bv[t][0]));
+                h[0][1] = fma2(al[t][1], h[0][1], mul2(dx2, Bv[t][1]));
             }
 #pragma unroll
             for (int t = GT - 1; t >= 0; --t) {
                 const float v = vp[t * GC].z;
-                const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(cp + t * NP);
                 const f32x2 dy2 = pk2(v, v);
-                u[0] = mul2(al[t][0], fma2(cv.x, dy2, u[0]));
-                u[1] = mul2(al[t][1], fma2(cv.y, dy2, u[1]));
+                u[0] = mul2(al[t][0], fma2(Cv[t][0], dy2, u[0]));
+                u[1] = mul2(al[t][1], fma2(Cv[t][1], dy2, u[1]));
             }
             *reinterpret_cast<ulonglong2 *>(EX + w * 128 + lane * 4) = make_ulonglong2(h[0][0], h[0][1]);
             *reinterpret_cast<ulonglong2 *>(EX + (GW + w) * 128 + lane * 4) = make_ulonglong2(u[0], u[1]);
             if (q == 0) Sd[w * 32 + cw] = sum;
             __syncthreads();
-            {
-                const float An = As[pc * NP + pn];
-                const float *sd = Sd + p / NP;
-                if (dir == 0) {
+            if (w < 2) {
+                ulonglong2 end[GW];
+                float sd[GW];
+                float *ex = EX + w * GW * 128 + lane * 4;
 #pragma unroll
-                    for (int k = 0; k < GW; ++k) {
-                        const float end = EX[k * 128 + p];
-                        EX[k * 128 + p] = carry;
-                        carry = fmaf(ex2f(An * sd[k * 32]), carry, end);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = GW - 1; k >= 0; --k) {
-                        const float end = EX[(GW + k) * 128 + p];
-                        EX[(GW + k) * 128 + p] = carry;
-                        carry = fmaf(ex2f(An * sd[k * 32]), carry, end);
-                    }
-                    if (it > 0 && cb + pc - CPW < c_hi) {           // the last channels' dA, over the warps
-                        float v = 0.f;
-#pragma unroll
-                        for (int k = 0; k < GW; ++k) v += DA[k * 128 + p];
-                        a.pA[((int64_t)slot * a.channels + cb + pc - CPW) * NP + pn] = v;
-                    }
+                for (int k = 0; k < GW; ++k) {
+                    end[k] = *reinterpret_cast<const ulonglong2 *>(ex + k * 128);
+                    sd[k] = Sd[k * 32 + cw];
                 }
+#pragma unroll
+                for (int kk = 0; kk < GW; ++kk) {
+                    // the state from the first warp's tokens on, the adjoint from the last one's
+                    const ulonglong2 e = w ? end[GW - 1 - kk] : end[kk];
+                    const float sk = w ? sd[GW - 1 - kk] : sd[kk];
+                    *reinterpret_cast<ulonglong2 *>(ex + (w ? GW - 1 - kk : kk) * 128) = carry;
+                    const f32x2 sd2 = pk2(sk, sk);
+                    carry.x = fma2(ex2x2(mul2(sd2, av.x)), carry.x, e.x);
+                    carry.y = fma2(ex2x2(mul2(sd2, av.y)), carry.y, e.y);
+                }
+            } else if (w == 2 && it > 0 && cb + c - CPW < c_hi) {   // the last channels' dA, over the warps
+                f32x2 v0 = 0, v1 = 0;
+#pragma unroll
+                for (int k = 0; k < GW; ++k) {
+                    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(DA + k * 128 + lane * 4);
+                    v0 = add2(v0, v.x);
+                    v1 = add2(v1, v.y);
+                }
+                *reinterpret_cast<ulonglong2 *>(a.pA + at - CPW * NP) = make_ulonglong2(v0, v1);
             }
             __syncthreads();
             {
@@ -305,29 +444,25 @@ __global__ void __launch_bounds__(GNT, 2) k_sel_grad(const SelArgs a) {
                 u[0] = e.x; u[1] = e.y;
             }
             float ys[GT], es[GT], fs[GT];
+            f32x2 dA[2] = {0, 0};
+            float4 sr[GT];
 #pragma unroll
             for (int t = 0; t < GT; ++t) {
-                const float4 v = vp[t * GC];
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(bp + t * NP);
-                const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(cp + t * NP);
-                const f32x2 dx2 = pk2(v.y, v.y), dy2 = pk2(v.z, v.z);
-                h[t + 1][0] = fma2(al[t][0], h[t][0], mul2(dx2, b.x));
-                h[t + 1][1] = fma2(al[t][1], h[t][1], mul2(dx2, b.y));
-                ys[t] = sum2(fma2(h[t + 1][1], cv.y, mul2(h[t + 1][0], cv.x)));
+                sr[t] = vp[t * GC];
+                const f32x2 dx2 = pk2(sr[t].y, sr[t].y), dy2 = pk2(sr[t].z, sr[t].z);
+                h[t + 1][0] = fma2(al[t][0], h[t][0], mul2(dx2, Bv[t][0]));
+                h[t + 1][1] = fma2(al[t][1], h[t][1], mul2(dx2, Bv[t][1]));
+                ys[t] = sum2(fma2(h[t + 1][1], Cv[t][1], mul2(h[t + 1][0], Cv[t][0])));
                 aC[t][0] = fma2(h[t + 1][0], dy2, aC[t][0]);
                 aC[t][1] = fma2(h[t + 1][1], dy2, aC[t][1]);
             }
-            f32x2 dA[2] = {0, 0};
 #pragma unroll
             for (int t = GT - 1; t >= 0; --t) {
-                const float4 v = vp[t * GC];
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(bp + t * NP);
-                const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(cp + t * NP);
-                const f32x2 dt2 = pk2(v.x, v.x), dx2 = pk2(v.y, v.y), dy2 = pk2(v.z, v.z);
-                const f32x2 g0 = fma2(cv.x, dy2, u[0]), g1 = fma2(cv.y, dy2, u[1]);
+                const f32x2 dt2 = pk2(sr[t].x, sr[t].x), dx2 = pk2(sr[t].y, sr[t].y), dy2 = pk2(sr[t].z, sr[t].z);
+                const f32x2 g0 = fma2(Cv[t][0], dy2, u[0]), g1 = fma2(Cv[t][1], dy2, u[1]);
                 aB[t][0] = fma2(g0, dx2, aB[t][0]);
                 aB[t][1] = fma2(g1, dx2, aB[t][1]);
-                es[t] = sum2(fma2(g1, b.y, mul2(g0, b.x)));
+                es[t] = sum2(fma2(g1, Bv[t][1], mul2(g0, Bv[t][0])));
                 u[0] = mul2(al[t][0], g0);
                 u[1] = mul2(al[t][1], g1);
                 const f32x2 k0 = mul2(u[0], h[t][0]), k1 = mul2(u[1], h[t][1]);
@@ -343,45 +478,78 @@ __global__ void __launch_bounds__(GNT, 2) k_sel_grad(const SelArgs a) {
                 fq += __shfl_xor_sync(0xffffffffu, fq, o);
             }
             if (q < GT) {
-                const int at = (w * GT + q) * GC + c;
-                ov[at] = yq;
-                ov[SEL_Q * GC + at] = eq;
-                ov[2 * SEL_Q * GC + at] = fq * 0.6931471805599453f;   // av holds A log2(e)
+                const int o = (w * GT + q) * GC + c;
+                ov[o] = yq;
+                ov[SEL_Q * GC + o] = eq;
+                ov[2 * SEL_Q * GC + o] = fq * 0.6931471805599453f;  // av holds A log2(e)
             }
             *reinterpret_cast<ulonglong2 *>(DA + w * 128 + lane * 4) = make_ulonglong2(dA[0], dA[1]);
         }
+        // for the elementwise end, ahead of the barrier
+        Raw4<T> r1, r2, r3;
+        r1.load(x + cb, nc, vec);
+        if (z) {
+            r2.load(dy + cb, nc, vec);
+            r3.load(z + cb, nc, vec);
+        }
         __syncthreads();
-        if (tid < 128) {
-            const int pc = (TPC - 1) * CPW + tid / NP, pn = tid % NP;
-            float v = 0.f;
+        if (w == 2 && cb + (TPC - 1) * CPW + cw < c_hi) {
+            f32x2 v0 = 0, v1 = 0;
 #pragma unroll
-            for (int k = 0; k < GW; ++k) v += DA[k * 128 + tid];
-            if (cb + pc < c_hi) a.pA[((int64_t)slot * a.channels + cb + pc) * NP + pn] = v;
-        }
-        float sD = 0.f, sb = 0.f;
-        const int c = tid % GC, dc = cb + c;
-        if (dc < c_hi) {
-            const float Dv = a.D ? a.D[dc] : 0.f, bias = a.bias ? a.bias[dc] : 0.f;
-#pragma unroll
-            for (int k = 0; k < SEL_Q * GC / GNT; ++k) {
-                const int i = tid + k * GNT, t = i / GC;
-                if (t >= n_tok) continue;
-                const float4 v = sv[i];
-                const float xv = to_f(x[t * a.xt + dc]), e = ov[SEL_Q * GC + i];
-                const float raw = ld_dt(a, dt0 + t * a.dtt + dc) + bias;
-                const float dr = fmaf(e, xv, ov[2 * SEL_Q * GC + i]) * sigf(raw);
-                dx[t * a.dxt + dc] = from_f<T>(fmaf(e, v.x, Dv * v.z));
-                if (a.dt_f32) static_cast<float *>(a.ddt)[ddt0 + t * a.ddtt + dc] = dr;
-                else static_cast<__nv_bfloat16 *>(a.ddt)[ddt0 + t * a.ddtt + dc] = __float2bfloat16_rn(dr);
-                if (z) {
-                    const float zv = to_f(z[t * a.zt + dc]), sg = sigf(zv);
-                    dz[t * a.dzt + dc] = from_f<T>(to_f(dy[t * a.dyt + dc]) * fmaf(Dv, xv, ov[i]) * sg * (1.f + zv * (1.f - sg)));
-                }
-                sD = fmaf(v.z, xv, sD);
-                sb += dr;
+            for (int k = 0; k < GW; ++k) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(DA + k * 128 + lane * 4);
+                v0 = add2(v0, v.x);
+                v1 = add2(v1, v.y);
             }
+            *reinterpret_cast<ulonglong2 *>(a.pA + ((int64_t)slot * a.channels + cb + (TPC - 1) * CPW + cw) * NP + q * 4) = make_ulonglong2(v0, v1);
         }
-        red[w * GC + c] = make_float2(sD, sb);                      // thread (w, c) had tokens w, w + 8, ...
+        float sD[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+        if (nc > 0) {
+            float xv[4], yv[4], zv[4], ox[4], ot[4], oz[4], ya[4], ea[4], fa[4];
+            const int o = pt * GC + pc;
+            r1.f(xv);
+            if (z) {
+                r2.f(yv);
+                r3.f(zv);
+            }
+            Raw4<float> rv;
+            rv.load(ov + o, 4, true);
+            rv.f(ya);
+            rv.load(ov + SEL_Q * GC + o, 4, true);
+            rv.f(ea);
+            rv.load(ov + 2 * SEL_Q * GC + o, 4, true);
+            rv.f(fa);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ox[i] = ot[i] = oz[i] = 0.f;
+                if (i < nc) {
+                    const float4 v = sv[o + i];
+                    const float Dv = a.D ? a.D[cb + pc + i] : 0.f;
+                    ox[i] = fmaf(ea[i], v.x, a.D ? Dv * v.z : 0.f);
+                    ot[i] = fmaf(ea[i], xv[i], fa[i]) * v.w;
+                    if (z) {
+                        const float sg = sigf(zv[i]);
+                        oz[i] = yv[i] * (a.D ? fmaf(Dv, xv[i], ya[i]) : ya[i]) * sg * fmaf(zv[i], 1.f - sg, 1.f);
+                    }
+                    sD[i] = v.z * xv[i];
+                    sb[i] = ot[i];
+                }
+            }
+            store4(dx + cb, ox, nc, a.vec_out);
+            if (a.dt_f32) store4(static_cast<float *>(a.ddt) + ddt0 + cb, ot, nc, a.vec_out);
+            else store4(static_cast<T *>(a.ddt) + ddt0 + cb, ot, nc, a.vec_out);
+            if (z) store4(dz + cb, oz, nc, a.vec_out);
+        }
+        // the chunk's share of dD and ddt_bias: over the warp's tokens (lanes 8 apart), then over the warps
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int o = GC / 4; o < 32; o <<= 1) {
+                sD[i] += __shfl_xor_sync(0xffffffffu, sD[i], o);
+                sb[i] += __shfl_xor_sync(0xffffffffu, sb[i], o);
+            }
+            if (lane < GC / 4) red[w * GC + pc + i] = make_float2(sD[i], sb[i]);
+        }
         __syncthreads();
         if (tid < GC && cb + tid < c_hi) {
             float2 v = make_float2(0.f, 0.f);
@@ -465,10 +633,11 @@ __global__ void __launch_bounds__(256) k_sel_cols(const SelArgs a, int64_t block
 template <typename T, typename F>
 cudaError_t launch_rev(const SelArgs &a, cudaStream_t st) {
     static int attr[64] = {0};
-    cudaError_t e = ensure_smem_attr(k_sel_rev<T, F>, (int)F::smem, attr);
+    const size_t sm = F::template smem<T>(a.dt_f32);
+    cudaError_t e = ensure_smem_attr(k_sel_rev<T, F>, (int)sm, attr);
     if (e != cudaSuccess) return e;
     const int cblocks = a.ngroups * ((a.dpg + F::CB - 1) / F::CB);
-    k_sel_rev<T, F><<<(unsigned)((int64_t)a.nseqs * cblocks), F::NT, F::smem, st>>>(a, cblocks);
+    k_sel_rev<T, F><<<(unsigned)((int64_t)a.nseqs * cblocks), F::NT, sm, st>>>(a, cblocks);
     return cudaGetLastError();
 }
 template <typename T, int NP>
@@ -484,10 +653,10 @@ template <typename T>
 cudaError_t run_bwd(const SelArgs &a, cudaStream_t st) {
     cudaError_t e;
     switch (a.NP) {
-        case 16: e = launch_rev<T, RevCfg<8, 2, 2, 8, 16>>(a, st); break;
-        case 32: e = launch_rev<T, RevCfg<8, 4, 4, 4, 16>>(a, st); break;
-        case 64: e = launch_rev<T, RevCfg<8, 8, 4, 4, 16>>(a, st); break;
-        default: e = launch_rev<T, RevCfg<8, 16, 4, 4, 16>>(a, st);
+        case 16: e = launch_rev<T, RevCfg<4, 4, 1, 8, 16, 2>>(a, st); break;
+        case 32: e = launch_rev<T, RevCfg<8, 4, 1, 8, 16, 2>>(a, st); break;
+        case 64: e = launch_rev<T, RevCfg<8, 8, 1, 4, 16, 3>>(a, st); break;
+        default: e = launch_rev<T, RevCfg<8, 16, 1, 4, 16, 2>>(a, st);
     }
     if (e != cudaSuccess) return e;
     if (a.nslots > 0) {

@@ -30,7 +30,7 @@ struct Cfg {
     static constexpr int U = TPC / 2;                                                    // tokens summed over lanes at once
     // fours of a warp's x and of its B: rows a pass of the warp covers, passes
     static constexpr int RX = 128 / CPW, PX = (TK + RX - 1) / RX, RB = NP < 128 ? 128 / NP : 1, PB = (TK + RB - 1) / RB;
-    static_assert(TPC >= 2 && TK % U == 0 && SEL_Q % TK == 0 && TT % SEL_Q == 0 && S % 4 == 0, "tile shape");
+    static_assert(TPC >= 2 && TK % U == 0 && (TW == 1 ? TK % SEL_Q == 0 : SEL_Q % TK == 0) && TT % SEL_Q == 0 && S % 4 == 0, "tile shape");
     static_assert(TW == 1 || CB * NP / 4 <= NT, "the joining takes a thread for four states");
     // bytes a warp keeps: (dt, dt x), B, C, and the next tile as it comes
     static constexpr size_t wsmem(size_t ts, size_t ds) {
@@ -278,23 +278,25 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
                     h[c][2 * i] = v.x;
                     h[c][2 * i + 1] = v.y;
                 }
-        } else if (a.states && t0 % SEL_Q == 0) {
-            const int slot = sq.slot0 + t0 / SEL_Q;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                if (d + c < dend && slot < a.nslots) {
-                    ulonglong2 *sp = reinterpret_cast<ulonglong2 *>(a.states + ((int64_t)slot * a.channels + d + c) * NP + q * S);
-#pragma unroll
-                    for (int i = 0; i < S / 4; ++i) sp[i] = make_ulonglong2(h[c][2 * i], h[c][2 * i + 1]);
-                }
         }
         if (TW == 1) early();
         if (live) {
             // The sums stay in registers over SB batches of tokens: a store after each would hold up the
             // next tokens' loads (the compiler cannot tell that they differ), and with them everything.
-            constexpr int SB = TK / U < 4 ? TK / U : 4;
+            constexpr int SB = SEL_Q / U < 4 ? SEL_Q / U : 4;
+            static_assert(SEL_Q % (SB * U) == 0 && TK % (SB * U) == 0, "chunks start at batches");
 #pragma unroll 1
             for (int t0s = 0; t0s < TK; t0s += SB * U) {
+                if (TW == 1 && a.states && t0s % SEL_Q == 0 && tw + t0s < len) {
+                    const int slot = sq.slot0 + (tw + t0s) / SEL_Q;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        if (d + c < dend && slot < a.nslots) {
+                            ulonglong2 *sp = reinterpret_cast<ulonglong2 *>(a.states + ((int64_t)slot * a.channels + d + c) * NP + q * S);
+#pragma unroll
+                            for (int i = 0; i < S / 4; ++i) sp[i] = make_ulonglong2(h[c][2 * i], h[c][2 * i + 1]);
+                        }
+                }
                 float yq[SB];
 #pragma unroll
                 for (int sb = 0; sb < SB; ++sb) {

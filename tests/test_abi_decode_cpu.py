@@ -109,13 +109,13 @@ def test_selective_outputs_and_workspace(m):
 
 
 def test_selective_chunk_states_size(m):
-    """f32 [chunk slots][channels][dstate padded]: a slot per 32 tokens; packed, one more per sequence."""
+    """f32 [chunk slots][channels][dstate padded]: a slot per 16 tokens; packed, one more per sequence."""
     def size(p):
         n = ctypes.c_size_t(0)
         assert m.load().ssd_selective_chunk_states_size(ctypes.byref(p), ctypes.byref(n)) == 0
         return n.value
-    assert size(m.SelectiveProblem(2, 65, 24, 2, 12, 0)) == 2 * 3 * 24 * 16 * 4
-    assert size(m.SelectiveProblem(1, 65, 24, 2, 17, 5)) == (2 + 5) * 24 * 32 * 4
+    assert size(m.SelectiveProblem(2, 65, 24, 2, 12, 0)) == 2 * 5 * 24 * 16 * 4
+    assert size(m.SelectiveProblem(1, 65, 24, 2, 17, 5)) == (4 + 5) * 24 * 32 * 4
     assert size(m.SelectiveProblem(2, 0, 24, 2, 12, 0)) == 0
 
 
