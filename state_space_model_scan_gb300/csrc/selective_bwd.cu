@@ -23,6 +23,10 @@
 #ifndef GRAD_OCC
 #define GRAD_OCC 3
 #endif
+#ifndef GRAD_UN
+#define GRAD_UN 1
+#endif
+constexpr int GRAD_U = GRAD_UN;
 
 namespace ssd {
 
@@ -254,29 +258,35 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
 }
 
 // ---- the gradients.  A block takes one chunk of SEL_Q tokens and a set of channels: warp w has the
-// w-th GT tokens, and the block goes through its channels 128 / NP at a time, a thread with four
-// states of one channel.  The thread's B, C, dB and dC (GT tokens x four states of each) stay in registers
-// for the block's life: shared memory hands a thread one value a cycle, and would be the bound.
-constexpr int GT = 4, GW = SEL_Q / GT, GNT = 32 * GW, GC = 32;   // tokens a warp, warps, threads, channels staged at once
-
-template <int NP>
-constexpr size_t grad_smem() {
-    return (size_t)SEL_Q * GC * 16 + (size_t)3 * SEL_Q * GC * 4 + (size_t)GC * NP * 4 + (size_t)3 * GW * 128 * 4 +
-           (size_t)GW * 32 * 4 + (size_t)GW * GC * 8;
-}
+// w-th GT tokens, a thread four states of one channel, and the block goes through its channels GC at a
+// time, in IT steps of 128 / NP.  The thread's B, C, dB and dC (GT tokens x four states of each) stay in
+// registers for the block's life: shared memory hands a thread one value a cycle, and would be the
+// bound.  For each GC channels the warps first sweep their tokens from zero (the state forwards, the
+// adjoint backwards), the ends are joined with what enters the chunk, and then the warps sweep again
+// from what really enters their tokens; the next channels' inputs come in the background.
+constexpr int GT = 4, GW = SEL_Q / GT, GNT = 32 * GW, IT = 4;   // tokens a warp, warps, threads, steps
+template <typename T, int NP>
+struct Grad {
+    static constexpr int TPC = NP / 4, CPW = 32 / TPC, GC = IT * CPW, OP = GC + (CPW > 4 ? CPW : 4);   // (OP: row of the sums, off the banks)
+    float4 sv[SEL_Q * GC];             // dt, dt x, dyp, softplus' of (token, channel), four channels of a row swapped by place()
+    float As[GC * NP];                 // A log2(e)
+    float EX[2][IT][GW][128];          // state and adjoint: what the warps end with, then what enters their tokens
+    float DA[IT][GW][128];             // shares of dA
+    float ov[3][SEL_Q * OP];           // the sums over the states: C.h, e, f
+    float Sd[IT][GW][32];              // sums of dt
+    float2 red[2][GW][GC];             // shares of dD and ddt_bias, of this and the last channels
+    T rx[2][SEL_Q * GC], ry[2][SEL_Q * GC], rz[2][SEL_Q * GC];   // the inputs as they come, of these and the next channels
+    float rd[2][SEL_Q * GC];           // dt: fp32 or T
+    // where channel c of a token lies: a thread writes four neighbours, eight threads neighbouring fours
+    static __device__ __forceinline__ int place(int c) { return c ^ (c >> 3 & 3); }
+};
 
 template <typename T, int NP>
 __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
-    constexpr int TPC = NP / 4, CPW = 32 / TPC;
-    static_assert(GNT == SEL_Q * GC / 4, "a thread has four channels of one token in the elementwise steps");
+    using G = Grad<T, NP>;
+    constexpr int TPC = G::TPC, CPW = G::CPW, GC = G::GC, OP = G::OP;
     extern __shared__ __align__(16) uint8_t sel_sm[];
-    float4 *sv = reinterpret_cast<float4 *>(sel_sm);                // [SEL_Q][GC]: dt, dt x, dyp, softplus'
-    float *As = reinterpret_cast<float *>(sv + SEL_Q * GC);         // [GC][NP]: A log2(e)
-    float *EX = As + GC * NP;                                       // [2][GW][128]: ends, then entering values
-    float *DA = EX + 2 * GW * 128;                                  // [GW][128]: shares of dA
-    float *ov = DA + GW * 128;                                      // [3][SEL_Q][GC]: sums over the states
-    float *Sd = ov + 3 * SEL_Q * GC;                                // [GW][32]: sums of dt
-    float2 *red = reinterpret_cast<float2 *>(Sd + GW * 32);         // [GW][GC]
+    G &m = *reinterpret_cast<G *>(sel_sm);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, q = lane % TPC, cw = lane / TPC;
     const int set = blockIdx.x % a.nsets, g = blockIdx.x / a.nsets % a.ngroups, slot = blockIdx.x / a.nsets / a.ngroups;
     const int N = a.N;
@@ -305,15 +315,16 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
     }
     const int64_t r0 = sq.t0 + tb;                                  // the chunk's first token in its row
     // the elementwise steps: this thread's token and first channel of those staged
-    const int pt = tid / (GC / 4), pc = 4 * (tid % (GC / 4));
-    const bool tok = pt < n_tok, vec = a.vec;
+    const int pt = tid / (GC / 4), pc = 4 * (tid % (GC / 4)), po = pt * GC + pc;
+    const bool tok = pt < n_tok, vec = a.vec, gated = a.z != nullptr;
     const int64_t rt = r0 + (tok ? pt : 0);
     const T *x = static_cast<const T *>(a.x) + sq.b * a.xb + rt * a.xt + pc;
     const T *dy = static_cast<const T *>(a.dy) + sq.b * a.dyb + rt * a.dyt + pc;
-    const T *z = a.z ? static_cast<const T *>(a.z) + sq.b * a.zb + rt * a.zt + pc : nullptr;
+    const T *z = gated ? static_cast<const T *>(a.z) + sq.b * a.zb + rt * a.zt + pc : nullptr;
     T *dx = static_cast<T *>(a.dx) + sq.b * a.dxb + rt * a.dxt + pc;
-    T *dz = a.z ? static_cast<T *>(a.dz) + sq.b * a.dzb + rt * a.dzt + pc : nullptr;
+    T *dz = gated ? static_cast<T *>(a.dz) + sq.b * a.dzb + rt * a.dzt + pc : nullptr;
     const int64_t dt0 = sq.b * a.dtb + rt * a.dtt + pc, ddt0 = sq.b * a.ddtb + rt * a.ddtt + pc;
+    const int64_t e0 = (int64_t)slot * a.channels * NP + tid * 4;   // this thread's four (channel, state) of IT x 32 fours
 
     f32x2 Bv[GT][2], Cv[GT][2], aB[GT][2], aC[GT][2];               // B and C, and this thread's dB and dC
 #pragma unroll
@@ -331,143 +342,179 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
         Cv[t][0] = pk2(c[0], c[1]); Cv[t][1] = pk2(c[2], c[3]);
         aB[t][0] = aB[t][1] = aC[t][0] = aC[t][1] = 0;
     }
+    auto count = [&](int cb) { return tok ? min(max(c_hi - cb - pc, 0), 4) : 0; };
+    auto fetch = [&](int cb, int k) {                               // the inputs of channels cb.., in the background
+        const int nc = count(cb);
+        fetch4(m.rx[k] + po, x + cb, nc, vec);
+        fetch4(m.ry[k] + po, dy + cb, nc, vec);
+        if (gated) fetch4(m.rz[k] + po, z + cb, nc, vec);
+        if (a.dt_f32) fetch4(m.rd[k] + po, static_cast<const float *>(a.dt) + dt0 + cb, nc, vec);
+        else fetch4(reinterpret_cast<T *>(m.rd[k]) + po, static_cast<const T *>(a.dt) + dt0 + cb, nc, vec);
+        cp_async_commit();
+    };
+    auto put_pD = [&](int cb, int k) {                              // the warps' shares of dD and ddt_bias
+        if (tid < GC && cb + tid < c_hi) {
+            float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < GW; ++i) {
+                v.x += m.red[k][i][tid].x;
+                v.y += m.red[k][i][tid].y;
+            }
+            reinterpret_cast<float2 *>(a.pD)[(int64_t)slot * a.channels + cb + tid] = v;
+        }
+    };
 
-    for (int cb = c_lo; cb < c_hi; cb += GC) {
-        const int nc = tok ? min(max(c_hi - cb - pc, 0), 4) : 0;
-        {
-            float4 v[4];
+    if (pt < SEL_Q) fetch(c_lo, 0);
+    int k = 0;                                                      // the buffer of these channels' inputs
+    for (int cb = c_lo; cb < c_hi; cb += GC, k ^= 1) {
+        const int nc = pt < SEL_Q ? count(cb) : 0;
+        // this thread's share of A and of what enters the chunk
+        const bool mine = cb + tid * 4 / NP < c_hi;
+        float Aq[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = tid * 4 % NP + e;
+            Aq[e] = mine && n < N ? a.A[(int64_t)(cb + tid * 4 / NP) * N + n] * kLog2e : 0.f;
+        }
+        ulonglong2 hin = make_ulonglong2(0, 0), uin = hin;
+        if (mine) {
+            hin = *reinterpret_cast<const ulonglong2 *>(a.states + e0 + (int64_t)cb * NP);
+            uin = *reinterpret_cast<const ulonglong2 *>(a.adj + e0 + (int64_t)cb * NP);
+        }
+        put4(m.As + tid * 4, Aq);
+        cp_async_wait_all();                                        // (a thread stages what it fetched itself)
+        if (pt < SEL_Q) {
             float xv[4], yv[4], zv[4], r[4];
-            Raw4<T> r1, r2, r3;
-            r1.load(x + cb, nc, vec);
-            r2.load(dy + cb, nc, vec);
-            if (z) r3.load(z + cb, nc, vec);
+            Raw4<T> r1;
+            r1.load(m.rx[k] + po, 4, true);
+            r1.f(xv);
+            r1.load(m.ry[k] + po, 4, true);
+            r1.f(yv);
+            if (gated) {
+                r1.load(m.rz[k] + po, 4, true);
+                r1.f(zv);
+            }
             if (a.dt_f32) {
                 Raw4<float> rd;
-                rd.load(static_cast<const float *>(a.dt) + dt0 + cb, nc, vec);
+                rd.load(m.rd[k] + po, 4, true);
                 rd.f(r);
             } else {
-                Raw4<T> rd;
-                rd.load(static_cast<const T *>(a.dt) + dt0 + cb, nc, vec);
-                rd.f(r);
+                r1.load(reinterpret_cast<const T *>(m.rd[k]) + po, 4, true);
+                r1.f(r);
             }
-            r1.f(xv);
-            r2.f(yv);
-            if (z) r3.f(zv);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (i < nc) {
                     const float raw = r[i] + (a.bias ? a.bias[cb + pc + i] : 0.f);
-                    v[i].x = sel_softplus(raw);
-                    v[i].y = v[i].x * xv[i];
-                    v[i].z = z ? yv[i] * zv[i] * sigf(zv[i]) : yv[i];
-                    v[i].w = sigf(raw);
+                    v.x = sel_softplus(raw);
+                    v.y = v.x * xv[i];
+                    v.z = gated ? yv[i] * zv[i] * sigf(zv[i]) : yv[i];
+                    v.w = sigf(raw);
                 }
+                m.sv[pt * GC + G::place(pc + i)] = v;
             }
-            __syncthreads();                                        // the last channels are done with
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sv[pt * GC + pc + i] = v[i];
-        }
-        for (int i = tid; i < GC * NP; i += GNT) {
-            const int c = i / NP, n = i % NP;
-            As[i] = cb + c < c_hi && n < N ? a.A[(int64_t)(cb + c) * N + n] * kLog2e : 0.f;
         }
         __syncthreads();
-#pragma unroll 1
-        for (int it = 0; it < TPC; ++it) {                          // CPW channels at a time
+        if (cb > c_lo) put_pD(cb - GC, k ^ 1);
+        if (cb + GC < c_hi && pt < SEL_Q) fetch(cb + GC, k ^ 1);
+        // from zero
+#pragma unroll GRAD_U
+        for (int it = 0; it < IT; ++it) {
             const int c = it * CPW + cw;
-            // what enters the chunk, for the joining below: warp 0 the state, warp 1 the adjoint, four states a lane
-            ulonglong2 carry = make_ulonglong2(0, 0);
-            const int64_t at = ((int64_t)slot * a.channels + cb + c) * NP + q * 4;
-            if (w < 2 && cb + c < c_hi) carry = *reinterpret_cast<const ulonglong2 *>((w ? a.adj : a.states) + at);
-
-            const ulonglong2 av = *reinterpret_cast<const ulonglong2 *>(As + c * NP + q * 4);
-            const float4 *vp = sv + w * GT * GC + c;
-            f32x2 al[GT][2], h[GT + 1][2], u[2];
-            h[0][0] = h[0][1] = u[0] = u[1] = 0;
-            float sum = 0.f;
+            const ulonglong2 av = *reinterpret_cast<const ulonglong2 *>(m.As + c * NP + q * 4);
+            const float4 *vp = m.sv + w * GT * GC + G::place(c);
+            f32x2 al[GT][2], h[2] = {0, 0}, u[2] = {0, 0};
+            float sum = 0.f, yv[GT];
 #pragma unroll
             for (int t = 0; t < GT; ++t) {
-                const float2 v = *reinterpret_cast<const float2 *>(vp + t * GC);
+                const float4 v = vp[t * GC];
                 const f32x2 dt2 = pk2(v.x, v.x), dx2 = pk2(v.y, v.y);
+                yv[t] = v.z;
                 sum += v.x;
                 al[t][0] = ex2x2(mul2(dt2, av.x));
                 al[t][1] = ex2x2(mul2(dt2, av.y));
-                h[0][0] = fma2(al[t][0], h[0][0], mul2(dx2, Bv[t][0]));
-                h[0][1] = fma2(al[t][1], h[0][1], mul2(dx2, Bv[t][1]));
+                h[0] = fma2(al[t][0], h[0], mul2(dx2, Bv[t][0]));
+                h[1] = fma2(al[t][1], h[1], mul2(dx2, Bv[t][1]));
             }
 #pragma unroll
             for (int t = GT - 1; t >= 0; --t) {
-                const float v = vp[t * GC].z;
-                const f32x2 dy2 = pk2(v, v);
+                const f32x2 dy2 = pk2(yv[t], yv[t]);
                 u[0] = mul2(al[t][0], fma2(Cv[t][0], dy2, u[0]));
                 u[1] = mul2(al[t][1], fma2(Cv[t][1], dy2, u[1]));
             }
-            *reinterpret_cast<ulonglong2 *>(EX + w * 128 + lane * 4) = make_ulonglong2(h[0][0], h[0][1]);
-            *reinterpret_cast<ulonglong2 *>(EX + (GW + w) * 128 + lane * 4) = make_ulonglong2(u[0], u[1]);
-            if (q == 0) Sd[w * 32 + cw] = sum;
-            __syncthreads();
-            if (w < 2) {
-                ulonglong2 end[GW];
-                float sd[GW];
-                float *ex = EX + w * GW * 128 + lane * 4;
+            *reinterpret_cast<ulonglong2 *>(&m.EX[0][it][w][lane * 4]) = make_ulonglong2(h[0], h[1]);
+            *reinterpret_cast<ulonglong2 *>(&m.EX[1][it][w][lane * 4]) = make_ulonglong2(u[0], u[1]);
+            if (q == 0) m.Sd[it][w][cw] = sum;
+        }
+        __syncthreads();
+        {                                                           // warp w joins step w: the state onwards, the adjoint backwards
+            ulonglong2 eh[GW], eu[GW];
+            float sd[GW];
+            const f32x2 A0 = pk2(Aq[0], Aq[1]), A1 = pk2(Aq[2], Aq[3]);
 #pragma unroll
-                for (int k = 0; k < GW; ++k) {
-                    end[k] = *reinterpret_cast<const ulonglong2 *>(ex + k * 128);
-                    sd[k] = Sd[k * 32 + cw];
-                }
-#pragma unroll
-                for (int kk = 0; kk < GW; ++kk) {
-                    // the state from the first warp's tokens on, the adjoint from the last one's
-                    const ulonglong2 e = w ? end[GW - 1 - kk] : end[kk];
-                    const float sk = w ? sd[GW - 1 - kk] : sd[kk];
-                    *reinterpret_cast<ulonglong2 *>(ex + (w ? GW - 1 - kk : kk) * 128) = carry;
-                    const f32x2 sd2 = pk2(sk, sk);
-                    carry.x = fma2(ex2x2(mul2(sd2, av.x)), carry.x, e.x);
-                    carry.y = fma2(ex2x2(mul2(sd2, av.y)), carry.y, e.y);
-                }
-            } else if (w == 2 && it > 0 && cb + c - CPW < c_hi) {   // the last channels' dA, over the warps
-                f32x2 v0 = 0, v1 = 0;
-#pragma unroll
-                for (int k = 0; k < GW; ++k) {
-                    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(DA + k * 128 + lane * 4);
-                    v0 = add2(v0, v.x);
-                    v1 = add2(v1, v.y);
-                }
-                *reinterpret_cast<ulonglong2 *>(a.pA + at - CPW * NP) = make_ulonglong2(v0, v1);
+            for (int i = 0; i < GW; ++i) {
+                eh[i] = *reinterpret_cast<const ulonglong2 *>(&m.EX[0][w][i][lane * 4]);
+                eu[i] = *reinterpret_cast<const ulonglong2 *>(&m.EX[1][w][i][lane * 4]);
+                sd[i] = m.Sd[w][i][cw];
             }
-            __syncthreads();
-            {
-                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(EX + w * 128 + lane * 4);
-                h[0][0] = v.x; h[0][1] = v.y;
-                const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(EX + (GW + w) * 128 + lane * 4);
-                u[0] = e.x; u[1] = e.y;
+            f32x2 d0[GW], d1[GW];
+#pragma unroll
+            for (int i = 0; i < GW; ++i) {
+                const f32x2 sd2 = pk2(sd[i], sd[i]);
+                d0[i] = ex2x2(mul2(sd2, A0));
+                d1[i] = ex2x2(mul2(sd2, A1));
             }
+#pragma unroll
+            for (int i = 0; i < GW; ++i) {
+                const int l = GW - 1 - i;
+                *reinterpret_cast<ulonglong2 *>(&m.EX[0][w][i][lane * 4]) = hin;
+                *reinterpret_cast<ulonglong2 *>(&m.EX[1][w][l][lane * 4]) = uin;
+                hin.x = fma2(d0[i], hin.x, eh[i].x);
+                hin.y = fma2(d1[i], hin.y, eh[i].y);
+                uin.x = fma2(d0[l], uin.x, eu[l].x);
+                uin.y = fma2(d1[l], uin.y, eu[l].y);
+            }
+        }
+        __syncthreads();
+        // from what enters
+#pragma unroll 1
+        for (int it = 0; it < IT; ++it) {
+            const int c = it * CPW + cw;
+            const ulonglong2 av = *reinterpret_cast<const ulonglong2 *>(m.As + c * NP + q * 4);
+            const ulonglong2 hv = *reinterpret_cast<const ulonglong2 *>(&m.EX[0][it][w][lane * 4]);
+            const ulonglong2 uv = *reinterpret_cast<const ulonglong2 *>(&m.EX[1][it][w][lane * 4]);
+            const float4 *vp = m.sv + w * GT * GC + G::place(c);
+            f32x2 al[GT][2], h[GT + 1][2], u[2] = {uv.x, uv.y}, dA[2] = {0, 0};
+            h[0][0] = hv.x;
+            h[0][1] = hv.y;
             float ys[GT], es[GT], fs[GT];
-            f32x2 dA[2] = {0, 0};
-            float4 sr[GT];
+            f32x2 dt2[GT], dx2[GT], dy2[GT];
 #pragma unroll
             for (int t = 0; t < GT; ++t) {
-                sr[t] = vp[t * GC];
-                const f32x2 dx2 = pk2(sr[t].y, sr[t].y), dy2 = pk2(sr[t].z, sr[t].z);
-                h[t + 1][0] = fma2(al[t][0], h[t][0], mul2(dx2, Bv[t][0]));
-                h[t + 1][1] = fma2(al[t][1], h[t][1], mul2(dx2, Bv[t][1]));
+                const float4 v = vp[t * GC];
+                dt2[t] = pk2(v.x, v.x);
+                dx2[t] = pk2(v.y, v.y);
+                dy2[t] = pk2(v.z, v.z);
+                al[t][0] = ex2x2(mul2(dt2[t], av.x));
+                al[t][1] = ex2x2(mul2(dt2[t], av.y));
+                h[t + 1][0] = fma2(al[t][0], h[t][0], mul2(dx2[t], Bv[t][0]));
+                h[t + 1][1] = fma2(al[t][1], h[t][1], mul2(dx2[t], Bv[t][1]));
                 ys[t] = sum2(fma2(h[t + 1][1], Cv[t][1], mul2(h[t + 1][0], Cv[t][0])));
-                aC[t][0] = fma2(h[t + 1][0], dy2, aC[t][0]);
-                aC[t][1] = fma2(h[t + 1][1], dy2, aC[t][1]);
+                aC[t][0] = fma2(h[t + 1][0], dy2[t], aC[t][0]);
+                aC[t][1] = fma2(h[t + 1][1], dy2[t], aC[t][1]);
             }
 #pragma unroll
             for (int t = GT - 1; t >= 0; --t) {
-                const f32x2 dt2 = pk2(sr[t].x, sr[t].x), dx2 = pk2(sr[t].y, sr[t].y), dy2 = pk2(sr[t].z, sr[t].z);
-                const f32x2 g0 = fma2(Cv[t][0], dy2, u[0]), g1 = fma2(Cv[t][1], dy2, u[1]);
-                aB[t][0] = fma2(g0, dx2, aB[t][0]);
-                aB[t][1] = fma2(g1, dx2, aB[t][1]);
+                const f32x2 g0 = fma2(Cv[t][0], dy2[t], u[0]), g1 = fma2(Cv[t][1], dy2[t], u[1]);
+                aB[t][0] = fma2(g0, dx2[t], aB[t][0]);
+                aB[t][1] = fma2(g1, dx2[t], aB[t][1]);
                 es[t] = sum2(fma2(g1, Bv[t][1], mul2(g0, Bv[t][0])));
                 u[0] = mul2(al[t][0], g0);
                 u[1] = mul2(al[t][1], g1);
                 const f32x2 k0 = mul2(u[0], h[t][0]), k1 = mul2(u[1], h[t][1]);
-                dA[0] = fma2(k0, dt2, dA[0]);
-                dA[1] = fma2(k1, dt2, dA[1]);
+                dA[0] = fma2(k0, dt2[t], dA[0]);
+                dA[1] = fma2(k1, dt2[t], dA[1]);
                 fs[t] = sum2(fma2(k1, av.y, mul2(k0, av.x)));
             }
             float yq = reduce_scatter<GT>(ys, q % GT), eq = reduce_scatter<GT>(es, q % GT), fq = reduce_scatter<GT>(fs, q % GT);
@@ -478,56 +525,53 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
                 fq += __shfl_xor_sync(0xffffffffu, fq, o);
             }
             if (q < GT) {
-                const int o = (w * GT + q) * GC + c;
-                ov[o] = yq;
-                ov[SEL_Q * GC + o] = eq;
-                ov[2 * SEL_Q * GC + o] = fq * 0.6931471805599453f;  // av holds A log2(e)
+                const int o = (w * GT + q) * OP + c;
+                m.ov[0][o] = yq;
+                m.ov[1][o] = eq;
+                m.ov[2][o] = fq;
             }
-            *reinterpret_cast<ulonglong2 *>(DA + w * 128 + lane * 4) = make_ulonglong2(dA[0], dA[1]);
-        }
-        // for the elementwise end, ahead of the barrier
-        Raw4<T> r1, r2, r3;
-        r1.load(x + cb, nc, vec);
-        if (z) {
-            r2.load(dy + cb, nc, vec);
-            r3.load(z + cb, nc, vec);
+            *reinterpret_cast<ulonglong2 *>(&m.DA[it][w][lane * 4]) = make_ulonglong2(dA[0], dA[1]);
         }
         __syncthreads();
-        if (w == 2 && cb + (TPC - 1) * CPW + cw < c_hi) {
+        if (mine) {                                                 // warp w: step w's dA, over the warps' tokens
             f32x2 v0 = 0, v1 = 0;
 #pragma unroll
-            for (int k = 0; k < GW; ++k) {
-                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(DA + k * 128 + lane * 4);
+            for (int i = 0; i < GW; ++i) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.DA[w][i][lane * 4]);
                 v0 = add2(v0, v.x);
                 v1 = add2(v1, v.y);
             }
-            *reinterpret_cast<ulonglong2 *>(a.pA + ((int64_t)slot * a.channels + cb + (TPC - 1) * CPW + cw) * NP + q * 4) = make_ulonglong2(v0, v1);
+            *reinterpret_cast<ulonglong2 *>(a.pA + e0 + (int64_t)cb * NP) = make_ulonglong2(v0, v1);
         }
         float sD[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
         if (nc > 0) {
             float xv[4], yv[4], zv[4], ox[4], ot[4], oz[4], ya[4], ea[4], fa[4];
-            const int o = pt * GC + pc;
+            const int o = pt * OP + pc;
+            Raw4<T> r1;
+            r1.load(m.rx[k] + po, 4, true);
             r1.f(xv);
-            if (z) {
-                r2.f(yv);
-                r3.f(zv);
+            if (gated) {
+                r1.load(m.ry[k] + po, 4, true);
+                r1.f(yv);
+                r1.load(m.rz[k] + po, 4, true);
+                r1.f(zv);
             }
             Raw4<float> rv;
-            rv.load(ov + o, 4, true);
+            rv.load(m.ov[0] + o, 4, true);
             rv.f(ya);
-            rv.load(ov + SEL_Q * GC + o, 4, true);
+            rv.load(m.ov[1] + o, 4, true);
             rv.f(ea);
-            rv.load(ov + 2 * SEL_Q * GC + o, 4, true);
+            rv.load(m.ov[2] + o, 4, true);
             rv.f(fa);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 ox[i] = ot[i] = oz[i] = 0.f;
                 if (i < nc) {
-                    const float4 v = sv[o + i];
+                    const float4 v = m.sv[pt * GC + G::place(pc + i)];
                     const float Dv = a.D ? a.D[cb + pc + i] : 0.f;
                     ox[i] = fmaf(ea[i], v.x, a.D ? Dv * v.z : 0.f);
-                    ot[i] = fmaf(ea[i], xv[i], fa[i]) * v.w;
-                    if (z) {
+                    ot[i] = fmaf(ea[i], xv[i], fa[i] * 0.6931471805599453f) * v.w;   // (f was summed with A log2(e))
+                    if (gated) {
                         const float sg = sigf(zv[i]);
                         oz[i] = yv[i] * (a.D ? fmaf(Dv, xv[i], ya[i]) : ya[i]) * sg * fmaf(zv[i], 1.f - sg, 1.f);
                     }
@@ -538,9 +582,9 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
             store4(dx + cb, ox, nc, a.vec_out);
             if (a.dt_f32) store4(static_cast<float *>(a.ddt) + ddt0 + cb, ot, nc, a.vec_out);
             else store4(static_cast<T *>(a.ddt) + ddt0 + cb, ot, nc, a.vec_out);
-            if (z) store4(dz + cb, oz, nc, a.vec_out);
+            if (gated) store4(dz + cb, oz, nc, a.vec_out);
         }
-        // the chunk's share of dD and ddt_bias: over the warp's tokens (lanes 8 apart), then over the warps
+        // the chunk's share of dD and ddt_bias: over the warp's tokens (GC / 4 lanes each); the warps' below
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -548,29 +592,21 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
                 sD[i] += __shfl_xor_sync(0xffffffffu, sD[i], o);
                 sb[i] += __shfl_xor_sync(0xffffffffu, sb[i], o);
             }
-            if (lane < GC / 4) red[w * GC + pc + i] = make_float2(sD[i], sb[i]);
+            if (lane < GC / 4) m.red[k][w][pc + i] = make_float2(sD[i], sb[i]);
         }
-        __syncthreads();
-        if (tid < GC && cb + tid < c_hi) {
-            float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < GW; ++k) {
-                v.x += red[k * GC + tid].x;
-                v.y += red[k * GC + tid].y;
-            }
-            reinterpret_cast<float2 *>(a.pD)[(int64_t)slot * a.channels + cb + tid] = v;
-        }
+        __syncthreads();                                            // sv, ov and DA are free
     }
+    put_pD(c_lo + (c_hi - c_lo - 1) / GC * GC, k ^ 1);
     // dB and dC of this channel set: over the warp's channels, then one row of NP values a token
     const int64_t rows = (int64_t)a.nbatch * a.seqlen * a.ngroups;
 #pragma unroll
     for (int t = 0; t < GT; ++t) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int o = TPC; o < 32; o <<= 1) {
-                aB[t][k] = add2(aB[t][k], __shfl_xor_sync(0xffffffffu, aB[t][k], o));
-                aC[t][k] = add2(aC[t][k], __shfl_xor_sync(0xffffffffu, aC[t][k], o));
+                aB[t][i] = add2(aB[t][i], __shfl_xor_sync(0xffffffffu, aB[t][i], o));
+                aC[t][i] = add2(aC[t][i], __shfl_xor_sync(0xffffffffu, aC[t][i], o));
             }
         }
         const int tt = w * GT + t;
@@ -643,9 +679,9 @@ cudaError_t launch_rev(const SelArgs &a, cudaStream_t st) {
 template <typename T, int NP>
 cudaError_t launch_grad(const SelArgs &a, cudaStream_t st) {
     static int attr[64] = {0};
-    cudaError_t e = ensure_smem_attr(k_sel_grad<T, NP>, (int)grad_smem<NP>(), attr);
+    cudaError_t e = ensure_smem_attr(k_sel_grad<T, NP>, (int)sizeof(Grad<T, NP>), attr);
     if (e != cudaSuccess) return e;
-    k_sel_grad<T, NP><<<(unsigned)((int64_t)a.nslots * a.ngroups * a.nsets), GNT, grad_smem<NP>(), st>>>(a);
+    k_sel_grad<T, NP><<<(unsigned)((int64_t)a.nslots * a.ngroups * a.nsets), GNT, sizeof(Grad<T, NP>), st>>>(a);
     return cudaGetLastError();
 }
 
@@ -681,7 +717,7 @@ cudaError_t run_bwd(const SelArgs &a, cudaStream_t st) {
 void sel_bwd_sets(int channels, int ngroups, int64_t nslots, int *nsets, int *cps) {
     const int dpg = channels / ngroups;
     int c = 256;
-    while (c > GC && nslots * ngroups * ((dpg + c - 1) / c) < 1216) c >>= 1;
+    while (c > 32 && nslots * ngroups * ((dpg + c - 1) / c) < 1216) c >>= 1;
     *cps = c;
     *nsets = (dpg + c - 1) / c;
 }
