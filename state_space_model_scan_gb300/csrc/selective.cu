@@ -109,6 +109,7 @@ SelArgs make_args(const ssd_selective_problem *p, const ssd_fwd_args *f) {
     a.nslots = (int)chunk_slots(p);
     a.states = static_cast<float *>(f->chunk_states);
     a.vec = (p->ngroups == 1 || a.dpg % 4 == 0) && fours(f->x, 2) && fours(f->dt, 2) && fours(f->z, 2);
+    a.vecA = p->dstate % 4 == 0 && al(f->A.ptr, 16);
     a.vecBC = fours(f->B, 3) && fours(f->C, 3);
     return a;
 }

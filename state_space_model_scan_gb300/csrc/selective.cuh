@@ -19,8 +19,8 @@ struct SelArgs {
     int64_t xb, xt, dtb, dtt, Bb, Bt, Bg, Cb, Ct, Cg, zb, zt, dyb, dyt;   // element strides: batch row, token (, group)
     const float *A, *D, *bias;
     const void *init, *dfinal;
-    // four elements at places divisible by four are aligned to their size, in the channel tensors / in B and C
-    bool vec, vecBC, vec_out;          // (vec_out: the gradients' channel tensors)
+    // four elements at places divisible by four are aligned to their size, in the channel tensors / in B and C / in A
+    bool vec, vecBC, vecA, vec_out;    // (vec_out: the gradients' channel tensors)
     bool dt_f32, init_bf16, final_bf16, dfinal_bf16, dinit_bf16;
     const int32_t *cu;                 // packed sequences (batch 1) or NULL
     int nbatch, seqlen, channels, ngroups, dpg, N, NP, nseqs, nslots;     // dpg: channels per group; nseqs: batch or packed

@@ -23,10 +23,6 @@
 #ifndef GRAD_OCC
 #define GRAD_OCC 3
 #endif
-#ifndef GRAD_UN
-#define GRAD_UN 1
-#endif
-constexpr int GRAD_U = GRAD_UN;
 
 namespace ssd {
 
@@ -277,6 +273,7 @@ struct Grad {
     float2 red[2][GW][GC];             // shares of dD and ddt_bias, of this and the last channels
     T rx[2][SEL_Q * GC], ry[2][SEL_Q * GC], rz[2][SEL_Q * GC];   // the inputs as they come, of these and the next channels
     float rd[2][SEL_Q * GC];           // dt: fp32 or T
+    float rA[2][GC * NP], rh[2][GC * NP], ru[2][GC * NP];   // A, and the state and adjoint that enter the chunk
     // where channel c of a token lies: a thread writes four neighbours, eight threads neighbouring fours
     static __device__ __forceinline__ int place(int c) { return c ^ (c >> 3 & 3); }
 };
@@ -350,6 +347,14 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
         if (gated) fetch4(m.rz[k] + po, z + cb, nc, vec);
         if (a.dt_f32) fetch4(m.rd[k] + po, static_cast<const float *>(a.dt) + dt0 + cb, nc, vec);
         else fetch4(reinterpret_cast<T *>(m.rd[k]) + po, static_cast<const T *>(a.dt) + dt0 + cb, nc, vec);
+    };
+    auto fetch_own = [&](int cb, int k) {                           // this thread's four of A and of what enters the chunk
+        const int c = cb + tid * 4 / NP;
+        if (c < c_hi) {
+            fetch4(m.rA[k] + tid * 4, a.A + (int64_t)c * N + tid * 4 % NP, min(max(N - tid * 4 % NP, 0), 4), a.vecA);
+            fetch4(m.rh[k] + tid * 4, a.states + e0 + (int64_t)cb * NP, 4, true);
+            fetch4(m.ru[k] + tid * 4, a.adj + e0 + (int64_t)cb * NP, 4, true);
+        }
         cp_async_commit();
     };
     auto put_pD = [&](int cb, int k) {                              // the warps' shares of dD and ddt_bias
@@ -365,24 +370,21 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
     };
 
     if (pt < SEL_Q) fetch(c_lo, 0);
+    fetch_own(c_lo, 0);
     int k = 0;                                                      // the buffer of these channels' inputs
     for (int cb = c_lo; cb < c_hi; cb += GC, k ^= 1) {
         const int nc = pt < SEL_Q ? count(cb) : 0;
-        // this thread's share of A and of what enters the chunk
-        const bool mine = cb + tid * 4 / NP < c_hi;
-        float Aq[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int n = tid * 4 % NP + e;
-            Aq[e] = mine && n < N ? a.A[(int64_t)(cb + tid * 4 / NP) * N + n] * kLog2e : 0.f;
-        }
+        const bool mine = cb + tid * 4 / NP < c_hi;                 // this thread's four of A exist
+        cp_async_wait_all();                                        // (a thread uses what it fetched itself)
+        float Aq[4] = {0.f, 0.f, 0.f, 0.f};
         ulonglong2 hin = make_ulonglong2(0, 0), uin = hin;
         if (mine) {
-            hin = *reinterpret_cast<const ulonglong2 *>(a.states + e0 + (int64_t)cb * NP);
-            uin = *reinterpret_cast<const ulonglong2 *>(a.adj + e0 + (int64_t)cb * NP);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) Aq[e] = tid * 4 % NP + e < N ? m.rA[k][tid * 4 + e] * kLog2e : 0.f;
+            hin = *reinterpret_cast<const ulonglong2 *>(m.rh[k] + tid * 4);
+            uin = *reinterpret_cast<const ulonglong2 *>(m.ru[k] + tid * 4);
         }
         put4(m.As + tid * 4, Aq);
-        cp_async_wait_all();                                        // (a thread stages what it fetched itself)
         if (pt < SEL_Q) {
             float xv[4], yv[4], zv[4], r[4];
             Raw4<T> r1;
@@ -417,9 +419,12 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
         }
         __syncthreads();
         if (cb > c_lo) put_pD(cb - GC, k ^ 1);
-        if (cb + GC < c_hi && pt < SEL_Q) fetch(cb + GC, k ^ 1);
+        if (cb + GC < c_hi) {
+            if (pt < SEL_Q) fetch(cb + GC, k ^ 1);
+            fetch_own(cb + GC, k ^ 1);
+        }
         // from zero
-#pragma unroll GRAD_U
+#pragma unroll
         for (int it = 0; it < IT; ++it) {
             const int c = it * CPW + cw;
             const ulonglong2 av = *reinterpret_cast<const ulonglong2 *>(m.As + c * NP + q * 4);
