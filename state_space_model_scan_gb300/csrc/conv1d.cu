@@ -7,21 +7,19 @@
 //   out[t,c] = silu(pre[t,c])  (or pre)
 //
 // The scan then reads x, B and C as strided views of `out` (no copy: the split is the view).
-// A thread owns 8 consecutive channels and sweeps a tile of TT tokens with its inputs' last
-// K rows in registers (forward), and, for the backward, also the K input-gradient rows still
-// receiving contributions; the weight and bias gradients are per-tile partial sums added in a
+// A thread owns W consecutive channels and sweeps a run of tokens with its inputs' last K rows in
+// registers, and, for the backward, also the K input-gradient rows still receiving contributions; the weight and bias gradients are per-tile partial sums added in a
 // fixed order afterwards (bitwise reproducible).  Every access of a warp is one contiguous
 // 512-byte (bf16) or 1 KB (fp32) row piece.
 #include <algorithm>
 
-#include "common.cuh"
+#include "f32x2.cuh"
 
 namespace ssd {
 
 namespace {
 
-constexpr int TT = 64;        // tokens per thread
-constexpr int CT = 256;       // threads per block (8 channels each)
+constexpr int TT = 64;        // tokens of a block of the backward
 constexpr int KMAX = 8;
 
 __device__ __forceinline__ void ld8(const __nv_bfloat16 *p, float *v) {
@@ -102,22 +100,17 @@ struct SeqCursor {
     }
 };
 
-// ---- staged sweeps.  A block covers TT tokens x CB channels; its threads first copy the tile
-// (plus the K-1 rows before it, and for the backward after it) into shared memory with
-// cp.async -- a whole tile of loads in flight at once -- and then thread (piece j, token group
-// g) sweeps its W channels over TG = 8 tokens (forward: W = 8, 256 threads) or TGB = 16 tokens
-// (backward: W = 4, 256 threads, about 110 registers, two blocks per SM) from shared memory.
-// (Measured: a forward with W = 4 is a third slower; a backward with W = 8 or 2 a tenth.)
+// ---- backward: a staged sweep.  A block covers TT tokens x CB channels; its threads first copy the tile
+// (plus the K-1 rows before and after it) into shared memory with cp.async -- a whole tile of loads in
+// flight at once -- and then thread (piece j, token group g) sweeps its W channels over TGB = 16 tokens
+// (W = 4, 256 threads, about 110 registers, two blocks per SM) from shared memory.
+// (Measured: with W = 8 or 2 a tenth slower.)
 constexpr int CB = 256;              // channels per block (32 pieces of 8)
-constexpr int TG = TT / (CT / 32);   // tokens per thread: 8
 constexpr int CTB = 128;             // backward: threads per block (two blocks per SM) ...
 constexpr int TGB = TT / (CTB / 32); // ... and tokens per thread: 16
 #define TAPS_BYTES(K) ((size_t)((K) + 1) * CB * sizeof(float))   // staged taps and bias
 #ifndef CONV_BWD_W
 #define CONV_BWD_W 4
-#endif
-#ifndef CONV_FWD_W
-#define CONV_FWD_W 8
 #endif
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
@@ -152,8 +145,6 @@ __device__ __forceinline__ void stage_rows(const T *src, int64_t sl, int64_t tb,
     cp_async_commit_wait();
 }
 
-template <typename T>
-__device__ __forceinline__ void lds8(const T *p, float *v) { ld8(p, v); }
 // 4 channels: 8 bytes (bf16) or 16 bytes (fp32)
 __device__ __forceinline__ void ld4(const __nv_bfloat16 *p, float *v) {
     const uint2 u = *reinterpret_cast<const uint2 *>(p);
@@ -225,6 +216,72 @@ __device__ __forceinline__ void stage_taps(const float *w, const float *bias, in
         ws[K * CB + c] = (bias != nullptr && c < nch) ? bias[cbase + c] : 0.f;
 }
 
+// ---- forward.  A thread sweeps FT tokens of its W channels: it loads FB rows at a time straight from
+// global memory (all in flight before the first is used; only the K - 1 rows before its run are read a
+// second time), keeps the last K rows as fp32 pairs, and does the taps and the gate's products
+// two channels to an instruction.
+// (Measured at 8191 x 6144 bf16, width 4: W = 8 at best 48 us, four rows in flight 47, 32 tokens a run 50,
+// 512-thread blocks 67; these 46.  The staged tile that it replaced: 56.)
+constexpr int kFwdW = 4, FG = 2, FT = 16, FB = 8;   // channels a thread; runs in a block; tokens of a run; rows in flight
+
+// W neighbouring channels of one row, as they lie in memory
+template <typename T, int W>
+struct Row;
+template <int W>
+struct Row<float, W> {
+    float4 v[W / 4];
+    __device__ __forceinline__ void load(const float *p) {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) v[i] = reinterpret_cast<const float4 *>(p)[i];
+    }
+    __device__ __forceinline__ void pairs(f32x2 (&o)[W / 2]) const {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+            o[2 * i] = pk2(v[i].x, v[i].y);
+            o[2 * i + 1] = pk2(v[i].z, v[i].w);
+        }
+    }
+};
+template <int W>
+struct Row<__nv_bfloat16, W> {
+    uint32_t v[W / 2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        if constexpr (W == 8) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            v[0] = u.x; v[1] = u.y;
+        }
+    }
+    __device__ __forceinline__ void pairs(f32x2 (&o)[W / 2]) const {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) o[i] = pk2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u));
+    }
+};
+
+// v (v silu's logistic function), in the arithmetic of sig_t<T>
+template <typename T>
+__device__ __forceinline__ f32x2 silu2(f32x2 v) {
+    float lo, hi;
+    if (sizeof(T) == 2) {
+        const f32x2 half = pk2(0.5f, 0.5f);
+        up2(mul2(half, v), lo, hi);
+        asm("tanh.approx.f32 %0, %0;" : "+f"(lo));
+        asm("tanh.approx.f32 %0, %0;" : "+f"(hi));
+        return mul2(v, fma2(half, pk2(lo, hi), half));
+    }
+    up2(v, lo, hi);
+    return pk2(lo * sig_fast(lo), hi * sig_fast(hi));
+}
+template <typename T, int W>
+__device__ __forceinline__ void store_pairs(T *p, const f32x2 (&v)[W / 2]) {
+    float o[W];
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) up2(v[i], o[2 * i], o[2 * i + 1]);
+    stw<W>(p, o);
+}
+
 // The carried window of sequence s (its rows are K - 1 back to 1 before the first token), or NULL for padding.
 template <typename T>
 __device__ __forceinline__ T *window(const ConvArgs &a, int64_t s, int K) {
@@ -233,11 +290,34 @@ __device__ __forceinline__ T *window(const ConvArgs &a, int64_t s, int K) {
     return static_cast<T *>(a.win) + k * a.sw;
 }
 
+// pre[t] -> out: the taps over the rows that `at` gives for back = K - 1 .. 0 (NULL: a row of zeros)
+template <typename T, int K, int W, typename At>
+__device__ __forceinline__ void one_token(const f32x2 (&w)[K][W / 2], const f32x2 (&bias)[W / 2], bool silu, T *out, At at) {
+    f32x2 acc[W / 2];
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) acc[i] = bias[i];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const T *p = at(K - 1 - k);
+        if (p == nullptr) continue;
+        Row<T, W> r;
+        f32x2 v[W / 2];
+        r.load(p);
+        r.pairs(v);
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) acc[i] = fma2(w[k][i], v[i], acc[i]);
+    }
+    if (silu) {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) acc[i] = silu2<T>(acc[i]);
+    }
+    store_pairs<T, W>(out, acc);
+}
+
 // With carried windows, a sequence's first K - 1 outputs and its new window come from the same
-// thread, which reads the old window before it writes (other blocks never touch windows): thread
-// (piece j, group) takes 8 channels of one sequence.
-template <typename T, int K>
-__device__ void conv_edge(const ConvArgs &a, int64_t s, int64_t c0, const float *ws, int j) {
+// thread, which reads the old window before it writes (other blocks never touch windows).
+template <typename T, int K, int W>
+__device__ void conv_edge(const ConvArgs &a, int64_t s, int64_t c0, const f32x2 (&w)[K][W / 2], const f32x2 (&bias)[W / 2]) {
     const int64_t b = a.cu ? 0 : s;
     const int64_t t0 = a.cu ? min(max((int64_t)a.cu[s], (int64_t)0), a.L) : 0;
     const int64_t t1 = a.cu ? min(max((int64_t)a.cu[s + 1], t0), a.L) : a.L;
@@ -246,122 +326,114 @@ __device__ void conv_edge(const ConvArgs &a, int64_t s, int64_t c0, const float 
     const T *u = static_cast<const T *>(a.u) + b * a.su_b + c0;
     T *o = static_cast<T *>(a.out) + b * a.so_b + c0;
     const int n = (int)min(t1 - t0, (int64_t)(K - 1));
-    for (int i = 0; i < n; ++i) {
-        float acc[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = ws[K * CB + 8 * j + e];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int r = i + k - (K - 1);   // row of tap k from the first token; below 0: in the window
-            if (r < 0 && !old) continue;
-            float v[8];
-            ld8(r < 0 ? win + (K - 1 + r) * a.Cn + c0 : u + (t0 + r) * a.su_l, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(ws[k * CB + 8 * j + e], v[e], acc[e]);
-        }
-        if (a.silu) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] *= sig_t<T>(acc[e]);
-        }
-        st8(o + (t0 + i) * a.so_l, acc);
-    }
+#pragma unroll 1
+    for (int i = 0; i < n; ++i)
+        one_token<T, K, W>(w, bias, a.silu, o + (t0 + i) * a.so_l, [&](int back) -> const T * {
+            const int r = i - back;   // the row from the first token; below 0: in the window
+            return r >= 0 ? u + (t0 + r) * a.su_l : old ? win + (K - 1 + r) * a.Cn + c0 : nullptr;
+        });
     if (win == nullptr) return;
     for (int k = 0; k < K - 1; ++k) {   // new row k is K - 1 - k before the end: a token, or old row n + k >= k
         const int64_t t = t1 - (K - 1) + k;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (t >= t0) ld8(u + t * a.su_l, v);
-        else if (old) ld8(win + (n + k) * a.Cn + c0, v);
-        st8(win + k * a.Cn + c0, v);
+        float v[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] = 0.f;
+        if (t >= t0) ldw<W>(u + t * a.su_l, v);
+        else if (old) ldw<W>(win + (n + k) * a.Cn + c0, v);
+        stw<W>(win + k * a.Cn + c0, v);
     }
 }
 
-// CARRY: sequences go on from carried windows; blocks past the token tiles do their edges.
-template <typename T, int K, int W, bool CARRY>   // W channels per thread (8: 256 threads, 4: 512 threads)
-__global__ void __launch_bounds__(CT * 8 / W, 4)   // four blocks per SM (64 registers) measured 2-3% faster than three
-k_conv_fwd(const ConvArgs a) {
-    constexpr int NPC = CB / W;        // channel pieces per row
-    extern __shared__ __align__(16) uint8_t conv_sm[];
-    float *ws = reinterpret_cast<float *>(conv_sm);                  // taps [K][CB], bias [CB]
-    T *tile = reinterpret_cast<T *>(conv_sm + TAPS_BYTES(K));        // rows t0-(K-1) .. t0+TT-1
+// CARRY: sequences go on from carried windows; blocks past the token runs do their edges.
+template <typename T, int K, int W, bool CARRY>
+__global__ void __launch_bounds__(FG * CB / W, K > 4 ? 1 : sizeof(T) == 2 ? 6 : 4) k_conv_fwd(const ConvArgs a, int cols) {
+    constexpr int NPC = CB / W;        // channel pieces of a block
     const int j = threadIdx.x % NPC, grp = threadIdx.x / NPC;
-    const int64_t cbase = (int64_t)blockIdx.y * CB, c0 = cbase + W * j;
-    const int64_t b = blockIdx.x / a.tiles_per_row, t0 = (blockIdx.x % a.tiles_per_row) * TT;
-    const int64_t tb = t0 - (K - 1);
-    stage_taps<K>(a.w, a.bias, cbase, a.Cn, ws);
-    if (CARRY) {
-        static_assert(!CARRY || W == 8, "conv_edge takes 8 channels a thread");
-        const int64_t tiles = a.B * a.tiles_per_row;
-        if (blockIdx.x >= tiles) {
-            __syncthreads();
-            const int64_t s = (blockIdx.x - tiles) * (CT / 32) + grp, ns = a.cu ? a.S : a.B;
-            if (s < ns && c0 < a.Cn) conv_edge<T, K>(a, s, c0, ws, j);
-            return;
+    const int64_t bx = blockIdx.x / cols, c0 = (int64_t)(blockIdx.x % cols) * CB + W * j;   // neighbouring blocks: one row's channels
+    if (c0 >= a.Cn) return;
+    f32x2 w[K][W / 2], bias[W / 2];
+    {
+        float wv[W * K];                // the W channels' taps are contiguous
+        const float *wp = a.w + c0 * K;
+        if ((uintptr_t)a.w % 16 == 0) {
+#pragma unroll
+            for (int i = 0; i < W * K / 4; ++i) {
+                const float4 v = reinterpret_cast<const float4 *>(wp)[i];
+                wv[4 * i] = v.x; wv[4 * i + 1] = v.y; wv[4 * i + 2] = v.z; wv[4 * i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < W * K; ++i) wv[i] = wp[i];
+        }
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) w[k][i] = pk2(wv[2 * i * K + k], wv[(2 * i + 1) * K + k]);
+            bias[i] = a.bias ? pk2(a.bias[c0 + 2 * i], a.bias[c0 + 2 * i + 1]) : pk2(0.f, 0.f);
         }
     }
-    stage_rows(static_cast<const T *>(a.u) + b * a.su_b, a.su_l, tb, TT + K - 1, a.L, cbase, a.Cn, tile);
-    __syncthreads();
-    if (c0 >= a.Cn) return;
-    const int64_t s0 = t0 + (int64_t)grp * TG, s1 = std::min(a.L, s0 + TG);   // this thread's tokens
-    if (s0 >= s1) return;
-    T *o = static_cast<T *>(a.out) + b * a.so_b + c0;
-    float w[K][W], bias[W];
-#pragma unroll
-    for (int k = 0; k <= K; ++k) {   // the thread's W channels of tap k (k = K: the bias)
-        float *dst = k < K ? w[k < K ? k : 0] : bias;
-#pragma unroll
-        for (int e = 0; e < W; ++e) dst[e] = ws[k * CB + W * j + e];
+    const int64_t runs = (a.L + FT * FG - 1) / (FT * FG);       // blocks per row
+    if (CARRY && bx >= a.B * runs) {
+        const int64_t s = (bx - a.B * runs) * FG + grp, ns = a.cu ? a.S : a.B;
+        if (s < ns) conv_edge<T, K, W>(a, s, c0, w, bias);
+        return;
     }
+    const int64_t b = bx / runs, s0 = (bx % runs * FG + grp) * FT, s1 = std::min(a.L, s0 + FT);   // this thread's tokens
+    if (s0 >= s1) return;
+    const T *u = static_cast<const T *>(a.u) + b * a.su_b + c0;
+    T *o = static_cast<T *>(a.out) + b * a.so_b + c0;
     SeqCursor cur;
     cur.init(a, s0);
-    const T *col = tile + W * j;   // row t at (t - tb) * 256 (offsets below fit 32 bits)
-    if (s0 - (K - 1) >= cur.start && s1 <= cur.next) {
-        // The thread's tokens and the K-1 before them lie in one sequence: no sequence starts
-        // to test, a 32-bit counter, pointers that step a row.
-        const T *rp = col + (int)(s0 - t0) * 256;   // row t - (K-1) of the current t
-        T *op = o + s0 * a.so_l;
-        const int n = (int)(s1 - s0);
-        for (int i = 0; i < n; ++i) {
-            float acc[W];
-#pragma unroll
-            for (int e = 0; e < W; ++e) acc[e] = bias[e];
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float v[W];
-                ldw<W>(rp + k * 256, v);
-#pragma unroll
-                for (int e = 0; e < W; ++e) acc[e] = fmaf(w[k][e], v[e], acc[e]);
-            }
-            if (a.silu) {
-#pragma unroll
-                for (int e = 0; e < W; ++e) acc[e] *= sig_t<T>(acc[e]);
-            }
-            stw<W>(op, acc);
-            rp += 256;
-            op += a.so_l;
+    if (s0 - (K - 1) < cur.start || s1 > cur.next) {   // a sequence starts within the run, or less than K - 1 tokens before it
+#pragma unroll 1
+        for (int64_t t = s0; t < s1; ++t) {
+            cur.advance(a, t);
+            if (CARRY && t - (K - 1) < cur.start) continue;     // conv_edge's
+            one_token<T, K, W>(w, bias, a.silu, o + t * a.so_l,
+                               [&](int back) -> const T * { return t - back >= cur.start ? u + (t - back) * a.su_l : nullptr; });
         }
         return;
     }
-    for (int64_t t = s0; t < s1; ++t) {
-        cur.advance(a, t);
-        if (CARRY && t - (K - 1) < cur.start) continue;   // conv_edge's
-        float acc[W];
+    f32x2 rows[K - 1 + FB][W / 2];
+    const T *p = u + (s0 - (K - 1)) * a.su_l;
+    T *q = o + s0 * a.so_l;
 #pragma unroll
-        for (int e = 0; e < W; ++e) acc[e] = bias[e];
+    for (int k = 0; k < K - 1; ++k, p += a.su_l) {
+        Row<T, W> r;
+        r.load(p);
+        r.pairs(rows[k]);
+    }
+    const int n = (int)(s1 - s0);
+    Row<T, W> raw[FB];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int64_t tp = t - (K - 1) + k;   // u[tp] feeds pre[t] when in t's sequence
-            if (tp >= cur.start) {
-                float v[W];
-                ldw<W>(col + (int)(tp - tb) * 256, v);
+    for (int e = 0; e < FB; ++e, p += a.su_l)
+        if (e < n) raw[e].load(p);
+#pragma unroll 1
+    for (int i = 0; i < n; i += FB) {
 #pragma unroll
-                for (int e = 0; e < W; ++e) acc[e] = fmaf(w[k][e], v[e], acc[e]);
+        for (int e = 0; e < FB; ++e, p += a.su_l) {
+            raw[e].pairs(rows[K - 1 + e]);
+            if (i + FB + e < n) raw[e].load(p);                 // FB rows are on their way all the time
+            if (i + e < n) {
+                f32x2 acc[W / 2];
+#pragma unroll
+                for (int h = 0; h < W / 2; ++h) {
+                    acc[h] = bias[h];
+#pragma unroll
+                    for (int k = 0; k < K; ++k) acc[h] = fma2(w[k][h], rows[e + k][h], acc[h]);
+                }
+                if (a.silu) {
+#pragma unroll
+                    for (int h = 0; h < W / 2; ++h) acc[h] = silu2<T>(acc[h]);
+                }
+                store_pairs<T, W>(q, acc);
+                q += a.so_l;
             }
         }
-        if (a.silu) {
 #pragma unroll
-            for (int e = 0; e < W; ++e) acc[e] *= sig_t<T>(acc[e]);
-        }
-        stw<W>(o + t * a.so_l, acc);
+        for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+            for (int h = 0; h < W / 2; ++h) rows[k][h] = rows[FB + k][h];
     }
 }
 
@@ -649,21 +721,18 @@ __global__ void __launch_bounds__(128) k_conv_step(const ConvArgs a) {
 }
 
 template <typename T, int K>
-size_t fwd_smem() { return TAPS_BYTES(K) + (size_t)(TT + K - 1) * 256 * sizeof(T); }
-template <typename T, int K>
 size_t bwd_smem() {
     const size_t stage = (size_t)(2 * TT + 3 * (K - 1)) * 256 * sizeof(T);
     const size_t red = (size_t)(TT / TGB) * (K + 1) * 256 * sizeof(float);
     return TAPS_BYTES(K) + (stage > red ? stage : red);
 }
-constexpr int kFwdW = CONV_FWD_W;   // channels per thread of the forward sweep
 template <typename T, int K, bool CARRY>
-cudaError_t launch_fwd_k(const ConvArgs &a, dim3 grid, cudaStream_t st) {
-    static int attr[64] = {0};
-    const size_t sm = fwd_smem<T, K>();
-    cudaError_t e = ensure_smem_attr(k_conv_fwd<T, K, kFwdW, CARRY>, (int)sm, attr);
-    if (e != cudaSuccess) return e;
-    k_conv_fwd<T, K, kFwdW, CARRY><<<grid, CT * 8 / kFwdW, sm, st>>>(a);
+cudaError_t launch_fwd_k(const ConvArgs &a, cudaStream_t st) {
+    const int64_t ns = a.cu ? a.S : a.B;
+    const int64_t blocks = a.B * ((a.L + FT * FG - 1) / (FT * FG)) + (CARRY ? (ns + FG - 1) / FG : 0);
+    const int64_t cols = (a.Cn + CB - 1) / CB;
+    if (blocks * cols > ((int64_t)1 << 31) - 1) return cudaErrorInvalidConfiguration;
+    k_conv_fwd<T, K, kFwdW, CARRY><<<(unsigned)(blocks * cols), FG * CB / kFwdW, 0, st>>>(a, (int)cols);
     return cudaGetLastError();
 }
 constexpr int kBwdW = CONV_BWD_W;   // channels per thread of the backward sweep
@@ -678,16 +747,16 @@ cudaError_t launch_bwd_k(const ConvArgs &a, dim3 grid, cudaStream_t st) {
 }
 
 template <typename T, bool CARRY>
-cudaError_t launch_fwd(const ConvArgs &a, dim3 grid, cudaStream_t st) {
+cudaError_t launch_fwd(const ConvArgs &a, cudaStream_t st) {
     switch (a.K) {
-        case 1: return launch_fwd_k<T, 1, CARRY>(a, grid, st);
-        case 2: return launch_fwd_k<T, 2, CARRY>(a, grid, st);
-        case 3: return launch_fwd_k<T, 3, CARRY>(a, grid, st);
-        case 4: return launch_fwd_k<T, 4, CARRY>(a, grid, st);
-        case 5: return launch_fwd_k<T, 5, CARRY>(a, grid, st);
-        case 6: return launch_fwd_k<T, 6, CARRY>(a, grid, st);
-        case 7: return launch_fwd_k<T, 7, CARRY>(a, grid, st);
-        default: return launch_fwd_k<T, 8, CARRY>(a, grid, st);
+        case 1: return launch_fwd_k<T, 1, CARRY>(a, st);
+        case 2: return launch_fwd_k<T, 2, CARRY>(a, st);
+        case 3: return launch_fwd_k<T, 3, CARRY>(a, st);
+        case 4: return launch_fwd_k<T, 4, CARRY>(a, st);
+        case 5: return launch_fwd_k<T, 5, CARRY>(a, st);
+        case 6: return launch_fwd_k<T, 6, CARRY>(a, st);
+        case 7: return launch_fwd_k<T, 7, CARRY>(a, st);
+        default: return launch_fwd_k<T, 8, CARRY>(a, st);
     }
 }
 template <typename T>
@@ -784,9 +853,8 @@ ssd_status ssd_conv1d_fwd(const ssd_conv_problem *p, const void *x, int64_t x_sb
     if (p->seqlen == 0) return SSD_OK;
     ConvArgs a = make_args(p, weight, bias, cu_seqlens);
     a.u = x; a.su_b = x_sb; a.su_l = x_sl; a.out = out; a.so_b = out_sb; a.so_l = out_sl;
-    const dim3 grid((unsigned)(a.B * a.tiles_per_row), (unsigned)((a.Cn + CB - 1) / CB));
     cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = p->dtype == SSD_BF16 ? launch_fwd<__nv_bfloat16, false>(a, grid, st) : launch_fwd<float, false>(a, grid, st);
+    const cudaError_t e = p->dtype == SSD_BF16 ? launch_fwd<__nv_bfloat16, false>(a, st) : launch_fwd<float, false>(a, st);
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
@@ -802,11 +870,8 @@ ssd_status ssd_conv1d_prompt(const ssd_conv_problem *p, const void *x, int64_t x
     ConvArgs a = make_args(p, weight, bias, cu_seqlens);
     a.u = x; a.su_b = x_sb; a.su_l = x_sl; a.out = out; a.so_b = out_sb; a.so_l = out_sl;
     a.win = conv_states; a.nslots = nslots; a.sw = slot_stride; a.slot = state_indices; a.has = has_initial;
-    const int64_t ns = cu_seqlens ? a.S : a.B, blocks = a.B * a.tiles_per_row + (ns + CT / 32 - 1) / (CT / 32);
-    if (blocks > ((int64_t)1 << 31) - 1) return SSD_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)blocks, (unsigned)((a.Cn + CB - 1) / CB));
     cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = p->dtype == SSD_BF16 ? launch_fwd<__nv_bfloat16, true>(a, grid, st) : launch_fwd<float, true>(a, grid, st);
+    const cudaError_t e = p->dtype == SSD_BF16 ? launch_fwd<__nv_bfloat16, true>(a, st) : launch_fwd<float, true>(a, st);
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 

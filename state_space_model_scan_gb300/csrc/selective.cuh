@@ -2,7 +2,7 @@
 // softplus, the chunk grid of its kept states, and the arguments of a call.
 #pragma once
 
-#include "common.cuh"
+#include "f32x2.cuh"
 
 namespace ssd {
 
@@ -57,34 +57,6 @@ __device__ __forceinline__ SelSeq sel_seq(const SelArgs &a, int s) {
     return q;
 }
 
-// ---- two fp32 lanes in a 64-bit register: one issue slot for two multiply-adds
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pk2(float lo, float hi) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void up2(f32x2 v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ float sum2(f32x2 v) {
-    float lo, hi;
-    up2(v, lo, hi);
-    return lo + hi;
-}
 // 2^v on the multi-function unit (relative error about 2^-22; results below 2^-126 flush to zero,
 // which a decay of that size is)
 __device__ __forceinline__ float ex2f(float v) {
