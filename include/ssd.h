@@ -519,11 +519,12 @@ ssd_status ssd_conv1d_step(const ssd_conv_problem *prob, const void *u, int64_t 
  * requests share, a request that is preempted).  A state is `rows` rows of `dstate` values; a row
  * is kept as int8 values and one f32 scale:
  *
- *   m = max_n |h[n]|,  q[n] = round_half_even(h[n] * (127 / m)),  scale = m / 127      (store)
+ *   m = max_n |h[n]|,  q[n] = round_half_even(h[n] * ((1 / m) * 127)),  scale = m / 127      (store)
  *   h[n] = q[n] * scale                                                                (load)
  *
- * so a value is off by half a scale at most.  A row with m < 1e-30 is kept as zeros with scale 0;
- * one that holds an infinity or a NaN is kept as zeros with scale NaN, and reads back as NaN.
+ * each operation rounded to f32, so a value is off by half a scale at most (to f32's rounding).
+ * A row with m < 1e-30 is kept as zeros with scale 0; one that holds an infinity or a NaN is
+ * kept as zeros with scale NaN, and reads back as NaN.
  * states [nslots][rows][dstate] f32 or bf16 at slot stride state_stride (rows contiguous);
  * snapshots int8 [nsnapshots][rows][dstate] and scales f32 [nsnapshots][rows], contiguous.
  * State state_indices[i] (NULL: i) goes to, or comes from, snapshot slots[i] (NULL: i); a pair

@@ -123,12 +123,12 @@ def conv(u, w, bias, window, silu=True):
 
 
 def snapshot(h):
-    """(q, scale) of rows [..., N] in the arithmetic the definition names: fp32 quotients, then products."""
+    """(q, scale) of rows [..., N] in the arithmetic the definition names, each operation rounded to fp32."""
     h = np.asarray(h, np.float32)
     with np.errstate(all="ignore"):
         m = np.abs(h).max(-1)
         ok = (m >= np.float32(1e-30)) & np.isfinite(m)
-        inv = np.where(ok, np.float32(127) / m, np.float32(0)).astype(np.float32)
+        inv = np.where(ok, (np.float32(1) / m) * np.float32(127), np.float32(0)).astype(np.float32)
         scale = np.where(ok, m / np.float32(127), np.where(np.isfinite(m), np.float32(0), np.float32("nan")))
         q = np.where(ok[..., None], np.rint(h * inv[..., None]), 0).astype(np.int8)
     return q, scale.astype(np.float32)

@@ -1,5 +1,5 @@
 // snapshot.cu -- states put aside in 8 bits and taken up again.  A row of dstate values h is kept as
-// q = round_half_even(h 127 / m) and the scale m / 127, m = max |h|.  Bytes bound it: 4 or 2 read
+// q = round_half_even(h ((1 / m) 127)) and the scale m / 127, m = max |h|, each step rounded to fp32.  Bytes bound it: 4 or 2 read
 // and 1 written per value, or the other way round.
 //
 // A row belongs to LPR lanes, each with NV pieces of four values, so that one exchange of the maximum
@@ -40,11 +40,11 @@ __device__ __forceinline__ void row_scale(float m, float &inv, float &scale) {
     } else if (m < kTiny) {
         inv = scale = 0.f;
     } else {
-        inv = __fdiv_rn(127.f, m);
+        inv = __fmul_rn(__frcp_rn(m), 127.f);
         scale = __fdiv_rn(m, 127.f);
     }
 }
-// round_half_even(h inv) in the last byte; |h inv| <= 127 (1 + 2^-23)
+// round_half_even(h inv) in the last byte; |h inv| <= 127 (1 + 2^-22)
 __device__ __forceinline__ uint32_t quant(float h, float inv) {
     return __float_as_uint(__fadd_rn(__fmul_rn(h, inv), 12582912.f));
 }
