@@ -32,6 +32,9 @@ struct Cfg {
     static constexpr int RX = 128 / CPW, PX = (TK + RX - 1) / RX, RB = NP < 128 ? 128 / NP : 1, PB = (TK + RB - 1) / RB;
     static_assert(TPC >= 2 && TK % U == 0 && (TW == 1 ? TK % SEL_Q == 0 : SEL_Q % TK == 0) && TT % SEL_Q == 0 && S % 4 == 0, "tile shape");
     static_assert(TW == 1 || CB * NP / 4 <= NT, "the joining takes a thread for four states");
+    // where the n-th four of channel c's states lies: a warp's threads write one of two neighbouring channels at a
+    // time, and every other pair has them swapped, so that eight threads meet eight different bank groups
+    static __device__ __forceinline__ int at(int c, int n) { return (c ^ (c >> 1 & 1)) * (NP / 4) + n; }
     // bytes a warp keeps: (dt, dt x), B, C, and the next tile as it comes
     static constexpr size_t wsmem(size_t ts, size_t ds) {
         return ((size_t)TK * CPW * 8 + (size_t)TK * NP * 8 + (size_t)TK * CPW * (ts + ds) + (size_t)TK * NP * 2 * ts);
@@ -56,7 +59,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
     float *rD = Cs + TK * NP;                                       // the next tile as it came: dt [TK][CPW], fp32 or T
     T *rX = reinterpret_cast<T *>(rD + TK * CPW / (a.dt_f32 ? 1 : 4 / (int)sizeof(T)));   // x [TK][CPW]
     T *rB = rX + TK * CPW, *rC = rB + TK * NP;                      // B, C [TK][NP]
-    float *E = reinterpret_cast<float *>(sel_sm + F::CW * TW * wbytes);   // [TW][NP / 4][CB][4]: end states, then entering states
+    float *E = reinterpret_cast<float *>(sel_sm + F::CW * TW * wbytes);   // [TW][CB][NP / 4] fours of end states, then entering states, placed by at()
     float *Sd = E + TW * CB * NP;                                   // [TW][CB]: sums of dt
     const int q = lane % TPC, cp0 = 2 * (lane / TPC), cl = cw * CPW + cp0;   // this thread's states [q S, q S + S) of channels cl, cl + 1
     const int cb = blockIdx.x % cblocks, s = blockIdx.x / cblocks;
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
             h[c][i] = pk2(hv[0], hv[1]);
         }
     // the joining over the warps: a thread takes four states of one channel, and carries them on
-    const int jc = tid % CB, jn = 4 * (tid / CB);
+    const int jc = tid / (NP / 4), jn = 4 * (tid % (NP / 4));
     const bool joins = TW > 1 && tid < CB * NP / 4;
     f32x2 jA[2] = {0, 0}, jh[2] = {0, 0};
     if (joins) {
@@ -171,9 +174,9 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
                         }
                     }
                 }
-                float4 *o = dd + (tl * CPW + pc) / 2;
-                o[0] = make_float4(v[0], v[1], v[2], v[3]);
-                o[1] = make_float4(v[4], v[5], v[6], v[7]);
+                float4 *o = dd + tl * (CPW / 2);                    // (odd tokens have neighbouring pairs swapped, off the banks)
+                o[pc / 2 ^ (tl & 1)] = make_float4(v[0], v[1], v[2], v[3]);
+                o[pc / 2 + 1 ^ (tl & 1)] = make_float4(v[4], v[5], v[6], v[7]);
             }
 #pragma unroll 4
             for (int k = 0; k < F::PB; ++k) {
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
         }
         __syncwarp();
         if (t0 + TT < len) fetch(t0 + TT);
-        const float4 *dp = dd + cp0 / 2;
+        const float4 *dp[2] = {dd + cp0 / 2, dd + (cp0 / 2 ^ 1)};   // even and odd tokens
         const float *bp = Bs + q * S, *cp = Cs + q * S;
         Raw4<T> rx[F::PX], rz[F::PX];                               // for the epilogue
         auto early = [&]() {
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
             if (live) {
 #pragma unroll 4
                 for (int t = 0; t < TK; ++t) {
-                    const float4 v = dp[t * (CPW / 2)];
+                    const float4 v = dp[t & 1][t * (CPW / 2)];
                     sum0 += v.x;
                     sum1 += v.z;
                     const f32x2 dt0 = pk2(v.x, v.x), dx0 = pk2(v.y, v.y), dt1 = pk2(v.z, v.z), dx1 = pk2(v.w, v.w);
@@ -236,11 +239,11 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
                     }
                 }
             }
-            ulonglong2 *ep = reinterpret_cast<ulonglong2 *>(E) + (w * (NP / 4) + q * (S / 4)) * CB + cl;
+            ulonglong2 *ep = reinterpret_cast<ulonglong2 *>(E) + w * CB * (NP / 4);
 #pragma unroll
             for (int i = 0; i < S / 4; ++i) {
-                ep[i * CB] = make_ulonglong2(e[0][2 * i], e[0][2 * i + 1]);
-                ep[i * CB + 1] = make_ulonglong2(e[1][2 * i], e[1][2 * i + 1]);
+                ep[F::at(cl, q * (S / 4) + i)] = make_ulonglong2(e[0][2 * i], e[0][2 * i + 1]);
+                ep[F::at(cl + 1, q * (S / 4) + i)] = make_ulonglong2(e[1][2 * i], e[1][2 * i + 1]);
             }
             if (q == 0) *reinterpret_cast<float2 *>(Sd + w * CB + cl) = make_float2(sum0, sum1);
             early();
@@ -250,7 +253,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
                 float sd[TW];
 #pragma unroll
                 for (int k = 0; k < TW; ++k) {
-                    end[k] = *(reinterpret_cast<const ulonglong2 *>(E) + (k * (NP / 4) + jn / 4) * CB + jc);
+                    end[k] = *(reinterpret_cast<const ulonglong2 *>(E) + k * CB * (NP / 4) + F::at(jc, jn / 4));
                     sd[k] = Sd[k * CB + jc];
                 }
 #pragma unroll
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
                                 make_ulonglong2(jh[0], jh[1]);
                     }
                     const f32x2 sd2 = pk2(sd[k], sd[k]);
-                    *(reinterpret_cast<ulonglong2 *>(E) + (k * (NP / 4) + jn / 4) * CB + jc) = make_ulonglong2(jh[0], jh[1]);
+                    *(reinterpret_cast<ulonglong2 *>(E) + k * CB * (NP / 4) + F::at(jc, jn / 4)) = make_ulonglong2(jh[0], jh[1]);
                     jh[0] = fma2(ex2x2(mul2(sd2, jA[0])), jh[0], end[k].x);
                     jh[1] = fma2(ex2x2(mul2(sd2, jA[1])), jh[1], end[k].y);
                 }
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
             for (int i = 0; i < S / 4; ++i)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const ulonglong2 v = ep[i * CB + c];
+                    const ulonglong2 v = ep[F::at(cl + c, q * (S / 4) + i)];
                     h[c][2 * i] = v.x;
                     h[c][2 * i + 1] = v.y;
                 }
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
             // The sums stay in registers over SB batches of tokens: a store after each would hold up the
             // next tokens' loads (the compiler cannot tell that they differ), and with them everything.
             constexpr int SB = SEL_Q / U < 4 ? SEL_Q / U : 4;
-            static_assert(SEL_Q % (SB * U) == 0 && TK % (SB * U) == 0, "chunks start at batches");
+            static_assert(SEL_Q % (SB * U) == 0 && TK % (SB * U) == 0 && SB * U % 2 == 0, "chunks start at batches, batches at even tokens");
 #pragma unroll 1
             for (int t0s = 0; t0s < TK; t0s += SB * U) {
                 if (TW == 1 && a.states && t0s % SEL_Q == 0 && tw + t0s < len) {
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
                     float yv[TPC];                                  // [token][channel]
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        const float4 v = dp[(t + u) * (CPW / 2)];
+                        const float4 v = dp[(sb * U + u) & 1][(t + u) * (CPW / 2)];
                         const f32x2 dt0 = pk2(v.x, v.x), dx0 = pk2(v.y, v.y), dt1 = pk2(v.z, v.z), dx1 = pk2(v.w, v.w);
                         const ulonglong2 *b = reinterpret_cast<const ulonglong2 *>(bp + (t + u) * NP);
                         const ulonglong2 *c = reinterpret_cast<const ulonglong2 *>(cp + (t + u) * NP);
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
                 }
 #pragma unroll
                 for (int sb = 0; sb < SB; ++sb)
-                    reinterpret_cast<float *>(dd)[((t0s + sb * U + q / 2) * CPW + cp0 + q % 2) * 2 + 1] = yq[sb];
+                    reinterpret_cast<float *>(dd + (t0s + sb * U + q / 2) * (CPW / 2) + (cp0 / 2 ^ ((sb * U + q / 2) & 1)))[q % 2 * 2 + 1] = yq[sb];
             }
         }
         if (y == nullptr) continue;
@@ -337,7 +340,8 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
         for (int k = 0; k < F::PX; ++k) {
             const int tl = pt + k * F::RX, t = tw + tl;
             if ((F::RX * F::PX == TK || tl < TK) && t < len) {
-                const float4 v0 = dd[(tl * CPW + pc) / 2], v1 = dd[(tl * CPW + pc) / 2 + 1];
+                const float4 *o4 = dd + tl * (CPW / 2);
+                const float4 v0 = o4[pc / 2 ^ (tl & 1)], v1 = o4[pc / 2 + 1 ^ (tl & 1)];
                 float o[4] = {v0.y, v0.w, v1.y, v1.w}, f[4];
                 if (a.D) {
                     rx[k].f(f);
