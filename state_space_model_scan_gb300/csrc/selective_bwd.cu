@@ -40,6 +40,8 @@ struct RevCfg {
     static constexpr int NP = S * TPC, CPW = 64 / TPC, CB = CW * CPW, TT = TW * TK, NT = 32 * CW * TW;
     static constexpr int RX = 128 / CPW, PX = (TK + RX - 1) / RX, RB = NP < 128 ? 128 / NP : 1, PB = (TK + RB - 1) / RB;
     static_assert(SEL_Q % TK == 0 && TT % SEL_Q == 0 && S % 4 == 0 && CB * NP / 4 <= NT, "tile shape");
+    // where the n-th four of channel c's states lies (as in the forward, off the banks)
+    static __device__ __forceinline__ int at(int c, int n) { return (c ^ (c >> 1 & 1)) * (NP / 4) + n; }
     // bytes a warp keeps: (dt, dyp), C, and the next tile's dt, dy, z and C as they come
     static constexpr size_t wsmem(size_t ts, size_t ds) {
         return (size_t)TK * CPW * 8 + (size_t)TK * NP * 4 + (size_t)TK * CPW * (2 * ts + ds) + (size_t)TK * NP * ts;
@@ -62,7 +64,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
     float *rD = Cs + TK * NP;                                        // dt [TK][CPW], fp32 or T
     T *rY = reinterpret_cast<T *>(rD + TK * CPW / (a.dt_f32 ? 1 : 4 / (int)sizeof(T)));   // dy, z [TK][CPW]
     T *rZ = rY + TK * CPW, *rC = rZ + TK * CPW;                      // C [TK][NP]
-    float *E = reinterpret_cast<float *>(sel_sm + F::CW * TW * wbytes);   // two of [TW][NP / 4][CB][4]: what each warp passes on
+    float *E = reinterpret_cast<float *>(sel_sm + F::CW * TW * wbytes);   // two of [TW][CB][NP / 4] fours, placed by at(): what each warp passes on
     float *Sd = E + 2 * TW * CB * NP;                                // two of [TW][CB]: sums of dt
     const int q = lane % TPC, cp0 = 2 * (lane / TPC), cl = cw * CPW + cp0;
     const int cb = blockIdx.x % cblocks, s = blockIdx.x / cblocks;
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
             }
             A2[c][i] = pk2(v[0], v[1]);
         }
-    const int jc = tid % CB, jn = 4 * (tid / CB);
+    const int jc = tid / (NP / 4), jn = 4 * (tid % (NP / 4));
     const bool joins = tid < CB * NP / 4;
     f32x2 jA[2] = {0, 0}, ju[2] = {0, 0};
     if (joins) {
@@ -171,9 +173,9 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
                             v[2 * i + 1] = gated ? yv[i] * zv[i] * sigf(zv[i]) : yv[i];
                         }
                 }
-                float4 *o = dd + (tl * CPW + pc) / 2;
-                o[0] = make_float4(v[0], v[1], v[2], v[3]);
-                o[1] = make_float4(v[4], v[5], v[6], v[7]);
+                float4 *o = dd + tl * (CPW / 2);                    // (odd tokens have neighbouring pairs swapped, off the banks)
+                o[pc / 2 ^ (tl & 1)] = make_float4(v[0], v[1], v[2], v[3]);
+                o[pc / 2 + 1 ^ (tl & 1)] = make_float4(v[4], v[5], v[6], v[7]);
             }
 #pragma unroll 4
             for (int k = 0; k < F::PB; ++k) {
@@ -194,11 +196,11 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
         __syncwarp();
         if (t0 > 0) fetch(t0 - TT);
         if (tw < len) {
-            const float4 *dp = dd + cp0 / 2;
+            const float4 *dp[2] = {dd + cp0 / 2, dd + (cp0 / 2 ^ 1)};   // even and odd tokens
             const float *cp = Cs + q * S;
 #pragma unroll 4
             for (int t = TK - 1; t >= 0; --t) {
-                const float4 v = dp[t * (CPW / 2)];
+                const float4 v = dp[t & 1][t * (CPW / 2)];
                 sum0 += v.x;
                 sum1 += v.z;
                 const f32x2 dt0 = pk2(v.x, v.x), y0 = pk2(v.y, v.y), dt1 = pk2(v.z, v.z), y1 = pk2(v.w, v.w);
@@ -213,11 +215,11 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
                 }
             }
         }
-        ulonglong2 *ep = reinterpret_cast<ulonglong2 *>(E) + ((buf * TW + w) * (NP / 4) + q * (S / 4)) * CB + cl;
+        ulonglong2 *ep = reinterpret_cast<ulonglong2 *>(E) + (buf * TW + w) * CB * (NP / 4);
 #pragma unroll
         for (int i = 0; i < S / 4; ++i) {
-            ep[i * CB] = make_ulonglong2(u[0][2 * i], u[0][2 * i + 1]);
-            ep[i * CB + 1] = make_ulonglong2(u[1][2 * i], u[1][2 * i + 1]);
+            ep[F::at(cl, q * (S / 4) + i)] = make_ulonglong2(u[0][2 * i], u[0][2 * i + 1]);
+            ep[F::at(cl + 1, q * (S / 4) + i)] = make_ulonglong2(u[1][2 * i], u[1][2 * i + 1]);
         }
         if (q == 0) *reinterpret_cast<float2 *>(Sd + (buf * TW + w) * CB + cl) = make_float2(sum0, sum1);
         __syncthreads();   // (the other buffer's joining is over: its threads are here)
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
             float sd[TW];
 #pragma unroll
             for (int k = 0; k < TW; ++k) {
-                fold[k] = *(reinterpret_cast<const ulonglong2 *>(E) + ((buf * TW + k) * (NP / 4) + jn / 4) * CB + jc);
+                fold[k] = *(reinterpret_cast<const ulonglong2 *>(E) + (buf * TW + k) * CB * (NP / 4) + F::at(jc, jn / 4));
                 sd[k] = Sd[(buf * TW + k) * CB + jc];
             }
 #pragma unroll
