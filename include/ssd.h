@@ -445,7 +445,7 @@ ssd_status ssd_complex_fwd(const ssd_complex_problem *prob, const void *x, const
  * chunk_states (optional): a device buffer of ssd_selective_chunk_states_size bytes, 16-byte
  * aligned, into which the forward writes the state entering every 16th token of each sequence
  * (f32, dstate padded to 16, 32, 64 or 128); the backward, given the same buffer, starts from
- * them instead of running the forward again.  The forward needs no workspace.  Gradient
+ * them instead of running the forward again.  Gradient
  * reductions run in a fixed order (bitwise reproducible); D, z, dt_bias and initial_states may
  * be absent, and then so is their gradient.
  */
@@ -454,9 +454,12 @@ typedef struct {
 } ssd_selective_problem;
 
 ssd_status ssd_selective_chunk_states_size(const ssd_selective_problem *prob, size_t *bytes);
-ssd_status ssd_selective_fwd(const ssd_selective_problem *prob, const ssd_fwd_args *args, void *stream);
 /* Workspace: at least *bytes bytes of device memory, 256-byte aligned; contents need not be
- * initialised.  Its size depends on whether args->fwd.chunk_states is given. */
+ * initialised.  The forward's is 0 (workspace may be NULL) unless a long sequence has few channels;
+ * the backward's depends on whether args->fwd.chunk_states is given. */
+ssd_status ssd_selective_fwd_workspace_size(const ssd_selective_problem *prob, size_t *bytes);
+ssd_status ssd_selective_fwd(const ssd_selective_problem *prob, const ssd_fwd_args *args, void *workspace,
+                             size_t workspace_bytes, void *stream);
 ssd_status ssd_selective_bwd_workspace_size(const ssd_selective_problem *prob, const ssd_bwd_args *args, size_t *bytes);
 ssd_status ssd_selective_bwd(const ssd_selective_problem *prob, const ssd_bwd_args *args, void *workspace,
                              size_t workspace_bytes, void *stream);

@@ -26,8 +26,8 @@ EXPORTS = ["ssd_fwd_workspace_size", "ssd_fwd", "ssd_bwd_workspace_size", "ssd_b
            "ssd_gated_norm_fwd", "ssd_gated_norm_bwd_workspace_size", "ssd_gated_norm_bwd",
            "ssd_conv1d_fwd", "ssd_conv1d_bwd_workspace_size", "ssd_conv1d_bwd",
            "ssd_complex_fwd_workspace_size", "ssd_complex_fwd",
-           "ssd_selective_chunk_states_size", "ssd_selective_fwd", "ssd_selective_bwd_workspace_size",
-           "ssd_selective_bwd", "ssd_step", "ssd_selective_step", "ssd_conv1d_prompt", "ssd_conv1d_step",
+           "ssd_selective_chunk_states_size", "ssd_selective_fwd_workspace_size", "ssd_selective_fwd",
+           "ssd_selective_bwd_workspace_size", "ssd_selective_bwd", "ssd_step", "ssd_selective_step", "ssd_conv1d_prompt", "ssd_conv1d_step",
            "ssd_snapshot_store", "ssd_snapshot_load"]
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -143,7 +143,8 @@ def load(path: str = LIB_PATH):
     lib.ssd_complex_fwd.argtypes = [P(ComplexProblem), V, V, V, V, V, V, V, V, V, V, ctypes.c_size_t, V]
     S = ctypes.c_size_t
     lib.ssd_selective_chunk_states_size.argtypes = [P(SelectiveProblem), P(S)]
-    lib.ssd_selective_fwd.argtypes = [P(SelectiveProblem), P(FwdArgs), V]
+    lib.ssd_selective_fwd_workspace_size.argtypes = [P(SelectiveProblem), P(S)]
+    lib.ssd_selective_fwd.argtypes = [P(SelectiveProblem), P(FwdArgs), V, S, V]
     lib.ssd_selective_bwd_workspace_size.argtypes = [P(SelectiveProblem), P(BwdArgs), P(S)]
     lib.ssd_selective_bwd.argtypes = [P(SelectiveProblem), P(BwdArgs), V, S, V]
     lib.ssd_step.argtypes = lib.ssd_selective_step.argtypes = [P(StepProblem)] + [V] * 12
@@ -155,7 +156,7 @@ def load(path: str = LIB_PATH):
               "ssd_noalloc_query_status", "ssd_varlen_metadata", "ssd_gated_norm_fwd",
               "ssd_gated_norm_bwd_workspace_size", "ssd_gated_norm_bwd", "ssd_conv1d_fwd",
               "ssd_conv1d_bwd_workspace_size", "ssd_conv1d_bwd", "ssd_complex_fwd_workspace_size",
-              "ssd_complex_fwd", "ssd_selective_chunk_states_size", "ssd_selective_fwd",
+              "ssd_complex_fwd", "ssd_selective_chunk_states_size", "ssd_selective_fwd_workspace_size", "ssd_selective_fwd",
               "ssd_selective_bwd_workspace_size", "ssd_selective_bwd", "ssd_step", "ssd_selective_step",
               "ssd_conv1d_prompt", "ssd_conv1d_step", "ssd_snapshot_store", "ssd_snapshot_load"):
         getattr(lib, f).restype = ctypes.c_int
@@ -400,7 +401,7 @@ def selective_chunk_states_size(prob):
 
 # ---- the compiled binding (csrc/binding.cpp) of the entry points that are called for single tokens
 _BINDING_ORDER = ["ssd_step", "ssd_selective_step", "ssd_conv1d_prompt", "ssd_conv1d_step", "ssd_snapshot_store",
-                  "ssd_snapshot_load", "ssd_selective_chunk_states_size", "ssd_selective_fwd",
+                  "ssd_snapshot_load", "ssd_selective_chunk_states_size", "ssd_selective_fwd_workspace_size", "ssd_selective_fwd",
                   "ssd_selective_bwd_workspace_size", "ssd_selective_bwd"]
 _fast = None
 

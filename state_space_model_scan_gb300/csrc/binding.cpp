@@ -28,6 +28,7 @@ struct Lib {
     decltype(&ssd_snapshot_store) snapshot_store;
     decltype(&ssd_snapshot_load) snapshot_load;
     decltype(&ssd_selective_chunk_states_size) chunk_states_size;
+    decltype(&ssd_selective_fwd_workspace_size) fwd_workspace_size;
     decltype(&ssd_selective_fwd) selective_fwd;
     decltype(&ssd_selective_bwd_workspace_size) bwd_workspace_size;
     decltype(&ssd_selective_bwd) selective_bwd;
@@ -333,7 +334,11 @@ PyObject *selective_fwd(PyObject *const *a) {
         kept = st.empty({(int64_t)n}, x.options().dtype(at::kByte));
         s.f.chunk_states = kept.data_ptr();
     }
-    check(lib.selective_fwd(&s.p, &s.f, st.handle), "ssd_selective_fwd");
+    size_t n = 0;
+    check(lib.fwd_workspace_size(&s.p, &n), "ssd_selective_fwd_workspace_size");
+    Tensor ws;
+    if (n > 0) ws = st.empty({(int64_t)n}, x.options().dtype(at::kByte));
+    check(lib.selective_fwd(&s.p, &s.f, ptr(ws), n, st.handle), "ssd_selective_fwd");
     PyObject *r = PyTuple_New(keep ? 3 : 2);
     if (!r) throw Raised();
     PyTuple_SET_ITEM(r, 0, wrap(y));

@@ -25,8 +25,9 @@ ssd_status check_problem(const ssd_selective_problem *p, bool varlen) {
     // counters of tokens, chunks and blocks are 32-bit; element offsets are 64-bit
     const int64_t ns = varlen ? p->nseqs : p->batch;
     if (p->seqlen > ((int64_t)1 << 30) || p->channels > ((int64_t)1 << 22) || ns > ((int64_t)1 << 24) ||
-        ns * ((p->channels + 7) / 8 + p->ngroups) > ((int64_t)1 << 30) ||
-        (p->seqlen / SEL_Q + 1) * ns > ((int64_t)1 << 30))
+        ns * ((p->channels + 3) / 4 + p->ngroups) > ((int64_t)1 << 30) ||
+        (p->seqlen / SEL_Q + 1) * ns > ((int64_t)1 << 30) ||
+        p->batch * p->seqlen * p->ngroups > ((int64_t)1 << 31))
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
@@ -108,6 +109,7 @@ SelArgs make_args(const ssd_selective_problem *p, const ssd_fwd_args *f) {
     a.nseqs = (int)(p->nseqs ? p->nseqs : p->batch);
     a.nslots = (int)chunk_slots(p);
     a.states = static_cast<float *>(f->chunk_states);
+    sel_segments(a.nseqs, p->channels, p->ngroups, p->seqlen, a.NP, &a.nseg, &a.seglen);
     a.vec = (p->ngroups == 1 || a.dpg % 4 == 0) && fours(f->x, 2) && fours(f->dt, 2) && fours(f->z, 2);
     a.vecA = p->dstate % 4 == 0 && al(f->A.ptr, 16);
     a.vecBC = fours(f->B, 3) && fours(f->C, 3);
@@ -118,10 +120,22 @@ size_t states_bytes(const ssd_selective_problem *p) {
     return (size_t)chunk_slots(p) * (size_t)p->channels * (size_t)sel_pad(p->dstate) * sizeof(float);
 }
 
-// The backward's workspace: adjoints, shares of dA and (dD, ddt_bias), shares of dB and dC, and the
-// forward's kept states where the caller brings none.
+// The segments' ends and sums of dt lie one after the other.
+void set_segments(SelArgs &a, void *at) {
+    a.segE = static_cast<float *>(at);
+    a.segS = a.segE + (size_t)a.nseqs * a.nseg * a.channels * a.NP;
+}
+size_t seg_bytes(const ssd_selective_problem *p) {
+    int nseg, seglen;
+    const int64_t ns = p->nseqs ? p->nseqs : p->batch;
+    sel_segments(ns, p->channels, p->ngroups, p->seqlen, sel_pad(p->dstate), &nseg, &seglen);
+    return up256(sel_seg_bytes(ns, p->channels, nseg, sel_pad(p->dstate)));
+}
+
+// The backward's workspace: adjoints, shares of dA and (dD, ddt_bias), shares of dB and dC, segments, and
+// the forward's kept states where the caller brings none.
 struct BwdPlan {
-    size_t adj, pA, pD, pBC, states, total;
+    size_t adj, pA, pD, pBC, seg, states, total;
     int nsets, cps;
 };
 BwdPlan plan(const ssd_selective_problem *p, bool kept) {
@@ -133,8 +147,9 @@ BwdPlan plan(const ssd_selective_problem *p, bool kept) {
     w.pA = st;
     w.pD = 2 * st;
     w.pBC = w.pD + up256((size_t)slots * (size_t)p->channels * 2 * sizeof(float));
-    w.states = w.pBC + up256((size_t)w.nsets * 2 * (size_t)(p->batch * p->seqlen * p->ngroups) *
+    w.seg = w.pBC + up256((size_t)w.nsets * 2 * (size_t)(p->batch * p->seqlen * p->ngroups) *
                              (size_t)sel_pad(p->dstate) * sizeof(float));
+    w.states = w.seg + seg_bytes(p);
     w.total = w.states + (kept ? 0 : st);
     return w;
 }
@@ -173,13 +188,26 @@ ssd_status ssd_selective_chunk_states_size(const ssd_selective_problem *p, size_
     return SSD_OK;
 }
 
-ssd_status ssd_selective_fwd(const ssd_selective_problem *p, const ssd_fwd_args *f, void *stream) {
+ssd_status ssd_selective_fwd_workspace_size(const ssd_selective_problem *p, size_t *bytes) {
+    if (bytes == nullptr) return SSD_ERR_INVALID_ARGUMENT;
+    SEL_TRY(check_problem(p, p != nullptr && p->nseqs != 0));
+    *bytes = seg_bytes(p);
+    return SSD_OK;
+}
+
+ssd_status ssd_selective_fwd(const ssd_selective_problem *p, const ssd_fwd_args *f, void *workspace, size_t workspace_bytes,
+                             void *stream) {
     SEL_TRY(check_inputs(p, f));
     SEL_TRY(check_tok(p, f->y, f->x.dtype, false));
     SEL_TRY(check_state(f->final_states, p));
+    if (const size_t need = seg_bytes(p)) {
+        if (workspace == nullptr || workspace_bytes < need) return SSD_ERR_WORKSPACE_TOO_SMALL;
+        if (!al(workspace, 256)) return SSD_ERR_MISALIGNED;
+    }
     if (p->seqlen == 0 && f->final_states.ptr == nullptr) return SSD_OK;
     SelArgs a = make_args(p, f);
     a.vec = a.vec && fours(f->y, 2);
+    set_segments(a, workspace);
     a.y = f->y.ptr; a.yb = f->y.stride[0]; a.yt = f->y.stride[1];
     a.final = f->final_states.ptr;
     a.final_bf16 = f->final_states.dtype == SSD_BF16;
@@ -206,6 +234,7 @@ ssd_status ssd_selective_bwd(const ssd_selective_problem *p, const ssd_bwd_args 
     cudaStream_t st = (cudaStream_t)stream;
     const bool bf16 = f->x.dtype == SSD_BF16;
     SelArgs a = make_args(p, f);
+    set_segments(a, ws + w.seg);
     if (a.states == nullptr && p->seqlen > 0) {       // the states entering the chunks, without an output
         a.states = reinterpret_cast<float *>(ws + w.states);
         if (sel_launch_fwd(a, bf16, st) != cudaSuccess) return SSD_ERR_CUDA;

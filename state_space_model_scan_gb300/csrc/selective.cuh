@@ -2,6 +2,8 @@
 // softplus, the chunk grid of its kept states, and the arguments of a call.
 #pragma once
 
+#include <algorithm>
+
 #include "f32x2.cuh"
 
 namespace ssd {
@@ -28,6 +30,11 @@ struct SelArgs {
     void *y, *final;
     int64_t yb, yt;
     float *states;                     // [nslots][channels][NP]: the state entering each chunk, or NULL
+    // a long sequence of few channels is cut into nseg segments of seglen tokens (a multiple of every tile); a first
+    // launch (ends) takes each from zero and leaves its end [nseqs][nseg][channels][NP] and sum of dt [nseqs][nseg][channels]
+    int nseg, seglen;
+    bool ends;
+    float *segE, *segS;
     // backward
     void *dx, *ddt, *dz, *dB, *dC, *dinit;
     int64_t dxb, dxt, ddtb, ddtt, dzb, dzt, dBb, dBt, dBg, dCb, dCt, dCg;
@@ -53,6 +60,17 @@ __device__ __forceinline__ SelSeq sel_seq(const SelArgs &a, int s) {
         q.t0 = min(max(a.cu[s], 0), a.seqlen);
         q.len = min(max(a.cu[s + 1], q.t0), a.seqlen) - q.t0;
         q.slot0 = q.t0 / SEL_Q + s;    // floor(end / Q) + 1 slots on: enough for ceil(len / Q) chunks
+    }
+    return q;
+}
+
+// Segment k of a sequence: its tokens (none, where the sequence is shorter) and first chunk slot.
+__device__ __forceinline__ SelSeq sel_segment(const SelArgs &a, SelSeq q, int k) {
+    if (a.nseg > 1) {
+        const int at = min(k * a.seglen, q.len);
+        q.slot0 += at / SEL_Q;
+        q.t0 += at;
+        q.len = min(q.len - at, a.seglen);
     }
     return q;
 }
@@ -123,6 +141,33 @@ __device__ __forceinline__ void fetch4(U *dst, const U *src, int n, bool vec) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (i < n) dst[i] = src[i];
+    }
+}
+// Rows whose addresses do not allow that, to shared memory: R rows of W neighbouring elements by NT threads,
+// element by element, neighbours by neighbours; fp32 in the background, bf16 (no asynchronous copy is that
+// small) eight loads at a time.  Row r's elements are src + r `bytes` bytes on; nr rows and nw elements exist.
+template <int R, int W, int NT, typename U>
+__device__ __forceinline__ void fetch_rows(U *dst, const U *src, int bytes, int nr, int nw, int tid) {
+    constexpr int E = (R * W + NT - 1) / NT, B = E < 8 ? E : 8;
+#pragma unroll
+    for (int k0 = 0; k0 < E; k0 += B) {
+        U v[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const int i = tid + (k0 + k) * NT, r = i / W, c = i % W;
+            if (r < nr && c < nw) {
+                const U *p = reinterpret_cast<const U *>(reinterpret_cast<uintptr_t>(src + c) + (int64_t)r * bytes);
+                if constexpr (sizeof(U) == 4) cp_async_small<4>(dst + i, p);
+                else v[k] = *p;
+            }
+        }
+        if constexpr (sizeof(U) != 4) {
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                const int i = tid + (k0 + k) * NT;
+                if (i / W < nr && i % W < nw) dst[i] = v[k];
+            }
+        }
     }
 }
 // as they lie in memory (two bf16 to a register)
@@ -202,10 +247,31 @@ __device__ __forceinline__ float reduce_scatter(float (&v)[R], int q) {
     return v[0];
 }
 
+// Tokens of a tile and channels of a block where the sequences are split over time, by padded dstate.
+__host__ __device__ constexpr int sel_tile(int NP) { return NP <= 32 ? 128 : 64; }
+__host__ __device__ constexpr int sel_block(int NP) { return NP <= 32 ? 16 : NP == 64 ? 8 : 4; }
+
+// Segments: where a third of the card or less would be busy (two blocks to an SM), enough of them to fill
+// it, of two tiles at least.  Both launches together do half as much again as one, so that two do not pay.
+inline void sel_segments(int64_t nseqs, int64_t channels, int64_t ngroups, int64_t seqlen, int NP, int *nseg, int *seglen) {
+    const int64_t cb = sel_block(NP), blocks = nseqs * ngroups * ((channels / ngroups + cb - 1) / cb), slots = 2 * 152;
+    *nseg = 1;
+    *seglen = (int)seqlen;
+    if (blocks * 3 > slots) return;
+    const int64_t t = sel_tile(NP), want = slots / blocks, tiles = (seqlen + t - 1) / t;
+    const int64_t per = std::max<int64_t>(2, (tiles + want - 1) / want), n = (tiles + per - 1) / per;
+    if (n < 3) return;
+    *nseg = (int)n;
+    *seglen = (int)(per * t);
+}
+inline size_t sel_seg_bytes(int64_t nseqs, int64_t channels, int nseg, int NP) {
+    return nseg > 1 ? (size_t)nseqs * nseg * channels * (NP + 1) * sizeof(float) : 0;
+}
+
 // selective_fwd.cu: the scan, or with y == NULL its kept states alone
-cudaError_t sel_launch_fwd(const SelArgs &a, bool bf16, cudaStream_t st);
+cudaError_t sel_launch_fwd(SelArgs a, bool bf16, cudaStream_t st);
 // selective_bwd.cu
-cudaError_t sel_launch_bwd(const SelArgs &a, bool bf16, cudaStream_t st);
+cudaError_t sel_launch_bwd(SelArgs a, bool bf16, cudaStream_t st);
 void sel_bwd_sets(int channels, int ngroups, int64_t nslots, int *nsets, int *cps);
 
 }  // namespace ssd

@@ -39,7 +39,7 @@ struct RevCfg {
     static constexpr int S = S_, TPC = TPC_, CW = CW_, TW = TW_, TK = TK_, OCC = OCC_;
     static constexpr int NP = S * TPC, CPW = 64 / TPC, CB = CW * CPW, TT = TW * TK, NT = 32 * CW * TW;
     static constexpr int RX = 128 / CPW, PX = (TK + RX - 1) / RX, RB = NP < 128 ? 128 / NP : 1, PB = (TK + RB - 1) / RB;
-    static_assert(SEL_Q % TK == 0 && TT % SEL_Q == 0 && S % 4 == 0 && CB * NP / 4 <= NT, "tile shape");
+    static_assert(SEL_Q % TK == 0 && TT == sel_tile(NP) && CB == sel_block(NP) && S % 4 == 0 && CB * NP / 4 <= NT, "tile shape");
     // where the n-th four of channel c's states lies (as in the forward, off the banks)
     static __device__ __forceinline__ int at(int c, int n) { return (c ^ (c >> 1 & 1)) * (NP / 4) + n; }
     // bytes a warp keeps: (dt, dyp), C, and the next tile's dt, dy, z and C as they come
@@ -52,7 +52,8 @@ struct RevCfg {
     }
 };
 
-template <typename T, typename F>
+// VEC: every row allows four elements an access.
+template <typename T, typename F, bool VEC>
 __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int cblocks) {
     constexpr int S = F::S, TPC = F::TPC, NP = F::NP, CB = F::CB, CPW = F::CPW, TT = F::TT, TK = F::TK, TW = F::TW;
     extern __shared__ __align__(16) uint8_t sel_sm[];
@@ -67,14 +68,14 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
     float *E = reinterpret_cast<float *>(sel_sm + F::CW * TW * wbytes);   // two of [TW][CB][NP / 4] fours, placed by at(): what each warp passes on
     float *Sd = E + 2 * TW * CB * NP;                                // two of [TW][CB]: sums of dt
     const int q = lane % TPC, cp0 = 2 * (lane / TPC), cl = cw * CPW + cp0;
-    const int cb = blockIdx.x % cblocks, s = blockIdx.x / cblocks;
+    const int cb = blockIdx.x % cblocks, s = blockIdx.x / cblocks / a.nseg, seg = blockIdx.x / cblocks % a.nseg;
     const int bpg = cblocks / a.ngroups, g = cb / bpg;
     const int d0 = g * a.dpg + (cb % bpg) * CB, dend = (g + 1) * a.dpg, d = d0 + cl;
-    const SelSeq sq = sel_seq(a, s);
+    const SelSeq sq = sel_segment(a, sel_seq(a, s), seg);
     const int N = a.N, len = sq.len;
     const int pc = 4 * (lane % (CPW / 4)), pt = lane / (CPW / 4), e0 = d0 + cw * CPW + pc, nc = min(max(dend - e0, 0), 4);
     const int pn = 4 * (lane % (NP / 4)), pbt = lane / (NP / 4), nn = min(max(N - pn, 0), 4);
-    const bool vec = a.vec, vecBC = a.vecBC, gated = a.z != nullptr;
+    const bool vec = VEC || a.vec, vecBC = VEC || a.vecBC, gated = a.z != nullptr;
     const int es = a.dt_f32 ? 4 : (int)sizeof(T), ds = (int)a.dtt * es;
     const int ys = (int)a.dyt * (int)sizeof(T), zs = (int)a.zt * (int)sizeof(T), cs = (int)a.Ct * (int)sizeof(T);
     const T *dy = static_cast<const T *>(a.dy) + sq.b * a.dyb + sq.t0 * a.dyt + e0;
@@ -85,21 +86,35 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
 #pragma unroll
     for (int i = 0; i < 4; ++i) bias[i] = a.bias && i < nc ? a.bias[e0 + i] : 0.f;
 
+    const int nch = min(dend - d0 - cw * CPW, CPW);
     auto fetch = [&](int t0) {
+        const int tw = t0 + w * TK, nr = len - tw;
+        if (vec) {
 #pragma unroll
-        for (int k = 0; k < F::PX; ++k) {
-            const int tl = pt + k * F::RX, t = t0 + w * TK + tl;
-            if ((F::RX * F::PX == TK || tl < TK) && t < len) {
-                if (a.dt_f32) fetch4(rD + tl * CPW + pc, reinterpret_cast<const float *>(row(dtp, t, ds)), nc, vec);
-                else fetch4(reinterpret_cast<T *>(rD) + tl * CPW + pc, reinterpret_cast<const T *>(row(dtp, t, ds)), nc, vec);
-                fetch4(rY + tl * CPW + pc, row(dy, t, ys), nc, vec);
-                if (gated) fetch4(rZ + tl * CPW + pc, row(z, t, zs), nc, vec);
+            for (int k = 0; k < F::PX; ++k) {
+                const int tl = pt + k * F::RX, t = tw + tl;
+                if ((F::RX * F::PX == TK || tl < TK) && t < len) {
+                    if (a.dt_f32) fetch4(rD + tl * CPW + pc, reinterpret_cast<const float *>(row(dtp, t, ds)), nc, vec);
+                    else fetch4(reinterpret_cast<T *>(rD) + tl * CPW + pc, reinterpret_cast<const T *>(row(dtp, t, ds)), nc, vec);
+                    fetch4(rY + tl * CPW + pc, row(dy, t, ys), nc, vec);
+                    if (gated) fetch4(rZ + tl * CPW + pc, row(z, t, zs), nc, vec);
+                }
             }
+        } else if (nr > 0) {
+            const uint8_t *dt0 = dtp - pc * es;
+            if (a.dt_f32) fetch_rows<TK, CPW, 32>(rD, reinterpret_cast<const float *>(row(dt0, tw, ds)), ds, nr, nch, lane);
+            else fetch_rows<TK, CPW, 32>(reinterpret_cast<T *>(rD), reinterpret_cast<const T *>(row(dt0, tw, ds)), ds, nr, nch, lane);
+            fetch_rows<TK, CPW, 32>(rY, row(dy - pc, tw, ys), ys, nr, nch, lane);
+            if (gated) fetch_rows<TK, CPW, 32>(rZ, row(z - pc, tw, zs), zs, nr, nch, lane);
         }
+        if (vecBC) {
 #pragma unroll 4
-        for (int k = 0; k < F::PB; ++k) {
-            const int tl = pbt + k * F::RB, t = t0 + w * TK + tl;
-            if (t < len) fetch4(rC + tl * NP + pn, row(C, t, cs), nn, vecBC);
+            for (int k = 0; k < F::PB; ++k) {
+                const int tl = pbt + k * F::RB, t = tw + tl;
+                if (t < len) fetch4(rC + tl * NP + pn, row(C, t, cs), nn, vecBC);
+            }
+        } else if (nr > 0) {
+            fetch_rows<TK, NP, 32>(rC, row(C - pn, tw, cs), cs, nr, N, lane);
         }
         cp_async_commit();
     };
@@ -126,11 +141,23 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
         for (int e = 0; e < 4; ++e) {
             const bool in = d0 + jc < dend && jn + e < N;
             v[e] = in ? a.A[(int64_t)(d0 + jc) * N + jn + e] * kLog2e : 0.f;
-            uv[e] = in && a.dfinal ? ld_st(a.dfinal, a.dfinal_bf16, ((int64_t)s * a.channels + d0 + jc) * N + jn + e) : 0.f;
+            uv[e] = in && a.dfinal && !a.ends ? ld_st(a.dfinal, a.dfinal_bf16, ((int64_t)s * a.channels + d0 + jc) * N + jn + e) : 0.f;
         }
         jA[0] = pk2(v[0], v[1]); jA[1] = pk2(v[2], v[3]);
         ju[0] = pk2(uv[0], uv[1]); ju[1] = pk2(uv[2], uv[3]);
+        if (!a.ends && d0 + jc < dend) {                             // what the segments after this one pass on
+            const int64_t at = (int64_t)s * a.nseg * a.channels + d0 + jc;
+#pragma unroll 4
+            for (int k = a.nseg - 1; k > seg; --k) {
+                const float sd = a.segS[at + (int64_t)k * a.channels];
+                const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(a.segE + (at + (int64_t)k * a.channels) * NP + jn);
+                const f32x2 sd2 = pk2(sd, sd);
+                ju[0] = fma2(ex2x2(mul2(sd2, jA[0])), ju[0], e.x);
+                ju[1] = fma2(ex2x2(mul2(sd2, jA[1])), ju[1], e.y);
+            }
+        }
     }
+    float jsum = 0.f;
     const int last = len > 0 ? (len - 1) / TT * TT : -1;
     if (last >= 0) fetch(last);
     int buf = 0;
@@ -234,19 +261,27 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
 #pragma unroll
             for (int k = TW - 1; k >= 0; --k) {
                 const int te = t0 + (k + 1) * TK;                   // the k-th warp's tokens end here
-                if (te % SEL_Q == 0 && te - SEL_Q < len && d0 + jc < dend) {
+                if (!a.ends && te % SEL_Q == 0 && te - SEL_Q < len && d0 + jc < dend) {
                     const int slot = sq.slot0 + te / SEL_Q - 1;
                     if (slot < a.nslots)
                         *reinterpret_cast<ulonglong2 *>(a.adj + ((int64_t)slot * a.channels + d0 + jc) * NP + jn) =
                             make_ulonglong2(ju[0], ju[1]);
                 }
                 const f32x2 sd2 = pk2(sd[k], sd[k]);
+                jsum += sd[k];
                 ju[0] = fma2(ex2x2(mul2(sd2, jA[0])), ju[0], fold[k].x);
                 ju[1] = fma2(ex2x2(mul2(sd2, jA[1])), ju[1], fold[k].y);
             }
         }
     }
-    if (a.dinit == nullptr || !joins || d0 + jc >= dend) return;
+    if (!joins || d0 + jc >= dend) return;
+    if (a.ends) {
+        const int64_t at = ((int64_t)s * a.nseg + seg) * a.channels + d0 + jc;
+        *reinterpret_cast<ulonglong2 *>(a.segE + at * NP + jn) = make_ulonglong2(ju[0], ju[1]);
+        if (jn == 0) a.segS[at] = jsum;
+        return;
+    }
+    if (a.dinit == nullptr || seg > 0) return;
     float v[4];
     up2(ju[0], v[0], v[1]);
     up2(ju[1], v[2], v[3]);
@@ -280,7 +315,7 @@ struct Grad {
     static __device__ __forceinline__ int place(int c) { return c ^ (c >> 3 & 3); }
 };
 
-template <typename T, int NP>
+template <typename T, int NP, bool VEC>
 __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
     using G = Grad<T, NP>;
     constexpr int TPC = G::TPC, CPW = G::CPW, GC = G::GC, OP = G::OP;
@@ -315,7 +350,7 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
     const int64_t r0 = sq.t0 + tb;                                  // the chunk's first token in its row
     // the elementwise steps: this thread's token and first channel of those staged
     const int pt = tid / (GC / 4), pc = 4 * (tid % (GC / 4)), po = pt * GC + pc;
-    const bool tok = pt < n_tok, vec = a.vec, gated = a.z != nullptr;
+    const bool tok = pt < n_tok, vec = VEC || a.vec, gated = a.z != nullptr;
     const int64_t rt = r0 + (tok ? pt : 0);
     const T *x = static_cast<const T *>(a.x) + sq.b * a.xb + rt * a.xt + pc;
     const T *dy = static_cast<const T *>(a.dy) + sq.b * a.dyb + rt * a.dyt + pc;
@@ -342,8 +377,22 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
         aB[t][0] = aB[t][1] = aC[t][0] = aC[t][1] = 0;
     }
     auto count = [&](int cb) { return tok ? min(max(c_hi - cb - pc, 0), 4) : 0; };
+    const int xs = (int)a.xt * (int)sizeof(T), ys = (int)a.dyt * (int)sizeof(T), zs = (int)a.zt * (int)sizeof(T);
+    const int ds = (int)a.dtt * (a.dt_f32 ? 4 : (int)sizeof(T));
     auto fetch = [&](int cb, int k) {                               // the inputs of channels cb.., in the background
         const int nc = count(cb);
+        if (!vec) {
+            const int nw = min(c_hi - cb, GC);
+            const T *x0 = static_cast<const T *>(a.x) + sq.b * a.xb + r0 * a.xt + cb, *y0 = static_cast<const T *>(a.dy) + sq.b * a.dyb + r0 * a.dyt + cb;
+            fetch_rows<SEL_Q, GC, GNT>(m.rx[k], x0, xs, n_tok, nw, tid);
+            fetch_rows<SEL_Q, GC, GNT>(m.ry[k], y0, ys, n_tok, nw, tid);
+            if (gated) fetch_rows<SEL_Q, GC, GNT>(m.rz[k], static_cast<const T *>(a.z) + sq.b * a.zb + r0 * a.zt + cb, zs, n_tok, nw, tid);
+            const int64_t d0 = sq.b * a.dtb + r0 * a.dtt + cb;
+            if (a.dt_f32) fetch_rows<SEL_Q, GC, GNT>(m.rd[k], static_cast<const float *>(a.dt) + d0, ds, n_tok, nw, tid);
+            else fetch_rows<SEL_Q, GC, GNT>(reinterpret_cast<T *>(m.rd[k]), static_cast<const T *>(a.dt) + d0, ds, n_tok, nw, tid);
+            return;
+        }
+        if (pt >= SEL_Q) return;
         fetch4(m.rx[k] + po, x + cb, nc, vec);
         fetch4(m.ry[k] + po, dy + cb, nc, vec);
         if (gated) fetch4(m.rz[k] + po, z + cb, nc, vec);
@@ -371,13 +420,14 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
         }
     };
 
-    if (pt < SEL_Q) fetch(c_lo, 0);
+    fetch(c_lo, 0);
     fetch_own(c_lo, 0);
     int k = 0;                                                      // the buffer of these channels' inputs
     for (int cb = c_lo; cb < c_hi; cb += GC, k ^= 1) {
         const int nc = pt < SEL_Q ? count(cb) : 0;
         const bool mine = cb + tid * 4 / NP < c_hi;                 // this thread's four of A exist
-        cp_async_wait_all();                                        // (a thread uses what it fetched itself)
+        cp_async_wait_all();                                        // (a thread uses what it fetched itself, or)
+        if (!vec) __syncthreads();
         float Aq[4] = {0.f, 0.f, 0.f, 0.f};
         ulonglong2 hin = make_ulonglong2(0, 0), uin = hin;
         if (mine) {
@@ -422,7 +472,7 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
         __syncthreads();
         if (cb > c_lo) put_pD(cb - GC, k ^ 1);
         if (cb + GC < c_hi) {
-            if (pt < SEL_Q) fetch(cb + GC, k ^ 1);
+            fetch(cb + GC, k ^ 1);
             fetch_own(cb + GC, k ^ 1);
         }
         // from zero
@@ -673,34 +723,53 @@ __global__ void __launch_bounds__(256) k_sel_cols(const SelArgs a, int64_t block
     }
 }
 
-template <typename T, typename F>
-cudaError_t launch_rev(const SelArgs &a, cudaStream_t st) {
+template <typename T, typename F, bool VEC>
+cudaError_t launch_rev_rows(const SelArgs &a, cudaStream_t st) {
     static int attr[64] = {0};
     const size_t sm = F::template smem<T>(a.dt_f32);
-    cudaError_t e = ensure_smem_attr(k_sel_rev<T, F>, (int)sm, attr);
+    cudaError_t e = ensure_smem_attr(k_sel_rev<T, F, VEC>, (int)sm, attr);
     if (e != cudaSuccess) return e;
     const int cblocks = a.ngroups * ((a.dpg + F::CB - 1) / F::CB);
-    k_sel_rev<T, F><<<(unsigned)((int64_t)a.nseqs * cblocks), F::NT, sm, st>>>(a, cblocks);
+    k_sel_rev<T, F, VEC><<<(unsigned)((int64_t)a.nseqs * a.nseg * cblocks), F::NT, sm, st>>>(a, cblocks);
     return cudaGetLastError();
 }
-template <typename T, int NP>
-cudaError_t launch_grad(const SelArgs &a, cudaStream_t st) {
+template <typename T, typename F>
+cudaError_t launch_rev(const SelArgs &a, cudaStream_t st) {
+    return a.vec && a.vecBC ? launch_rev_rows<T, F, true>(a, st) : launch_rev_rows<T, F, false>(a, st);
+}
+template <typename T, int NP, bool VEC>
+cudaError_t launch_grad_rows(const SelArgs &a, cudaStream_t st) {
     static int attr[64] = {0};
-    cudaError_t e = ensure_smem_attr(k_sel_grad<T, NP>, (int)sizeof(Grad<T, NP>), attr);
+    cudaError_t e = ensure_smem_attr(k_sel_grad<T, NP, VEC>, (int)sizeof(Grad<T, NP>), attr);
     if (e != cudaSuccess) return e;
-    k_sel_grad<T, NP><<<(unsigned)((int64_t)a.nslots * a.ngroups * a.nsets), GNT, sizeof(Grad<T, NP>), st>>>(a);
+    k_sel_grad<T, NP, VEC><<<(unsigned)((int64_t)a.nslots * a.ngroups * a.nsets), GNT, sizeof(Grad<T, NP>), st>>>(a);
     return cudaGetLastError();
 }
 
+template <typename T, int NP>
+cudaError_t launch_grad(const SelArgs &a, cudaStream_t st) {
+    return a.vec ? launch_grad_rows<T, NP, true>(a, st) : launch_grad_rows<T, NP, false>(a, st);
+}
+
+template <typename T>
+cudaError_t rev(const SelArgs &a, cudaStream_t st) {
+    switch (a.NP) {
+        case 16: return launch_rev<T, RevCfg<4, 4, 1, 8, 16, 2>>(a, st);
+        case 32: return launch_rev<T, RevCfg<8, 4, 1, 8, 16, 2>>(a, st);
+        case 64: return launch_rev<T, RevCfg<8, 8, 1, 4, 16, 3>>(a, st);
+        default: return launch_rev<T, RevCfg<8, 16, 1, 4, 16, 2>>(a, st);
+    }
+}
 template <typename T>
 cudaError_t run_bwd(const SelArgs &a, cudaStream_t st) {
     cudaError_t e;
-    switch (a.NP) {
-        case 16: e = launch_rev<T, RevCfg<4, 4, 1, 8, 16, 2>>(a, st); break;
-        case 32: e = launch_rev<T, RevCfg<8, 4, 1, 8, 16, 2>>(a, st); break;
-        case 64: e = launch_rev<T, RevCfg<8, 8, 1, 4, 16, 3>>(a, st); break;
-        default: e = launch_rev<T, RevCfg<8, 16, 1, 4, 16, 2>>(a, st);
+    if (a.nseg > 1) {
+        SelArgs b = a;
+        b.ends = true;
+        e = rev<T>(b, st);
+        if (e != cudaSuccess) return e;
     }
+    e = rev<T>(a, st);
     if (e != cudaSuccess) return e;
     if (a.nslots > 0) {
         switch (a.NP) {
@@ -729,7 +798,7 @@ void sel_bwd_sets(int channels, int ngroups, int64_t nslots, int *nsets, int *cp
     *nsets = (dpg + c - 1) / c;
 }
 
-cudaError_t sel_launch_bwd(const SelArgs &a, bool bf16, cudaStream_t st) {
+cudaError_t sel_launch_bwd(SelArgs a, bool bf16, cudaStream_t st) {
     return bf16 ? run_bwd<__nv_bfloat16>(a, st) : run_bwd<float>(a, st);
 }
 

@@ -31,7 +31,7 @@ struct Cfg {
     // fours of a warp's x and of its B: rows a pass of the warp covers, passes
     static constexpr int RX = 128 / CPW, PX = (TK + RX - 1) / RX, RB = NP < 128 ? 128 / NP : 1, PB = (TK + RB - 1) / RB;
     static_assert(TPC >= 2 && TK % U == 0 && (TW == 1 ? TK % SEL_Q == 0 : SEL_Q % TK == 0) && TT % SEL_Q == 0 && S % 4 == 0, "tile shape");
-    static_assert(TW == 1 || CB * NP / 4 <= NT, "the joining takes a thread for four states");
+    static_assert(TW == 1 || (CB * NP / 4 <= NT && TT == sel_tile(NP) && CB == sel_block(NP)), "the joining takes a thread for four states");
     // where the n-th four of channel c's states lies: a warp's threads write one of two neighbouring channels at a
     // time, and every other pair has them swapped, so that eight threads meet eight different bank groups
     static __device__ __forceinline__ int at(int c, int n) { return (c ^ (c >> 1 & 1)) * (NP / 4) + n; }
@@ -46,7 +46,8 @@ struct Cfg {
     }
 };
 
-template <typename T, typename F>
+// VEC: every row allows four elements an access.
+template <typename T, typename F, bool VEC>
 __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int cblocks) {
     constexpr int S = F::S, TPC = F::TPC, NP = F::NP, CB = F::CB, CPW = F::CPW, TT = F::TT, TK = F::TK, TW = F::TW, U = F::U;
     extern __shared__ __align__(16) uint8_t sel_sm[];
@@ -62,15 +63,15 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
     float *E = reinterpret_cast<float *>(sel_sm + F::CW * TW * wbytes);   // [TW][CB][NP / 4] fours of end states, then entering states, placed by at()
     float *Sd = E + TW * CB * NP;                                   // [TW][CB]: sums of dt
     const int q = lane % TPC, cp0 = 2 * (lane / TPC), cl = cw * CPW + cp0;   // this thread's states [q S, q S + S) of channels cl, cl + 1
-    const int cb = blockIdx.x % cblocks, s = blockIdx.x / cblocks;
+    const int cb = blockIdx.x % cblocks, s = blockIdx.x / cblocks / a.nseg, seg = blockIdx.x / cblocks % a.nseg;
     const int bpg = cblocks / a.ngroups, g = cb / bpg;
     const int d0 = g * a.dpg + (cb % bpg) * CB, dend = (g + 1) * a.dpg, d = d0 + cl;
-    const SelSeq sq = sel_seq(a, s);
+    const SelSeq whole = sel_seq(a, s), sq = sel_segment(a, whole, seg);
     const int N = a.N, len = sq.len;
     // for the elementwise steps: this thread's four channels (the first is e0) and first token, and of B and C
     const int pc = 4 * (lane % (CPW / 4)), pt = lane / (CPW / 4), e0 = d0 + cw * CPW + pc, nc = min(max(dend - e0, 0), 4);
     const int pn = 4 * (lane % (NP / 4)), pbt = lane / (NP / 4), nn = min(max(N - pn, 0), 4);
-    const bool vec = a.vec, vecBC = a.vecBC;
+    const bool vec = VEC || a.vec, vecBC = VEC || a.vecBC;
     const int xs = (int)a.xt * (int)sizeof(T), zs = (int)a.zt * (int)sizeof(T), ys = (int)a.yt * (int)sizeof(T);
     const int es = a.dt_f32 ? 4 : (int)sizeof(T), ds = (int)a.dtt * es;
     const int bs = (int)a.Bt * (int)sizeof(T), cs = (int)a.Ct * (int)sizeof(T);
@@ -87,23 +88,39 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
         Dv[i] = a.D && i < nc ? a.D[e0 + i] : 0.f;
     }
 
+    // the channels and states of the warp that exist, and its rows' first elements, for rows taken element by element
+    const int nch = min(dend - d0 - cw * CPW, CPW);
+    const T *x0 = x - pc, *z0 = z - pc, *B0 = B - pn, *C0 = C - pn;
     auto fetch = [&](int t0) {                                      // the warp's tokens of a tile, in the background
+        const int tw = t0 + w * TK, nr = len - tw;
+        if (vec) {
 #pragma unroll
-        for (int k = 0; k < F::PX; ++k) {
-            const int tl = pt + k * F::RX, t = t0 + w * TK + tl;
-            if ((F::RX * F::PX == TK || tl < TK) && t < len) {
-                fetch4(rX + tl * CPW + pc, row(x, t, xs), nc, vec);
-                if (a.dt_f32) fetch4(rD + tl * CPW + pc, reinterpret_cast<const float *>(row(dtp, t, ds)), nc, vec);
-                else fetch4(reinterpret_cast<T *>(rD) + tl * CPW + pc, reinterpret_cast<const T *>(row(dtp, t, ds)), nc, vec);
+            for (int k = 0; k < F::PX; ++k) {
+                const int tl = pt + k * F::RX, t = tw + tl;
+                if ((F::RX * F::PX == TK || tl < TK) && t < len) {
+                    fetch4(rX + tl * CPW + pc, row(x, t, xs), nc, vec);
+                    if (a.dt_f32) fetch4(rD + tl * CPW + pc, reinterpret_cast<const float *>(row(dtp, t, ds)), nc, vec);
+                    else fetch4(reinterpret_cast<T *>(rD) + tl * CPW + pc, reinterpret_cast<const T *>(row(dtp, t, ds)), nc, vec);
+                }
             }
+        } else if (nr > 0) {
+            fetch_rows<TK, CPW, 32>(rX, row(x0, tw, xs), xs, nr, nch, lane);
+            const uint8_t *dt0 = dtp - pc * es;
+            if (a.dt_f32) fetch_rows<TK, CPW, 32>(rD, reinterpret_cast<const float *>(row(dt0, tw, ds)), ds, nr, nch, lane);
+            else fetch_rows<TK, CPW, 32>(reinterpret_cast<T *>(rD), reinterpret_cast<const T *>(row(dt0, tw, ds)), ds, nr, nch, lane);
         }
+        if (vecBC) {
 #pragma unroll 4
-        for (int k = 0; k < F::PB; ++k) {
-            const int tl = pbt + k * F::RB, t = t0 + w * TK + tl;
-            if (t < len) {
-                fetch4(rB + tl * NP + pn, row(B, t, bs), nn, vecBC);
-                fetch4(rC + tl * NP + pn, row(C, t, cs), nn, vecBC);
+            for (int k = 0; k < F::PB; ++k) {
+                const int tl = pbt + k * F::RB, t = tw + tl;
+                if (t < len) {
+                    fetch4(rB + tl * NP + pn, row(B, t, bs), nn, vecBC);
+                    fetch4(rC + tl * NP + pn, row(C, t, cs), nn, vecBC);
+                }
             }
+        } else if (nr > 0) {
+            fetch_rows<TK, NP, 32>(rB, row(B0, tw, bs), bs, nr, N, lane);
+            fetch_rows<TK, NP, 32>(rC, row(C0, tw, cs), cs, nr, N, lane);
         }
         cp_async_commit();
     };
@@ -128,16 +145,28 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
     const int jc = tid / (NP / 4), jn = 4 * (tid % (NP / 4));
     const bool joins = TW > 1 && tid < CB * NP / 4;
     f32x2 jA[2] = {0, 0}, jh[2] = {0, 0};
+    float jsum = 0.f;
     if (joins) {
         float v[4], hv[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const bool in = d0 + jc < dend && jn + e < N;
             v[e] = in ? a.A[(int64_t)(d0 + jc) * N + jn + e] * kLog2e : 0.f;
-            hv[e] = in && a.init ? ld_st(a.init, a.init_bf16, ((int64_t)s * a.channels + d0 + jc) * N + jn + e) : 0.f;
+            hv[e] = in && a.init && !a.ends ? ld_st(a.init, a.init_bf16, ((int64_t)s * a.channels + d0 + jc) * N + jn + e) : 0.f;
         }
         jA[0] = pk2(v[0], v[1]); jA[1] = pk2(v[2], v[3]);
         jh[0] = pk2(hv[0], hv[1]); jh[1] = pk2(hv[2], hv[3]);
+        if (!a.ends && d0 + jc < dend) {                            // what the segments before this one leave
+            const int64_t at = (int64_t)s * a.nseg * a.channels + d0 + jc;
+#pragma unroll 4
+            for (int k = 0; k < seg; ++k) {
+                const float sd = a.segS[at + (int64_t)k * a.channels];
+                const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(a.segE + (at + (int64_t)k * a.channels) * NP + jn);
+                const f32x2 sd2 = pk2(sd, sd);
+                jh[0] = fma2(ex2x2(mul2(sd2, jA[0])), jh[0], e.x);
+                jh[1] = fma2(ex2x2(mul2(sd2, jA[1])), jh[1], e.y);
+            }
+        }
     }
     fetch(0);
     for (int t0 = 0; t0 < len; t0 += TT) {
@@ -206,7 +235,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
         const float *bp = Bs + q * S, *cp = Cs + q * S;
         Raw4<T> rx[F::PX], rz[F::PX];                               // for the epilogue
         auto early = [&]() {
-            if (y == nullptr) return;
+            if (y == nullptr || !vec) return;
 #pragma unroll
             for (int k = 0; k < F::PX; ++k) {
                 const int tl = pt + k * F::RX, t = tw + tl;
@@ -266,6 +295,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
                                 make_ulonglong2(jh[0], jh[1]);
                     }
                     const f32x2 sd2 = pk2(sd[k], sd[k]);
+                    jsum += sd[k];
                     *(reinterpret_cast<ulonglong2 *>(E) + k * CB * (NP / 4) + F::at(jc, jn / 4)) = make_ulonglong2(jh[0], jh[1]);
                     jh[0] = fma2(ex2x2(mul2(sd2, jA[0])), jh[0], end[k].x);
                     jh[1] = fma2(ex2x2(mul2(sd2, jA[1])), jh[1], end[k].y);
@@ -336,6 +366,35 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
         }
         if (y == nullptr) continue;
         __syncwarp();
+        if (!vec) {                                                 // element by element, eight of x and z at a time
+            constexpr int E = TK * CPW / 32, EB = E < 8 ? E : 8;
+            const int c = lane % CPW, rr = lane / CPW;
+            const bool in = c < nch;
+            const float Dc = a.D && in ? a.D[d0 + cw * CPW + c] : 0.f;
+#pragma unroll 1
+            for (int k0 = 0; k0 < E; k0 += EB) {
+                T xv[EB], zv[EB];
+#pragma unroll
+                for (int k = 0; k < EB; ++k) {
+                    const int t = tw + (k0 + k) * (32 / CPW) + rr;
+                    if (in && t < len) {
+                        xv[k] = row(x0, t, xs)[c];
+                        if (z) zv[k] = row(z0, t, zs)[c];
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < EB; ++k) {
+                    const int tl = (k0 + k) * (32 / CPW) + rr, t = tw + tl;
+                    if (in && t < len) {
+                        float v = reinterpret_cast<const float *>(dd + tl * (CPW / 2) + (c / 2 ^ (tl & 1)))[c % 2 * 2 + 1];
+                        if (a.D) v = fmaf(Dc, to_f(xv[k]), v);
+                        if (z) v = sel_gate<T>(v, to_f(zv[k]));
+                        row(y - pc, t, ys)[c] = from_f<T>(v);
+                    }
+                }
+            }
+            continue;
+        }
 #pragma unroll
         for (int k = 0; k < F::PX; ++k) {
             const int tl = pt + k * F::RX, t = tw + tl;
@@ -357,7 +416,16 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
             }
         }
     }
-    if (a.final == nullptr) return;
+    if (TW > 1 && a.ends) {
+        if (joins && d0 + jc < dend) {
+            const int64_t at = ((int64_t)s * a.nseg + seg) * a.channels + d0 + jc;
+            *reinterpret_cast<ulonglong2 *>(a.segE + at * NP + jn) = make_ulonglong2(jh[0], jh[1]);
+            if (jn == 0) a.segS[at] = jsum;
+        }
+        return;
+    }
+    // the segment that holds the sequence's last token (the first one, where there is none) has the final state
+    if (a.final == nullptr || sq.t0 + len != whole.t0 + whole.len || (len == 0 && seg > 0)) return;
     auto put = [&](int c, int n0, f32x2 lo, f32x2 hi) {             // states n0 .. n0 + 3 of channel d0 + c
         if (d0 + c >= dend) return;
         float v[4];
@@ -377,15 +445,19 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
     }
 }
 
-template <typename T, typename F>
-cudaError_t launch(const SelArgs &a, cudaStream_t st) {
+template <typename T, typename F, bool VEC>
+cudaError_t launch_rows(const SelArgs &a, cudaStream_t st) {
     static int attr[64] = {0};
     const size_t sm = F::template smem<T>(a.dt_f32);
-    cudaError_t e = ensure_smem_attr(k_sel_fwd<T, F>, (int)sm, attr);
+    cudaError_t e = ensure_smem_attr(k_sel_fwd<T, F, VEC>, (int)sm, attr);
     if (e != cudaSuccess) return e;
     const int cblocks = a.ngroups * ((a.dpg + F::CB - 1) / F::CB);
-    k_sel_fwd<T, F><<<(unsigned)((int64_t)a.nseqs * cblocks), F::NT, sm, st>>>(a, cblocks);
+    k_sel_fwd<T, F, VEC><<<(unsigned)((int64_t)a.nseqs * a.nseg * cblocks), F::NT, sm, st>>>(a, cblocks);
     return cudaGetLastError();
+}
+template <typename T, typename F>
+cudaError_t launch(const SelArgs &a, cudaStream_t st) {
+    return a.vec && a.vecBC ? launch_rows<T, F, true>(a, st) : launch_rows<T, F, false>(a, st);
 }
 
 // Without a split over time nothing is computed twice, but a sequence's tokens follow one another at
@@ -395,7 +467,7 @@ cudaError_t launch(const SelArgs &a, cudaStream_t st) {
 // them, 16111 tokens x 4096 channels, 650 / 724.
 template <typename T>
 cudaError_t pick(const SelArgs &a, cudaStream_t st) {
-    if ((int64_t)a.nseqs * a.channels >= (a.cu ? 65536 : 16384)) {
+    if (a.nseg == 1 && (int64_t)a.nseqs * a.channels >= (a.cu ? 65536 : 16384)) {
         switch (a.NP) {
             case 16: return launch<T, Cfg<4, 4, 4, 1, 32, 4>>(a, st);
             case 32: return launch<T, Cfg<8, 4, 4, 1, 32, 3>>(a, st);
@@ -413,7 +485,15 @@ cudaError_t pick(const SelArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t sel_launch_fwd(const SelArgs &a, bool bf16, cudaStream_t st) {
+cudaError_t sel_launch_fwd(SelArgs a, bool bf16, cudaStream_t st) {
+    if (a.nseg > 1) {                                               // the segments' ends from zero
+        SelArgs e = a;
+        e.ends = true;
+        e.y = nullptr;
+        e.states = nullptr;
+        const cudaError_t rc = bf16 ? pick<__nv_bfloat16>(e, st) : pick<float>(e, st);
+        if (rc != cudaSuccess) return rc;
+    }
     return bf16 ? pick<__nv_bfloat16>(a, st) : pick<float>(a, st);
 }
 

@@ -82,14 +82,14 @@ def test_selective_refusals(m, mutate, code):
     assert bwd_size(m, p, b)[0] == 0
     mutate(p, f)
     b.fwd = f
-    assert m.load().ssd_selective_fwd(ctypes.byref(p), ctypes.byref(f), None) == code
+    assert m.load().ssd_selective_fwd(ctypes.byref(p), ctypes.byref(f), None, ctypes.c_size_t(0), None) == code
     assert bwd_size(m, p, b)[0] == code
 
 
 def test_selective_outputs_and_workspace(m):
     p, f, b = sel_case(m)
     f.y = m.Tensor()
-    assert m.load().ssd_selective_fwd(ctypes.byref(p), ctypes.byref(f), None) == 1
+    assert m.load().ssd_selective_fwd(ctypes.byref(p), ctypes.byref(f), None, ctypes.c_size_t(0), None) == 1
     p, f, b = sel_case(m)
     rc, n = bwd_size(m, p, b)
     assert rc == 0 and n > 0
@@ -117,6 +117,22 @@ def test_selective_chunk_states_size(m):
     assert size(m.SelectiveProblem(2, 65, 24, 2, 12, 0)) == 2 * 5 * 24 * 16 * 4
     assert size(m.SelectiveProblem(1, 65, 24, 2, 17, 5)) == (4 + 5) * 24 * 32 * 4
     assert size(m.SelectiveProblem(2, 0, 24, 2, 12, 0)) == 0
+
+
+def test_selective_forward_workspace(m):
+    """None, but for a long sequence of few channels: f32 (dstate padded + 1) a segment and channel."""
+    def size(p):
+        n = ctypes.c_size_t(0)
+        assert m.load().ssd_selective_fwd_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0
+        return n.value
+    assert size(m.SelectiveProblem(1, 2048, 4096, 1, 16, 0)) == 0 and size(m.SelectiveProblem(1, 300, 32, 1, 16, 0)) == 0
+    p, f, b = sel_case(m, Bt=1, L=16000, Dm=24, G=2, N=16)
+    n = size(p)
+    assert n >= 3 * 24 * 17 * 4
+    run = m.load().ssd_selective_fwd
+    assert run(ctypes.byref(p), ctypes.byref(f), D, ctypes.c_size_t(n - 1), None) == 4
+    assert run(ctypes.byref(p), ctypes.byref(f), None, ctypes.c_size_t(n), None) == 4
+    assert run(ctypes.byref(p), ctypes.byref(f), at(16), ctypes.c_size_t(n), None) == 3
 
 
 def step_problem(m, **k):

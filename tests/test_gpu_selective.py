@@ -141,6 +141,14 @@ def test_packed_sequences(lens, dtype):
     check(make(lens=lens, Dm=35, G=1, N=16, dtype=dtype, seed=len(lens)))
 
 
+@pytest.mark.parametrize("dtype,N", [("bf16", 16), ("f32", 13), ("f32", 40)])
+@pytest.mark.parametrize("shape", [dict(L=1300), dict(L=2561, G=2), dict(Bt=2, L=999), dict(lens=[1, 1200, 0, 257, 900, 3]), dict(lens=[1025])])
+def test_long_sequences_of_few_channels(dtype, N, shape):
+    """Few channels, many tokens: the sequences are cut into segments whose ends are joined."""
+    for keep in (True, False):
+        check(make(Dm=6, N=N, dtype=dtype, seed=N, **shape), keep)
+
+
 def test_packed_is_separate_and_poison_stays_in_its_sequence():
     i = make(lens=[40, 37, 64], Dm=33, N=16, z=True)
     clean = gpu(i)
