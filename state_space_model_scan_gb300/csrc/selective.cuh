@@ -144,30 +144,46 @@ __device__ __forceinline__ void fetch4(U *dst, const U *src, int n, bool vec) {
     }
 }
 // Rows whose addresses do not allow that, to shared memory: R rows of W neighbouring elements by NT threads,
-// element by element, neighbours by neighbours; fp32 in the background, bf16 (no asynchronous copy is that
-// small) eight loads at a time.  Row r's elements are src + r `bytes` bytes on; nr rows and nw elements exist.
+// element by element, neighbours by neighbours.  fp32 goes in the background at load(); bf16 (no
+// asynchronous copy is that small) waits in registers for store().  Row r's elements are src + r `bytes`
+// bytes on; nr rows and nw elements exist (one of each at least; for the others the last one's are read,
+// so that no load waits for a branch).
 template <int R, int W, int NT, typename U>
-__device__ __forceinline__ void fetch_rows(U *dst, const U *src, int bytes, int nr, int nw, int tid) {
-    constexpr int E = (R * W + NT - 1) / NT, B = E < 8 ? E : 8;
+struct Rows {
+    static constexpr int E = (R * W + NT - 1) / NT;
+    U v[sizeof(U) == 4 ? 1 : E];
+    __device__ __forceinline__ void load(U *dst, const U *src, int bytes, int nr, int nw, int tid) {
 #pragma unroll
-    for (int k0 = 0; k0 < E; k0 += B) {
-        U v[B];
-#pragma unroll
-        for (int k = 0; k < B; ++k) {
-            const int i = tid + (k0 + k) * NT, r = i / W, c = i % W;
-            if (r < nr && c < nw) {
-                const U *p = reinterpret_cast<const U *>(reinterpret_cast<uintptr_t>(src + c) + (int64_t)r * bytes);
-                if constexpr (sizeof(U) == 4) cp_async_small<4>(dst + i, p);
-                else v[k] = *p;
+        for (int k = 0; k < E; ++k) {
+            const int i = tid + k * NT, r = i / W, c = i % W;
+            if constexpr (sizeof(U) == 4) {
+                if (r < nr && c < nw)
+                    cp_async_small<4>(dst + i, reinterpret_cast<const U *>(reinterpret_cast<uintptr_t>(src + c) + (int64_t)r * bytes));
+            } else {
+                v[k] = *reinterpret_cast<const U *>(reinterpret_cast<uintptr_t>(src + min(c, nw - 1)) + (int64_t)min(r, nr - 1) * bytes);
             }
         }
+    }
+    __device__ __forceinline__ void store(U *dst, int nr, int nw, int tid) const {
         if constexpr (sizeof(U) != 4) {
 #pragma unroll
-            for (int k = 0; k < B; ++k) {
-                const int i = tid + (k0 + k) * NT;
+            for (int k = 0; k < E; ++k) {
+                const int i = tid + k * NT;
                 if (i / W < nr && i % W < nw) dst[i] = v[k];
             }
         }
+    }
+};
+// both at once, eight elements at a time
+template <int R, int W, int NT, typename U>
+__device__ __forceinline__ void fetch_rows(U *dst, const U *src, int bytes, int nr, int nw, int tid) {
+    constexpr int B = 8 * NT >= W && (8 * NT) % W == 0 && R % (8 * NT / W) == 0 ? 8 * NT / W : R;   // rows at a time
+#pragma unroll 1
+    for (int r = 0; r < R && r < nr; r += B) {
+        Rows<B, W, NT, U> g;
+        const U *p = reinterpret_cast<const U *>(reinterpret_cast<uintptr_t>(src) + (int64_t)r * bytes);
+        g.load(dst + r * W, p, bytes, min(nr - r, B), nw, tid);
+        g.store(dst + r * W, min(nr - r, B), nw, tid);
     }
 }
 // as they lie in memory (two bf16 to a register)

@@ -87,6 +87,8 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
     for (int i = 0; i < 4; ++i) bias[i] = a.bias && i < nc ? a.bias[e0 + i] : 0.f;
 
     const int nch = min(dend - d0 - cw * CPW, CPW);
+    Rows<TK, CPW, 32, T> ld, ly, lz;
+    Rows<TK, CPW, 32, float> lf;
     auto fetch = [&](int t0) {
         const int tw = t0 + w * TK, nr = len - tw;
         if (vec) {
@@ -100,12 +102,12 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
                     if (gated) fetch4(rZ + tl * CPW + pc, row(z, t, zs), nc, vec);
                 }
             }
-        } else if (nr > 0) {
+        } else if (nr > 0 && nch > 0) {                              // (element by element; the copies end in put())
             const uint8_t *dt0 = dtp - pc * es;
-            if (a.dt_f32) fetch_rows<TK, CPW, 32>(rD, reinterpret_cast<const float *>(row(dt0, tw, ds)), ds, nr, nch, lane);
-            else fetch_rows<TK, CPW, 32>(reinterpret_cast<T *>(rD), reinterpret_cast<const T *>(row(dt0, tw, ds)), ds, nr, nch, lane);
-            fetch_rows<TK, CPW, 32>(rY, row(dy - pc, tw, ys), ys, nr, nch, lane);
-            if (gated) fetch_rows<TK, CPW, 32>(rZ, row(z - pc, tw, zs), zs, nr, nch, lane);
+            if (a.dt_f32) lf.load(rD, reinterpret_cast<const float *>(row(dt0, tw, ds)), ds, nr, nch, lane);
+            else ld.load(reinterpret_cast<T *>(rD), reinterpret_cast<const T *>(row(dt0, tw, ds)), ds, nr, nch, lane);
+            ly.load(rY, row(dy - pc, tw, ys), ys, nr, nch, lane);
+            if (gated) lz.load(rZ, row(z - pc, tw, zs), zs, nr, nch, lane);
         }
         if (vecBC) {
 #pragma unroll 4
@@ -117,6 +119,13 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
             fetch_rows<TK, NP, 32>(rC, row(C - pn, tw, cs), cs, nr, N, lane);
         }
         cp_async_commit();
+    };
+    auto put = [&](int t0) {
+        const int nr = len - t0 - w * TK;
+        if (vec || nr <= 0 || nch <= 0) return;
+        if (!a.dt_f32) ld.store(reinterpret_cast<T *>(rD), nr, nch, lane);
+        ly.store(rY, nr, nch, lane);
+        if (gated) lz.store(rZ, nr, nch, lane);
     };
 
     f32x2 A2[2][S / 2];
@@ -159,7 +168,10 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
     }
     float jsum = 0.f;
     const int last = len > 0 ? (len - 1) / TT * TT : -1;
-    if (last >= 0) fetch(last);
+    if (last >= 0) {
+        fetch(last);
+        put(last);
+    }
     int buf = 0;
     for (int t0 = last; t0 >= 0; t0 -= TT, buf ^= 1) {
         cp_async_wait_all();
@@ -242,6 +254,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
                 }
             }
         }
+        if (t0 > 0) put(t0 - TT);
         ulonglong2 *ep = reinterpret_cast<ulonglong2 *>(E) + (buf * TW + w) * CB * (NP / 4);
 #pragma unroll
         for (int i = 0; i < S / 4; ++i) {
@@ -379,17 +392,19 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
     auto count = [&](int cb) { return tok ? min(max(c_hi - cb - pc, 0), 4) : 0; };
     const int xs = (int)a.xt * (int)sizeof(T), ys = (int)a.dyt * (int)sizeof(T), zs = (int)a.zt * (int)sizeof(T);
     const int ds = (int)a.dtt * (a.dt_f32 ? 4 : (int)sizeof(T));
+    Rows<SEL_Q, GC, GNT, T> lx, ly, lz, ld;
+    Rows<SEL_Q, GC, GNT, float> lf;
     auto fetch = [&](int cb, int k) {                               // the inputs of channels cb.., in the background
         const int nc = count(cb);
-        if (!vec) {
+        if (!vec) {                                                 // (element by element; the copies end in put())
             const int nw = min(c_hi - cb, GC);
             const T *x0 = static_cast<const T *>(a.x) + sq.b * a.xb + r0 * a.xt + cb, *y0 = static_cast<const T *>(a.dy) + sq.b * a.dyb + r0 * a.dyt + cb;
-            fetch_rows<SEL_Q, GC, GNT>(m.rx[k], x0, xs, n_tok, nw, tid);
-            fetch_rows<SEL_Q, GC, GNT>(m.ry[k], y0, ys, n_tok, nw, tid);
-            if (gated) fetch_rows<SEL_Q, GC, GNT>(m.rz[k], static_cast<const T *>(a.z) + sq.b * a.zb + r0 * a.zt + cb, zs, n_tok, nw, tid);
+            lx.load(m.rx[k], x0, xs, n_tok, nw, tid);
+            ly.load(m.ry[k], y0, ys, n_tok, nw, tid);
+            if (gated) lz.load(m.rz[k], static_cast<const T *>(a.z) + sq.b * a.zb + r0 * a.zt + cb, zs, n_tok, nw, tid);
             const int64_t d0 = sq.b * a.dtb + r0 * a.dtt + cb;
-            if (a.dt_f32) fetch_rows<SEL_Q, GC, GNT>(m.rd[k], static_cast<const float *>(a.dt) + d0, ds, n_tok, nw, tid);
-            else fetch_rows<SEL_Q, GC, GNT>(reinterpret_cast<T *>(m.rd[k]), static_cast<const T *>(a.dt) + d0, ds, n_tok, nw, tid);
+            if (a.dt_f32) lf.load(m.rd[k], static_cast<const float *>(a.dt) + d0, ds, n_tok, nw, tid);
+            else ld.load(reinterpret_cast<T *>(m.rd[k]), static_cast<const T *>(a.dt) + d0, ds, n_tok, nw, tid);
             return;
         }
         if (pt >= SEL_Q) return;
@@ -398,6 +413,14 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
         if (gated) fetch4(m.rz[k] + po, z + cb, nc, vec);
         if (a.dt_f32) fetch4(m.rd[k] + po, static_cast<const float *>(a.dt) + dt0 + cb, nc, vec);
         else fetch4(reinterpret_cast<T *>(m.rd[k]) + po, static_cast<const T *>(a.dt) + dt0 + cb, nc, vec);
+    };
+    auto put = [&](int cb, int k) {
+        if (vec) return;
+        const int nw = min(c_hi - cb, GC);
+        lx.store(m.rx[k], n_tok, nw, tid);
+        ly.store(m.ry[k], n_tok, nw, tid);
+        if (gated) lz.store(m.rz[k], n_tok, nw, tid);
+        if (!a.dt_f32) ld.store(reinterpret_cast<T *>(m.rd[k]), n_tok, nw, tid);
     };
     auto fetch_own = [&](int cb, int k) {                           // this thread's four of A and of what enters the chunk
         const int c = cb + tid * 4 / NP;
@@ -421,6 +444,7 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
     };
 
     fetch(c_lo, 0);
+    put(c_lo, 0);
     fetch_own(c_lo, 0);
     int k = 0;                                                      // the buffer of these channels' inputs
     for (int cb = c_lo; cb < c_hi; cb += GC, k ^= 1) {
@@ -504,6 +528,7 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
             *reinterpret_cast<ulonglong2 *>(&m.EX[1][it][w][lane * 4]) = make_ulonglong2(u[0], u[1]);
             if (q == 0) m.Sd[it][w][cw] = sum;
         }
+        if (cb + GC < c_hi) put(cb + GC, k ^ 1);
         __syncthreads();
         {                                                           // warp w joins step w: the state onwards, the adjoint backwards
             ulonglong2 eh[GW], eu[GW];

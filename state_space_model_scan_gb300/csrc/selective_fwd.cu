@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
                     else fetch4(reinterpret_cast<T *>(rD) + tl * CPW + pc, reinterpret_cast<const T *>(row(dtp, t, ds)), nc, vec);
                 }
             }
-        } else if (nr > 0) {
+        } else if (nr > 0 && nch > 0) {
             fetch_rows<TK, CPW, 32>(rX, row(x0, tw, xs), xs, nr, nch, lane);
             const uint8_t *dt0 = dtp - pc * es;
             if (a.dt_f32) fetch_rows<TK, CPW, 32>(rD, reinterpret_cast<const float *>(row(dt0, tw, ds)), ds, nr, nch, lane);
@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
         if (y == nullptr) continue;
         __syncwarp();
         if (!vec) {                                                 // element by element, eight of x and z at a time
+            if (!live || nch <= 0) continue;
             constexpr int E = TK * CPW / 32, EB = E < 8 ? E : 8;
             const int c = lane % CPW, rr = lane / CPW;
             const bool in = c < nch;
@@ -376,11 +377,9 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
                 T xv[EB], zv[EB];
 #pragma unroll
                 for (int k = 0; k < EB; ++k) {
-                    const int t = tw + (k0 + k) * (32 / CPW) + rr;
-                    if (in && t < len) {
-                        xv[k] = row(x0, t, xs)[c];
-                        if (z) zv[k] = row(z0, t, zs)[c];
-                    }
+                    const int t = min(tw + (k0 + k) * (32 / CPW) + rr, len - 1), e = min(c, nch - 1);   // (no load waits for a branch)
+                    xv[k] = row(x0, t, xs)[e];
+                    zv[k] = z ? row(z0, t, zs)[e] : xv[k];
                 }
 #pragma unroll
                 for (int k = 0; k < EB; ++k) {
