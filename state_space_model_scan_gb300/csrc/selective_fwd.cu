@@ -461,9 +461,9 @@ cudaError_t launch(const SelArgs &a, cudaStream_t st) {
 
 // Without a split over time nothing is computed twice, but a sequence's tokens follow one another at
 // some 200 cycles each, so it takes many (sequence, channel) pairs to fill the card.  Measured at dstate
-// 16, bf16, split against whole: 1 x 2048 tokens x 4096 channels 100 / 266 us, 2 x 2048 x 8192 340 / 324,
-// 16 x 1024 x 4096 647 / 447.  Packed sequences differ in length and the longest one decides: 9 of
-// them, 16111 tokens x 4096 channels, 650 / 724.
+// 16, bf16, split against whole: 4 x 2048 tokens x 2048 channels 185 / 279 us, 2 x 2048 x 8192 326 / 326,
+// 16 x 1024 x 4096 610 / 434.  Packed sequences differ in length and the longest one decides: 9 of
+// them, 16111 tokens x 4096 channels, 614 / 724.
 template <typename T>
 cudaError_t pick(const SelArgs &a, cudaStream_t st) {
     if (a.nseg == 1 && (int64_t)a.nseqs * a.channels >= (a.cu ? 65536 : 16384)) {
