@@ -119,6 +119,30 @@ inline cudaError_t ensure_smem_attr(K kernel, int bytes, int *set_bytes /* [64] 
     return e;
 }
 
+// Launch of a kernel whose start may overlap the end of the one before it in the stream: its blocks come onto
+// the SMs as that one's leave them, and wait in after_previous() until it has ended and its memory is
+// visible.  The kernel calls that first, in every block (a block that ended without waiting would let the
+// next kernel start before the previous one is done).  Calls of ssd_conv1d_step for 64 requests one after the
+// other: 6.1 us each with plain launches, 3.9 so (5.9 with blocks that come while all of the previous
+// kernel's still run).
+template <typename... P, typename... A>
+inline cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, const A &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __device__ __forceinline__ void set_status(int32_t *hdr, int32_t code) {
     atomicCAS(&hdr[HDR_STATUS], 0, code);
 }

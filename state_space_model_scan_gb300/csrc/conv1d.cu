@@ -347,6 +347,7 @@ __device__ void conv_edge(const ConvArgs &a, int64_t s, int64_t c0, const f32x2 
 // CARRY: sequences go on from carried windows; blocks past the token runs do their edges.
 template <typename T, int K, int W, bool CARRY>
 __global__ void __launch_bounds__(FG * CB / W, K > 4 ? 1 : sizeof(T) == 2 ? 6 : 4) k_conv_fwd(const ConvArgs a, int cols) {
+    after_previous();
     constexpr int NPC = CB / W;        // channel pieces of a block
     const int j = threadIdx.x % NPC, grp = threadIdx.x / NPC;
     const int64_t bx = blockIdx.x / cols, c0 = (int64_t)(blockIdx.x % cols) * CB + W * j;   // neighbouring blocks: one row's channels
@@ -680,8 +681,9 @@ __global__ void __launch_bounds__(256) k_conv_dw(const float *partials, int64_t 
 // One token for each of a batch of requests: thread (request, 8 channels) reads the window's K - 1
 // rows and the new one, and writes the window one row on.
 template <typename T, int K>
-__global__ void __launch_bounds__(128) k_conv_step(const ConvArgs a) {
-    const int64_t c0 = ((int64_t)blockIdx.x * 128 + threadIdx.x) * 8, b = blockIdx.y;
+__global__ void __launch_bounds__(128) k_conv_step(const ConvArgs a, int cols) {
+    after_previous();
+    const int64_t c0 = ((int64_t)(blockIdx.x % cols) * 128 + threadIdx.x) * 8, b = blockIdx.x / cols;
     if (c0 >= a.Cn) return;
     T *win = window<T>(a, b, K);
     float rows[K][8], w[8 * K];
@@ -732,8 +734,7 @@ cudaError_t launch_fwd_k(const ConvArgs &a, cudaStream_t st) {
     const int64_t blocks = a.B * ((a.L + FT * FG - 1) / (FT * FG)) + (CARRY ? (ns + FG - 1) / FG : 0);
     const int64_t cols = (a.Cn + CB - 1) / CB;
     if (blocks * cols > ((int64_t)1 << 31) - 1) return cudaErrorInvalidConfiguration;
-    k_conv_fwd<T, K, kFwdW, CARRY><<<(unsigned)(blocks * cols), FG * CB / kFwdW, 0, st>>>(a, (int)cols);
-    return cudaGetLastError();
+    return launch_early(k_conv_fwd<T, K, kFwdW, CARRY>, (unsigned)(blocks * cols), FG * CB / kFwdW, 0, st, a, (int)cols);
 }
 constexpr int kBwdW = CONV_BWD_W;   // channels per thread of the backward sweep
 template <typename T, int K>
@@ -775,18 +776,18 @@ cudaError_t launch_bwd(const ConvArgs &a, dim3 grid, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_step(const ConvArgs &a, cudaStream_t st) {
-    const dim3 grid((unsigned)((a.Cn / 8 + 127) / 128), (unsigned)a.B);
+    const int cols = (int)((a.Cn / 8 + 127) / 128);
+    const unsigned grid = (unsigned)(cols * a.B);
     switch (a.K) {
-        case 1: k_conv_step<T, 1><<<grid, 128, 0, st>>>(a); break;
-        case 2: k_conv_step<T, 2><<<grid, 128, 0, st>>>(a); break;
-        case 3: k_conv_step<T, 3><<<grid, 128, 0, st>>>(a); break;
-        case 4: k_conv_step<T, 4><<<grid, 128, 0, st>>>(a); break;
-        case 5: k_conv_step<T, 5><<<grid, 128, 0, st>>>(a); break;
-        case 6: k_conv_step<T, 6><<<grid, 128, 0, st>>>(a); break;
-        case 7: k_conv_step<T, 7><<<grid, 128, 0, st>>>(a); break;
-        default: k_conv_step<T, 8><<<grid, 128, 0, st>>>(a);
+        case 1: return launch_early(k_conv_step<T, 1>, grid, 128, 0, st, a, cols);
+        case 2: return launch_early(k_conv_step<T, 2>, grid, 128, 0, st, a, cols);
+        case 3: return launch_early(k_conv_step<T, 3>, grid, 128, 0, st, a, cols);
+        case 4: return launch_early(k_conv_step<T, 4>, grid, 128, 0, st, a, cols);
+        case 5: return launch_early(k_conv_step<T, 5>, grid, 128, 0, st, a, cols);
+        case 6: return launch_early(k_conv_step<T, 6>, grid, 128, 0, st, a, cols);
+        case 7: return launch_early(k_conv_step<T, 7>, grid, 128, 0, st, a, cols);
+        default: return launch_early(k_conv_step<T, 8>, grid, 128, 0, st, a, cols);
     }
-    return cudaGetLastError();
 }
 
 bool al16(const void *p) { return ((uintptr_t)p) % 16 == 0; }
@@ -880,7 +881,7 @@ ssd_status ssd_conv1d_step(const ssd_conv_problem *p, const void *x, int64_t x_s
                            const int32_t *state_indices, void *out, int64_t out_stride, void *stream) {
     CONV_TRY(check_conv(p, false));
     if (p->seqlen != 1) return SSD_ERR_INVALID_ARGUMENT;
-    if (p->batch > 65535) return SSD_ERR_UNSUPPORTED;
+    if (p->batch * ((p->channels + 1023) / 1024) > ((int64_t)1 << 31) - 1) return SSD_ERR_UNSUPPORTED;
     CONV_TRY(check_tok(p, x, x_stride, p->channels));
     CONV_TRY(check_tok(p, out, out_stride, p->channels));
     if (weight == nullptr) return SSD_ERR_INVALID_ARGUMENT;

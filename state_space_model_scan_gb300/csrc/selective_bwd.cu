@@ -55,6 +55,7 @@ struct RevCfg {
 // VEC: every row allows four elements an access.
 template <typename T, typename F, bool VEC>
 __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int cblocks) {
+    after_previous();
     constexpr int S = F::S, TPC = F::TPC, NP = F::NP, CB = F::CB, CPW = F::CPW, TT = F::TT, TK = F::TK, TW = F::TW;
     extern __shared__ __align__(16) uint8_t sel_sm[];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -330,6 +331,7 @@ struct Grad {
 
 template <typename T, int NP, bool VEC>
 __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
+    after_previous();
     using G = Grad<T, NP>;
     constexpr int TPC = G::TPC, CPW = G::CPW, GC = G::GC, OP = G::OP;
     extern __shared__ __align__(16) uint8_t sel_sm[];
@@ -704,6 +706,7 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
 // dB and dC: the channel sets' shares in order
 template <typename T>
 __global__ void __launch_bounds__(256) k_sel_dbc(const SelArgs a) {
+    after_previous();
     const int64_t rows = (int64_t)a.nbatch * a.seqlen * a.ngroups, per = rows * a.NP;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= 2 * per) return;
@@ -721,6 +724,7 @@ __global__ void __launch_bounds__(256) k_sel_dbc(const SelArgs a) {
 // dA, dD and ddt_bias: sums of the chunks' shares over the slots.  A block takes 32 columns; warp w
 // sums slots w, w + 8, ... in order, and the eight sums are added in order.
 __global__ void __launch_bounds__(256) k_sel_cols(const SelArgs a, int64_t blocksA) {
+    after_previous();
     __shared__ float red[8][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const bool isA = blockIdx.x < blocksA;
@@ -755,8 +759,7 @@ cudaError_t launch_rev_rows(const SelArgs &a, cudaStream_t st) {
     cudaError_t e = ensure_smem_attr(k_sel_rev<T, F, VEC>, (int)sm, attr);
     if (e != cudaSuccess) return e;
     const int cblocks = a.ngroups * ((a.dpg + F::CB - 1) / F::CB);
-    k_sel_rev<T, F, VEC><<<(unsigned)((int64_t)a.nseqs * a.nseg * cblocks), F::NT, sm, st>>>(a, cblocks);
-    return cudaGetLastError();
+    return launch_early(k_sel_rev<T, F, VEC>, (unsigned)((int64_t)a.nseqs * a.nseg * cblocks), F::NT, sm, st, a, cblocks);
 }
 template <typename T, typename F>
 cudaError_t launch_rev(const SelArgs &a, cudaStream_t st) {
@@ -767,8 +770,7 @@ cudaError_t launch_grad_rows(const SelArgs &a, cudaStream_t st) {
     static int attr[64] = {0};
     cudaError_t e = ensure_smem_attr(k_sel_grad<T, NP, VEC>, (int)sizeof(Grad<T, NP>), attr);
     if (e != cudaSuccess) return e;
-    k_sel_grad<T, NP, VEC><<<(unsigned)((int64_t)a.nslots * a.ngroups * a.nsets), GNT, sizeof(Grad<T, NP>), st>>>(a);
-    return cudaGetLastError();
+    return launch_early(k_sel_grad<T, NP, VEC>, (unsigned)((int64_t)a.nslots * a.ngroups * a.nsets), GNT, sizeof(Grad<T, NP>), st, a);
 }
 
 template <typename T, int NP>
@@ -806,10 +808,12 @@ cudaError_t run_bwd(const SelArgs &a, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     const int64_t n = (int64_t)2 * a.nbatch * a.seqlen * a.ngroups * a.NP;
-    if (n > 0) k_sel_dbc<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
+    if (n > 0) {
+        e = launch_early(k_sel_dbc<T>, (unsigned)((n + 255) / 256), 256, 0, st, a);
+        if (e != cudaSuccess) return e;
+    }
     const int64_t bA = ((int64_t)a.channels * a.NP + 31) / 32, bD = ((int64_t)a.channels * 2 + 31) / 32;
-    k_sel_cols<<<(unsigned)(bA + bD), 256, 0, st>>>(a, bA);
-    return cudaGetLastError();
+    return launch_early(k_sel_cols, (unsigned)(bA + bD), 256, 0, st, a, bA);
 }
 
 }  // namespace

@@ -49,6 +49,7 @@ struct Cfg {
 // VEC: every row allows four elements an access.
 template <typename T, typename F, bool VEC>
 __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int cblocks) {
+    after_previous();
     constexpr int S = F::S, TPC = F::TPC, NP = F::NP, CB = F::CB, CPW = F::CPW, TT = F::TT, TK = F::TK, TW = F::TW, U = F::U;
     extern __shared__ __align__(16) uint8_t sel_sm[];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -451,8 +452,7 @@ cudaError_t launch_rows(const SelArgs &a, cudaStream_t st) {
     cudaError_t e = ensure_smem_attr(k_sel_fwd<T, F, VEC>, (int)sm, attr);
     if (e != cudaSuccess) return e;
     const int cblocks = a.ngroups * ((a.dpg + F::CB - 1) / F::CB);
-    k_sel_fwd<T, F, VEC><<<(unsigned)((int64_t)a.nseqs * a.nseg * cblocks), F::NT, sm, st>>>(a, cblocks);
-    return cudaGetLastError();
+    return launch_early(k_sel_fwd<T, F, VEC>, (unsigned)((int64_t)a.nseqs * a.nseg * cblocks), F::NT, sm, st, a, cblocks);
 }
 template <typename T, typename F>
 cudaError_t launch(const SelArgs &a, cudaStream_t st) {

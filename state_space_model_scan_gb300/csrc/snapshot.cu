@@ -83,6 +83,7 @@ __device__ __forceinline__ bool place(const SnapArgs &a, int64_t &r0, int &l, in
 // The loads of RU rows of NV pieces a lane are issued before the first is used.
 template <typename ST, int NV, int RU>
 __global__ void __launch_bounds__(SN_NT) k_snap_store(const SnapArgs a) {
+    after_previous();
     int64_t r0;
     int l, rpw;
     ST *st;
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(SN_NT) k_snap_store(const SnapArgs a) {
 
 template <typename ST, int NV, int RU>
 __global__ void __launch_bounds__(SN_NT) k_snap_load(const SnapArgs a) {
+    after_previous();
     int64_t r0;
     int l, rpw;
     ST *st;
@@ -165,6 +167,7 @@ __global__ void __launch_bounds__(SN_NT) k_snap_load(const SnapArgs a) {
 // Rows that do not allow four values an access: single ones, read twice.
 template <typename ST>
 __global__ void __launch_bounds__(SN_NT) k_snap_store1(const SnapArgs a) {
+    after_previous();
     int64_t r;
     int l, rpw;
     ST *st;
@@ -184,6 +187,7 @@ __global__ void __launch_bounds__(SN_NT) k_snap_store1(const SnapArgs a) {
 }
 template <typename ST>
 __global__ void __launch_bounds__(SN_NT) k_snap_load1(const SnapArgs a) {
+    after_previous();
     int64_t r;
     int l, rpw;
     ST *st;
@@ -234,18 +238,22 @@ ssd_status make(const ssd_snapshot_problem *p, const void *states, const int32_t
 }
 
 template <typename ST>
-void store(const SnapArgs &a, Cut how, unsigned grid, cudaStream_t st) {
-    if (how.nv == 0) k_snap_store1<ST><<<grid, SN_NT, 0, st>>>(a);
-    else if (how.nv == 1) k_snap_store<ST, 1, 4><<<grid, SN_NT, 0, st>>>(a);
-    else if (how.nv == 4) k_snap_store<ST, 4, 1><<<grid, SN_NT, 0, st>>>(a);
-    else k_snap_store<ST, 8, 1><<<grid, SN_NT, 0, st>>>(a);
+cudaError_t store(const SnapArgs &a, Cut how, unsigned grid, cudaStream_t st) {
+    switch (how.nv) {
+        case 0: return launch_early(k_snap_store1<ST>, grid, SN_NT, 0, st, a);
+        case 1: return launch_early(k_snap_store<ST, 1, 4>, grid, SN_NT, 0, st, a);
+        case 4: return launch_early(k_snap_store<ST, 4, 1>, grid, SN_NT, 0, st, a);
+        default: return launch_early(k_snap_store<ST, 8, 1>, grid, SN_NT, 0, st, a);
+    }
 }
 template <typename ST>
-void load(const SnapArgs &a, Cut how, unsigned grid, cudaStream_t st) {
-    if (how.nv == 0) k_snap_load1<ST><<<grid, SN_NT, 0, st>>>(a);
-    else if (how.nv == 1) k_snap_load<ST, 1, 4><<<grid, SN_NT, 0, st>>>(a);
-    else if (how.nv == 4) k_snap_load<ST, 4, 1><<<grid, SN_NT, 0, st>>>(a);
-    else k_snap_load<ST, 8, 1><<<grid, SN_NT, 0, st>>>(a);
+cudaError_t load(const SnapArgs &a, Cut how, unsigned grid, cudaStream_t st) {
+    switch (how.nv) {
+        case 0: return launch_early(k_snap_load1<ST>, grid, SN_NT, 0, st, a);
+        case 1: return launch_early(k_snap_load<ST, 1, 4>, grid, SN_NT, 0, st, a);
+        case 4: return launch_early(k_snap_load<ST, 4, 1>, grid, SN_NT, 0, st, a);
+        default: return launch_early(k_snap_load<ST, 8, 1>, grid, SN_NT, 0, st, a);
+    }
 }
 
 }  // namespace
@@ -262,9 +270,9 @@ ssd_status ssd_snapshot_store(const ssd_snapshot_problem *p, const void *states,
     unsigned grid = 0;
     const ssd_status s = make(p, states, state_indices, snapshots, scales, slots, a, how, grid);
     if (s != SSD_OK || grid == 0) return s;
-    if (p->state_dtype == SSD_BF16) store<__nv_bfloat16>(a, how, grid, (cudaStream_t)stream);
-    else store<float>(a, how, grid, (cudaStream_t)stream);
-    return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = p->state_dtype == SSD_BF16 ? store<__nv_bfloat16>(a, how, grid, st) : store<float>(a, how, grid, st);
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 ssd_status ssd_snapshot_load(const ssd_snapshot_problem *p, const int8_t *snapshots, const float *scales,
@@ -274,9 +282,9 @@ ssd_status ssd_snapshot_load(const ssd_snapshot_problem *p, const int8_t *snapsh
     unsigned grid = 0;
     const ssd_status s = make(p, states, state_indices, snapshots, scales, slots, a, how, grid);
     if (s != SSD_OK || grid == 0) return s;
-    if (p->state_dtype == SSD_BF16) load<__nv_bfloat16>(a, how, grid, (cudaStream_t)stream);
-    else load<float>(a, how, grid, (cudaStream_t)stream);
-    return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = p->state_dtype == SSD_BF16 ? load<__nv_bfloat16>(a, how, grid, st) : load<float>(a, how, grid, st);
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -95,6 +95,7 @@ __device__ __forceinline__ float raw_dt(const StepArgs &a, int64_t at, int64_t p
 // One rate per head.  T: type of x, B, C, z, y.  ST: of the state.  Segments are heads.
 template <typename T, typename ST, int V, int NV, int RU>
 __global__ void __launch_bounds__(ST_NT) k_step_head(const StepArgs a) {
+    after_previous();
     const int rb = blockIdx.x % a.nrb, bs = blockIdx.x / a.nrb, seg = bs % a.segs, b = bs / a.segs;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int l = lane & (a.lpr - 1), rpw = 32 / a.lpr;             // lane of the row, rows of a warp
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(ST_NT) k_step_head(const StepArgs a) {
 // requests.  Lane u of a row that has RU lanes reads, softens and finishes request u for all of them.
 template <typename T, typename ST, int V, int NV, int RU>
 __global__ void __launch_bounds__(ST_NT) k_step_channel(const StepArgs a) {
+    after_previous();
     const int rb = blockIdx.x % a.nrb, bs = blockIdx.x / a.nrb, seg = bs % a.segs, b0 = bs / a.segs * RU;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int l = lane & (a.lpr - 1), rpw = 32 / a.lpr;
@@ -290,16 +292,14 @@ cudaError_t launch_head(StepArgs a, cudaStream_t st) {
     lanes(a, V);
     const int per = (ST_NT / 32) * (32 / a.lpr) * RU;
     a.nrb = (a.rows + per - 1) / per;
-    k_step_head<T, ST, V, NV, RU><<<(unsigned)((int64_t)a.batch * a.segs * a.nrb), ST_NT, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(k_step_head<T, ST, V, NV, RU>, (unsigned)((int64_t)a.batch * a.segs * a.nrb), ST_NT, 0, st, a);
 }
 template <typename T, typename ST, int V, int NV, int RU>
 cudaError_t launch_channel(StepArgs a, cudaStream_t st) {
     lanes(a, V);
     const int per = (ST_NT / 32) * (32 / a.lpr), nb = (a.batch + RU - 1) / RU;
     a.nrb = (a.rows + per - 1) / per;
-    k_step_channel<T, ST, V, NV, RU><<<(unsigned)((int64_t)nb * a.segs * a.nrb), ST_NT, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(k_step_channel<T, ST, V, NV, RU>, (unsigned)((int64_t)nb * a.segs * a.nrb), ST_NT, 0, st, a);
 }
 
 // Rows or requests in flight per thread: measured at 256 requests x 80 heads x 64 x 128, bf16 states, 4 / 8 /

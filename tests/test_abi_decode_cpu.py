@@ -186,7 +186,7 @@ def test_conv_window_refusals(m):
     assert g(ctypes.byref(q), D, 16, D, None, None, 2, 48, None, D, 16, None) == 1
     assert g(ctypes.byref(q), D, 20, D, None, D, 2, 48, None, D, 16, None) == 3
     assert g(ctypes.byref(q), D, 16, None, None, D, 2, 48, None, D, 16, None) == 1
-    q.batch = 65536
+    q.batch = 1 << 31
     assert g(ctypes.byref(q), D, 16, D, None, D, 2, 48, None, D, 16, None) == 2
 
 
