@@ -64,7 +64,7 @@ def build_binding(force: bool = False) -> str:
     tmp = BINDING + ".tmp.%d" % os.getpid()
     cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi()] +
            [f for i in inc for f in ("-isystem", i)] + [src, "-o", tmp, "-L" + os.path.join(home, "lib"),
-                                                        "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+                                                        "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"])
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed for %s:\n%s\n%s" % (src, " ".join(cmd), r.stdout + r.stderr))

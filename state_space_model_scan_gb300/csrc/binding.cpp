@@ -4,7 +4,8 @@
 // outputs with torch and calls the C ABI.  A failed check raises ValueError, a refusal SSDError.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -121,8 +122,8 @@ struct Stream {
         handle = other ? PyLong_AsVoidPtr(o) : (void *)c10::cuda::getCurrentCUDAStream(dev).stream();
         if (PyErr_Occurred()) throw Raised();
     }
-    Tensor empty(at::IntArrayRef shape, const at::TensorOptions &opt) const {
-        Tensor t = at::empty(shape, opt);
+    Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
+        Tensor t = at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
         used(t);
         return t;
     }
@@ -165,7 +166,7 @@ PyObject *step(PyObject *const *a) {
     if (idx.defined()) like("state_indices", idx, {n}, I32, dev, 1);
     else NEED(slots >= n, "the state pool has fewer slots than there are requests");
     const Stream st(a[11], dev);
-    Tensor y = st.empty(x.sizes(), x.options());
+    Tensor y = st.empty(x.sizes(), x.scalar_type());
     const ssd_step_problem p{n, slots, H, P, G, N, state.stride(0), x.stride(0), dt.stride(0), stride0(z), B.stride(0), C.stride(0),
                              H * P, code(x), code(dt), code(state), 0};
     check((sel ? lib.selective_step : lib.step)(&p, ptr(state), ptr_as<int32_t>(idx), ptr(x), ptr(dt), ptr_as<float>(A), ptr(B), ptr(C),
@@ -201,7 +202,7 @@ PyObject *conv1d_prompt(PyObject *const *a) {
     }
     if (has.defined()) like("has_initial", has, {n}, U8 | BOOL, dev, 1);
     const Stream st(a[8], dev);
-    Tensor out = st.empty({Bt, L, Cn}, u.options());
+    Tensor out = st.empty({Bt, L, Cn}, u.scalar_type());
     const ssd_conv_problem p{Bt, L, Cn, K, cu.defined() ? n : 0, code(u), a[7] == Py_True, 0, 0};
     check(lib.conv1d_prompt(&p, ptr(u), u.stride(0), u.stride(1), ptr_as<float>(w), ptr_as<float>(bias), ptr_as<int32_t>(cu), ptr(win),
                             win.size(0), win.stride(0), ptr_as<int32_t>(idx), ptr_as<uint8_t>(has), ptr(out), L * Cn, Cn, st.handle),
@@ -216,7 +217,7 @@ PyObject *conv1d_step(PyObject *const *a) {
     const int dev = lead("xbc", u, 2);
     const int64_t n = u.size(0), Cn = u.size(1), K = check_conv(u, w, bias, win, idx, n, dev);
     const Stream st(a[6], dev);
-    Tensor out = st.empty({n, Cn}, u.options());
+    Tensor out = st.empty({n, Cn}, u.scalar_type());
     if (n > 0) {
         const ssd_conv_problem p{n, 1, Cn, K, 0, code(u), a[5] == Py_True, 0, 0};
         check(lib.conv1d_step(&p, ptr(u), u.stride(0), ptr_as<float>(w), ptr_as<float>(bias), ptr(win), win.size(0), win.stride(0),
@@ -321,23 +322,23 @@ PyObject *selective_fwd(PyObject *const *a) {
     const bool want_final = a[10] == Py_True, keep = a[12] == Py_True;
     const long sd = PyLong_AsLong(a[11]);
     const Stream st(a[13], s.dev);
-    Tensor y = st.empty({s.Bt, s.L, s.Dm}, x.options()), final, kept;
+    Tensor y = st.empty({s.Bt, s.L, s.Dm}, x.scalar_type()), final, kept;
     s.f.y = desc(y, 3);
     if (want_final) {
         const bool bf16 = sd < 0 ? init.defined() && init.scalar_type() == at::kBFloat16 : sd == SSD_BF16;
-        final = st.empty({s.S, s.Dm, s.N}, x.options().dtype(bf16 ? at::kBFloat16 : at::kFloat));
+        final = st.empty({s.S, s.Dm, s.N}, bf16 ? at::kBFloat16 : at::kFloat);
         s.f.final_states = desc(final, 3);
     }
     if (keep) {
         size_t n = 0;
         check(lib.chunk_states_size(&s.p, &n), "ssd_selective_chunk_states_size");
-        kept = st.empty({(int64_t)n}, x.options().dtype(at::kByte));
+        kept = st.empty({(int64_t)n}, at::kByte);
         s.f.chunk_states = kept.data_ptr();
     }
     size_t n = 0;
     check(lib.fwd_workspace_size(&s.p, &n), "ssd_selective_fwd_workspace_size");
     Tensor ws;
-    if (n > 0) ws = st.empty({(int64_t)n}, x.options().dtype(at::kByte));
+    if (n > 0) ws = st.empty({(int64_t)n}, at::kByte);
     check(lib.selective_fwd(&s.p, &s.f, ptr(ws), n, st.handle), "ssd_selective_fwd");
     PyObject *r = PyTuple_New(keep ? 3 : 2);
     if (!r) throw Raised();
@@ -364,7 +365,7 @@ PyObject *selective_bwd(PyObject *const *a) {
         s.f.chunk_states = kept.data_ptr();
     }
     const Stream st(a[14], s.dev);
-    const auto f32 = x.options().dtype(at::kFloat);
+    const auto f32 = at::kFloat;
     ssd_bwd_args b{};
     b.fwd = s.f;
     b.dy = desc(dy, 1);
@@ -372,23 +373,23 @@ PyObject *selective_bwd(PyObject *const *a) {
     PyObject *g = PyDict_New();
     if (!g) throw Raised();
     try {
-        auto out = [&](const char *name, ssd_tensor &d, at::IntArrayRef shape, const at::TensorOptions &opt) {
-            Tensor v = st.empty(shape, opt);
+        auto out = [&](const char *name, ssd_tensor &d, at::IntArrayRef shape, at::ScalarType type) {
+            Tensor v = st.empty(shape, type);
             d = desc(v, (int)v.dim());
             PyObject *o = wrap(v);
             const int rc = o ? PyDict_SetItemString(g, name, o) : -1;
             Py_XDECREF(o);
             if (rc) throw Raised();
         };
-        out("dx", b.dx, {s.Bt, s.L, s.Dm}, x.options());
-        out("ddt", b.ddt, {s.Bt, s.L, s.Dm}, dt.options());
+        out("dx", b.dx, {s.Bt, s.L, s.Dm}, x.scalar_type());
+        out("ddt", b.ddt, {s.Bt, s.L, s.Dm}, dt.scalar_type());
         out("dA", b.dA, {s.Dm, s.N}, f32);
-        out("dB", b.dB, {s.Bt, s.L, s.G, s.N}, x.options());
-        out("dC", b.dC, {s.Bt, s.L, s.G, s.N}, x.options());
+        out("dB", b.dB, {s.Bt, s.L, s.G, s.N}, x.scalar_type());
+        out("dC", b.dC, {s.Bt, s.L, s.G, s.N}, x.scalar_type());
         if (D.defined()) out("dD", b.dD, {s.Dm}, f32);
-        if (z.defined()) out("dz", b.dz, {s.Bt, s.L, s.Dm}, x.options());
+        if (z.defined()) out("dz", b.dz, {s.Bt, s.L, s.Dm}, x.scalar_type());
         if (bias.defined()) out("ddt_bias", b.ddt_bias, {s.Dm}, f32);
-        if (init.defined()) out("dinitial_states", b.dinitial_states, {s.S, s.Dm, s.N}, init.options());
+        if (init.defined()) out("dinitial_states", b.dinitial_states, {s.S, s.Dm, s.N}, init.scalar_type());
         size_t n = 0;
         check(lib.bwd_workspace_size(&s.p, &b, &n), "ssd_selective_bwd_workspace_size");
         Tensor ws;
@@ -401,7 +402,7 @@ PyObject *selective_bwd(PyObject *const *a) {
             NEED(ok && ws.is_cuda() && ws.is_contiguous(), "workspace.get(bytes) gives a contiguous tensor on the GPU");
             st.used(ws);
         } else {
-            ws = st.empty({(int64_t)(n < 256 ? 256 : n)}, x.options().dtype(at::kByte));
+            ws = st.empty({(int64_t)(n < 256 ? 256 : n)}, at::kByte);
         }
         check(lib.selective_bwd(&s.p, &b, ws.data_ptr(), ws.nbytes(), st.handle), "ssd_selective_bwd");
     } catch (...) {

@@ -27,7 +27,7 @@ ssd_status check_problem(const ssd_selective_problem *p, bool varlen) {
     if (p->seqlen > ((int64_t)1 << 30) || p->channels > ((int64_t)1 << 22) || ns > ((int64_t)1 << 24) ||
         ns * ((p->channels + 3) / 4 + p->ngroups) > ((int64_t)1 << 30) ||
         (p->seqlen / SEL_Q + 1) * ns > ((int64_t)1 << 30) ||
-        p->batch * p->seqlen * p->ngroups > ((int64_t)1 << 31))
+        p->batch * p->seqlen * p->ngroups > ((int64_t)1 << 29))
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }

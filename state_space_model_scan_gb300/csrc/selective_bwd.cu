@@ -703,29 +703,29 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
     }
 }
 
-// dB and dC: the channel sets' shares in order
+// The sums of the shares, each in a fixed order.  dA, dD and ddt_bias: a block takes 32 columns; warp w sums the
+// chunk slots w, w + 8, ... in order, and the eight sums are added in order.  dB and dC (the blocks after
+// them): a thread sums one value's channel sets in order.
 template <typename T>
-__global__ void __launch_bounds__(256) k_sel_dbc(const SelArgs a) {
-    after_previous();
-    const int64_t rows = (int64_t)a.nbatch * a.seqlen * a.ngroups, per = rows * a.NP;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= 2 * per) return;
-    const int64_t row = i % per / a.NP;
-    const int n = (int)(i % a.NP), which = i >= per;
-    if (n >= a.N) return;
-    float v = 0.f;
-    for (int k = 0; k < a.nsets; ++k) v += a.pBC[k * 2 * per + i];
-    const int g = (int)(row % a.ngroups);
-    const int64_t tok = row / a.ngroups, b = tok / a.seqlen, t = tok % a.seqlen;
-    if (which) static_cast<T *>(a.dC)[b * a.dCb + t * a.dCt + g * a.dCg + n] = from_f<T>(v);
-    else static_cast<T *>(a.dB)[b * a.dBb + t * a.dBt + g * a.dBg + n] = from_f<T>(v);
-}
-
-// dA, dD and ddt_bias: sums of the chunks' shares over the slots.  A block takes 32 columns; warp w
-// sums slots w, w + 8, ... in order, and the eight sums are added in order.
-__global__ void __launch_bounds__(256) k_sel_cols(const SelArgs a, int64_t blocksA) {
+__global__ void __launch_bounds__(256) k_sel_sums(const SelArgs a, int64_t blocksA, int64_t blocksAD) {
     after_previous();
     __shared__ float red[8][32];
+    if (blockIdx.x >= blocksAD) {
+        const int64_t rows = (int64_t)a.nbatch * a.seqlen * a.ngroups, per = rows * a.NP;
+        const int64_t i = (blockIdx.x - blocksAD) * 256 + threadIdx.x;
+        if (i >= 2 * per) return;
+        const int64_t row = i % per / a.NP;
+        const int n = (int)(i % a.NP), which = i >= per;
+        if (n >= a.N) return;
+        float v = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < a.nsets; ++k) v += a.pBC[k * 2 * per + i];
+        const int g = (int)(row % a.ngroups);
+        const int64_t tok = row / a.ngroups, b = tok / a.seqlen, t = tok % a.seqlen;
+        if (which) static_cast<T *>(a.dC)[b * a.dCb + t * a.dCt + g * a.dCg + n] = from_f<T>(v);
+        else static_cast<T *>(a.dB)[b * a.dBb + t * a.dBt + g * a.dBg + n] = from_f<T>(v);
+        return;
+    }
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const bool isA = blockIdx.x < blocksA;
     const int64_t cols = isA ? (int64_t)a.channels * a.NP : (int64_t)a.channels * 2;
@@ -808,12 +808,8 @@ cudaError_t run_bwd(const SelArgs &a, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     const int64_t n = (int64_t)2 * a.nbatch * a.seqlen * a.ngroups * a.NP;
-    if (n > 0) {
-        e = launch_early(k_sel_dbc<T>, (unsigned)((n + 255) / 256), 256, 0, st, a);
-        if (e != cudaSuccess) return e;
-    }
     const int64_t bA = ((int64_t)a.channels * a.NP + 31) / 32, bD = ((int64_t)a.channels * 2 + 31) / 32;
-    return launch_early(k_sel_cols, (unsigned)(bA + bD), 256, 0, st, a, bA);
+    return launch_early(k_sel_sums<T>, (unsigned)(bA + bD + (n + 255) / 256), 256, 0, st, a, bA, bA + bD);
 }
 
 }  // namespace
