@@ -11,7 +11,7 @@ import torch
 
 from oracle import selective as osel
 from state_space_model_scan_gb300 import _lib
-from state_space_model_scan_gb300.api import SelectiveScanFunction, selective_scan_backward, selective_scan_forward
+from state_space_model_scan_gb300.api import SelectiveScanFunction, selective_scan_backward, selective_scan_forward, selective_scan_step
 from helpers import rel_l2
 
 pytestmark = pytest.mark.gpu
@@ -216,6 +216,27 @@ def test_extreme_steps():
     i["dt"][:, ::3] = 30.0
     i["dt"][:, 1::3] = -40.0
     check(i)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gate_far_below_zero(dtype):
+    # Every term has one sign, so that each element keeps its own relative accuracy: the type's rounding and a
+    # state's, as in the tolerances above, where silu(z) is as small as e^-40 too.
+    i = make(Bt=2, L=40, Dm=48, N=16, dtype=dtype, seed=23)
+    for k in ("x", "B", "C", "D", "init", "dy", "dfinal"):
+        i[k] = i[k].abs() + 0.125
+    i["dfinal"] = torch.zeros_like(i["dfinal"])
+    i["z"] = torch.linspace(-40, -2, i["z"].numel(), dtype=torch.float64).reshape(i["z"].shape).to(i["z"].dtype)
+    got, want = gpu(i), oracle(i)
+    for k in ("y", "dx", "dz"):
+        err = np.abs(h(got[k]) - want[k]) / np.abs(want[k])
+        assert err.max() < TOL[i["x"].dtype], (k, err.max())
+    d = dev(i)
+    state = d["init"].clone()
+    y = selective_scan_step(state, d["x"][:, 0], d["dt"][:, 0], d["A"], d["B"][:, 0], d["C"][:, 0], D=d["D"], z=d["z"][:, 0],
+                            dt_bias=d["dt_bias"])
+    err = np.abs(h(y) - want["y"][:, 0]) / np.abs(want["y"][:, 0])
+    assert err.max() < TOL[i["x"].dtype], err.max()
 
 
 def test_autograd_and_another_stream():
