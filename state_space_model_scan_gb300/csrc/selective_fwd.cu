@@ -15,6 +15,13 @@
 // joined in order (h <- exp(A sum dt) h + end), and each warp goes through its tokens again from the
 // state that really enters them.  A warp brings in, converts and finishes its own tokens (the next
 // tile's in the background), so that nothing but the joining needs the block's barriers.
+//
+// Bytes do not bound it: 2048 tokens x 4096 channels, dstate 16, bf16 (68 MB, 10 us of HBM) take 94 us,
+// two sweeps of 134 million exponentials, 13 us each at the multi-function units' 32 a clock and SM.
+// Instructions issue in 56% of the cycles with 13 warps an SM, shared memory is busy for 58%, the
+// multi-function unit for 36%: latency between the few warps that 128 registers a thread leave.
+// Three blocks an SM (80 registers, spills) took 108 us, 12 and 16 warps a block 112 and 131; a
+// thread for one channel, which reads B and C twice as often, 100.
 #include <algorithm>
 
 #include "selective.cuh"

@@ -1,6 +1,7 @@
 // snapshot.cu -- states put aside in 8 bits and taken up again.  A row of dstate values h is kept as
-// q = round_half_even(h ((1 / m) 127)) and the scale m / 127, m = max |h|, each step rounded to fp32.  Bytes bound it: 4 or 2 read
-// and 1 written per value, or the other way round.
+// q = round_half_even(h ((1 / m) 127)) and the scale m / 127, m = max |h|, each step rounded to fp32.  Bytes bound
+// it: 4 or 2 read and 1 written per value, or the other way round.  96 states of 4096 rows x 128, fp32, stored
+// and loaded: 81 us for 506 MB (6.2 TB/s, 92% of a plain copy).
 //
 // A row belongs to LPR lanes, each with NV pieces of four values, so that one exchange of the maximum
 // serves 16 values a lane.  The maximum lets a NaN through, so that one comparison finds rows that
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(SN_NT) k_snap_load1(const SnapArgs a) {
 
 // How a row is cut: pieces a lane and rows in flight (0: single values).  At dstate 64 and above four pieces
 // a lane, so that a row's lanes still read 64 bytes or more at once.  Round trip of 96 states of 4096 rows x 128,
-// fp32: four pieces of one row 86 us, one piece of four rows to store and of eight to load 113 us.
+// fp32: four pieces of one row 81 us, one piece of four rows to store and of eight to load 108 us.
 struct Cut {
     int nv, ru;
 };
