@@ -20,9 +20,6 @@
 #include <algorithm>
 
 #include "selective.cuh"
-#ifndef GRAD_OCC
-#define GRAD_OCC 3
-#endif
 
 namespace ssd {
 
@@ -33,7 +30,8 @@ __device__ __forceinline__ float sigf(float v) { return __fdividef(1.f, 1.f + ex
 
 // ---- the adjoint at the chunks' right ends: the forward's first sweep, backwards.  Warp (w, cw) has the w-th TK
 // tokens of a tile and the cw-th 64 / TPC channels, a thread S states of two channels; the warps' folds are
-// joined from the last to the first while the next tile is on its way.
+// joined from the last to the first while the next tile is on its way.  Bound as the forward: 2 x 2048 tokens x
+// 4096 channels, dstate 16, bf16 take 101 us (139 MB, 20 us of HBM); one sweep with states kept at the end.
 template <int S_, int TPC_, int CW_, int TW_, int TK_, int OCC_>
 struct RevCfg {
     static constexpr int S = S_, TPC = TPC_, CW = CW_, TW = TW_, TK = TK_, OCC = OCC_;
@@ -311,7 +309,11 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
 // bound.  For each GC channels the warps first sweep their tokens from zero (the state forwards, the
 // adjoint backwards), the ends are joined with what enters the chunk, and then the warps sweep again
 // from what really enters their tokens; the next channels' inputs come in the background.
+// 2 x 2048 tokens x 4096 channels, dstate 16, bf16: 393 us for 420 MB (62 us of HBM), instructions in 55% of
+// the cycles with 12 warps an SM (168 registers a thread), shared memory busy for 55%.  One step between
+// barriers instead of four took 900 us for the whole training step, instead of 743; dB and dC in shared memory 1009.
 constexpr int GT = 4, GW = SEL_Q / GT, GNT = 32 * GW, IT = 4;   // tokens a warp, warps, threads, steps
+constexpr int GOCC = 3;   // blocks per SM: the whole backward and forward at the size above took 795 us with two, 727 with three, 927 with four (spills)
 template <typename T, int NP>
 struct Grad {
     static constexpr int TPC = NP / 4, CPW = 32 / TPC, GC = IT * CPW, OP = GC + (CPW > 4 ? CPW : 4);   // (OP: row of the sums, off the banks)
@@ -330,7 +332,7 @@ struct Grad {
 };
 
 template <typename T, int NP, bool VEC>
-__global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
+__global__ void __launch_bounds__(GNT, GOCC) k_sel_grad(const SelArgs a) {
     after_previous();
     using G = Grad<T, NP>;
     constexpr int TPC = G::TPC, CPW = G::CPW, GC = G::GC, OP = G::OP;
@@ -705,7 +707,8 @@ __global__ void __launch_bounds__(GNT, GRAD_OCC) k_sel_grad(const SelArgs a) {
 
 // The sums of the shares, each in a fixed order.  dA, dD and ddt_bias: a block takes 32 columns; warp w sums the
 // chunk slots w, w + 8, ... in order, and the eight sums are added in order.  dB and dC (the blocks after
-// them): a thread sums one value's channel sets in order.
+// them): a thread sums one value's channel sets in order.  86 MB of shares at 2 x 2048 tokens x 4096 channels in 19 us
+// (4.5 TB/s); a launch for each kind took 2 us more in a call of 110.
 template <typename T>
 __global__ void __launch_bounds__(256) k_sel_sums(const SelArgs a, int64_t blocksA, int64_t blocksAD) {
     after_previous();
@@ -814,13 +817,23 @@ cudaError_t run_bwd(const SelArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-// Channels per set: as many as leave a few blocks per SM (each set writes its own shares of dB and dC).
+// Channels per set: those for which the card's rounds of blocks (GOCC on each of 152 SMs), each as long as its channels and
+// a start worth 16 more (a block loads B and C and fills its pipeline), are over soonest.  At most 256: a set's own shares
+// of dB and dC cost little by then.  Measured, training, dstate 16, bf16, by this rule / halving from 256 until
+// eight blocks are there for each SM / until four are: 1 x 256 x 4096 59 / 73 / 65 us, 1 x 512 x 2048 63 / 73 / 67,
+// 1 x 2048 x 1024 132 / 134 / 132, 4 x 1024 x 512 122 / 122 / 121, 2 x 2048 x 4096 704 with each.
 void sel_bwd_sets(int channels, int ngroups, int64_t nslots, int *nsets, int *cps) {
     const int dpg = channels / ngroups;
-    int c = 256;
-    while (c > 32 && nslots * ngroups * ((dpg + c - 1) / c) < 1216) c >>= 1;
-    *cps = c;
-    *nsets = (dpg + c - 1) / c;
+    int64_t best = INT64_MAX;
+    for (int c = 256; c >= 32; c -= 32) {
+        const int n = (dpg + c - 1) / c;
+        const int64_t rounds = (nslots * ngroups * n + 152 * GOCC - 1) / (152 * GOCC), cost = rounds * (std::min(c, dpg) + 16);
+        if (cost < best) {
+            best = cost;
+            *nsets = n;
+            *cps = c;
+        }
+    }
 }
 
 cudaError_t sel_launch_bwd(SelArgs a, bool bf16, cudaStream_t st) {
