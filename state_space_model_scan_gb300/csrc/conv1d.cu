@@ -345,13 +345,80 @@ __device__ void conv_edge(const ConvArgs &a, int64_t s, int64_t c0, const f32x2 
     }
 }
 
-// CARRY: sequences go on from carried windows; blocks past the token runs do their edges.
+// The tokens [s0, s1) of a run.  STARTS: sequences start there or less than K - 1 tokens before; a start clears the
+// rows before it, and with CARRY the K - 1 outputs after it are conv_edge's.
+template <typename T, int K, int W, bool CARRY, bool STARTS>
+__device__ __forceinline__ void conv_run(const ConvArgs &a, SeqCursor &cur, int64_t s0, int64_t s1, const T *u, T *o,
+                                         const f32x2 (&w)[K][W / 2], const f32x2 (&bias)[W / 2]) {
+    f32x2 rows[K - 1 + FB][W / 2];
+    const T *p = u + (s0 - (K - 1)) * a.su_l;
+    T *q = o + s0 * a.so_l;
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k, p += a.su_l) {
+        Row<T, W> r;
+        const bool in = !STARTS || s0 - (K - 1) + k >= cur.start;
+        r.load(in ? p : u + s0 * a.su_l);
+        r.pairs(rows[k]);
+        if (!in) {
+#pragma unroll
+            for (int h = 0; h < W / 2; ++h) rows[k][h] = 0;
+        }
+    }
+    const int n = (int)(s1 - s0);
+    Row<T, W> raw[FB];
+#pragma unroll
+    for (int e = 0; e < FB; ++e, p += a.su_l)
+        if (e < n) raw[e].load(p);
+#pragma unroll 1
+    for (int i = 0; i < n; i += FB) {
+#pragma unroll
+        for (int e = 0; e < FB; ++e, p += a.su_l) {
+            raw[e].pairs(rows[K - 1 + e]);
+            if (i + FB + e < n) raw[e].load(p);                 // FB rows are on their way all the time
+            if (i + e < n) {
+                bool put = true;
+                if (STARTS) {
+                    const int64_t t = s0 + i + e;
+                    cur.advance(a, t);
+                    const int fresh = (int)min(max(cur.start - (t - (K - 1)), (int64_t)0), (int64_t)K);   // rows before the start
+                    if (fresh > 0) {
+#pragma unroll
+                        for (int k = 0; k < K; ++k)
+#pragma unroll
+                            for (int h = 0; h < W / 2; ++h) rows[e + k][h] = k < fresh ? 0 : rows[e + k][h];
+                    }
+                    put = !CARRY || fresh == 0;
+                }
+                f32x2 acc[W / 2];
+#pragma unroll
+                for (int h = 0; h < W / 2; ++h) {
+                    acc[h] = bias[h];
+#pragma unroll
+                    for (int k = 0; k < K; ++k) acc[h] = fma2(w[k][h], rows[e + k][h], acc[h]);
+                }
+                if (a.silu) {
+#pragma unroll
+                    for (int h = 0; h < W / 2; ++h) acc[h] = silu2<T>(acc[h]);
+                }
+                if (put) store_pairs<T, W>(q, acc);
+                q += a.so_l;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+            for (int h = 0; h < W / 2; ++h) rows[k][h] = rows[FB + k][h];
+    }
+}
+
+// CARRY: sequences go on from carried windows; the first blocks do their edges, which take longest.
 template <typename T, int K, int W, bool CARRY>
 __global__ void __launch_bounds__(FG * CB / W, K > 4 ? 1 : sizeof(T) == 2 ? 6 : 4) k_conv_fwd(const ConvArgs a, int cols) {
     after_previous();
     constexpr int NPC = CB / W;        // channel pieces of a block
     const int j = threadIdx.x % NPC, grp = threadIdx.x / NPC;
-    const int64_t bx = blockIdx.x / cols, c0 = (int64_t)(blockIdx.x % cols) * CB + W * j;   // neighbouring blocks: one row's channels
+    int64_t bx = blockIdx.x / cols;
+    const int64_t c0 = (int64_t)(blockIdx.x % cols) * CB + W * j;   // neighbouring blocks: one row's channels
     if (c0 >= a.Cn) return;
     f32x2 w[K][W / 2], bias[W / 2];
     {
@@ -375,10 +442,13 @@ __global__ void __launch_bounds__(FG * CB / W, K > 4 ? 1 : sizeof(T) == 2 ? 6 : 
         }
     }
     const int64_t runs = (a.L + FT * FG - 1) / (FT * FG);       // blocks per row
-    if (CARRY && bx >= a.B * runs) {
-        const int64_t s = (bx - a.B * runs) * FG + grp, ns = a.cu ? a.S : a.B;
-        if (s < ns) conv_edge<T, K, W>(a, s, c0, w, bias);
-        return;
+    if (CARRY) {
+        const int64_t ns = a.cu ? a.S : a.B, edges = (ns + FG - 1) / FG;
+        if (bx < edges) {
+            if (bx * FG + grp < ns) conv_edge<T, K, W>(a, bx * FG + grp, c0, w, bias);
+            return;
+        }
+        bx -= edges;
     }
     const int64_t b = bx / runs, s0 = (bx % runs * FG + grp) * FT, s1 = std::min(a.L, s0 + FT);   // this thread's tokens
     if (s0 >= s1) return;
@@ -386,57 +456,10 @@ __global__ void __launch_bounds__(FG * CB / W, K > 4 ? 1 : sizeof(T) == 2 ? 6 : 
     T *o = static_cast<T *>(a.out) + b * a.so_b + c0;
     SeqCursor cur;
     cur.init(a, s0);
-    if (s0 - (K - 1) < cur.start || s1 > cur.next) {   // a sequence starts within the run, or less than K - 1 tokens before it
-#pragma unroll 1
-        for (int64_t t = s0; t < s1; ++t) {
-            cur.advance(a, t);
-            if (CARRY && t - (K - 1) < cur.start) continue;     // conv_edge's
-            one_token<T, K, W>(w, bias, a.silu, o + t * a.so_l,
-                               [&](int back) -> const T * { return t - back >= cur.start ? u + (t - back) * a.su_l : nullptr; });
-        }
-        return;
-    }
-    f32x2 rows[K - 1 + FB][W / 2];
-    const T *p = u + (s0 - (K - 1)) * a.su_l;
-    T *q = o + s0 * a.so_l;
-#pragma unroll
-    for (int k = 0; k < K - 1; ++k, p += a.su_l) {
-        Row<T, W> r;
-        r.load(p);
-        r.pairs(rows[k]);
-    }
-    const int n = (int)(s1 - s0);
-    Row<T, W> raw[FB];
-#pragma unroll
-    for (int e = 0; e < FB; ++e, p += a.su_l)
-        if (e < n) raw[e].load(p);
-#pragma unroll 1
-    for (int i = 0; i < n; i += FB) {
-#pragma unroll
-        for (int e = 0; e < FB; ++e, p += a.su_l) {
-            raw[e].pairs(rows[K - 1 + e]);
-            if (i + FB + e < n) raw[e].load(p);                 // FB rows are on their way all the time
-            if (i + e < n) {
-                f32x2 acc[W / 2];
-#pragma unroll
-                for (int h = 0; h < W / 2; ++h) {
-                    acc[h] = bias[h];
-#pragma unroll
-                    for (int k = 0; k < K; ++k) acc[h] = fma2(w[k][h], rows[e + k][h], acc[h]);
-                }
-                if (a.silu) {
-#pragma unroll
-                    for (int h = 0; h < W / 2; ++h) acc[h] = silu2<T>(acc[h]);
-                }
-                store_pairs<T, W>(q, acc);
-                q += a.so_l;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-            for (int h = 0; h < W / 2; ++h) rows[k][h] = rows[FB + k][h];
-    }
+    if (s0 - (K - 1) < cur.start || s1 > cur.next)              // a sequence starts within the run, or less than K - 1 tokens before it
+        conv_run<T, K, W, CARRY, true>(a, cur, s0, s1, u, o, w, bias);
+    else
+        conv_run<T, K, W, CARRY, false>(a, cur, s0, s1, u, o, w, bias);
 }
 
 // Backward over the thread's tokens [s0, s1): the sweep runs t from s0 to s1 + K - 2 computing
