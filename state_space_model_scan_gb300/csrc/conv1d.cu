@@ -220,8 +220,8 @@ __device__ __forceinline__ void stage_taps(const float *w, const float *bias, in
 // global memory (all in flight before the first is used; only the K - 1 rows before its run are read a
 // second time), keeps the last K rows as fp32 pairs, and does the taps and the gate's products
 // two channels to an instruction.
-// Bytes bound it: at 8191 x 6144 bf16, width 4, 43 us for 201 MB (4.7 TB/s, 69% of a plain copy; instructions
-// issue in 59% of the cycles).  Before launches overlapped it took 46; W = 8 then at best 48, four rows in flight 47, 32
+// Bytes bound it: at 8191 x 6144 bf16, width 4, 38 us for 201 MB (5.2 TB/s, 77% of a plain copy; instructions
+// issue in 60% of the cycles), 40 in six packed pieces.  Before launches overlapped it took 46; W = 8 then at best 48, four rows in flight 47, 32
 // tokens a run 50, 512-thread blocks 67, a staged tile in shared memory 56.
 constexpr int kFwdW = 4, FG = 2, FT = 16, FB = 8;   // channels a thread; runs in a block; tokens of a run; rows in flight
 
@@ -231,6 +231,14 @@ struct Row;
 template <int W>
 struct Row<float, W> {
     float4 v[W / 4];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ void store(float *p) const {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) reinterpret_cast<float4 *>(p)[i] = v[i];
+    }
     __device__ __forceinline__ void load(const float *p) {
 #pragma unroll
         for (int i = 0; i < W / 4; ++i) v[i] = reinterpret_cast<const float4 *>(p)[i];
@@ -246,6 +254,14 @@ struct Row<float, W> {
 template <int W>
 struct Row<__nv_bfloat16, W> {
     uint32_t v[W / 2];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) v[i] = 0;
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+        if constexpr (W == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(v[0], v[1], v[2], v[3]);
+        else *reinterpret_cast<uint2 *>(p) = make_uint2(v[0], v[1]);
+    }
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
         if constexpr (W == 8) {
             const uint4 u = *reinterpret_cast<const uint4 *>(p);
@@ -291,32 +307,26 @@ __device__ __forceinline__ T *window(const ConvArgs &a, int64_t s, int K) {
     return static_cast<T *>(a.win) + k * a.sw;
 }
 
-// pre[t] -> out: the taps over the rows that `at` gives for back = K - 1 .. 0 (NULL: a row of zeros)
-template <typename T, int K, int W, typename At>
-__device__ __forceinline__ void one_token(const f32x2 (&w)[K][W / 2], const f32x2 (&bias)[W / 2], bool silu, T *out, At at) {
+// the taps over rows[0 .. K - 1] -> out
+template <typename T, int K, int W>
+__device__ __forceinline__ void one_row(const f32x2 (&w)[K][W / 2], const f32x2 (&bias)[W / 2], bool silu, T *out, const f32x2 (*rows)[W / 2]) {
     f32x2 acc[W / 2];
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) acc[i] = bias[i];
+    for (int h = 0; h < W / 2; ++h) {
+        acc[h] = bias[h];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const T *p = at(K - 1 - k);
-        if (p == nullptr) continue;
-        Row<T, W> r;
-        f32x2 v[W / 2];
-        r.load(p);
-        r.pairs(v);
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) acc[i] = fma2(w[k][i], v[i], acc[i]);
+        for (int k = 0; k < K; ++k) acc[h] = fma2(w[k][h], rows[k][h], acc[h]);
     }
     if (silu) {
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) acc[i] = silu2<T>(acc[i]);
+        for (int h = 0; h < W / 2; ++h) acc[h] = silu2<T>(acc[h]);
     }
     store_pairs<T, W>(out, acc);
 }
 
 // With carried windows, a sequence's first K - 1 outputs and its new window come from the same
-// thread, which reads the old window before it writes (other blocks never touch windows).
+// thread, which reads the old window before it writes (other blocks never touch windows).  1025 tokens of 40
+// sequences x 6144 take 10 us with all its loads at once, 12 with a token's after another's.
 template <typename T, int K, int W>
 __device__ void conv_edge(const ConvArgs &a, int64_t s, int64_t c0, const f32x2 (&w)[K][W / 2], const f32x2 (&bias)[W / 2]) {
     const int64_t b = a.cu ? 0 : s;
@@ -327,21 +337,38 @@ __device__ void conv_edge(const ConvArgs &a, int64_t s, int64_t c0, const f32x2 
     const T *u = static_cast<const T *>(a.u) + b * a.su_b + c0;
     T *o = static_cast<T *>(a.out) + b * a.so_b + c0;
     const int n = (int)min(t1 - t0, (int64_t)(K - 1));
-#pragma unroll 1
-    for (int i = 0; i < n; ++i)
-        one_token<T, K, W>(w, bias, a.silu, o + (t0 + i) * a.so_l, [&](int back) -> const T * {
-            const int r = i - back;   // the row from the first token; below 0: in the window
-            return r >= 0 ? u + (t0 + r) * a.su_l : old ? win + (K - 1 + r) * a.Cn + c0 : nullptr;
-        });
-    if (win == nullptr) return;
-    for (int k = 0; k < K - 1; ++k) {   // new row k is K - 1 - k before the end: a token, or old row n + k >= k
-        const int64_t t = t1 - (K - 1) + k;
-        float v[W];
+    if constexpr (K > 1) {
+        Row<T, W> last[K - 1], first[K - 1], before[K - 1];   // everything is on its way before the first is used
+        if (win) {
 #pragma unroll
-        for (int e = 0; e < W; ++e) v[e] = 0.f;
-        if (t >= t0) ldw<W>(u + t * a.su_l, v);
-        else if (old) ldw<W>(win + (n + k) * a.Cn + c0, v);
-        stw<W>(win + k * a.Cn + c0, v);
+            for (int k = 0; k < K - 1; ++k) {   // new row k is K - 1 - k before the end: a token, or old row n + k
+                const int64_t t = t1 - (K - 1) + k;
+                last[k].zero();
+                if (t >= t0) last[k].load(u + t * a.su_l);
+                else if (old) last[k].load(win + (n + k) * a.Cn + c0);
+            }
+        }
+        if (n > 0) {
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k) {
+                before[k].zero();
+                if (old) before[k].load(win + k * a.Cn + c0);
+                first[k].load(u + (t0 + min(k, n - 1)) * a.su_l);
+            }
+            f32x2 rows[2 * K - 2][W / 2];
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k) {
+                before[k].pairs(rows[k]);
+                first[k].pairs(rows[K - 1 + k]);
+            }
+#pragma unroll
+            for (int i = 0; i < K - 1; ++i)
+                if (i < n) one_row<T, K, W>(w, bias, a.silu, o + (t0 + i) * a.so_l, rows + i);
+        }
+        if (win) {
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k) last[k].store(win + k * a.Cn + c0);
+        }
     }
 }
 
@@ -389,18 +416,7 @@ __device__ __forceinline__ void conv_run(const ConvArgs &a, SeqCursor &cur, int6
                     }
                     put = !CARRY || fresh == 0;
                 }
-                f32x2 acc[W / 2];
-#pragma unroll
-                for (int h = 0; h < W / 2; ++h) {
-                    acc[h] = bias[h];
-#pragma unroll
-                    for (int k = 0; k < K; ++k) acc[h] = fma2(w[k][h], rows[e + k][h], acc[h]);
-                }
-                if (a.silu) {
-#pragma unroll
-                    for (int h = 0; h < W / 2; ++h) acc[h] = silu2<T>(acc[h]);
-                }
-                if (put) store_pairs<T, W>(q, acc);
+                if (put) one_row<T, K, W>(w, bias, a.silu, q, rows + e);
                 q += a.so_l;
             }
         }
