@@ -11,6 +11,9 @@ Contents
 ``quadratic``   the materialised semiseparable (closed) form, NumPy float64.
 ``chunked64``   the chunkwise decomposition (intra-chunk segment sums + carried
                 chunk states), NumPy float64.
+``selective``   the scan with a decay rate per channel and state: forward, exact
+                adjoint, the single-token steps, the convolution with a carried
+                window and the 8-bit snapshots, NumPy float64.
 
 Parity status of each function is recorded in its module docstring.
 """

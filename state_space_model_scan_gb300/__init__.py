@@ -1,7 +1,8 @@
-"""GB300 (sm_103a) Mamba-2 SSD chunked scan.
+"""GB300 (sm_103a) state-space scans: the Mamba-2 SSD chunked scan, the selective scan with a decay rate per
+channel and state, and what serving them takes (single tokens, carried windows, 8-bit snapshots).
 
 The compute lives in libssd.so (C ABI, include/ssd.h); this package holds its
-thin ctypes binding (``_lib``), convenience wrappers that allocate outputs and
+thin ctypes binding (``_lib``) and the compiled one of the newer calls (``_binding``), convenience wrappers that allocate outputs and
 workspace with torch (``api``), the seeded input generator (``inputs``) and the
 build script (``build``).  Importing the package does not load the library; the
 first call does, and raises if it has not been built.

@@ -3,7 +3,9 @@
 Argument marshalling only: every step of the scan runs in the library's CUDA
 kernels.  Torch is used to own device memory and to supply the current stream;
 nothing here computes any part of the scan.  If libssd.so is missing the calls
-raise -- there is no fallback.
+raise -- there is no fallback.  The selective scan, the single-token steps, the
+carried windows and the snapshots are marshalled by a compiled module instead
+(csrc/binding.cpp, loaded by ``fast``): a step's call takes 4 us that way, 37 here.
 """
 import ctypes
 import os
