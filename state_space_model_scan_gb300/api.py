@@ -275,18 +275,22 @@ def selective_scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, in
 
 
 class SelectiveScanFunction(torch.autograd.Function):
-    """Autograd wrapper of the selective scan; the forward keeps its chunk states for the backward."""
+    """Autograd wrapper of the selective scan; the forward keeps its chunk states for the backward, and an output that
+    nothing was computed from costs no gradient of zeros.  A second differentiation is refused."""
 
     @staticmethod
     def forward(ctx, x, dt, A, B, C, D=None, z=None, dt_bias=None, initial_states=None, cu_seqlens=None):
         y, fin, kept = selective_scan_forward(x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, initial_states=initial_states,
                                               cu_seqlens=cu_seqlens, keep_chunk_states=True)
         ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens, kept)
+        ctx.set_materialize_grads(False)
         return y, fin
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dfin):
         x, dt, A, B, C, D, z, dt_bias, init, cu, kept = ctx.saved_tensors
+        dy = torch.zeros_like(x) if dy is None else dy
         g = selective_scan_backward(x, dt, A, B, C, dy.contiguous(), D=D, z=z, dt_bias=dt_bias, initial_states=init,
                                     dfinal_states=None if dfin is None else dfin.contiguous(), cu_seqlens=cu,
                                     chunk_states=kept)

@@ -258,6 +258,27 @@ def test_autograd_and_another_stream():
     assert torch.equal(y2, want["y"]) and torch.equal(fin2, want["final"]) and torch.equal(g2["dA"], want["dA"])
 
 
+def test_autograd_of_one_output():
+    i = make(Bt=2, L=20, Dm=32, dtype="f32", seed=29)
+    d = dev(i)
+    names = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "init")
+    a = (d["x"], d["dt"], d["A"], d["B"], d["C"])
+    none = torch.zeros_like(d["dy"]), torch.zeros_like(d["dfinal"])
+    for only_y in (True, False):
+        v = {k: d[k].clone().requires_grad_() for k in names}
+        y, fin = SelectiveScanFunction.apply(*(v[k] for k in names), None)
+        (y.sum() if only_y else fin.sum()).backward()      # gradients that are one value, expanded
+        want = selective_scan_backward(*a, torch.ones_like(d["dy"]) if only_y else none[0],
+                                       dfinal_states=none[1] if only_y else torch.ones_like(d["dfinal"]), **kw(d))
+        for k in names:
+            assert torch.equal(v[k].grad, want["d" + {"init": "initial_states"}.get(k, k)]), k
+    x = d["x"].clone().requires_grad_()
+    y, _ = SelectiveScanFunction.apply(x, *a[1:], None, None, None, None, None)
+    g, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
 @pytest.mark.parametrize("name", ["x", "dt", "A", "B", "C", "D", "z", "dt_bias", "init"])
 def test_gradients_against_differences(name):
     """The derivative along a random direction, from two forwards.  The loss sums some 4000 products with fp32 errors
