@@ -191,15 +191,12 @@ __device__ __forceinline__ void stw(T *p, const float *v) {
 // logistic function with the fast exponential and divide (relative error ~1e-6; 1/inf = 0
 // gives the right limit for very negative arguments)
 __device__ __forceinline__ float sig_fast(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
-// the same through one tanh.approx (relative error ~2^-11): (1 + tanh(v/2)) / 2, for bf16 data,
-// whose own rounding is 2^-9
-__device__ __forceinline__ float sig_tanh(float v) {
-    float t;
-    asm("tanh.approx.f32 %0, %1;" : "=f"(t) : "f"(0.5f * v));
-    return fmaf(0.5f, t, 0.5f);
-}
+// the same for bf16 data, without the division's range checks.  Not (1 + tanh(v / 2)) / 2 with the approximate tanh, one
+// operation of the multi-function unit instead of two: its error, 2^-12 of 1, is 1% of the result at v = -4 and all
+// of it from v = -8 on.
+__device__ __forceinline__ float sig_rcp(float v) { return rcpf(1.f + ex2f(-kLog2e * v)); }
 template <typename T>
-__device__ __forceinline__ float sig_t(float v) { return sizeof(T) == 2 ? sig_tanh(v) : sig_fast(v); }
+__device__ __forceinline__ float sig_t(float v) { return sizeof(T) == 2 ? sig_rcp(v) : sig_fast(v); }
 
 // The block's taps and biases, staged once in shared memory as [k][channel] (then [K][c] =
 // the bias): weight [Cn][K] holds channels cbase .. cbase+255 as 256K contiguous floats, read
@@ -221,7 +218,7 @@ __device__ __forceinline__ void stage_taps(const float *w, const float *bias, in
 // second time), keeps the last K rows as fp32 pairs, and does the taps and the gate's products
 // two channels to an instruction.
 // Bytes bound it: at 8191 x 6144 bf16, width 4, 38 us for 201 MB (5.2 TB/s, 77% of a plain copy; instructions
-// issue in 60% of the cycles), 40 in six packed pieces.  Before launches overlapped it took 46; W = 8 then at best 48, four rows in flight 47, 32
+// issue in 60% of the cycles), 41 in six packed pieces (40 with a single approximate tanh for the gate).  Before launches overlapped it took 46; W = 8 then at best 48, four rows in flight 47, 32
 // tokens a run 50, 512-thread blocks 67, a staged tile in shared memory 56.
 constexpr int kFwdW = 4, FG = 2, FT = 16, FB = 8;   // channels a thread; runs in a block; tokens of a run; rows in flight
 
@@ -282,11 +279,9 @@ template <typename T>
 __device__ __forceinline__ f32x2 silu2(f32x2 v) {
     float lo, hi;
     if (sizeof(T) == 2) {
-        const f32x2 half = pk2(0.5f, 0.5f);
-        up2(mul2(half, v), lo, hi);
-        asm("tanh.approx.f32 %0, %0;" : "+f"(lo));
-        asm("tanh.approx.f32 %0, %0;" : "+f"(hi));
-        return mul2(v, fma2(half, pk2(lo, hi), half));
+        up2(mul2(pk2(-kLog2e, -kLog2e), v), lo, hi);
+        up2(add2(pk2(1.f, 1.f), pk2(ex2f(lo), ex2f(hi))), lo, hi);
+        return mul2(v, pk2(rcpf(lo), rcpf(hi)));
     }
     up2(v, lo, hi);
     return pk2(lo * sig_fast(lo), hi * sig_fast(hi));

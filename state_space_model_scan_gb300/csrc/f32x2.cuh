@@ -1,4 +1,4 @@
-// f32x2.cuh -- arithmetic on pairs of fp32 values in one 64-bit register.
+// f32x2.cuh -- arithmetic on pairs of fp32 values in one 64-bit register, and the multi-function unit's 2^v and 1 / v.
 #pragma once
 
 #include "common.cuh"
@@ -33,4 +33,18 @@ __device__ __forceinline__ float sum2(f32x2 v) {
     up2(v, lo, hi);
     return lo + hi;
 }
+
+// 2^v (relative error about 2^-22; results below 2^-126 flush to zero)
+__device__ __forceinline__ float ex2f(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcpf(float v) {   // 1 / v to about 2^-23
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
 }  // namespace ssd

@@ -75,26 +75,12 @@ __device__ __forceinline__ SelSeq sel_segment(const SelArgs &a, SelSeq q, int k)
     return q;
 }
 
-// 2^v on the multi-function unit (relative error about 2^-22; results below 2^-126 flush to zero,
-// which a decay of that size is)
-__device__ __forceinline__ float ex2f(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
 __device__ __forceinline__ f32x2 ex2x2(f32x2 v) {
     float lo, hi;
     up2(v, lo, hi);
     return pk2(ex2f(lo), ex2f(hi));
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float rcpf(float v) {   // 1 / v to about 2^-23
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
 // softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1].  log1p(e) = 2 atanh(s) with
 // s = e / (2 + e) <= 1/3; 2 atanh(s) / s is a polynomial of degree 4 in s^2 there, fitted to
 // its smallest largest relative error, 4e-9.  No cancellation: small steps keep their relative accuracy.

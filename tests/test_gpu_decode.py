@@ -7,9 +7,10 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import conv1d as oconv
 from oracle import selective as osel
 from state_space_model_scan_gb300 import _lib
-from state_space_model_scan_gb300.api import (conv1d_forward, conv1d_prompt, conv1d_step, selective_scan_forward,
+from state_space_model_scan_gb300.api import (conv1d_backward, conv1d_forward, conv1d_prompt, conv1d_step, selective_scan_forward,
                                               selective_scan_step, snapshot_load, snapshot_store, ssd_forward, ssd_step)
 from helpers import rel_l2
 
@@ -364,3 +365,37 @@ def test_refusals():
     for args in ((st, q[:, :2], sc), (st, q.float(), sc), (st, q, sc[:, 0]), (st.double(), q, sc), (st, q[:1], sc[:1])):
         with pytest.raises(ValueError):
             snapshot_store(*args)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_conv_silu_far_below_zero(dtype):
+    """Each element's own relative accuracy where silu is as small as e^-40.  All products of an output have one sign, so
+    the sum before the activation is off by some 2^-22 of 40, 1e-5, and its silu by as much of itself; a result's rounding:
+    2^-8 allowed in bf16, 5e-5 in fp32.  So for the gradients: below -2 silu' keeps its sign too."""
+    Cn, K, L = 64, 4, 150
+    r = gen(41)
+    w = (0.5 + r(Cn, K).abs()).float()
+    w = w / w.sum(1, keepdim=True)
+    depth = torch.linspace(2.5, 40, Cn, dtype=torch.float64)
+    u = (-depth * (1 + 0.02 * r(1, L, Cn))).to(TD[dtype])
+    win = (-depth * (1 + 0.02 * r(1, K - 1, Cn))).to(TD[dtype])
+    dout = (r(1, L, Cn).abs() + 0.125).to(TD[dtype])
+    lim = 2.0 ** -8 if dtype == "bf16" else 5e-5
+
+    def close(got, want, what):
+        err = np.abs(h(got) - want) / np.abs(want)
+        assert err.max() <= lim, (what, err.max())
+    ud, wd, pool, dd = u.cuda(), w.cuda(), win.cuda(), dout.cuda()
+    want, _ = osel.conv(h(u[0]), h(w), None, h(win[0]))
+    close(conv1d_prompt(ud, wd, None, pool.clone())[0], want, "prompt")
+    steps = [conv1d_step(ud[:, t], wd, None, pool)[0] for t in range(L)]
+    close(torch.stack(steps), want, "step")
+    # from zeros the first sums are smaller, of one sign all the same
+    want, _ = oconv.forward(h(u[0]), h(w), None)
+    close(conv1d_forward(ud, wd, None)[0], want, "forward")
+    bias = -2.0 * torch.ones(Cn)
+    du, dw, db = conv1d_backward(ud, wd, dd, bias.cuda())
+    odu, odw, odb = oconv.backward(h(u[0]), h(w), h(dout[0]), h(bias))
+    close(du[0], odu, "du")
+    close(dw, odw, "dw")
+    close(db, odb, "db")
