@@ -241,7 +241,8 @@ def complex_ssd_forward(x, A, B, C, dt, initial_states=None, chunk_size=64, retu
 # The selective scan, the convolution with a carried window, single-token steps and 8-bit
 # snapshots of states.  Checks, allocation and the call are the compiled binding's
 # (csrc/binding.cpp): ValueError for tensors that do not fit together, SSDError for what the
-# library refuses.
+# library refuses.  stream: launch there instead of on the current stream; the caller orders the two around the call.
+# The outputs are then that stream's memory, and may be freed while the caller's current stream still reads them.
 def _handle(stream):
     return None if stream is None else stream.cuda_stream
 

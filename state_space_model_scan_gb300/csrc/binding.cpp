@@ -7,6 +7,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -111,26 +112,30 @@ template <typename P>
 P *ptr_as(const Tensor &t) { return static_cast<P *>(ptr(t)); }
 int64_t stride0(const Tensor &t) { return t.defined() ? t.stride(0) : 0; }
 
-// The stream to launch on: a handle, or None for the device's current one.  The caching allocator learns of a
-// stream other than that for what is allocated here.
+// The stream to launch on: a handle, or None for the device's current one.  While it lives a given stream is the current
+// one, so that what is allocated comes from that stream's memory: a block that the caller's stream has freed may still be in
+// use there.  The caller's stream, which will read the outputs, is noted for them.
 struct Stream {
     void *handle;
-    bool other;
     int dev;
-    Stream(PyObject *o, int dev_) : dev(dev_) {
-        other = o != Py_None;
-        handle = other ? PyLong_AsVoidPtr(o) : (void *)c10::cuda::getCurrentCUDAStream(dev).stream();
+    c10::cuda::CUDAStream caller;
+    c10::cuda::OptionalCUDAStreamGuard guard;
+    Stream(PyObject *o, int dev_) : dev(dev_), caller(c10::cuda::getCurrentCUDAStream(dev_)) {
+        handle = o != Py_None ? PyLong_AsVoidPtr(o) : (void *)caller.stream();
         if (PyErr_Occurred()) throw Raised();
+        if (handle != caller.stream()) guard.reset_stream(c10::cuda::getStreamFromExternal((cudaStream_t)handle, (c10::DeviceIndex)dev));
     }
     Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-        Tensor t = at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
-        used(t);
+        return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
+    }
+    Tensor output(at::IntArrayRef shape, at::ScalarType type) const {
+        Tensor t = empty(shape, type);
+        if (guard.current_stream() && t.numel() > 0) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), caller);
         return t;
     }
-    void used(const Tensor &t) const {
-        if (other && t.numel() > 0)
-            c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(),
-                                                          c10::cuda::getStreamFromExternal((cudaStream_t)handle, (c10::DeviceIndex)dev));
+    void used(const Tensor &t) const {                              // a tensor of the caller's that the call works in
+        if (guard.current_stream() && t.numel() > 0)
+            c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *guard.current_stream());
     }
 };
 
@@ -166,7 +171,7 @@ PyObject *step(PyObject *const *a) {
     if (idx.defined()) like("state_indices", idx, {n}, I32, dev, 1);
     else NEED(slots >= n, "the state pool has fewer slots than there are requests");
     const Stream st(a[11], dev);
-    Tensor y = st.empty(x.sizes(), x.scalar_type());
+    Tensor y = st.output(x.sizes(), x.scalar_type());
     const ssd_step_problem p{n, slots, H, P, G, N, state.stride(0), x.stride(0), dt.stride(0), stride0(z), B.stride(0), C.stride(0),
                              H * P, code(x), code(dt), code(state), 0};
     check((sel ? lib.selective_step : lib.step)(&p, ptr(state), ptr_as<int32_t>(idx), ptr(x), ptr(dt), ptr_as<float>(A), ptr(B), ptr(C),
@@ -202,7 +207,7 @@ PyObject *conv1d_prompt(PyObject *const *a) {
     }
     if (has.defined()) like("has_initial", has, {n}, U8 | BOOL, dev, 1);
     const Stream st(a[8], dev);
-    Tensor out = st.empty({Bt, L, Cn}, u.scalar_type());
+    Tensor out = st.output({Bt, L, Cn}, u.scalar_type());
     const ssd_conv_problem p{Bt, L, Cn, K, cu.defined() ? n : 0, code(u), a[7] == Py_True, 0, 0};
     check(lib.conv1d_prompt(&p, ptr(u), u.stride(0), u.stride(1), ptr_as<float>(w), ptr_as<float>(bias), ptr_as<int32_t>(cu), ptr(win),
                             win.size(0), win.stride(0), ptr_as<int32_t>(idx), ptr_as<uint8_t>(has), ptr(out), L * Cn, Cn, st.handle),
@@ -217,7 +222,7 @@ PyObject *conv1d_step(PyObject *const *a) {
     const int dev = lead("xbc", u, 2);
     const int64_t n = u.size(0), Cn = u.size(1), K = check_conv(u, w, bias, win, idx, n, dev);
     const Stream st(a[6], dev);
-    Tensor out = st.empty({n, Cn}, u.scalar_type());
+    Tensor out = st.output({n, Cn}, u.scalar_type());
     if (n > 0) {
         const ssd_conv_problem p{n, 1, Cn, K, 0, code(u), a[5] == Py_True, 0, 0};
         check(lib.conv1d_step(&p, ptr(u), u.stride(0), ptr_as<float>(w), ptr_as<float>(bias), ptr(win), win.size(0), win.stride(0),
@@ -322,17 +327,17 @@ PyObject *selective_fwd(PyObject *const *a) {
     const bool want_final = a[10] == Py_True, keep = a[12] == Py_True;
     const long sd = PyLong_AsLong(a[11]);
     const Stream st(a[13], s.dev);
-    Tensor y = st.empty({s.Bt, s.L, s.Dm}, x.scalar_type()), final, kept;
+    Tensor y = st.output({s.Bt, s.L, s.Dm}, x.scalar_type()), final, kept;
     s.f.y = desc(y, 3);
     if (want_final) {
         const bool bf16 = sd < 0 ? init.defined() && init.scalar_type() == at::kBFloat16 : sd == SSD_BF16;
-        final = st.empty({s.S, s.Dm, s.N}, bf16 ? at::kBFloat16 : at::kFloat);
+        final = st.output({s.S, s.Dm, s.N}, bf16 ? at::kBFloat16 : at::kFloat);
         s.f.final_states = desc(final, 3);
     }
     if (keep) {
         size_t n = 0;
         check(lib.chunk_states_size(&s.p, &n), "ssd_selective_chunk_states_size");
-        kept = st.empty({(int64_t)n}, at::kByte);
+        kept = st.output({(int64_t)n}, at::kByte);
         s.f.chunk_states = kept.data_ptr();
     }
     size_t n = 0;
@@ -374,7 +379,7 @@ PyObject *selective_bwd(PyObject *const *a) {
     if (!g) throw Raised();
     try {
         auto out = [&](const char *name, ssd_tensor &d, at::IntArrayRef shape, at::ScalarType type) {
-            Tensor v = st.empty(shape, type);
+            Tensor v = st.output(shape, type);
             d = desc(v, (int)v.dim());
             PyObject *o = wrap(v);
             const int rc = o ? PyDict_SetItemString(g, name, o) : -1;

@@ -1,0 +1,100 @@
+"""Calls on a stream of the caller's: their outputs come from that stream's memory, never from a block that work still
+pending on another stream may be using, and stay the caller's as long as its own stream reads them."""
+import pytest
+import torch
+
+from state_space_model_scan_gb300 import api
+
+pytestmark = pytest.mark.gpu
+N16 = torch.bfloat16
+
+
+def randn(*s, dtype=torch.float32, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(sum(s))
+    return (torch.randn(*s, generator=g, device="cuda") * scale).to(dtype)
+
+
+def scan_args(L=512, Dm=1024, N=16):
+    return (randn(1, L, Dm, dtype=N16), randn(1, L, Dm, dtype=N16), -torch.exp(randn(Dm, N, scale=0.1)), randn(1, L, 1, N, dtype=N16),
+            randn(1, L, 1, N, dtype=N16))
+
+
+def new_calls():
+    """Name, call(stream) -> tensors.  Calls that update something in place give the same output every time: states that
+    a step of 50 forgets, windows that the taps do not see."""
+    a = scan_args()
+    dy = randn(1, 512, 1024, dtype=N16)
+    n, H, P, N = 256, 40, 64, 16
+    pool = torch.zeros(n, H, P, N, device="cuda")
+    step = (randn(n, H, P, dtype=N16), 50 + randn(n, H), -1 - randn(H).abs(), randn(n, 1, N, dtype=N16), randn(n, 1, N, dtype=N16))
+    pool2 = torch.zeros(n, 4096, N, device="cuda")
+    step2 = (randn(n, 4096, dtype=N16), (50 + randn(n, 4096)).to(N16), -1 - randn(4096, N).abs(), step[3], step[4])
+    u, win = randn(1, 1024, 1024, dtype=N16), torch.zeros(1, 3, 1024, dtype=N16, device="cuda")
+    u1, win1 = randn(512, 2048, dtype=N16), torch.zeros(512, 3, 2048, dtype=N16, device="cuda")
+    w, w1 = randn(1024, 4), randn(2048, 4)
+    w[:, :3] = w1[:, :3] = 0
+    return {
+        "selective_scan_forward": lambda s: api.selective_scan_forward(*a, keep_chunk_states=True, stream=s),
+        "selective_scan_backward": lambda s: tuple(api.selective_scan_backward(*a, dy, stream=s).values()),
+        "ssd_step": lambda s: (api.ssd_step(pool, *step, stream=s),),
+        "selective_scan_step": lambda s: (api.selective_scan_step(pool2, *step2, stream=s),),
+        "conv1d_prompt": lambda s: (api.conv1d_prompt(u, w, None, win, stream=s),),
+        "conv1d_step": lambda s: (api.conv1d_step(u1, w1, None, win1, stream=s),),
+    }
+
+
+NEW = ["selective_scan_forward", "selective_scan_backward", "ssd_step", "selective_scan_step", "conv1d_prompt", "conv1d_step"]
+
+
+def spans(ts):
+    return [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in ts]
+
+
+def apart(a, b):
+    return all(x1 <= y0 or y1 <= x0 for x0, x1 in a for y0, y1 in b)
+
+
+def check_outputs(call):
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    want = [t.clone() for t in call(None)]
+    # blocks that the current stream has freed, of the outputs' very sizes
+    mine = [torch.empty_like(t) for t in want]
+    freed = spans(mine)
+    torch.cuda.synchronize()
+    del mine
+    got = call(side)
+    assert apart(freed, spans(got))
+    torch.cuda.current_stream().wait_stream(side)
+    for t, v in zip(got, want):
+        assert torch.equal(t, v)
+    # given back while the current stream still has to read them, they are not handed out for the next call
+    torch.cuda.synchronize()
+    del t, v
+    held = spans(got)
+    torch.cuda._sleep(200_000_000)                                 # a tenth of a second of the current stream
+    keep = [g.clone() for g in got]
+    del got
+    again = call(side)
+    assert apart(held, spans(again))
+    torch.cuda.synchronize()
+    for t, v in zip(keep, want):
+        assert torch.equal(t, v)
+
+
+@pytest.mark.parametrize("name", NEW)
+def test_outputs_come_from_the_streams_own_memory(name):
+    check_outputs(new_calls()[name])
+
+
+@pytest.mark.parametrize("name", NEW)
+def test_default_stream_given_inside_another(name):
+    call = new_calls()[name]
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = call(torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    for t, v in zip(got, want):
+        assert torch.equal(t, v)
