@@ -112,15 +112,17 @@ template <typename P>
 P *ptr_as(const Tensor &t) { return static_cast<P *>(ptr(t)); }
 int64_t stride0(const Tensor &t) { return t.defined() ? t.stride(0) : 0; }
 
-// The stream to launch on: a handle, or None for the device's current one.  While it lives a given stream is the current
-// one, so that what is allocated comes from that stream's memory: a block that the caller's stream has freed may still be in
+// The stream to launch on: a handle, or None for the device's current one.  While it lives the tensors' device is the current
+// one (a null handle means the current device's default stream, and the library asks for the current device), and a given
+// stream too, so that what is allocated comes from that stream's memory: a block that the caller's stream has freed may still be in
 // use there.  The caller's stream, which will read the outputs, is noted for them.
 struct Stream {
     void *handle;
     int dev;
+    c10::cuda::CUDAGuard device;
     c10::cuda::CUDAStream caller;
     c10::cuda::OptionalCUDAStreamGuard guard;
-    Stream(PyObject *o, int dev_) : dev(dev_), caller(c10::cuda::getCurrentCUDAStream(dev_)) {
+    Stream(PyObject *o, int dev_) : dev(dev_), device((c10::DeviceIndex)dev_), caller(c10::cuda::getCurrentCUDAStream(dev_)) {
         handle = o != Py_None ? PyLong_AsVoidPtr(o) : (void *)caller.stream();
         if (PyErr_Occurred()) throw Raised();
         if (handle != caller.stream()) guard.reset_stream(c10::cuda::getStreamFromExternal((cudaStream_t)handle, (c10::DeviceIndex)dev));
@@ -404,7 +406,7 @@ PyObject *selective_bwd(PyObject *const *a) {
             const bool ok = THPVariable_Check(o);
             if (ok) ws = THPVariable_Unpack(o);
             Py_DECREF(o);
-            NEED(ok && ws.is_cuda() && ws.is_contiguous(), "workspace.get(bytes) gives a contiguous tensor on the GPU");
+            NEED(ok && ws.is_cuda() && ws.get_device() == s.dev && ws.is_contiguous(), "workspace.get(bytes) gives a contiguous tensor on GPU %d", s.dev);
             st.used(ws);
         } else {
             ws = st.empty({(int64_t)(n < 256 ? 256 : n)}, at::kByte);
