@@ -4,9 +4,32 @@ They allocate outputs and workspace with torch, marshal pointers/strides/stream
 into the ABI structs and raise on a non-OK status.  All arithmetic runs in
 libssd.so.
 """
+import functools
+import inspect
+
 import torch
 
 from . import _lib
+
+
+def _on_stream(f):
+    """f with a ``stream`` argument: what it allocates comes from that stream's memory (a block that the caller's stream has
+    freed may still be in use there), and the caller's stream, which will read the outputs, is noted for them."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = kw.get("stream") if len(args) <= at else args[at]
+        if stream is None:
+            return f(*args, **kw)
+        caller = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            out = f(*args, **kw)
+        for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+            if t is not None and t.numel() > 0:
+                t.record_stream(caller)
+        return out
+    return call
 
 
 class Workspace:
@@ -27,6 +50,7 @@ def _nseqs(x, cu_seqlens):
     return (cu_seqlens.numel() - 1) if cu_seqlens is not None else x.shape[0]
 
 
+@_on_stream
 def ssd_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, initial_states=None, cu_seqlens=None,
                 chunk_size=128, return_final_states=True, algo="auto", seg_chunks=0, workspace=None,
                 y=None, final_states=None, stream=None, keep_chunk_states=False, chunk_states=None,
@@ -68,6 +92,7 @@ def ssd_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, initial_states=Non
     return y, final_states
 
 
+@_on_stream
 def ssd_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, initial_states=None, dfinal_states=None,
                  cu_seqlens=None, chunk_size=128, algo="auto", seg_chunks=0, bwd_heads=0, workspace=None,
                  stream=None, chunk_states=None):
@@ -111,6 +136,7 @@ def _rows(t, width):
     return t.reshape(-1, width)
 
 
+@_on_stream
 def gated_norm_forward(y, weight, group_size, z=None, eps=1e-5, layer_norm=False, gate_after=False, stream=None):
     """out, rstd = the gated normalisation of y over groups of `group_size` features (see
     include/ssd.h, ssd_gated_norm_fwd): RMS (default) or LayerNorm (layer_norm=True, no bias)
@@ -126,6 +152,7 @@ def gated_norm_forward(y, weight, group_size, z=None, eps=1e-5, layer_norm=False
     return out.reshape(y.shape), rstd
 
 
+@_on_stream
 def gated_norm_backward(y, weight, rstd, dout, group_size, z=None, eps=1e-5, layer_norm=False, gate_after=False,
                         stream=None):
     """dy, dz (None without z), dweight: gradients of sum(dout * out) (same options as the forward)."""
@@ -141,6 +168,7 @@ def gated_norm_backward(y, weight, rstd, dout, group_size, z=None, eps=1e-5, lay
     return dy.reshape(y.shape), (dz.reshape(z.shape) if dz is not None else None), dw
 
 
+@_on_stream
 def conv1d_forward(xbc, weight, bias=None, cu_seqlens=None, silu=True, stream=None):
     """Causal depthwise conv1d (+ SiLU) over the sequence axis of xbc [batch, seqlen, channels]
     (see include/ssd.h, ssd_conv1d_fwd); packed sequences (cu_seqlens, batch 1) never mix."""
@@ -152,6 +180,7 @@ def conv1d_forward(xbc, weight, bias=None, cu_seqlens=None, silu=True, stream=No
     return out
 
 
+@_on_stream
 def conv1d_backward(xbc, weight, dout, bias=None, cu_seqlens=None, silu=True, stream=None):
     """dxbc, dweight, dbias (None without bias): gradients of sum(dout * conv1d_forward(...))."""
     Bsz, L, Cn = xbc.shape
@@ -207,6 +236,7 @@ class SSDFunction(torch.autograd.Function):
                 g.get("dinitial_states"), None, None)
 
 
+@_on_stream
 def complex_ssd_forward(x, A, B, C, dt, initial_states=None, chunk_size=64, return_imag=False,
                         return_final=False, stream=None):
     """Complex-A SSD scan (Mamba-3-Lite): h_t = exp(softplus(dt_t) A) h_{t-1} + x_t (outer) B_t,

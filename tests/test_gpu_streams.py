@@ -46,6 +46,30 @@ def new_calls():
 NEW = ["selective_scan_forward", "selective_scan_backward", "ssd_step", "selective_scan_step", "conv1d_prompt", "conv1d_step"]
 
 
+def scan_calls():
+    """The same for the calls of the per-head scan, the normalisation, the plain convolution and the complex scan."""
+    L, H, P, G, N = 512, 16, 64, 1, 128
+    a = (randn(1, L, H, P, dtype=N16), randn(1, L, H), -torch.exp(randn(H)), randn(1, L, G, N, dtype=N16), randn(1, L, G, N, dtype=N16))
+    y, nw = randn(512, 2048, dtype=N16), randn(2048)
+    _, rstd = api.gated_norm_forward(y, nw, 1024, z=y)
+    u, w = randn(1, 1024, 1024, dtype=N16), randn(1024, 4)
+    c = [randn(1, 256, 8, 64, 2).view(1, 256, 8, 64, 2) for _ in range(3)]
+    c = [torch.view_as_complex(t) for t in c]
+    cA, cdt = torch.complex(-torch.exp(randn(8)), randn(8)), randn(1, 256, 8)
+    return {
+        "ssd_forward": lambda s: api.ssd_forward(*a, stream=s),
+        "ssd_backward": lambda s: tuple(api.ssd_backward(*a, a[0], stream=s).values()),
+        "gated_norm_forward": lambda s: api.gated_norm_forward(y, nw, 1024, z=y, stream=s),
+        "gated_norm_backward": lambda s: api.gated_norm_backward(y, nw, rstd, y, 1024, z=y, stream=s),
+        "conv1d_forward": lambda s: (api.conv1d_forward(u, w, None, None, True, s),),
+        "conv1d_backward": lambda s: api.conv1d_backward(u, w, u, stream=s)[:2],
+        "complex_ssd_forward": lambda s: (api.complex_ssd_forward(c[0], cA, c[1], c[2], cdt, stream=s),),
+    }
+
+
+SCAN = ["ssd_forward", "ssd_backward", "gated_norm_forward", "gated_norm_backward", "conv1d_forward", "conv1d_backward", "complex_ssd_forward"]
+
+
 def spans(ts):
     return [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in ts]
 
@@ -98,3 +122,8 @@ def test_default_stream_given_inside_another(name):
     torch.cuda.synchronize()
     for t, v in zip(got, want):
         assert torch.equal(t, v)
+
+
+@pytest.mark.parametrize("name", SCAN)
+def test_scan_outputs_come_from_the_streams_own_memory(name):
+    check_outputs(scan_calls()[name])
