@@ -13,12 +13,18 @@ from . import _lib
 
 
 def _on_stream(f):
-    """f with a ``stream`` argument: what it allocates comes from that stream's memory (a block that the caller's stream has
-    freed may still be in use there), and the caller's stream, which will read the outputs, is noted for them."""
-    at = list(inspect.signature(f).parameters).index("stream")
+    """f with a ``stream`` argument and a tensor first.  The tensor's GPU is the current one meanwhile (the library launches
+    there, and a stream of None is that GPU's current one).  What f allocates comes from the given stream's memory (a block that
+    the caller's stream has freed may still be in use there), and the caller's stream, which will read the outputs, is noted for them."""
+    params = list(inspect.signature(f).parameters)
+    first, at = params[0], params.index("stream")
 
     @functools.wraps(f)
     def call(*args, **kw):
+        dev = (args[0] if args else kw[first]).device
+        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return call(*args, **kw)
         stream = kw.get("stream") if len(args) <= at else args[at]
         if stream is None:
             return f(*args, **kw)
