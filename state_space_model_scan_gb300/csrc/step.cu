@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(ST_NT, sizeof(T) == 2 && V * RU == 16 ? 12 : 1
 #pragma unroll
         for (int u = 0; u < RU; ++u) h[u][k].load(st[u] + n);
         Av[k].load(a.A + c * N + n);
-        const T *Bp = static_cast<const T *>(a.B) + b0 * a.bs + seg * N + n, *Cp = static_cast<const T *>(a.C) + b0 * a.cs + seg * N + n;
+        const int64_t bc = (int64_t)seg * N + n;
+        const T *Bp = static_cast<const T *>(a.B) + b0 * a.bs + bc, *Cp = static_cast<const T *>(a.C) + b0 * a.cs + bc;
 #pragma unroll
         for (int u = 0; u < RU; ++u) {
             Bv[u][k].load(Bp);

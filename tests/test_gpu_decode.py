@@ -399,3 +399,19 @@ def test_conv_silu_far_below_zero(dtype):
     close(du[0], odu, "du")
     close(dw, odw, "dw")
     close(db, odb, "db")
+
+
+def test_selective_step_past_32_bits():
+    """B and C of 2^23 + 8 groups of 256 states: the last groups' elements lie past 2^31 (22 GB in all)."""
+    Dm, N = (1 << 23) + 8, 256
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_(generator=g)  # noqa: E731
+    state, B, C = r(1, Dm, N), r(1, Dm, N), r(1, Dm, N)
+    A = torch.empty(Dm, N, device="cuda").uniform_(-2, -0.5, generator=g)
+    x, dt = r(1, Dm), r(1, Dm)
+    parts = (slice(0, 4), slice((1 << 23) - 4, (1 << 23) + 8))
+    before = [h(state[0, p]) for p in parts]
+    y = selective_scan_step(state, x, dt, A, B, C)
+    for p, old in zip(parts, before):
+        new, want = osel.step(old, h(x[0, p]), h(dt[0, p]), h(A[p]), h(B[0, p]), h(C[0, p]))
+        assert rel_l2(h(y[0, p]), want) <= TOL[torch.bfloat16] and rel_l2(h(state[0, p]), new) <= TOL[torch.bfloat16]
