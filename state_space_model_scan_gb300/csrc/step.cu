@@ -295,19 +295,25 @@ void lanes(StepArgs &a, int V) {
     a.lpr = 1;
     while (a.lpr < 32 && a.lpr * V < a.N) a.lpr <<= 1;
 }
+// (a grid has at most 2^31 - 1 blocks)
+template <typename K>
+cudaError_t launch_blocks(K kernel, int64_t blocks, cudaStream_t st, const StepArgs &a) {
+    if (blocks > ((int64_t)1 << 31) - 1) return cudaErrorInvalidConfiguration;
+    return launch_early(kernel, (unsigned)blocks, ST_NT, 0, st, a);
+}
 template <typename T, typename ST, int V, int NV, int RU>
 cudaError_t launch_head(StepArgs a, cudaStream_t st) {
     lanes(a, V);
     const int per = (ST_NT / 32) * (32 / a.lpr) * RU;
     a.nrb = (a.rows + per - 1) / per;
-    return launch_early(k_step_head<T, ST, V, NV, RU>, (unsigned)((int64_t)a.batch * a.segs * a.nrb), ST_NT, 0, st, a);
+    return launch_blocks(k_step_head<T, ST, V, NV, RU>, (int64_t)a.batch * a.segs * a.nrb, st, a);
 }
 template <typename T, typename ST, int V, int NV, int RU>
 cudaError_t launch_channel(StepArgs a, cudaStream_t st) {
     lanes(a, V);
     const int per = (ST_NT / 32) * (32 / a.lpr), nb = (a.batch + RU - 1) / RU;
     a.nrb = (a.rows + per - 1) / per;
-    return launch_early(k_step_channel<T, ST, V, NV, RU>, (unsigned)((int64_t)nb * a.segs * a.nrb), ST_NT, 0, st, a);
+    return launch_blocks(k_step_channel<T, ST, V, NV, RU>, (int64_t)nb * a.segs * a.nrb, st, a);
 }
 
 // Rows or requests in flight per thread: measured at 256 requests x 80 heads x 64 x 128, bf16 states, 4 / 8 /
@@ -357,7 +363,6 @@ ssd_status step(const ssd_step_problem *p, bool selective, void *state, const in
         p->nheads * p->headdim > ((int64_t)1 << 24) || p->batch > ((int64_t)1 << 20))
         return SSD_ERR_UNSUPPORTED;
     const int64_t rows = p->nheads * p->headdim, segs = selective ? p->ngroups : p->nheads, spr = rows / segs;
-    if (p->batch * segs * ((spr + 3) / 4) > ((int64_t)1 << 31) - 1) return SSD_ERR_UNSUPPORTED;
     if (p->batch == 0) return SSD_OK;
     if (!x || !dt || !A || !B || !C || !y || (p->nslots > 0 && !state)) return SSD_ERR_INVALID_ARGUMENT;
     const int64_t bc = p->ngroups * p->dstate, nd = selective ? rows : p->nheads;
@@ -378,8 +383,8 @@ ssd_status step(const ssd_step_problem *p, bool selective, void *state, const in
     a.batch = (int)p->batch; a.segs = (int)segs; a.rows = (int)spr; a.spg = (int)(segs / p->ngroups); a.N = (int)p->dstate;
     a.dt_f32 = p->dt_dtype == SSD_F32;
     const bool bf16 = p->dtype == SSD_BF16, sb = p->state_dtype == SSD_BF16;
-    return (selective ? pick_types<true>(a, bf16, sb, st) : pick_types<false>(a, bf16, sb, st)) == cudaSuccess ? SSD_OK
-                                                                                                            : SSD_ERR_CUDA;
+    const cudaError_t err = selective ? pick_types<true>(a, bf16, sb, st) : pick_types<false>(a, bf16, sb, st);
+    return err == cudaSuccess ? SSD_OK : err == cudaErrorInvalidConfiguration ? SSD_ERR_UNSUPPORTED : SSD_ERR_CUDA;
 }
 
 }  // namespace

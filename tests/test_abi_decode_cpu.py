@@ -206,3 +206,14 @@ def test_snapshot_refusals(m, k, code):
     assert m.load().ssd_snapshot_store(ctypes.byref(q), None, None, D, D, None, None) == 1
     assert m.load().ssd_snapshot_store(ctypes.byref(q), at(2), None, D, D, None, None) == 3
     assert m.load().ssd_snapshot_load(ctypes.byref(q), D, at(2), None, D, None, None) == 3
+
+
+def test_step_too_many_blocks(m):
+    """More blocks than a grid can have (rows of 33 states, two to a block): refused before the launch."""
+    k = dict(batch=1 << 20, nheads=1536, headdim=4, ngroups=1, dstate=33, slot_stride=1 << 30, x_stride=6144, dt_stride=1536,
+             z_stride=6144, b_stride=33, c_stride=33, y_stride=6144)
+    p = step_problem(m, **k)
+    f, g = m.load().ssd_step, m.load().ssd_selective_step
+    assert f(ctypes.byref(p), D, None, D, D, D, D, D, None, D, None, D, None) == 2
+    p = step_problem(m, **dict(k, nheads=6144, headdim=1, dt_stride=6144))
+    assert g(ctypes.byref(p), D, None, D, D, D, D, D, None, D, None, D, None) == 2
