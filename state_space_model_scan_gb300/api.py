@@ -279,6 +279,7 @@ def complex_ssd_forward(x, A, B, C, dt, initial_states=None, chunk_size=64, retu
 # (csrc/binding.cpp): ValueError for tensors that do not fit together, SSDError for what the
 # library refuses.  stream: launch there instead of on the current stream; the caller orders the two around the call.
 # The outputs are then that stream's memory, and may be freed while the caller's current stream still reads them.
+# Outputs carry no gradient (SelectiveScanFunction's do); what a call updates in place counts as changed for autograd.
 def _handle(stream):
     return None if stream is None else stream.cuda_stream
 

@@ -141,6 +141,11 @@ struct Stream {
     }
 };
 
+// Tells autograd that a call has written t, as torch's own operations in place do (an inference tensor is not watched).
+void written(const Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject *wrap(const Tensor &t) { return THPVariable_Wrap(t); }
 
 // step(selective, state, x, dt, A, B, C, D, z, dt_bias, state_indices, stream)
@@ -179,6 +184,7 @@ PyObject *step(PyObject *const *a) {
     check((sel ? lib.selective_step : lib.step)(&p, ptr(state), ptr_as<int32_t>(idx), ptr(x), ptr(dt), ptr_as<float>(A), ptr(B), ptr(C),
                                                 ptr_as<float>(D), ptr(z), ptr_as<float>(bias), ptr(y), st.handle),
           sel ? "ssd_selective_step" : "ssd_step");
+    written(state);
     return wrap(y);
 }
 
@@ -214,6 +220,7 @@ PyObject *conv1d_prompt(PyObject *const *a) {
     check(lib.conv1d_prompt(&p, ptr(u), u.stride(0), u.stride(1), ptr_as<float>(w), ptr_as<float>(bias), ptr_as<int32_t>(cu), ptr(win),
                             win.size(0), win.stride(0), ptr_as<int32_t>(idx), ptr_as<uint8_t>(has), ptr(out), L * Cn, Cn, st.handle),
           "ssd_conv1d_prompt");
+    written(win);
     return wrap(out);
 }
 
@@ -230,6 +237,7 @@ PyObject *conv1d_step(PyObject *const *a) {
         check(lib.conv1d_step(&p, ptr(u), u.stride(0), ptr_as<float>(w), ptr_as<float>(bias), ptr(win), win.size(0), win.stride(0),
                               ptr_as<int32_t>(idx), ptr(out), Cn, st.handle),
               "ssd_conv1d_step");
+        written(win);
     }
     return wrap(out);
 }
@@ -260,12 +268,16 @@ PyObject *snapshot(PyObject *const *a) {
     else NEED(snaps.size(0) >= n, "there are fewer snapshots than states");
     const Stream st(a[6], dev);
     const ssd_snapshot_problem p{n, rows, n1, states.size(0), snaps.size(0), states.stride(0), code(states), 0};
-    if (store)
+    if (store) {
         check(lib.snapshot_store(&p, ptr(states), ptr_as<int32_t>(idx), ptr_as<int8_t>(snaps), ptr_as<float>(scales), ptr_as<int32_t>(slots), st.handle),
               "ssd_snapshot_store");
-    else
+        written(snaps);
+        written(scales);
+    } else {
         check(lib.snapshot_load(&p, ptr_as<int8_t>(snaps), ptr_as<float>(scales), ptr_as<int32_t>(slots), ptr(states), ptr_as<int32_t>(idx), st.handle),
               "ssd_snapshot_load");
+        written(states);
+    }
     Py_RETURN_NONE;
 }
 

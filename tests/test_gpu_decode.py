@@ -3,6 +3,8 @@ snapshots, against the float64 oracle; prompts in pieces and tokens one by one a
 
 Tolerances (relative 2-norm): bf16 results are rounded once, at most 2^-9: 2^-8 allowed.  fp32 steps take a dozen
 operations with errors near 2^-22 each: 4e-6 allowed; over a sequence, 5e-5 as for the scan."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -415,3 +417,54 @@ def test_selective_step_past_32_bits():
     for p, old in zip(parts, before):
         new, want = osel.step(old, h(x[0, p]), h(dt[0, p]), h(A[p]), h(B[0, p]), h(C[0, p]))
         assert rel_l2(h(y[0, p]), want) <= TOL[torch.bfloat16] and rel_l2(h(state[0, p]), new) <= TOL[torch.bfloat16]
+
+
+def test_step_on_an_empty_pool():
+    """No slots: every request is padding.  Through C a single request's rows have no stride to speak of."""
+    i = {k: v.cuda() for k, v in step_inputs(1, 4, 8, 2, 16).items()}
+    for stride in (0, 32, 40):
+        y = torch.full((1, 32), 7.0, device="cuda")
+        p = _lib.StepProblem(1, 0, 4, 8, 2, 16, 0, stride, 0, 0, 0, 0, stride, 0, 0, 0, 0)
+        a = [i[k].data_ptr() for k in ("state", "idx", "x", "dt", "A", "B", "C")]
+        assert _lib.load().ssd_step(ctypes.byref(p), *a, None, None, None, y.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+        assert (y == 0).all()
+    y = ssd_step(i["state"][:0], *(i[k] for k in ("x", "dt", "A", "B", "C")), state_indices=i["idx"])
+    assert y.shape == i["x"].shape and (y == 0).all()
+
+
+def in_place_calls():
+    """(name, tensors that the call writes, call)"""
+    i = {k: v.cuda() for k, v in step_inputs(2, 4, 8, 2, 16).items()}
+    j = {k: v.cuda() for k, v in step_inputs(2, 4, 8, 2, 16, selective=True).items()}
+    u, w, b, win = (t.cuda() for t in conv_inputs(16, 4, "f32", 2, (2, 5)))
+    st = i["state"].clone()
+    q, sc = torch.zeros(st.shape, dtype=torch.int8, device="cuda"), torch.zeros(st.shape[:-1], device="cuda")
+    a = ("x", "dt", "A", "B", "C")
+    return [("ssd_step", [i["state"]], lambda: ssd_step(i["state"], *(i[k] for k in a), state_indices=i["idx"])),
+            ("selective_scan_step", [j["state"]], lambda: selective_scan_step(j["state"], *(j[k] for k in a), state_indices=j["idx"])),
+            ("conv1d_prompt", [win], lambda: conv1d_prompt(u, w, b, win)),
+            ("conv1d_step", [win], lambda: conv1d_step(u[:, 0].contiguous(), w, b, win)),
+            ("snapshot_store", [q, sc], lambda: snapshot_store(st, q, sc)),
+            ("snapshot_load", [st], lambda: snapshot_load(q, sc, st))]
+
+
+@pytest.mark.parametrize("k", range(6))
+def test_updates_in_place_are_seen_by_autograd(k):
+    """What a call writes counts as changed: a graph that saved it for its backward says so."""
+    name, written, call = in_place_calls()[k]
+    before = [t._version for t in written]
+    leaf = torch.ones((), device="cuda", requires_grad=True)
+    graph = (leaf * written[-1]).sum()
+    call()
+    assert all(t._version > v for t, v in zip(written, before)), name
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        graph.backward()
+
+
+def test_pools_made_in_inference_mode():
+    for k in range(6):
+        with torch.inference_mode():
+            _, written, call = in_place_calls()[k]
+        call()
+        with torch.inference_mode():
+            call()
