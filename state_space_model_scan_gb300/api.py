@@ -313,14 +313,22 @@ def selective_scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, in
 
 
 class SelectiveScanFunction(torch.autograd.Function):
-    """Autograd wrapper of the selective scan; the forward keeps its chunk states for the backward, and an output that
-    nothing was computed from costs no gradient of zeros.  A second differentiation is refused."""
+    """Autograd wrapper of the selective scan.  Where gradients are asked for, the forward keeps its chunk states for the backward
+    (4 bytes a token, channel and dstate / 16, dstate padded as in ssd_selective_chunk_states_size; with keep_chunk_states=False the
+    backward computes them again).  An output that nothing was computed from costs no gradient of zeros.  A second
+    differentiation is refused."""
+
+    @classmethod
+    def apply(cls, x, dt, A, B, C, D=None, z=None, dt_bias=None, initial_states=None, cu_seqlens=None, keep_chunk_states=True):
+        inputs = (x, dt, A, B, C, D, z, dt_bias, initial_states)
+        keep = keep_chunk_states and torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)
+        return super().apply(*inputs, cu_seqlens, keep)
 
     @staticmethod
-    def forward(ctx, x, dt, A, B, C, D=None, z=None, dt_bias=None, initial_states=None, cu_seqlens=None):
-        y, fin, kept = selective_scan_forward(x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, initial_states=initial_states,
-                                              cu_seqlens=cu_seqlens, keep_chunk_states=True)
-        ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens, kept)
+    def forward(ctx, x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens, keep):
+        y, fin, *kept = selective_scan_forward(x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, initial_states=initial_states,
+                                               cu_seqlens=cu_seqlens, keep_chunk_states=keep)
+        ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, initial_states, cu_seqlens, kept[0] if keep else None)
         ctx.set_materialize_grads(False)
         return y, fin
 
@@ -333,7 +341,7 @@ class SelectiveScanFunction(torch.autograd.Function):
                                     dfinal_states=None if dfin is None else dfin.contiguous(), cu_seqlens=cu,
                                     chunk_states=kept)
         return (g["dx"], g["ddt"], g["dA"], g["dB"], g["dC"], g.get("dD"), g.get("dz"), g.get("ddt_bias"),
-                g.get("dinitial_states"), None)
+                g.get("dinitial_states"), None, None)
 
 
 def ssd_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, state_indices=None, stream=None):

@@ -326,3 +326,30 @@ def test_refusals():
     with pytest.raises(_lib.SSDError) as e:
         selective_scan_forward(j["x"], j["dt"], j["A"], j["B"], j["C"])
     assert e.value.code == 2
+
+
+def test_autograd_keeps_states_for_gradients_only(monkeypatch):
+    """Chunk states are kept where a backward can follow, and not where the caller would rather compute them again."""
+    from state_space_model_scan_gb300 import api
+    d = dev(make(Bt=2, L=50, Dm=33, dtype="f32"))
+    names = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "init")
+    args = [d[k] for k in names]
+    forward, kept = api.selective_scan_forward, []
+
+    def spy(*a, keep_chunk_states=False, **k):
+        kept.append(keep_chunk_states)
+        return forward(*a, keep_chunk_states=keep_chunk_states, **k)
+    monkeypatch.setattr(api, "selective_scan_forward", spy)
+    want, _ = SelectiveScanFunction.apply(*args, None)
+    assert kept.pop() is False and not want.requires_grad
+    leaves = [t.clone().requires_grad_() for t in args]
+    with torch.no_grad():
+        y, _ = SelectiveScanFunction.apply(*leaves, None)
+    assert kept.pop() is False and not y.requires_grad and torch.equal(y, want)
+    grads = []
+    for k in (True, False):
+        y, fin = SelectiveScanFunction.apply(*leaves, keep_chunk_states=k)
+        assert kept.pop() is k
+        grads.append(torch.autograd.grad((y * d["dy"]).sum() + (fin * d["dfinal"]).sum(), leaves))
+    for a, b in zip(*grads):
+        assert torch.equal(a, b)
