@@ -49,15 +49,23 @@ def _compile(src, obj, extra):
 
 
 BINDING = os.path.join(PKG, "_binding.so")
+BUILT_FOR = os.path.join(BUILD_DIR, "_binding.txt")   # the torch and Python whose headers the binding was built with
 
 
 def build_binding(force: bool = False) -> str:
-    """Compile csrc/binding.cpp into the extension module _binding; returns its path."""
+    """Compile csrc/binding.cpp into the extension module _binding; returns its path.  Built again when a source is newer, or
+    for another torch or Python."""
     import torch
     src, deps = os.path.join(CSRC, "binding.cpp"), [os.path.join(ROOT, "include", "ssd.h")]
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(f) for f in [src] + deps):
-        return BINDING
     home = os.path.dirname(torch.__file__)
+    built_for = "torch %s (%s) in %s, python %s" % (torch.__version__, torch.version.git_version, home, sys.version)
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(f) for f in [src] + deps):
+        try:
+            with open(BUILT_FOR) as f:
+                if f.read() == built_for:
+                    return BINDING
+        except OSError:
+            pass
     inc = [sysconfig.get_paths()["include"], os.path.join(home, "include"),
            os.path.join(home, "include", "torch", "csrc", "api", "include"),
            os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
@@ -69,6 +77,9 @@ def build_binding(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("g++ failed for %s:\n%s\n%s" % (src, " ".join(cmd), r.stdout + r.stderr))
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(BUILT_FOR, "w") as f:
+        f.write(built_for)
     return BINDING
 
 
