@@ -468,3 +468,17 @@ def test_pools_made_in_inference_mode():
         call()
         with torch.inference_mode():
             call()
+
+
+@pytest.mark.parametrize("dtype,state_dtype", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("n,H,P,G,N", [(8, 3, 64, 1, 128), (9, 4, 33, 2, 64), (17, 2, 5, 1, 40), (33, 2, 64, 1, 16), (8, 2, 67, 2, 8),
+                                       (9, 3, 64, 3, 4), (8, 2, 130, 1, 256), (10, 2, 24, 2, 132)])
+def test_ssd_step_of_many_requests(n, H, P, G, N, dtype, state_dtype):
+    """Eight rows in flight a thread (from eight requests on): rows that fill no block, rows of fewer lanes than rows in
+    flight, padding requests."""
+    i = step_inputs(n, H, P, G, N, dtype, state_dtype, seed=N + n)
+    check_step(i, False)
+    i["idx"][2], i["idx"][n - 1] = -1, i["state"].shape[0]
+    y, _ = check_step(i, False)
+    assert y[2].abs().max() == 0 and y[n - 1].abs().max() == 0
+    check_step(i, False, ("z", "D"))

@@ -353,3 +353,101 @@ def test_autograd_keeps_states_for_gradients_only(monkeypatch):
         grads.append(torch.autograd.grad((y * d["dy"]).sum() + (fin * d["dfinal"]).sum(), leaves))
     for a, b in zip(*grads):
         assert torch.equal(a, b)
+
+
+def whole_case(dtype, N, packed, Dm):
+    """A batch with enough (sequence, channel) pairs for the form that does not split sequences over time: 16384, packed
+    65536.  Packed lengths: none, one, chunk and tile edges, one long."""
+    if not packed:
+        return make(Bt=17 if Dm > 512 else 33, L=45, Dm=Dm, N=N, G=1, dtype=dtype, seed=N)
+    lens = [0, 1, 2, 15, 16, 17, 31, 32, 33, 64, 0, 70, 3, 129]
+    lens += [1 + k % 5 for k in range((65536 + Dm - 1) // Dm - len(lens))]
+    return make(lens=lens, Dm=Dm, N=N, dtype=dtype, seed=N)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,Dm", [(16, 1000), (13, 1003), (32, 512), (29, 999), (64, 1000), (128, 1000), (128, 997)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_sequences_that_are_not_split(dtype, N, Dm, packed):
+    """Values, kept states, final states and the gradients that start from the kept states, or recompute them, in that form;
+    channels that are taken in fours and channels that are not.  Checked on some of the channels (B and C alone couple
+    them: all of dy's other channels are zero)."""
+    i = whole_case(dtype, N, packed, Dm)
+    cols = np.unique(np.concatenate([np.arange(3), np.linspace(5, Dm - 6, 9).astype(int), np.arange(Dm - 3, Dm)]))
+    off = torch.ones(Dm, dtype=torch.bool)
+    off[cols] = False
+    i["dy"][..., off] = 0
+    i["dfinal"][:, off] = 0
+    got, again = gpu(i), gpu(i, keep=False)
+    part = dict(i)
+    for k in ("x", "dt", "z", "dy"):
+        part[k] = i[k][..., cols]
+    for k in ("A", "D", "dt_bias"):
+        part[k] = i[k][cols]
+    for k in ("init", "dfinal"):
+        part[k] = i[k][:, cols]
+    want = oracle(part)
+    for k, v in got.items():
+        assert torch.isfinite(v).all(), k
+        assert torch.equal(v, again[k]), k
+        w = h(v)
+        if k in ("y", "dx", "ddt", "dz"):
+            w = w[..., cols]
+        elif k in ("dA", "dD", "ddt_bias"):
+            w = w[cols]
+        elif k in ("final", "dinitial_states"):
+            w = w[:, cols]
+        assert rel_l2(w, want[k]) <= TOL[v.dtype], (k, rel_l2(w, want[k]))
+
+
+@pytest.mark.parametrize("N,G", [(32, 1), (64, 1), (128, 1), (20, 2), (64, 2), (124, 2)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_large_states_in_wide_rows(N, G, dtype):
+    """Channels and states that allow four elements an access, at state sizes above 16."""
+    check(make(Bt=2, L=70, Dm=72, N=N, G=G, dtype=dtype, seed=N))
+
+
+def some_channels(i, cols, want_keys, got):
+    """got's values at these channels against the oracle's, which runs on them alone."""
+    part = dict(i)
+    for k in ("x", "dt", "z", "dy"):
+        part[k] = None if i[k] is None else i[k][..., cols]
+    for k in ("A", "D", "dt_bias"):
+        part[k] = None if i[k] is None else i[k][cols]
+    for k in ("init", "dfinal"):
+        part[k] = None if i[k] is None else i[k][:, cols]
+    want = oracle(part)
+    for k in want_keys:
+        v = got[k]
+        w = h(v)[..., cols] if k in ("y", "dx", "ddt", "dz") else h(v)[cols] if k in ("dA", "dD", "ddt_bias") else h(v)[:, cols]
+        assert torch.isfinite(v).all() and rel_l2(w, want[k]) <= TOL[v.dtype], (k, rel_l2(w, want[k]))
+
+
+@pytest.mark.parametrize("opt", [dict(z=False), dict(D=False, bias=False), dict(init=False), dict(state_dtype=torch.bfloat16),
+                                 dict(dt_dtype="f32"), dict(L=1), dict(L=200, Bt=9, Dm=1900)])
+@pytest.mark.parametrize("G", [1, 2])
+def test_options_where_sequences_are_not_split(opt, G):
+    """Absent inputs, types, groups whose channels are taken in fours (and, 501 of them, are not), one token, many tiles."""
+    i = make(**dict(dict(Bt=17, L=40, Dm=1002, G=G, dtype="bf16", seed=G), **opt))
+    got = gpu(i)
+    Dm = i["x"].shape[2]
+    cols = np.concatenate([np.arange(4), np.arange(Dm // G - 2, Dm // G), np.arange(Dm - 3, Dm)]) if G == 1 else None
+    keys = ["y", "final", "dx", "ddt", "dA"] + [k for k in ("dz", "dD", "ddt_bias", "dinitial_states") if k in got]
+    if G == 1:
+        some_channels(i, np.unique(cols), keys, got)
+    else:                                             # as many channels of each group
+        part = np.concatenate([g * (Dm // G) + np.r_[0:3, Dm // G - 3:Dm // G] for g in range(G)])
+        some_channels(i, part, keys, got)
+
+
+def test_poison_stays_in_its_sequence_where_they_are_not_split():
+    i = make(lens=[17, 3, 33] + [2] * 64, Dm=1000, dtype="bf16", seed=2)
+    clean = gpu(i)
+    for k in ("x", "B", "dt", "z", "dy"):
+        i[k][:, 20:53] = float("nan")
+    i["init"][2] = float("inf")
+    bad = gpu(i)
+    for k in ("y", "dx", "ddt", "dB", "dC", "dz"):
+        assert torch.equal(bad[k][:, :20], clean[k][:, :20]) and torch.equal(bad[k][:, 53:], clean[k][:, 53:]), k
+    keep = [s for s in range(67) if s != 2]
+    assert torch.equal(bad["final"][keep], clean["final"][keep]) and torch.isnan(bad["y"][:, 20:53]).all()
