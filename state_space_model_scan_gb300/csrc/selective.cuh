@@ -81,6 +81,12 @@ __device__ __forceinline__ f32x2 ex2x2(f32x2 v) {
     return pk2(ex2f(lo), ex2f(hi));
 }
 
+// A log2(e), kept finite: a rate of -inf (or near fp32's lowest value) forgets all of a state in any step, and a step of
+// 0, which stands for the tokens past a sequence's end, leaves it as it is instead of making it 0 x inf.
+__device__ __forceinline__ float sel_rate(float A) {
+    const float v = A * kLog2e;
+    return v < -3.402823466e38f ? -3.402823466e38f : v;
+}
 // softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1].  log1p(e) = 2 atanh(s) with
 // s = e / (2 + e) <= 1/3; 2 atanh(s) / s is a polynomial of degree 4 in s^2 there, fitted to
 // its smallest largest relative error, 4e-9.  No cancellation: small steps keep their relative accuracy.

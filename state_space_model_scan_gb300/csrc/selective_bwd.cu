@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int n = q * S + 2 * i + e;
-                v[e] = d + c < dend && n < N ? a.A[(int64_t)(d + c) * N + n] * kLog2e : 0.f;
+                v[e] = d + c < dend && n < N ? sel_rate(a.A[(int64_t)(d + c) * N + n]) : 0.f;
             }
             A2[c][i] = pk2(v[0], v[1]);
         }
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_rev(const SelArgs a, int 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const bool in = d0 + jc < dend && jn + e < N;
-            v[e] = in ? a.A[(int64_t)(d0 + jc) * N + jn + e] * kLog2e : 0.f;
+            v[e] = in ? sel_rate(a.A[(int64_t)(d0 + jc) * N + jn + e]) : 0.f;
             uv[e] = in && a.dfinal && !a.ends ? ld_st(a.dfinal, a.dfinal_bf16, ((int64_t)s * a.channels + d0 + jc) * N + jn + e) : 0.f;
         }
         jA[0] = pk2(v[0], v[1]); jA[1] = pk2(v[2], v[3]);
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(GNT, GOCC) k_sel_grad(const SelArgs a) {
         ulonglong2 hin = make_ulonglong2(0, 0), uin = hin;
         if (mine) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) Aq[e] = tid * 4 % NP + e < N ? m.rA[k][tid * 4 + e] * kLog2e : 0.f;
+            for (int e = 0; e < 4; ++e) Aq[e] = tid * 4 % NP + e < N ? sel_rate(m.rA[k][tid * 4 + e]) : 0.f;
             hin = *reinterpret_cast<const ulonglong2 *>(m.rh[k] + tid * 4);
             uin = *reinterpret_cast<const ulonglong2 *>(m.ru[k] + tid * 4);
         }

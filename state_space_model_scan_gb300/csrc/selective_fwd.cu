@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
             for (int e = 0; e < 2; ++e) {
                 const int n = q * S + 2 * i + e;
                 const bool in = d + c < dend && n < N;
-                v[e] = in ? a.A[(int64_t)(d + c) * N + n] * kLog2e : 0.f;
+                v[e] = in ? sel_rate(a.A[(int64_t)(d + c) * N + n]) : 0.f;
                 hv[e] = (TW == 1 && in && a.init) ? ld_st(a.init, a.init_bf16, ((int64_t)s * a.channels + d + c) * N + n) : 0.f;
             }
             A2[c][i] = pk2(v[0], v[1]);
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(F::NT, F::OCC) k_sel_fwd(const SelArgs a, int 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const bool in = d0 + jc < dend && jn + e < N;
-            v[e] = in ? a.A[(int64_t)(d0 + jc) * N + jn + e] * kLog2e : 0.f;
+            v[e] = in ? sel_rate(a.A[(int64_t)(d0 + jc) * N + jn + e]) : 0.f;
             hv[e] = in && a.init && !a.ends ? ld_st(a.init, a.init_bf16, ((int64_t)s * a.channels + d0 + jc) * N + jn + e) : 0.f;
         }
         jA[0] = pk2(v[0], v[1]); jA[1] = pk2(v[2], v[3]);

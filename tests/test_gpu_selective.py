@@ -451,3 +451,22 @@ def test_poison_stays_in_its_sequence_where_they_are_not_split():
         assert torch.equal(bad[k][:, :20], clean[k][:, :20]) and torch.equal(bad[k][:, 53:], clean[k][:, 53:]), k
     keep = [s for s in range(67) if s != 2]
     assert torch.equal(bad["final"][keep], clean["final"][keep]) and torch.isnan(bad["y"][:, 20:53]).all()
+
+
+@pytest.mark.parametrize("shape", [dict(Bt=2, L=37), dict(lens=[1, 0, 40, 17]), dict(L=1300), dict(Bt=33, L=21, Dm=512)])
+def test_rates_that_forget_everything(shape):
+    """A = -inf, and fp32's lowest value: the state is the last token's term alone, and no step of another rate, sequence end
+    or tile end makes a NaN of it.  (Their decays have no gradient; the oracle's rate is -1e30.)"""
+    i = make(**dict(dict(Dm=6, N=16), **shape))
+    i["A"][:, 3], i["A"][::2, 5] = float("-inf"), torch.finfo(torch.float32).min
+    i["dt"].clamp_(min=-3.0)
+    got = gpu(i)
+    state = i["init"][:1].cuda()
+    y = selective_scan_step(state, *(t.cuda().contiguous() for t in (i["x"][:1, 0], i["dt"][:1, 0], i["A"], i["B"][:1, 0], i["C"][:1, 0])),
+                            D=i["D"].cuda(), z=i["z"][:1, 0].cuda(), dt_bias=i["dt_bias"].cuda())
+    i["A"].clamp_(min=-1e30)
+    want = oracle(i)
+    for k, v in got.items():
+        assert torch.isfinite(v).all(), k
+        assert rel_l2(h(v), want[k]) <= TOL[v.dtype], (k, rel_l2(h(v), want[k]))
+    assert rel_l2(h(y), want["y"][:1, 0]) <= TOL[torch.float32]
