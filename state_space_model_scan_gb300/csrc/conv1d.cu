@@ -10,7 +10,7 @@
 // A thread owns W consecutive channels and sweeps a run of tokens with its inputs' last K rows in
 // registers, and, for the backward, also the K input-gradient rows still receiving contributions; the weight and bias gradients are per-tile partial sums added in a
 // fixed order afterwards (bitwise reproducible).  Every access of a warp is one contiguous
-// 512-byte (bf16) or 1 KB (fp32) row piece.
+// row piece: 4 channels a thread, 256 bytes in bf16 or 512 in fp32; in the single-token step 8, twice that.
 #include <algorithm>
 
 #include "f32x2.cuh"
@@ -217,7 +217,7 @@ __device__ __forceinline__ void stage_taps(const float *w, const float *bias, in
 // global memory (all in flight before the first is used; only the K - 1 rows before its run are read a
 // second time), keeps the last K rows as fp32 pairs, and does the taps and the gate's products
 // two channels to an instruction.
-// Bytes bound it: at 8191 x 6144 bf16, width 4, 38 us for 201 MB (5.2 TB/s, 77% of a plain copy; instructions
+// Bytes bound it: at 8191 x 6144 bf16, width 4, 39 us for 201 MB (5.1 TB/s, 76% of a plain copy; instructions
 // issue in 60% of the cycles), 41 in six packed pieces (40 with a single approximate tanh for the gate).  Before launches overlapped it took 46; W = 8 then at best 48, four rows in flight 47, 32
 // tokens a run 50, 512-thread blocks 67, a staged tile in shared memory 56.
 constexpr int kFwdW = 4, FG = 2, FT = 16, FB = 8;   // channels a thread; runs in a block; tokens of a run; rows in flight

@@ -817,7 +817,7 @@ cudaError_t run_bwd(const SelArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-// Channels per set: those for which the card's rounds of blocks (GOCC on each of 152 SMs), each as long as its channels and
+// Channels per set: those for which the card's rounds of blocks (GOCC on each SM), each as long as its channels and
 // a start worth 16 more (a block loads B and C and fills its pipeline), are over soonest.  At most 256: a set's own shares
 // of dB and dC cost little by then.  Measured, training, dstate 16, bf16, by this rule / halving from 256 until
 // eight blocks are there for each SM / until four are: 1 x 256 x 4096 59 / 73 / 65 us, 1 x 512 x 2048 63 / 73 / 67,
@@ -827,7 +827,7 @@ void sel_bwd_sets(int channels, int ngroups, int64_t nslots, int *nsets, int *cp
     int64_t best = INT64_MAX;
     for (int c = 256; c >= 32; c -= 32) {
         const int n = (dpg + c - 1) / c;
-        const int64_t rounds = (nslots * ngroups * n + 152 * GOCC - 1) / (152 * GOCC), cost = rounds * (std::min(c, dpg) + 16);
+        const int64_t rounds = (nslots * ngroups * n + kSMs * GOCC - 1) / (kSMs * GOCC), cost = rounds * (std::min(c, dpg) + 16);
         if (cost < best) {
             best = cost;
             *nsets = n;

@@ -469,8 +469,10 @@ cudaError_t launch(const SelArgs &a, cudaStream_t st) {
 // Without a split over time nothing is computed twice, but a sequence's tokens follow one another at
 // some 200 cycles each, so it takes many (sequence, channel) pairs to fill the card.  Measured at dstate
 // 16, bf16, split against whole: 4 x 2048 tokens x 2048 channels 185 / 279 us, 2 x 2048 x 8192 326 / 326,
-// 16 x 1024 x 4096 610 / 434.  Packed sequences differ in length and the longest one decides: 9 of
-// them, 16111 tokens x 4096 channels, 614 / 724.
+// 16 x 1024 x 4096 610 / 434.  Of packed sequences the host knows the number and not the lengths.  Its limit is
+// right where the lengths are alike: x 4096 channels, 16 of 500 tokens 317 / 221, 64 of 64 295 / 124, 64 of 1 217 / 54; 9 of mixed
+// lengths, 16111 tokens, 614 / 724 (below the limit).  It is wrong for one long sequence among many short
+// ones: 8000 tokens and 14 single ones (split) take 358 us, and 15 (whole) 1080 where split they would take 359.
 template <typename T>
 cudaError_t pick(const SelArgs &a, cudaStream_t st) {
     if (a.nseg == 1 && (int64_t)a.nseqs * a.channels >= (a.cu ? 65536 : 16384)) {
