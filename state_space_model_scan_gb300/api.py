@@ -49,6 +49,7 @@ class Workspace:
         nbytes = max(int(nbytes), 256)
         if self.buf is None or self.buf.numel() < nbytes:
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device or "cuda")
+        self.buf.record_stream(torch.cuda.current_stream(self.buf.device))   # it may be another than when it was allocated
         return self.buf
 
 

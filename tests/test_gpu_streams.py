@@ -127,3 +127,17 @@ def test_default_stream_given_inside_another(name):
 @pytest.mark.parametrize("name", SCAN)
 def test_scan_outputs_come_from_the_streams_own_memory(name):
     check_outputs(scan_calls()[name])
+
+
+def test_workspace_grows_while_another_stream_uses_it():
+    """The buffer that a growing workspace gives up is not handed out while a stream that has worked in it may still do so."""
+    ws, side = api.Workspace(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = spans([ws.get(8 << 20)])
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        ws.get(8 << 20).fill_(1)
+    ws.get(16 << 20)
+    assert apart(old, spans([torch.empty(8 << 20, dtype=torch.uint8, device="cuda")]))
+    torch.cuda.synchronize()
