@@ -517,6 +517,117 @@ ssd_status ssd_conv1d_step(const ssd_conv_problem *prob, const void *u, int64_t 
                            const float *bias, void *conv_states, int64_t nslots, int64_t slot_stride,
                            const int32_t *state_indices, void *out, int64_t out_stride, void *stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The gated delta rule: a state whose transition is not diagonal.  Per sequence and value head h, with the
+ * queries and keys of group h / (nheads / ngroups) and a state S [headdim][dstate]:
+ *
+ *   S   <- exp(g_t[h]) S
+ *   u_t  = beta_t[h] (v_t[h] - S k_t)                what the key held is forgotten, the new value taken up
+ *   S   <- S + u_t k_t^T
+ *   o_t[h] = scale * S q_t
+ *
+ * g is the logarithm of a decay (at most 0; -inf forgets everything; positive ones are computed, their accuracy is
+ * not vouched for); keys are expected at unit length and beta in [0, 2], or the state grows without bound.
+ *
+ * Layouts (element strides, outermost first; any strides for what is read, none of 0 or overlapping for what is written):
+ *   q, k, dq, dk   : [batch, seqlen, ngroups, dstate], innermost stride 1       `dtype`
+ *   v, o, dO, dv   : [batch, seqlen, nheads, headdim], innermost stride 1       `dtype`
+ *   g, beta, dg, dbeta : [batch, seqlen, nheads]                                f32, or `dtype`; gradients as their inputs
+ *   initial/final/dinitial/dfinal states : [nstate][nheads][headdim][dstate], contiguous, f32 or bf16
+ *                         each (nstate = batch, or nseqs with cu_seqlens)
+ *   cu_seqlens     : int32 [nseqs + 1], device, batch 1.  Its contents are not validated: bad ones give
+ *                    unspecified values, yet every access stays inside the tensors described here.
+ * A sequence without tokens has final state = initial state (zero without one), and passes dfinal on to
+ * dinitial.  headdim and dstate 1..256, else SSD_ERR_UNSUPPORTED.
+ *
+ * It is computed in chunks of 64 tokens.  f32 data: fp32 arithmetic throughout.  bf16 data with headdim and dstate
+ * up to 128: tensor cores with fp32 accumulation; what is carried from chunk to chunk goes into them as the
+ * sum of two bf16 values (2^-17), so that states are right to fp32's measure (about 1e-5); outputs and gradients
+ * are sums of products of bf16 operands (each rounded once, 2^-9), whatever type g, beta and their gradients have.
+ *
+ * chunk_states (optional): a device buffer of ssd_delta_chunk_states_size bytes, 256-byte aligned, into which the
+ * forward writes what the backward of the same problem starts from instead of running the forward again.
+ * Workspaces: device memory, 256-byte aligned, contents need not be initialised.  Gradients are summed
+ * in a fixed order (bitwise reproducible).
+ */
+typedef struct {
+    int64_t batch, seqlen, nheads, ngroups, headdim, dstate, nseqs;   /* nseqs: packed sequences (cu_seqlens), else 0 */
+    float scale;
+    int32_t dtype;                                                    /* ssd_dtype of q, k, v, o */
+} ssd_delta_problem;
+typedef struct {
+    ssd_tensor q, k, v, g, beta, initial_states;                      /* initial_states optional */
+    ssd_tensor o, final_states;                                       /* final_states optional */
+    const int32_t *cu_seqlens;
+    void *chunk_states;
+} ssd_delta_args;
+typedef struct {
+    ssd_delta_args fwd;                                               /* o and final_states are not looked at */
+    ssd_tensor dO, dfinal_states;                                     /* dfinal_states optional */
+    ssd_tensor dq, dk, dv, dg, dbeta, dinitial_states;                /* dinitial_states: with initial_states */
+} ssd_delta_bwd_args;
+
+ssd_status ssd_delta_chunk_states_size(const ssd_delta_problem *prob, size_t *bytes);
+ssd_status ssd_delta_fwd_workspace_size(const ssd_delta_problem *prob, size_t *bytes);
+ssd_status ssd_delta_fwd(const ssd_delta_problem *prob, const ssd_delta_args *args, void *workspace, size_t workspace_bytes,
+                         void *stream);
+/* kept: whether the call will bring chunk_states */
+ssd_status ssd_delta_bwd_workspace_size(const ssd_delta_problem *prob, int32_t kept, size_t *bytes);
+ssd_status ssd_delta_bwd(const ssd_delta_problem *prob, const ssd_delta_bwd_args *args, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * One token of the gated delta rule for each of `batch` requests, on a pool of states [nslots][nheads][headdim][dstate]; rules
+ * as for ssd_step.  q, k [batch][ngroups * dstate], v, o [batch][nheads * headdim] of `dtype`, g, beta [batch][nheads] f32 or
+ * `dtype`, rows contiguous at the given element strides.  dstate 1..256.
+ */
+typedef struct {
+    int64_t batch, nslots, nheads, headdim, ngroups, dstate;
+    int64_t slot_stride, q_stride, k_stride, v_stride, g_stride, beta_stride, o_stride;
+    float scale;
+    int32_t dtype, g_dtype, beta_dtype, state_dtype;
+} ssd_delta_step_problem;
+ssd_status ssd_delta_step(const ssd_delta_step_problem *prob, void *state, const int32_t *state_indices, const void *q,
+                          const void *k, const void *v, const void *g, const void *beta, void *o, void *stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Queries and keys before an attention or a delta rule: each head's vector x [dim] is normalised, weighted and rotated by
+ * its token's position in one pass,
+ *
+ *   n = x * rstd * w,   rstd = 1 / sqrt(mean x^2 + eps)   (SSD_QK_RMS)   or   1 / sqrt(sum x^2 + eps)   (SSD_QK_L2)
+ *   (y_a, y_b) = (n_a c - n_b s, n_a s + n_b c)           c = cos[position][i], s = sin[position][i], i < rotary / 2
+ *
+ * with (a, b) = (i, i + rotary / 2), or (2 i, 2 i + 1) when `interleaved`; features from `rotary` on are not turned.
+ *   q, q_out, dq.. : [batch, seqlen, q_heads, dim], k.. : [batch, seqlen, k_heads, dim], `dtype`, innermost stride 1, any
+ *                    strides for what is read; 0 heads of k: queries alone
+ *   q_weight, k_weight : f32 [dim], optional;  cos, sin : f32 [table_rows][rotary / 2], contiguous, when rotary > 0
+ *   positions      : int32 [batch][seqlen] at (pos_stride, 1), optional (a token's place in its row).  A token whose
+ *                    position is outside [0, table_rows) is padding: its outputs and gradients are zero (and it adds
+ *                    nothing to the weights' gradients).  Without a rotation positions are not read.
+ * The backward reads the inputs again (nothing is kept), gives the gradients of q and k in `dtype` and those of the
+ * weights in f32, summed in a fixed order.  dim 1..512, rotary even and at most dim.  All arithmetic in fp32.
+ */
+enum { SSD_QK_RMS = 0, SSD_QK_L2 = 1 };
+typedef struct {
+    int64_t batch, seqlen, q_heads, k_heads, dim, rotary, table_rows, pos_stride;
+    float eps;
+    int32_t dtype, mode, interleaved;
+} ssd_qk_problem;
+typedef struct {
+    ssd_tensor q, k, q_out, k_out;
+    const float *q_weight, *k_weight, *cos, *sin;
+    const int32_t *positions;
+} ssd_qk_args;
+typedef struct {
+    ssd_qk_args fwd;                                                  /* q_out, k_out are not looked at */
+    ssd_tensor dq_out, dk_out, dq, dk;
+    float *dq_weight, *dk_weight;                                     /* with their weights */
+} ssd_qk_bwd_args;
+ssd_status ssd_qk_norm_fwd(const ssd_qk_problem *prob, const ssd_qk_args *args, void *stream);
+ssd_status ssd_qk_norm_bwd_workspace_size(const ssd_qk_problem *prob, size_t *bytes);
+ssd_status ssd_qk_norm_bwd(const ssd_qk_problem *prob, const ssd_qk_bwd_args *args, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
 /*
  * State snapshots in 8 bits: `count` states of a pool put aside and taken up again (a prefix that
  * requests share, a request that is preempted).  A state is `rows` rows of `dstate` values; a row

@@ -10,3 +10,5 @@ first call does, and raises if it has not been built.
 from .api import ssd_forward, ssd_backward, Workspace  # noqa: F401
 from .api import (selective_scan_forward, selective_scan_backward, SelectiveScanFunction, ssd_step,  # noqa: F401
                   selective_scan_step, conv1d_prompt, conv1d_step, snapshot_store, snapshot_load)
+from .api import (gated_delta_forward, gated_delta_backward, GatedDeltaFunction, gated_delta_step, qk_norm_forward,  # noqa: F401
+                  qk_norm_backward, QKNormFunction)

@@ -30,7 +30,9 @@ EXPORTS = ["ssd_fwd_workspace_size", "ssd_fwd", "ssd_bwd_workspace_size", "ssd_b
            "ssd_complex_fwd_workspace_size", "ssd_complex_fwd",
            "ssd_selective_chunk_states_size", "ssd_selective_fwd_workspace_size", "ssd_selective_fwd",
            "ssd_selective_bwd_workspace_size", "ssd_selective_bwd", "ssd_step", "ssd_selective_step", "ssd_conv1d_prompt", "ssd_conv1d_step",
-           "ssd_snapshot_store", "ssd_snapshot_load"]
+           "ssd_snapshot_store", "ssd_snapshot_load", "ssd_delta_chunk_states_size", "ssd_delta_fwd_workspace_size", "ssd_delta_fwd",
+           "ssd_delta_bwd_workspace_size", "ssd_delta_bwd", "ssd_delta_step", "ssd_qk_norm_fwd", "ssd_qk_norm_bwd_workspace_size",
+           "ssd_qk_norm_bwd"]
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -98,6 +100,44 @@ class SnapshotProblem(ctypes.Structure):
                 [("state_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)])
 
 
+class DeltaProblem(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("batch", "seqlen", "nheads", "ngroups", "headdim", "dstate", "nseqs")] +
+                [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)])
+
+
+class DeltaArgs(ctypes.Structure):
+    _fields_ = ([(n, Tensor) for n in ("q", "k", "v", "g", "beta", "initial_states", "o", "final_states")] +
+                [("cu_seqlens", ctypes.c_void_p), ("chunk_states", ctypes.c_void_p)])
+
+
+class DeltaBwdArgs(ctypes.Structure):
+    _fields_ = [("fwd", DeltaArgs)] + [(n, Tensor) for n in ("dO", "dfinal_states", "dq", "dk", "dv", "dg", "dbeta", "dinitial_states")]
+
+
+class DeltaStepProblem(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("batch", "nslots", "nheads", "headdim", "ngroups", "dstate", "slot_stride", "q_stride",
+                                               "k_stride", "v_stride", "g_stride", "beta_stride", "o_stride")] +
+                [("scale", ctypes.c_float)] + [(n, ctypes.c_int32) for n in ("dtype", "g_dtype", "beta_dtype", "state_dtype")])
+
+
+SSD_QK_RMS, SSD_QK_L2 = 0, 1
+
+
+class QkProblem(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("batch", "seqlen", "q_heads", "k_heads", "dim", "rotary", "table_rows", "pos_stride")] +
+                [("eps", ctypes.c_float)] + [(n, ctypes.c_int32) for n in ("dtype", "mode", "interleaved")])
+
+
+class QkArgs(ctypes.Structure):
+    _fields_ = ([(n, Tensor) for n in ("q", "k", "q_out", "k_out")] +
+                [(n, ctypes.c_void_p) for n in ("q_weight", "k_weight", "cos", "sin", "positions")])
+
+
+class QkBwdArgs(ctypes.Structure):
+    _fields_ = ([("fwd", QkArgs)] + [(n, Tensor) for n in ("dq_out", "dk_out", "dq", "dk")] +
+                [(n, ctypes.c_void_p) for n in ("dq_weight", "dk_weight")])
+
+
 class DebugLayout(ctypes.Structure):
     _fields_ = [("meta_counts", ctypes.c_int64), ("chunk_info", ctypes.c_int64), ("dt", ctypes.c_int64),
                 ("cs", ctypes.c_int64), ("states", ctypes.c_int64), ("units", ctypes.c_int64),
@@ -152,6 +192,14 @@ def load(path: str = LIB_PATH):
     lib.ssd_step.argtypes = lib.ssd_selective_step.argtypes = [P(StepProblem)] + [V] * 12
     lib.ssd_conv1d_prompt.argtypes = [P(ConvProblem), V, I64, I64, V, V, V, V, I64, I64, V, V, V, I64, I64, V]
     lib.ssd_conv1d_step.argtypes = [P(ConvProblem), V, I64, V, V, V, I64, I64, V, V, I64, V]
+    lib.ssd_delta_chunk_states_size.argtypes = lib.ssd_delta_fwd_workspace_size.argtypes = [P(DeltaProblem), P(S)]
+    lib.ssd_delta_fwd.argtypes = [P(DeltaProblem), P(DeltaArgs), V, S, V]
+    lib.ssd_delta_bwd_workspace_size.argtypes = [P(DeltaProblem), ctypes.c_int32, P(S)]
+    lib.ssd_delta_bwd.argtypes = [P(DeltaProblem), P(DeltaBwdArgs), V, S, V]
+    lib.ssd_delta_step.argtypes = [P(DeltaStepProblem)] + [V] * 9
+    lib.ssd_qk_norm_fwd.argtypes = [P(QkProblem), P(QkArgs), V]
+    lib.ssd_qk_norm_bwd_workspace_size.argtypes = [P(QkProblem), P(S)]
+    lib.ssd_qk_norm_bwd.argtypes = [P(QkProblem), P(QkBwdArgs), V, S, V]
     lib.ssd_snapshot_store.argtypes = lib.ssd_snapshot_load.argtypes = [P(SnapshotProblem)] + [V] * 6
     for f in ("ssd_fwd_workspace_size", "ssd_fwd", "ssd_bwd_workspace_size", "ssd_bwd", "ssd_query_status",
               "ssd_fwd_debug_layout", "ssd_fwd_noalloc", "ssd_selftest_bounded_wait", "ssd_chunk_states_size",
@@ -160,7 +208,9 @@ def load(path: str = LIB_PATH):
               "ssd_conv1d_bwd_workspace_size", "ssd_conv1d_bwd", "ssd_complex_fwd_workspace_size",
               "ssd_complex_fwd", "ssd_selective_chunk_states_size", "ssd_selective_fwd_workspace_size", "ssd_selective_fwd",
               "ssd_selective_bwd_workspace_size", "ssd_selective_bwd", "ssd_step", "ssd_selective_step",
-              "ssd_conv1d_prompt", "ssd_conv1d_step", "ssd_snapshot_store", "ssd_snapshot_load"):
+              "ssd_conv1d_prompt", "ssd_conv1d_step", "ssd_snapshot_store", "ssd_snapshot_load", "ssd_delta_chunk_states_size",
+              "ssd_delta_fwd_workspace_size", "ssd_delta_fwd", "ssd_delta_bwd_workspace_size", "ssd_delta_bwd", "ssd_delta_step",
+              "ssd_qk_norm_fwd", "ssd_qk_norm_bwd_workspace_size", "ssd_qk_norm_bwd"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -404,7 +454,9 @@ def selective_chunk_states_size(prob):
 # ---- the compiled binding (csrc/binding.cpp) of the entry points that are called for single tokens
 _BINDING_ORDER = ["ssd_step", "ssd_selective_step", "ssd_conv1d_prompt", "ssd_conv1d_step", "ssd_snapshot_store",
                   "ssd_snapshot_load", "ssd_selective_chunk_states_size", "ssd_selective_fwd_workspace_size", "ssd_selective_fwd",
-                  "ssd_selective_bwd_workspace_size", "ssd_selective_bwd"]
+                  "ssd_selective_bwd_workspace_size", "ssd_selective_bwd", "ssd_delta_chunk_states_size",
+                  "ssd_delta_fwd_workspace_size", "ssd_delta_fwd", "ssd_delta_bwd_workspace_size", "ssd_delta_bwd", "ssd_delta_step",
+                  "ssd_qk_norm_fwd", "ssd_qk_norm_bwd_workspace_size", "ssd_qk_norm_bwd"]
 _fast = None
 
 

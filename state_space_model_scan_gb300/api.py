@@ -387,3 +387,125 @@ def snapshot_store(states, snapshots, scales, state_indices=None, slots=None, st
 def snapshot_load(snapshots, scales, states, slots=None, state_indices=None, stream=None):
     """Takes states up again: snapshot slots[i] is read back into state state_indices[i] of the pool `states`."""
     _lib.fast().snapshot(False, states, snapshots, scales, state_indices, slots, _handle(stream))
+
+
+# ---------------------------------------------------------------------------------------------
+# The gated delta rule (chunked, with every gradient, and one token at a time) and the norm of queries and keys with the
+# rotation by position that precedes it, or an attention.  Streams, outputs and errors as above.
+def _state_code(state_dtype):
+    if state_dtype not in (None, torch.float32, torch.bfloat16):
+        raise ValueError("state_dtype is float32 or bfloat16")
+    return -1 if state_dtype is None else _lib.SSD_BF16 if state_dtype == torch.bfloat16 else _lib.SSD_F32
+
+
+def gated_delta_forward(q, k, v, g, beta, scale=None, initial_states=None, cu_seqlens=None, return_final_states=True, state_dtype=None,
+                        keep_chunk_states=False, stream=None):
+    """o, final_states = the gated delta rule (see include/ssd.h, ssd_delta_fwd): per value head a state S [headdim, dstate],
+    S <- exp(g_t) S, u = beta_t (v_t - S k_t), S <- S + u k_t^T, o_t = scale S q_t.
+
+    q, k: [batch, seqlen, ngroups, dstate]; v, o: [batch, seqlen, nheads, headdim], q's type; head h reads group
+    h // (nheads // ngroups); g (log decay, at most 0), beta: [batch, seqlen, nheads] float32 or v's type; scale: dstate ** -0.5
+    by default; initial_states: [S, nheads, headdim, dstate] float32 or bfloat16; cu_seqlens: int32 [S + 1] (batch 1).  Keys are expected
+    at unit length (qk_norm_forward(mode="l2")).  state_dtype: of the final states (default: that of
+    initial_states, else float32).  keep_chunk_states: also return the buffer that gated_delta_backward(chunk_states=...)
+    starts from."""
+    return _lib.fast().delta_fwd(q, k, v, g, beta, initial_states, cu_seqlens, scale, bool(return_final_states), _state_code(state_dtype),
+                                 bool(keep_chunk_states), _handle(stream))
+
+
+def gated_delta_backward(q, k, v, g, beta, do, scale=None, initial_states=None, dfinal_states=None, cu_seqlens=None, chunk_states=None,
+                         workspace=None, stream=None):
+    """Gradients of sum(do * o) + sum(dfinal_states * final_states): a dict with dq, dk, dv, dg, dbeta and, with initial_states,
+    dinitial_states, each of its input's type.  chunk_states: the buffer that gated_delta_forward(keep_chunk_states=True)
+    returned for the same inputs (without it the forward runs again)."""
+    return _lib.fast().delta_bwd(q, k, v, g, beta, initial_states, cu_seqlens, scale, do, dfinal_states, chunk_states, workspace,
+                                 _handle(stream))
+
+
+class GatedDeltaFunction(torch.autograd.Function):
+    """Autograd wrapper of the gated delta rule.  Where gradients are asked for, the forward keeps what the backward starts from
+    (ssd_delta_chunk_states_size; with keep_chunk_states=False the backward computes it again).  An unused output costs no gradient
+    of zeros.  A second differentiation is refused."""
+
+    @classmethod
+    def apply(cls, q, k, v, g, beta, initial_states=None, cu_seqlens=None, scale=None, keep_chunk_states=True):
+        inputs = (q, k, v, g, beta, initial_states)
+        keep = keep_chunk_states and torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)
+        return super().apply(*inputs, cu_seqlens, scale, keep)
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, initial_states, cu_seqlens, scale, keep):
+        o, fin, *kept = gated_delta_forward(q, k, v, g, beta, scale=scale, initial_states=initial_states, cu_seqlens=cu_seqlens,
+                                            keep_chunk_states=keep)
+        ctx.save_for_backward(q, k, v, g, beta, initial_states, cu_seqlens, kept[0] if keep else None)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return o, fin
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do, dfin):
+        q, k, v, g, beta, init, cu, kept = ctx.saved_tensors
+        do = torch.zeros_like(v, memory_format=torch.contiguous_format) if do is None else do
+        d = gated_delta_backward(q, k, v, g, beta, do if do.stride(-1) == 1 else do.contiguous(), scale=ctx.scale, initial_states=init,
+                                 dfinal_states=None if dfin is None else dfin.contiguous(), cu_seqlens=cu, chunk_states=kept)
+        return d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"], d.get("dinitial_states"), None, None, None
+
+
+def gated_delta_step(state, q, k, v, g, beta, scale=None, state_indices=None, stream=None):
+    """o = one token of gated_delta_forward's recurrence for each request; `state` [nslots, nheads, headdim, dstate] float32 or
+    bfloat16 is updated in place at state_indices.  q, k: [batch, ngroups, dstate]; v, o: [batch, nheads, headdim]; g, beta:
+    [batch, nheads] float32 or v's type.  Slots as in ssd_step."""
+    return _lib.fast().delta_step(state, q, k, v, g, beta, scale, state_indices, _handle(stream))
+
+
+_QK_MODES = {"rms": _lib.SSD_QK_RMS, "l2": _lib.SSD_QK_L2}
+
+
+def _qk_mode(mode):
+    if mode not in _QK_MODES:
+        raise ValueError("mode is 'rms' or 'l2'")
+    return _QK_MODES[mode]
+
+
+def qk_norm_forward(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, mode="rms", interleaved=False, eps=1e-6,
+                    stream=None):
+    """q_out, k_out = queries and keys normalised per head (mode "rms": x / sqrt(mean x^2 + eps), "l2": x / sqrt(sum x^2 + eps)), times
+    the weights, and rotated by their tokens' positions (see include/ssd.h, ssd_qk_norm_fwd) in one pass.
+
+    q: [batch, seqlen, q_heads, dim], k: [batch, seqlen, k_heads, dim] of the same type, or None; weights: float32 [dim];
+    cos, sin: float32 [rows, rotary / 2], without them nothing is rotated; positions: int32 [batch, seqlen] (default: a token's
+    place in its row), a token with one outside the table is padding: its outputs are zero.  interleaved: features (2i, 2i + 1)
+    are a pair, else (i, i + rotary / 2)."""
+    return _lib.fast().qk_fwd(q, k, q_weight, k_weight, cos, sin, positions, _qk_mode(mode), bool(interleaved), eps, _handle(stream))
+
+
+def qk_norm_backward(q, k, dq, dk, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, mode="rms", interleaved=False,
+                     eps=1e-6, workspace=None, stream=None):
+    """Gradients of sum(dq * q_out) + sum(dk * k_out): a dict with dq, dk (when k is given) and, with the weights, dq_weight, dk_weight
+    (float32).  Nothing but the inputs is needed from the forward."""
+    return _lib.fast().qk_bwd(q, k, q_weight, k_weight, cos, sin, positions, _qk_mode(mode), bool(interleaved), eps, dq, dk, workspace,
+                              _handle(stream))
+
+
+class QKNormFunction(torch.autograd.Function):
+    """Autograd wrapper of the norm and rotation of queries and keys; it keeps its inputs alone.  cos, sin and positions get no
+    gradient.  A second differentiation is refused."""
+
+    @classmethod
+    def apply(cls, q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, mode="rms", interleaved=False, eps=1e-6):
+        return super().apply(q, k, q_weight, k_weight, cos, sin, positions, mode, interleaved, eps)
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, mode, interleaved, eps):
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+        ctx.how = dict(mode=mode, interleaved=interleaved, eps=eps)
+        return qk_norm_forward(q, k, q_weight, k_weight, cos, sin, positions, **ctx.how)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk):
+        q, k, wq, wk, cos, sin, pos = ctx.saved_tensors
+        dq, dk = (t if t is None or t.stride(-1) == 1 else t.contiguous() for t in (dq, dk))
+        d = qk_norm_backward(q, k, dq, dk, wq, wk, cos, sin, pos, **ctx.how)
+        return (d["dq"], d.get("dk"), d.get("dq_weight"), d.get("dk_weight")) + (None,) * 6

@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <math.h>
 #include <stdarg.h>
 
 #include <initializer_list>
@@ -34,6 +35,15 @@ struct Lib {
     decltype(&ssd_selective_fwd) selective_fwd;
     decltype(&ssd_selective_bwd_workspace_size) bwd_workspace_size;
     decltype(&ssd_selective_bwd) selective_bwd;
+    decltype(&ssd_delta_chunk_states_size) delta_states_size;
+    decltype(&ssd_delta_fwd_workspace_size) delta_fwd_workspace_size;
+    decltype(&ssd_delta_fwd) delta_fwd;
+    decltype(&ssd_delta_bwd_workspace_size) delta_bwd_workspace_size;
+    decltype(&ssd_delta_bwd) delta_bwd;
+    decltype(&ssd_delta_step) delta_step;
+    decltype(&ssd_qk_norm_fwd) qk_fwd;
+    decltype(&ssd_qk_norm_bwd_workspace_size) qk_bwd_workspace_size;
+    decltype(&ssd_qk_norm_bwd) qk_bwd;
 } lib;
 PyObject *ssd_error, *out_of_memory;   // the exception classes SSDError(code, where) and torch's
 
@@ -431,6 +441,275 @@ PyObject *selective_bwd(PyObject *const *a) {
     return g;
 }
 
+// ---- the gated delta rule
+struct Delta {
+    int dev;
+    int64_t S, B, L, G, H, V, K;
+    ssd_delta_problem p;
+    ssd_delta_args f;
+};
+const char *const delta_names[7] = {"q", "k", "v", "g", "beta", "initial_states", "cu_seqlens"};
+
+// A float argument, or `other` where it is None.
+double number(PyObject *o, const char *name, double other) {
+    if (o == Py_None) return other;
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        fail(PyExc_TypeError, "%s is not a number", name);
+    }
+    return v;
+}
+
+// q, k, v, g, beta, initial_states, cu_seqlens; scale: dstate^-0.5 where it is None
+Delta delta_inputs(const Tensor *const *t, PyObject *scale) {
+    const Tensor &q = *t[0], &k = *t[1], &v = *t[2], &g = *t[3], &beta = *t[4], &init = *t[5], &cu = *t[6];
+    Delta s{};
+    const int dev = s.dev = lead("v", v, 4), own = type_of(v);
+    NEED(q.dim() == 4, "q has shape [batch, seqlen, ngroups, dstate]");
+    s.B = v.size(0); s.L = v.size(1); s.H = v.size(2); s.V = v.size(3); s.G = q.size(2); s.K = q.size(3);
+    s.S = s.B;
+    if (cu.defined()) {
+        s.S = cu.numel() - 1;
+        NEED(s.S >= 1, "cu_seqlens holds no sequence");
+        like("cu_seqlens", cu, {s.S + 1}, I32, dev, 1);
+    }
+    like("q", q, {s.B, s.L, s.G, s.K}, own, dev, 1);
+    like("k", k, {s.B, s.L, s.G, s.K}, own, dev, 1);
+    like("v", v, {s.B, s.L, s.H, s.V}, own, dev, 1);
+    like("g", g, {s.B, s.L, s.H}, F32 | own, dev, 0);
+    like("beta", beta, {s.B, s.L, s.H}, F32 | own, dev, 0);
+    if (init.defined()) like("initial_states", init, {s.S, s.H, s.V, s.K}, F32 | BF16, dev, 4);
+    s.p = {s.B, s.L, s.H, s.G, s.V, s.K, cu.defined() ? s.S : 0, (float)number(scale, "scale", s.K > 0 ? 1.0 / sqrt((double)s.K) : 1.0), code(v)};
+    s.f.q = desc(q, 1); s.f.k = desc(k, 1); s.f.v = desc(v, 1); s.f.g = desc(g, 0); s.f.beta = desc(beta, 0);
+    s.f.initial_states = desc(init, 4);
+    s.f.cu_seqlens = ptr_as<int32_t>(cu);
+    return s;
+}
+
+// delta_fwd(the inputs, scale, return_final, state_dtype (-1: the initial states' or f32), keep, stream)
+PyObject *delta_fwd(PyObject *const *a) {
+    const Tensor *t[7];
+    for (int i = 0; i < 7; ++i) t[i] = &arg(a[i], delta_names[i], i >= 5);
+    Delta s = delta_inputs(t, a[7]);
+    const Tensor &v = *t[2], &init = *t[5];
+    const bool want_final = a[8] == Py_True, keep = a[10] == Py_True;
+    const long sd = PyLong_AsLong(a[9]);
+    const Stream st(a[11], s.dev);
+    Tensor o = st.output({s.B, s.L, s.H, s.V}, v.scalar_type()), final, kept;
+    s.f.o = desc(o, 4);
+    if (want_final) {
+        const bool bf16 = sd < 0 ? init.defined() && init.scalar_type() == at::kBFloat16 : sd == SSD_BF16;
+        final = st.output({s.S, s.H, s.V, s.K}, bf16 ? at::kBFloat16 : at::kFloat);
+        s.f.final_states = desc(final, 4);
+    }
+    if (keep) {
+        size_t n = 0;
+        check(lib.delta_states_size(&s.p, &n), "ssd_delta_chunk_states_size");
+        kept = st.output({(int64_t)n}, at::kByte);
+        s.f.chunk_states = kept.data_ptr();
+    }
+    size_t n = 0;
+    check(lib.delta_fwd_workspace_size(&s.p, &n), "ssd_delta_fwd_workspace_size");
+    Tensor ws;
+    if (n > 0) ws = st.empty({(int64_t)n}, at::kByte);
+    check(lib.delta_fwd(&s.p, &s.f, ptr(ws), n, st.handle), "ssd_delta_fwd");
+    PyObject *r = PyTuple_New(keep ? 3 : 2);
+    if (!r) throw Raised();
+    PyTuple_SET_ITEM(r, 0, wrap(o));
+    PyTuple_SET_ITEM(r, 1, want_final ? wrap(final) : Py_NewRef(Py_None));
+    if (keep) PyTuple_SET_ITEM(r, 2, wrap(kept));
+    return r;
+}
+
+// A dict's tensors, allocated and described one by one.
+struct Grads {
+    PyObject *g = PyDict_New();
+    const Stream &st;
+    explicit Grads(const Stream &s) : st(s) {
+        if (!g) throw Raised();
+    }
+    ~Grads() { Py_XDECREF(g); }
+    Tensor out(const char *name, at::IntArrayRef shape, at::ScalarType type) {
+        Tensor v = st.output(shape, type);
+        PyObject *o = wrap(v);
+        const int rc = o ? PyDict_SetItemString(g, name, o) : -1;
+        Py_XDECREF(o);
+        if (rc) throw Raised();
+        return v;
+    }
+    PyObject *take() {
+        PyObject *r = g;
+        g = nullptr;
+        return r;
+    }
+};
+// The backward's workspace: from an object with get(bytes), or of its own.
+Tensor workspace_of(PyObject *o, size_t n, const Stream &st) {
+    if (o == Py_None) return st.empty({(int64_t)(n < 256 ? 256 : n)}, at::kByte);
+    PyObject *r = PyObject_CallMethod(o, "get", "n", (Py_ssize_t)n);
+    if (!r) throw Raised();
+    const bool ok = THPVariable_Check(r);
+    Tensor ws;
+    if (ok) ws = THPVariable_Unpack(r);
+    Py_DECREF(r);
+    NEED(ok && ws.is_cuda() && ws.get_device() == st.dev && ws.is_contiguous(), "workspace.get(bytes) gives a contiguous tensor on GPU %d", st.dev);
+    st.used(ws);
+    return ws;
+}
+
+// delta_bwd(the inputs, scale, do, dfinal_states, chunk_states, workspace, stream)
+PyObject *delta_bwd(PyObject *const *a) {
+    const Tensor *t[7];
+    for (int i = 0; i < 7; ++i) t[i] = &arg(a[i], delta_names[i], i >= 5);
+    Delta s = delta_inputs(t, a[7]);
+    const Tensor &v = *t[2], &g = *t[3], &beta = *t[4], &init = *t[5];
+    const Tensor &dO = arg(a[8], "do"), &dfinal = arg(a[9], "dfinal_states", true), &kept = arg(a[10], "chunk_states", true);
+    like("do", dO, {s.B, s.L, s.H, s.V}, type_of(v), s.dev, 1);
+    if (dfinal.defined()) like("dfinal_states", dfinal, {s.S, s.H, s.V, s.K}, F32 | BF16, s.dev, 4);
+    if (kept.defined()) {
+        size_t n = 0;
+        check(lib.delta_states_size(&s.p, &n), "ssd_delta_chunk_states_size");
+        NEED(kept.is_cuda() && kept.get_device() == s.dev && kept.is_contiguous(), "chunk_states: a contiguous buffer on GPU %d", s.dev);
+        NEED(kept.nbytes() >= n, "chunk_states is smaller than %zu bytes", n);
+        s.f.chunk_states = kept.data_ptr();
+    }
+    const Stream st(a[12], s.dev);
+    ssd_delta_bwd_args b{};
+    b.fwd = s.f;
+    b.dO = desc(dO, 1);
+    b.dfinal_states = desc(dfinal, 4);
+    Grads d(st);
+    b.dq = desc(d.out("dq", {s.B, s.L, s.G, s.K}, v.scalar_type()), 4);
+    b.dk = desc(d.out("dk", {s.B, s.L, s.G, s.K}, v.scalar_type()), 4);
+    b.dv = desc(d.out("dv", {s.B, s.L, s.H, s.V}, v.scalar_type()), 4);
+    b.dg = desc(d.out("dg", {s.B, s.L, s.H}, g.scalar_type()), 3);
+    b.dbeta = desc(d.out("dbeta", {s.B, s.L, s.H}, beta.scalar_type()), 3);
+    if (init.defined()) b.dinitial_states = desc(d.out("dinitial_states", {s.S, s.H, s.V, s.K}, init.scalar_type()), 4);
+    size_t n = 0;
+    check(lib.delta_bwd_workspace_size(&s.p, kept.defined(), &n), "ssd_delta_bwd_workspace_size");
+    Tensor ws = workspace_of(a[11], n, st);
+    check(lib.delta_bwd(&s.p, &b, ws.data_ptr(), ws.nbytes(), st.handle), "ssd_delta_bwd");
+    return d.take();
+}
+
+// delta_step(state, q, k, v, g, beta, scale, state_indices, stream)
+PyObject *delta_step(PyObject *const *a) {
+    const Tensor &state = arg(a[0], "state"), &q = arg(a[1], "q"), &k = arg(a[2], "k"), &v = arg(a[3], "v"), &g = arg(a[4], "g"),
+                 &beta = arg(a[5], "beta"), &idx = arg(a[7], "state_indices", true);
+    const int dev = lead("v", v, 3), own = type_of(v);
+    NEED(q.dim() == 3, "q has shape [batch, ngroups, dstate]");
+    NEED(state.dim() == 4, "state has shape [nslots, nheads, headdim, dstate]");
+    const int64_t n = v.size(0), H = v.size(1), V = v.size(2), G = q.size(1), K = q.size(2), slots = state.size(0);
+    like("v", v, {n, H, V}, own, dev, 2);
+    like("q", q, {n, G, K}, own, dev, 2);
+    like("k", k, {n, G, K}, own, dev, 2);
+    like("g", g, {n, H}, F32 | own, dev, 1);
+    like("beta", beta, {n, H}, F32 | own, dev, 1);
+    like("state", state, {slots, H, V, K}, F32 | BF16, dev, 3);
+    if (idx.defined()) like("state_indices", idx, {n}, I32, dev, 1);
+    else NEED(slots >= n, "the state pool has fewer slots than there are requests");
+    const double scale = number(a[6], "scale", K > 0 ? 1.0 / sqrt((double)K) : 1.0);
+    const Stream st(a[8], dev);
+    Tensor o = st.output(v.sizes(), v.scalar_type());
+    const ssd_delta_step_problem p{n, slots, H, V, G, K, state.stride(0), q.stride(0), k.stride(0), v.stride(0), g.stride(0), beta.stride(0),
+                                   H * V, (float)scale, code(v), code(g), code(beta), code(state)};
+    check(lib.delta_step(&p, ptr(state), ptr_as<int32_t>(idx), ptr(q), ptr(k), ptr(v), ptr(g), ptr(beta), ptr(o), st.handle), "ssd_delta_step");
+    written(state);
+    return wrap(o);
+}
+
+// ---- queries and keys: norm and rotation
+struct Qk {
+    int dev;
+    int64_t B, L, Hq, Hk, D;
+    ssd_qk_problem p;
+    ssd_qk_args f;
+};
+const char *const qk_names[7] = {"q", "k", "q_weight", "k_weight", "cos", "sin", "positions"};
+// q, k, q_weight, k_weight, cos, sin, positions; mode, interleaved, eps
+Qk qk_inputs(const Tensor *const *t, PyObject *mode, PyObject *interleaved, PyObject *eps) {
+    const Tensor &q = *t[0], &k = *t[1], &wq = *t[2], &wk = *t[3], &cos = *t[4], &sin = *t[5], &pos = *t[6];
+    Qk s{};
+    const int dev = s.dev = lead("q", q, 4), own = type_of(q);
+    s.B = q.size(0); s.L = q.size(1); s.Hq = q.size(2); s.D = q.size(3);
+    s.Hk = 0;
+    like("q", q, {s.B, s.L, s.Hq, s.D}, own, dev, 1);
+    if (k.defined()) {
+        NEED(k.dim() == 4, "k has shape [batch, seqlen, heads, dim]");
+        s.Hk = k.size(2);
+        like("k", k, {s.B, s.L, s.Hk, s.D}, own, dev, 1);
+    }
+    if (wq.defined()) like("q_weight", wq, {s.D}, F32, dev, 1);
+    if (wk.defined()) {
+        NEED(k.defined(), "k_weight without k");
+        like("k_weight", wk, {s.D}, F32, dev, 1);
+    }
+    NEED(cos.defined() == sin.defined(), "cos and sin are given together");
+    int64_t rotary = 0, rows = 0;
+    if (cos.defined()) {
+        NEED(cos.dim() == 2, "cos has shape [positions, rotary / 2]");
+        rows = cos.size(0);
+        rotary = 2 * cos.size(1);
+        like("cos", cos, {rows, rotary / 2}, F32, dev, 2);
+        like("sin", sin, {rows, rotary / 2}, F32, dev, 2);
+        NEED(rotary <= s.D, "the rotation is wider than the heads");
+    }
+    if (pos.defined()) like("positions", pos, {s.B, s.L}, I32, dev, 1);
+    s.p = {s.B, s.L, s.Hq, s.Hk, s.D, rotary, rows, pos.defined() ? pos.stride(0) : 0, (float)number(eps, "eps", 1e-6), code(q),
+           (int32_t)PyLong_AsLong(mode), interleaved == Py_True};
+    s.f.q = desc(q, 1); s.f.k = desc(k, 1);
+    s.f.q_weight = ptr_as<float>(wq); s.f.k_weight = ptr_as<float>(wk); s.f.cos = ptr_as<float>(cos); s.f.sin = ptr_as<float>(sin);
+    s.f.positions = ptr_as<int32_t>(pos);
+    return s;
+}
+
+// qk_fwd(the inputs, mode, interleaved, eps, stream)
+PyObject *qk_fwd(PyObject *const *a) {
+    const Tensor *t[7];
+    for (int i = 0; i < 7; ++i) t[i] = &arg(a[i], qk_names[i], i >= 1);
+    Qk s = qk_inputs(t, a[7], a[8], a[9]);
+    const Stream st(a[10], s.dev);
+    Tensor q = st.output({s.B, s.L, s.Hq, s.D}, t[0]->scalar_type()), k;
+    s.f.q_out = desc(q, 4);
+    if (t[1]->defined()) {
+        k = st.output({s.B, s.L, s.Hk, s.D}, t[0]->scalar_type());
+        s.f.k_out = desc(k, 4);
+    }
+    check(lib.qk_fwd(&s.p, &s.f, st.handle), "ssd_qk_norm_fwd");
+    PyObject *r = PyTuple_New(2);
+    if (!r) throw Raised();
+    PyTuple_SET_ITEM(r, 0, wrap(q));
+    PyTuple_SET_ITEM(r, 1, k.defined() ? wrap(k) : Py_NewRef(Py_None));
+    return r;
+}
+
+// qk_bwd(the inputs, mode, interleaved, eps, dq_out, dk_out, workspace, stream)
+PyObject *qk_bwd(PyObject *const *a) {
+    const Tensor *t[7];
+    for (int i = 0; i < 7; ++i) t[i] = &arg(a[i], qk_names[i], i >= 1);
+    Qk s = qk_inputs(t, a[7], a[8], a[9]);
+    const Tensor &dq = arg(a[10], "dq"), &dk = arg(a[11], "dk", true);
+    NEED(dk.defined() == t[1]->defined(), "dk is given where k is");
+    like("dq", dq, {s.B, s.L, s.Hq, s.D}, type_of(*t[0]), s.dev, 1);
+    if (dk.defined()) like("dk", dk, {s.B, s.L, s.Hk, s.D}, type_of(*t[0]), s.dev, 1);
+    const Stream st(a[13], s.dev);
+    ssd_qk_bwd_args b{};
+    b.fwd = s.f;
+    b.dq_out = desc(dq, 1); b.dk_out = desc(dk, 1);
+    Grads d(st);
+    b.dq = desc(d.out("dq", {s.B, s.L, s.Hq, s.D}, t[0]->scalar_type()), 4);
+    if (dk.defined()) b.dk = desc(d.out("dk", {s.B, s.L, s.Hk, s.D}, t[0]->scalar_type()), 4);
+    if (t[2]->defined()) b.dq_weight = ptr_as<float>(d.out("dq_weight", {s.D}, at::kFloat));
+    if (t[3]->defined()) b.dk_weight = ptr_as<float>(d.out("dk_weight", {s.D}, at::kFloat));
+    size_t n = 0;
+    check(lib.qk_bwd_workspace_size(&s.p, &n), "ssd_qk_norm_bwd_workspace_size");
+    Tensor ws;
+    if (b.dq_weight || b.dk_weight) ws = workspace_of(a[12], n, st);
+    check(lib.qk_bwd(&s.p, &b, ptr(ws), ws.defined() ? ws.nbytes() : 0, st.handle), "ssd_qk_norm_bwd");
+    return d.take();
+}
+
 // init(SSDError, torch.OutOfMemoryError, addresses of the library's functions in Lib's order)
 PyObject *init(PyObject *const *a) {
     void **to = reinterpret_cast<void **>(&lib);
@@ -465,6 +744,8 @@ PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n) {
 #define ENTRY(name, n) {#name, (PyCFunction)(void *)entry<name, n>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(step, 12),          ENTRY(conv1d_prompt, 9), ENTRY(conv1d_step, 7),
                          ENTRY(snapshot, 7),       ENTRY(selective_fwd, 14), ENTRY(selective_bwd, 15),
+                         ENTRY(delta_fwd, 12),     ENTRY(delta_bwd, 13),    ENTRY(delta_step, 9),
+                         ENTRY(qk_fwd, 11),        ENTRY(qk_bwd, 14),
                          ENTRY(init, 2 + sizeof(Lib) / sizeof(void *)),      {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,210 @@
+// delta.cu -- the C entry points of the gated delta rule: validation, workspace, launches.
+#include "delta.cuh"
+
+using namespace ssd;
+
+namespace {
+
+bool al(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+size_t esize(int dtype) { return dtype == SSD_BF16 ? 2 : 4; }
+bool type_ok(int dtype) { return dtype == SSD_F32 || dtype == SSD_BF16; }
+
+#define DELTA_TRY(expr)                \
+    do {                               \
+        ssd_status _s = (expr);        \
+        if (_s != SSD_OK) return _s;   \
+    } while (0)
+
+int64_t nstates(const ssd_delta_problem *p) { return p->nseqs ? p->nseqs : p->batch; }
+int64_t slots(const ssd_delta_problem *p) {
+    return p->seqlen == 0 ? 0 : p->nseqs ? p->seqlen / DQ + p->nseqs : p->batch * ((p->seqlen + DQ - 1) / DQ);
+}
+
+ssd_status check_problem(const ssd_delta_problem *p) {
+    if (p == nullptr) return SSD_ERR_INVALID_ARGUMENT;
+    if (p->batch < 1 || p->seqlen < 0 || p->nheads < 1 || p->ngroups < 1 || p->headdim < 1 || p->dstate < 1 || p->nseqs < 0 ||
+        p->nheads % p->ngroups != 0 || (p->nseqs > 0 && p->batch != 1) || !type_ok(p->dtype))
+        return SSD_ERR_INVALID_ARGUMENT;
+    if (p->headdim > 256 || p->dstate > 256) return SSD_ERR_UNSUPPORTED;
+    // counters of tokens, chunks and blocks are 32-bit; element offsets are 64-bit
+    if (p->batch > ((int64_t)1 << 24) || p->seqlen > ((int64_t)1 << 30) || p->nheads > ((int64_t)1 << 16) || p->nseqs > ((int64_t)1 << 24) ||
+        nstates(p) * p->nheads > ((int64_t)1 << 27) || p->batch * (p->seqlen / DQ + 1) > ((int64_t)1 << 30) || slots(p) * p->nheads > ((int64_t)1 << 30))
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+// A token tensor [batch, seqlen, n (, inner)].  What is read may have any strides but negative ones; what is written
+// has rows that do not meet in any of its dimensions.
+ssd_status check_tok(const ssd_delta_problem *p, const ssd_tensor &t, int dtype, int64_t n, int64_t inner, bool written) {
+    if (p->seqlen == 0) return SSD_OK;
+    if (t.ptr == nullptr || t.dtype != dtype || (inner > 1 && t.stride[3] != 1)) return SSD_ERR_INVALID_ARGUMENT;
+    const int64_t size[3] = {p->batch, p->seqlen, n};
+    for (int i = 0; i < 3; ++i)
+        if (size[i] > 1 && t.stride[i] < (written ? inner : 0)) return SSD_ERR_INVALID_ARGUMENT;
+    return al(t.ptr, esize(dtype)) ? SSD_OK : SSD_ERR_MISALIGNED;
+}
+ssd_status check_state(const ssd_delta_problem *p, const ssd_tensor &t) {
+    if (t.ptr == nullptr) return SSD_OK;
+    if (!type_ok(t.dtype) || (p->dstate > 1 && t.stride[3] != 1) || (p->headdim > 1 && t.stride[2] != p->dstate) ||
+        (p->nheads > 1 && t.stride[1] != p->headdim * p->dstate) || (nstates(p) > 1 && t.stride[0] != p->nheads * p->headdim * p->dstate))
+        return SSD_ERR_INVALID_ARGUMENT;
+    return al(t.ptr, esize(t.dtype)) ? SSD_OK : SSD_ERR_MISALIGNED;
+}
+ssd_status check_inputs(const ssd_delta_problem *p, const ssd_delta_args *a) {
+    DELTA_TRY(check_problem(p));
+    if (a == nullptr || (a->cu_seqlens != nullptr) != (p->nseqs > 0)) return SSD_ERR_INVALID_ARGUMENT;
+    for (const ssd_tensor *t : {&a->g, &a->beta})
+        if (p->seqlen > 0 && t->dtype != SSD_F32 && t->dtype != p->dtype) return SSD_ERR_INVALID_ARGUMENT;
+    DELTA_TRY(check_tok(p, a->q, p->dtype, p->ngroups, p->dstate, false));
+    DELTA_TRY(check_tok(p, a->k, p->dtype, p->ngroups, p->dstate, false));
+    DELTA_TRY(check_tok(p, a->v, p->dtype, p->nheads, p->headdim, false));
+    DELTA_TRY(check_tok(p, a->g, a->g.dtype, p->nheads, 1, false));
+    DELTA_TRY(check_tok(p, a->beta, a->beta.dtype, p->nheads, 1, false));
+    DELTA_TRY(check_state(p, a->initial_states));
+    if (!al(a->chunk_states, 256)) return SSD_ERR_MISALIGNED;
+    if (!al(a->cu_seqlens, 4)) return SSD_ERR_MISALIGNED;
+    return SSD_OK;
+}
+
+// What the forward keeps and the backward starts from: the state that enters each chunk, and U.
+struct Kept {
+    size_t S, U, total;
+};
+Kept kept_plan(const ssd_delta_problem *p) {
+    const size_t ch = (size_t)slots(p) * p->nheads;
+    Kept k;
+    k.S = 0;
+    k.U = up256(ch * p->headdim * p->dstate * 4);
+    k.total = k.U + up256(ch * DQ * p->headdim * 4);
+    return k;
+}
+struct Plan {
+    size_t gates, sys, att, a, dS, mu, part, kept, total;
+};
+Plan plan(const ssd_delta_problem *p, bool back, bool kept) {
+    const size_t ch = (size_t)slots(p) * p->nheads, mat = up256(ch * DQ * DQ * 4);
+    Plan w{};
+    size_t at = 0;
+    auto take = [&](size_t n) { const size_t o = at; at += up256(n); return o; };
+    w.gates = take(ch * DGATES * 4);
+    w.sys = take(mat);
+    w.att = take(mat);
+    if (back) {
+        w.a = take(mat);
+        w.dS = take(ch * p->headdim * p->dstate * 4);
+        w.mu = take(ch * DQ * p->headdim * 4);
+        w.part = take(p->nheads > p->ngroups ? 2 * ch * DQ * p->dstate * 4 : 0);
+        w.kept = take(kept ? 0 : kept_plan(p).total);
+    }
+    w.total = at;
+    return w;
+}
+
+void set3(int64_t *to, const ssd_tensor &t) {
+    for (int i = 0; i < 3; ++i) to[i] = t.stride[i];
+}
+DeltaArgs make(const ssd_delta_problem *p, const ssd_delta_args *f, const Plan &w, uint8_t *ws) {
+    DeltaArgs a{};
+    a.q = f->q.ptr; a.k = f->k.ptr; a.v = f->v.ptr; a.g = f->g.ptr; a.beta = f->beta.ptr;
+    set3(a.qs, f->q); set3(a.ks, f->k); set3(a.vs, f->v); set3(a.gs, f->g); set3(a.bs, f->beta);
+    a.init = f->initial_states.ptr;
+    a.init_bf16 = f->initial_states.dtype == SSD_BF16;
+    a.g_f32 = f->g.dtype == SSD_F32; a.beta_f32 = f->beta.dtype == SSD_F32;
+    a.cu = f->cu_seqlens;
+    a.seqlen = (int)p->seqlen; a.H = (int)p->nheads; a.G = (int)p->ngroups; a.V = (int)p->headdim; a.K = (int)p->dstate;
+    a.nseqs = (int)nstates(p); a.nslots = (int)slots(p);
+    a.scale = p->scale;
+    a.gates = reinterpret_cast<float *>(ws + w.gates);
+    a.sys = reinterpret_cast<float *>(ws + w.sys);
+    a.att = reinterpret_cast<float *>(ws + w.att);
+    a.a = reinterpret_cast<float *>(ws + w.a);
+    return a;
+}
+void set_kept(DeltaArgs &a, const ssd_delta_problem *p, void *at) {
+    const Kept k = kept_plan(p);
+    a.S = static_cast<uint8_t *>(at) + k.S;
+    a.U = static_cast<uint8_t *>(at) + k.U;
+}
+ssd_status check_workspace(const void *ws, size_t bytes, size_t need) {
+    if (need == 0) return SSD_OK;
+    if (ws == nullptr || bytes < need) return SSD_ERR_WORKSPACE_TOO_SMALL;
+    return al(ws, 256) ? SSD_OK : SSD_ERR_MISALIGNED;
+}
+ssd_status of_cuda(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+ssd_status ssd_delta_chunk_states_size(const ssd_delta_problem *p, size_t *bytes) {
+    if (bytes == nullptr) return SSD_ERR_INVALID_ARGUMENT;
+    DELTA_TRY(check_problem(p));
+    *bytes = kept_plan(p).total;
+    return SSD_OK;
+}
+ssd_status ssd_delta_fwd_workspace_size(const ssd_delta_problem *p, size_t *bytes) {
+    if (bytes == nullptr) return SSD_ERR_INVALID_ARGUMENT;
+    DELTA_TRY(check_problem(p));
+    *bytes = plan(p, false, false).total;
+    return SSD_OK;
+}
+ssd_status ssd_delta_bwd_workspace_size(const ssd_delta_problem *p, int32_t kept, size_t *bytes) {
+    if (bytes == nullptr) return SSD_ERR_INVALID_ARGUMENT;
+    DELTA_TRY(check_problem(p));
+    *bytes = plan(p, true, kept != 0).total;
+    return SSD_OK;
+}
+
+ssd_status ssd_delta_fwd(const ssd_delta_problem *p, const ssd_delta_args *f, void *workspace, size_t workspace_bytes, void *stream) {
+    DELTA_TRY(check_inputs(p, f));
+    DELTA_TRY(check_tok(p, f->o, p->dtype, p->nheads, p->headdim, true));
+    DELTA_TRY(check_state(p, f->final_states));
+    const Plan w = plan(p, false, false);
+    DELTA_TRY(check_workspace(workspace, workspace_bytes, w.total));
+    DeltaArgs a = make(p, f, w, static_cast<uint8_t *>(workspace));
+    a.o = f->o.ptr;
+    set3(a.os, f->o);
+    a.final = f->final_states.ptr;
+    a.final_bf16 = f->final_states.dtype == SSD_BF16;
+    if (f->chunk_states) set_kept(a, p, f->chunk_states);
+    return of_cuda(delta_simt_fwd(a, p->dtype == SSD_BF16, (cudaStream_t)stream));
+}
+
+ssd_status ssd_delta_bwd(const ssd_delta_problem *p, const ssd_delta_bwd_args *b, void *workspace, size_t workspace_bytes, void *stream) {
+    if (b == nullptr) return SSD_ERR_INVALID_ARGUMENT;
+    const ssd_delta_args *f = &b->fwd;
+    DELTA_TRY(check_inputs(p, f));
+    DELTA_TRY(check_tok(p, b->dO, p->dtype, p->nheads, p->headdim, false));
+    DELTA_TRY(check_tok(p, b->dq, p->dtype, p->ngroups, p->dstate, true));
+    DELTA_TRY(check_tok(p, b->dk, p->dtype, p->ngroups, p->dstate, true));
+    DELTA_TRY(check_tok(p, b->dv, p->dtype, p->nheads, p->headdim, true));
+    DELTA_TRY(check_tok(p, b->dg, f->g.dtype, p->nheads, 1, true));
+    DELTA_TRY(check_tok(p, b->dbeta, f->beta.dtype, p->nheads, 1, true));
+    DELTA_TRY(check_state(p, b->dfinal_states));
+    if (f->initial_states.ptr && b->dinitial_states.ptr == nullptr) return SSD_ERR_INVALID_ARGUMENT;
+    DELTA_TRY(check_state(p, b->dinitial_states));
+    const bool kept = f->chunk_states != nullptr;
+    const Plan w = plan(p, true, kept);
+    DELTA_TRY(check_workspace(workspace, workspace_bytes, w.total));
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const bool bf16 = p->dtype == SSD_BF16;
+    cudaStream_t st = (cudaStream_t)stream;
+    DeltaArgs a = make(p, f, w, ws);
+    set_kept(a, p, kept ? f->chunk_states : ws + w.kept);
+    if (!kept && p->seqlen > 0) DELTA_TRY(of_cuda(delta_simt_fwd(a, bf16, st)));
+    a.dO = b->dO.ptr; set3(a.dos, b->dO);
+    a.dq = b->dq.ptr; set3(a.dqs, b->dq);
+    a.dk = b->dk.ptr; set3(a.dks, b->dk);
+    a.dv = b->dv.ptr; set3(a.dvs, b->dv);
+    a.dg = b->dg.ptr; set3(a.dgs, b->dg);
+    a.dbeta = b->dbeta.ptr; set3(a.dbs, b->dbeta);
+    a.dfinal = b->dfinal_states.ptr; a.dfinal_bf16 = b->dfinal_states.dtype == SSD_BF16;
+    a.dinit = b->dinitial_states.ptr; a.dinit_bf16 = b->dinitial_states.dtype == SSD_BF16;
+    a.dS = ws + w.dS;
+    a.mu = ws + w.mu;
+    a.part = p->nheads > p->ngroups ? reinterpret_cast<float *>(ws + w.part) : nullptr;
+    return of_cuda(delta_simt_bwd(a, bf16, st));
+}
+
+}  // extern "C"

@@ -1,0 +1,203 @@
+// delta.cuh -- what the gated delta rule's kernels share: the arguments of a call, the chunks of its sequences, the
+// gates of a chunk and the inverse of its triangular system.
+//
+// Per value head, with a state S [headdim][dstate] and k, q of the head's group:
+//
+//   S <- e^g S,  u = beta (v - S k),  S <- S + u k^T,  o = scale S q
+//
+// In chunks of 64 tokens, G the sum of g from the chunk's first token on, S the state that enters it, and
+// a_ij = e^(G_i - G_j) k_i.k_j below the diagonal (rows of K, Q, V are tokens):
+//
+//   U = (I + a diag(beta))^-1 (V - e^G K S^T),  W = beta U,  O = scale (e^G Q S^T + att W),  att_ij = e^(G_i - G_j) q_i.k_j, j <= i
+//   S' = e^Gc S + (e^(Gc - G) W)^T K
+//
+// and backwards, from dS' and dO:
+//
+//   N = scale att^T dO + e^(Gc - G) K dS'^T,  mu = (I + diag(beta) a)^-T N,  lam = beta mu
+//   dS = e^Gc dS' + (scale e^G dO)^T Q - (e^G lam)^T K
+//   E_ij = -e^(G_i - G_j) lam_i.W_j (j < i),  F_ij = scale e^(G_i - G_j) dO_i.W_j (j <= i)
+//   dQ = F K + scale e^G dO S,  dK = (E + E^T) K + F^T Q - e^G lam S + e^(Gc - G) W dS',  dV = lam,  dbeta = mu.U
+//   dg_t = sum over i >= t > j of (F_ij q_i.k_j + E_ij k_i.k_j)            (what crosses token t inside the chunk)
+//        + sum over i >= t of (scale e^G_i q_i.(dO S)_i - e^G_i k_i.(lam S)_i)       (what comes from before it)
+//        + sum over j < t of e^(Gc - G_j) k_j.(W dS')_j + e^Gc <dS', S>               (what leaves it, and what passes)
+//
+// Both ways the sequential part (the chain) is the same: a product with the state, a product with the inverse, a
+// product with K onto the state.
+#pragma once
+
+#include "f32x2.cuh"
+
+namespace ssd {
+
+constexpr int DQ = 64;          // tokens of a chunk
+constexpr int DGATES = 5 * DQ;  // of a chunk and head: e^G, e^(Gc - G), beta, G as the sum of two floats
+
+struct DeltaArgs {
+    const void *q, *k, *v, *g, *beta, *dO;
+    int64_t qs[3], ks[3], vs[3], gs[3], bs[3], dos[3];   // element strides: batch row, token, group or head
+    const void *init, *dfinal;
+    void *o, *final, *dq, *dk, *dv, *dg, *dbeta, *dinit;
+    int64_t os[3], dqs[3], dks[3], dvs[3], dgs[3], dbs[3];
+    bool g_f32, beta_f32, init_bf16, final_bf16, dfinal_bf16, dinit_bf16;
+    const int32_t *cu;          // packed sequences (batch 1) or NULL
+    int seqlen, H, G, V, K, nseqs, nslots;   // nseqs: batch or packed; nslots: chunks of all sequences, at most
+    float scale;
+    // workspace and kept states
+    float *gates;               // [nslots][H][DGATES]
+    float *sys, *att, *a;       // SIMT: [nslots][H][64][64] each: the inverse, att, and (backward) a
+    void *S, *U;                // state entering each chunk [nslots][H][V][K]; U [nslots][H][64][V]   (kept by a training forward)
+    void *dS, *mu;              // gradient of the state leaving each chunk, mu: the same shapes
+    float *part;                // [2][nslots][H][64][K]: dq and dk of each value head, where heads share a group
+    void *tiles;                // tensor-core path: operand images of every chunk and head
+};
+
+// Sequence s: batch row, first token in the row, length, first chunk.  Whatever cu_seqlens holds, the
+// tokens lie inside the row and the chunks inside [0, nslots).
+struct DeltaSeq {
+    int b, t0, len, slot0;
+};
+__device__ __forceinline__ DeltaSeq delta_seq(const DeltaArgs &a, int s) {
+    DeltaSeq q;
+    if (a.cu == nullptr) {
+        q.b = s; q.t0 = 0; q.len = a.seqlen;
+        q.slot0 = s * ((a.seqlen + DQ - 1) / DQ);
+    } else {
+        q.b = 0;
+        q.t0 = min(max(a.cu[s], 0), a.seqlen);
+        q.len = min(max(a.cu[s + 1], q.t0), a.seqlen) - q.t0;
+        q.slot0 = q.t0 / DQ + s;       // floor(end / 64) + 1 slots on: enough for ceil(len / 64) chunks
+    }
+    return q;
+}
+// Chunk of a slot: batch row, first token, tokens (0: nothing lies in the slot).  Slots of packed sequences
+// ascend, so the sequence is found by halving; one that does not ascend leaves slots empty or taken twice,
+// inside the row all the same.
+struct DeltaChunk {
+    int b, t0, len;
+};
+__device__ __forceinline__ DeltaChunk delta_chunk(const DeltaArgs &a, int slot) {
+    DeltaChunk c;
+    int at;
+    DeltaSeq q;
+    if (a.cu == nullptr) {
+        const int n = (a.seqlen + DQ - 1) / DQ;
+        q = delta_seq(a, slot / n);
+        at = slot % n;
+    } else {
+        int lo = 0, hi = a.nseqs - 1;  // the last sequence whose first slot is at most `slot`
+        while (lo < hi) {
+            const int m = (lo + hi + 1) / 2;
+            if (min(max(a.cu[m], 0), a.seqlen) / DQ + m <= slot) lo = m;
+            else hi = m - 1;
+        }
+        q = delta_seq(a, lo);
+        at = slot - q.slot0;
+    }
+    c.b = q.b;
+    c.t0 = q.t0 + at * DQ;
+    c.len = at < 0 ? 0 : max(0, min(DQ, q.len - at * DQ));
+    return c;
+}
+
+__device__ __forceinline__ float delta_ld(const void *p, bool f32, int64_t at) {
+    return f32 ? static_cast<const float *>(p)[at] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[at]);
+}
+__device__ __forceinline__ void delta_st(void *p, bool f32, int64_t at, float v) {
+    if (f32) static_cast<float *>(p)[at] = v;
+    else static_cast<__nv_bfloat16 *>(p)[at] = __float2bfloat16_rn(v);
+}
+
+// e^(G_i - G_j) of two sums that are each held as two floats: next to a token that forgets nearly everything (g of
+// -300, say) a difference of single floats would be off by 2e-5, and so would every decay after it.
+__device__ __forceinline__ float delta_decay(float hi_i, float lo_i, float hi_j, float lo_j) {
+    return expf((hi_i - hi_j) + (lo_i - lo_j));
+}
+
+// The gates of a chunk by its first warp (lane l: tokens 2l and 2l + 1), into `to` [DGATES].  Tokens past the
+// chunk's end keep the state as it is (g = 0) and write nothing (beta = 0).  A g below -200, -inf among
+// them, is taken as -200: its exponential is 0 in fp32 either way, and sums of such stay finite.
+__device__ __forceinline__ void delta_gates(const DeltaArgs &a, const DeltaChunk &c, int h, float *to, int lane) {
+    double g[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i = 2 * lane + e;
+        float v = 0.f, b = 0.f;
+        if (i < c.len) {
+            v = delta_ld(a.g, a.g_f32, c.b * a.gs[0] + (int64_t)(c.t0 + i) * a.gs[1] + h * a.gs[2]);
+            b = delta_ld(a.beta, a.beta_f32, c.b * a.bs[0] + (int64_t)(c.t0 + i) * a.bs[1] + h * a.bs[2]);
+        }
+        g[e] = v < -200.f ? -200.f : v;
+        to[2 * DQ + i] = b;
+    }
+    g[1] += g[0];
+    double sum = g[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double t = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += t;
+    }
+    const double before = sum - g[1], all = __shfl_sync(0xffffffffu, sum, 31);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i = 2 * lane + e;
+        const double G = before + g[e];
+        const float hi = (float)G;
+        to[i] = expf((float)G);
+        to[DQ + i] = expf((float)(all - G));
+        to[3 * DQ + i] = hi;
+        to[4 * DQ + i] = (float)(G - (double)hi);
+    }
+}
+
+// Inverse of I + M, M strictly lower triangular 64 x 64, in place in shared memory (row stride LD), by 256 threads: the
+// four 16 x 16 blocks on the diagonal by substitution, a thread a column; then twice the block below the
+// diagonal of a pair, -T22 M21 T11 (t: 32 x 33 floats of scratch).  M's upper part and diagonal are written, not read.
+template <int LD>
+__device__ __forceinline__ void delta_invert(float *M, float *t, int tid) {
+    if (tid < 64) {
+        const int o = tid / 16 * 16, j = tid & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == j ? 1.f : 0.f;
+#pragma unroll
+            for (int l = 0; l < i; ++l) s = fmaf(-M[(o + i) * LD + o + l], x[l], s);
+            x[i] = s;
+        }
+        __syncwarp();
+        // every column of a block is read by its sixteen threads before one of them writes: they are in one warp
+#pragma unroll
+        for (int i = 0; i < 16; ++i) M[(o + i) * LD + o + j] = x[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 16; n <= 32; n *= 2) {
+        // pairs of n x n blocks: two of 16, one of 32; t = M21 T11, then M21 = -T22 t
+        for (int e = tid; e < 32 * n; e += 256) {
+            const int p = e / (n * n), i = e / n % n, j = e % n, o = p * 2 * n;
+            float s = 0.f;
+            for (int l = 0; l < n; ++l) s = fmaf(M[(o + n + i) * LD + o + l], M[(o + l) * LD + o + j], s);
+            t[(p * n + i) * 33 + j] = s;
+        }
+        __syncthreads();
+        for (int e = tid; e < 32 * n; e += 256) {
+            const int p = e / (n * n), i = e / n % n, j = e % n, o = p * 2 * n;
+            float s = 0.f;
+            for (int l = 0; l <= i; ++l) s = fmaf(-M[(o + n + i) * LD + o + n + l], t[(p * n + l) * 33 + j], s);
+            M[(o + n + i) * LD + o + j] = s;
+        }
+        __syncthreads();
+    }
+    // above the diagonal blocks
+    for (int e = tid; e < 64 * 64; e += 256) {
+        const int i = e / 64, j = e % 64;
+        if (j / 16 > i / 16) M[i * LD + j] = 0.f;
+    }
+    __syncthreads();
+}
+
+// delta_simt.cu: any type and size.  states: leave a.S and a.U (and no o, where a.o is NULL).
+cudaError_t delta_simt_fwd(const DeltaArgs &a, bool bf16, cudaStream_t st);
+cudaError_t delta_simt_bwd(const DeltaArgs &a, bool bf16, cudaStream_t st);
+
+}  // namespace ssd

@@ -1,0 +1,546 @@
+// delta_simt.cu -- the gated delta rule in plain fp32 arithmetic, for every type and size that the tensor-core path
+// does not take (fp32 data among them, which is computed in fp32 throughout).
+//
+// Four kernels (formulas in delta.cuh): k_prep, a block a chunk and head: the triangular system's inverse and att;
+// k_chain, a block a sequence, head and 32 values, from chunk to chunk with its rows of the state in shared memory,
+// forwards (o, states, U) or backwards (mu, dS); k_grads, a block a chunk and head: everything else of the
+// gradients; k_share, the sum over the heads that share a group.  Products go through shared memory in slices of 32,
+// a thread a few rows and columns of the result.  Bound by the chain's shared-memory reads: one chunk of 64 tokens
+// at dstate 128 takes about 11 us, whatever the number of heads, until the card is full.
+#include "delta.cuh"
+
+namespace ssd {
+
+namespace {
+
+constexpr int NT = 256;
+constexpr int VS = 32;              // values of a chain block
+constexpr int LD = 33;              // row stride of a slice of 32
+constexpr int MLD = 65;             // row stride of a 64 x 64 matrix
+
+// rows [0, 64) of a slice of 32 columns from column k0 of a chunk's rows (row stride `step` elements); zeros past the chunk and past n
+template <typename T>
+__device__ __forceinline__ void load_slice(float *to, const T *p, int64_t step, int len, int k0, int n, int tid) {
+    for (int e = tid; e < 64 * 32; e += NT) {
+        const int i = e / 32, c = e % 32;
+        to[i * LD + c] = i < len && k0 + c < n ? to_f(p[i * step + k0 + c]) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ const T *rows_of(const void *p, const int64_t *s, const DeltaChunk &c, int h) {
+    return static_cast<const T *>(p) + c.b * s[0] + c.t0 * s[1] + h * s[2];
+}
+// R x 2 of a product over a slice: rows i = 16 r + ty of A [64][LD] (n of them: R = n / 16), columns 2 tx and 2 tx + 1 of B^T [32][..]
+template <int R>
+__device__ __forceinline__ void fma_slice(float (&acc)[R][2], const float *A, int lda, const float *B, int ldb, int n, int ty, int tx) {
+#pragma unroll 8
+    for (int l = 0; l < n; ++l) {
+        const float b0 = B[l * ldb + 2 * tx], b1 = B[l * ldb + 2 * tx + 1];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float x = A[(16 * r + ty) * lda + l];
+            acc[r][0] = fmaf(x, b0, acc[r][0]);
+            acc[r][1] = fmaf(x, b1, acc[r][1]);
+        }
+    }
+}
+// the same with A given by columns: A^T [n][lda]
+template <int R>
+__device__ __forceinline__ void fma_slice_t(float (&acc)[R][2], const float *A, int lda, const float *B, int ldb, int n, int ty, int tx) {
+#pragma unroll 8
+    for (int l = 0; l < n; ++l) {
+        const float b0 = B[l * ldb + 2 * tx], b1 = B[l * ldb + 2 * tx + 1];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float x = A[l * lda + 16 * r + ty];
+            acc[r][0] = fmaf(x, b0, acc[r][0]);
+            acc[r][1] = fmaf(x, b1, acc[r][1]);
+        }
+    }
+}
+
+// ---- the chunk's matrices: sys = (I + a diag(beta))^-1 or, backwards, (I + diag(beta) a)^-1; att; a.
+template <typename T>
+__global__ void __launch_bounds__(NT) k_prep(const DeltaArgs a, const bool back) {
+    __shared__ float Ks[64 * LD], Qs[64 * LD], M[64 * MLD], gate[DGATES];
+    const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
+    const DeltaChunk c = delta_chunk(a, slot);
+    if (c.len == 0) return;
+    const int grp = h / (a.H / a.G);
+    if (tid < 32) delta_gates(a, c, h, gate, tid);
+    const T *q = rows_of<T>(a.q, a.qs, c, grp), *k = rows_of<T>(a.k, a.ks, c, grp);
+    const int ty = tid / 16, tx = tid % 16;
+    float kk[4][4], qk[4][4];          // rows 16 r + ty, columns 16 s + tx
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) kk[r][s] = qk[r][s] = 0.f;
+    for (int k0 = 0; k0 < a.K; k0 += 32) {
+        __syncthreads();
+        load_slice(Ks, k, a.ks[1], c.len, k0, a.K, tid);
+        load_slice(Qs, q, a.qs[1], c.len, k0, a.K, tid);
+        __syncthreads();
+#pragma unroll 4
+        for (int l = 0; l < 32; ++l) {
+            float kr[4], qr[4], kc[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                kr[r] = Ks[(16 * r + ty) * LD + l];
+                qr[r] = Qs[(16 * r + ty) * LD + l];
+                kc[r] = Ks[(16 * r + tx) * LD + l];
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    kk[r][s] = fmaf(kr[r], kc[s], kk[r][s]);
+                    qk[r][s] = fmaf(qr[r], kc[s], qk[r][s]);
+                }
+        }
+    }
+    const int64_t at = ((int64_t)slot * a.H + h) * 4096;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int i = 16 * r + ty, j = 16 * s + tx;
+            const float d = j <= i ? delta_decay(gate[3 * DQ + i], gate[4 * DQ + i], gate[3 * DQ + j], gate[4 * DQ + j]) : 0.f;
+            a.att[at + i * 64 + j] = j <= i ? d * qk[r][s] : 0.f;
+            const float low = j < i ? d * kk[r][s] : 0.f;
+            if (back) a.a[at + i * 64 + j] = low;
+            M[i * MLD + j] = j < i ? low * gate[2 * DQ + (back ? i : j)] : 0.f;
+        }
+    if (tid < DQ)
+#pragma unroll
+        for (int e = 0; e < 5; ++e) a.gates[((int64_t)slot * a.H + h) * DGATES + e * DQ + tid] = gate[e * DQ + tid];
+    __syncthreads();
+    delta_invert<MLD>(M, Ks, tid);
+    for (int e = tid; e < 4096; e += NT) a.sys[at + e] = M[e / 64 * MLD + e % 64];
+}
+
+__device__ __forceinline__ void load_matrix(float *to, const float *p, int tid) {
+    for (int e = tid; e < 4096; e += NT) to[e / 64 * MLD + e % 64] = p[e];
+}
+
+// ---- the chain.  Shared memory: the state's rows [VS][KP], a slice of K and of Q, two [64][LD] of this block's
+// values, a 64 x 64 matrix, the gates.
+__host__ __device__ constexpr int chain_floats(int KP) { return VS * (KP + 1) + 4 * 64 * LD + 64 * MLD + DGATES; }
+
+template <typename T, bool BACK>
+__global__ void __launch_bounds__(NT) k_chain(const DeltaArgs a) {
+    extern __shared__ float sm[];
+    const int KP = (a.K + 31) / 32 * 32, SLD = KP + 1;
+    float *S = sm, *Ks = S + VS * SLD, *Qs = Ks + 64 * LD, *Y = Qs + 64 * LD, *Z = Y + 64 * LD, *M = Z + 64 * LD, *gate = M + 64 * MLD;
+    const int nv = (a.V + VS - 1) / VS, tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+    const int v0 = blockIdx.x % nv * VS, h = blockIdx.x / nv % a.H, s = blockIdx.x / nv / a.H, grp = h / (a.H / a.G);
+    const DeltaSeq q = delta_seq(a, s);
+    const int64_t sat = ((int64_t)s * a.H + h) * a.V * a.K;
+    const void *in = BACK ? a.dfinal : a.init;
+    const bool in16 = BACK ? a.dfinal_bf16 : a.init_bf16;
+    for (int e = tid; e < VS * KP; e += NT) {
+        const int v = e / KP, k = e % KP;
+        S[v * SLD + k] = in && v0 + v < a.V && k < a.K ? delta_ld(in, !in16, sat + (int64_t)(v0 + v) * a.K + k) : 0.f;
+    }
+    const int nch = (q.len + DQ - 1) / DQ;
+    float *kept = static_cast<float *>(BACK ? a.dS : a.S), *vals = static_cast<float *>(BACK ? a.mu : a.U);
+    for (int n = 0; n < nch; ++n) {
+        const int ci = BACK ? nch - 1 - n : n;
+        const DeltaChunk c{q.b, q.t0 + ci * DQ, min(DQ, q.len - ci * DQ)};
+        const int64_t ch = (int64_t)(q.slot0 + ci) * a.H + h;
+        const T *kp = rows_of<T>(a.k, a.ks, c, grp), *qp = rows_of<T>(a.q, a.qs, c, grp);
+        __syncthreads();
+        for (int e = tid; e < DGATES; e += NT) gate[e] = a.gates[ch * DGATES + e];
+        if (kept)
+            for (int e = tid; e < VS * KP; e += NT) {
+                const int v = e / KP, k = e % KP;
+                if (v0 + v < a.V && k < a.K) kept[(ch * a.V + v0 + v) * a.K + k] = S[v * SLD + k];
+            }
+        // P = K S^T and, forwards, Q S^T: the state's rows as columns
+        float P[4][2] = {}, O[4][2] = {};
+        for (int k0 = 0; k0 < KP; k0 += 32) {
+            __syncthreads();
+            load_slice(Ks, kp, a.ks[1], c.len, k0, a.K, tid);
+            if (!BACK) load_slice(Qs, qp, a.qs[1], c.len, k0, a.K, tid);
+            __syncthreads();
+#pragma unroll 8
+            for (int l = 0; l < 32; ++l) {
+                const float b0 = S[2 * tx * SLD + k0 + l], b1 = S[(2 * tx + 1) * SLD + k0 + l];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float x = Ks[(16 * r + ty) * LD + l];
+                    P[r][0] = fmaf(x, b0, P[r][0]);
+                    P[r][1] = fmaf(x, b1, P[r][1]);
+                    if (!BACK) {
+                        const float y = Qs[(16 * r + ty) * LD + l];
+                        O[r][0] = fmaf(y, b0, O[r][0]);
+                        O[r][1] = fmaf(y, b1, O[r][1]);
+                    }
+                }
+            }
+        }
+        const T *vp = BACK ? rows_of<T>(a.dO, a.dos, c, h) : rows_of<T>(a.v, a.vs, c, h);
+        const int64_t vstep = BACK ? a.dos[1] : a.vs[1];
+        __syncthreads();
+        load_matrix(M, BACK ? a.att + ch * 4096 : a.sys + ch * 4096, tid);
+        float N[4][2] = {};
+        if (BACK) {                                        // N = scale att^T dO + e^(Gc - G) P
+            load_slice(Z, vp, vstep, c.len, v0, a.V, tid);
+            __syncthreads();
+            fma_slice_t(N, M, MLD, Z, LD, 64, ty, tx);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 16 * r + ty, v = 2 * tx + e;
+                float y;
+                if (BACK) y = fmaf(gate[DQ + i], P[r][e], a.scale * N[r][e]);
+                else y = (i < c.len && v0 + v < a.V ? to_f(vp[i * vstep + v0 + v]) : 0.f) - gate[i] * P[r][e];
+                Y[i * LD + v] = y;
+            }
+        __syncthreads();
+        if (BACK) {
+            load_matrix(M, a.sys + ch * 4096, tid);
+            __syncthreads();
+        }
+        float U[4][2] = {};
+        if (BACK) fma_slice_t(U, M, MLD, Y, LD, 64, ty, tx);
+        else fma_slice(U, M, MLD, Y, LD, 64, ty, tx);
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 16 * r + ty, v = 2 * tx + e;
+                if (vals && v0 + v < a.V) vals[(ch * 64 + i) * a.V + v0 + v] = U[r][e];
+                Y[i * LD + v] = gate[2 * DQ + i] * U[r][e];     // W, or lam
+            }
+        if (!BACK && a.o) {
+            load_matrix(M, a.att + ch * 4096, tid);
+            __syncthreads();
+            float A[4][2] = {};
+            fma_slice(A, M, MLD, Y, LD, 64, ty, tx);
+            T *op = static_cast<T *>(a.o) + c.b * a.os[0] + c.t0 * a.os[1] + h * a.os[2] + v0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = 16 * r + ty, v = 2 * tx + e;
+                    if (i < c.len && v0 + v < a.V) op[i * a.os[1] + v] = from_f<T>(a.scale * fmaf(gate[i], O[r][e], A[r][e]));
+                }
+        }
+        // the state: rows v = 16 r + ty, columns of a slice
+        const float whole = gate[DQ - 1];
+        __syncthreads();
+        for (int e = tid; e < 64 * VS; e += NT) {
+            const int i = e / VS, v = e % VS;
+            if (BACK) {
+                Z[i * LD + v] *= a.scale * gate[i];           // scale e^G dO
+                Y[i * LD + v] *= -gate[i];                    // -e^G lam
+            } else {
+                Y[i * LD + v] *= gate[DQ + i];                // e^(Gc - G) W
+            }
+        }
+        for (int k0 = 0; k0 < KP; k0 += 32) {
+            __syncthreads();
+            load_slice(Ks, kp, a.ks[1], c.len, k0, a.K, tid);
+            if (BACK) load_slice(Qs, qp, a.qs[1], c.len, k0, a.K, tid);
+            __syncthreads();
+            float D[2][2] = {};
+            fma_slice_t(D, Y, LD, Ks, LD, 64, ty, tx);
+            if (BACK) fma_slice_t(D, Z, LD, Qs, LD, 64, ty, tx);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float &x = S[(16 * r + ty) * SLD + k0 + 2 * tx + e];
+                    x = fmaf(whole, x, D[r][e]);
+                }
+        }
+    }
+    __syncthreads();
+    void *out = BACK ? a.dinit : a.final;
+    const bool out16 = BACK ? a.dinit_bf16 : a.final_bf16;
+    if (out)
+        for (int e = tid; e < VS * KP; e += NT) {
+            const int v = e / KP, k = e % KP;
+            if (v0 + v < a.V && k < a.K) delta_st(out, !out16, sat + (int64_t)(v0 + v) * a.K + k, S[v * SLD + k]);
+        }
+}
+
+// rows [0, 64) x 32 columns from column c0 of a contiguous fp32 matrix of n columns, row i times f[i]
+__device__ __forceinline__ void load_plain(float *to, const float *p, int rows, int c0, int n, const float *f, int tid) {
+    for (int e = tid; e < 64 * 32; e += NT) {
+        const int i = e / 32, c = e % 32;
+        to[i * LD + c] = i < rows && c0 + c < n ? p[(int64_t)i * n + c0 + c] * (f ? f[i] : 1.f) : 0.f;
+    }
+}
+__device__ __forceinline__ float row16(float v) {                  // sum over the 16 threads that share a row
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// ---- a chunk's gradients.  Shared memory: E + E^T and F (64 x 64), four slices, the gates, sums per row.
+constexpr int GRADS_FLOATS = 2 * 64 * MLD + 4 * 64 * LD + DGATES + 5 * 64 + 64 + 8;
+
+template <typename T>
+__global__ void __launch_bounds__(NT) k_grads(const DeltaArgs a) {
+    extern __shared__ float sm[];
+    float *E = sm, *F = E + 64 * MLD, *s0 = F + 64 * MLD, *s1 = s0 + 64 * LD, *s2 = s1 + 64 * LD, *s3 = s2 + 64 * LD;
+    float *gate = s3 + 64 * LD, *R = gate + DGATES, *X = R + 64, *flow = X + 64, *fg = flow + 64, *fd = fg + 64, *fl = fd + 64, *red = fl + 64;
+    const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, grp = h / (a.H / a.G), tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+    const DeltaChunk c = delta_chunk(a, slot);
+    if (c.len == 0) return;
+    const int64_t ch = (int64_t)slot * a.H + h;
+    const float *U = static_cast<const float *>(a.U) + ch * 64 * a.V, *mu = static_cast<const float *>(a.mu) + ch * 64 * a.V;
+    const float *S = static_cast<const float *>(a.S) + ch * a.V * a.K, *dS = static_cast<const float *>(a.dS) + ch * a.V * a.K;
+    const T *dop = rows_of<T>(a.dO, a.dos, c, h), *kp = rows_of<T>(a.k, a.ks, c, grp), *qp = rows_of<T>(a.q, a.qs, c, grp);
+    for (int e = tid; e < DGATES; e += NT) gate[e] = a.gates[ch * DGATES + e];
+    __syncthreads();
+    const float *beta = gate + 2 * DQ;
+    if (tid < 64) {
+        R[tid] = X[tid] = 0.f;
+        fg[tid] = a.scale * gate[tid];                              // scale e^G
+        fd[tid] = beta[tid] * gate[DQ + tid];                       // e^(Gc - G) beta
+        fl[tid] = -gate[tid] * beta[tid];                           // -e^G beta
+    }
+    // lam_i.W_j and dO_i.W_j; dV = lam; dbeta = mu.U
+    float lw[4][4], ow[4][4];
+    float db[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) lw[r][s] = ow[r][s] = 0.f;
+    for (int v0 = 0; v0 < a.V; v0 += 32) {
+        __syncthreads();
+        load_plain(s0, U, 64, v0, a.V, beta, tid);
+        load_plain(s1, mu, 64, v0, a.V, beta, tid);
+        load_slice(s2, dop, a.dos[1], c.len, v0, a.V, tid);
+        __syncthreads();
+        T *dv = static_cast<T *>(a.dv) + c.b * a.dvs[0] + c.t0 * a.dvs[1] + h * a.dvs[2];
+        for (int e = tid; e < 64 * 32; e += NT) {
+            const int i = e / 32, v = e % 32;
+            if (i < c.len && v0 + v < a.V) dv[i * a.dvs[1] + v0 + v] = from_f<T>(s1[i * LD + v]);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int v = v0 + 2 * tx + e, i = 16 * r + ty;
+                if (v < a.V) db[r] = fmaf(mu[(int64_t)i * a.V + v], U[(int64_t)i * a.V + v], db[r]);
+            }
+#pragma unroll 4
+        for (int l = 0; l < 32; ++l) {
+            float x[4], y[4], w[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                x[r] = s1[(16 * r + ty) * LD + l];
+                y[r] = s2[(16 * r + ty) * LD + l];
+                w[r] = s0[(16 * r + tx) * LD + l];
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    lw[r][s] = fmaf(x[r], w[s], lw[r][s]);
+                    ow[r][s] = fmaf(y[r], w[s], ow[r][s]);
+                }
+        }
+    }
+    // F, E, and what crosses the tokens: W_ij = F_ij q_i.k_j + E_ij k_i.k_j below the diagonal
+    float W[4][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        db[r] = row16(db[r]);
+        const int i = 16 * r + ty;
+        if (tx == 0 && i < c.len) delta_st(a.dbeta, a.beta_f32, c.b * a.dbs[0] + (int64_t)(c.t0 + i) * a.dbs[1] + h * a.dbs[2], db[r]);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int j = 16 * s + tx;
+            const float d = j <= i ? delta_decay(gate[3 * DQ + i], gate[4 * DQ + i], gate[3 * DQ + j], gate[4 * DQ + j]) : 0.f;
+            F[i * MLD + j] = j <= i ? a.scale * ow[r][s] * d : 0.f;
+            E[i * MLD + j] = j < i ? -lw[r][s] * d : 0.f;
+            W[r][s] = j < i ? a.scale * ow[r][s] * a.att[ch * 4096 + i * 64 + j] - lw[r][s] * a.a[ch * 4096 + i * 64 + j] : 0.f;
+        }
+    }
+    // the slices' memory holds W meanwhile; then flow_t = sum over i >= t > j of W_ij
+    __syncthreads();
+    float *Wm = s0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) Wm[(16 * r + ty) * MLD + 16 * s + tx] = W[r][s];
+    __syncthreads();
+    if (tid < 64) {                                                  // along each row: sums before the column
+        float run = 0.f;
+        for (int j = 0; j < 64; ++j) {
+            const float w = Wm[tid * MLD + j];
+            Wm[tid * MLD + j] = run;
+            run += w;
+        }
+    }
+    __syncthreads();
+    if (tid < 64) {
+        float f = 0.f;
+        for (int i = tid; i < 64; ++i) f += Wm[i * MLD + tid];
+        flow[tid] = f;
+    }
+    __syncthreads();
+    // E + E^T
+    for (int e = tid; e < 4096; e += NT) {
+        const int i = e / 64, j = e % 64;
+        if (j < i) E[j * MLD + i] = E[i * MLD + j];
+    }
+    float SS = 0.f;
+    T *dqp = static_cast<T *>(a.dq) + c.b * a.dqs[0] + c.t0 * a.dqs[1] + grp * a.dqs[2];
+    T *dkp = static_cast<T *>(a.dk) + c.b * a.dks[0] + c.t0 * a.dks[1] + grp * a.dks[2];
+    for (int k0 = 0; k0 < a.K; k0 += 32) {
+        float dq[4][2] = {}, kr[4][2] = {}, kw[4][2] = {};
+        for (int v0 = 0; v0 < a.V; v0 += 32) {
+            // scale e^G dO S, -e^G lam S
+            __syncthreads();
+            load_slice(s0, dop, a.dos[1], c.len, v0, a.V, tid);
+            load_plain(s1, mu, 64, v0, a.V, fl, tid);
+            for (int e = tid; e < 32 * 32; e += NT) {
+                const int v = e / 32, k = e % 32;
+                const bool in = v0 + v < a.V && k0 + k < a.K;
+                const float x = in ? S[(int64_t)(v0 + v) * a.K + k0 + k] : 0.f, y = in ? dS[(int64_t)(v0 + v) * a.K + k0 + k] : 0.f;
+                s2[v * LD + k] = x;
+                s2[(32 + v) * LD + k] = y;
+                SS = fmaf(x, y, SS);
+            }
+            load_plain(s3, U, 64, v0, a.V, fd, tid);
+            __syncthreads();
+            fma_slice(dq, s0, LD, s2, LD, 32, ty, tx);
+            fma_slice(kr, s1, LD, s2, LD, 32, ty, tx);
+            fma_slice(kw, s3, LD, s2 + 32 * LD, LD, 32, ty, tx);
+        }
+        __syncthreads();
+        load_slice(s0, kp, a.ks[1], c.len, k0, a.K, tid);
+        load_slice(s1, qp, a.qs[1], c.len, k0, a.K, tid);
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 16 * r + ty;
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float kv = s0[i * LD + 2 * tx + e], qv = s1[i * LD + 2 * tx + e];
+                dq[r][e] *= fg[i];
+                x += qv * dq[r][e] + kv * kr[r][e];
+                y += kv * kw[r][e];
+                kr[r][e] += kw[r][e];
+            }
+            x = row16(x);
+            y = row16(y);
+            if (tx == 0) {
+                R[i] += x;
+                X[i] += y;
+            }
+        }
+        fma_slice(dq, F, MLD, s0, LD, 64, ty, tx);
+        fma_slice(kr, E, MLD, s0, LD, 64, ty, tx);
+        fma_slice_t(kr, F, MLD, s1, LD, 64, ty, tx);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 16 * r + ty, k = k0 + 2 * tx + e;
+                if (i >= c.len || k >= a.K) continue;
+                if (a.part) {
+                    a.part[(ch * 64 + i) * a.K + k] = dq[r][e];
+                    a.part[(((int64_t)a.nslots * a.H + ch) * 64 + i) * a.K + k] = kr[r][e];
+                } else {
+                    dqp[i * a.dqs[1] + k] = from_f<T>(dq[r][e]);
+                    dkp[i * a.dks[1] + k] = from_f<T>(kr[r][e]);
+                }
+            }
+    }
+    SS = warp_sum(SS);
+    if (tid % 32 == 0) red[tid / 32] = SS;
+    __syncthreads();
+    if (tid == 0) {
+        float all = 0.f;
+        for (int w = 0; w < NT / 32; ++w) all += red[w];
+        all *= gate[DQ - 1];
+        float x = 0.f;
+        for (int t = 0; t < 64; ++t) {                               // what left the tokens before t, and what passes all
+            flow[t] += x + all;
+            x += X[t];
+        }
+        float y = 0.f;
+        for (int t = 63; t >= 0; --t) {
+            y += R[t];
+            flow[t] += y;
+        }
+    }
+    __syncthreads();
+    if (tid < c.len) delta_st(a.dg, a.g_f32, c.b * a.dgs[0] + (int64_t)(c.t0 + tid) * a.dgs[1] + h * a.dgs[2], flow[tid]);
+}
+
+// dq and dk of a group: the sum over its heads, in their order
+template <typename T>
+__global__ void __launch_bounds__(NT) k_share(const DeltaArgs a) {
+    const int slot = blockIdx.x / a.G, grp = blockIdx.x % a.G, per = a.H / a.G;
+    const DeltaChunk c = delta_chunk(a, slot);
+    T *dqp = static_cast<T *>(a.dq) + c.b * a.dqs[0] + c.t0 * a.dqs[1] + grp * a.dqs[2];
+    T *dkp = static_cast<T *>(a.dk) + c.b * a.dks[0] + c.t0 * a.dks[1] + grp * a.dks[2];
+    const int64_t other = (int64_t)a.nslots * a.H * 64 * a.K;
+    for (int e = threadIdx.x; e < c.len * a.K; e += NT) {
+        const int i = e / a.K, k = e % a.K;
+        float x = 0.f, y = 0.f;
+        for (int r = 0; r < per; ++r) {
+            const int64_t at = (((int64_t)slot * a.H + grp * per + r) * 64 + i) * a.K + k;
+            x += a.part[at];
+            y += a.part[other + at];
+        }
+        dqp[i * a.dqs[1] + k] = from_f<T>(x);
+        dkp[i * a.dks[1] + k] = from_f<T>(y);
+    }
+}
+
+template <typename T, bool BACK>
+cudaError_t chain(const DeltaArgs &a, cudaStream_t st) {
+    static int set[64] = {};
+    const int bytes = chain_floats((a.K + 31) / 32 * 32) * (int)sizeof(float);
+    if (cudaError_t e = ensure_smem_attr(k_chain<T, BACK>, bytes, set); e != cudaSuccess) return e;
+    k_chain<T, BACK><<<(unsigned)(a.nseqs * (int64_t)a.H * ((a.V + VS - 1) / VS)), NT, bytes, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t fwd(const DeltaArgs &a, cudaStream_t st) {
+    if (a.nslots > 0) {
+        k_prep<T><<<(unsigned)((int64_t)a.nslots * a.H), NT, 0, st>>>(a, false);
+        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    }
+    return chain<T, false>(a, st);
+}
+template <typename T>
+cudaError_t bwd(const DeltaArgs &a, cudaStream_t st) {
+    if (a.nslots > 0) {
+        k_prep<T><<<(unsigned)((int64_t)a.nslots * a.H), NT, 0, st>>>(a, true);
+        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    }
+    if (cudaError_t e = chain<T, true>(a, st); e != cudaSuccess) return e;
+    if (a.nslots == 0) return cudaSuccess;
+    static int set[64] = {};
+    const int bytes = GRADS_FLOATS * (int)sizeof(float);
+    if (cudaError_t e = ensure_smem_attr(k_grads<T>, bytes, set); e != cudaSuccess) return e;
+    k_grads<T><<<(unsigned)((int64_t)a.nslots * a.H), NT, bytes, st>>>(a);
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess || a.part == nullptr) return e;
+    k_share<T><<<(unsigned)((int64_t)a.nslots * a.G), NT, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t delta_simt_fwd(const DeltaArgs &a, bool bf16, cudaStream_t st) {
+    return bf16 ? fwd<__nv_bfloat16>(a, st) : fwd<float>(a, st);
+}
+cudaError_t delta_simt_bwd(const DeltaArgs &a, bool bf16, cudaStream_t st) {
+    return bf16 ? bwd<__nv_bfloat16>(a, st) : bwd<float>(a, st);
+}
+
+}  // namespace ssd

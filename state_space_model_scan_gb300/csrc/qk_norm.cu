@@ -1,0 +1,550 @@
+// qk_norm.cu -- queries and keys normalised per head, weighted and rotated by position, in one pass, and its backward:
+//
+//   n = x rstd w,  rstd = 1 / sqrt(mean x^2 + eps) or 1 / sqrt(sum x^2 + eps)
+//   (y_a, y_b) = (n_a c - n_b s, n_a s + n_b c)
+//   dn = w o (rotation backwards of dy),  dx = rstd (dn - x rstd <dn, x rstd> / (dim or 1)),  dw = sum of (rotated back dy) o x rstd
+//
+// A few operations a value, each value read once (backwards x and dy) and written once: bound by memory.  A head's vector
+// belongs to 32 lanes or a power of two fewer, V neighbouring features each, so that a load is 16 bytes
+// and the partner of a rotated feature lies in another lane's registers (a shuffle) or, interleaved, in
+// the lane's own.  A group of lanes takes HB heads of one token: their loads are all on the way
+// before the first is used, and the token's cosines and sines are loaded once for them.  What the shapes or addresses keep
+// from that goes feature by feature through shared memory.  The weights' gradients are summed in registers over a
+// block's tokens, then over its groups, then by a second launch over the blocks, each in a fixed order.
+#include "selective.cuh"
+
+namespace ssd {
+
+namespace {
+
+constexpr int QK_NT = 256, QK_HB = 4, QK_MAXD = 512;
+constexpr int QK_BLOCKS = 4 * kSMs;     // of the backward, for queries and for keys: each leaves its share of the weights' gradients
+
+struct QkSide {                         // queries, or keys
+    const void *x, *dy;
+    void *y;                            // the output, or dx
+    int64_t xs[3], dys[3], ys[3];       // element strides: batch row, token, head
+    const float *w;
+    int heads, per;                     // heads, blocks of QK_HB heads in a token
+    int64_t items;                      // tokens x per
+    float *share;                       // [blocks of this side][dim], or NULL
+    float *dw;
+};
+struct QkArgs {
+    QkSide side[2];
+    int blocks0, blocks1;               // blocks of either side
+    const float *cos, *sin;
+    const int32_t *pos;
+    int64_t pos_stride;
+    int64_t tokens;
+    int seqlen, dim, half, rows;        // half: rotary / 2; rows: of the table
+    int lpr;
+    float eps, inv;                     // inv: 1 / dim, or 1
+    bool interleaved;
+};
+
+// An item's place: token, first head; and the token's position, -1 for padding.
+struct QkAt {
+    int64_t b;
+    int t, h0, pos;
+};
+__device__ __forceinline__ QkAt qk_at(const QkArgs &a, const QkSide &s, int64_t item) {
+    QkAt q;
+    const int64_t tok = item / s.per;
+    q.h0 = (int)(item - tok * s.per) * QK_HB;
+    q.b = tok / a.seqlen;
+    q.t = (int)(tok - q.b * a.seqlen);
+    q.pos = 0;
+    if (a.half > 0) {
+        q.pos = a.pos ? a.pos[q.b * a.pos_stride + q.t] : q.t;
+        if ((unsigned)q.pos >= (unsigned)a.rows) q.pos = -1;
+    }
+    return q;
+}
+
+// V features at a place divisible by V
+template <typename T, int V>
+struct QkVec {
+    float f[V];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int c = 0; c < V / 8; ++c) {
+                const uint4 u = reinterpret_cast<const uint4 *>(p)[c];
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[8 * c + 2 * e] = __uint_as_float(w[e] << 16);
+                    f[8 * c + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < V / 4; ++c) {
+                const float4 u = reinterpret_cast<const float4 *>(p)[c];
+                f[4 * c] = u.x; f[4 * c + 1] = u.y; f[4 * c + 2] = u.z; f[4 * c + 3] = u.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int c = 0; c < V / 8; ++c) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(f[8 * c + 2 * e], f[8 * c + 2 * e + 1]);
+                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                reinterpret_cast<uint4 *>(p)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < V / 4; ++c)
+                reinterpret_cast<float4 *>(p)[c] = make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[e] = 0.f;
+    }
+};
+
+// The token's cosines and sines for a lane's features, the sines with the sign that the feature's partner gets.
+template <int V, bool INTER>
+struct QkTurn {
+    float c[INTER ? V / 2 : V], s[INTER ? V / 2 : V];
+    int from;                           // lane of the partners
+    bool on;
+    __device__ __forceinline__ void load(const QkArgs &a, int pos, int l, int lane) {
+        const int e0 = l * V;
+        on = e0 < 2 * a.half && pos >= 0;     // (a padding token's outputs are set to zero, and the table may be empty)
+        from = lane;
+        const int64_t row = (int64_t)pos * a.half;
+        if constexpr (INTER) {
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+                c[e] = on ? a.cos[row + e0 / 2 + e] : 1.f;
+                s[e] = on ? a.sin[row + e0 / 2 + e] : 0.f;
+            }
+        } else {
+            const bool second = e0 >= a.half;
+            const int i = second ? e0 - a.half : e0;
+            if (on) {
+                from = second ? lane - a.half / V : lane + a.half / V;
+#pragma unroll
+                for (int e = 0; e < V; e += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(a.cos + row + i + e), y = *reinterpret_cast<const float4 *>(a.sin + row + i + e);
+                    c[e] = x.x; c[e + 1] = x.y; c[e + 2] = x.z; c[e + 3] = x.w;
+                    s[e] = y.x; s[e + 1] = y.y; s[e + 2] = y.z; s[e + 3] = y.w;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) { c[e] = 1.f; s[e] = 0.f; }
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) s[e] = second ? s[e] : -s[e];
+        }
+    }
+    // BACK: by the opposite angle
+    template <bool BACK, typename T>
+    __device__ __forceinline__ void turn(QkVec<T, V> &x, int half) const {
+        if (half == 0) return;
+        if constexpr (INTER) {
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+                const float p = x.f[2 * e], q = x.f[2 * e + 1], sn = BACK ? -s[e] : s[e];
+                x.f[2 * e] = p * c[e] - q * sn;
+                x.f[2 * e + 1] = p * sn + q * c[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float p = __shfl_sync(0xffffffffu, x.f[e], from);
+                x.f[e] = x.f[e] * c[e] + p * (BACK ? -s[e] : s[e]);
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ float qk_group(float v, int lpr) {
+    for (int o = lpr >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <typename T, int V, bool INTER>
+__global__ void __launch_bounds__(QK_NT) k_qk_fwd(const QkArgs a) {
+    after_previous();
+    const bool keys = blockIdx.x >= a.blocks0;
+    const QkSide &s = a.side[keys];
+    const int lane = threadIdx.x & 31, l = lane & (a.lpr - 1), gpb = QK_NT / a.lpr;
+    const int64_t item0 = (int64_t)(blockIdx.x - (keys ? a.blocks0 : 0)) * gpb + threadIdx.x / a.lpr;
+    const bool live = item0 < s.items;                       // (idle groups stay for the shuffles)
+    const QkAt q = qk_at(a, s, live ? item0 : s.items - 1);
+    const bool in = l * V < a.dim;
+    const T *x = static_cast<const T *>(s.x) + q.b * s.xs[0] + q.t * s.xs[1] + l * V;
+    T *y = static_cast<T *>(s.y) + q.b * s.ys[0] + q.t * s.ys[1] + l * V;
+    QkVec<T, V> v[QK_HB];
+    QkTurn<V, INTER> r;
+#pragma unroll
+    for (int u = 0; u < QK_HB; ++u) {
+        if (in && q.h0 + u < s.heads) v[u].load(x + (q.h0 + u) * s.xs[2]);
+        else v[u].zero();
+    }
+    if (a.half > 0) r.load(a, q.pos, l, lane);
+    QkVec<float, V> w;
+    if (s.w && in) {
+        w.load(s.w + l * V);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) w.f[e] = 1.f;
+    }
+#pragma unroll
+    for (int u = 0; u < QK_HB; ++u) {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) m = fmaf(v[u].f[e], v[u].f[e], m);
+        m = qk_group(m, a.lpr);
+        const float rstd = rsqrtf(fmaf(m, a.inv, a.eps));
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[u].f[e] = v[u].f[e] * rstd * w.f[e];
+        r.template turn<false>(v[u], a.half);
+        if (q.pos < 0) v[u].zero();
+        if (live && in && q.h0 + u < s.heads) v[u].store(y + (q.h0 + u) * s.ys[2]);
+    }
+}
+
+template <typename T, int V, bool INTER>
+__global__ void __launch_bounds__(QK_NT) k_qk_bwd(const QkArgs a) {
+    __shared__ float sum[QK_NT * V];
+    const bool keys = blockIdx.x >= a.blocks0;
+    const QkSide &s = a.side[keys];
+    const int lane = threadIdx.x & 31, l = lane & (a.lpr - 1), gpb = QK_NT / a.lpr, grp = threadIdx.x / a.lpr;
+    const int nb = keys ? a.blocks1 : a.blocks0, bi = blockIdx.x - (keys ? a.blocks0 : 0);
+    const bool in = l * V < a.dim;
+    QkVec<float, V> w;
+    if (s.w && in) {
+        w.load(s.w + l * V);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) w.f[e] = 1.f;
+    }
+    float acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    for (int64_t first = (int64_t)bi * gpb; first < s.items; first += (int64_t)nb * gpb) {
+        const bool live = first + grp < s.items;
+        const QkAt q = qk_at(a, s, live ? first + grp : s.items - 1);
+        const T *x = static_cast<const T *>(s.x) + q.b * s.xs[0] + q.t * s.xs[1] + l * V;
+        const T *dy = static_cast<const T *>(s.dy) + q.b * s.dys[0] + q.t * s.dys[1] + l * V;
+        T *dx = static_cast<T *>(s.y) + q.b * s.ys[0] + q.t * s.ys[1] + l * V;
+        QkVec<T, V> xv[QK_HB], dv[QK_HB];
+        QkTurn<V, INTER> r;
+#pragma unroll
+        for (int u = 0; u < QK_HB; ++u) {
+            if (live && in && q.pos >= 0 && q.h0 + u < s.heads) {
+                xv[u].load(x + (q.h0 + u) * s.xs[2]);
+                dv[u].load(dy + (q.h0 + u) * s.dys[2]);
+            } else {
+                xv[u].zero();
+                dv[u].zero();
+            }
+        }
+        if (a.half > 0) r.load(a, q.pos, l, lane);
+#pragma unroll
+        for (int u = 0; u < QK_HB; ++u) {
+            float m = 0.f, d = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) m = fmaf(xv[u].f[e], xv[u].f[e], m);
+            m = qk_group(m, a.lpr);
+            // (a vector that is not there: rstd could be infinite with eps 0)
+            const float rstd = live && q.pos >= 0 && q.h0 + u < s.heads ? rsqrtf(fmaf(m, a.inv, a.eps)) : 0.f;
+            r.template turn<true>(dv[u], a.half);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                xv[u].f[e] *= rstd;
+                acc[e] = fmaf(dv[u].f[e], xv[u].f[e], acc[e]);
+                dv[u].f[e] *= w.f[e];
+                d = fmaf(dv[u].f[e], xv[u].f[e], d);
+            }
+            d = qk_group(d, a.lpr) * a.inv;
+#pragma unroll
+            for (int e = 0; e < V; ++e) dv[u].f[e] = rstd * fmaf(-d, xv[u].f[e], dv[u].f[e]);
+            if (live && in && q.h0 + u < s.heads) dv[u].store(dx + (q.h0 + u) * s.ys[2]);
+        }
+    }
+    if (!s.share) return;
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[(grp * a.lpr + l) * V + e] = acc[e];
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.dim; e += QK_NT) {
+        float t = 0.f;
+        for (int g = 0; g < gpb; ++g) t += sum[g * a.lpr * V + e];
+        s.share[(int64_t)bi * a.dim + e] = t;
+    }
+}
+
+// ---- any shape and address: a warp a head's vector, features 32 apart, the rotation through shared memory.
+template <typename T, bool BACK>
+__global__ void __launch_bounds__(QK_NT) k_qk_any(const QkArgs a) {
+    __shared__ float rows[QK_NT / 32][QK_MAXD], grads[BACK ? QK_NT / 32 : 1][QK_MAXD];
+    const bool keys = blockIdx.x >= a.blocks0;
+    const QkSide &s = a.side[keys];
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, D = a.dim;
+    const int nb = keys ? a.blocks1 : a.blocks0, bi = blockIdx.x - (keys ? a.blocks0 : 0);
+    float *row = rows[wp];
+    if (BACK)
+        for (int e = lane; e < D; e += 32) grads[wp][e] = 0.f;
+    for (int64_t item = (int64_t)bi * (QK_NT / 32) + wp; item < s.items; item += (int64_t)nb * (QK_NT / 32)) {
+        const QkAt q = qk_at(a, s, item);
+        for (int u = 0; u < QK_HB && q.h0 + u < s.heads; ++u) {
+            const T *x = static_cast<const T *>(s.x) + q.b * s.xs[0] + q.t * s.xs[1] + (q.h0 + u) * s.xs[2];
+            T *y = static_cast<T *>(s.y) + q.b * s.ys[0] + q.t * s.ys[1] + (q.h0 + u) * s.ys[2];
+            if (q.pos < 0) {
+                for (int e = lane; e < D; e += 32) y[e] = from_f<T>(0.f);
+                continue;
+            }
+            float m = 0.f;
+            for (int e = lane; e < D; e += 32) m = fmaf(to_f(x[e]), to_f(x[e]), m);
+            const float rstd = rsqrtf(fmaf(warp_sum(m), a.inv, a.eps));
+            __syncwarp();
+            const T *dy = BACK ? static_cast<const T *>(s.dy) + q.b * s.dys[0] + q.t * s.dys[1] + (q.h0 + u) * s.dys[2] : nullptr;
+            for (int e = lane; e < D; e += 32) row[e] = BACK ? to_f(dy[e]) : to_f(x[e]) * rstd * (s.w ? s.w[e] : 1.f);
+            __syncwarp();
+            float d = 0.f;
+            for (int e = lane; e < D; e += 32) {
+                float v = row[e];
+                if (e < 2 * a.half) {
+                    const bool second = a.interleaved ? e & 1 : e >= a.half;
+                    const int i = a.interleaved ? e / 2 : second ? e - a.half : e;
+                    const float p = row[a.interleaved ? e ^ 1 : second ? e - a.half : e + a.half];
+                    const float c = a.cos[(int64_t)q.pos * a.half + i], sn = a.sin[(int64_t)q.pos * a.half + i];
+                    v = v * c + p * (second != BACK ? sn : -sn);
+                }
+                if (BACK) {
+                    const float n = to_f(x[e]) * rstd;
+                    grads[wp][e] = fmaf(v, n, grads[wp][e]);
+                    d = fmaf(v * (s.w ? s.w[e] : 1.f), n, d);
+                } else {
+                    y[e] = from_f<T>(v);
+                }
+            }
+            if (BACK) {
+                d = warp_sum(d) * a.inv;
+                for (int e = lane; e < D; e += 32) {             // the rotation again: nothing holds 16 features a lane
+                    float v = row[e];
+                    if (e < 2 * a.half) {
+                        const bool second = a.interleaved ? e & 1 : e >= a.half;
+                        const int i = a.interleaved ? e / 2 : second ? e - a.half : e;
+                        const float p = row[a.interleaved ? e ^ 1 : second ? e - a.half : e + a.half];
+                        const float c = a.cos[(int64_t)q.pos * a.half + i], sn = a.sin[(int64_t)q.pos * a.half + i];
+                        v = v * c + p * (second ? -sn : sn);
+                    }
+                    y[e] = from_f<T>(rstd * fmaf(-d, to_f(x[e]) * rstd, v * (s.w ? s.w[e] : 1.f)));
+                }
+            }
+        }
+    }
+    if (BACK && s.share) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < D; e += QK_NT) {
+            float t = 0.f;
+            for (int g = 0; g < QK_NT / 32; ++g) t += grads[g][e];
+            s.share[(int64_t)bi * D + e] = t;
+        }
+    }
+}
+
+// sum of the blocks' shares: 32 features a block, eight threads a feature
+__global__ void __launch_bounds__(256) k_qk_dw(const QkArgs a) {
+    __shared__ float part[8][32];
+    const int per = (a.dim + 31) / 32, side = blockIdx.x / per, e = blockIdx.x % per * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+    const QkSide &s = a.side[side];
+    if (!s.share) return;
+    const int n = side ? a.blocks1 : a.blocks0;
+    float t = 0.f;
+    if (e < a.dim)
+        for (int b = g; b < n; b += 8) t += s.share[(int64_t)b * a.dim + e];
+    part[g][threadIdx.x & 31] = t;
+    __syncthreads();
+    if (g == 0 && e < a.dim) {
+        float r = 0.f;
+        for (int i = 0; i < 8; ++i) r += part[i][threadIdx.x];
+        s.dw[e] = r;
+    }
+}
+
+bool al(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
+
+// strides and address of a tensor whose heads are read or written in pieces of 16 bytes
+bool pieces(const void *p, const int64_t *s, const ssd_qk_problem *q, int heads) {
+    const int64_t n = q->dtype == SSD_BF16 ? 8 : 4;
+    return al(p, 16) && (q->batch == 1 || s[0] % n == 0) && (q->seqlen == 1 || s[1] % n == 0) && (heads == 1 || s[2] % n == 0);
+}
+
+ssd_status check_tensor(const ssd_qk_problem *p, const ssd_tensor &t, int64_t heads, bool written) {
+    if (heads == 0) return SSD_OK;
+    if (t.ptr == nullptr || t.dtype != p->dtype || (p->dim > 1 && t.stride[3] != 1)) return SSD_ERR_INVALID_ARGUMENT;
+    const int64_t n[3] = {p->batch, p->seqlen, heads};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && t.stride[i] < (written ? p->dim : 0)) return SSD_ERR_INVALID_ARGUMENT;
+    return al(t.ptr, p->dtype == SSD_BF16 ? 2 : 4) ? SSD_OK : SSD_ERR_MISALIGNED;
+}
+
+ssd_status check(const ssd_qk_problem *p, const ssd_qk_args *f) {
+    if (p == nullptr) return SSD_ERR_INVALID_ARGUMENT;
+    if (p->batch < 0 || p->seqlen < 0 || p->q_heads < 1 || p->k_heads < 0 || p->dim < 1 || p->rotary < 0 || p->rotary % 2 != 0 ||
+        p->rotary > p->dim || p->table_rows < 0 || !(p->eps >= 0.f) || (p->mode != SSD_QK_RMS && p->mode != SSD_QK_L2) ||
+        (p->interleaved != 0 && p->interleaved != 1) || (p->dtype != SSD_F32 && p->dtype != SSD_BF16))
+        return SSD_ERR_INVALID_ARGUMENT;
+    const int64_t tokens = p->batch * p->seqlen;
+    if (p->dim > QK_MAXD || p->batch > ((int64_t)1 << 30) || p->seqlen > ((int64_t)1 << 30) || p->q_heads > ((int64_t)1 << 16) || p->k_heads > ((int64_t)1 << 16) ||
+        tokens > ((int64_t)1 << 30) || p->table_rows > ((int64_t)1 << 30) || tokens * ((p->q_heads + 3) / 4 + (p->k_heads + 3) / 4) > ((int64_t)1 << 32))
+        return SSD_ERR_UNSUPPORTED;
+    if (f == nullptr) return SSD_OK;
+    if (tokens == 0) return SSD_OK;
+    ssd_status s = check_tensor(p, f->q, p->q_heads, false);
+    if (s == SSD_OK) s = check_tensor(p, f->k, p->k_heads, false);
+    if (s != SSD_OK) return s;
+    if (p->rotary > 0 && p->table_rows > 0 && (!f->cos || !f->sin)) return SSD_ERR_INVALID_ARGUMENT;
+    if (!al(f->q_weight, 4) || !al(f->k_weight, 4) || !al(f->cos, 4) || !al(f->sin, 4) || !al(f->positions, 4)) return SSD_ERR_MISALIGNED;
+    return SSD_OK;
+}
+
+void set3(int64_t *to, const ssd_tensor &t) {
+    for (int i = 0; i < 3; ++i) to[i] = t.stride[i];
+}
+
+// V: features of a lane in the kernels by pieces, 0 where the shapes or addresses do not allow them
+QkArgs make(const ssd_qk_problem *p, const ssd_qk_args *f, const ssd_tensor &yq, const ssd_tensor &yk, const ssd_tensor *dyq, const ssd_tensor *dyk, int *V) {
+    QkArgs a{};
+    const ssd_tensor *x[2] = {&f->q, &f->k}, *y[2] = {&yq, &yk}, *dy[2] = {dyq, dyk};
+    const int64_t heads[2] = {p->q_heads, p->k_heads};
+    a.tokens = p->batch * p->seqlen;
+    const int least = p->dtype == SSD_BF16 ? 8 : 4;
+    *V = p->dim <= 32 * least ? least : 2 * least;
+    if (p->dim > 32 * *V) *V = 16;
+    bool vec = p->dim % *V == 0 && (p->interleaved ? p->rotary : p->rotary / 2) % *V == 0 && (p->rotary == 0 || (al(f->cos, 16) && al(f->sin, 16)));
+    for (int i = 0; i < 2; ++i) {
+        QkSide &s = a.side[i];
+        s.x = x[i]->ptr; s.y = y[i]->ptr; set3(s.xs, *x[i]); set3(s.ys, *y[i]);
+        s.heads = (int)heads[i];
+        s.per = (int)((heads[i] + QK_HB - 1) / QK_HB);
+        s.items = a.tokens * s.per;
+        s.w = i ? f->k_weight : f->q_weight;
+        if (heads[i] == 0) continue;
+        vec = vec && al(s.w, 16) && pieces(s.x, s.xs, p, s.heads) && pieces(s.y, s.ys, p, s.heads);
+        if (dy[i]) {
+            s.dy = dy[i]->ptr;
+            set3(s.dys, *dy[i]);
+            vec = vec && pieces(s.dy, s.dys, p, s.heads);
+        }
+    }
+    if (!vec) *V = 0;
+    a.cos = f->cos; a.sin = f->sin; a.pos = f->positions; a.pos_stride = p->pos_stride;
+    a.seqlen = (int)p->seqlen; a.dim = (int)p->dim; a.half = (int)(p->rotary / 2); a.rows = (int)p->table_rows;
+    a.eps = p->eps;
+    a.inv = p->mode == SSD_QK_RMS ? 1.f / (float)p->dim : 1.f;
+    a.interleaved = p->interleaved != 0;
+    a.lpr = 1;
+    while (a.lpr < 32 && a.lpr * *V < p->dim) a.lpr <<= 1;
+    if (*V == 0) a.lpr = 32;
+    return a;
+}
+int blocks_for(const QkArgs &a, int side, int most) {
+    const int64_t gpb = QK_NT / a.lpr, n = (a.side[side].items + gpb - 1) / gpb;
+    return (int)(most > 0 && n > most ? most : n);
+}
+
+template <typename T, int V>
+cudaError_t launch(const QkArgs &a, bool back, cudaStream_t st) {
+    const unsigned grid = (unsigned)(a.blocks0 + a.blocks1);
+    if (back) {
+        if (a.interleaved) k_qk_bwd<T, V, true><<<grid, QK_NT, 0, st>>>(a);
+        else k_qk_bwd<T, V, false><<<grid, QK_NT, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    return a.interleaved ? launch_early(k_qk_fwd<T, V, true>, grid, QK_NT, 0, st, a) : launch_early(k_qk_fwd<T, V, false>, grid, QK_NT, 0, st, a);
+}
+template <typename T>
+cudaError_t pick(const QkArgs &a, int V, bool back, cudaStream_t st) {
+    constexpr int least = 16 / sizeof(T);
+    if (V == 0) {
+        const unsigned grid = (unsigned)(a.blocks0 + a.blocks1);
+        if (back) k_qk_any<T, true><<<grid, QK_NT, 0, st>>>(a);
+        else k_qk_any<T, false><<<grid, QK_NT, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    if (V == least) return launch<T, least>(a, back, st);
+    if constexpr (least == 4) {
+        if (V == 8) return launch<T, 8>(a, back, st);
+    }
+    return launch<T, 16>(a, back, st);
+}
+
+}  // namespace
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" {
+
+ssd_status ssd_qk_norm_fwd(const ssd_qk_problem *p, const ssd_qk_args *f, void *stream) {
+    if (f == nullptr) return SSD_ERR_INVALID_ARGUMENT;
+    if (ssd_status s = check(p, f); s != SSD_OK) return s;
+    if (p->batch * p->seqlen == 0) return SSD_OK;
+    if (ssd_status s = check_tensor(p, f->q_out, p->q_heads, true); s != SSD_OK) return s;
+    if (ssd_status s = check_tensor(p, f->k_out, p->k_heads, true); s != SSD_OK) return s;
+    int V;
+    QkArgs a = make(p, f, f->q_out, f->k_out, nullptr, nullptr, &V);
+    a.blocks0 = blocks_for(a, 0, V ? 0 : 16 * kSMs);
+    a.blocks1 = blocks_for(a, 1, V ? 0 : 16 * kSMs);
+    const cudaError_t e = p->dtype == SSD_BF16 ? pick<__nv_bfloat16>(a, V, false, (cudaStream_t)stream) : pick<float>(a, V, false, (cudaStream_t)stream);
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+ssd_status ssd_qk_norm_bwd_workspace_size(const ssd_qk_problem *p, size_t *bytes) {
+    if (bytes == nullptr) return SSD_ERR_INVALID_ARGUMENT;
+    if (ssd_status s = check(p, nullptr); s != SSD_OK) return s;
+    *bytes = (size_t)2 * QK_BLOCKS * (size_t)p->dim * sizeof(float);
+    return SSD_OK;
+}
+
+ssd_status ssd_qk_norm_bwd(const ssd_qk_problem *p, const ssd_qk_bwd_args *b, void *workspace, size_t workspace_bytes, void *stream) {
+    if (b == nullptr) return SSD_ERR_INVALID_ARGUMENT;
+    const ssd_qk_args *f = &b->fwd;
+    if (ssd_status s = check(p, f); s != SSD_OK) return s;
+    float *dw[2] = {f->q_weight ? b->dq_weight : nullptr, f->k_weight && p->k_heads > 0 ? b->dk_weight : nullptr};
+    if ((f->q_weight && !dw[0]) || (f->k_weight && p->k_heads > 0 && !dw[1])) return SSD_ERR_INVALID_ARGUMENT;
+    if (!al(dw[0], 4) || !al(dw[1], 4)) return SSD_ERR_MISALIGNED;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (p->batch * p->seqlen == 0) {
+        for (float *d : dw)
+            if (d && cudaMemsetAsync(d, 0, (size_t)p->dim * sizeof(float), st) != cudaSuccess) return SSD_ERR_CUDA;
+        return SSD_OK;
+    }
+    for (const ssd_tensor *t : {&b->dq_out, &b->dq})
+        if (ssd_status s = check_tensor(p, *t, p->q_heads, t == &b->dq); s != SSD_OK) return s;
+    for (const ssd_tensor *t : {&b->dk_out, &b->dk})
+        if (ssd_status s = check_tensor(p, *t, p->k_heads, t == &b->dk); s != SSD_OK) return s;
+    if (dw[0] || dw[1]) {
+        if (workspace == nullptr || workspace_bytes < (size_t)2 * QK_BLOCKS * (size_t)p->dim * sizeof(float)) return SSD_ERR_WORKSPACE_TOO_SMALL;
+        if (!al(workspace, 256)) return SSD_ERR_MISALIGNED;
+    }
+    int V;
+    QkArgs a = make(p, f, b->dq, b->dk, &b->dq_out, &b->dk_out, &V);
+    a.blocks0 = blocks_for(a, 0, QK_BLOCKS);
+    a.blocks1 = blocks_for(a, 1, QK_BLOCKS);
+    for (int i = 0; i < 2; ++i) {
+        a.side[i].dw = dw[i];
+        a.side[i].share = dw[i] ? static_cast<float *>(workspace) + (size_t)i * QK_BLOCKS * p->dim : nullptr;
+    }
+    cudaError_t e = p->dtype == SSD_BF16 ? pick<__nv_bfloat16>(a, V, true, st) : pick<float>(a, V, true, st);
+    if (e == cudaSuccess && (dw[0] || dw[1])) {
+        k_qk_dw<<<2 * ((a.dim + 31) / 32), 256, 0, st>>>(a);
+        e = cudaGetLastError();
+    }
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+}  // extern "C"

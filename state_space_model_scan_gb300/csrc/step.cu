@@ -291,6 +291,139 @@ __global__ void __launch_bounds__(ST_NT, sizeof(T) == 2 && V * RU == 16 ? 12 : 1
     }
 }
 
+// ---- the gated delta rule, one token for each request:
+//
+//   h <- e^g h,  u = beta (v - h k),  h <- h + u k^T,  o = scale h q
+//
+// Both sums over the old state are taken in one pass (o = scale (e^g h q + u k.q)), so that a value is read and
+// written once.  Measured: 192 requests x 32 heads x 128 x 128, fp32 states, 805 MB: see the launch.
+struct DeltaStepArgs {
+    void *state;
+    const int32_t *idx;
+    const void *q, *k, *v, *g, *beta;
+    void *o;
+    int nslots;
+    int64_t slot_stride, qs, ks, vs, gs, bs, os;
+    int batch, H, V, K, hpg;             // heads, values, keys, heads per group of keys
+    int lpr, nrb;                        // lanes per row of the state, row blocks per head
+    float scale;
+    bool g_f32, beta_f32;
+};
+
+template <typename T, typename ST, int V, int NV, int RU>
+__global__ void __launch_bounds__(ST_NT) k_step_delta(const DeltaStepArgs a) {
+    after_previous();
+    const int rb = blockIdx.x % a.nrb, bh = blockIdx.x / a.nrb, head = bh % a.H, b = bh / a.H;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int l = lane & (a.lpr - 1), rpw = 32 / a.lpr;
+    const int r0 = (rb * (ST_NT / 32) + w) * rpw * RU + lane / a.lpr;
+    T *o = static_cast<T *>(a.o) + b * a.os + (int64_t)head * a.V;
+    const int slot = a.idx ? a.idx[b] : b;
+    if ((unsigned)slot >= (unsigned)a.nslots) {                      // padding
+        for (int u = 0; u < RU; ++u)
+            if (l == 0 && r0 + u * rpw < a.V) o[r0 + u * rpw] = from_f<T>(0.f);
+        return;
+    }
+    ST *st = static_cast<ST *>(a.state) + slot * a.slot_stride + (int64_t)head * a.V * a.K;
+    Raw<ST, V> h[RU][NV];
+    Raw<T, V> kv[NV], qv[NV];
+#pragma unroll
+    for (int u = 0; u < RU; ++u)
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int n = (c * a.lpr + l) * V, r = r0 + u * rpw;
+            if (r < a.V && n < a.K) h[u][c].load(st + (int64_t)r * a.K + n);
+        }
+    const int64_t row = (int64_t)(head / a.hpg) * a.K;
+    const T *kp = static_cast<const T *>(a.k) + b * a.ks + row, *qp = static_cast<const T *>(a.q) + b * a.qs + row;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int n = (c * a.lpr + l) * V;
+        if (n < a.K) {
+            kv[c].load(kp + n);
+            qv[c].load(qp + n);
+        }
+    }
+    const int64_t gat = b * a.gs + head, bat = b * a.bs + head;
+    const float g = a.g_f32 ? static_cast<const float *>(a.g)[gat] : to_f(static_cast<const __nv_bfloat16 *>(a.g)[gat]);
+    const float beta = a.beta_f32 ? static_cast<const float *>(a.beta)[bat] : to_f(static_cast<const __nv_bfloat16 *>(a.beta)[bat]);
+    const float decay = expf(g);
+    const T *vp = static_cast<const T *>(a.v) + b * a.vs + (int64_t)head * a.V;
+    // where a row has at least RU lanes, lane u finishes row u; else its first lane every row
+    const bool spread = a.lpr >= RU;
+    float vr[RU];
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+        if (spread && u > 0) break;
+        const int r = r0 + (spread ? l & (RU - 1) : u) * rpw;
+        vr[u] = r < a.V ? to_f(vp[r]) : 0.f;
+    }
+    float hk[RU], hq[RU], kq = 0.f;
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+        hk[u] = hq[u] = 0.f;
+        const int r = r0 + u * rpw;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int n = (c * a.lpr + l) * V;
+            if (r < a.V && n < a.K) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    hk[u] = fmaf(h[u][c].f(e), kv[c].f(e), hk[u]);
+                    hq[u] = fmaf(h[u][c].f(e), qv[c].f(e), hq[u]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int n = (c * a.lpr + l) * V;
+        if (n < a.K) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) kq = fmaf(kv[c].f(e), qv[c].f(e), kq);
+        }
+    }
+    for (int s = a.lpr >> 1; s > 0; s >>= 1) kq += __shfl_xor_sync(0xffffffffu, kq, s);
+    float up[RU];
+    if (spread) {
+        float x = reduce_scatter<RU>(hk, l & (RU - 1)), y = reduce_scatter<RU>(hq, l & (RU - 1));
+        for (int s = RU; s < a.lpr; s <<= 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, s);
+            y += __shfl_xor_sync(0xffffffffu, y, s);
+        }
+        const float u = beta * (vr[0] - decay * x);
+        const int r = r0 + l * rpw;
+        if (l < RU && r < a.V) o[r] = from_f<T>(a.scale * fmaf(decay, y, u * kq));
+#pragma unroll
+        for (int i = 0; i < RU; ++i) up[i] = __shfl_sync(0xffffffffu, u, i, a.lpr);
+    } else {
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+            for (int s = a.lpr >> 1; s > 0; s >>= 1) {
+                hk[u] += __shfl_xor_sync(0xffffffffu, hk[u], s);
+                hq[u] += __shfl_xor_sync(0xffffffffu, hq[u], s);
+            }
+            up[u] = beta * (vr[u] - decay * hk[u]);
+            const int r = r0 + u * rpw;
+            if (l == 0 && r < a.V) o[r] = from_f<T>(a.scale * fmaf(decay, hq[u], up[u] * kq));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+        const int r = r0 + u * rpw;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int n = (c * a.lpr + l) * V;
+            if (r < a.V && n < a.K) {
+                Piece<V> p;
+#pragma unroll
+                for (int e = 0; e < V; ++e) p.v[e] = fmaf(up[u], kv[c].f(e), decay * h[u][c].f(e));
+                stp<V>(st + (int64_t)r * a.K + n, p);
+            }
+        }
+    }
+}
+
 void lanes(StepArgs &a, int V) {
     a.lpr = 1;
     while (a.lpr < 32 && a.lpr * V < a.N) a.lpr <<= 1;
@@ -387,6 +520,66 @@ ssd_status step(const ssd_step_problem *p, bool selective, void *state, const in
     return err == cudaSuccess ? SSD_OK : err == cudaErrorInvalidConfiguration ? SSD_ERR_UNSUPPORTED : SSD_ERR_CUDA;
 }
 
+template <typename T, typename ST, int V, int NV, int RU>
+cudaError_t launch_delta(DeltaStepArgs a, cudaStream_t st) {
+    a.lpr = 1;
+    while (a.lpr < 32 && a.lpr * V < a.K) a.lpr <<= 1;
+    const int per = (ST_NT / 32) * (32 / a.lpr) * RU;
+    a.nrb = (a.V + per - 1) / per;
+    const int64_t blocks = (int64_t)a.batch * a.H * a.nrb;
+    if (blocks > ((int64_t)1 << 31) - 1) return cudaErrorInvalidConfiguration;
+    return launch_early(k_step_delta<T, ST, V, NV, RU>, (unsigned)blocks, ST_NT, 0, st, a);
+}
+template <typename T, typename ST>
+cudaError_t pick_delta(const DeltaStepArgs &a, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(ST);
+    constexpr uintptr_t qk = V * sizeof(T) < 16 ? V * sizeof(T) : 16;
+    const bool vec = a.K % V == 0 && (uintptr_t)a.state % 16 == 0 && a.slot_stride % V == 0 && (uintptr_t)a.q % qk == 0 &&
+                     (uintptr_t)a.k % qk == 0 && a.qs % V == 0 && a.ks % V == 0;
+    if (!vec) return launch_delta<T, ST, 1, 8, 1>(a, st);
+    if constexpr (V == 4) {
+        if (a.K > 32 * V) return launch_delta<T, ST, V, 2, 2>(a, st);
+    }
+    return a.batch < 8 ? launch_delta<T, ST, V, 1, 2>(a, st) : launch_delta<T, ST, V, 1, 8>(a, st);
+}
+
+ssd_status delta_step(const ssd_delta_step_problem *p, void *state, const int32_t *idx, const void *q, const void *k, const void *v,
+                      const void *g, const void *beta, void *o, cudaStream_t st) {
+    if (p == nullptr || p->batch < 0 || p->nslots < 0 || p->nheads < 1 || p->headdim < 1 || p->ngroups < 1 || p->dstate < 1 ||
+        p->nheads % p->ngroups != 0)
+        return SSD_ERR_INVALID_ARGUMENT;
+    if (!type_ok(p->dtype) || !type_ok(p->state_dtype) || !(p->g_dtype == SSD_F32 || p->g_dtype == p->dtype) ||
+        !(p->beta_dtype == SSD_F32 || p->beta_dtype == p->dtype))
+        return SSD_ERR_INVALID_ARGUMENT;
+    if (p->dstate > 256 || p->nheads > ((int64_t)1 << 24) || p->headdim > ((int64_t)1 << 16) ||
+        p->nheads * p->headdim > ((int64_t)1 << 24) || p->batch > ((int64_t)1 << 20))
+        return SSD_ERR_UNSUPPORTED;
+    if (p->batch == 0) return SSD_OK;
+    if (!q || !k || !v || !g || !beta || !o || (p->nslots > 0 && !state)) return SSD_ERR_INVALID_ARGUMENT;
+    const int64_t rows = p->nheads * p->headdim, qk = p->ngroups * p->dstate;
+    if (p->nslots > 1 && p->slot_stride < rows * p->dstate) return SSD_ERR_INVALID_ARGUMENT;
+    if (p->batch > 1 && (p->q_stride < qk || p->k_stride < qk || p->v_stride < rows || p->o_stride < rows ||
+                         p->g_stride < p->nheads || p->beta_stride < p->nheads))
+        return SSD_ERR_INVALID_ARGUMENT;
+    const size_t e = p->dtype == SSD_BF16 ? 2 : 4;
+    if (!al(q, e) || !al(k, e) || !al(v, e) || !al(o, e) || !al(g, p->g_dtype == SSD_BF16 ? 2 : 4) ||
+        !al(beta, p->beta_dtype == SSD_BF16 ? 2 : 4) || !al(idx, 4) || !al(state, p->state_dtype == SSD_BF16 ? 2 : 4))
+        return SSD_ERR_MISALIGNED;
+    if (p->nslots == 0)
+        return cudaMemset2DAsync(o, p->o_stride * e, 0, rows * e, p->batch, st) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    DeltaStepArgs a{};
+    a.state = state; a.idx = idx; a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.o = o;
+    a.nslots = (int)(p->nslots < 0x7fffffff ? p->nslots : 0x7fffffff); a.slot_stride = p->slot_stride;
+    a.qs = p->q_stride; a.ks = p->k_stride; a.vs = p->v_stride; a.gs = p->g_stride; a.bs = p->beta_stride; a.os = p->o_stride;
+    a.batch = (int)p->batch; a.H = (int)p->nheads; a.V = (int)p->headdim; a.K = (int)p->dstate; a.hpg = (int)(p->nheads / p->ngroups);
+    a.scale = p->scale; a.g_f32 = p->g_dtype == SSD_F32; a.beta_f32 = p->beta_dtype == SSD_F32;
+    const bool sb = p->state_dtype == SSD_BF16;
+    cudaError_t err;
+    if (p->dtype == SSD_BF16) err = sb ? pick_delta<__nv_bfloat16, __nv_bfloat16>(a, st) : pick_delta<__nv_bfloat16, float>(a, st);
+    else err = sb ? pick_delta<float, __nv_bfloat16>(a, st) : pick_delta<float, float>(a, st);
+    return err == cudaSuccess ? SSD_OK : err == cudaErrorInvalidConfiguration ? SSD_ERR_UNSUPPORTED : SSD_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace ssd
 
@@ -401,6 +594,11 @@ ssd_status ssd_selective_step(const ssd_step_problem *p, void *state, const int3
                               const float *A, const void *B, const void *C, const float *D, const void *z,
                               const float *bias, void *y, void *stream) {
     return ssd::step(p, true, state, idx, x, dt, A, B, C, D, z, bias, y, (cudaStream_t)stream);
+}
+
+ssd_status ssd_delta_step(const ssd_delta_step_problem *p, void *state, const int32_t *idx, const void *q, const void *k,
+                          const void *v, const void *g, const void *beta, void *o, void *stream) {
+    return ssd::delta_step(p, state, idx, q, k, v, g, beta, o, (cudaStream_t)stream);
 }
 
 }  // extern "C"
