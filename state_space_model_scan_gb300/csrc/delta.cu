@@ -1,5 +1,5 @@
 // delta.cu -- the C entry points of the gated delta rule: validation, workspace, launches.
-#include "delta.cuh"
+#include "delta_tc.cuh"
 
 using namespace ssd;
 
@@ -67,34 +67,45 @@ ssd_status check_inputs(const ssd_delta_problem *p, const ssd_delta_args *a) {
     return SSD_OK;
 }
 
+// The tensor-core path takes bf16 data of up to 128 values and keys; fp32 data is computed in fp32.
+bool on_tensor_cores(const ssd_delta_problem *p) { return p->dtype == SSD_BF16 && p->headdim <= 128 && p->dstate <= 128; }
+
 // What the forward keeps and the backward starts from: the state that enters each chunk, and U.
 struct Kept {
     size_t S, U, total;
 };
+size_t state_bytes(const ssd_delta_problem *p) { return on_tensor_cores(p) ? dtc::STATE_BYTES : (size_t)p->headdim * p->dstate * 4; }
+size_t value_bytes(const ssd_delta_problem *p) { return on_tensor_cores(p) ? dtc::VAL_BYTES : (size_t)DQ * p->headdim * 4; }
 Kept kept_plan(const ssd_delta_problem *p) {
     const size_t ch = (size_t)slots(p) * p->nheads;
     Kept k;
     k.S = 0;
-    k.U = up256(ch * p->headdim * p->dstate * 4);
-    k.total = k.U + up256(ch * DQ * p->headdim * 4);
+    k.U = up256(ch * state_bytes(p));
+    k.total = k.U + up256(ch * value_bytes(p));
     return k;
 }
 struct Plan {
-    size_t gates, sys, att, a, dS, mu, part, kept, total;
+    size_t hdr, gates, sys, att, a, tiles, dS, mu, part, kept, total;
 };
 Plan plan(const ssd_delta_problem *p, bool back, bool kept) {
-    const size_t ch = (size_t)slots(p) * p->nheads, mat = up256(ch * DQ * DQ * 4);
+    const size_t ch = (size_t)slots(p) * p->nheads, mat = ch * DQ * DQ * 4;
+    const bool tc = on_tensor_cores(p);
     Plan w{};
     size_t at = 0;
     auto take = [&](size_t n) { const size_t o = at; at += up256(n); return o; };
-    w.gates = take(ch * DGATES * 4);
-    w.sys = take(mat);
-    w.att = take(mat);
+    w.hdr = take(HDR_WORDS * 4);
+    if (tc) {
+        w.tiles = take(ch * dtc::OPS_BYTES);
+    } else {
+        w.gates = take(ch * DGATES * 4);
+        w.sys = take(mat);
+        w.att = take(mat);
+        if (back) w.a = take(mat);
+    }
     if (back) {
-        w.a = take(mat);
-        w.dS = take(ch * p->headdim * p->dstate * 4);
-        w.mu = take(ch * DQ * p->headdim * 4);
-        w.part = take(p->nheads > p->ngroups ? 2 * ch * DQ * p->dstate * 4 : 0);
+        w.dS = take(ch * state_bytes(p));
+        w.mu = take(ch * value_bytes(p));
+        w.part = take(!tc && p->nheads > p->ngroups ? 2 * ch * DQ * p->dstate * 4 : 0);
         w.kept = take(kept ? 0 : kept_plan(p).total);
     }
     w.total = at;
@@ -115,6 +126,8 @@ DeltaArgs make(const ssd_delta_problem *p, const ssd_delta_args *f, const Plan &
     a.seqlen = (int)p->seqlen; a.H = (int)p->nheads; a.G = (int)p->ngroups; a.V = (int)p->headdim; a.K = (int)p->dstate;
     a.nseqs = (int)nstates(p); a.nslots = (int)slots(p);
     a.scale = p->scale;
+    a.hdr = reinterpret_cast<int32_t *>(ws + w.hdr);
+    a.tiles = ws + w.tiles;
     a.gates = reinterpret_cast<float *>(ws + w.gates);
     a.sys = reinterpret_cast<float *>(ws + w.sys);
     a.att = reinterpret_cast<float *>(ws + w.att);
@@ -130,6 +143,17 @@ ssd_status check_workspace(const void *ws, size_t bytes, size_t need) {
     if (need == 0) return SSD_OK;
     if (ws == nullptr || bytes < need) return SSD_ERR_WORKSPACE_TOO_SMALL;
     return al(ws, 256) ? SSD_OK : SSD_ERR_MISALIGNED;
+}
+DeltaMaps maps(const ssd_delta_problem *p, const ssd_delta_args *f, const ssd_tensor *dO) {
+    DeltaMaps m{};
+    m.has_q = delta_map(&m.q, f->q.ptr, p->dstate, p->ngroups, p->seqlen, p->batch, f->q.stride);
+    m.has_k = delta_map(&m.k, f->k.ptr, p->dstate, p->ngroups, p->seqlen, p->batch, f->k.stride);
+    m.has_v = delta_map(&m.v, f->v.ptr, p->headdim, p->nheads, p->seqlen, p->batch, f->v.stride);
+    m.has_dO = dO != nullptr && delta_map(&m.dO, dO->ptr, p->headdim, p->nheads, p->seqlen, p->batch, dO->stride);
+    return m;
+}
+cudaError_t run_fwd(const ssd_delta_problem *p, const ssd_delta_args *f, const DeltaArgs &a, cudaStream_t st) {
+    return on_tensor_cores(p) && a.nslots > 0 ? delta_tc_fwd(a, maps(p, f, nullptr), st) : delta_simt_fwd(a, p->dtype == SSD_BF16, st);
 }
 ssd_status of_cuda(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
 
@@ -168,7 +192,7 @@ ssd_status ssd_delta_fwd(const ssd_delta_problem *p, const ssd_delta_args *f, vo
     a.final = f->final_states.ptr;
     a.final_bf16 = f->final_states.dtype == SSD_BF16;
     if (f->chunk_states) set_kept(a, p, f->chunk_states);
-    return of_cuda(delta_simt_fwd(a, p->dtype == SSD_BF16, (cudaStream_t)stream));
+    return of_cuda(run_fwd(p, f, a, (cudaStream_t)stream));
 }
 
 ssd_status ssd_delta_bwd(const ssd_delta_problem *p, const ssd_delta_bwd_args *b, void *workspace, size_t workspace_bytes, void *stream) {
@@ -188,11 +212,10 @@ ssd_status ssd_delta_bwd(const ssd_delta_problem *p, const ssd_delta_bwd_args *b
     const Plan w = plan(p, true, kept);
     DELTA_TRY(check_workspace(workspace, workspace_bytes, w.total));
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const bool bf16 = p->dtype == SSD_BF16;
     cudaStream_t st = (cudaStream_t)stream;
     DeltaArgs a = make(p, f, w, ws);
     set_kept(a, p, kept ? f->chunk_states : ws + w.kept);
-    if (!kept && p->seqlen > 0) DELTA_TRY(of_cuda(delta_simt_fwd(a, bf16, st)));
+    if (!kept && p->seqlen > 0) DELTA_TRY(of_cuda(run_fwd(p, f, a, st)));
     a.dO = b->dO.ptr; set3(a.dos, b->dO);
     a.dq = b->dq.ptr; set3(a.dqs, b->dq);
     a.dk = b->dk.ptr; set3(a.dks, b->dk);
@@ -203,8 +226,8 @@ ssd_status ssd_delta_bwd(const ssd_delta_problem *p, const ssd_delta_bwd_args *b
     a.dinit = b->dinitial_states.ptr; a.dinit_bf16 = b->dinitial_states.dtype == SSD_BF16;
     a.dS = ws + w.dS;
     a.mu = ws + w.mu;
-    a.part = p->nheads > p->ngroups ? reinterpret_cast<float *>(ws + w.part) : nullptr;
-    return of_cuda(delta_simt_bwd(a, bf16, st));
+    a.part = !on_tensor_cores(p) && p->nheads > p->ngroups ? reinterpret_cast<float *>(ws + w.part) : nullptr;
+    return of_cuda(on_tensor_cores(p) && a.nslots > 0 ? delta_tc_bwd(a, maps(p, f, &b->dO), st) : delta_simt_bwd(a, p->dtype == SSD_BF16, st));
 }
 
 }  // extern "C"

@@ -30,7 +30,7 @@
 namespace ssd {
 
 constexpr int DQ = 64;          // tokens of a chunk
-constexpr int DGATES = 5 * DQ;  // of a chunk and head: e^G, e^(Gc - G), beta, G as the sum of two floats
+constexpr int DGATES = 6 * DQ;  // of a chunk and head: e^G, e^(Gc - G), beta, G as the sum of two floats, -e^G
 
 struct DeltaArgs {
     const void *q, *k, *v, *g, *beta, *dO;
@@ -43,10 +43,12 @@ struct DeltaArgs {
     int seqlen, H, G, V, K, nseqs, nslots;   // nseqs: batch or packed; nslots: chunks of all sequences, at most
     float scale;
     // workspace and kept states
+    int32_t *hdr;               // the workspace's first words (HeaderWord): the status of bounded waits
     float *gates;               // [nslots][H][DGATES]
     float *sys, *att, *a;       // SIMT: [nslots][H][64][64] each: the inverse, att, and (backward) a
-    void *S, *U;                // state entering each chunk [nslots][H][V][K]; U [nslots][H][64][V]   (kept by a training forward)
-    void *dS, *mu;              // gradient of the state leaving each chunk, mu: the same shapes
+    // state entering each chunk and U (kept by a training forward), gradient of the state leaving each chunk and mu: SIMT
+    // [nslots][H][V][K] and [nslots][H][64][V] fp32, tensor-core path [nslots][H] operand images of 32 KB and [64][128] bf16
+    void *S, *U, *dS, *mu;
     float *part;                // [2][nslots][H][64][K]: dq and dk of each value head, where heads share a group
     void *tiles;                // tensor-core path: operand images of every chunk and head
 };
@@ -143,6 +145,7 @@ __device__ __forceinline__ void delta_gates(const DeltaArgs &a, const DeltaChunk
         const double G = before + g[e];
         const float hi = (float)G;
         to[i] = expf((float)G);
+        to[5 * DQ + i] = -to[i];
         to[DQ + i] = expf((float)(all - G));
         to[3 * DQ + i] = hi;
         to[4 * DQ + i] = (float)(G - (double)hi);

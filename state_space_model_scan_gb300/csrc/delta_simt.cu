@@ -64,6 +64,7 @@ template <typename T>
 __global__ void __launch_bounds__(NT) k_prep(const DeltaArgs a, const bool back) {
     __shared__ float Ks[64 * LD], Qs[64 * LD], M[64 * MLD], gate[DGATES];
     const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
+    if (blockIdx.x == 0 && tid < HDR_WORDS) a.hdr[tid] = 0;
     const DeltaChunk c = delta_chunk(a, slot);
     if (c.len == 0) return;
     const int grp = h / (a.H / a.G);
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(NT) k_prep(const DeltaArgs a, const bool back)
         }
     if (tid < DQ)
 #pragma unroll
-        for (int e = 0; e < 5; ++e) a.gates[((int64_t)slot * a.H + h) * DGATES + e * DQ + tid] = gate[e * DQ + tid];
+        for (int e = 0; e < DGATES / DQ; ++e) a.gates[((int64_t)slot * a.H + h) * DGATES + e * DQ + tid] = gate[e * DQ + tid];
     __syncthreads();
     delta_invert<MLD>(M, Ks, tid);
     for (int e = tid; e < 4096; e += NT) a.sys[at + e] = M[e / 64 * MLD + e % 64];

@@ -1,0 +1,979 @@
+// delta_tc.cu -- the gated delta rule on tcgen05 tensor cores: bf16 data, headdim and dstate up to 128 (smaller ones as
+// the zero-extended part of 128).  Formulas in delta.cuh.
+//
+// Two kernels forwards.  k_prep, a block a chunk and head: K K^T and Q K^T in one product (K's rows and Q's rows as the 128
+// rows of A), the gates, the triangular system, its inverse (fp32, by blocks) and att, left as operand images.  k_chain, a block a sequence and head, walks the chunks.  It works on transposed matrices, so that the
+// 128 TMEM lanes are the values: lane v holds row v of the state S [values][keys], and every product
+//
+//     P^T = S K^T   [v][i]        Y = V^T - e^G P^T     U^T = Y sys^T  [v][i]      S' = e^Gc S + (e^(Gc - G) beta U)^T K   [v][k]
+//
+// has its left operand in tensor memory, put there from registers by the threads that own the lane, and its right one (K,
+// sys, att, Q as they lie) in shared memory: between two products of the chain there is one tcgen05.ld, a
+// little arithmetic and one tcgen05.st, and no shared memory is written.  The state stays in registers, in fp32.
+// What is carried (S, Y, e^(Gc - G) beta U, sys) enters a product as the sum of two bf16 values (2^-17), two or three products of
+// which the small ones are the cheaper price than tf32's single one of half the rate and 2^-11; what only leaves as bf16
+// (att, beta U in o) as one.
+// Backwards the same chain runs from the last chunk to the first (sys transposed, dS in S's place).
+//
+// Warps of a chain block: sixteen with four threads a lane, each a quarter of the columns; three that load the chunk after next; one
+// thread that issues every product.  A product of 128 x 64 x 16 takes as long as one of 128 x 128 x 16 (64 cycles), so that K's and
+// Q's rows, and both terms of sys, go as one right operand of 128 rows.  All waits are bounded.
+#include <cudaTypedefs.h>
+
+#include "delta_tc.cuh"
+
+namespace ssd {
+
+namespace {
+
+using namespace dtc;
+
+// ---------------------------------------------------------------------------------------- the chunk's matrices
+constexpr int PREP_NT = 128;
+constexpr int MLD = 68;                 // rows of 16-byte pieces, four banks apart
+// K's and Q's rows; once their product is out, the system and scratch lie over them
+constexpr uint32_t P_A = 0, P_M = 0, P_T = 64 * MLD * 4, P_GATE = 4 * HALF, P_COLS = P_GATE + GATE_BYTES, P_MISC = P_COLS + 2 * DQ * 4, P_BYTES = P_MISC + 64 + 1024;
+
+// e^(G_i - G_j), as delta_decay, by the multi-function unit: off by 2^-22 and by 2^-24 of the exponent
+__device__ __forceinline__ float decay_of(float hi_i, float lo_i, float hi_j, float lo_j) {
+    return ex2f(kLog2e * ((hi_i - hi_j) + (lo_i - lo_j)));
+}
+// Inverse of I + M, M strictly lower triangular 64 x 64, in place (rows MLD apart), by 128 threads, as delta_invert does it: blocks of
+// 16 on the diagonal by substitution, then twice the block below the diagonal of a pair, a thread four neighbouring columns of a
+// row.  The blocks above the diagonal are neither read nor written.
+__device__ __forceinline__ void invert(float *M, float *t, int tid) {
+    if (tid < 64) {
+        const int o = tid / 16 * 16, j = tid & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == j ? 1.f : 0.f;
+#pragma unroll
+            for (int l = 0; l < i; l += 4) {
+                const float4 m = *reinterpret_cast<const float4 *>(M + (o + i) * MLD + o + l);
+                s = fmaf(-m.x, x[l], s);
+                if (l + 1 < i) s = fmaf(-m.y, x[l + 1], s);
+                if (l + 2 < i) s = fmaf(-m.z, x[l + 2], s);
+                if (l + 3 < i) s = fmaf(-m.w, x[l + 3], s);
+            }
+            x[i] = s;
+        }
+        __syncwarp();                                        // a block's sixteen threads are in one warp
+#pragma unroll
+        for (int i = 0; i < 16; ++i) M[(o + i) * MLD + o + j] = x[i];
+    }
+    {                                                        // the blocks of 16 above a pair's diagonal: zeros, for the pair of 32
+        const int o = tid / 64 * 32;
+        *reinterpret_cast<float4 *>(M + (o + tid % 64 / 4) * MLD + o + 16 + tid % 4 * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 16; n <= 32; n *= 2) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {               // t = M21 T11, then M21 = -T22 t
+#pragma unroll 1
+            for (int k = 0; k < n / 16; ++k) {
+                const int it = tid + k * PREP_NT, per = n * n / 4, p = it / per, i = it % per / (n / 4), j = it % (n / 4) * 4, o = p * 2 * n;
+                f32x2 s0 = 0, s1 = 0;
+                const float *A = M + (o + n + i) * MLD + o + (half ? n : 0), *B = half ? t + p * n * 36 + j : M + o * MLD + o + j;
+                const int ldb = half ? 36 : MLD;
+#pragma unroll 2
+                for (int l = 0; l < n; l += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(A + l);
+                    const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(B + (l + e) * ldb);
+                        const f32x2 xx = pk2(xs[e], xs[e]);
+                        s0 = fma2(xx, y.x, s0);
+                        s1 = fma2(xx, y.y, s1);
+                    }
+                }
+                float4 r;
+                up2(s0, r.x, r.y);
+                up2(s1, r.z, r.w);
+                if (half) *reinterpret_cast<float4 *>(M + (o + n + i) * MLD + o + j) = make_float4(-r.x, -r.y, -r.z, -r.w);
+                else *reinterpret_cast<float4 *>(t + (p * n + i) * 36 + j) = r;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// a block a chunk and head
+template <bool BACK>
+__global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __grid_constant__ DeltaMaps m) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    float *M = reinterpret_cast<float *>(sm + P_M), *T = reinterpret_cast<float *>(sm + P_T), *gate = reinterpret_cast<float *>(sm + P_GATE);
+    float *cols = reinterpret_cast<float *>(sm + P_COLS);   // e^(G_end - G_j), end the last token of j's block of 16; and times beta_j
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + P_MISC);
+    uint32_t *tm = reinterpret_cast<uint32_t *>(sm + P_MISC + 16);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    if (blockIdx.x == 0 && tid < HDR_WORDS) a.hdr[tid] = 0;
+    const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, grp = h / (a.H / a.G);
+    const DeltaChunk c = delta_chunk(a, slot);
+    if (c.len == 0) return;
+    if (w == 1) tmem_alloc(tm, 64);
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        mbar_init(bar + 1, 1);
+        fence_mbar_init();
+        if (m.has_k || m.has_q) {
+            mbar_expect_tx(bar, (m.has_k + m.has_q) * TOK_BYTES);
+            if (m.has_k) tma_rows(sm + P_A, 2 * HALF, &m.k, bar, c, grp);
+            if (m.has_q) tma_rows(sm + P_A + HALF, 2 * HALF, &m.q, bar, c, grp);
+        }
+    }
+    __syncwarp();
+    if (w == 0) delta_gates(a, c, h, gate, lane);
+    if (!m.has_k) load_rows<PREP_NT>(sm + P_A, 2 * HALF, tok_rows(a.k, a.ks, c, grp), a.ks[1], c.len, a.K, tid);
+    if (!m.has_q) load_rows<PREP_NT>(sm + P_A + HALF, 2 * HALF, tok_rows(a.q, a.qs, c, grp), a.qs[1], c.len, a.K, tid);
+    __syncthreads();
+    bool ok = true;
+    if (m.has_k || m.has_q) {
+        ok = mbar_wait(bar, 0);
+        if (m.has_k && c.len < DQ) zero_rows<PREP_NT>(sm + P_A, 2 * HALF, c.len, tid);
+        if (m.has_q && c.len < DQ) zero_rows<PREP_NT>(sm + P_A + HALF, 2 * HALF, c.len, tid);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tm, base = smem_u32(sm + P_A);
+    if (tid == 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) umma_bf16(tmem, kmaj(base, k, 2 * HALF), kmaj(base, k, 2 * HALF), idesc_bf16(128, 64, 0, 0), k > 0);
+        umma_commit(bar + 1);
+    }
+    uint8_t *ops = static_cast<uint8_t *>(a.tiles) + ((int64_t)slot * a.H + h) * OPS_BYTES;
+    if (tid >= 64) {                                         // (warps 2 and 3: while the product runs)
+        const int j = tid - 64, e = j | 15;
+        const float f = decay_of(gate[3 * DQ + e], gate[4 * DQ + e], gate[3 * DQ + j], gate[4 * DQ + j]);
+        cols[j] = f;
+        cols[DQ + j] = f * gate[2 * DQ + j];
+    }
+    for (int e = tid; e < DGATES / 4; e += PREP_NT) reinterpret_cast<float4 *>(ops + GATES)[e] = reinterpret_cast<const float4 *>(gate)[e];
+    ok = mbar_wait(bar + 1, 0) && ok;
+    __syncthreads();
+    if (!ok && tid == 0) set_status(a.hdr, SSD_ERR_DEVICE_TIMEOUT);
+    tc_fence_after();
+    // Row of K K^T (warps 0, 1) or of Q K^T (2, 3); columns in blocks of 16, as far as the warp's rows reach.  In the block on the
+    // diagonal every decay is an exponential of its own; left of it e^(G_i - G_j) is the product of one of the row
+    // (from the end of j's block on) and one of the column (to that end), each at most 1.
+    const int i = tid & 63, ib = i >> 4, nb = 2 * (w & 1) + 2;
+    const float ghi = gate[3 * DQ + i], glo = gate[4 * DQ + i], b = BACK && w < 2 ? gate[2 * DQ + i] : 1.f;
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) {
+        float x[16];
+        if (jb < nb) {
+            tmem_ld16(tmem + ((uint32_t)w << 21) + 16 * jb, x);
+            tmem_wait_ld();
+            if (jb < ib) {
+                const float f = b * decay_of(ghi, glo, gate[3 * DQ + 16 * jb + 15], gate[4 * DQ + 16 * jb + 15]);
+                const float *col = cols + (w < 2 && !BACK ? DQ : 0) + 16 * jb;
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(col + e);
+                    x[e] *= f * v.x; x[e + 1] *= f * v.y; x[e + 2] *= f * v.z; x[e + 3] *= f * v.w;
+                }
+            } else if (jb == ib) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 h4 = *reinterpret_cast<const float4 *>(gate + 3 * DQ + 16 * jb + e), l4 = *reinterpret_cast<const float4 *>(gate + 4 * DQ + 16 * jb + e);
+                    const float4 b4 = *reinterpret_cast<const float4 *>(gate + 2 * DQ + 16 * jb + e);
+                    const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, ls[4] = {l4.x, l4.y, l4.z, l4.w}, bs[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const int j = 16 * jb + e + d;
+                        float f = b * decay_of(ghi, glo, hs[d], ls[d]) * x[e + d];
+                        if (!BACK && w < 2) f *= bs[d];
+                        x[e + d] = (w < 2 ? j < i : j <= i) ? f : 0.f;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = 0.f;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = 0.f;
+        }
+        if (w < 2) {
+            if (jb < nb)
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4 *>(M + i * MLD + 16 * jb + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                *reinterpret_cast<uint4 *>(ops + ATT + i * 128 + (((2 * jb + q) ^ (i & 7)) << 4)) =
+                    make_uint4(pack_bf16(x[8 * q], x[8 * q + 1]), pack_bf16(x[8 * q + 2], x[8 * q + 3]), pack_bf16(x[8 * q + 4], x[8 * q + 5]),
+                               pack_bf16(x[8 * q + 6], x[8 * q + 7]));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (w == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 64);
+    }
+    invert(M, T, tid);
+    // rows of the right operand: N index n, K index k; backwards the transposed inverse
+    const int n = tid >> 1;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+        const int k0 = (tid & 1) * 32 + q * 8;
+        if (BACK ? k0 / 16 >= n / 16 : k0 / 16 <= n / 16) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2)
+                split2(BACK ? M[(k0 + e) * MLD + n] : M[n * MLD + k0 + e], BACK ? M[(k0 + e + 1) * MLD + n] : M[n * MLD + k0 + e + 1], hi[e / 2], lo[e / 2]);
+        }
+        uint8_t *to = ops + n * 128 + (((k0 / 8) ^ (n & 7)) << 4);
+        *reinterpret_cast<uint4 *>(to + SYS_HI) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(to + SYS_LO) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+}
+
+// ---------------------------------------------------------------------------------------- the chain
+constexpr int CH_CW = 16, CH_LW = 3, CH_NT = (CH_CW + CH_LW + 1) * 32;   // warps of the lanes, of the loads, and one for the products
+constexpr int CH_C = CH_CW * 32, CH_L = CH_LW * 32;
+// a stage: K and Q (two images of 128 rows: K's, Q's), V (backwards dO), operands
+constexpr uint32_t ST_KQ = 0, ST_X = 2 * TOK_BYTES, ST_OPS = 3 * TOK_BYTES, ST_BYTES = (ST_OPS + OPS_BYTES + 1023) / 1024 * 1024;
+constexpr uint32_t CH_MISC = 2 * ST_BYTES, CH_BYTES = CH_MISC + 256 + 1024;
+// TMEM columns.  A lane's columns of each belong to four threads, a quarter each; a quarter of an operand lies over the quarter
+// that its thread has read, both terms one after the other.
+//   S   state (its operand; then what is added to it)      P   K S, then Y      R   Q S; backwards att^T dO
+//   U   Y sys, its two shares in U and W; then what goes to the state in U, and W = beta U in W
+//   X   att W; backwards scale e^G dO
+constexpr uint32_t TM_S = 0, TM_P = 128, TM_R = 192, TM_U = 256, TM_W = 320, TM_X = 384;
+enum { B_FULL0, B_FULL1, B_TMA0, B_TMA1, B_P, B_U, B_S, B_O, B_END, B_AY, B_AW, B_AS, B_AF, NB };
+
+struct ChainBars {
+    uint64_t bar[NB];
+    uint32_t tmem;
+    int abort_;
+};
+
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// two values as the sums of two bf16 each (split2 on a pair)
+__device__ __forceinline__ void split_pair(f32x2 v, uint32_t &hi, uint32_t &lo) {
+    float x, y;
+    up2(v, x, y);
+    hi = pack_bf16(x, y);
+    up2(fma2(pk2(bf_lo(hi), bf_hi(hi)), pk2(-1.f, -1.f), v), x, y);
+    lo = pack_bf16(x, y);
+}
+// a thread's 16 values as both terms of an operand at its quarter
+__device__ __forceinline__ void put_terms(uint32_t at, const f32x2 (&y)[8]) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split_pair(y[e], hi[e], lo[e]);
+    tmem_st8(at, hi);
+    tmem_st8(at + 8, lo);
+}
+__device__ __forceinline__ void tmem_ld16x2(uint32_t at, f32x2 (&v)[8]) {
+    float x[16];
+    tmem_ld16(at, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = pk2(x[2 * e], x[2 * e + 1]);
+}
+// gates of tokens 4e .. 4e + 3 as two pairs (shared memory, the same for all lanes)
+__device__ __forceinline__ void ld_gates(f32x2 &g0, f32x2 &g1, const float *p) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p);
+    g0 = v.x;
+    g1 = v.y;
+}
+// a column of 16 tokens of one value, rounded, to rows `step` elements apart
+__device__ __forceinline__ void st_column(__nv_bfloat16 *p, int64_t step, const f32x2 (&v)[8], int left) {
+    if (left >= 16) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float x, y;
+            up2(v[e], x, y);
+            const uint32_t h = pack_bf16(x, y);
+            *reinterpret_cast<unsigned short *>(p) = (unsigned short)h;
+            p += step;
+            *reinterpret_cast<unsigned short *>(p) = (unsigned short)(h >> 16);
+            p += step;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float x, y;
+            up2(v[e], x, y);
+            if (2 * e < left) p[2 * e * step] = __float2bfloat16_rn(x);
+            if (2 * e + 1 < left) p[(2 * e + 1) * step] = __float2bfloat16_rn(y);
+        }
+    }
+}
+
+template <bool BACK>
+__global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __grid_constant__ DeltaMaps m) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    ChainBars *ms = reinterpret_cast<ChainBars *>(sm + CH_MISC);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int s = blockIdx.x / a.H, h = blockIdx.x % a.H, grp = h / (a.H / a.G);
+    if (tid == 0) {
+        for (int b : {B_FULL0, B_FULL1}) mbar_init(&ms->bar[b], CH_LW);
+        for (int b : {B_TMA0, B_TMA1, B_P, B_U, B_S, B_O, B_END}) mbar_init(&ms->bar[b], 1);
+        for (int b : {B_AY, B_AW, B_AS, B_AF}) mbar_init(&ms->bar[b], CH_CW);
+        ms->abort_ = 0;
+        fence_mbar_init();
+    }
+    if (w == 0) tmem_alloc(&ms->tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ms->tmem;
+    const DeltaSeq q = delta_seq(a, s);
+    const int n = (q.len + DQ - 1) / DQ;
+    volatile int *ab = &ms->abort_;
+    auto wait = [&](int b, int c) { return mbar_wait_abort(&ms->bar[b], c & 1, ab); };   // the (c + 1)-th completion
+    auto full = [&](int c) { return mbar_wait_abort(&ms->bar[B_FULL0 + (c & 1)], (c >> 1) & 1, ab); };
+    // a warp's one arrival, after what its lanes have written
+    auto arrive = [&](int b) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms->bar[b]);
+    };
+    auto stage = [&](int c) { return sm + (c & 1) * ST_BYTES; };
+    const bool outputs = BACK || a.o != nullptr;
+
+    if (w < CH_CW) {
+        // ------------------------------------------------------------ four threads a lane: quarter qu of the columns
+        const int qu = w >> 2, v = (w & 3) * 32 + lane;
+        const uint32_t at = tmem + ((uint32_t)(w & 3) << 21);
+        const bool mine = v < a.V;
+        f32x2 S[16];                                         // row v, keys 32 qu ..
+        const int64_t row = (((int64_t)s * a.H + h) * a.V + v) * a.K + 32 * qu;
+        {
+            const void *in = BACK ? a.dfinal : a.init;
+            const bool f32 = BACK ? !a.dfinal_bf16 : !a.init_bf16;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int k = 32 * qu + 2 * e;
+                const float x = in && mine && k < a.K ? delta_ld(in, f32, row + 2 * e) : 0.f;
+                const float y = in && mine && k + 1 < a.K ? delta_ld(in, f32, row + 2 * e + 1) : 0.f;
+                S[e] = pk2(x, y);
+            }
+        }
+        uint8_t *kept = static_cast<uint8_t *>(BACK ? a.dS : a.S), *vals = static_cast<uint8_t *>(BACK ? a.mu : a.U);
+        // the state as chunk c's operand, and kept as the one that enters it (backwards: whose gradient leaves it)
+        auto publish = [&](int c) {
+            uint8_t *to = kept + (((int64_t)q.slot0 + (BACK ? n - 1 - c : c)) * a.H + h) * STATE_BYTES + (qu >> 1) * (STATE_BYTES / 2) + v * 128;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) split_pair(S[8 * g + e], hi[e], lo[e]);
+                tmem_st8(at + TM_S + 32 * qu + 8 * g, hi);
+                tmem_st8(at + TM_S + 32 * qu + 16 + 8 * g, lo);
+                if (kept)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+                        *reinterpret_cast<uint4 *>(to + (((4 * (qu & 1) + 2 * g + p) ^ (v & 7)) << 4)) = make_uint4(hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
+            }
+            tmem_wait_st();
+            arrive(B_AS);
+        };
+        if (n > 0) publish(0);
+        for (int c = 0; c < n; ++c) {
+            const int ci = BACK ? n - 1 - c : c, t0 = ci * DQ + 16 * qu, left = q.len - t0;   // this thread's 16 tokens
+            const int64_t ch = ((int64_t)q.slot0 + ci) * a.H + h;
+            const uint8_t *st = stage(c);
+            const float *gate = reinterpret_cast<const float *>(st + ST_OPS + GATES) + 16 * qu;
+            if (!full(c)) break;
+            const float whole = reinterpret_cast<const float *>(st + ST_OPS + GATES)[DQ - 1];
+            f32x2 x[8], r[8], y[8], g0, g1;
+            // V (dO) of the lane's value while the first product runs
+            {
+                const uint8_t *xs = st + ST_X + (v >> 6) * HALF + 16 * qu * 128 + (v & 7) * 2;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t u0 = *reinterpret_cast<const unsigned short *>(xs + 2 * e * 128 + ((((v & 63) >> 3) ^ ((2 * e) & 7)) << 4));
+                    const uint32_t u1 = *reinterpret_cast<const unsigned short *>(xs + (2 * e + 1) * 128 + ((((v & 63) >> 3) ^ ((2 * e + 1) & 7)) << 4));
+                    y[e] = pk2(bf_lo(u0), bf_lo(u1));
+                }
+            }
+            if (BACK) {                                      // scale e^G dO
+                const f32x2 sc = pk2(a.scale, a.scale);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    ld_gates(g0, g1, gate + 2 * e);
+                    y[e] = mul2(mul2(sc, g0), y[e]);
+                    y[e + 1] = mul2(mul2(sc, g1), y[e + 1]);
+                }
+                put_terms(at + TM_X + 16 * qu, y);
+                tmem_wait_st();
+                arrive(B_AF);
+            }
+            // ---- Y = V - e^G P; backwards N = scale att^T dO + e^(Gc - G) P
+            if (!wait(B_P, c)) break;
+            tc_fence_after();
+            tmem_ld16x2(at + TM_P + 16 * qu, x);
+            if (outputs) tmem_ld16x2(at + TM_R + 16 * qu, r);
+            tmem_wait_ld();
+            if (BACK) {
+                const f32x2 sc = pk2(a.scale, a.scale);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    ld_gates(g0, g1, gate + DQ + 2 * e);
+                    y[e] = fma2(g0, x[e], mul2(sc, r[e]));
+                    y[e + 1] = fma2(g1, x[e + 1], mul2(sc, r[e + 1]));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    ld_gates(g0, g1, gate + 5 * DQ + 2 * e);
+                    y[e] = fma2(g0, x[e], y[e]);
+                    y[e + 1] = fma2(g1, x[e + 1], y[e + 1]);
+                    r[e] = mul2(g0, r[e]);                   // -e^G Q S
+                    r[e + 1] = mul2(g1, r[e + 1]);
+                }
+            }
+            put_terms(at + TM_P + 16 * qu, y);
+            tmem_wait_st();
+            arrive(B_AY);
+            // ---- U (backwards mu)
+            if (!wait(B_U, c)) break;
+            tc_fence_after();
+            tmem_ld16x2(at + TM_U + 16 * qu, x);
+            tmem_ld16x2(at + TM_W + 16 * qu, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = add2(x[e], y[e]);
+            if (vals) {
+                uint8_t *to = vals + ch * VAL_BYTES + (v >> 6) * HALF + 16 * qu * 128 + (v & 7) * 2;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float p, o;
+                    up2(x[e], p, o);
+                    const uint32_t b2 = pack_bf16(p, o);
+                    *reinterpret_cast<unsigned short *>(to + 2 * e * 128 + ((((v & 63) >> 3) ^ ((2 * e) & 7)) << 4)) = (unsigned short)b2;
+                    *reinterpret_cast<unsigned short *>(to + (2 * e + 1) * 128 + ((((v & 63) >> 3) ^ ((2 * e + 1) & 7)) << 4)) = (unsigned short)(b2 >> 16);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                ld_gates(g0, g1, gate + 2 * DQ + 2 * e);
+                x[e] = mul2(g0, x[e]);                       // W = beta U, lam = beta mu
+                x[e + 1] = mul2(g1, x[e + 1]);
+                ld_gates(g0, g1, gate + (BACK ? 5 * DQ : DQ) + 2 * e);
+                y[e] = mul2(g0, x[e]);
+                y[e + 1] = mul2(g1, x[e + 1]);
+            }
+            put_terms(at + TM_U + 16 * qu, y);
+            if (!BACK) {
+                uint32_t hi[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float p, o;
+                    up2(x[e], p, o);
+                    hi[e] = pack_bf16(p, o);
+                }
+                tmem_st8(at + TM_W + 16 * qu, hi);
+            }
+            tmem_wait_st();
+            arrive(B_AW);
+            if (BACK && mine)
+                st_column(static_cast<__nv_bfloat16 *>(a.dv) + q.b * a.dvs[0] + (q.t0 + t0) * a.dvs[1] + h * a.dvs[2] + v, a.dvs[1], x, left);
+            // ---- the state
+            if (!wait(B_S, c)) break;
+            tc_fence_after();
+            const f32x2 wh = pk2(whole, whole);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                tmem_ld16x2(at + TM_S + 32 * qu + 16 * g, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) S[8 * g + e] = fma2(wh, S[8 * g + e], x[e]);
+            }
+            if (c + 1 < n) publish(c + 1);
+            // ---- o, while the next chunk's first product runs
+            if (!BACK && outputs) {
+                if (!wait(B_O, c)) break;
+                tc_fence_after();
+                tmem_ld16x2(at + TM_X + 16 * qu, x);
+                tmem_wait_ld();
+                tc_fence_before();                           // (the next product into these columns follows this thread's next arrival)
+                const f32x2 sc = pk2(a.scale, a.scale), minus = pk2(-1.f, -1.f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = mul2(sc, fma2(minus, r[e], x[e]));
+                if (mine)
+                    st_column(static_cast<__nv_bfloat16 *>(a.o) + q.b * a.os[0] + (q.t0 + t0) * a.os[1] + h * a.os[2] + v, a.os[1], x, left);
+            }
+        }
+        void *out = BACK ? a.dinit : a.final;
+        const bool f32 = BACK ? !a.dinit_bf16 : !a.final_bf16;
+        if (out && mine)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int k = 32 * qu + 2 * e;
+                float x, y;
+                up2(S[e], x, y);
+                if (k < a.K) delta_st(out, f32, row + 2 * e, x);
+                if (k + 1 < a.K) delta_st(out, f32, row + 2 * e + 1, y);
+            }
+        tc_fence_before();
+    } else if (w < CH_CW + CH_LW) {
+        // ------------------------------------------------------------ loads
+        const int t = tid - CH_C;
+        const CUtensorMap *mx = BACK ? &m.dO : &m.v;
+        const bool has_x = BACK ? m.has_dO : m.has_v;
+        auto chunk = [&](int c) {
+            const int ci = BACK ? n - 1 - c : c;
+            return DeltaChunk{q.b, q.t0 + ci * DQ, min(DQ, q.len - ci * DQ)};
+        };
+        auto issue = [&](int c) {
+            const DeltaChunk k = chunk(c);
+            uint8_t *st = stage(c);
+            uint64_t *bar = &ms->bar[B_TMA0 + (c & 1)];
+            if (t == 0) {
+                mbar_expect_tx(bar, OPS_BYTES + (m.has_k + has_x + (m.has_q && outputs)) * TOK_BYTES);
+                if (m.has_k) tma_rows(st + ST_KQ, 2 * HALF, &m.k, bar, k, grp);
+                if (has_x) tma_rows(st + ST_X, HALF, mx, bar, k, h);
+                bulk_load(st + ST_OPS, static_cast<const uint8_t *>(a.tiles) + (((int64_t)q.slot0 + (BACK ? n - 1 - c : c)) * a.H + h) * OPS_BYTES, OPS_BYTES, bar);
+                if (m.has_q && outputs) tma_rows(st + ST_KQ + HALF, 2 * HALF, &m.q, bar, k, grp);
+            }
+            if (!m.has_k) load_rows<CH_L>(st + ST_KQ, 2 * HALF, tok_rows(a.k, a.ks, k, grp), a.ks[1], k.len, a.K, t);
+            if (!has_x) {
+                if (BACK) load_rows<CH_L>(st + ST_X, HALF, tok_rows(a.dO, a.dos, k, h), a.dos[1], k.len, a.V, t);
+                else load_rows<CH_L>(st + ST_X, HALF, tok_rows(a.v, a.vs, k, h), a.vs[1], k.len, a.V, t);
+            }
+            if (!m.has_q && outputs) load_rows<CH_L>(st + ST_KQ + HALF, 2 * HALF, tok_rows(a.q, a.qs, k, grp), a.qs[1], k.len, a.K, t);
+        };
+        if (n > 0) issue(0);
+        if (n > 1) issue(1);
+        for (int c = 0; c < n; ++c) {
+            if (!mbar_wait_abort(&ms->bar[B_TMA0 + (c & 1)], (c >> 1) & 1, ab)) break;
+            if (const int len = chunk(c).len; len < DQ) {    // the next sequence's tokens
+                if (m.has_k) zero_rows<CH_L>(stage(c) + ST_KQ, 2 * HALF, len, t);
+                if (has_x) zero_rows<CH_L>(stage(c) + ST_X, HALF, len, t);
+                if (m.has_q && outputs) zero_rows<CH_L>(stage(c) + ST_KQ + HALF, 2 * HALF, len, t);
+            }
+            fence_proxy_async_smem();
+            arrive(B_FULL0 + (c & 1));
+            if (c + 2 < n) {
+                if (!wait(B_O, c)) break;                    // the products of chunk c are done with its stage (and so is every lane)
+                issue(c + 2);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ the products
+        if (lane == 0) {
+            const uint32_t s0 = smem_u32(sm);
+            constexpr uint32_t id64 = idesc_bf16(128, 64, 0, 0), id128 = idesc_bf16(128, 128, 0, 0), id128t = idesc_bf16(128, 128, 0, 1);
+            for (int c = 0; c < n; ++c) {
+                const uint32_t st = s0 + (c & 1) * ST_BYTES, K = st + ST_KQ, Q = K + HALF, X = st + ST_X, ops = st + ST_OPS;
+                if (!full(c)) break;
+                if (BACK) {                                  // att^T dO: dO by columns, att by columns
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16(tmem + TM_R, mnmaj(X, k, HALF), mnmaj(ops + ATT, k, HALF), idesc_bf16(128, 64, 1, 1), k > 0);
+                }
+                if (!wait(B_AS, c)) break;
+                tc_fence_after();
+                // K S and Q S in one: their rows are the 128 rows of the right operand
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t A = tmem + TM_S + 32 * (k >> 1) + 8 * (k & 1);
+                    umma_bf16_ta(tmem + TM_P, A, kmaj(K, k, 2 * HALF), BACK ? id64 : id128, k > 0);
+                    umma_bf16_ta(tmem + TM_P, A + 16, kmaj(K, k, 2 * HALF), BACK ? id64 : id128, 1);
+                }
+                umma_commit(&ms->bar[B_P]);
+                auto from_o = [&](int term) {                // (scale e^G dO)^T Q
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16_ta(tmem + TM_S, tmem + TM_X + 16 * k + 8 * term, mnmaj(Q, k, 2 * HALF), id128t, term || k > 0);
+                };
+                if (BACK) {
+                    if (!wait(B_AF, c) || !wait(B_P, c)) break;   // P is done with the columns that are written now
+                    tc_fence_after();
+                    from_o(0);
+                }
+                if (!wait(B_AY, c)) break;
+                tc_fence_after();
+                // both terms of sys in one: its images are the 128 rows of the right operand
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_bf16_ta(tmem + TM_U, tmem + TM_P + 16 * k, kmaj(ops + SYS_HI, k, 0), id128, k > 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_bf16_ta(tmem + TM_U, tmem + TM_P + 16 * k + 8, kmaj(ops + SYS_HI, k, 0), id64, 1);
+                umma_commit(&ms->bar[B_U]);
+                if (BACK) from_o(1);
+                if (!wait(B_AW, c)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    umma_bf16_ta(tmem + TM_S, tmem + TM_U + 16 * k, mnmaj(K, k, 2 * HALF), id128t, BACK || k > 0);
+                    umma_bf16_ta(tmem + TM_S, tmem + TM_U + 16 * k + 8, mnmaj(K, k, 2 * HALF), id128t, 1);
+                }
+                umma_commit(&ms->bar[B_S]);
+                if (!BACK && outputs)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) umma_bf16_ta(tmem + TM_X, tmem + TM_W + 16 * k, kmaj(ops + ATT, k, 0), id64, k > 0);
+                umma_commit(&ms->bar[B_O]);
+            }
+            // nothing is in flight when the tensor memory is given up, also where a wait has given up
+            umma_commit(&ms->bar[B_END]);
+            mbar_wait(&ms->bar[B_END], 0);
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    if (tid == 0 && *ab) set_status(a.hdr, SSD_ERR_DEVICE_TIMEOUT);
+    if (w == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------------------- a chunk's gradients
+// A block a chunk and group, the group's heads one after the other (their dQ and dK are added up in registers, in fp32).  Rows 0..63
+// of the 128 TMEM lanes are K's side of a token, rows 64..127 Q's:
+//
+//   D0 = [K; Q] K^T        D1 = [mu; dO] U^T        D2 = [mu; dO] S       D3 = mu's rows: U dS
+//   D4 = [E; F] K + [E^T K + F^T Q; 0]              dK, dQ = f D2 + D4 (+ f D3)
+//
+// Every operand is a tile as it lies in memory or was left by the chains; factors of a token (beta, e^G, scale) go into E and F or
+// multiply a row of the result, in fp32.  dbeta is D1's diagonal.  dg adds up, for each token, what crosses it inside
+// the chunk (E and F times D0: sums before the column along a row, then down the columns), and rows of D2 and D3 times K, Q.
+// Bound by the work between the products, a block alone on its SM.
+constexpr int GR_NT = 256;
+constexpr uint32_t G_KQ = 0, G_A = G_KQ + 4 * HALF, G_U = G_A + 4 * HALF, G_S = G_U + TOK_BYTES, G_DS = G_S + STATE_BYTES, G_EF = G_DS + STATE_BYTES,
+                   G_Z = G_EF + 2 * HALF, G_GATE = G_Z + HALF, G_COLS = G_GATE + GATE_BYTES, G_SUM = G_COLS + DQ * 4, G_MISC = G_SUM + (8 * 32 + 4 * 64 + 8) * 4,
+                   G_BYTES = G_MISC + 64 + 1024;
+constexpr uint32_t T_D0 = 0, T_D1 = 64, T_D2 = 128, T_D3 = 256, T_D4 = 384;
+
+// row r of a tile of 128 rows, half a feature image of 64
+__device__ __forceinline__ void ld_row(const uint8_t *tile, int r, int q, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(tile + r * 128 + ((q ^ (r & 7)) << 4));
+    v[0] = bf_lo(u.x); v[1] = bf_hi(u.x); v[2] = bf_lo(u.y); v[3] = bf_hi(u.y);
+    v[4] = bf_lo(u.z); v[5] = bf_hi(u.z); v[6] = bf_lo(u.w); v[7] = bf_hi(u.w);
+}
+// sums over a warp's lanes of v[e], for lane e
+__device__ __forceinline__ float warp_columns(float (&v)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    return v[0];
+}
+
+__global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __grid_constant__ DeltaMaps m) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    float *gate = reinterpret_cast<float *>(sm + G_GATE), *cols = reinterpret_cast<float *>(sm + G_COLS), *colsum = reinterpret_cast<float *>(sm + G_SUM);
+    float *R = colsum + 8 * 32, *X = R + 128, *SSw = X + 128;    // [2][64] each: both halves of a row
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + G_MISC);
+    uint32_t *tm = reinterpret_cast<uint32_t *>(sm + G_MISC + 48);
+    enum { L_KQ, L_HEAD, L_D1, L_D2, L_D4 };
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int slot = blockIdx.x / a.G, grp = blockIdx.x % a.G, per = a.H / a.G;
+    const DeltaChunk c = delta_chunk(a, slot);
+    if (c.len == 0) return;
+    if (w == 0) tmem_alloc(tm, 512);
+    if (tid == 0) {
+        for (int i = 0; i < 5; ++i) mbar_init(bar + i, 1);
+        fence_mbar_init();
+    }
+    for (int e = tid; e < (int)HALF / 16; e += GR_NT) reinterpret_cast<uint4 *>(sm + G_Z)[e] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    auto issue = [&](int r) {                                // a head's operands
+        const int h = grp * per + r;
+        const int64_t ch = (int64_t)slot * a.H + h;
+        if (tid == 0) {
+            uint64_t *b = bar + L_HEAD;
+            mbar_expect_tx(b, GATE_BYTES + 2 * VAL_BYTES + 2 * STATE_BYTES + (m.has_dO ? TOK_BYTES : 0));
+            const uint8_t *mu = static_cast<const uint8_t *>(a.mu) + ch * VAL_BYTES;
+            bulk_load(sm + G_A, mu, HALF, b);
+            bulk_load(sm + G_A + 2 * HALF, mu + HALF, HALF, b);
+            if (m.has_dO) tma_rows(sm + G_A + HALF, 2 * HALF, &m.dO, b, c, h);
+            bulk_load(sm + G_U, static_cast<const uint8_t *>(a.U) + ch * VAL_BYTES, VAL_BYTES, b);
+            bulk_load(sm + G_GATE, static_cast<const uint8_t *>(a.tiles) + ch * OPS_BYTES + GATES, GATE_BYTES, b);
+            bulk_load(sm + G_S, static_cast<const uint8_t *>(a.S) + ch * STATE_BYTES, STATE_BYTES, b);
+            bulk_load(sm + G_DS, static_cast<const uint8_t *>(a.dS) + ch * STATE_BYTES, STATE_BYTES, b);
+        }
+        if (!m.has_dO) load_rows<GR_NT>(sm + G_A + HALF, 2 * HALF, tok_rows(a.dO, a.dos, c, h), a.dos[1], c.len, a.V, tid);
+    };
+    if (tid == 0 && (m.has_k || m.has_q)) {
+        mbar_expect_tx(bar + L_KQ, (m.has_k + m.has_q) * TOK_BYTES);
+        if (m.has_k) tma_rows(sm + G_KQ, 2 * HALF, &m.k, bar + L_KQ, c, grp);
+        if (m.has_q) tma_rows(sm + G_KQ + HALF, 2 * HALF, &m.q, bar + L_KQ, c, grp);
+    }
+    if (!m.has_k) load_rows<GR_NT>(sm + G_KQ, 2 * HALF, tok_rows(a.k, a.ks, c, grp), a.ks[1], c.len, a.K, tid);
+    if (!m.has_q) load_rows<GR_NT>(sm + G_KQ + HALF, 2 * HALF, tok_rows(a.q, a.qs, c, grp), a.qs[1], c.len, a.K, tid);
+    issue(0);
+    bool ok = true;
+    if (m.has_k || m.has_q) ok = mbar_wait(bar + L_KQ, 0);
+    if (c.len < DQ) {
+        if (m.has_k) zero_rows<GR_NT>(sm + G_KQ, 2 * HALF, c.len, tid);
+        if (m.has_q) zero_rows<GR_NT>(sm + G_KQ + HALF, 2 * HALF, c.len, tid);
+    }
+    const uint32_t base = smem_u32(sm), KQ = base + G_KQ, A = base + G_A, U = base + G_U, S = base + G_S, dS = base + G_DS, EF = base + G_EF, Z = base + G_Z;
+    const int row = (w & 3) * 32 + lane, i = row & 63, hf = w >> 2;
+    const bool qside = row >= 64;
+    uint32_t tmem = 0;
+    float acc[64];
+#pragma unroll
+    for (int e = 0; e < 64; ++e) acc[e] = 0.f;
+    for (int r = 0; r < per; ++r) {
+        const int h = grp * per + r;
+        ok = mbar_wait(bar + L_HEAD, r & 1) && ok;
+        if (c.len < DQ && m.has_dO) zero_rows<GR_NT>(sm + G_A + HALF, 2 * HALF, c.len, tid);
+        if (tid < DQ) {                                      // beta_j e^(G_end - G_j), end the last token of j's block of 16
+            const int e = tid | 15;
+            cols[tid] = gate[2 * DQ + tid] * ex2f(kLog2e * ((gate[3 * DQ + e] - gate[3 * DQ + tid]) + (gate[4 * DQ + e] - gate[4 * DQ + tid])));
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        tmem = *tm;
+        if (tid == 0) {
+            if (r == 0)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) umma_bf16(tmem + T_D0, kmaj(KQ, k, 2 * HALF), kmaj(KQ, k, 2 * HALF), idesc_bf16(128, 64, 0, 0), k > 0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) umma_bf16(tmem + T_D1, kmaj(A, k, 2 * HALF), kmaj(U, k, HALF), idesc_bf16(128, 64, 0, 0), k > 0);
+            umma_commit(bar + L_D1);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) umma_bf16(tmem + T_D2, kmaj(A, k, 2 * HALF), mnmaj(S, k, STATE_BYTES / 2), idesc_bf16(128, 128, 0, 1), k > 0);
+            // (rows 64..127 of this left operand are the state's first rows: nothing reads what comes of them)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) umma_bf16(tmem + T_D3, kmaj(U, k, HALF), mnmaj(dS, k, STATE_BYTES / 2), idesc_bf16(128, 128, 0, 1), k > 0);
+            umma_commit(bar + L_D2);
+        }
+        // <S, dS> meanwhile
+        float ss = 0.f;
+#pragma unroll 4
+        for (int e = tid; e < (int)STATE_BYTES / 16; e += GR_NT) {
+            const uint4 x = reinterpret_cast<const uint4 *>(sm + G_S)[e], y = reinterpret_cast<const uint4 *>(sm + G_DS)[e];
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                ss = fmaf(bf_lo(xs[d]), bf_lo(ys[d]), ss);
+                ss = fmaf(bf_hi(xs[d]), bf_hi(ys[d]), ss);
+            }
+        }
+        ss = warp_sum(ss);
+        if (lane == 0) SSw[w] = ss;
+        // ---- E, F: this thread's row, tokens j = 32 hf ..
+        const float ghi = gate[3 * DQ + i], glo = gate[4 * DQ + i], bi = gate[2 * DQ + i], eg = gate[i];
+        const float f1 = qside ? a.scale : -bi;
+        float flow[32], x[32];
+        ok = mbar_wait(bar + L_D1, r & 1) && ok;
+        tc_fence_after();
+        tmem_ld32(tmem + ((uint32_t)(w & 3) << 21) + T_D1 + 32 * hf, x);
+        tmem_ld32(tmem + ((uint32_t)(w & 3) << 21) + T_D0 + 32 * hf, flow);
+        tmem_wait_ld();
+        float before = 0.f;                                  // sum of the row's w_ij so far
+        {
+            uint8_t *to = sm + G_EF + row * 128;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {                    // blocks of 16
+                const int j0 = 32 * hf + 16 * b;
+                const float left = f1 * ex2f(kLog2e * ((ghi - gate[3 * DQ + j0 + 15]) + (glo - gate[4 * DQ + j0 + 15])));
+                const bool diag = (i >> 4) == (j0 >> 4), none = j0 > i;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int j = j0 + e;
+                    const float d = x[16 * b + e];
+                    float v;
+                    if (diag) v = f1 * gate[2 * DQ + j] * ex2f(kLog2e * ((ghi - gate[3 * DQ + j]) + (glo - gate[4 * DQ + j]))) * d;
+                    else v = left * cols[j] * d;
+                    if (!qside && j == i && j < c.len)
+                        delta_st(a.dbeta, a.beta_f32, c.b * a.dbs[0] + (int64_t)(c.t0 + j) * a.dbs[1] + h * a.dbs[2], d);
+                    v = none || j > i || (!qside && j == i) ? 0.f : v;
+                    const float wij = j < i ? v * flow[16 * b + e] : 0.f;
+                    flow[16 * b + e] = j <= i ? before : 0.f;   // what comes from before j, if it reaches i
+                    before += wij;
+                    x[16 * b + e] = v;
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float *y = x + 16 * b + 8 * q;
+                    *reinterpret_cast<uint4 *>(to + (((j0 / 8 + q) ^ (row & 7)) << 4)) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+                }
+            }
+        }
+        if (hf == 0) X[row] = before;                        // for the row's other half
+        fence_proxy_async_smem();
+        tc_fence_before();
+        ok = mbar_wait(bar + L_D2, r & 1) && ok;
+        __syncthreads();
+        tc_fence_after();
+        if (tid == 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_bf16(tmem + T_D4, kmaj(EF, k, 0), mnmaj(KQ, k, 2 * HALF), idesc_bf16(128, 128, 0, 1), k > 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_bf16(tmem + T_D4, mnmaj(EF, k, Z - EF), mnmaj(KQ, k, 2 * HALF), idesc_bf16(128, 128, 1, 1), 1);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_bf16(tmem + T_D4, mnmaj(EF + HALF, k, Z - EF - HALF), mnmaj(KQ + HALF, k, 2 * HALF), idesc_bf16(128, 128, 1, 1), 1);
+            umma_commit(bar + L_D4);
+        }
+        {
+            const float mine = hf ? X[row] : 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) flow[e] += 32 * hf + e <= i ? mine : 0.f;
+            colsum[w * 32 + lane] = warp_columns(flow, lane);
+        }
+        const float fd = gate[DQ + i] * bi, whole = gate[DQ - 1];
+        // the head's gates and operands have been read: the next head's may come, except this head's gates (copied above)
+        float ssum = 0.f;
+        if (tid < 64)
+            for (int e = 0; e < 8; ++e) ssum += SSw[e];
+        __syncthreads();
+        if (r + 1 < per) issue(r + 1);
+        // ---- rows of D2, D3 times K or Q, and their sum; keys 64 hf ..
+        const uint8_t *kq = sm + G_KQ + hf * 2 * HALF;
+        const float f2 = qside ? a.scale * eg : -eg * bi;
+        float dot = 0.f, dotx = 0.f;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            float y[32];
+            tmem_ld32(tmem + ((uint32_t)(w & 3) << 21) + T_D2 + 64 * hf + 32 * g, x);
+            if (!qside) tmem_ld32(tmem + ((uint32_t)(w & 3) << 21) + T_D3 + 64 * hf + 32 * g, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float z[8];
+                ld_row(kq, row, 4 * g + q, z);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dot = fmaf(x[8 * q + e], z[e], dot);
+                    acc[32 * g + 8 * q + e] = fmaf(f2, x[8 * q + e], acc[32 * g + 8 * q + e]);
+                    if (!qside) {
+                        dotx = fmaf(y[8 * q + e], z[e], dotx);
+                        acc[32 * g + 8 * q + e] = fmaf(fd, y[8 * q + e], acc[32 * g + 8 * q + e]);
+                    }
+                }
+            }
+        }
+        // (the flows are done with X) R: a token's reads, by K's and by Q's rows, X: its writes; one half after the other
+        if (hf == 0) {
+            R[row] = f2 * dot;
+            if (!qside) X[i] = fd * dotx;
+        }
+        __syncthreads();
+        if (hf == 1) {
+            R[row] += f2 * dot;
+            if (!qside) X[i] += fd * dotx;
+        }
+        ok = mbar_wait(bar + L_D4, r & 1) && ok;
+        tc_fence_after();
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            tmem_ld32(tmem + ((uint32_t)(w & 3) << 21) + T_D4 + 64 * hf + 32 * g, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[32 * g + e] += x[e];
+        }
+        tc_fence_before();
+        __syncthreads();
+        // ---- dg: token t, two warps of them
+        if (tid < 64) {
+            float f = whole * ssum;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f += colsum[((tid >> 5) * 4 + k) * 32 + lane];
+            float rs = R[tid] + R[64 + tid], xs = X[tid];
+            float pr = rs, px = xs;                          // inclusive sums: of reads from the end, of writes from the start
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float u = __shfl_down_sync(0xffffffffu, pr, o), v = __shfl_up_sync(0xffffffffu, px, o);
+                if (lane + o < 32) pr += u;
+                if (lane >= o) px += v;
+            }
+            // and the other 32 tokens': their reads come after the first ones, their writes before the last
+            const float other = warp_sum(tid < 32 ? R[32 + lane] + R[96 + lane] : X[lane]);
+            f += pr + (px - xs) + other;
+            if (tid < c.len) delta_st(a.dg, a.g_f32, c.b * a.dgs[0] + (int64_t)(c.t0 + tid) * a.dgs[1] + h * a.dgs[2], f);
+        }
+    }
+    if (!ok && tid == 0) set_status(a.hdr, SSD_ERR_DEVICE_TIMEOUT);
+    if (i < c.len) {
+        __nv_bfloat16 *to = qside ? static_cast<__nv_bfloat16 *>(a.dq) + c.b * a.dqs[0] + (int64_t)(c.t0 + i) * a.dqs[1] + grp * a.dqs[2]
+                                  : static_cast<__nv_bfloat16 *>(a.dk) + c.b * a.dks[0] + (int64_t)(c.t0 + i) * a.dks[1] + grp * a.dks[2];
+        to += 64 * hf;
+        const int n = a.K - 64 * hf;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float *y = acc + 8 * q;
+            if (8 * q + 8 <= n && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
+                *reinterpret_cast<uint4 *>(to + 8 * q) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (8 * q + e < n) to[8 * q + e] = __float2bfloat16_rn(y[e]);
+            }
+        }
+    }
+    __syncthreads();
+    if (w == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <bool BACK>
+cudaError_t prep(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
+    static int set[64] = {};
+    if (cudaError_t e = ensure_smem_attr(k_prep<BACK>, (int)P_BYTES, set); e != cudaSuccess) return e;
+    k_prep<BACK><<<(unsigned)((int64_t)a.nslots * a.H), PREP_NT, P_BYTES, st>>>(a, m);
+    return cudaGetLastError();
+}
+template <bool BACK>
+cudaError_t chain(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
+    static int set[64] = {};
+    if (cudaError_t e = ensure_smem_attr(k_chain<BACK>, (int)CH_BYTES, set); e != cudaSuccess) return e;
+    k_chain<BACK><<<(unsigned)(a.nseqs * (int64_t)a.H), CH_NT, CH_BYTES, st>>>(a, m);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool delta_map(CUtensorMap *m, const void *p, int64_t inner, int64_t heads, int64_t tokens, int64_t batch, const int64_t *strides) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    if (encode == nullptr) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }
+    const int64_t n[3] = {heads, tokens, batch}, s[3] = {strides[2], strides[1], strides[0]};
+    if (encode == nullptr || (uintptr_t)p % 16 != 0 || inner % 8 != 0) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)inner, (cuuint64_t)heads, (cuuint64_t)tokens, (cuuint64_t)batch}, by[3];
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] > 1 && (s[i] % 8 != 0 || s[i] < inner || s[i] >= ((int64_t)1 << 38))) return false;
+        by[i] = (cuuint64_t)(n[i] > 1 ? s[i] : inner) * 2;
+    }
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)DQ, 1}, step[4] = {1, 1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, by, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t delta_tc_fwd(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
+    if (cudaError_t e = prep<false>(a, m, st); e != cudaSuccess) return e;
+    return chain<false>(a, m, st);
+}
+cudaError_t delta_tc_bwd(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
+    if (cudaError_t e = prep<true>(a, m, st); e != cudaSuccess) return e;
+    if (cudaError_t e = chain<true>(a, m, st); e != cudaSuccess) return e;
+    static int set[64] = {};
+    if (cudaError_t e = ensure_smem_attr(k_grads, (int)G_BYTES, set); e != cudaSuccess) return e;
+    k_grads<<<(unsigned)((int64_t)a.nslots * a.G), GR_NT, G_BYTES, st>>>(a, m);
+    return cudaGetLastError();
+}
+
+}  // namespace ssd
