@@ -144,16 +144,21 @@ ssd_status check_workspace(const void *ws, size_t bytes, size_t need) {
     if (ws == nullptr || bytes < need) return SSD_ERR_WORKSPACE_TOO_SMALL;
     return al(ws, 256) ? SSD_OK : SSD_ERR_MISALIGNED;
 }
-DeltaMaps maps(const ssd_delta_problem *p, const ssd_delta_args *f, const ssd_tensor *dO) {
+DeltaMaps maps(const ssd_delta_problem *p, const ssd_delta_args *f, const DeltaArgs &a, const ssd_tensor *dO, const ssd_tensor &out) {
     DeltaMaps m{};
     m.has_q = delta_map(&m.q, f->q.ptr, p->dstate, p->ngroups, p->seqlen, p->batch, f->q.stride);
     m.has_k = delta_map(&m.k, f->k.ptr, p->dstate, p->ngroups, p->seqlen, p->batch, f->k.stride);
     m.has_v = delta_map(&m.v, f->v.ptr, p->headdim, p->nheads, p->seqlen, p->batch, f->v.stride);
-    m.has_dO = dO != nullptr && delta_map(&m.dO, dO->ptr, p->headdim, p->nheads, p->seqlen, p->batch, dO->stride);
+    m.has_out = out.ptr != nullptr && delta_map(&m.out, out.ptr, p->headdim, p->nheads, p->seqlen, p->batch, out.stride, true);
+    if (dO != nullptr) {
+        m.has_dO = delta_map(&m.dO, dO->ptr, p->headdim, p->nheads, p->seqlen, p->batch, dO->stride);
+        const int64_t rows[3] = {0, 128, DQ * 128}, ch = (int64_t)a.nslots * a.H;
+        m.has_vals = delta_map(&m.U, a.U, 128, ch, DQ, 1, rows) && delta_map(&m.mu, a.mu, 128, ch, DQ, 1, rows);
+    }
     return m;
 }
-cudaError_t run_fwd(const ssd_delta_problem *p, const ssd_delta_args *f, const DeltaArgs &a, cudaStream_t st) {
-    return on_tensor_cores(p) && a.nslots > 0 ? delta_tc_fwd(a, maps(p, f, nullptr), st) : delta_simt_fwd(a, p->dtype == SSD_BF16, st);
+cudaError_t run_fwd(const ssd_delta_problem *p, const ssd_delta_args *f, const DeltaArgs &a, const ssd_tensor &o, cudaStream_t st) {
+    return on_tensor_cores(p) && a.nslots > 0 ? delta_tc_fwd(a, maps(p, f, a, nullptr, o), st) : delta_simt_fwd(a, p->dtype == SSD_BF16, st);
 }
 ssd_status of_cuda(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
 
@@ -192,7 +197,7 @@ ssd_status ssd_delta_fwd(const ssd_delta_problem *p, const ssd_delta_args *f, vo
     a.final = f->final_states.ptr;
     a.final_bf16 = f->final_states.dtype == SSD_BF16;
     if (f->chunk_states) set_kept(a, p, f->chunk_states);
-    return of_cuda(run_fwd(p, f, a, (cudaStream_t)stream));
+    return of_cuda(run_fwd(p, f, a, f->o, (cudaStream_t)stream));
 }
 
 ssd_status ssd_delta_bwd(const ssd_delta_problem *p, const ssd_delta_bwd_args *b, void *workspace, size_t workspace_bytes, void *stream) {
@@ -215,7 +220,7 @@ ssd_status ssd_delta_bwd(const ssd_delta_problem *p, const ssd_delta_bwd_args *b
     cudaStream_t st = (cudaStream_t)stream;
     DeltaArgs a = make(p, f, w, ws);
     set_kept(a, p, kept ? f->chunk_states : ws + w.kept);
-    if (!kept && p->seqlen > 0) DELTA_TRY(of_cuda(run_fwd(p, f, a, st)));
+    if (!kept && p->seqlen > 0) DELTA_TRY(of_cuda(run_fwd(p, f, a, ssd_tensor{}, st)));
     a.dO = b->dO.ptr; set3(a.dos, b->dO);
     a.dq = b->dq.ptr; set3(a.dqs, b->dq);
     a.dk = b->dk.ptr; set3(a.dks, b->dk);
@@ -227,7 +232,7 @@ ssd_status ssd_delta_bwd(const ssd_delta_problem *p, const ssd_delta_bwd_args *b
     a.dS = ws + w.dS;
     a.mu = ws + w.mu;
     a.part = !on_tensor_cores(p) && p->nheads > p->ngroups ? reinterpret_cast<float *>(ws + w.part) : nullptr;
-    return of_cuda(on_tensor_cores(p) && a.nslots > 0 ? delta_tc_bwd(a, maps(p, f, &b->dO), st) : delta_simt_bwd(a, p->dtype == SSD_BF16, st));
+    return of_cuda(on_tensor_cores(p) && a.nslots > 0 ? delta_tc_bwd(a, maps(p, f, a, &b->dO, b->dv), st) : delta_simt_bwd(a, p->dtype == SSD_BF16, st));
 }
 
 }  // extern "C"

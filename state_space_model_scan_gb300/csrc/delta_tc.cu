@@ -15,8 +15,8 @@
 // (att, beta U in o) as one.
 // Backwards the same chain runs from the last chunk to the first (sys transposed, dS in S's place).
 //
-// Warps of a chain block: sixteen with four threads a lane, each a quarter of the columns; three that load the chunk after next; one
-// thread that issues every product.  A product of 128 x 64 x 16 takes as long as one of 128 x 128 x 16 (64 cycles), so that K's and
+// Warps of a chain block: eight with two threads a lane, each half of the columns; four with one thread a lane for what is off
+// the chain; two that load the next chunk, one that stores; one thread that issues every product.  A product of 128 x 64 x 16 takes as long as one of 128 x 128 x 16 (64 cycles), so that K's and
 // Q's rows, and both terms of sys, go as one right operand of 128 rows.  All waits are bounded.
 #include <cudaTypedefs.h>
 
@@ -236,18 +236,48 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
 }
 
 // ---------------------------------------------------------------------------------------- the chain
-constexpr int CH_CW = 16, CH_LW = 3, CH_NT = (CH_CW + CH_LW + 1) * 32;   // warps of the lanes, of the loads, and one for the products
-constexpr int CH_C = CH_CW * 32, CH_L = CH_LW * 32;
+// warps: of the lanes, four more of the lanes for what is off the chain (o, backwards scale e^G dO), of the loads, one that stores, one for the products
+constexpr int CH_CW = 8, CH_EW = 4, CH_LW = 2, CH_NT = (CH_CW + CH_EW + CH_LW + 2) * 32;
+constexpr int CH_L = CH_LW * 32, CH_L0 = (CH_CW + CH_EW) * 32;
 // a stage: K and Q (two images of 128 rows: K's, Q's), V (backwards dO), operands
 constexpr uint32_t ST_KQ = 0, ST_X = 2 * TOK_BYTES, ST_OPS = 3 * TOK_BYTES, ST_BYTES = (ST_OPS + OPS_BYTES + 1023) / 1024 * 1024;
-constexpr uint32_t CH_MISC = 2 * ST_BYTES, CH_BYTES = CH_MISC + 256 + 1024;
-// TMEM columns.  A lane's columns of each belong to four threads, a quarter each; a quarter of an operand lies over the quarter
-// that its thread has read, both terms one after the other.
-//   S   state (its operand; then what is added to it)      P   K S, then Y      R   Q S; backwards att^T dO
-//   U   Y sys, its two shares in U and W; then what goes to the state in U, and W = beta U in W
-//   X   att W; backwards scale e^G dO
-constexpr uint32_t TM_S = 0, TM_P = 128, TM_R = 192, TM_U = 256, TM_W = 320, TM_X = 384;
-enum { B_FULL0, B_FULL1, B_TMA0, B_TMA1, B_P, B_U, B_S, B_O, B_END, B_AY, B_AW, B_AS, B_AF, NB };
+// and two tiles [64][128], plain, that leave by bulk copies: o (backwards dV), U (mu); and a copy of e^G for each warp that computes o
+constexpr uint32_t CH_O = 2 * ST_BYTES, CH_V = CH_O + VAL_BYTES, CH_EG = CH_V + VAL_BYTES, CH_MISC = CH_EG + CH_EW * DQ * 4, CH_BYTES = CH_MISC + 256 + 1024;
+// TMEM columns.  A lane's columns of each belong to two threads, two of its quarters each, taken one after the other; a quarter of
+// an operand lies over the quarter that its thread has read, both terms one after the other.
+//   S   state (its operand; then what is added to it)
+//   P   K S, then Y, then forwards att W          R   Q S; backwards att^T dO
+//   U   sys Y, its two shares in U and W; then what goes to the state in U, and W = beta U in W
+//   X   backwards scale e^G dO
+// Forwards P and R are there twice, for even and odd chunks: o is read from them while the next chunk runs.
+template <bool BACK>
+struct Cols {
+    static constexpr uint32_t S = 0, U = BACK ? 256 : 384, W = U + 64, X = 384;
+    static __device__ __forceinline__ uint32_t P(int c) { return BACK ? 128 : 128 + 128 * (c & 1); }
+    static __device__ __forceinline__ uint32_t R(int c) { return P(c) + 64; }
+};
+// Barriers.  A wait tells the completions of a barrier apart by their parity: nothing completes twice before every waiter has seen the
+// first, because a waiter's own next step is needed for the second; where that is two steps off there is one barrier
+// for even chunks and one for odd.
+enum { B_FULL0, B_FULL1, B_TMA0, B_TMA1, B_O0, B_O1, B_WO0, B_WO1, B_EG0, B_EG1, B_P, B_U, B_S, B_END, B_AF, B_WV, B_FO, B_FV,
+       B_AY, B_AW = B_AY + 2, B_AS = B_AW + 2, NB = B_AS + 2 };   // (one for each thread's first quarter, one for its second)
+
+// a column of 16 tokens of one value, two to a register, into a plain tile
+__device__ __forceinline__ void tile_column(unsigned short *to, const uint32_t (&y)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        to[2 * e * 128] = (unsigned short)y[e];
+        to[(2 * e + 1) * 128] = (unsigned short)(y[e] >> 16);
+    }
+}
+// and to rows `step` elements apart, `left` of them
+__device__ __forceinline__ void st_column(__nv_bfloat16 *p, int64_t step, const uint32_t (&y)[8], int left) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        if (e < left) *reinterpret_cast<unsigned short *>(p) = (unsigned short)(y[e >> 1] >> (16 * (e & 1)));
+        p += step;
+    }
+}
 
 struct ChainBars {
     uint64_t bar[NB];
@@ -288,31 +318,8 @@ __device__ __forceinline__ void ld_gates(f32x2 &g0, f32x2 &g1, const float *p) {
     g0 = v.x;
     g1 = v.y;
 }
-// a column of 16 tokens of one value, rounded, to rows `step` elements apart
-__device__ __forceinline__ void st_column(__nv_bfloat16 *p, int64_t step, const f32x2 (&v)[8], int left) {
-    if (left >= 16) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float x, y;
-            up2(v[e], x, y);
-            const uint32_t h = pack_bf16(x, y);
-            *reinterpret_cast<unsigned short *>(p) = (unsigned short)h;
-            p += step;
-            *reinterpret_cast<unsigned short *>(p) = (unsigned short)(h >> 16);
-            p += step;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float x, y;
-            up2(v[e], x, y);
-            if (2 * e < left) p[2 * e * step] = __float2bfloat16_rn(x);
-            if (2 * e + 1 < left) p[(2 * e + 1) * step] = __float2bfloat16_rn(y);
-        }
-    }
-}
-
-template <bool BACK>
+// KEEP: U, or mu, and the states are left for the gradients; OUT: o is computed
+template <bool BACK, bool KEEP, bool OUT>
 __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __grid_constant__ DeltaMaps m) {
     extern __shared__ uint8_t raw[];
     uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -321,8 +328,11 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
     const int s = blockIdx.x / a.H, h = blockIdx.x % a.H, grp = h / (a.H / a.G);
     if (tid == 0) {
         for (int b : {B_FULL0, B_FULL1}) mbar_init(&ms->bar[b], CH_LW);
-        for (int b : {B_TMA0, B_TMA1, B_P, B_U, B_S, B_O, B_END}) mbar_init(&ms->bar[b], 1);
-        for (int b : {B_AY, B_AW, B_AS, B_AF}) mbar_init(&ms->bar[b], CH_CW);
+        for (int b : {B_TMA0, B_TMA1, B_O0, B_O1, B_P, B_U, B_S, B_END, B_FO, B_FV}) mbar_init(&ms->bar[b], 1);
+        mbar_init(&ms->bar[B_WV], CH_CW);
+        for (int b = B_AY; b < NB; ++b) mbar_init(&ms->bar[b], CH_CW);
+        for (int b : {B_AF, B_EG0, B_EG1}) mbar_init(&ms->bar[b], CH_EW);
+        for (int b : {B_WO0, B_WO1}) mbar_init(&ms->bar[b], BACK ? CH_CW : CH_EW);
         ms->abort_ = 0;
         fence_mbar_init();
     }
@@ -335,7 +345,8 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
     const int n = (q.len + DQ - 1) / DQ;
     volatile int *ab = &ms->abort_;
     auto wait = [&](int b, int c) { return mbar_wait_abort(&ms->bar[b], c & 1, ab); };   // the (c + 1)-th completion
-    auto full = [&](int c) { return mbar_wait_abort(&ms->bar[B_FULL0 + (c & 1)], (c >> 1) & 1, ab); };
+    auto wait2 = [&](int b, int c) { return mbar_wait_abort(&ms->bar[b + (c & 1)], (c >> 1) & 1, ab); };   // of a pair
+    auto full = [&](int c) { return wait2(B_FULL0, c); };
     // a warp's one arrival, after what its lanes have written
     auto arrive = [&](int b) {
         tc_fence_before();
@@ -343,187 +354,246 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         if (lane == 0) mbar_arrive(&ms->bar[b]);
     };
     auto stage = [&](int c) { return sm + (c & 1) * ST_BYTES; };
-    const bool outputs = BACK || a.o != nullptr;
+    constexpr bool outputs = BACK || OUT;
+    using C = Cols<BACK>;
 
     if (w < CH_CW) {
-        // ------------------------------------------------------------ four threads a lane: quarter qu of the columns
-        const int qu = w >> 2, v = (w & 3) * 32 + lane;
+        // ------------------------------------------------------------ two threads a lane: quarters 2 hf and 2 hf + 1 of the columns
+        const int hf = w >> 2, v = (w & 3) * 32 + lane;
         const uint32_t at = tmem + ((uint32_t)(w & 3) << 21);
         const bool mine = v < a.V;
-        f32x2 S[16];                                         // row v, keys 32 qu ..
-        const int64_t row = (((int64_t)s * a.H + h) * a.V + v) * a.K + 32 * qu;
+        f32x2 S[32];                                         // row v, keys 64 hf ..
+        const int64_t row = (((int64_t)s * a.H + h) * a.V + v) * a.K + 64 * hf;
         {
             const void *in = BACK ? a.dfinal : a.init;
             const bool f32 = BACK ? !a.dfinal_bf16 : !a.init_bf16;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int k = 32 * qu + 2 * e;
+            for (int e = 0; e < 32; ++e) {
+                const int k = 64 * hf + 2 * e;
                 const float x = in && mine && k < a.K ? delta_ld(in, f32, row + 2 * e) : 0.f;
                 const float y = in && mine && k + 1 < a.K ? delta_ld(in, f32, row + 2 * e + 1) : 0.f;
                 S[e] = pk2(x, y);
             }
         }
-        uint8_t *kept = static_cast<uint8_t *>(BACK ? a.dS : a.S), *vals = static_cast<uint8_t *>(BACK ? a.mu : a.U);
-        // the state as chunk c's operand, and kept as the one that enters it (backwards: whose gradient leaves it)
-        auto publish = [&](int c) {
-            uint8_t *to = kept + (((int64_t)q.slot0 + (BACK ? n - 1 - c : c)) * a.H + h) * STATE_BYTES + (qu >> 1) * (STATE_BYTES / 2) + v * 128;
+        uint8_t *kept = static_cast<uint8_t *>(BACK ? a.dS : a.S);
+        // quarter 2 hf + g of the state as chunk c's operand, and kept as the state that enters it (backwards: whose gradient leaves it)
+        auto publish = [&](int c, int g) {
+            uint32_t hi[16];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t hi[8], lo[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) split_pair(S[8 * g + e], hi[e], lo[e]);
-                tmem_st8(at + TM_S + 32 * qu + 8 * g, hi);
-                tmem_st8(at + TM_S + 32 * qu + 16 + 8 * g, lo);
-                if (kept)
-#pragma unroll
-                    for (int p = 0; p < 2; ++p)
-                        *reinterpret_cast<uint4 *>(to + (((4 * (qu & 1) + 2 * g + p) ^ (v & 7)) << 4)) = make_uint4(hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
-            }
-            tmem_wait_st();
-            arrive(B_AS);
-        };
-        if (n > 0) publish(0);
-        for (int c = 0; c < n; ++c) {
-            const int ci = BACK ? n - 1 - c : c, t0 = ci * DQ + 16 * qu, left = q.len - t0;   // this thread's 16 tokens
-            const int64_t ch = ((int64_t)q.slot0 + ci) * a.H + h;
-            const uint8_t *st = stage(c);
-            const float *gate = reinterpret_cast<const float *>(st + ST_OPS + GATES) + 16 * qu;
-            if (!full(c)) break;
-            const float whole = reinterpret_cast<const float *>(st + ST_OPS + GATES)[DQ - 1];
-            f32x2 x[8], r[8], y[8], g0, g1;
-            // V (dO) of the lane's value while the first product runs
-            {
-                const uint8_t *xs = st + ST_X + (v >> 6) * HALF + 16 * qu * 128 + (v & 7) * 2;
+            for (int d = 0; d < 2; ++d) {
+                uint32_t h8[8], lo[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const uint32_t u0 = *reinterpret_cast<const unsigned short *>(xs + 2 * e * 128 + ((((v & 63) >> 3) ^ ((2 * e) & 7)) << 4));
-                    const uint32_t u1 = *reinterpret_cast<const unsigned short *>(xs + (2 * e + 1) * 128 + ((((v & 63) >> 3) ^ ((2 * e + 1) & 7)) << 4));
-                    y[e] = pk2(bf_lo(u0), bf_lo(u1));
+                    split_pair(S[16 * g + 8 * d + e], h8[e], lo[e]);
+                    hi[8 * d + e] = h8[e];
                 }
+                tmem_st8(at + C::S + 64 * hf + 32 * g + 16 * d, h8);
+                tmem_st8(at + C::S + 64 * hf + 32 * g + 16 * d + 8, lo);
             }
-            if (BACK) {                                      // scale e^G dO
-                const f32x2 sc = pk2(a.scale, a.scale);
+            tmem_wait_st();
+            arrive(B_AS + g);
+            if (KEEP) {
+                uint8_t *to = kept + (((int64_t)q.slot0 + (BACK ? n - 1 - c : c)) * a.H + h) * STATE_BYTES + hf * (STATE_BYTES / 2) + v * 128;
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    ld_gates(g0, g1, gate + 2 * e);
-                    y[e] = mul2(mul2(sc, g0), y[e]);
-                    y[e + 1] = mul2(mul2(sc, g1), y[e + 1]);
-                }
-                put_terms(at + TM_X + 16 * qu, y);
-                tmem_wait_st();
-                arrive(B_AF);
+                for (int p = 0; p < 4; ++p)
+                    *reinterpret_cast<uint4 *>(to + (((4 * g + p) ^ (v & 7)) << 4)) = make_uint4(hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
             }
-            // ---- Y = V - e^G P; backwards N = scale att^T dO + e^(Gc - G) P
+        };
+        if (n > 0) {
+            publish(0, 0);
+            publish(0, 1);
+        }
+        const f32x2 sc = pk2(a.scale, a.scale);
+        for (int c = 0; c < n; ++c) {
+            const int ci = BACK ? n - 1 - c : c;
+            const float *gates = reinterpret_cast<const float *>(stage(c) + ST_OPS + GATES);
+            if (!full(c)) break;
+            const float whole = gates[DQ - 1];
+            f32x2 x[8], y[8], g0, g1;
+            // ---- Y = -e^G P (V's part of U is a product of its own); backwards N = scale att^T dO + e^(Gc - G) P
             if (!wait(B_P, c)) break;
             tc_fence_after();
-            tmem_ld16x2(at + TM_P + 16 * qu, x);
-            if (outputs) tmem_ld16x2(at + TM_R + 16 * qu, r);
-            tmem_wait_ld();
-            if (BACK) {
-                const f32x2 sc = pk2(a.scale, a.scale);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int i0 = 32 * hf + 16 * g;             // 16 tokens
+                tmem_ld16x2(at + C::P(c) + i0, x);
+                if (BACK) tmem_ld16x2(at + C::R(c) + i0, y);
+                tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                    ld_gates(g0, g1, gate + DQ + 2 * e);
-                    y[e] = fma2(g0, x[e], mul2(sc, r[e]));
-                    y[e + 1] = fma2(g1, x[e + 1], mul2(sc, r[e + 1]));
+                    ld_gates(g0, g1, gates + (BACK ? 1 : 5) * DQ + i0 + 2 * e);
+                    y[e] = BACK ? fma2(g0, x[e], mul2(sc, y[e])) : mul2(g0, x[e]);
+                    y[e + 1] = BACK ? fma2(g1, x[e + 1], mul2(sc, y[e + 1])) : mul2(g1, x[e + 1]);
                 }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    ld_gates(g0, g1, gate + 5 * DQ + 2 * e);
-                    y[e] = fma2(g0, x[e], y[e]);
-                    y[e + 1] = fma2(g1, x[e + 1], y[e + 1]);
-                    r[e] = mul2(g0, r[e]);                   // -e^G Q S
-                    r[e + 1] = mul2(g1, r[e + 1]);
-                }
+                put_terms(at + C::P(c) + i0, y);
+                tmem_wait_st();
+                arrive(B_AY + g);
             }
-            put_terms(at + TM_P + 16 * qu, y);
-            tmem_wait_st();
-            arrive(B_AY);
             // ---- U (backwards mu)
             if (!wait(B_U, c)) break;
             tc_fence_after();
-            tmem_ld16x2(at + TM_U + 16 * qu, x);
-            tmem_ld16x2(at + TM_W + 16 * qu, y);
-            tmem_wait_ld();
+            bool go = true;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = add2(x[e], y[e]);
-            if (vals) {
-                uint8_t *to = vals + ch * VAL_BYTES + (v >> 6) * HALF + 16 * qu * 128 + (v & 7) * 2;
+            for (int g = 0; g < 2; ++g) {
+                const int i0 = 32 * hf + 16 * g;
+                tmem_ld16x2(at + C::U + i0, x);
+                tmem_ld16x2(at + C::W + i0, y);
+                tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < 8; ++e) x[e] = add2(x[e], y[e]);
+                uint32_t hi[8], lo[8], wb[8];
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    f32x2 d0, d1;
+                    ld_gates(g0, g1, gates + 2 * DQ + i0 + 2 * e);
+                    ld_gates(d0, d1, gates + (BACK ? 5 * DQ : DQ) + i0 + 2 * e);
+                    g0 = mul2(g0, x[e]);                     // W = beta U, lam = beta mu
+                    g1 = mul2(g1, x[e + 1]);
                     float p, o;
-                    up2(x[e], p, o);
-                    const uint32_t b2 = pack_bf16(p, o);
-                    *reinterpret_cast<unsigned short *>(to + 2 * e * 128 + ((((v & 63) >> 3) ^ ((2 * e) & 7)) << 4)) = (unsigned short)b2;
-                    *reinterpret_cast<unsigned short *>(to + (2 * e + 1) * 128 + ((((v & 63) >> 3) ^ ((2 * e + 1) & 7)) << 4)) = (unsigned short)(b2 >> 16);
+                    up2(g0, p, o);
+                    wb[e] = pack_bf16(p, o);
+                    up2(g1, p, o);
+                    wb[e + 1] = pack_bf16(p, o);
+                    split_pair(mul2(d0, g0), hi[e], lo[e]);
+                    split_pair(mul2(d1, g1), hi[e + 1], lo[e + 1]);
+                }
+                tmem_st8(at + C::U + i0, hi);
+                tmem_st8(at + C::U + i0 + 8, lo);
+                if (!BACK) tmem_st8(at + C::W + i0, wb);
+                tmem_wait_st();
+                arrive(B_AW + g);
+                if (KEEP) {
+                    if (g == 0 && c > 0) go = wait(B_FV, c - 1);
+                    if (!go) break;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float p, o;
+                        up2(x[e], p, o);
+                        hi[e] = pack_bf16(p, o);
+                    }
+                    tile_column(reinterpret_cast<unsigned short *>(sm + CH_V) + i0 * 128 + v, hi);
+                    if (g == 1) {
+                        fence_proxy_async_smem();
+                        arrive(B_WV);
+                    }
+                }
+                if (BACK) {                                  // dV: a whole chunk through a tile, as one copy; another by itself
+                    if (g == 0 && c > 0) go = wait(B_FO, c - 1);
+                    if (!go) break;
+                    if (m.has_out && q.len - ci * DQ >= DQ) {
+                        tile_column(reinterpret_cast<unsigned short *>(sm + CH_O) + i0 * 128 + v, wb);
+                        if (g == 1) fence_proxy_async_smem();
+                    } else if (mine) {
+                        st_column(static_cast<__nv_bfloat16 *>(a.dv) + q.b * a.dvs[0] + (q.t0 + ci * DQ + i0) * a.dvs[1] + h * a.dvs[2] + v, a.dvs[1], wb, q.len - ci * DQ - i0);
+                    }
+                    if (g == 1) arrive(B_WO0 + (c & 1));
                 }
             }
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                ld_gates(g0, g1, gate + 2 * DQ + 2 * e);
-                x[e] = mul2(g0, x[e]);                       // W = beta U, lam = beta mu
-                x[e + 1] = mul2(g1, x[e + 1]);
-                ld_gates(g0, g1, gate + (BACK ? 5 * DQ : DQ) + 2 * e);
-                y[e] = mul2(g0, x[e]);
-                y[e + 1] = mul2(g1, x[e + 1]);
-            }
-            put_terms(at + TM_U + 16 * qu, y);
-            if (!BACK) {
-                uint32_t hi[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float p, o;
-                    up2(x[e], p, o);
-                    hi[e] = pack_bf16(p, o);
-                }
-                tmem_st8(at + TM_W + 16 * qu, hi);
-            }
-            tmem_wait_st();
-            arrive(B_AW);
-            if (BACK && mine)
-                st_column(static_cast<__nv_bfloat16 *>(a.dv) + q.b * a.dvs[0] + (q.t0 + t0) * a.dvs[1] + h * a.dvs[2] + v, a.dvs[1], x, left);
             // ---- the state
-            if (!wait(B_S, c)) break;
+            if (!go || !wait(B_S, c)) break;
             tc_fence_after();
             const f32x2 wh = pk2(whole, whole);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                tmem_ld16x2(at + TM_S + 32 * qu + 16 * g, x);
+                tmem_ld16x2(at + C::S + 64 * hf + 32 * g, x);
+                tmem_ld16x2(at + C::S + 64 * hf + 32 * g + 16, y);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) S[8 * g + e] = fma2(wh, S[8 * g + e], x[e]);
-            }
-            if (c + 1 < n) publish(c + 1);
-            // ---- o, while the next chunk's first product runs
-            if (!BACK && outputs) {
-                if (!wait(B_O, c)) break;
-                tc_fence_after();
-                tmem_ld16x2(at + TM_X + 16 * qu, x);
-                tmem_wait_ld();
-                tc_fence_before();                           // (the next product into these columns follows this thread's next arrival)
-                const f32x2 sc = pk2(a.scale, a.scale), minus = pk2(-1.f, -1.f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = mul2(sc, fma2(minus, r[e], x[e]));
-                if (mine)
-                    st_column(static_cast<__nv_bfloat16 *>(a.o) + q.b * a.os[0] + (q.t0 + t0) * a.os[1] + h * a.os[2] + v, a.os[1], x, left);
+                for (int e = 0; e < 8; ++e) {
+                    S[16 * g + e] = fma2(wh, S[16 * g + e], x[e]);
+                    S[16 * g + 8 + e] = fma2(wh, S[16 * g + 8 + e], y[e]);
+                }
+                if (c + 1 < n) publish(c + 1, g);
             }
         }
         void *out = BACK ? a.dinit : a.final;
         const bool f32 = BACK ? !a.dinit_bf16 : !a.final_bf16;
         if (out && mine)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int k = 32 * qu + 2 * e;
+            for (int e = 0; e < 32; ++e) {
+                const int k = 64 * hf + 2 * e;
                 float x, y;
                 up2(S[e], x, y);
                 if (k < a.K) delta_st(out, f32, row + 2 * e, x);
                 if (k + 1 < a.K) delta_st(out, f32, row + 2 * e + 1, y);
             }
         tc_fence_before();
-    } else if (w < CH_CW + CH_LW) {
+    } else if (w < CH_CW + CH_EW) {
+        // ------------------------------------------------------------ one thread a lane, off the chain
+        const int v = (w & 3) * 32 + lane;
+        const uint32_t at = tmem + ((uint32_t)(w & 3) << 21);
+        const f32x2 sc = pk2(a.scale, a.scale);
+        if (BACK) {
+            for (int c = 0; c < n; ++c) {                    // scale e^G dO
+                if (!full(c) || (c > 0 && !wait2(B_O0, c - 1))) break;
+                const float *gate = reinterpret_cast<const float *>(stage(c) + ST_OPS + GATES);
+                const uint8_t *xs = stage(c) + ST_X + (v >> 6) * HALF + (v & 7) * 2;
+                tc_fence_after();
+#pragma unroll
+                for (int qu = 0; qu < 4; ++qu) {
+                    f32x2 y[8], g0, g1;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int i = 16 * qu + 2 * e;
+                        const uint32_t u0 = *reinterpret_cast<const unsigned short *>(xs + i * 128 + ((((v & 63) >> 3) ^ (i & 7)) << 4));
+                        const uint32_t u1 = *reinterpret_cast<const unsigned short *>(xs + (i + 1) * 128 + ((((v & 63) >> 3) ^ ((i + 1) & 7)) << 4));
+                        y[e] = mul2(sc, pk2(bf_lo(u0), bf_lo(u1)));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        ld_gates(g0, g1, gate + 16 * qu + 2 * e);
+                        y[e] = mul2(g0, y[e]);
+                        y[e + 1] = mul2(g1, y[e + 1]);
+                    }
+                    put_terms(at + C::X + 16 * qu, y);
+                }
+                tmem_wait_st();
+                arrive(B_AF);
+            }
+        } else if (outputs) {
+            float *eg = reinterpret_cast<float *>(sm + CH_EG) + (w & 3) * DQ;
+            for (int c = 0; c < n; ++c) {                    // o = scale (e^G Q S + att W)
+                if (!full(c)) break;
+                __syncwarp();
+                const float *gate = reinterpret_cast<const float *>(stage(c) + ST_OPS + GATES);
+                eg[lane] = gate[lane];                       // (the stage is filled anew once the products are done with it)
+                eg[32 + lane] = gate[32 + lane];
+                arrive(B_EG0 + (c & 1));
+                const bool tile = m.has_out && q.len - c * DQ >= DQ;
+                if (!wait2(B_O0, c) || (c > 0 && !wait(B_FO, c - 1))) break;
+                tc_fence_after();
+                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + q.b * a.os[0] + (q.t0 + (int64_t)c * DQ) * a.os[1] + h * a.os[2] + v;
+                unsigned short *to = reinterpret_cast<unsigned short *>(sm + CH_O) + v;
+#pragma unroll 1
+                for (int qu = 0; qu < 4; ++qu) {
+                    f32x2 x[8], r[8], g0, g1;
+                    tmem_ld16x2(at + C::P(c) + 16 * qu, x);
+                    tmem_ld16x2(at + C::R(c) + 16 * qu, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        ld_gates(g0, g1, eg + 16 * qu + 2 * e);
+                        x[e] = mul2(sc, fma2(g0, r[e], x[e]));
+                        x[e + 1] = mul2(sc, fma2(g1, r[e + 1], x[e + 1]));
+                    }
+                    uint32_t b2[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float p, o2;
+                        up2(x[e], p, o2);
+                        b2[e] = pack_bf16(p, o2);
+                    }
+                    if (tile) tile_column(to + 16 * qu * 128, b2);
+                    else if (v < a.V) st_column(o + 16 * qu * a.os[1], a.os[1], b2, q.len - c * DQ - 16 * qu);
+                }
+                if (tile) fence_proxy_async_smem();
+                arrive(B_WO0 + (c & 1));                                // (and the columns may be written again)
+            }
+        }
+        tc_fence_before();
+    } else if (w < CH_CW + CH_EW + CH_LW) {
         // ------------------------------------------------------------ loads
-        const int t = tid - CH_C;
+        const int t = tid - CH_L0;
         const CUtensorMap *mx = BACK ? &m.dO : &m.v;
         const bool has_x = BACK ? m.has_dO : m.has_v;
         auto chunk = [&](int c) {
@@ -551,7 +621,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         if (n > 0) issue(0);
         if (n > 1) issue(1);
         for (int c = 0; c < n; ++c) {
-            if (!mbar_wait_abort(&ms->bar[B_TMA0 + (c & 1)], (c >> 1) & 1, ab)) break;
+            if (!wait2(B_TMA0, c)) break;
             if (const int len = chunk(c).len; len < DQ) {    // the next sequence's tokens
                 if (m.has_k) zero_rows<CH_L>(stage(c) + ST_KQ, 2 * HALF, len, t);
                 if (has_x) zero_rows<CH_L>(stage(c) + ST_X, HALF, len, t);
@@ -559,11 +629,38 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
             }
             fence_proxy_async_smem();
             arrive(B_FULL0 + (c & 1));
-            if (c + 2 < n) {
-                if (!wait(B_O, c)) break;                    // the products of chunk c are done with its stage (and so is every lane)
-                issue(c + 2);
+            // chunk c has been announced; chunk c - 1's products are done with its stage (and so is every lane): chunk c + 1
+            if (c > 0 && c + 1 < n) {
+                if (!wait2(B_O0, c - 1) || (!BACK && OUT && !wait2(B_EG0, c - 1))) break;
+                issue(c + 1);
             }
         }
+    } else if (w == CH_CW + CH_EW + CH_LW) {
+        // ------------------------------------------------------------ tiles that leave
+        if (lane == 0) {
+            uint8_t *vals = static_cast<uint8_t *>(BACK ? a.mu : a.U);
+            for (int c = 0; c < n; ++c) {
+                const int ci = BACK ? n - 1 - c : c;
+                if (KEEP) {
+                    if (!wait(B_WV, c)) break;
+                    bulk_store(vals + (((int64_t)q.slot0 + ci) * a.H + h) * VAL_BYTES, sm + CH_V, VAL_BYTES);
+                    bulk_commit();
+                    bulk_wait_read0();
+                    mbar_arrive(&ms->bar[B_FV]);
+                }
+                if (outputs) {
+                    if (!wait2(B_WO0, c)) break;
+                    if (m.has_out && q.len - ci * DQ >= DQ) {
+                        tma_store_4d(&m.out, sm + CH_O, 0, h, q.t0 + ci * DQ, q.b);
+                        bulk_commit();
+                        bulk_wait_read0();
+                    }
+                    mbar_arrive(&ms->bar[B_FO]);
+                }
+            }
+            bulk_wait0();
+        }
+        __syncwarp();
     } else {
         // ------------------------------------------------------------ the products
         if (lane == 0) {
@@ -576,49 +673,72 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        umma_bf16(tmem + TM_R, mnmaj(X, k, HALF), mnmaj(ops + ATT, k, HALF), idesc_bf16(128, 64, 1, 1), k > 0);
+                        umma_bf16(tmem + C::R(c), mnmaj(X, k, HALF), mnmaj(ops + ATT, k, HALF), idesc_bf16(128, 64, 1, 1), k > 0);
                 }
-                if (!wait(B_AS, c)) break;
-                tc_fence_after();
-                // K S and Q S in one: their rows are the 128 rows of the right operand
+                bool go = BACK || !outputs || c < 2 || wait2(B_WO0, c - 2);   // o of the chunk before last has been read
+                // K S and Q S in one: their rows are the 128 rows of the right operand.  Each thread's first quarter
+                // while it still writes the second; so with the other products.
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t A = tmem + TM_S + 32 * (k >> 1) + 8 * (k & 1);
-                    umma_bf16_ta(tmem + TM_P, A, kmaj(K, k, 2 * HALF), BACK ? id64 : id128, k > 0);
-                    umma_bf16_ta(tmem + TM_P, A + 16, kmaj(K, k, 2 * HALF), BACK ? id64 : id128, 1);
+                for (int g = 0; g < 2 && go; ++g) {
+                    if (!(go = wait(B_AS + g, c))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const int k = 4 * (d >> 1) + 2 * g + (d & 1);
+                        const uint32_t A = tmem + C::S + 16 * k;
+                        umma_bf16_ta(tmem + C::P(c), A, kmaj(K, k, 2 * HALF), BACK ? id64 : id128, g || d);
+                        umma_bf16_ta(tmem + C::P(c), A + 8, kmaj(K, k, 2 * HALF), BACK ? id64 : id128, 1);
+                    }
                 }
+                if (!go) break;
                 umma_commit(&ms->bar[B_P]);
+                if (!BACK) {                                 // V's part of U: V by columns, both terms of sys
+                    if (c > 0 && !wait2(B_O0, c - 1)) break;   // (att W has read its operand there)
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16(tmem + C::U, mnmaj(X, k, HALF), kmaj(ops + SYS_HI, k, 0), idesc_bf16(128, 128, 1, 0), k > 0);
+                }
                 auto from_o = [&](int term) {                // (scale e^G dO)^T Q
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        umma_bf16_ta(tmem + TM_S, tmem + TM_X + 16 * k + 8 * term, mnmaj(Q, k, 2 * HALF), id128t, term || k > 0);
+                        umma_bf16_ta(tmem + C::S, tmem + C::X + 16 * k + 8 * term, mnmaj(Q, k, 2 * HALF), id128t, term || k > 0);
                 };
                 if (BACK) {
                     if (!wait(B_AF, c) || !wait(B_P, c)) break;   // P is done with the columns that are written now
                     tc_fence_after();
                     from_o(0);
                 }
-                if (!wait(B_AY, c)) break;
-                tc_fence_after();
                 // both terms of sys in one: its images are the 128 rows of the right operand
 #pragma unroll
-                for (int k = 0; k < 4; ++k) umma_bf16_ta(tmem + TM_U, tmem + TM_P + 16 * k, kmaj(ops + SYS_HI, k, 0), id128, k > 0);
+                for (int g = 0; g < 2 && go; ++g) {
+                    if (!(go = wait(B_AY + g, c))) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) umma_bf16_ta(tmem + TM_U, tmem + TM_P + 16 * k + 8, kmaj(ops + SYS_HI, k, 0), id64, 1);
+                    for (int k = g; k < 4; k += 2) {
+                        umma_bf16_ta(tmem + C::U, tmem + C::P(c) + 16 * k, kmaj(ops + SYS_HI, k, 0), id128, !BACK || k > 0);
+                        umma_bf16_ta(tmem + C::U, tmem + C::P(c) + 16 * k + 8, kmaj(ops + SYS_HI, k, 0), id128, 1);
+                    }
+                }
+                if (!go) break;
                 umma_commit(&ms->bar[B_U]);
                 if (BACK) from_o(1);
-                if (!wait(B_AW, c)) break;
-                tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    umma_bf16_ta(tmem + TM_S, tmem + TM_U + 16 * k, mnmaj(K, k, 2 * HALF), id128t, BACK || k > 0);
-                    umma_bf16_ta(tmem + TM_S, tmem + TM_U + 16 * k + 8, mnmaj(K, k, 2 * HALF), id128t, 1);
+                for (int g = 0; g < 2 && go; ++g) {
+                    if (!(go = wait(B_AW + g, c))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = g; k < 4; k += 2) {
+                        umma_bf16_ta(tmem + C::S, tmem + C::U + 16 * k, mnmaj(K, k, 2 * HALF), id128t, BACK || k > 0);
+                        umma_bf16_ta(tmem + C::S, tmem + C::U + 16 * k + 8, mnmaj(K, k, 2 * HALF), id128t, 1);
+                    }
                 }
+                if (!go) break;
                 umma_commit(&ms->bar[B_S]);
                 if (!BACK && outputs)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) umma_bf16_ta(tmem + TM_X, tmem + TM_W + 16 * k, kmaj(ops + ATT, k, 0), id64, k > 0);
-                umma_commit(&ms->bar[B_O]);
+                    for (int k = 0; k < 4; ++k) umma_bf16_ta(tmem + C::P(c), tmem + C::W + 16 * k, kmaj(ops + ATT, k, 0), id64, k > 0);
+                umma_commit(&ms->bar[B_O0 + (c & 1)]);
             }
             // nothing is in flight when the tensor memory is given up, also where a wait has given up
             umma_commit(&ms->bar[B_END]);
@@ -696,11 +816,10 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
         if (tid == 0) {
             uint64_t *b = bar + L_HEAD;
             mbar_expect_tx(b, GATE_BYTES + 2 * VAL_BYTES + 2 * STATE_BYTES + (m.has_dO ? TOK_BYTES : 0));
-            const uint8_t *mu = static_cast<const uint8_t *>(a.mu) + ch * VAL_BYTES;
-            bulk_load(sm + G_A, mu, HALF, b);
-            bulk_load(sm + G_A + 2 * HALF, mu + HALF, HALF, b);
+            const DeltaChunk vals{0, 0, DQ};
+            tma_rows(sm + G_A, 2 * HALF, &m.mu, b, vals, (int)ch);
             if (m.has_dO) tma_rows(sm + G_A + HALF, 2 * HALF, &m.dO, b, c, h);
-            bulk_load(sm + G_U, static_cast<const uint8_t *>(a.U) + ch * VAL_BYTES, VAL_BYTES, b);
+            tma_rows(sm + G_U, HALF, &m.U, b, vals, (int)ch);
             bulk_load(sm + G_GATE, static_cast<const uint8_t *>(a.tiles) + ch * OPS_BYTES + GATES, GATE_BYTES, b);
             bulk_load(sm + G_S, static_cast<const uint8_t *>(a.S) + ch * STATE_BYTES, STATE_BYTES, b);
             bulk_load(sm + G_DS, static_cast<const uint8_t *>(a.dS) + ch * STATE_BYTES, STATE_BYTES, b);
@@ -933,17 +1052,17 @@ cudaError_t prep(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
     k_prep<BACK><<<(unsigned)((int64_t)a.nslots * a.H), PREP_NT, P_BYTES, st>>>(a, m);
     return cudaGetLastError();
 }
-template <bool BACK>
+template <bool BACK, bool KEEP, bool OUT>
 cudaError_t chain(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
     static int set[64] = {};
-    if (cudaError_t e = ensure_smem_attr(k_chain<BACK>, (int)CH_BYTES, set); e != cudaSuccess) return e;
-    k_chain<BACK><<<(unsigned)(a.nseqs * (int64_t)a.H), CH_NT, CH_BYTES, st>>>(a, m);
+    if (cudaError_t e = ensure_smem_attr(k_chain<BACK, KEEP, OUT>, (int)CH_BYTES, set); e != cudaSuccess) return e;
+    k_chain<BACK, KEEP, OUT><<<(unsigned)(a.nseqs * (int64_t)a.H), CH_NT, CH_BYTES, st>>>(a, m);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-bool delta_map(CUtensorMap *m, const void *p, int64_t inner, int64_t heads, int64_t tokens, int64_t batch, const int64_t *strides) {
+bool delta_map(CUtensorMap *m, const void *p, int64_t inner, int64_t heads, int64_t tokens, int64_t batch, const int64_t *strides, bool out) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     if (encode == nullptr) {
         void *f = nullptr;
@@ -951,6 +1070,9 @@ bool delta_map(CUtensorMap *m, const void *p, int64_t inner, int64_t heads, int6
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess)
             encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     }
+    // the encoder wants the device's context current, which a thread that has made no other call yet (autograd's) has not
+    static thread_local int bound = -1;
+    if (int dev = 0; cudaGetDevice(&dev) == cudaSuccess && dev != bound && cudaSetDevice(dev) == cudaSuccess) bound = dev;
     const int64_t n[3] = {heads, tokens, batch}, s[3] = {strides[2], strides[1], strides[0]};
     if (encode == nullptr || (uintptr_t)p % 16 != 0 || inner % 8 != 0) return false;
     cuuint64_t dims[4] = {(cuuint64_t)inner, (cuuint64_t)heads, (cuuint64_t)tokens, (cuuint64_t)batch}, by[3];
@@ -958,18 +1080,19 @@ bool delta_map(CUtensorMap *m, const void *p, int64_t inner, int64_t heads, int6
         if (n[i] > 1 && (s[i] % 8 != 0 || s[i] < inner || s[i] >= ((int64_t)1 << 38))) return false;
         by[i] = (cuuint64_t)(n[i] > 1 ? s[i] : inner) * 2;
     }
-    const cuuint32_t box[4] = {64, 1, (cuuint32_t)DQ, 1}, step[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {out ? 128u : 64u, 1, (cuuint32_t)DQ, 1}, step[4] = {1, 1, 1, 1};
     return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, by, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  out ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t delta_tc_fwd(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
     if (cudaError_t e = prep<false>(a, m, st); e != cudaSuccess) return e;
-    return chain<false>(a, m, st);
+    return a.S == nullptr ? chain<false, false, true>(a, m, st) : a.o != nullptr ? chain<false, true, true>(a, m, st) : chain<false, true, false>(a, m, st);
 }
 cudaError_t delta_tc_bwd(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
+    if (!m.has_vals) return cudaErrorNotSupported;
     if (cudaError_t e = prep<true>(a, m, st); e != cudaSuccess) return e;
-    if (cudaError_t e = chain<true>(a, m, st); e != cudaSuccess) return e;
+    if (cudaError_t e = chain<true, true, true>(a, m, st); e != cudaSuccess) return e;
     static int set[64] = {};
     if (cudaError_t e = ensure_smem_attr(k_grads, (int)G_BYTES, set); e != cudaSuccess) return e;
     k_grads<<<(unsigned)((int64_t)a.nslots * a.G), GR_NT, G_BYTES, st>>>(a, m);

@@ -19,7 +19,7 @@ constexpr uint32_t GATE_BYTES = DGATES * 4;
 // per chunk and head: the inverse's two terms, att, gates (in the workspace one after the other, as they are loaded)
 constexpr uint32_t SYS_HI = 0, SYS_LO = MAT_BYTES, ATT = 2 * MAT_BYTES, GATES = 3 * MAT_BYTES, OPS_BYTES = GATES + GATE_BYTES;
 constexpr uint32_t STATE_BYTES = 128 * 128 * 2;  // kept state: two images (keys 0..63, 64..127) of 128 rows (values)
-constexpr uint32_t VAL_BYTES = TOK_BYTES;        // kept U, and mu: a tile of 64 tokens
+constexpr uint32_t VAL_BYTES = DQ * 128 * 2;     // kept U, and mu: [64][128], plain
 
 // K-major operand at K step k (16 elements), images of `half` bytes; MN-major operand at K step k (16 rows)
 __device__ __forceinline__ uint64_t kmaj(uint32_t base, int k, uint32_t half) {
@@ -69,14 +69,16 @@ __device__ __forceinline__ const __nv_bfloat16 *tok_rows(const void *p, const in
 }  // namespace dtc
 
 // Tensor maps of the token tensors [feature][head][token][batch row], a box 64 features of 64 tokens; has*: the tensor has one.
+// out: o, backwards dv, without a swizzle, a box 128 features of 64 tokens.  U, mu: [chunk and head][64][128] in the workspace or
+// kept, read as swizzled tiles.
 struct DeltaMaps {
-    CUtensorMap q, k, v, dO;
-    bool has_q, has_k, has_v, has_dO;
+    CUtensorMap q, k, v, dO, out, U, mu;
+    bool has_q, has_k, has_v, has_dO, has_out, has_vals;
 };
 // delta_tc.cu: bf16 data, headdim and dstate up to 128
 cudaError_t delta_tc_fwd(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st);
 // whether the tensor has a map (16-byte rows, strides of 16-byte multiples)
-bool delta_map(CUtensorMap *m, const void *p, int64_t inner, int64_t heads, int64_t tokens, int64_t batch, const int64_t *strides);
+bool delta_map(CUtensorMap *m, const void *p, int64_t inner, int64_t heads, int64_t tokens, int64_t batch, const int64_t *strides, bool out = false);
 cudaError_t delta_tc_bwd(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st);
 
 }  // namespace ssd
