@@ -435,21 +435,31 @@ class GatedDeltaFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, initial_states, cu_seqlens, scale, keep):
-        o, fin, *kept = gated_delta_forward(q, k, v, g, beta, scale=scale, initial_states=initial_states, cu_seqlens=cu_seqlens,
-                                            keep_chunk_states=keep)
+        o, fin, *kept = _lib.fast().delta_fwd(q, k, v, g, beta, initial_states, cu_seqlens, scale, True, -1, keep, None)
         ctx.save_for_backward(q, k, v, g, beta, initial_states, cu_seqlens, kept[0] if keep else None)
         ctx.scale = scale
         ctx.set_materialize_grads(False)
         return o, fin
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, do, dfin):
-        q, k, v, g, beta, init, cu, kept = ctx.saved_tensors
-        do = torch.zeros_like(v, memory_format=torch.contiguous_format) if do is None else do
-        d = gated_delta_backward(q, k, v, g, beta, do if do.stride(-1) == 1 else do.contiguous(), scale=ctx.scale, initial_states=init,
-                                 dfinal_states=None if dfin is None else dfin.contiguous(), cu_seqlens=cu, chunk_states=kept)
-        return d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"], d.get("dinitial_states"), None, None, None
+        return (_once if torch.is_grad_enabled() else _delta_grads)(_delta_grads, ctx, do, dfin)
+
+
+def _delta_grads(_, ctx, do, dfin):
+    q, k, v, g, beta, init, cu, kept = ctx.saved_tensors
+    if do is None:
+        do = torch.zeros_like(v, memory_format=torch.contiguous_format)
+    elif do.stride(-1) != 1:
+        do = do.contiguous()
+    d = _lib.fast().delta_bwd(q, k, v, g, beta, init, cu, ctx.scale, do, None if dfin is None else dfin.contiguous(), kept, None, None)
+    return d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"], d.get("dinitial_states"), None, None, None
+
+
+@torch.autograd.function.once_differentiable
+def _once(f, *args):
+    """f's gradients where a graph of them is asked for: differentiating them again is refused.  (20 us a call, so not otherwise.)"""
+    return f(f, *args)
 
 
 def gated_delta_step(state, q, k, v, g, beta, scale=None, state_indices=None, stream=None):
@@ -499,13 +509,16 @@ class QKNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, mode, interleaved, eps):
         ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
-        ctx.how = dict(mode=mode, interleaved=interleaved, eps=eps)
-        return qk_norm_forward(q, k, q_weight, k_weight, cos, sin, positions, **ctx.how)
+        ctx.how = how = _qk_mode(mode), bool(interleaved), eps
+        return _lib.fast().qk_fwd(q, k, q_weight, k_weight, cos, sin, positions, *how, None)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dq, dk):
-        q, k, wq, wk, cos, sin, pos = ctx.saved_tensors
-        dq, dk = (t if t is None or t.stride(-1) == 1 else t.contiguous() for t in (dq, dk))
-        d = qk_norm_backward(q, k, dq, dk, wq, wk, cos, sin, pos, **ctx.how)
-        return (d["dq"], d.get("dk"), d.get("dq_weight"), d.get("dk_weight")) + (None,) * 6
+        return (_once if torch.is_grad_enabled() else _qk_grads)(_qk_grads, ctx, dq, dk)
+
+
+def _qk_grads(_, ctx, dq, dk):
+    q, k, wq, wk, cos, sin, pos = ctx.saved_tensors
+    dq, dk = (t if t is None or t.stride(-1) == 1 else t.contiguous() for t in (dq, dk))
+    d = _lib.fast().qk_bwd(q, k, wq, wk, cos, sin, pos, *ctx.how, dq, dk, None, None)
+    return d["dq"], d.get("dk"), d.get("dq_weight"), d.get("dk_weight"), None, None, None, None, None, None

@@ -85,7 +85,8 @@ Kept kept_plan(const ssd_delta_problem *p) {
     return k;
 }
 struct Plan {
-    size_t hdr, gates, sys, att, a, tiles, dS, mu, part, kept, total;
+    size_t hdr, gates, sys, att, a, tiles, seg, dS, mu, part, kept, total;
+    int nseg, seglen;
 };
 Plan plan(const ssd_delta_problem *p, bool back, bool kept) {
     const size_t ch = (size_t)slots(p) * p->nheads, mat = ch * DQ * DQ * 4;
@@ -96,6 +97,8 @@ Plan plan(const ssd_delta_problem *p, bool back, bool kept) {
     w.hdr = take(HDR_WORDS * 4);
     if (tc) {
         w.tiles = take(ch * dtc::OPS_BYTES);
+        dtc::delta_segments(nstates(p), p->nheads, (p->seqlen + DQ - 1) / DQ, &w.nseg, &w.seglen);
+        w.seg = take(2 * (size_t)(w.nseg - 1) * nstates(p) * p->nheads * dtc::SEG_BYTES);
     } else {
         w.gates = take(ch * DGATES * 4);
         w.sys = take(mat);
@@ -128,6 +131,9 @@ DeltaArgs make(const ssd_delta_problem *p, const ssd_delta_args *f, const Plan &
     a.scale = p->scale;
     a.hdr = reinterpret_cast<int32_t *>(ws + w.hdr);
     a.tiles = ws + w.tiles;
+    a.nseg = w.nseg; a.seglen = w.seglen;
+    a.segB = ws + w.seg;
+    a.segM = ws + w.seg + (size_t)(w.nseg > 1 ? w.nseg - 1 : 0) * nstates(p) * p->nheads * dtc::SEG_BYTES;
     a.gates = reinterpret_cast<float *>(ws + w.gates);
     a.sys = reinterpret_cast<float *>(ws + w.sys);
     a.att = reinterpret_cast<float *>(ws + w.att);

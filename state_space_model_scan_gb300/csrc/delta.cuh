@@ -51,6 +51,10 @@ struct DeltaArgs {
     void *S, *U, *dS, *mu;
     float *part;                // [2][nslots][H][64][K]: dq and dk of each value head, where heads share a group
     void *tiles;                // tensor-core path: operand images of every chunk and head
+    // tensor-core path: a chain of few heads is cut into nseg segments of seglen chunks; a first launch leaves, for all but the last,
+    // its end from a zero state [nseqs][H][nseg - 1][128][128] fp32 and what it makes of one (as two terms, 64 KB each)
+    int nseg, seglen;
+    void *segB, *segM;
 };
 
 // Sequence s: batch row, first token in the row, length, first chunk.  Whatever cu_seqlens holds, the

@@ -259,7 +259,7 @@ struct Cols {
 // Barriers.  A wait tells the completions of a barrier apart by their parity: nothing completes twice before every waiter has seen the
 // first, because a waiter's own next step is needed for the second; where that is two steps off there is one barrier
 // for even chunks and one for odd.
-enum { B_FULL0, B_FULL1, B_TMA0, B_TMA1, B_O0, B_O1, B_WO0, B_WO1, B_EG0, B_EG1, B_P, B_U, B_S, B_END, B_AF, B_WV, B_FO, B_FV,
+enum { B_FULL0, B_FULL1, B_TMA0, B_TMA1, B_O0, B_O1, B_WO0, B_WO1, B_EG0, B_EG1, B_P, B_U, B_S, B_END, B_AF, B_WV, B_FO, B_FV, B_JM0, B_JM1, B_JD,
        B_AY, B_AW = B_AY + 2, B_AS = B_AW + 2, NB = B_AS + 2 };   // (one for each thread's first quarter, one for its second)
 
 // a column of 16 tokens of one value, two to a register, into a plain tile
@@ -318,17 +318,25 @@ __device__ __forceinline__ void ld_gates(f32x2 &g0, f32x2 &g1, const float *p) {
     g0 = v.x;
     g1 = v.y;
 }
-// KEEP: U, or mu, and the states are left for the gradients; OUT: o is computed
-template <bool BACK, bool KEEP, bool OUT>
+// KEEP: U, or mu, and the states are left for the gradients; OUT: o (backwards dV) is computed; ENDS: a segment's end from a zero state, or
+// its matrix, is left and nothing else
+template <bool BACK, bool KEEP, bool OUT, bool ENDS>
 __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __grid_constant__ DeltaMaps m) {
     extern __shared__ uint8_t raw[];
     uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     ChainBars *ms = reinterpret_cast<ChainBars *>(sm + CH_MISC);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    const int s = blockIdx.x / a.H, h = blockIdx.x % a.H, grp = h / (a.H / a.G);
+    // unit: sequence and head; segment; of a segment's two, its end or (mat) what it makes of the state before it, S -> S M
+    const int units = a.nseqs * a.H, unit = blockIdx.x % units, part = blockIdx.x / units, s = unit / a.H, h = unit % a.H, grp = h / (a.H / a.G);
+    const bool mat = ENDS && part >= a.nseg - 1;
+    const int seg = mat ? part - (a.nseg - 1) + 1 : part;
+    const DeltaSeq q = delta_seq(a, s);
+    const int all = (q.len + DQ - 1) / DQ, c0 = seg * a.seglen;            // chunks of the sequence; the segment's first step
+    if (ENDS ? c0 + a.seglen >= all : seg > 0 && c0 >= all) return;        // no segment follows; nothing in it
+    const int n = min(a.seglen, all - c0), joins = ENDS ? 0 : max(0, seg - 1);
     if (tid == 0) {
         for (int b : {B_FULL0, B_FULL1}) mbar_init(&ms->bar[b], CH_LW);
-        for (int b : {B_TMA0, B_TMA1, B_O0, B_O1, B_P, B_U, B_S, B_END, B_FO, B_FV}) mbar_init(&ms->bar[b], 1);
+        for (int b : {B_TMA0, B_TMA1, B_O0, B_O1, B_P, B_U, B_S, B_END, B_FO, B_FV, B_JM0, B_JM1, B_JD}) mbar_init(&ms->bar[b], 1);
         mbar_init(&ms->bar[B_WV], CH_CW);
         for (int b = B_AY; b < NB; ++b) mbar_init(&ms->bar[b], CH_CW);
         for (int b : {B_AF, B_EG0, B_EG1}) mbar_init(&ms->bar[b], CH_EW);
@@ -341,8 +349,6 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ms->tmem;
-    const DeltaSeq q = delta_seq(a, s);
-    const int n = (q.len + DQ - 1) / DQ;
     volatile int *ab = &ms->abort_;
     auto wait = [&](int b, int c) { return mbar_wait_abort(&ms->bar[b], c & 1, ab); };   // the (c + 1)-th completion
     auto wait2 = [&](int b, int c) { return mbar_wait_abort(&ms->bar[b + (c & 1)], (c >> 1) & 1, ab); };   // of a pair
@@ -354,7 +360,9 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         if (lane == 0) mbar_arrive(&ms->bar[b]);
     };
     auto stage = [&](int c) { return sm + (c & 1) * ST_BYTES; };
-    constexpr bool outputs = BACK || OUT;
+    auto idx = [&](int c) { return BACK ? all - 1 - c0 - c : c0 + c; };    // the chunk of step c
+    // Q and, backwards, dO are needed for the state's sake too
+    const bool outputs = BACK ? !mat : OUT, values = !mat;
     using C = Cols<BACK>;
 
     if (w < CH_CW) {
@@ -364,7 +372,18 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         const bool mine = v < a.V;
         f32x2 S[32];                                         // row v, keys 64 hf ..
         const int64_t row = (((int64_t)s * a.H + h) * a.V + v) * a.K + 64 * hf;
-        {
+        const float *ends = static_cast<const float *>(a.segB) + (int64_t)unit * (a.nseg - 1) * (128 * 128) + v * 128 + 64 * hf;
+        if (!ENDS && seg > 0) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                const float4 x = *reinterpret_cast<const float4 *>(ends + 2 * e);
+                S[e] = pk2(x.x, x.y);
+                S[e + 1] = pk2(x.z, x.w);
+            }
+        } else if (ENDS && (mat || seg > 0)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) S[e] = pk2(mat && v == 64 * hf + 2 * e ? 1.f : 0.f, mat && v == 64 * hf + 2 * e + 1 ? 1.f : 0.f);
+        } else {
             const void *in = BACK ? a.dfinal : a.init;
             const bool f32 = BACK ? !a.dfinal_bf16 : !a.init_bf16;
 #pragma unroll
@@ -377,7 +396,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         }
         uint8_t *kept = static_cast<uint8_t *>(BACK ? a.dS : a.S);
         // quarter 2 hf + g of the state as chunk c's operand, and kept as the state that enters it (backwards: whose gradient leaves it)
-        auto publish = [&](int c, int g) {
+        auto publish = [&](int c, int g, bool keep) {
             uint32_t hi[16];
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
@@ -392,20 +411,41 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
             }
             tmem_wait_st();
             arrive(B_AS + g);
-            if (KEEP) {
-                uint8_t *to = kept + (((int64_t)q.slot0 + (BACK ? n - 1 - c : c)) * a.H + h) * STATE_BYTES + hf * (STATE_BYTES / 2) + v * 128;
+            if (KEEP && keep) {
+                uint8_t *to = kept + (((int64_t)q.slot0 + idx(c)) * a.H + h) * STATE_BYTES + hf * (STATE_BYTES / 2) + v * 128;
 #pragma unroll
                 for (int p = 0; p < 4; ++p)
                     *reinterpret_cast<uint4 *>(to + (((4 * g + p) ^ (v & 7)) << 4)) = make_uint4(hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
             }
         };
+        // the state that enters the segment: from segment to segment S <- S M + end
+        bool go = true;
+        for (int j = 0; j < joins; ++j) {
+            publish(0, 0, false);
+            publish(0, 1, false);
+            if (!(go = wait(B_JD, j))) break;
+            tc_fence_after();
+            ends += 128 * 128;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                f32x2 x[8];
+                tmem_ld16x2(at + C::U + 64 * hf + 16 * g, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float4 y = *reinterpret_cast<const float4 *>(ends + 16 * g + 2 * e);
+                    S[8 * g + e] = add2(x[e], pk2(y.x, y.y));
+                    S[8 * g + e + 1] = add2(x[e + 1], pk2(y.z, y.w));
+                }
+            }
+        }
         if (n > 0) {
-            publish(0, 0);
-            publish(0, 1);
+            publish(0, 0, true);
+            publish(0, 1, true);
         }
         const f32x2 sc = pk2(a.scale, a.scale);
-        for (int c = 0; c < n; ++c) {
-            const int ci = BACK ? n - 1 - c : c;
+        for (int c = 0; c < n && go; ++c) {
+            const int ci = idx(c);
             const float *gates = reinterpret_cast<const float *>(stage(c) + ST_OPS + GATES);
             if (!full(c)) break;
             const float whole = gates[DQ - 1];
@@ -417,8 +457,11 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
             for (int g = 0; g < 2; ++g) {
                 const int i0 = 32 * hf + 16 * g;             // 16 tokens
                 tmem_ld16x2(at + C::P(c) + i0, x);
-                if (BACK) tmem_ld16x2(at + C::R(c) + i0, y);
+                if (BACK && values) tmem_ld16x2(at + C::R(c) + i0, y);
                 tmem_wait_ld();
+                if (BACK && !values)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = 0;
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
                     ld_gates(g0, g1, gates + (BACK ? 1 : 5) * DQ + i0 + 2 * e);
@@ -432,7 +475,6 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
             // ---- U (backwards mu)
             if (!wait(B_U, c)) break;
             tc_fence_after();
-            bool go = true;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 const int i0 = 32 * hf + 16 * g;
@@ -477,7 +519,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                         arrive(B_WV);
                     }
                 }
-                if (BACK) {                                  // dV: a whole chunk through a tile, as one copy; another by itself
+                if (BACK && OUT) {                           // dV: a whole chunk through a tile, as one copy; another by itself
                     if (g == 0 && c > 0) go = wait(B_FO, c - 1);
                     if (!go) break;
                     if (m.has_out && q.len - ci * DQ >= DQ) {
@@ -503,11 +545,31 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                     S[16 * g + e] = fma2(wh, S[16 * g + e], x[e]);
                     S[16 * g + 8 + e] = fma2(wh, S[16 * g + 8 + e], y[e]);
                 }
-                if (c + 1 < n) publish(c + 1, g);
+                if (c + 1 < n) publish(c + 1, g, true);
             }
         }
-        void *out = BACK ? a.dinit : a.final;
+        void *out = ENDS || c0 + n < all ? nullptr : BACK ? a.dinit : a.final;
         const bool f32 = BACK ? !a.dinit_bf16 : !a.final_bf16;
+        if (ENDS && !mat) {
+            float *to = const_cast<float *>(ends) + seg * (128 * 128);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                float4 x;
+                up2(S[e], x.x, x.y);
+                up2(S[e + 1], x.z, x.w);
+                *reinterpret_cast<float4 *>(to + 2 * e) = x;
+            }
+        } else if (ENDS) {
+            uint8_t *to = static_cast<uint8_t *>(a.segM) + ((int64_t)unit * (a.nseg - 1) + seg) * SEG_BYTES + hf * (STATE_BYTES / 2) + v * 128;
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split_pair(S[4 * p + e], hi[e], lo[e]);
+                *reinterpret_cast<uint4 *>(to + ((p ^ (v & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(to + STATE_BYTES + ((p ^ (v & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        }
         if (out && mine)
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -523,7 +585,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         const int v = (w & 3) * 32 + lane;
         const uint32_t at = tmem + ((uint32_t)(w & 3) << 21);
         const f32x2 sc = pk2(a.scale, a.scale);
-        if (BACK) {
+        if (BACK && values) {
             for (int c = 0; c < n; ++c) {                    // scale e^G dO
                 if (!full(c) || (c > 0 && !wait2(B_O0, c - 1))) break;
                 const float *gate = reinterpret_cast<const float *>(stage(c) + ST_OPS + GATES);
@@ -550,7 +612,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 tmem_wait_st();
                 arrive(B_AF);
             }
-        } else if (outputs) {
+        } else if (!BACK && OUT) {
             float *eg = reinterpret_cast<float *>(sm + CH_EG) + (w & 3) * DQ;
             for (int c = 0; c < n; ++c) {                    // o = scale (e^G Q S + att W)
                 if (!full(c)) break;
@@ -559,10 +621,11 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 eg[lane] = gate[lane];                       // (the stage is filled anew once the products are done with it)
                 eg[32 + lane] = gate[32 + lane];
                 arrive(B_EG0 + (c & 1));
-                const bool tile = m.has_out && q.len - c * DQ >= DQ;
+                const int t0 = idx(c) * DQ;
+                const bool tile = m.has_out && q.len - t0 >= DQ;
                 if (!wait2(B_O0, c) || (c > 0 && !wait(B_FO, c - 1))) break;
                 tc_fence_after();
-                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + q.b * a.os[0] + (q.t0 + (int64_t)c * DQ) * a.os[1] + h * a.os[2] + v;
+                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + q.b * a.os[0] + (q.t0 + (int64_t)t0) * a.os[1] + h * a.os[2] + v;
                 unsigned short *to = reinterpret_cast<unsigned short *>(sm + CH_O) + v;
 #pragma unroll 1
                 for (int qu = 0; qu < 4; ++qu) {
@@ -584,7 +647,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                         b2[e] = pack_bf16(p, o2);
                     }
                     if (tile) tile_column(to + 16 * qu * 128, b2);
-                    else if (v < a.V) st_column(o + 16 * qu * a.os[1], a.os[1], b2, q.len - c * DQ - 16 * qu);
+                    else if (v < a.V) st_column(o + 16 * qu * a.os[1], a.os[1], b2, q.len - t0 - 16 * qu);
                 }
                 if (tile) fence_proxy_async_smem();
                 arrive(B_WO0 + (c & 1));                                // (and the columns may be written again)
@@ -595,9 +658,9 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         // ------------------------------------------------------------ loads
         const int t = tid - CH_L0;
         const CUtensorMap *mx = BACK ? &m.dO : &m.v;
-        const bool has_x = BACK ? m.has_dO : m.has_v;
+        const bool has_x = values && (BACK ? m.has_dO : m.has_v);
         auto chunk = [&](int c) {
-            const int ci = BACK ? n - 1 - c : c;
+            const int ci = idx(c);
             return DeltaChunk{q.b, q.t0 + ci * DQ, min(DQ, q.len - ci * DQ)};
         };
         auto issue = [&](int c) {
@@ -608,19 +671,30 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 mbar_expect_tx(bar, OPS_BYTES + (m.has_k + has_x + (m.has_q && outputs)) * TOK_BYTES);
                 if (m.has_k) tma_rows(st + ST_KQ, 2 * HALF, &m.k, bar, k, grp);
                 if (has_x) tma_rows(st + ST_X, HALF, mx, bar, k, h);
-                bulk_load(st + ST_OPS, static_cast<const uint8_t *>(a.tiles) + (((int64_t)q.slot0 + (BACK ? n - 1 - c : c)) * a.H + h) * OPS_BYTES, OPS_BYTES, bar);
+                bulk_load(st + ST_OPS, static_cast<const uint8_t *>(a.tiles) + (((int64_t)q.slot0 + idx(c)) * a.H + h) * OPS_BYTES, OPS_BYTES, bar);
                 if (m.has_q && outputs) tma_rows(st + ST_KQ + HALF, 2 * HALF, &m.q, bar, k, grp);
             }
             if (!m.has_k) load_rows<CH_L>(st + ST_KQ, 2 * HALF, tok_rows(a.k, a.ks, k, grp), a.ks[1], k.len, a.K, t);
-            if (!has_x) {
+            if (!has_x && values) {
                 if (BACK) load_rows<CH_L>(st + ST_X, HALF, tok_rows(a.dO, a.dos, k, h), a.dos[1], k.len, a.V, t);
                 else load_rows<CH_L>(st + ST_X, HALF, tok_rows(a.v, a.vs, k, h), a.vs[1], k.len, a.V, t);
             }
             if (!m.has_q && outputs) load_rows<CH_L>(st + ST_KQ + HALF, 2 * HALF, tok_rows(a.q, a.qs, k, grp), a.qs[1], k.len, a.K, t);
         };
-        if (n > 0) issue(0);
-        if (n > 1) issue(1);
-        for (int c = 0; c < n; ++c) {
+        bool go = true;
+        for (int j = 0; j < joins && go; ++j) {              // the matrices of the segments between, in either stage's memory in turn
+            if (j > 1 && !(go = wait(B_JD, j - 2))) break;
+            if (t == 0) {
+                uint64_t *bar = &ms->bar[B_JM0 + (j & 1)];
+                mbar_expect_tx(bar, SEG_BYTES);
+                bulk_load(stage(j), static_cast<const uint8_t *>(a.segM) + ((int64_t)unit * (a.nseg - 1) + 1 + j) * SEG_BYTES, SEG_BYTES, bar);
+            }
+        }
+        if (joins > 1 && go) go = wait(B_JD, joins - 2);
+        if (joins > 0 && go) go = wait(B_JD, joins - 1);
+        if (go && n > 0) issue(0);
+        if (go && n > 1) issue(1);
+        for (int c = 0; c < n && go; ++c) {
             if (!wait2(B_TMA0, c)) break;
             if (const int len = chunk(c).len; len < DQ) {    // the next sequence's tokens
                 if (m.has_k) zero_rows<CH_L>(stage(c) + ST_KQ, 2 * HALF, len, t);
@@ -640,7 +714,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         if (lane == 0) {
             uint8_t *vals = static_cast<uint8_t *>(BACK ? a.mu : a.U);
             for (int c = 0; c < n; ++c) {
-                const int ci = BACK ? n - 1 - c : c;
+                const int ci = idx(c);
                 if (KEEP) {
                     if (!wait(B_WV, c)) break;
                     bulk_store(vals + (((int64_t)q.slot0 + ci) * a.H + h) * VAL_BYTES, sm + CH_V, VAL_BYTES);
@@ -648,7 +722,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                     bulk_wait_read0();
                     mbar_arrive(&ms->bar[B_FV]);
                 }
-                if (outputs) {
+                if (OUT) {
                     if (!wait2(B_WO0, c)) break;
                     if (m.has_out && q.len - ci * DQ >= DQ) {
                         tma_store_4d(&m.out, sm + CH_O, 0, h, q.t0 + ci * DQ, q.b);
@@ -666,21 +740,35 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         if (lane == 0) {
             const uint32_t s0 = smem_u32(sm);
             constexpr uint32_t id64 = idesc_bf16(128, 64, 0, 0), id128 = idesc_bf16(128, 128, 0, 0), id128t = idesc_bf16(128, 128, 0, 1);
-            for (int c = 0; c < n; ++c) {
+            bool go = true;
+            for (int j = 0; j < joins && go; ++j) {          // S M, both terms of each but the product of the small ones, into U and W (R may be written before it has been read)
+                if (!(go = wait2(B_JM0, j) && wait(B_AS, j) && wait(B_AS + 1, j))) break;
+                tc_fence_after();
+                const uint32_t M = s0 + (j & 1) * ST_BYTES;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t A = tmem + C::S + 16 * k;
+                    umma_bf16_ta(tmem + C::U, A, mnmaj(M, k, STATE_BYTES / 2), id128t, k > 0);
+                    umma_bf16_ta(tmem + C::U, A + 8, mnmaj(M, k, STATE_BYTES / 2), id128t, 1);
+                    umma_bf16_ta(tmem + C::U, A, mnmaj(M + STATE_BYTES, k, STATE_BYTES / 2), id128t, 1);
+                }
+                umma_commit(&ms->bar[B_JD]);
+            }
+            for (int c = 0; c < n && go; ++c) {
                 const uint32_t st = s0 + (c & 1) * ST_BYTES, K = st + ST_KQ, Q = K + HALF, X = st + ST_X, ops = st + ST_OPS;
                 if (!full(c)) break;
-                if (BACK) {                                  // att^T dO: dO by columns, att by columns
+                if (BACK && values) {                        // att^T dO: dO by columns, att by columns
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         umma_bf16(tmem + C::R(c), mnmaj(X, k, HALF), mnmaj(ops + ATT, k, HALF), idesc_bf16(128, 64, 1, 1), k > 0);
                 }
-                bool go = BACK || !outputs || c < 2 || wait2(B_WO0, c - 2);   // o of the chunk before last has been read
+                go = BACK || !OUT || c < 2 || wait2(B_WO0, c - 2);   // o of the chunk before last has been read
                 // K S and Q S in one: their rows are the 128 rows of the right operand.  Each thread's first quarter
                 // while it still writes the second; so with the other products.
 #pragma unroll
                 for (int g = 0; g < 2 && go; ++g) {
-                    if (!(go = wait(B_AS + g, c))) break;
+                    if (!(go = wait(B_AS + g, joins + c))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int d = 0; d < 4; ++d) {
@@ -692,7 +780,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 }
                 if (!go) break;
                 umma_commit(&ms->bar[B_P]);
-                if (!BACK) {                                 // V's part of U: V by columns, both terms of sys
+                if (!BACK && values) {                       // V's part of U: V by columns, both terms of sys
                     if (c > 0 && !wait2(B_O0, c - 1)) break;   // (att W has read its operand there)
                     tc_fence_after();
 #pragma unroll
@@ -704,7 +792,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                     for (int k = 0; k < 4; ++k)
                         umma_bf16_ta(tmem + C::S, tmem + C::X + 16 * k + 8 * term, mnmaj(Q, k, 2 * HALF), id128t, term || k > 0);
                 };
-                if (BACK) {
+                if (BACK && values) {
                     if (!wait(B_AF, c) || !wait(B_P, c)) break;   // P is done with the columns that are written now
                     tc_fence_after();
                     from_o(0);
@@ -716,26 +804,26 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                     tc_fence_after();
 #pragma unroll
                     for (int k = g; k < 4; k += 2) {
-                        umma_bf16_ta(tmem + C::U, tmem + C::P(c) + 16 * k, kmaj(ops + SYS_HI, k, 0), id128, !BACK || k > 0);
+                        umma_bf16_ta(tmem + C::U, tmem + C::P(c) + 16 * k, kmaj(ops + SYS_HI, k, 0), id128, (!BACK && values) || k > 0);
                         umma_bf16_ta(tmem + C::U, tmem + C::P(c) + 16 * k + 8, kmaj(ops + SYS_HI, k, 0), id128, 1);
                     }
                 }
                 if (!go) break;
                 umma_commit(&ms->bar[B_U]);
-                if (BACK) from_o(1);
+                if (BACK && values) from_o(1);
 #pragma unroll
                 for (int g = 0; g < 2 && go; ++g) {
                     if (!(go = wait(B_AW + g, c))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int k = g; k < 4; k += 2) {
-                        umma_bf16_ta(tmem + C::S, tmem + C::U + 16 * k, mnmaj(K, k, 2 * HALF), id128t, BACK || k > 0);
+                        umma_bf16_ta(tmem + C::S, tmem + C::U + 16 * k, mnmaj(K, k, 2 * HALF), id128t, (BACK && values) || k > 0);
                         umma_bf16_ta(tmem + C::S, tmem + C::U + 16 * k + 8, mnmaj(K, k, 2 * HALF), id128t, 1);
                     }
                 }
                 if (!go) break;
                 umma_commit(&ms->bar[B_S]);
-                if (!BACK && outputs)
+                if (!BACK && OUT)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) umma_bf16_ta(tmem + C::P(c), tmem + C::W + 16 * k, kmaj(ops + ATT, k, 0), id64, k > 0);
                 umma_commit(&ms->bar[B_O0 + (c & 1)]);
@@ -1052,12 +1140,18 @@ cudaError_t prep(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
     k_prep<BACK><<<(unsigned)((int64_t)a.nslots * a.H), PREP_NT, P_BYTES, st>>>(a, m);
     return cudaGetLastError();
 }
+template <bool BACK, bool KEEP, bool OUT, bool ENDS>
+cudaError_t launch_chain(const DeltaArgs &a, const DeltaMaps &m, int parts, cudaStream_t st) {
+    static int set[64] = {};
+    if (cudaError_t e = ensure_smem_attr(k_chain<BACK, KEEP, OUT, ENDS>, (int)CH_BYTES, set); e != cudaSuccess) return e;
+    k_chain<BACK, KEEP, OUT, ENDS><<<(unsigned)(a.nseqs * (int64_t)a.H * parts), CH_NT, CH_BYTES, st>>>(a, m);
+    return cudaGetLastError();
+}
 template <bool BACK, bool KEEP, bool OUT>
 cudaError_t chain(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
-    static int set[64] = {};
-    if (cudaError_t e = ensure_smem_attr(k_chain<BACK, KEEP, OUT>, (int)CH_BYTES, set); e != cudaSuccess) return e;
-    k_chain<BACK, KEEP, OUT><<<(unsigned)(a.nseqs * (int64_t)a.H), CH_NT, CH_BYTES, st>>>(a, m);
-    return cudaGetLastError();
+    if (a.nseg > 1)
+        if (cudaError_t e = launch_chain<BACK, false, false, true>(a, m, 2 * a.nseg - 3, st); e != cudaSuccess) return e;
+    return launch_chain<BACK, KEEP, OUT, false>(a, m, a.nseg, st);
 }
 
 }  // namespace

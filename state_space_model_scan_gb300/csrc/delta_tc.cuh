@@ -21,6 +21,28 @@ constexpr uint32_t SYS_HI = 0, SYS_LO = MAT_BYTES, ATT = 2 * MAT_BYTES, GATES = 
 constexpr uint32_t STATE_BYTES = 128 * 128 * 2;  // kept state: two images (keys 0..63, 64..127) of 128 rows (values)
 constexpr uint32_t VAL_BYTES = DQ * 128 * 2;     // kept U, and mu: [64][128], plain
 
+constexpr uint32_t SEG_BYTES = 128 * 128 * 4;    // of a segment: its end in fp32; its matrix as two states' images
+
+// Segments of the chains of nseqs x H sequences and heads, at most `chunks` long.  Cut into m, a chain's first launch takes 2 m - 3
+// blocks (every end but the last, every matrix but the first and last), the second m, each of chunks / m steps on kSMs SMs;
+// and joining the ends before a segment takes 0.8 of a step each.
+inline void delta_segments(int64_t nseqs, int64_t H, int64_t chunks, int *nseg, int *seglen) {
+    const int64_t sms = 152, U = nseqs * H;
+    *nseg = 1;
+    *seglen = (int)(chunks > 0 ? chunks : 1);
+    double best = (double)chunks * ((U + sms - 1) / sms);
+    if (3 * U > sms) return;
+    for (int64_t m = 3; m <= 32 && chunks / m >= 4; ++m) {
+        const int64_t len = (chunks + m - 1) / m;
+        const double t = (double)len * ((U * (2 * m - 3) + sms - 1) / sms + (U * m + sms - 1) / sms) + 0.8 * (m - 2) + 4;
+        if (t < best) {
+            best = t;
+            *seglen = (int)len;
+            *nseg = (int)((chunks + len - 1) / len);
+        }
+    }
+}
+
 // K-major operand at K step k (16 elements), images of `half` bytes; MN-major operand at K step k (16 rows)
 __device__ __forceinline__ uint64_t kmaj(uint32_t base, int k, uint32_t half) {
     return sdesc(base + (uint32_t)(k >> 2) * half + (uint32_t)(k & 3) * 32u, 16u, 1024u);

@@ -7,7 +7,7 @@
 // A few operations a value, each value read once (backwards x and dy) and written once: bound by memory.  A head's vector
 // belongs to 32 lanes or a power of two fewer, V neighbouring features each, so that a load is 16 bytes
 // and the partner of a rotated feature lies in another lane's registers (a shuffle) or, interleaved, in
-// the lane's own.  A group of lanes takes HB heads of one token: their loads are all on the way
+// the lane's own.  A group of lanes takes several heads of one token: their loads are all on the way
 // before the first is used, and the token's cosines and sines are loaded once for them.  What the shapes or addresses keep
 // from that goes feature by feature through shared memory.  The weights' gradients are summed in registers over a
 // block's tokens, then over its groups, then by a second launch over the blocks, each in a fixed order.
@@ -17,16 +17,16 @@ namespace ssd {
 
 namespace {
 
-constexpr int QK_NT = 256, QK_HB = 4, QK_MAXD = 512;
-constexpr int QK_BLOCKS = 4 * kSMs;     // of the backward, for queries and for keys: each leaves its share of the weights' gradients
+constexpr int QK_NT = 256, QK_HB_MIN = 2, QK_MAXD = 512;
+constexpr int QK_BLOCKS = 3 * kSMs;     // of the backward: each leaves its share of the weights' gradients
 
 struct QkSide {                         // queries, or keys
     const void *x, *dy;
     void *y;                            // the output, or dx
     int64_t xs[3], dys[3], ys[3];       // element strides: batch row, token, head
     const float *w;
-    int heads, per;                     // heads, blocks of QK_HB heads in a token
-    int64_t items;                      // tokens x per
+    int heads, per;                     // heads, items of a token
+    uint32_t items;                     // tokens x per
     float *share;                       // [blocks of this side][dim], or NULL
     float *dw;
 };
@@ -36,7 +36,6 @@ struct QkArgs {
     const float *cos, *sin;
     const int32_t *pos;
     int64_t pos_stride;
-    int64_t tokens;
     int seqlen, dim, half, rows;        // half: rotary / 2; rows: of the table
     int lpr;
     float eps, inv;                     // inv: 1 / dim, or 1
@@ -48,12 +47,12 @@ struct QkAt {
     int64_t b;
     int t, h0, pos;
 };
-__device__ __forceinline__ QkAt qk_at(const QkArgs &a, const QkSide &s, int64_t item) {
+__device__ __forceinline__ QkAt qk_at(const QkArgs &a, const QkSide &s, uint32_t item, int hb) {
     QkAt q;
-    const int64_t tok = item / s.per;
-    q.h0 = (int)(item - tok * s.per) * QK_HB;
-    q.b = tok / a.seqlen;
-    q.t = (int)(tok - q.b * a.seqlen);
+    const uint32_t tok = item / (uint32_t)s.per, b = tok / (uint32_t)a.seqlen;
+    q.h0 = (int)(item - tok * s.per) * hb;
+    q.b = b;
+    q.t = (int)(tok - b * a.seqlen);
     q.pos = 0;
     if (a.half > 0) {
         q.pos = a.pos ? a.pos[q.b * a.pos_stride + q.t] : q.t;
@@ -62,53 +61,47 @@ __device__ __forceinline__ QkAt qk_at(const QkArgs &a, const QkSide &s, int64_t 
     return q;
 }
 
-// V features at a place divisible by V
+// V features at a place divisible by V, as they lie in memory (two bf16 to a register)
 template <typename T, int V>
-struct QkVec {
-    float f[V];
+struct QkRaw {
+    uint32_t w[V * sizeof(T) / 4];
     __device__ __forceinline__ void load(const T *p) {
-        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-            for (int c = 0; c < V / 8; ++c) {
-                const uint4 u = reinterpret_cast<const uint4 *>(p)[c];
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f[8 * c + 2 * e] = __uint_as_float(w[e] << 16);
-                    f[8 * c + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < V / 4; ++c) {
-                const float4 u = reinterpret_cast<const float4 *>(p)[c];
-                f[4 * c] = u.x; f[4 * c + 1] = u.y; f[4 * c + 2] = u.z; f[4 * c + 3] = u.w;
-            }
-        }
-    }
-    __device__ __forceinline__ void store(T *p) const {
-        if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int c = 0; c < V / 8; ++c) {
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(f[8 * c + 2 * e], f[8 * c + 2 * e + 1]);
-                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
-                }
-                reinterpret_cast<uint4 *>(p)[c] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < V / 4; ++c)
-                reinterpret_cast<float4 *>(p)[c] = make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
+        for (int c = 0; c < (int)(V * sizeof(T) / 16); ++c) {
+            const uint4 u = reinterpret_cast<const uint4 *>(p)[c];
+            w[4 * c] = u.x; w[4 * c + 1] = u.y; w[4 * c + 2] = u.z; w[4 * c + 3] = u.w;
         }
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int e = 0; e < V; ++e) f[e] = 0.f;
+        for (int e = 0; e < (int)(V * sizeof(T) / 4); ++e) w[e] = 0u;
+    }
+    __device__ __forceinline__ void to(float (&f)[V]) const {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if constexpr (sizeof(T) == 4) f[e] = __uint_as_float(w[e]);
+            else f[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+        }
     }
 };
+template <typename T, int V>
+__device__ __forceinline__ void qk_store(T *p, const float (&f)[V]) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int c = 0; c < V / 8; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[8 * c + 2 * e], f[8 * c + 2 * e + 1]);
+                w[e] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            reinterpret_cast<uint4 *>(p)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < V / 4; ++c) reinterpret_cast<float4 *>(p)[c] = make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
+    }
+}
 
 // The token's cosines and sines for a lane's features, the sines with the sign that the feature's partner gets.
 template <int V, bool INTER>
@@ -147,21 +140,21 @@ struct QkTurn {
         }
     }
     // BACK: by the opposite angle
-    template <bool BACK, typename T>
-    __device__ __forceinline__ void turn(QkVec<T, V> &x, int half) const {
+    template <bool BACK>
+    __device__ __forceinline__ void turn(float (&x)[V], int half) const {
         if (half == 0) return;
         if constexpr (INTER) {
 #pragma unroll
             for (int e = 0; e < V / 2; ++e) {
-                const float p = x.f[2 * e], q = x.f[2 * e + 1], sn = BACK ? -s[e] : s[e];
-                x.f[2 * e] = p * c[e] - q * sn;
-                x.f[2 * e + 1] = p * sn + q * c[e];
+                const float p = x[2 * e], q = x[2 * e + 1], sn = BACK ? -s[e] : s[e];
+                x[2 * e] = p * c[e] - q * sn;
+                x[2 * e + 1] = p * sn + q * c[e];
             }
         } else {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float p = __shfl_sync(0xffffffffu, x.f[e], from);
-                x.f[e] = x.f[e] * c[e] + p * (BACK ? -s[e] : s[e]);
+                const float p = __shfl_sync(0xffffffffu, x[e], from);
+                x[e] = x[e] * c[e] + p * (BACK ? -s[e] : s[e]);
             }
         }
     }
@@ -172,105 +165,111 @@ __device__ __forceinline__ float qk_group(float v, int lpr) {
     return v;
 }
 
-template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(QK_NT) k_qk_fwd(const QkArgs a) {
+template <int V>
+__device__ __forceinline__ void qk_weight(float (&w)[V], const float *p, bool in) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] = 1.f;
+    if (p && in)
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(p + e);
+            w[e] = u.x; w[e + 1] = u.y; w[e + 2] = u.z; w[e + 3] = u.w;
+        }
+}
+
+template <typename T, int V, bool INTER, int HB>
+__global__ void __launch_bounds__(QK_NT, V <= 8 ? 4 : 2) k_qk_fwd(const QkArgs a) {
     after_previous();
     const bool keys = blockIdx.x >= a.blocks0;
     const QkSide &s = a.side[keys];
     const int lane = threadIdx.x & 31, l = lane & (a.lpr - 1), gpb = QK_NT / a.lpr;
-    const int64_t item0 = (int64_t)(blockIdx.x - (keys ? a.blocks0 : 0)) * gpb + threadIdx.x / a.lpr;
-    const bool live = item0 < s.items;                       // (idle groups stay for the shuffles)
-    const QkAt q = qk_at(a, s, live ? item0 : s.items - 1);
+    const uint32_t item = (uint32_t)(blockIdx.x - (keys ? a.blocks0 : 0)) * gpb + threadIdx.x / a.lpr;
+    const bool live = item < s.items;                        // (idle groups stay for the shuffles)
+    const QkAt q = qk_at(a, s, live ? item : s.items - 1, HB);
     const bool in = l * V < a.dim;
-    const T *x = static_cast<const T *>(s.x) + q.b * s.xs[0] + q.t * s.xs[1] + l * V;
-    T *y = static_cast<T *>(s.y) + q.b * s.ys[0] + q.t * s.ys[1] + l * V;
-    QkVec<T, V> v[QK_HB];
+    const T *x = static_cast<const T *>(s.x) + q.b * s.xs[0] + q.t * s.xs[1] + q.h0 * s.xs[2] + l * V;
+    T *y = static_cast<T *>(s.y) + q.b * s.ys[0] + q.t * s.ys[1] + q.h0 * s.ys[2] + l * V;
+    QkRaw<T, V> v[HB];
     QkTurn<V, INTER> r;
 #pragma unroll
-    for (int u = 0; u < QK_HB; ++u) {
-        if (in && q.h0 + u < s.heads) v[u].load(x + (q.h0 + u) * s.xs[2]);
+    for (int u = 0; u < HB; ++u) {
+        if (in && q.h0 + u < s.heads) v[u].load(x + u * s.xs[2]);
         else v[u].zero();
     }
     if (a.half > 0) r.load(a, q.pos, l, lane);
-    QkVec<float, V> w;
-    if (s.w && in) {
-        w.load(s.w + l * V);
-    } else {
+    float w[V];
+    qk_weight<V>(w, s.w ? s.w + l * V : nullptr, in);
 #pragma unroll
-        for (int e = 0; e < V; ++e) w.f[e] = 1.f;
-    }
+    for (int u = 0; u < HB; ++u) {
+        float f[V], m = 0.f;
+        v[u].to(f);
 #pragma unroll
-    for (int u = 0; u < QK_HB; ++u) {
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) m = fmaf(v[u].f[e], v[u].f[e], m);
+        for (int e = 0; e < V; ++e) m = fmaf(f[e], f[e], m);
         m = qk_group(m, a.lpr);
         const float rstd = rsqrtf(fmaf(m, a.inv, a.eps));
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[u].f[e] = v[u].f[e] * rstd * w.f[e];
-        r.template turn<false>(v[u], a.half);
-        if (q.pos < 0) v[u].zero();
-        if (live && in && q.h0 + u < s.heads) v[u].store(y + (q.h0 + u) * s.ys[2]);
+        for (int e = 0; e < V; ++e) f[e] = f[e] * rstd * w[e];
+        r.template turn<false>(f, a.half);
+        if (q.pos < 0)
+#pragma unroll
+            for (int e = 0; e < V; ++e) f[e] = 0.f;
+        if (live && in && q.h0 + u < s.heads) qk_store<T, V>(y + u * s.ys[2], f);
     }
 }
 
-template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(QK_NT) k_qk_bwd(const QkArgs a) {
+template <typename T, int V, bool INTER, int HB>
+__global__ void __launch_bounds__(QK_NT, V <= 8 ? 3 : 2) k_qk_bwd(const QkArgs a) {
     __shared__ float sum[QK_NT * V];
     const bool keys = blockIdx.x >= a.blocks0;
     const QkSide &s = a.side[keys];
     const int lane = threadIdx.x & 31, l = lane & (a.lpr - 1), gpb = QK_NT / a.lpr, grp = threadIdx.x / a.lpr;
     const int nb = keys ? a.blocks1 : a.blocks0, bi = blockIdx.x - (keys ? a.blocks0 : 0);
     const bool in = l * V < a.dim;
-    QkVec<float, V> w;
-    if (s.w && in) {
-        w.load(s.w + l * V);
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) w.f[e] = 1.f;
-    }
-    float acc[V];
+    float w[V], acc[V];
+    qk_weight<V>(w, s.w ? s.w + l * V : nullptr, in);
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    for (int64_t first = (int64_t)bi * gpb; first < s.items; first += (int64_t)nb * gpb) {
+    for (uint32_t first = (uint32_t)bi * gpb; first < s.items; first += (uint32_t)nb * gpb) {
         const bool live = first + grp < s.items;
-        const QkAt q = qk_at(a, s, live ? first + grp : s.items - 1);
-        const T *x = static_cast<const T *>(s.x) + q.b * s.xs[0] + q.t * s.xs[1] + l * V;
-        const T *dy = static_cast<const T *>(s.dy) + q.b * s.dys[0] + q.t * s.dys[1] + l * V;
-        T *dx = static_cast<T *>(s.y) + q.b * s.ys[0] + q.t * s.ys[1] + l * V;
-        QkVec<T, V> xv[QK_HB], dv[QK_HB];
+        const QkAt q = qk_at(a, s, live ? first + grp : s.items - 1, HB);
+        const T *x = static_cast<const T *>(s.x) + q.b * s.xs[0] + q.t * s.xs[1] + q.h0 * s.xs[2] + l * V;
+        const T *dy = static_cast<const T *>(s.dy) + q.b * s.dys[0] + q.t * s.dys[1] + q.h0 * s.dys[2] + l * V;
+        T *dx = static_cast<T *>(s.y) + q.b * s.ys[0] + q.t * s.ys[1] + q.h0 * s.ys[2] + l * V;
+        QkRaw<T, V> xr[HB], dr[HB];
         QkTurn<V, INTER> r;
 #pragma unroll
-        for (int u = 0; u < QK_HB; ++u) {
+        for (int u = 0; u < HB; ++u) {
             if (live && in && q.pos >= 0 && q.h0 + u < s.heads) {
-                xv[u].load(x + (q.h0 + u) * s.xs[2]);
-                dv[u].load(dy + (q.h0 + u) * s.dys[2]);
+                xr[u].load(x + u * s.xs[2]);
+                dr[u].load(dy + u * s.dys[2]);
             } else {
-                xv[u].zero();
-                dv[u].zero();
+                xr[u].zero();
+                dr[u].zero();
             }
         }
         if (a.half > 0) r.load(a, q.pos, l, lane);
 #pragma unroll
-        for (int u = 0; u < QK_HB; ++u) {
-            float m = 0.f, d = 0.f;
+        for (int u = 0; u < HB; ++u) {
+            float xv[V], dv[V], m = 0.f, d = 0.f;
+            xr[u].to(xv);
+            dr[u].to(dv);
 #pragma unroll
-            for (int e = 0; e < V; ++e) m = fmaf(xv[u].f[e], xv[u].f[e], m);
+            for (int e = 0; e < V; ++e) m = fmaf(xv[e], xv[e], m);
             m = qk_group(m, a.lpr);
             // (a vector that is not there: rstd could be infinite with eps 0)
             const float rstd = live && q.pos >= 0 && q.h0 + u < s.heads ? rsqrtf(fmaf(m, a.inv, a.eps)) : 0.f;
-            r.template turn<true>(dv[u], a.half);
+            r.template turn<true>(dv, a.half);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                xv[u].f[e] *= rstd;
-                acc[e] = fmaf(dv[u].f[e], xv[u].f[e], acc[e]);
-                dv[u].f[e] *= w.f[e];
-                d = fmaf(dv[u].f[e], xv[u].f[e], d);
+                xv[e] *= rstd;
+                acc[e] = fmaf(dv[e], xv[e], acc[e]);
+                dv[e] *= w[e];
+                d = fmaf(dv[e], xv[e], d);
             }
             d = qk_group(d, a.lpr) * a.inv;
 #pragma unroll
-            for (int e = 0; e < V; ++e) dv[u].f[e] = rstd * fmaf(-d, xv[u].f[e], dv[u].f[e]);
-            if (live && in && q.h0 + u < s.heads) dv[u].store(dx + (q.h0 + u) * s.ys[2]);
+            for (int e = 0; e < V; ++e) dv[e] = rstd * fmaf(-d, xv[e], dv[e]);
+            if (live && in && q.h0 + u < s.heads) qk_store<T, V>(dx + u * s.ys[2], dv);
         }
     }
     if (!s.share) return;
@@ -295,9 +294,9 @@ __global__ void __launch_bounds__(QK_NT) k_qk_any(const QkArgs a) {
     float *row = rows[wp];
     if (BACK)
         for (int e = lane; e < D; e += 32) grads[wp][e] = 0.f;
-    for (int64_t item = (int64_t)bi * (QK_NT / 32) + wp; item < s.items; item += (int64_t)nb * (QK_NT / 32)) {
-        const QkAt q = qk_at(a, s, item);
-        for (int u = 0; u < QK_HB && q.h0 + u < s.heads; ++u) {
+    for (uint32_t item = (uint32_t)bi * (QK_NT / 32) + wp; item < s.items; item += (uint32_t)nb * (QK_NT / 32)) {
+        const QkAt q = qk_at(a, s, item, QK_HB_MIN);
+        for (int u = 0; u < QK_HB_MIN && q.h0 + u < s.heads; ++u) {
             const T *x = static_cast<const T *>(s.x) + q.b * s.xs[0] + q.t * s.xs[1] + (q.h0 + u) * s.xs[2];
             T *y = static_cast<T *>(s.y) + q.b * s.ys[0] + q.t * s.ys[1] + (q.h0 + u) * s.ys[2];
             if (q.pos < 0) {
@@ -355,23 +354,21 @@ __global__ void __launch_bounds__(QK_NT) k_qk_any(const QkArgs a) {
     }
 }
 
-// sum of the blocks' shares: 32 features a block, eight threads a feature
-__global__ void __launch_bounds__(256) k_qk_dw(const QkArgs a) {
-    __shared__ float part[8][32];
+// sum of the blocks' shares: 32 features a block, 32 threads a feature
+__global__ void __launch_bounds__(1024) k_qk_dw(const QkArgs a) {
+    __shared__ float part[32][33];
     const int per = (a.dim + 31) / 32, side = blockIdx.x / per, e = blockIdx.x % per * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
     const QkSide &s = a.side[side];
     if (!s.share) return;
     const int n = side ? a.blocks1 : a.blocks0;
     float t = 0.f;
     if (e < a.dim)
-        for (int b = g; b < n; b += 8) t += s.share[(int64_t)b * a.dim + e];
+#pragma unroll 4
+        for (int b = g; b < n; b += 32) t += s.share[(int64_t)b * a.dim + e];
     part[g][threadIdx.x & 31] = t;
     __syncthreads();
-    if (g == 0 && e < a.dim) {
-        float r = 0.f;
-        for (int i = 0; i < 8; ++i) r += part[i][threadIdx.x];
-        s.dw[e] = r;
-    }
+    const float v = warp_sum(part[threadIdx.x & 31][g]);     // warp g: feature g
+    if ((threadIdx.x & 31) == 0 && blockIdx.x % per * 32 + g < a.dim) s.dw[blockIdx.x % per * 32 + g] = v;
 }
 
 bool al(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
@@ -399,7 +396,7 @@ ssd_status check(const ssd_qk_problem *p, const ssd_qk_args *f) {
         return SSD_ERR_INVALID_ARGUMENT;
     const int64_t tokens = p->batch * p->seqlen;
     if (p->dim > QK_MAXD || p->batch > ((int64_t)1 << 30) || p->seqlen > ((int64_t)1 << 30) || p->q_heads > ((int64_t)1 << 16) || p->k_heads > ((int64_t)1 << 16) ||
-        tokens > ((int64_t)1 << 30) || p->table_rows > ((int64_t)1 << 30) || tokens * ((p->q_heads + 3) / 4 + (p->k_heads + 3) / 4) > ((int64_t)1 << 32))
+        tokens > ((int64_t)1 << 30) || p->table_rows > ((int64_t)1 << 30) || tokens * ((p->q_heads + 1) / QK_HB_MIN + (p->k_heads + 1) / QK_HB_MIN) > ((int64_t)1 << 30))
         return SSD_ERR_UNSUPPORTED;
     if (f == nullptr) return SSD_OK;
     if (tokens == 0) return SSD_OK;
@@ -416,11 +413,11 @@ void set3(int64_t *to, const ssd_tensor &t) {
 }
 
 // V: features of a lane in the kernels by pieces, 0 where the shapes or addresses do not allow them
-QkArgs make(const ssd_qk_problem *p, const ssd_qk_args *f, const ssd_tensor &yq, const ssd_tensor &yk, const ssd_tensor *dyq, const ssd_tensor *dyk, int *V) {
+QkArgs make(const ssd_qk_problem *p, const ssd_qk_args *f, const ssd_tensor &yq, const ssd_tensor &yk, const ssd_tensor *dyq, const ssd_tensor *dyk, int *V, int *HB) {
     QkArgs a{};
     const ssd_tensor *x[2] = {&f->q, &f->k}, *y[2] = {&yq, &yk}, *dy[2] = {dyq, dyk};
     const int64_t heads[2] = {p->q_heads, p->k_heads};
-    a.tokens = p->batch * p->seqlen;
+    const int64_t tokens = p->batch * p->seqlen;
     const int least = p->dtype == SSD_BF16 ? 8 : 4;
     *V = p->dim <= 32 * least ? least : 2 * least;
     if (p->dim > 32 * *V) *V = 16;
@@ -429,8 +426,6 @@ QkArgs make(const ssd_qk_problem *p, const ssd_qk_args *f, const ssd_tensor &yq,
         QkSide &s = a.side[i];
         s.x = x[i]->ptr; s.y = y[i]->ptr; set3(s.xs, *x[i]); set3(s.ys, *y[i]);
         s.heads = (int)heads[i];
-        s.per = (int)((heads[i] + QK_HB - 1) / QK_HB);
-        s.items = a.tokens * s.per;
         s.w = i ? f->k_weight : f->q_weight;
         if (heads[i] == 0) continue;
         vec = vec && al(s.w, 16) && pieces(s.x, s.xs, p, s.heads) && pieces(s.y, s.ys, p, s.heads);
@@ -441,6 +436,16 @@ QkArgs make(const ssd_qk_problem *p, const ssd_qk_args *f, const ssd_tensor &yq,
         }
     }
     if (!vec) *V = 0;
+    // Heads of an item: 128 bytes of them on the way to a lane (64 backwards, of x and of dy) where that still fills the card, two where
+    // few tokens come.
+    const bool back = dyq != nullptr;
+    const int64_t lanes = tokens * (p->q_heads + p->k_heads) * p->dim / (*V ? *V : 16);
+    const int many = (back ? 64 : 128) / ((*V ? *V : 16) * (p->dtype == SSD_BF16 ? 2 : 4));
+    *HB = *V && many > QK_HB_MIN && lanes / many >= 2 * kSMs * QK_NT ? many : QK_HB_MIN;
+    for (int i = 0; i < 2; ++i) {
+        a.side[i].per = (int)((heads[i] + *HB - 1) / *HB);
+        a.side[i].items = (uint32_t)(tokens * a.side[i].per);
+    }
     a.cos = f->cos; a.sin = f->sin; a.pos = f->positions; a.pos_stride = p->pos_stride;
     a.seqlen = (int)p->seqlen; a.dim = (int)p->dim; a.half = (int)(p->rotary / 2); a.rows = (int)p->table_rows;
     a.eps = p->eps;
@@ -451,23 +456,34 @@ QkArgs make(const ssd_qk_problem *p, const ssd_qk_args *f, const ssd_tensor &yq,
     if (*V == 0) a.lpr = 32;
     return a;
 }
-int blocks_for(const QkArgs &a, int side, int most) {
+int blocks_for(const QkArgs &a, int side, int64_t most) {
     const int64_t gpb = QK_NT / a.lpr, n = (a.side[side].items + gpb - 1) / gpb;
-    return (int)(most > 0 && n > most ? most : n);
+    if (most == 0) return (int)n;
+    const uint64_t all = (uint64_t)a.side[0].items + a.side[1].items;   // blocks in proportion to the items
+    const int64_t share = std::max<int64_t>(1, (int64_t)((uint64_t)most * a.side[side].items / all));
+    return (int)(a.side[side].items == 0 ? 0 : std::min(n, share));
 }
 
-template <typename T, int V>
+template <typename T, int V, bool INTER, int HB>
 cudaError_t launch(const QkArgs &a, bool back, cudaStream_t st) {
     const unsigned grid = (unsigned)(a.blocks0 + a.blocks1);
-    if (back) {
-        if (a.interleaved) k_qk_bwd<T, V, true><<<grid, QK_NT, 0, st>>>(a);
-        else k_qk_bwd<T, V, false><<<grid, QK_NT, 0, st>>>(a);
-        return cudaGetLastError();
+    if (!back) return launch_early(k_qk_fwd<T, V, INTER, HB>, grid, QK_NT, 0, st, a);
+    k_qk_bwd<T, V, INTER, HB><<<grid, QK_NT, 0, st>>>(a);
+    return cudaGetLastError();
+}
+template <typename T, int V>
+cudaError_t pick_hb(const QkArgs &a, int HB, bool back, cudaStream_t st) {
+    constexpr int fwd = 128 / (V * sizeof(T)), bwd = 64 / (V * sizeof(T));
+    if constexpr (fwd > QK_HB_MIN) {
+        if (!back && HB == fwd) return a.interleaved ? launch<T, V, true, fwd>(a, back, st) : launch<T, V, false, fwd>(a, back, st);
     }
-    return a.interleaved ? launch_early(k_qk_fwd<T, V, true>, grid, QK_NT, 0, st, a) : launch_early(k_qk_fwd<T, V, false>, grid, QK_NT, 0, st, a);
+    if constexpr (bwd > QK_HB_MIN) {
+        if (back && HB == bwd) return a.interleaved ? launch<T, V, true, bwd>(a, back, st) : launch<T, V, false, bwd>(a, back, st);
+    }
+    return a.interleaved ? launch<T, V, true, QK_HB_MIN>(a, back, st) : launch<T, V, false, QK_HB_MIN>(a, back, st);
 }
 template <typename T>
-cudaError_t pick(const QkArgs &a, int V, bool back, cudaStream_t st) {
+cudaError_t pick(const QkArgs &a, int V, int HB, bool back, cudaStream_t st) {
     constexpr int least = 16 / sizeof(T);
     if (V == 0) {
         const unsigned grid = (unsigned)(a.blocks0 + a.blocks1);
@@ -475,11 +491,11 @@ cudaError_t pick(const QkArgs &a, int V, bool back, cudaStream_t st) {
         else k_qk_any<T, false><<<grid, QK_NT, 0, st>>>(a);
         return cudaGetLastError();
     }
-    if (V == least) return launch<T, least>(a, back, st);
+    if (V == least) return pick_hb<T, least>(a, HB, back, st);
     if constexpr (least == 4) {
-        if (V == 8) return launch<T, 8>(a, back, st);
+        if (V == 8) return pick_hb<T, 8>(a, HB, back, st);
     }
-    return launch<T, 16>(a, back, st);
+    return pick_hb<T, 16>(a, HB, back, st);
 }
 
 }  // namespace
@@ -495,11 +511,11 @@ ssd_status ssd_qk_norm_fwd(const ssd_qk_problem *p, const ssd_qk_args *f, void *
     if (p->batch * p->seqlen == 0) return SSD_OK;
     if (ssd_status s = check_tensor(p, f->q_out, p->q_heads, true); s != SSD_OK) return s;
     if (ssd_status s = check_tensor(p, f->k_out, p->k_heads, true); s != SSD_OK) return s;
-    int V;
-    QkArgs a = make(p, f, f->q_out, f->k_out, nullptr, nullptr, &V);
+    int V, HB;
+    QkArgs a = make(p, f, f->q_out, f->k_out, nullptr, nullptr, &V, &HB);
     a.blocks0 = blocks_for(a, 0, V ? 0 : 16 * kSMs);
     a.blocks1 = blocks_for(a, 1, V ? 0 : 16 * kSMs);
-    const cudaError_t e = p->dtype == SSD_BF16 ? pick<__nv_bfloat16>(a, V, false, (cudaStream_t)stream) : pick<float>(a, V, false, (cudaStream_t)stream);
+    const cudaError_t e = p->dtype == SSD_BF16 ? pick<__nv_bfloat16>(a, V, HB, false, (cudaStream_t)stream) : pick<float>(a, V, HB, false, (cudaStream_t)stream);
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
@@ -531,17 +547,17 @@ ssd_status ssd_qk_norm_bwd(const ssd_qk_problem *p, const ssd_qk_bwd_args *b, vo
         if (workspace == nullptr || workspace_bytes < (size_t)2 * QK_BLOCKS * (size_t)p->dim * sizeof(float)) return SSD_ERR_WORKSPACE_TOO_SMALL;
         if (!al(workspace, 256)) return SSD_ERR_MISALIGNED;
     }
-    int V;
-    QkArgs a = make(p, f, b->dq, b->dk, &b->dq_out, &b->dk_out, &V);
+    int V, HB;
+    QkArgs a = make(p, f, b->dq, b->dk, &b->dq_out, &b->dk_out, &V, &HB);
     a.blocks0 = blocks_for(a, 0, QK_BLOCKS);
     a.blocks1 = blocks_for(a, 1, QK_BLOCKS);
     for (int i = 0; i < 2; ++i) {
         a.side[i].dw = dw[i];
         a.side[i].share = dw[i] ? static_cast<float *>(workspace) + (size_t)i * QK_BLOCKS * p->dim : nullptr;
     }
-    cudaError_t e = p->dtype == SSD_BF16 ? pick<__nv_bfloat16>(a, V, true, st) : pick<float>(a, V, true, st);
+    cudaError_t e = p->dtype == SSD_BF16 ? pick<__nv_bfloat16>(a, V, HB, true, st) : pick<float>(a, V, HB, true, st);
     if (e == cudaSuccess && (dw[0] || dw[1])) {
-        k_qk_dw<<<2 * ((a.dim + 31) / 32), 256, 0, st>>>(a);
+        k_qk_dw<<<2 * ((a.dim + 31) / 32), 1024, 0, st>>>(a);
         e = cudaGetLastError();
     }
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;

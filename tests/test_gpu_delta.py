@@ -126,6 +126,27 @@ def test_long_sequences_and_memory_of_the_past():
         assert rel(o[:, :, h], w["o"][:, :, h]) <= OUT[BF16] and rel(f[:, h], w["final"][:, h]) <= OUT[F32]
 
 
+@pytest.mark.parametrize("B,L,G,H,lens,init", [(1, 1500, 1, 1, None, F32), (1, 1301, 1, 2, [700, 3, 0, 598], BF16), (3, 700, 1, 1, None, None),
+                                               (1, 900, 1, 2, [1, 899], None), (1, 640, 2, 2, None, F32)])
+def test_chains_in_segments(B, L, G, H, lens, init):
+    """Few heads and many chunks: the chains are cut, their segments joined; every output as of a whole one."""
+    x = make(B, L, G, H, 128, 128, BF16, F32, lens and len(lens), init, train=True, seed=4)
+    x["g"] *= 0.02                                                     # the past matters across segments
+    cu = None if lens is None else packed(lens)
+    a = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    o, f, kept = pkg.gated_delta_forward(*a, initial_states=x["init"], cu_seqlens=cu, state_dtype=F32, keep_chunk_states=True)
+    d = pkg.gated_delta_backward(*a, x["do"], initial_states=x["init"], dfinal_states=x["dfinal"], cu_seqlens=cu, chunk_states=kept)
+    w = want(x, 128 ** -0.5, None if cu is None else cu.tolist(), back=True)
+    assert rel(o, w["o"]) <= OUT[BF16] and rel(f, w["final"]) <= OUT[F32]
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert rel(d[n], w[n]) <= GRAD[BF16], n
+    if init is not None:
+        assert rel(d["dinitial_states"], w["dinit"]) <= GRAD[BF16]
+    assert torch.equal(pkg.gated_delta_forward(*a, initial_states=x["init"], cu_seqlens=cu)[0], o)
+    d2 = pkg.gated_delta_backward(*a, x["do"], initial_states=x["init"], dfinal_states=x["dfinal"], cu_seqlens=cu)
+    assert all(torch.equal(d[n], d2[n]) for n in d)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_gates_at_their_ends(dtype):
     """Decays of 1 and of 0 (g = -inf, fp32's lowest value, -300 next to small ones), beta of 0, 1 and 2."""
