@@ -150,14 +150,16 @@ ssd_status check_workspace(const void *ws, size_t bytes, size_t need) {
     if (ws == nullptr || bytes < need) return SSD_ERR_WORKSPACE_TOO_SMALL;
     return al(ws, 256) ? SSD_OK : SSD_ERR_MISALIGNED;
 }
-DeltaMaps maps(const ssd_delta_problem *p, const ssd_delta_args *f, const DeltaArgs &a, const ssd_tensor *dO, const ssd_tensor &out) {
+DeltaMaps maps(const ssd_delta_problem *p, const ssd_delta_args *f, const DeltaArgs &a, const ssd_delta_bwd_args *b, const ssd_tensor &out) {
     DeltaMaps m{};
     m.has_q = delta_map(&m.q, f->q.ptr, p->dstate, p->ngroups, p->seqlen, p->batch, f->q.stride);
     m.has_k = delta_map(&m.k, f->k.ptr, p->dstate, p->ngroups, p->seqlen, p->batch, f->k.stride);
     m.has_v = delta_map(&m.v, f->v.ptr, p->headdim, p->nheads, p->seqlen, p->batch, f->v.stride);
     m.has_out = out.ptr != nullptr && delta_map(&m.out, out.ptr, p->headdim, p->nheads, p->seqlen, p->batch, out.stride, true);
-    if (dO != nullptr) {
-        m.has_dO = delta_map(&m.dO, dO->ptr, p->headdim, p->nheads, p->seqlen, p->batch, dO->stride);
+    if (b != nullptr) {
+        m.has_dO = delta_map(&m.dO, b->dO.ptr, p->headdim, p->nheads, p->seqlen, p->batch, b->dO.stride);
+        m.has_dqk = delta_map(&m.dq, b->dq.ptr, p->dstate, p->ngroups, p->seqlen, p->batch, b->dq.stride) &&
+                    delta_map(&m.dk, b->dk.ptr, p->dstate, p->ngroups, p->seqlen, p->batch, b->dk.stride);
         const int64_t rows[3] = {0, 128, DQ * 128}, ch = (int64_t)a.nslots * a.H;
         m.has_vals = delta_map(&m.U, a.U, 128, ch, DQ, 1, rows) && delta_map(&m.mu, a.mu, 128, ch, DQ, 1, rows);
     }
@@ -238,7 +240,7 @@ ssd_status ssd_delta_bwd(const ssd_delta_problem *p, const ssd_delta_bwd_args *b
     a.dS = ws + w.dS;
     a.mu = ws + w.mu;
     a.part = !on_tensor_cores(p) && p->nheads > p->ngroups ? reinterpret_cast<float *>(ws + w.part) : nullptr;
-    return of_cuda(on_tensor_cores(p) && a.nslots > 0 ? delta_tc_bwd(a, maps(p, f, a, &b->dO, b->dv), st) : delta_simt_bwd(a, p->dtype == SSD_BF16, st));
+    return of_cuda(on_tensor_cores(p) && a.nslots > 0 ? delta_tc_bwd(a, maps(p, f, a, b, b->dv), st) : delta_simt_bwd(a, p->dtype == SSD_BF16, st));
 }
 
 }  // extern "C"

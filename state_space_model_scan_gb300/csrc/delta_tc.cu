@@ -20,6 +20,8 @@
 // Q's rows, and both terms of sys, go as one right operand of 128 rows.  All waits are bounded.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+
 #include "delta_tc.cuh"
 
 namespace ssd {
@@ -843,8 +845,8 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
 }
 
 // ---------------------------------------------------------------------------------------- a chunk's gradients
-// A block a chunk and group, the group's heads one after the other (their dQ and dK are added up in registers, in fp32).  Rows 0..63
-// of the 128 TMEM lanes are K's side of a token, rows 64..127 Q's:
+// Persistent blocks over the chunks and groups, a group's heads one after the other (their dQ and dK are added up in registers, in
+// fp32).  Rows 0..63 of the 128 TMEM lanes are K's side of a token, rows 64..127 Q's:
 //
 //   D0 = [K; Q] K^T        D1 = [mu; dO] U^T        D2 = [mu; dO] S       D3 = mu's rows: U dS
 //   D4 = [E; F] K + [E^T K + F^T Q; 0]              dK, dQ = f D2 + D4 (+ f D3)
@@ -852,23 +854,24 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
 // Every operand is a tile as it lies in memory or was left by the chains; factors of a token (beta, e^G, scale) go into E and F or
 // multiply a row of the result, in fp32.  dbeta is D1's diagonal.  dg adds up, for each token, what crosses it inside
 // the chunk (E and F times D0: sums before the column along a row, then down the columns), and rows of D2 and D3 times K, Q.
-// Bound by the work between the products, a block alone on its SM.
-constexpr int GR_NT = 256;
-constexpr uint32_t G_KQ = 0, G_A = G_KQ + 4 * HALF, G_U = G_A + 4 * HALF, G_S = G_U + TOK_BYTES, G_DS = G_S + STATE_BYTES, G_EF = G_DS + STATE_BYTES,
-                   G_Z = G_EF + 2 * HALF, G_GATE = G_Z + HALF, G_COLS = G_GATE + GATE_BYTES, G_SUM = G_COLS + DQ * 4, G_MISC = G_SUM + (8 * 32 + 4 * 64 + 8) * 4,
-                   G_BYTES = G_MISC + 64 + 1024;
+// Four threads a row, a quarter of the columns each.  The next head's tiles (115 KB) are on their way as soon as the products with
+// this one's are done.  Bound by the work and the waits between the products, a block alone on its SM.
+constexpr int GR_NT = 512;
+constexpr uint32_t G_KQ = 0, G_A = G_KQ + 8 * HALF, G_U = G_A + 4 * HALF, G_S = G_U + TOK_BYTES, G_DS = G_S + STATE_BYTES, G_EF = G_DS + STATE_BYTES,
+                   G_Z = G_EF + 2 * HALF, G_GATE = G_Z + HALF, G_COLS = G_GATE + GATE_BYTES, G_SUM = G_COLS + DQ * 4,
+                   G_MISC = G_SUM + (2 * (16 * 16 + 4 * 128 + 4 * 64 + 16) + 4 * 128) * 4, G_BYTES = G_MISC + 64 + 1024;
 constexpr uint32_t T_D0 = 0, T_D1 = 64, T_D2 = 128, T_D3 = 256, T_D4 = 384;
 
-// row r of a tile of 128 rows, half a feature image of 64
+// 8 features from piece q on of row r of a tile's image
 __device__ __forceinline__ void ld_row(const uint8_t *tile, int r, int q, float (&v)[8]) {
     const uint4 u = *reinterpret_cast<const uint4 *>(tile + r * 128 + ((q ^ (r & 7)) << 4));
     v[0] = bf_lo(u.x); v[1] = bf_hi(u.x); v[2] = bf_lo(u.y); v[3] = bf_hi(u.y);
     v[4] = bf_lo(u.z); v[5] = bf_hi(u.z); v[6] = bf_lo(u.w); v[7] = bf_hi(u.w);
 }
-// sums over a warp's lanes of v[e], for lane e
-__device__ __forceinline__ float warp_columns(float (&v)[32], int lane) {
+// sums over a warp's lanes of v[e], for lanes e and e + 16
+__device__ __forceinline__ float warp_columns(float (&v)[16], int lane) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = 8; o > 0; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -876,256 +879,322 @@ __device__ __forceinline__ float warp_columns(float (&v)[32], int lane) {
             v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
     }
-    return v[0];
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
 __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __grid_constant__ DeltaMaps m) {
     extern __shared__ uint8_t raw[];
     uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     float *gate = reinterpret_cast<float *>(sm + G_GATE), *cols = reinterpret_cast<float *>(sm + G_COLS), *colsum = reinterpret_cast<float *>(sm + G_SUM);
-    float *R = colsum + 8 * 32, *X = R + 128, *SSw = X + 128;    // [2][64] each: both halves of a row
+    // sums by quarter, warp: two sets of all but the first
+    constexpr int SUMS = 16 * 16 + 4 * 128 + 4 * 64 + 16;
+    float *R = colsum + 16 * 16, *X = R + 4 * 128, *SSw = X + 4 * 64, *sofar = colsum + 2 * SUMS;
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + G_MISC);
     uint32_t *tm = reinterpret_cast<uint32_t *>(sm + G_MISC + 48);
     enum { L_KQ, L_HEAD, L_D1, L_D2, L_D4 };
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    const int slot = blockIdx.x / a.G, grp = blockIdx.x % a.G, per = a.H / a.G;
-    const DeltaChunk c = delta_chunk(a, slot);
-    if (c.len == 0) return;
+    const int per = a.H / a.G, units = a.nslots * a.G;
+    // the block's next chunk and group from u on that holds tokens
+    DeltaChunk c{}, c2{};
+    auto find = [&](int u, DeltaChunk &to) {
+        for (; u < units; u += gridDim.x)
+            if (to = delta_chunk(a, u / a.G); to.len > 0) break;
+        return u;
+    };
+    int unit = find(blockIdx.x, c);
+    if (unit >= units) return;
     if (w == 0) tmem_alloc(tm, 512);
     if (tid == 0) {
-        for (int i = 0; i < 5; ++i) mbar_init(bar + i, 1);
+        for (int i = 0; i < 5; ++i) mbar_init(bar + i, i == L_KQ ? 2 : i == L_HEAD ? 5 : 1);
         fence_mbar_init();
     }
     for (int e = tid; e < (int)HALF / 16; e += GR_NT) reinterpret_cast<uint4 *>(sm + G_Z)[e] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
-    auto issue = [&](int r) {                                // a head's operands
-        const int h = grp * per + r;
+    // A copy takes the thread that issues it some 180 cycles: they are spread over warps of Q's side, which has less to do.
+    const bool one = lane == 0;
+    auto issue_kq = [&](const DeltaChunk &k, int grp, uint8_t *kq) {
+        if (one && (w == 11 || w == 14)) {
+            const bool has = w == 11 ? m.has_k : m.has_q;
+            bulk_wait_read0();                               // (the chunk before this one has left that tile: the same thread sent it)
+            mbar_expect_tx(bar + L_KQ, has ? TOK_BYTES : 0);
+            if (has) tma_rows(w == 11 ? kq : kq + HALF, 2 * HALF, w == 11 ? &m.k : &m.q, bar + L_KQ, k, grp);
+        }
+        if (!m.has_k) load_rows<GR_NT>(kq, 2 * HALF, tok_rows(a.k, a.ks, k, grp), a.ks[1], k.len, a.K, tid);
+        if (!m.has_q) load_rows<GR_NT>(kq + HALF, 2 * HALF, tok_rows(a.q, a.qs, k, grp), a.qs[1], k.len, a.K, tid);
+    };
+    auto issue = [&](const DeltaChunk &k, int slot, int h) {   // a head's operands
         const int64_t ch = (int64_t)slot * a.H + h;
-        if (tid == 0) {
-            uint64_t *b = bar + L_HEAD;
-            mbar_expect_tx(b, GATE_BYTES + 2 * VAL_BYTES + 2 * STATE_BYTES + (m.has_dO ? TOK_BYTES : 0));
-            const DeltaChunk vals{0, 0, DQ};
+        const DeltaChunk vals{0, 0, DQ};
+        uint64_t *b = bar + L_HEAD;
+        if (one && w == 2) {
+            mbar_expect_tx(b, VAL_BYTES);
             tma_rows(sm + G_A, 2 * HALF, &m.mu, b, vals, (int)ch);
-            if (m.has_dO) tma_rows(sm + G_A + HALF, 2 * HALF, &m.dO, b, c, h);
+        } else if (one && w == 3) {
+            mbar_expect_tx(b, m.has_dO ? TOK_BYTES : 0);
+            if (m.has_dO) tma_rows(sm + G_A + HALF, 2 * HALF, &m.dO, b, k, h);
+        } else if (one && w == 6) {
+            mbar_expect_tx(b, VAL_BYTES);
             tma_rows(sm + G_U, HALF, &m.U, b, vals, (int)ch);
+        } else if (one && w == 7) {
+            mbar_expect_tx(b, GATE_BYTES + STATE_BYTES);
             bulk_load(sm + G_GATE, static_cast<const uint8_t *>(a.tiles) + ch * OPS_BYTES + GATES, GATE_BYTES, b);
             bulk_load(sm + G_S, static_cast<const uint8_t *>(a.S) + ch * STATE_BYTES, STATE_BYTES, b);
+        } else if (one && w == 10) {
+            mbar_expect_tx(b, STATE_BYTES);
             bulk_load(sm + G_DS, static_cast<const uint8_t *>(a.dS) + ch * STATE_BYTES, STATE_BYTES, b);
         }
-        if (!m.has_dO) load_rows<GR_NT>(sm + G_A + HALF, 2 * HALF, tok_rows(a.dO, a.dos, c, h), a.dos[1], c.len, a.V, tid);
+        if (!m.has_dO) load_rows<GR_NT>(sm + G_A + HALF, 2 * HALF, tok_rows(a.dO, a.dos, k, h), a.dos[1], k.len, a.V, tid);
     };
-    if (tid == 0 && (m.has_k || m.has_q)) {
-        mbar_expect_tx(bar + L_KQ, (m.has_k + m.has_q) * TOK_BYTES);
-        if (m.has_k) tma_rows(sm + G_KQ, 2 * HALF, &m.k, bar + L_KQ, c, grp);
-        if (m.has_q) tma_rows(sm + G_KQ + HALF, 2 * HALF, &m.q, bar + L_KQ, c, grp);
-    }
-    if (!m.has_k) load_rows<GR_NT>(sm + G_KQ, 2 * HALF, tok_rows(a.k, a.ks, c, grp), a.ks[1], c.len, a.K, tid);
-    if (!m.has_q) load_rows<GR_NT>(sm + G_KQ + HALF, 2 * HALF, tok_rows(a.q, a.qs, c, grp), a.qs[1], c.len, a.K, tid);
-    issue(0);
+    issue_kq(c, unit % a.G, sm + G_KQ);
+    issue(c, unit / a.G, unit % a.G * per);
     bool ok = true;
-    if (m.has_k || m.has_q) ok = mbar_wait(bar + L_KQ, 0);
-    if (c.len < DQ) {
-        if (m.has_k) zero_rows<GR_NT>(sm + G_KQ, 2 * HALF, c.len, tid);
-        if (m.has_q) zero_rows<GR_NT>(sm + G_KQ + HALF, 2 * HALF, c.len, tid);
-    }
-    const uint32_t base = smem_u32(sm), KQ = base + G_KQ, A = base + G_A, U = base + G_U, S = base + G_S, dS = base + G_DS, EF = base + G_EF, Z = base + G_Z;
-    const int row = (w & 3) * 32 + lane, i = row & 63, hf = w >> 2;
+    const uint32_t base = smem_u32(sm), A = base + G_A, U = base + G_U, S = base + G_S, dS = base + G_DS, EF = base + G_EF, Z = base + G_Z;
+    const int row = (w & 3) * 32 + lane, i = row & 63, qu = w >> 2, j0 = 16 * qu;
     const bool qside = row >= 64;
+    const uint32_t lanes = (uint32_t)(w & 3) << 21;
     uint32_t tmem = 0;
-    float acc[64];
+    // dg of the head before, whose sums are complete (two sets of them in turn): by the first two warps, while the next head's first
+    // products run
+    DeltaChunk was{};
+    int was_h = 0;
+    float was_whole = 0.f;
+    auto write_dg = [&](int set) {
+        const float *cs = colsum + set * SUMS, *Rs = R + set * SUMS, *Xs = X + set * SUMS, *ss = SSw + set * SUMS;
+        float f = lane < 14 ? ss[2 + lane] : 0.f;
+        f = warp_sum(f) * was_whole;
+        float rs = 0.f, xs = 0.f, other = 0.f;
 #pragma unroll
-    for (int e = 0; e < 64; ++e) acc[e] = 0.f;
-    for (int r = 0; r < per; ++r) {
-        const int h = grp * per + r;
-        ok = mbar_wait(bar + L_HEAD, r & 1) && ok;
-        if (c.len < DQ && m.has_dO) zero_rows<GR_NT>(sm + G_A + HALF, 2 * HALF, c.len, tid);
-        if (tid < DQ) {                                      // beta_j e^(G_end - G_j), end the last token of j's block of 16
-            const int e = tid | 15;
-            cols[tid] = gate[2 * DQ + tid] * ex2f(kLog2e * ((gate[3 * DQ + e] - gate[3 * DQ + tid]) + (gate[4 * DQ + e] - gate[4 * DQ + tid])));
+        for (int k = 0; k < 4; ++k) {
+            f += cs[((tid >> 4) * 4 + k) * 16 + (tid & 15)];
+            rs += Rs[k * 128 + tid] + Rs[k * 128 + 64 + tid];
+            xs += Xs[k * 64 + tid];
+            other += tid < 32 ? Rs[k * 128 + 32 + lane] + Rs[k * 128 + 96 + lane] : Xs[k * 64 + lane];
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        tmem = *tm;
-        if (tid == 0) {
-            if (r == 0)
+        float pr = rs, px = xs;                              // inclusive sums: of reads from the end, of writes from the start
 #pragma unroll
-                for (int k = 0; k < 8; ++k) umma_bf16(tmem + T_D0, kmaj(KQ, k, 2 * HALF), kmaj(KQ, k, 2 * HALF), idesc_bf16(128, 64, 0, 0), k > 0);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) umma_bf16(tmem + T_D1, kmaj(A, k, 2 * HALF), kmaj(U, k, HALF), idesc_bf16(128, 64, 0, 0), k > 0);
-            umma_commit(bar + L_D1);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) umma_bf16(tmem + T_D2, kmaj(A, k, 2 * HALF), mnmaj(S, k, STATE_BYTES / 2), idesc_bf16(128, 128, 0, 1), k > 0);
-            // (rows 64..127 of this left operand are the state's first rows: nothing reads what comes of them)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) umma_bf16(tmem + T_D3, kmaj(U, k, HALF), mnmaj(dS, k, STATE_BYTES / 2), idesc_bf16(128, 128, 0, 1), k > 0);
-            umma_commit(bar + L_D2);
+        for (int o = 1; o < 32; o <<= 1) {
+            const float u = __shfl_down_sync(0xffffffffu, pr, o), v = __shfl_up_sync(0xffffffffu, px, o);
+            if (lane + o < 32) pr += u;
+            if (lane >= o) px += v;
         }
-        // <S, dS> meanwhile
-        float ss = 0.f;
-#pragma unroll 4
-        for (int e = tid; e < (int)STATE_BYTES / 16; e += GR_NT) {
-            const uint4 x = reinterpret_cast<const uint4 *>(sm + G_S)[e], y = reinterpret_cast<const uint4 *>(sm + G_DS)[e];
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+        // and the other 32 tokens': their reads come after the first ones, their writes before the last
+        f += pr + (px - xs) + warp_sum(other);
+        if (tid < was.len) delta_st(a.dg, a.g_f32, was.b * a.dgs[0] + (int64_t)(was.t0 + tid) * a.dgs[1] + was_h * a.dgs[2], f);
+    };
+    int it = 0;
+    for (int nu = 0; unit < units; ++nu) {
+        const int grp = unit % a.G;
+        const int next = find(unit + gridDim.x, c2);
+        uint8_t *kqt = sm + G_KQ + (nu & 1) * 4 * HALF;
+        const uint32_t KQ = smem_u32(kqt);
+        ok = mbar_wait(bar + L_KQ, nu & 1) && ok;
+        if (c.len < DQ) {
+            if (m.has_k) zero_rows<GR_NT>(kqt, 2 * HALF, c.len, tid);
+            if (m.has_q) zero_rows<GR_NT>(kqt + HALF, 2 * HALF, c.len, tid);
+        }
+        float acc[32];                                       // dK's, dQ's row: keys 32 qu ..
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                ss = fmaf(bf_lo(xs[d]), bf_lo(ys[d]), ss);
-                ss = fmaf(bf_hi(xs[d]), bf_hi(ys[d]), ss);
+        for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+        for (int r = 0; r < per; ++r, ++it) {
+            const int h = grp * per + r;
+            ok = mbar_wait(bar + L_HEAD, it & 1) && ok;
+            if (c.len < DQ && m.has_dO) zero_rows<GR_NT>(sm + G_A + HALF, 2 * HALF, c.len, tid);
+            if (tid < DQ) {                                  // beta_j e^(G_end - G_j), end the last token of j's block of 16
+                const int e = tid | 15;
+                cols[tid] = gate[2 * DQ + tid] * ex2f(kLog2e * ((gate[3 * DQ + e] - gate[3 * DQ + tid]) + (gate[4 * DQ + e] - gate[4 * DQ + tid])));
             }
-        }
-        ss = warp_sum(ss);
-        if (lane == 0) SSw[w] = ss;
-        // ---- E, F: this thread's row, tokens j = 32 hf ..
-        const float ghi = gate[3 * DQ + i], glo = gate[4 * DQ + i], bi = gate[2 * DQ + i], eg = gate[i];
-        const float f1 = qside ? a.scale : -bi;
-        float flow[32], x[32];
-        ok = mbar_wait(bar + L_D1, r & 1) && ok;
-        tc_fence_after();
-        tmem_ld32(tmem + ((uint32_t)(w & 3) << 21) + T_D1 + 32 * hf, x);
-        tmem_ld32(tmem + ((uint32_t)(w & 3) << 21) + T_D0 + 32 * hf, flow);
-        tmem_wait_ld();
-        float before = 0.f;                                  // sum of the row's w_ij so far
-        {
-            uint8_t *to = sm + G_EF + row * 128;
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncthreads();
+            tc_fence_after();
+            tmem = *tm;
+            if (tid == 15 * 32) {
+                if (r == 0)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {                    // blocks of 16
-                const int j0 = 32 * hf + 16 * b;
-                const float left = f1 * ex2f(kLog2e * ((ghi - gate[3 * DQ + j0 + 15]) + (glo - gate[4 * DQ + j0 + 15])));
-                const bool diag = (i >> 4) == (j0 >> 4), none = j0 > i;
+                    for (int k = 0; k < 8; ++k) umma_bf16(tmem + T_D0, kmaj(KQ, k, 2 * HALF), kmaj(KQ, k, 2 * HALF), idesc_bf16(128, 64, 0, 0), k > 0);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) umma_bf16(tmem + T_D1, kmaj(A, k, 2 * HALF), kmaj(U, k, HALF), idesc_bf16(128, 64, 0, 0), k > 0);
+                umma_commit(bar + L_D1);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) umma_bf16(tmem + T_D2, kmaj(A, k, 2 * HALF), mnmaj(S, k, STATE_BYTES / 2), idesc_bf16(128, 128, 0, 1), k > 0);
+                // (rows 64..127 of this left operand are the state's first rows: nothing reads what comes of them)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) umma_bf16(tmem + T_D3, kmaj(U, k, HALF), mnmaj(dS, k, STATE_BYTES / 2), idesc_bf16(128, 128, 0, 1), k > 0);
+                umma_commit(bar + L_D2);
+            }
+            // <S, dS> meanwhile, by the warps that have no dg to write
+            const int set = (it & 1) * SUMS;
+            if (w >= 2) {
+                float ss = 0.f;
+#pragma unroll 2
+                for (int e = tid - 64; e < (int)STATE_BYTES / 16; e += GR_NT - 64) {
+                    const uint4 x = reinterpret_cast<const uint4 *>(sm + G_S)[e], y = reinterpret_cast<const uint4 *>(sm + G_DS)[e];
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        ss = fmaf(bf_lo(xs[d]), bf_lo(ys[d]), ss);
+                        ss = fmaf(bf_hi(xs[d]), bf_hi(ys[d]), ss);
+                    }
+                }
+                ss = warp_sum(ss);
+                if (lane == 0) SSw[set + w] = ss;
+            } else if (it > 0) {
+                write_dg(~it & 1);
+            }
+            // ---- E, F: this thread's row, tokens j0 .. j0 + 15
+            const float ghi = gate[3 * DQ + i], glo = gate[4 * DQ + i], bi = gate[2 * DQ + i], eg = gate[i];
+            const float fd = gate[DQ + i] * bi, whole = gate[DQ - 1], f1 = qside ? a.scale : -bi, f2 = qside ? a.scale * eg : -eg * bi;
+            float flow[16], x[16], before = 0.f;             // before: sum of the row's w_ij so far
+            ok = mbar_wait(bar + L_D1, it & 1) && ok;
+            tc_fence_after();
+            tmem_ld16(tmem + lanes + T_D1 + j0, x);
+            tmem_ld16(tmem + lanes + T_D0 + j0, flow);
+            tmem_wait_ld();
+            {
+                // the warp's rows lie in two blocks of 16: columns left of both have e^(G_i - G_j) as a product (as in k_prep), those
+                // of either one by one, those right of both are zero
+                const int b0 = 2 * (w & 1);
+                float diag = 0.f;
+                if (qu < b0) {
+                    const float left = f1 * ex2f(kLog2e * ((ghi - gate[3 * DQ + j0 + 15]) + (glo - gate[4 * DQ + j0 + 15])));
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const float4 col = *reinterpret_cast<const float4 *>(cols + j0 + e);
+                        x[e] *= left * col.x; x[e + 1] *= left * col.y; x[e + 2] *= left * col.z; x[e + 3] *= left * col.w;
+                    }
+                } else if (qu <= b0 + 1) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const float4 h4 = *reinterpret_cast<const float4 *>(gate + 3 * DQ + j0 + e), l4 = *reinterpret_cast<const float4 *>(gate + 4 * DQ + j0 + e);
+                        const float4 b4 = *reinterpret_cast<const float4 *>(gate + 2 * DQ + j0 + e);
+                        const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, ls[4] = {l4.x, l4.y, l4.z, l4.w}, bs[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int j = j0 + e + k;
+                            const float d = x[e + k];
+                            diag = j == i ? d : diag;
+                            const float v = f1 * bs[k] * ex2f(kLog2e * ((ghi - hs[k]) + (glo - ls[k]))) * d;
+                            x[e + k] = j > i || (!qside && j == i) ? 0.f : v;
+                        }
+                    }
+                    if (!qside && (i >> 4) == qu && i < c.len)
+                        delta_st(a.dbeta, a.beta_f32, c.b * a.dbs[0] + (int64_t)(c.t0 + i) * a.dbs[1] + h * a.dbs[2], diag);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = 0.f;
+                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int j = j0 + e;
-                    const float d = x[16 * b + e];
-                    float v;
-                    if (diag) v = f1 * gate[2 * DQ + j] * ex2f(kLog2e * ((ghi - gate[3 * DQ + j]) + (glo - gate[4 * DQ + j]))) * d;
-                    else v = left * cols[j] * d;
-                    if (!qside && j == i && j < c.len)
-                        delta_st(a.dbeta, a.beta_f32, c.b * a.dbs[0] + (int64_t)(c.t0 + j) * a.dbs[1] + h * a.dbs[2], d);
-                    v = none || j > i || (!qside && j == i) ? 0.f : v;
-                    const float wij = j < i ? v * flow[16 * b + e] : 0.f;
-                    flow[16 * b + e] = j <= i ? before : 0.f;   // what comes from before j, if it reaches i
+                    const float wij = j < i ? x[e] * flow[e] : 0.f;
+                    flow[e] = j <= i ? before : 0.f;         // what comes from before j, if it reaches i
                     before += wij;
-                    x[16 * b + e] = v;
                 }
+                uint8_t *to = sm + G_EF + row * 128;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    *reinterpret_cast<uint4 *>(to + (((2 * qu + q) ^ (row & 7)) << 4)) = make_uint4(pack_bf16(x[8 * q], x[8 * q + 1]), pack_bf16(x[8 * q + 2], x[8 * q + 3]),
+                                                                                                  pack_bf16(x[8 * q + 4], x[8 * q + 5]), pack_bf16(x[8 * q + 6], x[8 * q + 7]));
+            }
+            sofar[qu * 128 + row] = before;
+            fence_proxy_async_smem();
+            tc_fence_before();
+            ok = mbar_wait(bar + L_D2, it & 1) && ok;
+            __syncthreads();
+            tc_fence_after();
+            if (tid == 15 * 32) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_bf16(tmem + T_D4, kmaj(EF, k, 0), mnmaj(KQ, k, 2 * HALF), idesc_bf16(128, 128, 0, 1), k > 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_bf16(tmem + T_D4, mnmaj(EF, k, Z - EF), mnmaj(KQ, k, 2 * HALF), idesc_bf16(128, 128, 1, 1), 1);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_bf16(tmem + T_D4, mnmaj(EF + HALF, k, Z - EF - HALF), mnmaj(KQ + HALF, k, 2 * HALF), idesc_bf16(128, 128, 1, 1), 1);
+                umma_commit(bar + L_D4);
+            }
+            // this head's tiles and gates have been read: the next head's may come, or the next chunk's
+            if (r + 1 < per) {
+                issue(c, unit / a.G, h + 1);
+            } else if (next < units) {
+                issue_kq(c2, next % a.G, sm + G_KQ + (~nu & 1) * 4 * HALF);
+                issue(c2, next / a.G, next % a.G * per);
+            }
+            {
+                float mine = 0.f;
+                for (int k = 0; k < qu; ++k) mine += sofar[k * 128 + row];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) flow[e] += j0 + e <= i ? mine : 0.f;
+                const float sum = warp_columns(flow, lane);
+                if (lane < 16) colsum[set + w * 16 + lane] = sum;
+            }
+            // ---- rows of D2, D3 times K or Q, and their sum; keys 32 qu ..
+            const uint8_t *kq = kqt + (qu >> 1) * 2 * HALF;
+            float dot = 0.f, dotx = 0.f;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                float y[16];
+                tmem_ld16(tmem + lanes + T_D2 + 32 * qu + 16 * g, x);
+                if (!qside) tmem_ld16(tmem + lanes + T_D3 + 32 * qu + 16 * g, y);
+                tmem_wait_ld();
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const float *y = x + 16 * b + 8 * q;
-                    *reinterpret_cast<uint4 *>(to + (((j0 / 8 + q) ^ (row & 7)) << 4)) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-                }
-            }
-        }
-        if (hf == 0) X[row] = before;                        // for the row's other half
-        fence_proxy_async_smem();
-        tc_fence_before();
-        ok = mbar_wait(bar + L_D2, r & 1) && ok;
-        __syncthreads();
-        tc_fence_after();
-        if (tid == 0) {
+                    float z[8];
+                    ld_row(kq, row, 4 * (qu & 1) + 2 * g + q, z);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) umma_bf16(tmem + T_D4, kmaj(EF, k, 0), mnmaj(KQ, k, 2 * HALF), idesc_bf16(128, 128, 0, 1), k > 0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) umma_bf16(tmem + T_D4, mnmaj(EF, k, Z - EF), mnmaj(KQ, k, 2 * HALF), idesc_bf16(128, 128, 1, 1), 1);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) umma_bf16(tmem + T_D4, mnmaj(EF + HALF, k, Z - EF - HALF), mnmaj(KQ + HALF, k, 2 * HALF), idesc_bf16(128, 128, 1, 1), 1);
-            umma_commit(bar + L_D4);
-        }
-        {
-            const float mine = hf ? X[row] : 0.f;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) flow[e] += 32 * hf + e <= i ? mine : 0.f;
-            colsum[w * 32 + lane] = warp_columns(flow, lane);
-        }
-        const float fd = gate[DQ + i] * bi, whole = gate[DQ - 1];
-        // the head's gates and operands have been read: the next head's may come, except this head's gates (copied above)
-        float ssum = 0.f;
-        if (tid < 64)
-            for (int e = 0; e < 8; ++e) ssum += SSw[e];
-        __syncthreads();
-        if (r + 1 < per) issue(r + 1);
-        // ---- rows of D2, D3 times K or Q, and their sum; keys 64 hf ..
-        const uint8_t *kq = sm + G_KQ + hf * 2 * HALF;
-        const float f2 = qside ? a.scale * eg : -eg * bi;
-        float dot = 0.f, dotx = 0.f;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            float y[32];
-            tmem_ld32(tmem + ((uint32_t)(w & 3) << 21) + T_D2 + 64 * hf + 32 * g, x);
-            if (!qside) tmem_ld32(tmem + ((uint32_t)(w & 3) << 21) + T_D3 + 64 * hf + 32 * g, y);
-            tmem_wait_ld();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float z[8];
-                ld_row(kq, row, 4 * g + q, z);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    dot = fmaf(x[8 * q + e], z[e], dot);
-                    acc[32 * g + 8 * q + e] = fmaf(f2, x[8 * q + e], acc[32 * g + 8 * q + e]);
-                    if (!qside) {
-                        dotx = fmaf(y[8 * q + e], z[e], dotx);
-                        acc[32 * g + 8 * q + e] = fmaf(fd, y[8 * q + e], acc[32 * g + 8 * q + e]);
+                    for (int e = 0; e < 8; ++e) {
+                        dot = fmaf(x[8 * q + e], z[e], dot);
+                        acc[16 * g + 8 * q + e] = fmaf(f2, x[8 * q + e], acc[16 * g + 8 * q + e]);
+                        if (!qside) {
+                            dotx = fmaf(y[8 * q + e], z[e], dotx);
+                            acc[16 * g + 8 * q + e] = fmaf(fd, y[8 * q + e], acc[16 * g + 8 * q + e]);
+                        }
                     }
                 }
             }
-        }
-        // (the flows are done with X) R: a token's reads, by K's and by Q's rows, X: its writes; one half after the other
-        if (hf == 0) {
-            R[row] = f2 * dot;
-            if (!qside) X[i] = fd * dotx;
-        }
-        __syncthreads();
-        if (hf == 1) {
-            R[row] += f2 * dot;
-            if (!qside) X[i] += fd * dotx;
-        }
-        ok = mbar_wait(bar + L_D4, r & 1) && ok;
-        tc_fence_after();
+            R[set + qu * 128 + row] = f2 * dot;                    // a token's reads, by K's and by Q's rows
+            if (!qside) X[set + qu * 64 + i] = fd * dotx;          // and its writes
+            ok = mbar_wait(bar + L_D4, it & 1) && ok;
+            tc_fence_after();
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            tmem_ld32(tmem + ((uint32_t)(w & 3) << 21) + T_D4 + 64 * hf + 32 * g, x);
-            tmem_wait_ld();
+            for (int g = 0; g < 2; ++g) {
+                tmem_ld16(tmem + lanes + T_D4 + 32 * qu + 16 * g, x);
+                tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) acc[32 * g + e] += x[e];
-        }
-        tc_fence_before();
-        __syncthreads();
-        // ---- dg: token t, two warps of them
-        if (tid < 64) {
-            float f = whole * ssum;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f += colsum[((tid >> 5) * 4 + k) * 32 + lane];
-            float rs = R[tid] + R[64 + tid], xs = X[tid];
-            float pr = rs, px = xs;                          // inclusive sums: of reads from the end, of writes from the start
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float u = __shfl_down_sync(0xffffffffu, pr, o), v = __shfl_up_sync(0xffffffffu, px, o);
-                if (lane + o < 32) pr += u;
-                if (lane >= o) px += v;
+                for (int e = 0; e < 16; ++e) acc[16 * g + e] += x[e];
             }
-            // and the other 32 tokens': their reads come after the first ones, their writes before the last
-            const float other = warp_sum(tid < 32 ? R[32 + lane] + R[96 + lane] : X[lane]);
-            f += pr + (px - xs) + other;
-            if (tid < c.len) delta_st(a.dg, a.g_f32, c.b * a.dgs[0] + (int64_t)(c.t0 + tid) * a.dgs[1] + h * a.dgs[2], f);
+            tc_fence_before();
+            __syncthreads();
+            was = c;
+            was_h = h;
+            was_whole = whole;
         }
+        // dK's and dQ's rows: a whole chunk through K's and Q's tile, which nothing reads any more, as one copy
+        uint32_t out[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) out[e] = pack_bf16(acc[2 * e], acc[2 * e + 1]);
+        if (m.has_dqk && c.len == DQ) {
+            uint8_t *to = kqt + (qu >> 1) * 2 * HALF + row * 128;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4 *>(to + (((4 * (qu & 1) + q) ^ (row & 7)) << 4)) = make_uint4(out[4 * q], out[4 * q + 1], out[4 * q + 2], out[4 * q + 3]);
+            fence_proxy_async_smem();
+            __syncthreads();
+            if (one && (w == 11 || w == 14)) {
+                for (int x = 0; x < 2; ++x) tma_store_4d(w == 11 ? &m.dk : &m.dq, kqt + x * 2 * HALF + (w == 11 ? 0 : HALF), 64 * x, grp, c.t0, c.b);
+                bulk_commit();
+            }
+        } else if (i < c.len) {
+            unsigned short *to = qside ? static_cast<unsigned short *>(a.dq) + c.b * a.dqs[0] + (int64_t)(c.t0 + i) * a.dqs[1] + grp * a.dqs[2]
+                                       : static_cast<unsigned short *>(a.dk) + c.b * a.dks[0] + (int64_t)(c.t0 + i) * a.dks[1] + grp * a.dks[2];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (32 * qu + e < a.K) to[32 * qu + e] = (unsigned short)(out[e >> 1] >> (16 * (e & 1)));
+        }
+        unit = next;
+        c = c2;
     }
+    if (w < 2) write_dg(~it & 1);
     if (!ok && tid == 0) set_status(a.hdr, SSD_ERR_DEVICE_TIMEOUT);
-    if (i < c.len) {
-        __nv_bfloat16 *to = qside ? static_cast<__nv_bfloat16 *>(a.dq) + c.b * a.dqs[0] + (int64_t)(c.t0 + i) * a.dqs[1] + grp * a.dqs[2]
-                                  : static_cast<__nv_bfloat16 *>(a.dk) + c.b * a.dks[0] + (int64_t)(c.t0 + i) * a.dks[1] + grp * a.dks[2];
-        to += 64 * hf;
-        const int n = a.K - 64 * hf;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const float *y = acc + 8 * q;
-            if (8 * q + 8 <= n && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
-                *reinterpret_cast<uint4 *>(to + 8 * q) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (8 * q + e < n) to[8 * q + e] = __float2bfloat16_rn(y[e]);
-            }
-        }
-    }
+    bulk_wait0();
     __syncthreads();
     if (w == 0) {
         tc_fence_after();
@@ -1189,7 +1258,7 @@ cudaError_t delta_tc_bwd(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st
     if (cudaError_t e = chain<true, true, true>(a, m, st); e != cudaSuccess) return e;
     static int set[64] = {};
     if (cudaError_t e = ensure_smem_attr(k_grads, (int)G_BYTES, set); e != cudaSuccess) return e;
-    k_grads<<<(unsigned)((int64_t)a.nslots * a.G), GR_NT, G_BYTES, st>>>(a, m);
+    k_grads<<<(unsigned)std::min<int64_t>((int64_t)a.nslots * a.G, 152), GR_NT, G_BYTES, st>>>(a, m);
     return cudaGetLastError();
 }
 

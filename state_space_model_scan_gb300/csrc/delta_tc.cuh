@@ -94,8 +94,8 @@ __device__ __forceinline__ const __nv_bfloat16 *tok_rows(const void *p, const in
 // out: o, backwards dv, without a swizzle, a box 128 features of 64 tokens.  U, mu: [chunk and head][64][128] in the workspace or
 // kept, read as swizzled tiles.
 struct DeltaMaps {
-    CUtensorMap q, k, v, dO, out, U, mu;
-    bool has_q, has_k, has_v, has_dO, has_out, has_vals;
+    CUtensorMap q, k, v, dO, out, U, mu, dq, dk;
+    bool has_q, has_k, has_v, has_dO, has_out, has_vals, has_dqk;
 };
 // delta_tc.cu: bf16 data, headdim and dstate up to 128
 cudaError_t delta_tc_fwd(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st);
