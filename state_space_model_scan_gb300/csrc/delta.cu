@@ -115,6 +115,11 @@ Plan plan(const ssd_delta_problem *p, bool back, bool kept) {
     return w;
 }
 
+// Whether every row of a token tensor starts at 16 bytes.
+bool aligned_rows(const ssd_delta_problem *p, const ssd_tensor &t, int64_t n) {
+    const int64_t e = 16 / (int64_t)esize(p->dtype);
+    return al(t.ptr, 16) && (p->batch == 1 || t.stride[0] % e == 0) && (p->seqlen == 1 || t.stride[1] % e == 0) && (n == 1 || t.stride[2] % e == 0);
+}
 void set3(int64_t *to, const ssd_tensor &t) {
     for (int i = 0; i < 3; ++i) to[i] = t.stride[i];
 }
@@ -122,6 +127,7 @@ DeltaArgs make(const ssd_delta_problem *p, const ssd_delta_args *f, const Plan &
     DeltaArgs a{};
     a.q = f->q.ptr; a.k = f->k.ptr; a.v = f->v.ptr; a.g = f->g.ptr; a.beta = f->beta.ptr;
     set3(a.qs, f->q); set3(a.ks, f->k); set3(a.vs, f->v); set3(a.gs, f->g); set3(a.bs, f->beta);
+    a.vq = aligned_rows(p, f->q, p->ngroups); a.vk = aligned_rows(p, f->k, p->ngroups); a.vv = aligned_rows(p, f->v, p->nheads);
     a.init = f->initial_states.ptr;
     a.init_bf16 = f->initial_states.dtype == SSD_BF16;
     a.g_f32 = f->g.dtype == SSD_F32; a.beta_f32 = f->beta.dtype == SSD_F32;
@@ -230,6 +236,7 @@ ssd_status ssd_delta_bwd(const ssd_delta_problem *p, const ssd_delta_bwd_args *b
     set_kept(a, p, kept ? f->chunk_states : ws + w.kept);
     if (!kept && p->seqlen > 0) DELTA_TRY(of_cuda(run_fwd(p, f, a, ssd_tensor{}, st)));
     a.dO = b->dO.ptr; set3(a.dos, b->dO);
+    a.vo = aligned_rows(p, b->dO, p->nheads);
     a.dq = b->dq.ptr; set3(a.dqs, b->dq);
     a.dk = b->dk.ptr; set3(a.dks, b->dk);
     a.dv = b->dv.ptr; set3(a.dvs, b->dv);

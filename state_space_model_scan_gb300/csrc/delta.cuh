@@ -38,6 +38,7 @@ struct DeltaArgs {
     const void *init, *dfinal;
     void *o, *final, *dq, *dk, *dv, *dg, *dbeta, *dinit;
     int64_t os[3], dqs[3], dks[3], dvs[3], dgs[3], dbs[3];
+    bool vq, vk, vv, vo;        // SIMT: rows of q, k, v, dO start at 16 bytes
     bool g_f32, beta_f32, init_bf16, final_bf16, dfinal_bf16, dinit_bf16;
     const int32_t *cu;          // packed sequences (batch 1) or NULL
     int seqlen, H, G, V, K, nseqs, nslots;   // nseqs: batch or packed; nslots: chunks of all sequences, at most

@@ -119,145 +119,255 @@ __global__ void __launch_bounds__(NT) k_prep(const DeltaArgs a, const bool back)
     for (int e = tid; e < 4096; e += NT) a.sys[at + e] = M[e / 64 * MLD + e % 64];
 }
 
-__device__ __forceinline__ void load_matrix(float *to, const float *p, int tid) {
-    for (int e = tid; e < 4096; e += NT) to[e / 64 * MLD + e % 64] = p[e];
+// ---- the chain.  Shared memory, in floats: the state's rows [VS][KL]; Y, Z [64][XL] of this block's values; and one or two stages (two
+// where they fit) of what a chunk needs: K and Q [64][KL], V or dO [64][XL], the inverse and att [64][ML], the gates.
+constexpr int XL = VS + 4, ML = 68;           // rows of 16-byte pieces, four banks apart
+struct ChainSizes {
+    int KP, KL, stage, stages, bytes;
+};
+__host__ __device__ inline ChainSizes chain_sizes(int K) {
+    ChainSizes z;
+    z.KP = (K + 3) / 4 * 4;
+    z.KL = z.KP + (z.KP % 8 == 0 ? 4 : 8);     // an odd number of pieces
+    z.stage = 2 * 64 * z.KL + 64 * XL + 2 * 64 * ML + DGATES;
+    const int fix = VS * z.KL + 2 * 64 * XL;
+    z.stages = (fix + 2 * z.stage) * 4 <= 227 * 1024 ? 2 : 1;
+    z.bytes = (fix + z.stages * z.stage) * 4;
+    return z;
 }
-
-// ---- the chain.  Shared memory: the state's rows [VS][KP], a slice of K and of Q, two [64][LD] of this block's
-// values, a 64 x 64 matrix, the gates.
-__host__ __device__ constexpr int chain_floats(int KP) { return VS * (KP + 1) + 4 * 64 * LD + 64 * MLD + DGATES; }
+__device__ __forceinline__ void copy_async(float *to, const float *from, int n) {   // n of 4 floats, zeros after them
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(4 * n) : "memory");
+}
+__device__ __forceinline__ void copy_async1(float *to, const float *from, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(in ? 4 : 0) : "memory");
+}
+// rows [0, 64) x columns [c0, c0 + W), W a multiple of 4, of a token tensor of n columns, zeros past `len` rows and n.  fp32 in the background.
+template <typename T>
+__device__ __forceinline__ void load_tile(float *to, int ld, const T *p, int64_t step, int len, int c0, int W, int n, bool vec, int tid) {
+    if constexpr (sizeof(T) == 4) {
+        if (vec) {
+            for (int e = tid; e < 64 * (W / 4); e += NT) {
+                const int i = e / (W / 4), c = e % (W / 4) * 4, left = i < len ? min(4, max(0, n - c0 - c)) : 0;
+                copy_async(to + i * ld + c, left > 0 ? p + i * step + c0 + c : p, left);
+            }
+        } else {
+            for (int e = tid; e < 64 * W; e += NT) {
+                const int i = e / W, c = e % W;
+                const bool in = i < len && c0 + c < n;
+                copy_async1(to + i * ld + c, in ? p + i * step + c0 + c : p, in);
+            }
+        }
+    } else {
+        for (int e = tid; e < 64 * W; e += NT) {
+            const int i = e / W, c = e % W;
+            to[i * ld + c] = i < len && c0 + c < n ? to_f(p[i * step + c0 + c]) : 0.f;
+        }
+    }
+}
+// C[i][v] += sum over j <= i of A[i][j] B[j][v]: rows i = ig + 16 r, columns v = 2 vg, 2 vg + 1
+__device__ __forceinline__ void mul_lower(float (&C)[4][2], const float *A, const float *B, int ig, int vg) {
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) {
+#pragma unroll
+        for (int j = 16 * jb; j < 16 * jb + 16; j += 4) {
+            float2 b[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const float2 *>(B + (j + e) * XL + 2 * vg);
+#pragma unroll
+            for (int r = jb; r < 4; ++r) {
+                const float4 x = *reinterpret_cast<const float4 *>(A + (ig + 16 * r) * ML + j);
+                const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    C[r][0] = fmaf(xs[e], b[e].x, C[r][0]);
+                    C[r][1] = fmaf(xs[e], b[e].y, C[r][1]);
+                }
+            }
+        }
+    }
+}
+// C[j][v] += sum over i >= j of A[i][j] B[i][v]: rows j = 4 ig + r
+__device__ __forceinline__ void mul_lower_t(float (&C)[4][2], const float *A, const float *B, int ig, int vg) {
+#pragma unroll 8
+    for (int i = ig / 4 * 16; i < 64; ++i) {
+        const float4 x = *reinterpret_cast<const float4 *>(A + i * ML + 4 * ig);
+        const float2 b = *reinterpret_cast<const float2 *>(B + i * XL + 2 * vg);
+        const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            C[r][0] = fmaf(xs[r], b.x, C[r][0]);
+            C[r][1] = fmaf(xs[r], b.y, C[r][1]);
+        }
+    }
+}
+// D[v][k] += sum over i of W[i][v] K[i][k]: TV values from v0 on, four keys
+template <int TV>
+__device__ __forceinline__ void mul_state(float (&D)[TV][4], const float *W, const float *K, int KL) {
+#pragma unroll 8
+    for (int i = 0; i < 64; ++i) {
+        const float4 k = *reinterpret_cast<const float4 *>(K + i * KL);
+        float w[TV];
+#pragma unroll
+        for (int e = 0; e < TV; e += 2) {
+            const float2 u = *reinterpret_cast<const float2 *>(W + i * XL + e);
+            w[e] = u.x;
+            w[e + 1] = u.y;
+        }
+#pragma unroll
+        for (int e = 0; e < TV; ++e) {
+            D[e][0] = fmaf(w[e], k.x, D[e][0]);
+            D[e][1] = fmaf(w[e], k.y, D[e][1]);
+            D[e][2] = fmaf(w[e], k.z, D[e][2]);
+            D[e][3] = fmaf(w[e], k.w, D[e][3]);
+        }
+    }
+}
+// S[v][k] = whole S + W^T K (+ Z^T Q), tiles of TV values x 4 keys
+template <int TV, bool BACK>
+__device__ __forceinline__ void update_state(float *S, const float *W, const float *Z, const float *K, const float *Q, float whole, int KP, int KL, int tid) {
+    for (int t = tid; t < VS / TV * (KP / 4); t += NT) {
+        const int v0 = t % (VS / TV) * TV, k0 = t / (VS / TV) * 4;
+        float D[TV][4] = {};
+        mul_state<TV>(D, W + v0, K + k0, KL);
+        if (BACK) mul_state<TV>(D, Z + v0, Q + k0, KL);
+#pragma unroll
+        for (int e = 0; e < TV; ++e) {
+            float4 *p = reinterpret_cast<float4 *>(S + (v0 + e) * KL + k0);
+            const float4 x = *p;
+            *p = make_float4(fmaf(whole, x.x, D[e][0]), fmaf(whole, x.y, D[e][1]), fmaf(whole, x.z, D[e][2]), fmaf(whole, x.w, D[e][3]));
+        }
+    }
+}
 
 template <typename T, bool BACK>
 __global__ void __launch_bounds__(NT) k_chain(const DeltaArgs a) {
     extern __shared__ float sm[];
-    const int KP = (a.K + 31) / 32 * 32, SLD = KP + 1;
-    float *S = sm, *Ks = S + VS * SLD, *Qs = Ks + 64 * LD, *Y = Qs + 64 * LD, *Z = Y + 64 * LD, *M = Z + 64 * LD, *gate = M + 64 * MLD;
-    const int nv = (a.V + VS - 1) / VS, tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+    const ChainSizes z = chain_sizes(a.K);
+    const int KP = z.KP, KL = z.KL;
+    float *S = sm, *Y = S + VS * KL, *Z = Y + 64 * XL, *stages = Z + 64 * XL;
+    const int nv = (a.V + VS - 1) / VS, tid = threadIdx.x, ig = tid / 16, vg = tid % 16;
     const int v0 = blockIdx.x % nv * VS, h = blockIdx.x / nv % a.H, s = blockIdx.x / nv / a.H, grp = h / (a.H / a.G);
     const DeltaSeq q = delta_seq(a, s);
     const int64_t sat = ((int64_t)s * a.H + h) * a.V * a.K;
+    const int nch = (q.len + DQ - 1) / DQ;
+    auto issue = [&](int n) {                               // what step n needs
+        const int ci = BACK ? nch - 1 - n : n;
+        const DeltaChunk c{q.b, q.t0 + ci * DQ, min(DQ, q.len - ci * DQ)};
+        const int64_t ch = (int64_t)(q.slot0 + ci) * a.H + h;
+        float *st = stages + (z.stages == 2 ? n & 1 : 0) * z.stage;
+        load_tile(st, KL, rows_of<T>(a.k, a.ks, c, grp), a.ks[1], c.len, 0, KP, a.K, a.vk, tid);
+        if (BACK || a.o) load_tile(st + 64 * KL, KL, rows_of<T>(a.q, a.qs, c, grp), a.qs[1], c.len, 0, KP, a.K, a.vq, tid);
+        if (BACK) load_tile(st + 128 * KL, XL, rows_of<T>(a.dO, a.dos, c, h), a.dos[1], c.len, v0, VS, a.V, a.vo, tid);
+        else load_tile(st + 128 * KL, XL, rows_of<T>(a.v, a.vs, c, h), a.vs[1], c.len, v0, VS, a.V, a.vv, tid);
+        float *M = st + 128 * KL + 64 * XL;
+        for (int e = tid; e < 64 * 16; e += NT) {
+            copy_async(M + e / 16 * ML + e % 16 * 4, a.sys + ch * 4096 + e * 4, 4);
+            copy_async(M + 64 * ML + e / 16 * ML + e % 16 * 4, a.att + ch * 4096 + e * 4, 4);
+        }
+        for (int e = tid; e < DGATES / 4; e += NT) copy_async(M + 2 * 64 * ML + e * 4, a.gates + ch * DGATES + e * 4, 4);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (nch > 0) issue(0);
     const void *in = BACK ? a.dfinal : a.init;
     const bool in16 = BACK ? a.dfinal_bf16 : a.init_bf16;
     for (int e = tid; e < VS * KP; e += NT) {
         const int v = e / KP, k = e % KP;
-        S[v * SLD + k] = in && v0 + v < a.V && k < a.K ? delta_ld(in, !in16, sat + (int64_t)(v0 + v) * a.K + k) : 0.f;
+        S[v * KL + k] = in && v0 + v < a.V && k < a.K ? delta_ld(in, !in16, sat + (int64_t)(v0 + v) * a.K + k) : 0.f;
     }
-    const int nch = (q.len + DQ - 1) / DQ;
     float *kept = static_cast<float *>(BACK ? a.dS : a.S), *vals = static_cast<float *>(BACK ? a.mu : a.U);
     for (int n = 0; n < nch; ++n) {
         const int ci = BACK ? nch - 1 - n : n;
         const DeltaChunk c{q.b, q.t0 + ci * DQ, min(DQ, q.len - ci * DQ)};
         const int64_t ch = (int64_t)(q.slot0 + ci) * a.H + h;
-        const T *kp = rows_of<T>(a.k, a.ks, c, grp), *qp = rows_of<T>(a.q, a.qs, c, grp);
+        if (z.stages == 2 && n + 1 < nch) {                 // (every thread is done with the other stage since the last sync)
+            issue(n + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
         __syncthreads();
-        for (int e = tid; e < DGATES; e += NT) gate[e] = a.gates[ch * DGATES + e];
+        const float *Ks = stages + (z.stages == 2 ? n & 1 : 0) * z.stage, *Qs = Ks + 64 * KL, *Xs = Qs + 64 * KL, *Ms = Xs + 64 * XL, *Ma = Ms + 64 * ML, *gate = Ma + 64 * ML;
         if (kept)
             for (int e = tid; e < VS * KP; e += NT) {
                 const int v = e / KP, k = e % KP;
-                if (v0 + v < a.V && k < a.K) kept[(ch * a.V + v0 + v) * a.K + k] = S[v * SLD + k];
+                if (v0 + v < a.V && k < a.K) kept[(ch * a.V + v0 + v) * a.K + k] = S[v * KL + k];
             }
-        // P = K S^T and, forwards, Q S^T: the state's rows as columns
+        // P = K S^T and, forwards, Q S^T: rows ig + 16 r (backwards 4 ig + r), columns 2 vg, 2 vg + 1
         float P[4][2] = {}, O[4][2] = {};
-        for (int k0 = 0; k0 < KP; k0 += 32) {
-            __syncthreads();
-            load_slice(Ks, kp, a.ks[1], c.len, k0, a.K, tid);
-            if (!BACK) load_slice(Qs, qp, a.qs[1], c.len, k0, a.K, tid);
-            __syncthreads();
-#pragma unroll 8
-            for (int l = 0; l < 32; ++l) {
-                const float b0 = S[2 * tx * SLD + k0 + l], b1 = S[(2 * tx + 1) * SLD + k0 + l];
+        const bool outs = !BACK && a.o;
+        auto rw = [&](int r) { return BACK ? 4 * ig + r : ig + 16 * r; };
+#pragma unroll 2
+        for (int l = 0; l < KP; l += 4) {
+            float4 b[2];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float x = Ks[(16 * r + ty) * LD + l];
-                    P[r][0] = fmaf(x, b0, P[r][0]);
-                    P[r][1] = fmaf(x, b1, P[r][1]);
-                    if (!BACK) {
-                        const float y = Qs[(16 * r + ty) * LD + l];
-                        O[r][0] = fmaf(y, b0, O[r][0]);
-                        O[r][1] = fmaf(y, b1, O[r][1]);
-                    }
+            for (int e = 0; e < 2; ++e) b[e] = *reinterpret_cast<const float4 *>(S + (2 * vg + e) * KL + l);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 x = *reinterpret_cast<const float4 *>(Ks + rw(r) * KL + l);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) P[r][e] = fmaf(x.x, b[e].x, fmaf(x.y, b[e].y, fmaf(x.z, b[e].z, fmaf(x.w, b[e].w, P[r][e]))));
+                if (outs) {
+                    const float4 y = *reinterpret_cast<const float4 *>(Qs + rw(r) * KL + l);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) O[r][e] = fmaf(y.x, b[e].x, fmaf(y.y, b[e].y, fmaf(y.z, b[e].z, fmaf(y.w, b[e].w, O[r][e]))));
                 }
             }
         }
-        const T *vp = BACK ? rows_of<T>(a.dO, a.dos, c, h) : rows_of<T>(a.v, a.vs, c, h);
-        const int64_t vstep = BACK ? a.dos[1] : a.vs[1];
-        __syncthreads();
-        load_matrix(M, BACK ? a.att + ch * 4096 : a.sys + ch * 4096, tid);
         float N[4][2] = {};
-        if (BACK) {                                        // N = scale att^T dO + e^(Gc - G) P
-            load_slice(Z, vp, vstep, c.len, v0, a.V, tid);
-            __syncthreads();
-            fma_slice_t(N, M, MLD, Z, LD, 64, ty, tx);
-        }
+        if (BACK) mul_lower_t(N, Ma, Xs, ig, vg);           // N = scale att^T dO + e^(Gc - G) P
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = 16 * r + ty, v = 2 * tx + e;
-                float y;
-                if (BACK) y = fmaf(gate[DQ + i], P[r][e], a.scale * N[r][e]);
-                else y = (i < c.len && v0 + v < a.V ? to_f(vp[i * vstep + v0 + v]) : 0.f) - gate[i] * P[r][e];
-                Y[i * LD + v] = y;
+        for (int r = 0; r < 4; ++r) {
+            const int i = rw(r);
+            float2 y;
+            if (BACK) {
+                y = make_float2(fmaf(gate[DQ + i], P[r][0], a.scale * N[r][0]), fmaf(gate[DQ + i], P[r][1], a.scale * N[r][1]));
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(Xs + i * XL + 2 * vg);
+                y = make_float2(fmaf(-gate[i], P[r][0], v.x), fmaf(-gate[i], P[r][1], v.y));
             }
-        __syncthreads();
-        if (BACK) {
-            load_matrix(M, a.sys + ch * 4096, tid);
-            __syncthreads();
+            *reinterpret_cast<float2 *>(Y + i * XL + 2 * vg) = y;
         }
+        __syncthreads();
         float U[4][2] = {};
-        if (BACK) fma_slice_t(U, M, MLD, Y, LD, 64, ty, tx);
-        else fma_slice(U, M, MLD, Y, LD, 64, ty, tx);
+        if (BACK) mul_lower_t(U, Ms, Y, ig, vg);
+        else mul_lower(U, Ms, Y, ig, vg);
         __syncthreads();
+        // W = beta U, or lam; what goes to the state: e^(Gc - G) W in Z, backwards -e^G lam in Y and scale e^G dO in Z
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r) {
+            const int i = rw(r);
+            if (vals)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = 16 * r + ty, v = 2 * tx + e;
-                if (vals && v0 + v < a.V) vals[(ch * 64 + i) * a.V + v0 + v] = U[r][e];
-                Y[i * LD + v] = gate[2 * DQ + i] * U[r][e];     // W, or lam
+                for (int e = 0; e < 2; ++e)
+                    if (v0 + 2 * vg + e < a.V) vals[(ch * 64 + i) * a.V + v0 + 2 * vg + e] = U[r][e];
+            const float w0 = gate[2 * DQ + i] * U[r][0], w1 = gate[2 * DQ + i] * U[r][1];
+            if (BACK) {
+                *reinterpret_cast<float2 *>(Y + i * XL + 2 * vg) = make_float2(-gate[i] * w0, -gate[i] * w1);
+                const float2 v = *reinterpret_cast<const float2 *>(Xs + i * XL + 2 * vg);
+                *reinterpret_cast<float2 *>(Z + i * XL + 2 * vg) = make_float2(a.scale * gate[i] * v.x, a.scale * gate[i] * v.y);
+            } else {
+                *reinterpret_cast<float2 *>(Y + i * XL + 2 * vg) = make_float2(w0, w1);
+                *reinterpret_cast<float2 *>(Z + i * XL + 2 * vg) = make_float2(gate[DQ + i] * w0, gate[DQ + i] * w1);
             }
-        if (!BACK && a.o) {
-            load_matrix(M, a.att + ch * 4096, tid);
-            __syncthreads();
+        }
+        __syncthreads();
+        const float whole = gate[DQ - 1];
+        if (outs) {
             float A[4][2] = {};
-            fma_slice(A, M, MLD, Y, LD, 64, ty, tx);
+            mul_lower(A, Ma, Y, ig, vg);
             T *op = static_cast<T *>(a.o) + c.b * a.os[0] + c.t0 * a.os[1] + h * a.os[2] + v0;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int i = 16 * r + ty, v = 2 * tx + e;
+                    const int i = ig + 16 * r, v = 2 * vg + e;
                     if (i < c.len && v0 + v < a.V) op[i * a.os[1] + v] = from_f<T>(a.scale * fmaf(gate[i], O[r][e], A[r][e]));
                 }
         }
-        // the state: rows v = 16 r + ty, columns of a slice
-        const float whole = gate[DQ - 1];
+        if (KP > 64) update_state<4, BACK>(S, BACK ? Y : Z, Z, Ks, Qs, whole, KP, KL, tid);
+        else update_state<2, BACK>(S, BACK ? Y : Z, Z, Ks, Qs, whole, KP, KL, tid);
         __syncthreads();
-        for (int e = tid; e < 64 * VS; e += NT) {
-            const int i = e / VS, v = e % VS;
-            if (BACK) {
-                Z[i * LD + v] *= a.scale * gate[i];           // scale e^G dO
-                Y[i * LD + v] *= -gate[i];                    // -e^G lam
-            } else {
-                Y[i * LD + v] *= gate[DQ + i];                // e^(Gc - G) W
-            }
-        }
-        for (int k0 = 0; k0 < KP; k0 += 32) {
-            __syncthreads();
-            load_slice(Ks, kp, a.ks[1], c.len, k0, a.K, tid);
-            if (BACK) load_slice(Qs, qp, a.qs[1], c.len, k0, a.K, tid);
-            __syncthreads();
-            float D[2][2] = {};
-            fma_slice_t(D, Y, LD, Ks, LD, 64, ty, tx);
-            if (BACK) fma_slice_t(D, Z, LD, Qs, LD, 64, ty, tx);
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float &x = S[(16 * r + ty) * SLD + k0 + 2 * tx + e];
-                    x = fmaf(whole, x, D[r][e]);
-                }
-        }
+        if (z.stages == 1 && n + 1 < nch) issue(n + 1);
     }
     __syncthreads();
     void *out = BACK ? a.dinit : a.final;
@@ -265,7 +375,7 @@ __global__ void __launch_bounds__(NT) k_chain(const DeltaArgs a) {
     if (out)
         for (int e = tid; e < VS * KP; e += NT) {
             const int v = e / KP, k = e % KP;
-            if (v0 + v < a.V && k < a.K) delta_st(out, !out16, sat + (int64_t)(v0 + v) * a.K + k, S[v * SLD + k]);
+            if (v0 + v < a.V && k < a.K) delta_st(out, !out16, sat + (int64_t)(v0 + v) * a.K + k, S[v * KL + k]);
         }
 }
 
@@ -504,7 +614,7 @@ __global__ void __launch_bounds__(NT) k_share(const DeltaArgs a) {
 template <typename T, bool BACK>
 cudaError_t chain(const DeltaArgs &a, cudaStream_t st) {
     static int set[64] = {};
-    const int bytes = chain_floats((a.K + 31) / 32 * 32) * (int)sizeof(float);
+    const int bytes = chain_sizes(a.K).bytes;
     if (cudaError_t e = ensure_smem_attr(k_chain<T, BACK>, bytes, set); e != cudaSuccess) return e;
     k_chain<T, BACK><<<(unsigned)(a.nseqs * (int64_t)a.H * ((a.V + VS - 1) / VS)), NT, bytes, st>>>(a);
     return cudaGetLastError();

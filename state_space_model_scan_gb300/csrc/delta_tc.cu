@@ -105,6 +105,7 @@ __device__ __forceinline__ void invert(float *M, float *t, int tid) {
 // a block a chunk and head
 template <bool BACK>
 __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __grid_constant__ DeltaMaps m) {
+    after_previous();
     extern __shared__ uint8_t raw[];
     uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     float *M = reinterpret_cast<float *>(sm + P_M), *T = reinterpret_cast<float *>(sm + P_T), *gate = reinterpret_cast<float *>(sm + P_GATE);
@@ -324,6 +325,7 @@ __device__ __forceinline__ void ld_gates(f32x2 &g0, f32x2 &g1, const float *p) {
 // its matrix, is left and nothing else
 template <bool BACK, bool KEEP, bool OUT, bool ENDS>
 __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __grid_constant__ DeltaMaps m) {
+    after_previous();
     extern __shared__ uint8_t raw[];
     uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     ChainBars *ms = reinterpret_cast<ChainBars *>(sm + CH_MISC);
@@ -883,6 +885,7 @@ __device__ __forceinline__ float warp_columns(float (&v)[16], int lane) {
 }
 
 __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __grid_constant__ DeltaMaps m) {
+    after_previous();
     extern __shared__ uint8_t raw[];
     uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     float *gate = reinterpret_cast<float *>(sm + G_GATE), *cols = reinterpret_cast<float *>(sm + G_COLS), *colsum = reinterpret_cast<float *>(sm + G_SUM);
@@ -1206,15 +1209,13 @@ template <bool BACK>
 cudaError_t prep(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
     static int set[64] = {};
     if (cudaError_t e = ensure_smem_attr(k_prep<BACK>, (int)P_BYTES, set); e != cudaSuccess) return e;
-    k_prep<BACK><<<(unsigned)((int64_t)a.nslots * a.H), PREP_NT, P_BYTES, st>>>(a, m);
-    return cudaGetLastError();
+    return launch_early(k_prep<BACK>, (unsigned)((int64_t)a.nslots * a.H), PREP_NT, P_BYTES, st, a, m);
 }
 template <bool BACK, bool KEEP, bool OUT, bool ENDS>
 cudaError_t launch_chain(const DeltaArgs &a, const DeltaMaps &m, int parts, cudaStream_t st) {
     static int set[64] = {};
     if (cudaError_t e = ensure_smem_attr(k_chain<BACK, KEEP, OUT, ENDS>, (int)CH_BYTES, set); e != cudaSuccess) return e;
-    k_chain<BACK, KEEP, OUT, ENDS><<<(unsigned)(a.nseqs * (int64_t)a.H * parts), CH_NT, CH_BYTES, st>>>(a, m);
-    return cudaGetLastError();
+    return launch_early(k_chain<BACK, KEEP, OUT, ENDS>, (unsigned)(a.nseqs * (int64_t)a.H * parts), CH_NT, CH_BYTES, st, a, m);
 }
 template <bool BACK, bool KEEP, bool OUT>
 cudaError_t chain(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
@@ -1258,8 +1259,7 @@ cudaError_t delta_tc_bwd(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st
     if (cudaError_t e = chain<true, true, true>(a, m, st); e != cudaSuccess) return e;
     static int set[64] = {};
     if (cudaError_t e = ensure_smem_attr(k_grads, (int)G_BYTES, set); e != cudaSuccess) return e;
-    k_grads<<<(unsigned)std::min<int64_t>((int64_t)a.nslots * a.G, 152), GR_NT, G_BYTES, st>>>(a, m);
-    return cudaGetLastError();
+    return launch_early(k_grads, (unsigned)std::min<int64_t>((int64_t)a.nslots * a.G, 152), GR_NT, G_BYTES, st, a, m);
 }
 
 }  // namespace ssd
