@@ -157,11 +157,15 @@ __device__ __forceinline__ void delta_gates(const DeltaArgs &a, const DeltaChunk
     }
 }
 
-// Inverse of I + M, M strictly lower triangular 64 x 64, in place in shared memory (row stride LD), by 256 threads: the
-// four 16 x 16 blocks on the diagonal by substitution, a thread a column; then twice the block below the
-// diagonal of a pair, -T22 M21 T11 (t: 32 x 33 floats of scratch).  M's upper part and diagonal are written, not read.
-template <int LD>
+constexpr int DELTA_ML = 68;    // row stride of a 64 x 64 matrix in shared memory: rows of 16-byte pieces, four banks apart
+
+// Inverse of I + M, M strictly lower triangular 64 x 64, in place in shared memory, by NT threads: the four 16 x 16 blocks on the
+// diagonal by substitution, a thread a column; then twice the block below the diagonal of a pair, -T22 M21 T11, a thread four
+// neighbouring columns of a row (t: 32 x 36 floats of scratch).  Of the blocks above the diagonal, those in the pairs of 32 are set
+// to zero, the other is neither read nor written.
+template <int NT>
 __device__ __forceinline__ void delta_invert(float *M, float *t, int tid) {
+    constexpr int MLD = DELTA_ML;
     if (tid < 64) {
         const int o = tid / 16 * 16, j = tid & 15;
         float x[16];
@@ -169,39 +173,55 @@ __device__ __forceinline__ void delta_invert(float *M, float *t, int tid) {
         for (int i = 0; i < 16; ++i) {
             float s = i == j ? 1.f : 0.f;
 #pragma unroll
-            for (int l = 0; l < i; ++l) s = fmaf(-M[(o + i) * LD + o + l], x[l], s);
+            for (int l = 0; l < i; l += 4) {
+                const float4 m = *reinterpret_cast<const float4 *>(M + (o + i) * MLD + o + l);
+                s = fmaf(-m.x, x[l], s);
+                if (l + 1 < i) s = fmaf(-m.y, x[l + 1], s);
+                if (l + 2 < i) s = fmaf(-m.z, x[l + 2], s);
+                if (l + 3 < i) s = fmaf(-m.w, x[l + 3], s);
+            }
             x[i] = s;
         }
-        __syncwarp();
-        // every column of a block is read by its sixteen threads before one of them writes: they are in one warp
+        __syncwarp();                                        // a block's sixteen threads are in one warp
 #pragma unroll
-        for (int i = 0; i < 16; ++i) M[(o + i) * LD + o + j] = x[i];
+        for (int i = 0; i < 16; ++i) M[(o + i) * MLD + o + j] = x[i];
+    }
+    if (tid < 128) {                                         // the blocks of 16 above a pair's diagonal: zeros, for the pair of 32
+        const int o = tid / 64 * 32;
+        *reinterpret_cast<float4 *>(M + (o + tid % 64 / 4) * MLD + o + 16 + tid % 4 * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     __syncthreads();
 #pragma unroll
     for (int n = 16; n <= 32; n *= 2) {
-        // pairs of n x n blocks: two of 16, one of 32; t = M21 T11, then M21 = -T22 t
-        for (int e = tid; e < 32 * n; e += 256) {
-            const int p = e / (n * n), i = e / n % n, j = e % n, o = p * 2 * n;
-            float s = 0.f;
-            for (int l = 0; l < n; ++l) s = fmaf(M[(o + n + i) * LD + o + l], M[(o + l) * LD + o + j], s);
-            t[(p * n + i) * 33 + j] = s;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {               // t = M21 T11, then M21 = -T22 t
+#pragma unroll 1
+            for (int it = tid; it < 8 * n; it += NT) {
+                const int per = n * n / 4, p = it / per, i = it % per / (n / 4), j = it % (n / 4) * 4, o = p * 2 * n;
+                f32x2 s0 = 0, s1 = 0;
+                const float *A = M + (o + n + i) * MLD + o + (half ? n : 0), *B = half ? t + p * n * 36 + j : M + o * MLD + o + j;
+                const int ldb = half ? 36 : MLD;
+#pragma unroll 2
+                for (int l = 0; l < n; l += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(A + l);
+                    const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(B + (l + e) * ldb);
+                        const f32x2 xx = pk2(xs[e], xs[e]);
+                        s0 = fma2(xx, y.x, s0);
+                        s1 = fma2(xx, y.y, s1);
+                    }
+                }
+                float4 r;
+                up2(s0, r.x, r.y);
+                up2(s1, r.z, r.w);
+                if (half) *reinterpret_cast<float4 *>(M + (o + n + i) * MLD + o + j) = make_float4(-r.x, -r.y, -r.z, -r.w);
+                else *reinterpret_cast<float4 *>(t + (p * n + i) * 36 + j) = r;
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        for (int e = tid; e < 32 * n; e += 256) {
-            const int p = e / (n * n), i = e / n % n, j = e % n, o = p * 2 * n;
-            float s = 0.f;
-            for (int l = 0; l <= i; ++l) s = fmaf(-M[(o + n + i) * LD + o + n + l], t[(p * n + l) * 33 + j], s);
-            M[(o + n + i) * LD + o + j] = s;
-        }
-        __syncthreads();
     }
-    // above the diagonal blocks
-    for (int e = tid; e < 64 * 64; e += 256) {
-        const int i = e / 64, j = e % 64;
-        if (j / 16 > i / 16) M[i * LD + j] = 0.f;
-    }
-    __syncthreads();
 }
 
 // delta_simt.cu: any type and size.  states: leave a.S and a.U (and no o, where a.o is NULL).

@@ -15,8 +15,8 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int VS = 32;              // values of a chain block
-constexpr int LD = 33;              // row stride of a slice of 32
-constexpr int MLD = 65;             // row stride of a 64 x 64 matrix
+constexpr int LD = 36;              // row stride of a slice of 32: rows of 16-byte pieces, four banks apart
+constexpr int MLD = DELTA_ML;
 
 // rows [0, 64) of a slice of 32 columns from column k0 of a chunk's rows (row stride `step` elements); zeros past the chunk and past n
 template <typename T>
@@ -30,17 +30,23 @@ template <typename T>
 __device__ __forceinline__ const T *rows_of(const void *p, const int64_t *s, const DeltaChunk &c, int h) {
     return static_cast<const T *>(p) + c.b * s[0] + c.t0 * s[1] + h * s[2];
 }
-// R x 2 of a product over a slice: rows i = 16 r + ty of A [64][LD] (n of them: R = n / 16), columns 2 tx and 2 tx + 1 of B^T [32][..]
+// R x 2 of a product over a slice of n: rows 16 r + ty of A, columns 2 tx and 2 tx + 1 of B [n][ldb]
 template <int R>
 __device__ __forceinline__ void fma_slice(float (&acc)[R][2], const float *A, int lda, const float *B, int ldb, int n, int ty, int tx) {
-#pragma unroll 8
-    for (int l = 0; l < n; ++l) {
-        const float b0 = B[l * ldb + 2 * tx], b1 = B[l * ldb + 2 * tx + 1];
+#pragma unroll 4
+    for (int l = 0; l < n; l += 4) {
+        float2 b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const float2 *>(B + (l + e) * ldb + 2 * tx);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float x = A[(16 * r + ty) * lda + l];
-            acc[r][0] = fmaf(x, b0, acc[r][0]);
-            acc[r][1] = fmaf(x, b1, acc[r][1]);
+            const float4 x = *reinterpret_cast<const float4 *>(A + (16 * r + ty) * lda + l);
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                acc[r][0] = fmaf(xs[e], b[e].x, acc[r][0]);
+                acc[r][1] = fmaf(xs[e], b[e].y, acc[r][1]);
+            }
         }
     }
 }
@@ -49,12 +55,30 @@ template <int R>
 __device__ __forceinline__ void fma_slice_t(float (&acc)[R][2], const float *A, int lda, const float *B, int ldb, int n, int ty, int tx) {
 #pragma unroll 8
     for (int l = 0; l < n; ++l) {
-        const float b0 = B[l * ldb + 2 * tx], b1 = B[l * ldb + 2 * tx + 1];
+        const float2 b = *reinterpret_cast<const float2 *>(B + l * ldb + 2 * tx);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float x = A[l * lda + 16 * r + ty];
-            acc[r][0] = fmaf(x, b0, acc[r][0]);
-            acc[r][1] = fmaf(x, b1, acc[r][1]);
+            acc[r][0] = fmaf(x, b.x, acc[r][0]);
+            acc[r][1] = fmaf(x, b.y, acc[r][1]);
+        }
+    }
+}
+// x[r][s] += rows 16 r + ty of A times rows 16 s + tx of B, y of A2 (all [64][LD], a slice of 32)
+__device__ __forceinline__ void mul_rows(float (&x)[4][4], float (&y)[4][4], const float *A, const float *A2, const float *B, int ty, int tx) {
+#pragma unroll 2
+    for (int l = 0; l < 32; l += 4) {
+        float4 b[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) b[s] = *reinterpret_cast<const float4 *>(B + (16 * s + tx) * LD + l);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float4 u = *reinterpret_cast<const float4 *>(A + (16 * r + ty) * LD + l), v = *reinterpret_cast<const float4 *>(A2 + (16 * r + ty) * LD + l);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                x[r][s] = fmaf(u.x, b[s].x, fmaf(u.y, b[s].y, fmaf(u.z, b[s].z, fmaf(u.w, b[s].w, x[r][s]))));
+                y[r][s] = fmaf(v.x, b[s].x, fmaf(v.y, b[s].y, fmaf(v.z, b[s].z, fmaf(v.w, b[s].w, y[r][s]))));
+            }
         }
     }
 }
@@ -62,7 +86,8 @@ __device__ __forceinline__ void fma_slice_t(float (&acc)[R][2], const float *A, 
 // ---- the chunk's matrices: sys = (I + a diag(beta))^-1 or, backwards, (I + diag(beta) a)^-1; att; a.
 template <typename T>
 __global__ void __launch_bounds__(NT) k_prep(const DeltaArgs a, const bool back) {
-    __shared__ float Ks[64 * LD], Qs[64 * LD], M[64 * MLD], gate[DGATES];
+    after_previous();
+    __shared__ __align__(16) float Ks[64 * LD], Qs[64 * LD], M[64 * MLD], gate[DGATES];
     const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
     if (blockIdx.x == 0 && tid < HDR_WORDS) a.hdr[tid] = 0;
     const DeltaChunk c = delta_chunk(a, slot);
@@ -81,23 +106,7 @@ __global__ void __launch_bounds__(NT) k_prep(const DeltaArgs a, const bool back)
         load_slice(Ks, k, a.ks[1], c.len, k0, a.K, tid);
         load_slice(Qs, q, a.qs[1], c.len, k0, a.K, tid);
         __syncthreads();
-#pragma unroll 4
-        for (int l = 0; l < 32; ++l) {
-            float kr[4], qr[4], kc[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                kr[r] = Ks[(16 * r + ty) * LD + l];
-                qr[r] = Qs[(16 * r + ty) * LD + l];
-                kc[r] = Ks[(16 * r + tx) * LD + l];
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    kk[r][s] = fmaf(kr[r], kc[s], kk[r][s]);
-                    qk[r][s] = fmaf(qr[r], kc[s], qk[r][s]);
-                }
-        }
+        mul_rows(kk, qk, Ks, Qs, Ks, ty, tx);
     }
     const int64_t at = ((int64_t)slot * a.H + h) * 4096;
 #pragma unroll
@@ -115,13 +124,13 @@ __global__ void __launch_bounds__(NT) k_prep(const DeltaArgs a, const bool back)
 #pragma unroll
         for (int e = 0; e < DGATES / DQ; ++e) a.gates[((int64_t)slot * a.H + h) * DGATES + e * DQ + tid] = gate[e * DQ + tid];
     __syncthreads();
-    delta_invert<MLD>(M, Ks, tid);
-    for (int e = tid; e < 4096; e += NT) a.sys[at + e] = M[e / 64 * MLD + e % 64];
+    delta_invert<NT>(M, Ks, tid);
+    for (int e = tid; e < 4096; e += NT) a.sys[at + e] = e % 64 / 16 <= e / 64 / 16 ? M[e / 64 * MLD + e % 64] : 0.f;
 }
 
 // ---- the chain.  Shared memory, in floats: the state's rows [VS][KL]; Y, Z [64][XL] of this block's values; and one or two stages (two
 // where they fit) of what a chunk needs: K and Q [64][KL], V or dO [64][XL], the inverse and att [64][ML], the gates.
-constexpr int XL = VS + 4, ML = 68;           // rows of 16-byte pieces, four banks apart
+constexpr int XL = VS + 4, ML = DELTA_ML;     // rows of 16-byte pieces, four banks apart
 struct ChainSizes {
     int KP, KL, stage, stages, bytes;
 };
@@ -241,6 +250,7 @@ __device__ __forceinline__ void update_state(float *S, const float *W, const flo
 
 template <typename T, bool BACK>
 __global__ void __launch_bounds__(NT) k_chain(const DeltaArgs a) {
+    after_previous();
     extern __shared__ float sm[];
     const ChainSizes z = chain_sizes(a.K);
     const int KP = z.KP, KL = z.KL;
@@ -397,6 +407,7 @@ constexpr int GRADS_FLOATS = 2 * 64 * MLD + 4 * 64 * LD + DGATES + 5 * 64 + 64 +
 
 template <typename T>
 __global__ void __launch_bounds__(NT) k_grads(const DeltaArgs a) {
+    after_previous();
     extern __shared__ float sm[];
     float *E = sm, *F = E + 64 * MLD, *s0 = F + 64 * MLD, *s1 = s0 + 64 * LD, *s2 = s1 + 64 * LD, *s3 = s2 + 64 * LD;
     float *gate = s3 + 64 * LD, *R = gate + DGATES, *X = R + 64, *flow = X + 64, *fg = flow + 64, *fd = fg + 64, *fl = fd + 64, *red = fl + 64;
@@ -441,23 +452,7 @@ __global__ void __launch_bounds__(NT) k_grads(const DeltaArgs a) {
                 const int v = v0 + 2 * tx + e, i = 16 * r + ty;
                 if (v < a.V) db[r] = fmaf(mu[(int64_t)i * a.V + v], U[(int64_t)i * a.V + v], db[r]);
             }
-#pragma unroll 4
-        for (int l = 0; l < 32; ++l) {
-            float x[4], y[4], w[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                x[r] = s1[(16 * r + ty) * LD + l];
-                y[r] = s2[(16 * r + ty) * LD + l];
-                w[r] = s0[(16 * r + tx) * LD + l];
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    lw[r][s] = fmaf(x[r], w[s], lw[r][s]);
-                    ow[r][s] = fmaf(y[r], w[s], ow[r][s]);
-                }
-        }
+        mul_rows(lw, ow, s1, s2, s0, ty, tx);
     }
     // F, E, and what crosses the tokens: W_ij = F_ij q_i.k_j + E_ij k_i.k_j below the diagonal
     float W[4][4];
@@ -593,6 +588,7 @@ __global__ void __launch_bounds__(NT) k_grads(const DeltaArgs a) {
 // dq and dk of a group: the sum over its heads, in their order
 template <typename T>
 __global__ void __launch_bounds__(NT) k_share(const DeltaArgs a) {
+    after_previous();
     const int slot = blockIdx.x / a.G, grp = blockIdx.x % a.G, per = a.H / a.G;
     const DeltaChunk c = delta_chunk(a, slot);
     T *dqp = static_cast<T *>(a.dq) + c.b * a.dqs[0] + c.t0 * a.dqs[1] + grp * a.dqs[2];
@@ -616,33 +612,26 @@ cudaError_t chain(const DeltaArgs &a, cudaStream_t st) {
     static int set[64] = {};
     const int bytes = chain_sizes(a.K).bytes;
     if (cudaError_t e = ensure_smem_attr(k_chain<T, BACK>, bytes, set); e != cudaSuccess) return e;
-    k_chain<T, BACK><<<(unsigned)(a.nseqs * (int64_t)a.H * ((a.V + VS - 1) / VS)), NT, bytes, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(k_chain<T, BACK>, (unsigned)(a.nseqs * (int64_t)a.H * ((a.V + VS - 1) / VS)), NT, bytes, st, a);
 }
 
 template <typename T>
 cudaError_t fwd(const DeltaArgs &a, cudaStream_t st) {
-    if (a.nslots > 0) {
-        k_prep<T><<<(unsigned)((int64_t)a.nslots * a.H), NT, 0, st>>>(a, false);
-        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-    }
+    if (a.nslots > 0)
+        if (cudaError_t e = launch_early(k_prep<T>, (unsigned)((int64_t)a.nslots * a.H), NT, 0, st, a, false); e != cudaSuccess) return e;
     return chain<T, false>(a, st);
 }
 template <typename T>
 cudaError_t bwd(const DeltaArgs &a, cudaStream_t st) {
-    if (a.nslots > 0) {
-        k_prep<T><<<(unsigned)((int64_t)a.nslots * a.H), NT, 0, st>>>(a, true);
-        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-    }
+    if (a.nslots > 0)
+        if (cudaError_t e = launch_early(k_prep<T>, (unsigned)((int64_t)a.nslots * a.H), NT, 0, st, a, true); e != cudaSuccess) return e;
     if (cudaError_t e = chain<T, true>(a, st); e != cudaSuccess) return e;
     if (a.nslots == 0) return cudaSuccess;
     static int set[64] = {};
     const int bytes = GRADS_FLOATS * (int)sizeof(float);
     if (cudaError_t e = ensure_smem_attr(k_grads<T>, bytes, set); e != cudaSuccess) return e;
-    k_grads<T><<<(unsigned)((int64_t)a.nslots * a.H), NT, bytes, st>>>(a);
-    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess || a.part == nullptr) return e;
-    k_share<T><<<(unsigned)((int64_t)a.nslots * a.G), NT, 0, st>>>(a);
-    return cudaGetLastError();
+    if (cudaError_t e = launch_early(k_grads<T>, (unsigned)((int64_t)a.nslots * a.H), NT, bytes, st, a); e != cudaSuccess || a.part == nullptr) return e;
+    return launch_early(k_share<T>, (unsigned)((int64_t)a.nslots * a.G), NT, 0, st, a);
 }
 
 }  // namespace

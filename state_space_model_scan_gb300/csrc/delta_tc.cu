@@ -32,7 +32,7 @@ using namespace dtc;
 
 // ---------------------------------------------------------------------------------------- the chunk's matrices
 constexpr int PREP_NT = 128;
-constexpr int MLD = 68;                 // rows of 16-byte pieces, four banks apart
+constexpr int MLD = DELTA_ML;
 // K's and Q's rows; once their product is out, the system and scratch lie over them
 constexpr uint32_t P_A = 0, P_M = 0, P_T = 64 * MLD * 4, P_GATE = 4 * HALF, P_COLS = P_GATE + GATE_BYTES, P_MISC = P_COLS + 2 * DQ * 4, P_BYTES = P_MISC + 64 + 1024;
 
@@ -40,68 +40,6 @@ constexpr uint32_t P_A = 0, P_M = 0, P_T = 64 * MLD * 4, P_GATE = 4 * HALF, P_CO
 __device__ __forceinline__ float decay_of(float hi_i, float lo_i, float hi_j, float lo_j) {
     return ex2f(kLog2e * ((hi_i - hi_j) + (lo_i - lo_j)));
 }
-// Inverse of I + M, M strictly lower triangular 64 x 64, in place (rows MLD apart), by 128 threads, as delta_invert does it: blocks of
-// 16 on the diagonal by substitution, then twice the block below the diagonal of a pair, a thread four neighbouring columns of a
-// row.  The blocks above the diagonal are neither read nor written.
-__device__ __forceinline__ void invert(float *M, float *t, int tid) {
-    if (tid < 64) {
-        const int o = tid / 16 * 16, j = tid & 15;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s = i == j ? 1.f : 0.f;
-#pragma unroll
-            for (int l = 0; l < i; l += 4) {
-                const float4 m = *reinterpret_cast<const float4 *>(M + (o + i) * MLD + o + l);
-                s = fmaf(-m.x, x[l], s);
-                if (l + 1 < i) s = fmaf(-m.y, x[l + 1], s);
-                if (l + 2 < i) s = fmaf(-m.z, x[l + 2], s);
-                if (l + 3 < i) s = fmaf(-m.w, x[l + 3], s);
-            }
-            x[i] = s;
-        }
-        __syncwarp();                                        // a block's sixteen threads are in one warp
-#pragma unroll
-        for (int i = 0; i < 16; ++i) M[(o + i) * MLD + o + j] = x[i];
-    }
-    {                                                        // the blocks of 16 above a pair's diagonal: zeros, for the pair of 32
-        const int o = tid / 64 * 32;
-        *reinterpret_cast<float4 *>(M + (o + tid % 64 / 4) * MLD + o + 16 + tid % 4 * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int n = 16; n <= 32; n *= 2) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {               // t = M21 T11, then M21 = -T22 t
-#pragma unroll 1
-            for (int k = 0; k < n / 16; ++k) {
-                const int it = tid + k * PREP_NT, per = n * n / 4, p = it / per, i = it % per / (n / 4), j = it % (n / 4) * 4, o = p * 2 * n;
-                f32x2 s0 = 0, s1 = 0;
-                const float *A = M + (o + n + i) * MLD + o + (half ? n : 0), *B = half ? t + p * n * 36 + j : M + o * MLD + o + j;
-                const int ldb = half ? 36 : MLD;
-#pragma unroll 2
-                for (int l = 0; l < n; l += 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(A + l);
-                    const float xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(B + (l + e) * ldb);
-                        const f32x2 xx = pk2(xs[e], xs[e]);
-                        s0 = fma2(xx, y.x, s0);
-                        s1 = fma2(xx, y.y, s1);
-                    }
-                }
-                float4 r;
-                up2(s0, r.x, r.y);
-                up2(s1, r.z, r.w);
-                if (half) *reinterpret_cast<float4 *>(M + (o + n + i) * MLD + o + j) = make_float4(-r.x, -r.y, -r.z, -r.w);
-                else *reinterpret_cast<float4 *>(t + (p * n + i) * 36 + j) = r;
-            }
-            __syncthreads();
-        }
-    }
-}
-
 // a block a chunk and head
 template <bool BACK>
 __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __grid_constant__ DeltaMaps m) {
@@ -220,7 +158,7 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
         tc_fence_after();
         tmem_dealloc(tmem, 64);
     }
-    invert(M, T, tid);
+    delta_invert<PREP_NT>(M, T, tid);
     // rows of the right operand: N index n, K index k; backwards the transposed inverse
     const int n = tid >> 1;
 #pragma unroll

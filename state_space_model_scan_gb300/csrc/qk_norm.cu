@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(QK_NT, V <= 8 ? 4 : 2) k_qk_fwd(const QkArgs a
 
 template <typename T, int V, bool INTER, int HB>
 __global__ void __launch_bounds__(QK_NT, V <= 8 ? 3 : 2) k_qk_bwd(const QkArgs a) {
+    after_previous();
     __shared__ float sum[QK_NT * V];
     const bool keys = blockIdx.x >= a.blocks0;
     const QkSide &s = a.side[keys];
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(QK_NT, V <= 8 ? 3 : 2) k_qk_bwd(const QkArgs a
 // ---- any shape and address: a warp a head's vector, features 32 apart, the rotation through shared memory.
 template <typename T, bool BACK>
 __global__ void __launch_bounds__(QK_NT) k_qk_any(const QkArgs a) {
+    after_previous();
     __shared__ float rows[QK_NT / 32][QK_MAXD], grads[BACK ? QK_NT / 32 : 1][QK_MAXD];
     const bool keys = blockIdx.x >= a.blocks0;
     const QkSide &s = a.side[keys];
@@ -356,6 +358,7 @@ __global__ void __launch_bounds__(QK_NT) k_qk_any(const QkArgs a) {
 
 // sum of the blocks' shares: 32 features a block, 32 threads a feature
 __global__ void __launch_bounds__(1024) k_qk_dw(const QkArgs a) {
+    after_previous();
     __shared__ float part[32][33];
     const int per = (a.dim + 31) / 32, side = blockIdx.x / per, e = blockIdx.x % per * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
     const QkSide &s = a.side[side];
@@ -468,8 +471,7 @@ template <typename T, int V, bool INTER, int HB>
 cudaError_t launch(const QkArgs &a, bool back, cudaStream_t st) {
     const unsigned grid = (unsigned)(a.blocks0 + a.blocks1);
     if (!back) return launch_early(k_qk_fwd<T, V, INTER, HB>, grid, QK_NT, 0, st, a);
-    k_qk_bwd<T, V, INTER, HB><<<grid, QK_NT, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(k_qk_bwd<T, V, INTER, HB>, grid, QK_NT, 0, st, a);
 }
 template <typename T, int V>
 cudaError_t pick_hb(const QkArgs &a, int HB, bool back, cudaStream_t st) {
@@ -487,9 +489,7 @@ cudaError_t pick(const QkArgs &a, int V, int HB, bool back, cudaStream_t st) {
     constexpr int least = 16 / sizeof(T);
     if (V == 0) {
         const unsigned grid = (unsigned)(a.blocks0 + a.blocks1);
-        if (back) k_qk_any<T, true><<<grid, QK_NT, 0, st>>>(a);
-        else k_qk_any<T, false><<<grid, QK_NT, 0, st>>>(a);
-        return cudaGetLastError();
+        return back ? launch_early(k_qk_any<T, true>, grid, QK_NT, 0, st, a) : launch_early(k_qk_any<T, false>, grid, QK_NT, 0, st, a);
     }
     if (V == least) return pick_hb<T, least>(a, HB, back, st);
     if constexpr (least == 4) {
@@ -557,8 +557,7 @@ ssd_status ssd_qk_norm_bwd(const ssd_qk_problem *p, const ssd_qk_bwd_args *b, vo
     }
     cudaError_t e = p->dtype == SSD_BF16 ? pick<__nv_bfloat16>(a, V, HB, true, st) : pick<float>(a, V, HB, true, st);
     if (e == cudaSuccess && (dw[0] || dw[1])) {
-        k_qk_dw<<<2 * ((a.dim + 31) / 32), 1024, 0, st>>>(a);
-        e = cudaGetLastError();
+        e = launch_early(k_qk_dw, (unsigned)(2 * ((a.dim + 31) / 32)), 1024, 0, st, a);
     }
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
