@@ -76,86 +76,92 @@ struct QkRaw {
 #pragma unroll
         for (int e = 0; e < (int)(V * sizeof(T) / 4); ++e) w[e] = 0u;
     }
-    __device__ __forceinline__ void to(float (&f)[V]) const {
+    __device__ __forceinline__ void to(f32x2 (&f)[V / 2]) const {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            if constexpr (sizeof(T) == 4) f[e] = __uint_as_float(w[e]);
-            else f[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+        for (int e = 0; e < V / 2; ++e) {
+            if constexpr (sizeof(T) == 4) f[e] = pk2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+            else f[e] = pk2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
         }
     }
 };
 template <typename T, int V>
-__device__ __forceinline__ void qk_store(T *p, const float (&f)[V]) {
+__device__ __forceinline__ void qk_store(T *p, const f32x2 (&f)[V / 2]) {
+    float x[V];
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) up2(f[e], x[2 * e], x[2 * e + 1]);
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
         for (int c = 0; c < V / 8; ++c) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(f[8 * c + 2 * e], f[8 * c + 2 * e + 1]);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * c + 2 * e], x[8 * c + 2 * e + 1]);
                 w[e] = *reinterpret_cast<const uint32_t *>(&h);
             }
             reinterpret_cast<uint4 *>(p)[c] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     } else {
 #pragma unroll
-        for (int c = 0; c < V / 4; ++c) reinterpret_cast<float4 *>(p)[c] = make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
+        for (int c = 0; c < V / 4; ++c) reinterpret_cast<float4 *>(p)[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
     }
 }
 
-// The token's cosines and sines for a lane's features, the sines with the sign that the feature's partner gets.
-template <int V, bool INTER>
+// The token's rotation of a lane's features: feature e becomes c x_e + s x_partner (backwards, by the opposite angle, c x_e - s x_partner),
+// the sign of the sine with the feature.  The partner lies in another lane (its loaded registers are exchanged, before they are
+// unpacked) or, interleaved, is the neighbour.
+template <typename T, int V, bool INTER>
 struct QkTurn {
-    float c[INTER ? V / 2 : V], s[INTER ? V / 2 : V];
-    int from;                           // lane of the partners
-    bool on;
-    __device__ __forceinline__ void load(const QkArgs &a, int pos, int l, int lane) {
+    f32x2 c[V / 2], s[V / 2];
+    int from, pl;                       // lane of the partners, and its place in the group
+    __device__ __forceinline__ void load(const QkArgs &a, int pos, int l, int lane, bool back) {
         const int e0 = l * V;
-        on = e0 < 2 * a.half && pos >= 0;     // (a padding token's outputs are set to zero, and the table may be empty)
-        from = lane;
+        const bool on = e0 < 2 * a.half && pos >= 0;         // (a padding token's outputs are set to zero, and the table may be empty)
         const int64_t row = (int64_t)pos * a.half;
+        from = lane;
+        pl = l;
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+            c[e] = pk2(1.f, 1.f);
+            s[e] = 0;
+        }
+        if (!on) return;
         if constexpr (INTER) {
 #pragma unroll
             for (int e = 0; e < V / 2; ++e) {
-                c[e] = on ? a.cos[row + e0 / 2 + e] : 1.f;
-                s[e] = on ? a.sin[row + e0 / 2 + e] : 0.f;
+                const float x = a.cos[row + e0 / 2 + e], y = a.sin[row + e0 / 2 + e];
+                c[e] = pk2(x, x);
+                s[e] = back ? pk2(y, -y) : pk2(-y, y);
             }
         } else {
             const bool second = e0 >= a.half;
             const int i = second ? e0 - a.half : e0;
-            if (on) {
-                from = second ? lane - a.half / V : lane + a.half / V;
+            pl = second ? l - a.half / V : l + a.half / V;
+            from = lane + pl - l;
+            const float sign = second != back ? 1.f : -1.f;
 #pragma unroll
-                for (int e = 0; e < V; e += 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(a.cos + row + i + e), y = *reinterpret_cast<const float4 *>(a.sin + row + i + e);
-                    c[e] = x.x; c[e + 1] = x.y; c[e + 2] = x.z; c[e + 3] = x.w;
-                    s[e] = y.x; s[e + 1] = y.y; s[e + 2] = y.z; s[e + 3] = y.w;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) { c[e] = 1.f; s[e] = 0.f; }
+            for (int e = 0; e < V; e += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(a.cos + row + i + e), y = *reinterpret_cast<const float4 *>(a.sin + row + i + e);
+                c[e / 2] = pk2(x.x, x.y);
+                c[e / 2 + 1] = pk2(x.z, x.w);
+                s[e / 2] = mul2(pk2(sign, sign), pk2(y.x, y.y));
+                s[e / 2 + 1] = mul2(pk2(sign, sign), pk2(y.z, y.w));
             }
-#pragma unroll
-            for (int e = 0; e < V; ++e) s[e] = second ? s[e] : -s[e];
         }
     }
-    // BACK: by the opposite angle
-    template <bool BACK>
-    __device__ __forceinline__ void turn(float (&x)[V], int half) const {
-        if (half == 0) return;
+    // the partners of a row's features
+    __device__ __forceinline__ void partners(const QkRaw<T, V> &x, const f32x2 (&f)[V / 2], f32x2 (&p)[V / 2]) const {
         if constexpr (INTER) {
 #pragma unroll
             for (int e = 0; e < V / 2; ++e) {
-                const float p = x[2 * e], q = x[2 * e + 1], sn = BACK ? -s[e] : s[e];
-                x[2 * e] = p * c[e] - q * sn;
-                x[2 * e + 1] = p * sn + q * c[e];
+                float u, v;
+                up2(f[e], u, v);
+                p[e] = pk2(v, u);
             }
         } else {
+            QkRaw<T, V> y;
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float p = __shfl_sync(0xffffffffu, x[e], from);
-                x[e] = x[e] * c[e] + p * (BACK ? -s[e] : s[e]);
-            }
+            for (int e = 0; e < (int)(V * sizeof(T) / 4); ++e) y.w[e] = __shfl_sync(0xffffffffu, x.w[e], from);
+            y.to(p);
         }
     }
 };
@@ -166,19 +172,21 @@ __device__ __forceinline__ float qk_group(float v, int lpr) {
 }
 
 template <int V>
-__device__ __forceinline__ void qk_weight(float (&w)[V], const float *p, bool in) {
+__device__ __forceinline__ void qk_weight(f32x2 (&w)[V / 2], const float *p, bool in) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) w[e] = 1.f;
+    for (int e = 0; e < V / 2; ++e) w[e] = pk2(1.f, 1.f);
     if (p && in)
 #pragma unroll
         for (int e = 0; e < V; e += 4) {
             const float4 u = *reinterpret_cast<const float4 *>(p + e);
-            w[e] = u.x; w[e + 1] = u.y; w[e + 2] = u.z; w[e + 3] = u.w;
+            w[e / 2] = pk2(u.x, u.y);
+            w[e / 2 + 1] = pk2(u.z, u.w);
         }
 }
 
+// y = rstd (c w x + s w' x'), x' and w' the partners': their factors are the token's
 template <typename T, int V, bool INTER, int HB>
-__global__ void __launch_bounds__(QK_NT, V <= 8 ? 4 : 2) k_qk_fwd(const QkArgs a) {
+__global__ void __launch_bounds__(QK_NT, V <= 8 ? 3 : 2) k_qk_fwd(const QkArgs a) {
     after_previous();
     const bool keys = blockIdx.x >= a.blocks0;
     const QkSide &s = a.side[keys];
@@ -190,29 +198,52 @@ __global__ void __launch_bounds__(QK_NT, V <= 8 ? 4 : 2) k_qk_fwd(const QkArgs a
     const T *x = static_cast<const T *>(s.x) + q.b * s.xs[0] + q.t * s.xs[1] + q.h0 * s.xs[2] + l * V;
     T *y = static_cast<T *>(s.y) + q.b * s.ys[0] + q.t * s.ys[1] + q.h0 * s.ys[2] + l * V;
     QkRaw<T, V> v[HB];
-    QkTurn<V, INTER> r;
+    QkTurn<T, V, INTER> r;
 #pragma unroll
     for (int u = 0; u < HB; ++u) {
         if (in && q.h0 + u < s.heads) v[u].load(x + u * s.xs[2]);
         else v[u].zero();
     }
-    if (a.half > 0) r.load(a, q.pos, l, lane);
-    float w[V];
+    if (a.half > 0) r.load(a, q.pos, l, lane, false);
+    f32x2 w[V / 2];
     qk_weight<V>(w, s.w ? s.w + l * V : nullptr, in);
+    if (a.half > 0) {
+        f32x2 wp[V / 2];
+        if constexpr (INTER) {
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+                float u, t;
+                up2(w[e], u, t);
+                wp[e] = pk2(t, u);
+            }
+        } else {
+            qk_weight<V>(wp, s.w ? s.w + r.pl * V : nullptr, in);
+        }
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+            w[e] = mul2(w[e], r.c[e]);
+            r.s[e] = mul2(wp[e], r.s[e]);
+        }
+    }
 #pragma unroll
     for (int u = 0; u < HB; ++u) {
-        float f[V], m = 0.f;
+        f32x2 f[V / 2], m = 0;
         v[u].to(f);
 #pragma unroll
-        for (int e = 0; e < V; ++e) m = fmaf(f[e], f[e], m);
-        m = qk_group(m, a.lpr);
-        const float rstd = rsqrtf(fmaf(m, a.inv, a.eps));
+        for (int e = 0; e < V / 2; ++e) m = fma2(f[e], f[e], m);
+        float rstd = rsqrtf(fmaf(qk_group(sum2(m), a.lpr), a.inv, a.eps));
+        if (a.half > 0) {
+            f32x2 p[V / 2];
+            r.partners(v[u], f, p);
 #pragma unroll
-        for (int e = 0; e < V; ++e) f[e] = f[e] * rstd * w[e];
-        r.template turn<false>(f, a.half);
-        if (q.pos < 0)
+            for (int e = 0; e < V / 2; ++e) f[e] = fma2(r.s[e], p[e], mul2(w[e], f[e]));
+        } else {
 #pragma unroll
-            for (int e = 0; e < V; ++e) f[e] = 0.f;
+            for (int e = 0; e < V / 2; ++e) f[e] = mul2(w[e], f[e]);
+        }
+        const f32x2 rr = pk2(rstd, rstd);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) f[e] = q.pos < 0 ? 0 : mul2(rr, f[e]);
         if (live && in && q.h0 + u < s.heads) qk_store<T, V>(y + u * s.ys[2], f);
     }
 }
@@ -226,10 +257,10 @@ __global__ void __launch_bounds__(QK_NT, V <= 8 ? 3 : 2) k_qk_bwd(const QkArgs a
     const int lane = threadIdx.x & 31, l = lane & (a.lpr - 1), gpb = QK_NT / a.lpr, grp = threadIdx.x / a.lpr;
     const int nb = keys ? a.blocks1 : a.blocks0, bi = blockIdx.x - (keys ? a.blocks0 : 0);
     const bool in = l * V < a.dim;
-    float w[V], acc[V];
+    f32x2 w[V / 2], acc[V / 2];
     qk_weight<V>(w, s.w ? s.w + l * V : nullptr, in);
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    for (int e = 0; e < V / 2; ++e) acc[e] = 0;
     for (uint32_t first = (uint32_t)bi * gpb; first < s.items; first += (uint32_t)nb * gpb) {
         const bool live = first + grp < s.items;
         const QkAt q = qk_at(a, s, live ? first + grp : s.items - 1, HB);
@@ -237,7 +268,7 @@ __global__ void __launch_bounds__(QK_NT, V <= 8 ? 3 : 2) k_qk_bwd(const QkArgs a
         const T *dy = static_cast<const T *>(s.dy) + q.b * s.dys[0] + q.t * s.dys[1] + q.h0 * s.dys[2] + l * V;
         T *dx = static_cast<T *>(s.y) + q.b * s.ys[0] + q.t * s.ys[1] + q.h0 * s.ys[2] + l * V;
         QkRaw<T, V> xr[HB], dr[HB];
-        QkTurn<V, INTER> r;
+        QkTurn<T, V, INTER> r;
 #pragma unroll
         for (int u = 0; u < HB; ++u) {
             if (live && in && q.pos >= 0 && q.h0 + u < s.heads) {
@@ -248,34 +279,40 @@ __global__ void __launch_bounds__(QK_NT, V <= 8 ? 3 : 2) k_qk_bwd(const QkArgs a
                 dr[u].zero();
             }
         }
-        if (a.half > 0) r.load(a, q.pos, l, lane);
+        if (a.half > 0) r.load(a, q.pos, l, lane, true);
 #pragma unroll
         for (int u = 0; u < HB; ++u) {
-            float xv[V], dv[V], m = 0.f, d = 0.f;
+            f32x2 xv[V / 2], dv[V / 2], m = 0, d2 = 0;
             xr[u].to(xv);
             dr[u].to(dv);
 #pragma unroll
-            for (int e = 0; e < V; ++e) m = fmaf(xv[e], xv[e], m);
-            m = qk_group(m, a.lpr);
+            for (int e = 0; e < V / 2; ++e) m = fma2(xv[e], xv[e], m);
             // (a vector that is not there: rstd could be infinite with eps 0)
-            const float rstd = live && q.pos >= 0 && q.h0 + u < s.heads ? rsqrtf(fmaf(m, a.inv, a.eps)) : 0.f;
-            r.template turn<true>(dv, a.half);
+            const float power = fmaf(qk_group(sum2(m), a.lpr), a.inv, a.eps), rstd = live && q.pos >= 0 && q.h0 + u < s.heads ? rsqrtf(power) : 0.f;
+            if (a.half > 0) {
+                f32x2 p[V / 2];
+                r.partners(dr[u], dv, p);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                xv[e] *= rstd;
-                acc[e] = fmaf(dv[e], xv[e], acc[e]);
-                dv[e] *= w[e];
-                d = fmaf(dv[e], xv[e], d);
+                for (int e = 0; e < V / 2; ++e) dv[e] = fma2(r.s[e], p[e], mul2(r.c[e], dv[e]));
             }
-            d = qk_group(d, a.lpr) * a.inv;
+            const f32x2 rr = pk2(rstd, rstd);
 #pragma unroll
-            for (int e = 0; e < V; ++e) dv[e] = rstd * fmaf(-d, xv[e], dv[e]);
+            for (int e = 0; e < V / 2; ++e) {
+                xv[e] = mul2(rr, xv[e]);
+                acc[e] = fma2(dv[e], xv[e], acc[e]);
+                dv[e] = mul2(w[e], dv[e]);
+                d2 = fma2(dv[e], xv[e], d2);
+            }
+            const float d = -qk_group(sum2(d2), a.lpr) * a.inv;
+            const f32x2 dd = pk2(d, d);
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) dv[e] = mul2(rr, fma2(dd, xv[e], dv[e]));
             if (live && in && q.h0 + u < s.heads) qk_store<T, V>(dx + u * s.ys[2], dv);
         }
     }
     if (!s.share) return;
 #pragma unroll
-    for (int e = 0; e < V; ++e) sum[(grp * a.lpr + l) * V + e] = acc[e];
+    for (int e = 0; e < V / 2; ++e) up2(acc[e], sum[(grp * a.lpr + l) * V + 2 * e], sum[(grp * a.lpr + l) * V + 2 * e + 1]);
     __syncthreads();
     for (int e = threadIdx.x; e < a.dim; e += QK_NT) {
         float t = 0.f;
@@ -439,11 +476,10 @@ QkArgs make(const ssd_qk_problem *p, const ssd_qk_args *f, const ssd_tensor &yq,
         }
     }
     if (!vec) *V = 0;
-    // Heads of an item: 128 bytes of them on the way to a lane (64 backwards, of x and of dy) where that still fills the card, two where
-    // few tokens come.
-    const bool back = dyq != nullptr;
+    // Heads of an item: 128 bytes of them on the way to a lane (backwards 64 of x and of dy each) where that still fills the card, two where
+    // few tokens come.  8192 tokens x 40 heads of 128: 4 / 8 heads 39.2 / 35.3 us; backwards 4096 tokens 32.7 / 48.6.
     const int64_t lanes = tokens * (p->q_heads + p->k_heads) * p->dim / (*V ? *V : 16);
-    const int many = (back ? 64 : 128) / ((*V ? *V : 16) * (p->dtype == SSD_BF16 ? 2 : 4));
+    const int many = (dyq != nullptr ? 64 : 128) / ((*V ? *V : 16) * (p->dtype == SSD_BF16 ? 2 : 4));
     *HB = *V && many > QK_HB_MIN && lanes / many >= 2 * kSMs * QK_NT ? many : QK_HB_MIN;
     for (int i = 0; i < 2; ++i) {
         a.side[i].per = (int)((heads[i] + *HB - 1) / *HB);
