@@ -70,9 +70,10 @@ ssd_status check_inputs(const ssd_delta_problem *p, const ssd_delta_args *a) {
 // The tensor-core path takes bf16 data of up to 128 values and keys; fp32 data is computed in fp32.
 bool on_tensor_cores(const ssd_delta_problem *p) { return p->dtype == SSD_BF16 && p->headdim <= 128 && p->dstate <= 128; }
 
-// What the forward keeps and the backward starts from: the state that enters each chunk, and U.
+// What the forward keeps and the backward starts from: the state that enters each chunk, U, and on the tensor cores the chunks'
+// matrices.
 struct Kept {
-    size_t S, U, total;
+    size_t S, U, tiles, total;
 };
 size_t state_bytes(const ssd_delta_problem *p) { return on_tensor_cores(p) ? dtc::STATE_BYTES : (size_t)p->headdim * p->dstate * 4; }
 size_t value_bytes(const ssd_delta_problem *p) { return on_tensor_cores(p) ? dtc::VAL_BYTES : (size_t)DQ * p->headdim * 4; }
@@ -81,7 +82,8 @@ Kept kept_plan(const ssd_delta_problem *p) {
     Kept k;
     k.S = 0;
     k.U = up256(ch * state_bytes(p));
-    k.total = k.U + up256(ch * value_bytes(p));
+    k.tiles = k.U + up256(ch * value_bytes(p));
+    k.total = k.tiles + (on_tensor_cores(p) ? up256(ch * dtc::OPS_BOTH) : 0);
     return k;
 }
 struct Plan {
@@ -96,7 +98,7 @@ Plan plan(const ssd_delta_problem *p, bool back, bool kept) {
     auto take = [&](size_t n) { const size_t o = at; at += up256(n); return o; };
     w.hdr = take(HDR_WORDS * 4);
     if (tc) {
-        w.tiles = take(ch * dtc::OPS_BYTES);
+        w.tiles = take(back ? 0 : ch * dtc::OPS_BYTES);
         dtc::delta_segments(nstates(p), p->nheads, (p->seqlen + DQ - 1) / DQ, &w.nseg, &w.seglen);
         w.seg = take(2 * (size_t)(w.nseg - 1) * nstates(p) * p->nheads * dtc::SEG_BYTES);
     } else {
@@ -150,6 +152,10 @@ void set_kept(DeltaArgs &a, const ssd_delta_problem *p, void *at) {
     const Kept k = kept_plan(p);
     a.S = static_cast<uint8_t *>(at) + k.S;
     a.U = static_cast<uint8_t *>(at) + k.U;
+    if (on_tensor_cores(p)) {
+        a.tiles = static_cast<uint8_t *>(at) + k.tiles;
+        a.both = true;
+    }
 }
 ssd_status check_workspace(const void *ws, size_t bytes, size_t need) {
     if (need == 0) return SSD_OK;
@@ -234,6 +240,7 @@ ssd_status ssd_delta_bwd(const ssd_delta_problem *p, const ssd_delta_bwd_args *b
     cudaStream_t st = (cudaStream_t)stream;
     DeltaArgs a = make(p, f, w, ws);
     set_kept(a, p, kept ? f->chunk_states : ws + w.kept);
+    a.fresh = kept;
     if (!kept && p->seqlen > 0) DELTA_TRY(of_cuda(run_fwd(p, f, a, ssd_tensor{}, st)));
     a.dO = b->dO.ptr; set3(a.dos, b->dO);
     a.vo = aligned_rows(p, b->dO, p->nheads);

@@ -51,7 +51,8 @@ struct DeltaArgs {
     // [nslots][H][V][K] and [nslots][H][64][V] fp32, tensor-core path [nslots][H] operand images of 32 KB and [64][128] bf16
     void *S, *U, *dS, *mu;
     float *part;                // [2][nslots][H][64][K]: dq and dk of each value head, where heads share a group
-    void *tiles;                // tensor-core path: operand images of every chunk and head
+    void *tiles;                // tensor-core path: operand images of every chunk and head, `both` for a backward too
+    bool both, fresh;           // fresh: a backward's first launch clears the header
     // tensor-core path: a chain of few heads is cut into nseg segments of seglen chunks; a first launch leaves, for all but the last,
     // its end from a zero state [nseqs][H][nseg - 1][128][128] fp32 and what it makes of one (as two terms, 64 KB each)
     int nseg, seglen;

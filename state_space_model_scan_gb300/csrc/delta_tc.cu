@@ -13,7 +13,8 @@
 // What is carried (S, Y, e^(Gc - G) beta U, sys) enters a product as the sum of two bf16 values (2^-17), two or three products of
 // which the small ones are the cheaper price than tf32's single one of half the rate and 2^-11; what only leaves as bf16
 // (att, beta U in o) as one.
-// Backwards the same chain runs from the last chunk to the first (sys transposed, dS in S's place).
+// Backwards the same chain runs from the last chunk to the first, with dS in S's place and the transposed inverse in sys's: k_prep
+// leaves both for it, which come of one substitution, and nothing of the chunks is computed twice.
 //
 // Warps of a chain block: eight with two threads a lane, each half of the columns; four with one thread a lane for what is off
 // the chain; two that load the next chunk, one that stores; one thread that issues every product.  A product of 128 x 64 x 16 takes as long as one of 128 x 128 x 16 (64 cycles), so that K's and
@@ -34,20 +35,97 @@ using namespace dtc;
 constexpr int PREP_NT = 128;
 constexpr int MLD = DELTA_ML;
 // K's and Q's rows; once their product is out, the system and scratch lie over them
-constexpr uint32_t P_A = 0, P_M = 0, P_T = 64 * MLD * 4, P_GATE = 4 * HALF, P_COLS = P_GATE + GATE_BYTES, P_MISC = P_COLS + 2 * DQ * 4, P_BYTES = P_MISC + 64 + 1024;
+constexpr uint32_t P_A = 0, P_M = 0, P_T = 64 * MLD * 4, P_GATE = 4 * HALF, P_COLS = P_GATE + GATE_BYTES, P_MISC = P_COLS + DQ * 4, P_BYTES = P_MISC + 64 + 1024;
 
 // e^(G_i - G_j), as delta_decay, by the multi-function unit: off by 2^-22 and by 2^-24 of the exponent
 __device__ __forceinline__ float decay_of(float hi_i, float lo_i, float hi_j, float lo_j) {
     return ex2f(kLog2e * ((hi_i - hi_j) + (lo_i - lo_j)));
 }
+// X = (I + a B)^-1 a = a (I + B a)^-1 for a strictly lower triangular 64 x 64, B = diag(beta), in place (rows MLD apart), by PREP_NT
+// threads.  Both inverses that are needed are in it: (I + a B)^-1 = I - X B and (I + B a)^-1 = I - B X.  Blocks of 16 on the diagonal by
+// substitution, a thread a column; then twice the block below the diagonal of a pair, X21 = t - X22 B2 t with
+// t = a21 - a21 B1 X11, a thread four neighbouring columns of a row (T: 32 x 36 floats of scratch, for B2 t).  Blocks above the
+// diagonal: those in the pairs of 32 are set to zero, the other is neither read nor written.
+__device__ __forceinline__ void solve(float *M, float *T, const float *beta, int tid) {
+    if (tid < 64) {
+        const int o = tid / 16 * 16, j = tid & 15;
+        float x[16], xb[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i > j ? M[(o + i) * MLD + o + j] : 0.f;
+#pragma unroll
+            for (int l = 0; l < i; l += 4) {
+                const float4 m = *reinterpret_cast<const float4 *>(M + (o + i) * MLD + o + l);
+                s = fmaf(-m.x, xb[l], s);
+                if (l + 1 < i) s = fmaf(-m.y, xb[l + 1], s);
+                if (l + 2 < i) s = fmaf(-m.z, xb[l + 2], s);
+                if (l + 3 < i) s = fmaf(-m.w, xb[l + 3], s);
+            }
+            x[i] = s;
+            xb[i] = beta[o + i] * s;
+        }
+        __syncwarp();                                        // a block's sixteen threads are in one warp
+#pragma unroll
+        for (int i = 0; i < 16; ++i) M[(o + i) * MLD + o + j] = x[i];
+    }
+    {
+        const int o = tid / 64 * 32;
+        *reinterpret_cast<float4 *>(M + (o + tid % 64 / 4) * MLD + o + 16 + tid % 4 * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 16; n <= 32; n *= 2) {
+        float4 t[2];                                         // this thread's elements of t (two of them at n = 32)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int k = 0; k < n / 16; ++k) {
+                const int it = tid + k * PREP_NT, per = n * n / 4, p = it / per, i = it % per / (n / 4), j = it % (n / 4) * 4, o = p * 2 * n;
+                f32x2 s0 = 0, s1 = 0;
+                const float *A = M + (o + n + i) * MLD + o + (half ? n : 0), *B = half ? T + p * n * 36 + j : M + o * MLD + o + j;
+                const int ldb = half ? 36 : MLD;
+#pragma unroll 2
+                for (int l = 0; l < n; l += 4) {
+                    float4 x = *reinterpret_cast<const float4 *>(A + l);
+                    if (!half) {
+                        const float4 f = *reinterpret_cast<const float4 *>(beta + o + l);
+                        x.x *= f.x; x.y *= f.y; x.z *= f.z; x.w *= f.w;
+                    }
+                    const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(B + (l + e) * ldb);
+                        const f32x2 xx = pk2(xs[e], xs[e]);
+                        s0 = fma2(xx, y.x, s0);
+                        s1 = fma2(xx, y.y, s1);
+                    }
+                }
+                float4 r, *own = reinterpret_cast<float4 *>(M + (o + n + i) * MLD + o + j);
+                up2(s0, r.x, r.y);
+                up2(s1, r.z, r.w);
+                const float4 u = half ? t[k] : *own;
+                const float4 d = make_float4(u.x - r.x, u.y - r.y, u.z - r.z, u.w - r.w);
+                if (half) {
+                    *own = d;
+                } else {
+                    const float f = beta[o + n + i];
+                    t[k] = d;
+                    *reinterpret_cast<float4 *>(T + (p * n + i) * 36 + j) = make_float4(f * d.x, f * d.y, f * d.z, f * d.w);
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
 // a block a chunk and head
-template <bool BACK>
+template <bool BOTH>
 __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __grid_constant__ DeltaMaps m) {
     after_previous();
     extern __shared__ uint8_t raw[];
     uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     float *M = reinterpret_cast<float *>(sm + P_M), *T = reinterpret_cast<float *>(sm + P_T), *gate = reinterpret_cast<float *>(sm + P_GATE);
-    float *cols = reinterpret_cast<float *>(sm + P_COLS);   // e^(G_end - G_j), end the last token of j's block of 16; and times beta_j
+    float *cols = reinterpret_cast<float *>(sm + P_COLS);   // e^(G_end - G_j), end the last token of j's block of 16
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + P_MISC);
     uint32_t *tm = reinterpret_cast<uint32_t *>(sm + P_MISC + 16);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
@@ -87,12 +165,11 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
         for (int k = 0; k < 8; ++k) umma_bf16(tmem, kmaj(base, k, 2 * HALF), kmaj(base, k, 2 * HALF), idesc_bf16(128, 64, 0, 0), k > 0);
         umma_commit(bar + 1);
     }
-    uint8_t *ops = static_cast<uint8_t *>(a.tiles) + ((int64_t)slot * a.H + h) * OPS_BYTES;
+    uint8_t *ops = static_cast<uint8_t *>(a.tiles) + ((int64_t)slot * a.H + h) * (BOTH ? OPS_BOTH : OPS_BYTES);
     if (tid >= 64) {                                         // (warps 2 and 3: while the product runs)
         const int j = tid - 64, e = j | 15;
         const float f = decay_of(gate[3 * DQ + e], gate[4 * DQ + e], gate[3 * DQ + j], gate[4 * DQ + j]);
         cols[j] = f;
-        cols[DQ + j] = f * gate[2 * DQ + j];
     }
     for (int e = tid; e < DGATES / 4; e += PREP_NT) reinterpret_cast<float4 *>(ops + GATES)[e] = reinterpret_cast<const float4 *>(gate)[e];
     ok = mbar_wait(bar + 1, 0) && ok;
@@ -103,7 +180,7 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
     // diagonal every decay is an exponential of its own; left of it e^(G_i - G_j) is the product of one of the row
     // (from the end of j's block on) and one of the column (to that end), each at most 1.
     const int i = tid & 63, ib = i >> 4, nb = 2 * (w & 1) + 2;
-    const float ghi = gate[3 * DQ + i], glo = gate[4 * DQ + i], b = BACK && w < 2 ? gate[2 * DQ + i] : 1.f;
+    const float ghi = gate[3 * DQ + i], glo = gate[4 * DQ + i];
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb) {
         float x[16];
@@ -111,8 +188,8 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
             tmem_ld16(tmem + ((uint32_t)w << 21) + 16 * jb, x);
             tmem_wait_ld();
             if (jb < ib) {
-                const float f = b * decay_of(ghi, glo, gate[3 * DQ + 16 * jb + 15], gate[4 * DQ + 16 * jb + 15]);
-                const float *col = cols + (w < 2 && !BACK ? DQ : 0) + 16 * jb;
+                const float f = decay_of(ghi, glo, gate[3 * DQ + 16 * jb + 15], gate[4 * DQ + 16 * jb + 15]);
+                const float *col = cols + 16 * jb;
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     const float4 v = *reinterpret_cast<const float4 *>(col + e);
@@ -122,13 +199,11 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     const float4 h4 = *reinterpret_cast<const float4 *>(gate + 3 * DQ + 16 * jb + e), l4 = *reinterpret_cast<const float4 *>(gate + 4 * DQ + 16 * jb + e);
-                    const float4 b4 = *reinterpret_cast<const float4 *>(gate + 2 * DQ + 16 * jb + e);
-                    const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, ls[4] = {l4.x, l4.y, l4.z, l4.w}, bs[4] = {b4.x, b4.y, b4.z, b4.w};
+                    const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, ls[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
                     for (int d = 0; d < 4; ++d) {
                         const int j = 16 * jb + e + d;
-                        float f = b * decay_of(ghi, glo, hs[d], ls[d]) * x[e + d];
-                        if (!BACK && w < 2) f *= bs[d];
+                        const float f = decay_of(ghi, glo, hs[d], ls[d]) * x[e + d];
                         x[e + d] = (w < 2 ? j < i : j <= i) ? f : 0.f;
                     }
                 }
@@ -158,21 +233,35 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
         tc_fence_after();
         tmem_dealloc(tmem, 64);
     }
-    delta_invert<PREP_NT>(M, T, tid);
-    // rows of the right operand: N index n, K index k; backwards the transposed inverse
+    const float *beta = gate + 2 * DQ;
+    solve(M, T, beta, tid);
+    // rows of the right operands, N index n, K index k: (I + a B)^-1; and of the transposed (I + B a)^-1
     const int n = tid >> 1;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
         const int k0 = (tid & 1) * 32 + q * 8;
-        if (BACK ? k0 / 16 >= n / 16 : k0 / 16 <= n / 16) {
-#pragma unroll
-            for (int e = 0; e < 8; e += 2)
-                split2(BACK ? M[(k0 + e) * MLD + n] : M[n * MLD + k0 + e], BACK ? M[(k0 + e + 1) * MLD + n] : M[n * MLD + k0 + e + 1], hi[e / 2], lo[e / 2]);
-        }
         uint8_t *to = ops + n * 128 + (((k0 / 8) ^ (n & 7)) << 4);
+        if (k0 / 16 <= n / 16)
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(M + n * MLD + k0 + e), f = *reinterpret_cast<const float4 *>(beta + k0 + e);
+                split2((k0 + e == n ? 1.f : 0.f) - x.x * f.x, (k0 + e + 1 == n ? 1.f : 0.f) - x.y * f.y, hi[e / 2], lo[e / 2]);
+                split2((k0 + e + 2 == n ? 1.f : 0.f) - x.z * f.z, (k0 + e + 3 == n ? 1.f : 0.f) - x.w * f.w, hi[e / 2 + 1], lo[e / 2 + 1]);
+            }
         *reinterpret_cast<uint4 *>(to + SYS_HI) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4 *>(to + SYS_LO) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (BOTH) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) hi[e] = lo[e] = 0u;
+            if (k0 / 16 >= n / 16)
+#pragma unroll
+                for (int e = 0; e < 8; e += 2)
+                    split2((k0 + e == n ? 1.f : 0.f) - beta[k0 + e] * M[(k0 + e) * MLD + n], (k0 + e + 1 == n ? 1.f : 0.f) - beta[k0 + e + 1] * M[(k0 + e + 1) * MLD + n],
+                           hi[e / 2], lo[e / 2]);
+            *reinterpret_cast<uint4 *>(to + SYS_T) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(to + SYS_T + MAT_BYTES) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
     }
 }
 
@@ -272,6 +361,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
     const int units = a.nseqs * a.H, unit = blockIdx.x % units, part = blockIdx.x / units, s = unit / a.H, h = unit % a.H, grp = h / (a.H / a.G);
     const bool mat = ENDS && part >= a.nseg - 1;
     const int seg = mat ? part - (a.nseg - 1) + 1 : part;
+    if (BACK && a.fresh && (ENDS || a.nseg == 1) && blockIdx.x == 0 && tid < HDR_WORDS) a.hdr[tid] = 0;
     const DeltaSeq q = delta_seq(a, s);
     const int all = (q.len + DQ - 1) / DQ, c0 = seg * a.seglen;            // chunks of the sequence; the segment's first step
     if (ENDS ? c0 + a.seglen >= all : seg > 0 && c0 >= all) return;        // no segment follows; nothing in it
@@ -613,7 +703,13 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 mbar_expect_tx(bar, OPS_BYTES + (m.has_k + has_x + (m.has_q && outputs)) * TOK_BYTES);
                 if (m.has_k) tma_rows(st + ST_KQ, 2 * HALF, &m.k, bar, k, grp);
                 if (has_x) tma_rows(st + ST_X, HALF, mx, bar, k, h);
-                bulk_load(st + ST_OPS, static_cast<const uint8_t *>(a.tiles) + (((int64_t)q.slot0 + idx(c)) * a.H + h) * OPS_BYTES, OPS_BYTES, bar);
+                const uint8_t *ops = static_cast<const uint8_t *>(a.tiles) + (((int64_t)q.slot0 + idx(c)) * a.H + h) * (a.both ? OPS_BOTH : OPS_BYTES);
+                if (BACK) {                                  // the other inverse in its place
+                    bulk_load(st + ST_OPS, ops + SYS_T, 2 * MAT_BYTES, bar);
+                    bulk_load(st + ST_OPS + ATT, ops + ATT, OPS_BYTES - ATT, bar);
+                } else {
+                    bulk_load(st + ST_OPS, ops, OPS_BYTES, bar);
+                }
                 if (m.has_q && outputs) tma_rows(st + ST_KQ + HALF, 2 * HALF, &m.q, bar, k, grp);
             }
             if (!m.has_k) load_rows<CH_L>(st + ST_KQ, 2 * HALF, tok_rows(a.k, a.ks, k, grp), a.ks[1], k.len, a.K, t);
@@ -878,7 +974,7 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
             tma_rows(sm + G_U, HALF, &m.U, b, vals, (int)ch);
         } else if (one && w == 7) {
             mbar_expect_tx(b, GATE_BYTES + STATE_BYTES);
-            bulk_load(sm + G_GATE, static_cast<const uint8_t *>(a.tiles) + ch * OPS_BYTES + GATES, GATE_BYTES, b);
+            bulk_load(sm + G_GATE, static_cast<const uint8_t *>(a.tiles) + ch * OPS_BOTH + GATES, GATE_BYTES, b);
             bulk_load(sm + G_S, static_cast<const uint8_t *>(a.S) + ch * STATE_BYTES, STATE_BYTES, b);
         } else if (one && w == 10) {
             mbar_expect_tx(b, STATE_BYTES);
@@ -1143,11 +1239,11 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
     }
 }
 
-template <bool BACK>
+template <bool BOTH>
 cudaError_t prep(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
     static int set[64] = {};
-    if (cudaError_t e = ensure_smem_attr(k_prep<BACK>, (int)P_BYTES, set); e != cudaSuccess) return e;
-    return launch_early(k_prep<BACK>, (unsigned)((int64_t)a.nslots * a.H), PREP_NT, P_BYTES, st, a, m);
+    if (cudaError_t e = ensure_smem_attr(k_prep<BOTH>, (int)P_BYTES, set); e != cudaSuccess) return e;
+    return launch_early(k_prep<BOTH>, (unsigned)((int64_t)a.nslots * a.H), PREP_NT, P_BYTES, st, a, m);
 }
 template <bool BACK, bool KEEP, bool OUT, bool ENDS>
 cudaError_t launch_chain(const DeltaArgs &a, const DeltaMaps &m, int parts, cudaStream_t st) {
@@ -1188,12 +1284,11 @@ bool delta_map(CUtensorMap *m, const void *p, int64_t inner, int64_t heads, int6
 }
 
 cudaError_t delta_tc_fwd(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
-    if (cudaError_t e = prep<false>(a, m, st); e != cudaSuccess) return e;
+    if (cudaError_t e = a.both ? prep<true>(a, m, st) : prep<false>(a, m, st); e != cudaSuccess) return e;
     return a.S == nullptr ? chain<false, false, true>(a, m, st) : a.o != nullptr ? chain<false, true, true>(a, m, st) : chain<false, true, false>(a, m, st);
 }
 cudaError_t delta_tc_bwd(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
     if (!m.has_vals) return cudaErrorNotSupported;
-    if (cudaError_t e = prep<true>(a, m, st); e != cudaSuccess) return e;
     if (cudaError_t e = chain<true, true, true>(a, m, st); e != cudaSuccess) return e;
     static int set[64] = {};
     if (cudaError_t e = ensure_smem_attr(k_grads, (int)G_BYTES, set); e != cudaSuccess) return e;

@@ -16,8 +16,10 @@ constexpr uint32_t HALF = DQ * 128;              // 64 rows of 128 bytes
 constexpr uint32_t TOK_BYTES = 2 * HALF;         // 64 tokens x 128 features
 constexpr uint32_t MAT_BYTES = HALF;             // 64 x 64
 constexpr uint32_t GATE_BYTES = DGATES * 4;
-// per chunk and head: the inverse's two terms, att, gates (in the workspace one after the other, as they are loaded)
+// per chunk and head, one after the other as they are loaded: the inverse's two terms, att, gates; for a backward also the two terms of
+// the transposed inverse with beta on the other side
 constexpr uint32_t SYS_HI = 0, SYS_LO = MAT_BYTES, ATT = 2 * MAT_BYTES, GATES = 3 * MAT_BYTES, OPS_BYTES = GATES + GATE_BYTES;
+constexpr uint32_t SYS_T = OPS_BYTES, OPS_BOTH = OPS_BYTES + 2 * MAT_BYTES;
 constexpr uint32_t STATE_BYTES = 128 * 128 * 2;  // kept state: two images (keys 0..63, 64..127) of 128 rows (values)
 constexpr uint32_t VAL_BYTES = DQ * 128 * 2;     // kept U, and mu: [64][128], plain
 
