@@ -271,8 +271,8 @@ constexpr int CH_CW = 8, CH_EW = 4, CH_LW = 2, CH_NT = (CH_CW + CH_EW + CH_LW + 
 constexpr int CH_L = CH_LW * 32, CH_L0 = (CH_CW + CH_EW) * 32;
 // a stage: K and Q (two images of 128 rows: K's, Q's), V (backwards dO), operands
 constexpr uint32_t ST_KQ = 0, ST_X = 2 * TOK_BYTES, ST_OPS = 3 * TOK_BYTES, ST_BYTES = (ST_OPS + OPS_BYTES + 1023) / 1024 * 1024;
-// and two tiles [64][128], plain, that leave by bulk copies: o (backwards dV), U (mu); and a copy of e^G for each warp that computes o
-constexpr uint32_t CH_O = 2 * ST_BYTES, CH_V = CH_O + VAL_BYTES, CH_EG = CH_V + VAL_BYTES, CH_MISC = CH_EG + CH_EW * DQ * 4, CH_BYTES = CH_MISC + 256 + 1024;
+// and what leaves by bulk copies: two tiles [64][128], plain, of o (backwards dV) and U (mu), the state's image; and a copy of e^G for each warp that computes o
+constexpr uint32_t CH_O = 2 * ST_BYTES, CH_V = CH_O + VAL_BYTES, CH_S = CH_V + VAL_BYTES, CH_EG = CH_S + STATE_BYTES, CH_MISC = CH_EG + CH_EW * DQ * 4, CH_BYTES = CH_MISC + 256 + 1024;
 // TMEM columns.  A lane's columns of each belong to two threads, two of its quarters each, taken one after the other; a quarter of
 // an operand lies over the quarter that its thread has read, both terms one after the other.
 //   S   state (its operand; then what is added to it)
@@ -289,7 +289,7 @@ struct Cols {
 // Barriers.  A wait tells the completions of a barrier apart by their parity: nothing completes twice before every waiter has seen the
 // first, because a waiter's own next step is needed for the second; where that is two steps off there is one barrier
 // for even chunks and one for odd.
-enum { B_FULL0, B_FULL1, B_TMA0, B_TMA1, B_O0, B_O1, B_WO0, B_WO1, B_EG0, B_EG1, B_P, B_U, B_S, B_END, B_AF, B_WV, B_FO, B_FV, B_JM0, B_JM1, B_JD,
+enum { B_FULL0, B_FULL1, B_TMA0, B_TMA1, B_O0, B_O1, B_WO0, B_WO1, B_EG0, B_EG1, B_P, B_U, B_S, B_END, B_AF, B_WV, B_WS, B_FO, B_FV, B_FS, B_JM0, B_JM1, B_JD,
        B_AY, B_AW = B_AY + 2, B_AS = B_AW + 2, NB = B_AS + 2 };   // (one for each thread's first quarter, one for its second)
 
 // a column of 16 tokens of one value, two to a register, into a plain tile
@@ -368,8 +368,8 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
     const int n = min(a.seglen, all - c0), joins = ENDS ? 0 : max(0, seg - 1);
     if (tid == 0) {
         for (int b : {B_FULL0, B_FULL1}) mbar_init(&ms->bar[b], CH_LW);
-        for (int b : {B_TMA0, B_TMA1, B_O0, B_O1, B_P, B_U, B_S, B_END, B_FO, B_FV, B_JM0, B_JM1, B_JD}) mbar_init(&ms->bar[b], 1);
-        mbar_init(&ms->bar[B_WV], CH_CW);
+        for (int b : {B_TMA0, B_TMA1, B_O0, B_O1, B_P, B_U, B_S, B_END, B_FO, B_FV, B_FS, B_JM0, B_JM1, B_JD}) mbar_init(&ms->bar[b], 1);
+        for (int b : {B_WV, B_WS}) mbar_init(&ms->bar[b], CH_CW);
         for (int b = B_AY; b < NB; ++b) mbar_init(&ms->bar[b], CH_CW);
         for (int b : {B_AF, B_EG0, B_EG1}) mbar_init(&ms->bar[b], CH_EW);
         for (int b : {B_WO0, B_WO1}) mbar_init(&ms->bar[b], BACK ? CH_CW : CH_EW);
@@ -426,7 +426,6 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 S[e] = pk2(x, y);
             }
         }
-        uint8_t *kept = static_cast<uint8_t *>(BACK ? a.dS : a.S);
         // quarter 2 hf + g of the state as chunk c's operand, and kept as the state that enters it (backwards: whose gradient leaves it)
         auto publish = [&](int c, int g, bool keep) {
             uint32_t hi[16];
@@ -444,10 +443,15 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
             tmem_wait_st();
             arrive(B_AS + g);
             if (KEEP && keep) {
-                uint8_t *to = kept + (((int64_t)q.slot0 + idx(c)) * a.H + h) * STATE_BYTES + hf * (STATE_BYTES / 2) + v * 128;
+                if (g == 0 && c > 0) wait(B_FS, c - 1);
+                uint8_t *to = sm + CH_S + hf * (STATE_BYTES / 2) + v * 128;
 #pragma unroll
                 for (int p = 0; p < 4; ++p)
                     *reinterpret_cast<uint4 *>(to + (((4 * g + p) ^ (v & 7)) << 4)) = make_uint4(hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
+                if (g == 1) {
+                    fence_proxy_async_smem();
+                    arrive(B_WS);
+                }
             }
         };
         // the state that enters the segment: from segment to segment S <- S M + end
@@ -750,10 +754,15 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
     } else if (w == CH_CW + CH_EW + CH_LW) {
         // ------------------------------------------------------------ tiles that leave
         if (lane == 0) {
-            uint8_t *vals = static_cast<uint8_t *>(BACK ? a.mu : a.U);
+            uint8_t *vals = static_cast<uint8_t *>(BACK ? a.mu : a.U), *kept = static_cast<uint8_t *>(BACK ? a.dS : a.S);
             for (int c = 0; c < n; ++c) {
                 const int ci = idx(c);
                 if (KEEP) {
+                    if (!wait(B_WS, c)) break;
+                    bulk_store(kept + (((int64_t)q.slot0 + ci) * a.H + h) * STATE_BYTES, sm + CH_S, STATE_BYTES);
+                    bulk_commit();
+                    bulk_wait_read0();
+                    mbar_arrive(&ms->bar[B_FS]);
                     if (!wait(B_WV, c)) break;
                     bulk_store(vals + (((int64_t)q.slot0 + ci) * a.H + h) * VAL_BYTES, sm + CH_V, VAL_BYTES);
                     bulk_commit();
