@@ -377,6 +377,12 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         fence_mbar_init();
     }
     if (w == 0) tmem_alloc(&ms->tmem, 512);
+    if (tid == CH_L0) {
+        prefetch_tmap(&m.k);
+        prefetch_tmap(BACK ? &m.dO : &m.v);
+        prefetch_tmap(&m.q);
+        if (OUT) prefetch_tmap(&m.out);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -418,12 +424,28 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         } else {
             const void *in = BACK ? a.dfinal : a.init;
             const bool f32 = BACK ? !a.dfinal_bf16 : !a.init_bf16;
+            const bool wide = (a.K & 7) == 0 && (reinterpret_cast<uintptr_t>(in) & 15) == 0;   // rows in pieces of 16 bytes
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 32; e += 4) {                // eight keys
                 const int k = 64 * hf + 2 * e;
-                const float x = in && mine && k < a.K ? delta_ld(in, f32, row + 2 * e) : 0.f;
-                const float y = in && mine && k + 1 < a.K ? delta_ld(in, f32, row + 2 * e + 1) : 0.f;
-                S[e] = pk2(x, y);
+                if (in && mine && wide && k < a.K) {
+                    if (f32) {
+                        const ulonglong2 x = reinterpret_cast<const ulonglong2 *>(static_cast<const float *>(in) + row + 2 * e)[0];
+                        const ulonglong2 y = reinterpret_cast<const ulonglong2 *>(static_cast<const float *>(in) + row + 2 * e)[1];
+                        S[e] = x.x; S[e + 1] = x.y; S[e + 2] = y.x; S[e + 3] = y.y;
+                    } else {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(in) + row + 2 * e);
+                        S[e] = pk2(bf_lo(x.x), bf_hi(x.x)); S[e + 1] = pk2(bf_lo(x.y), bf_hi(x.y));
+                        S[e + 2] = pk2(bf_lo(x.z), bf_hi(x.z)); S[e + 3] = pk2(bf_lo(x.w), bf_hi(x.w));
+                    }
+                } else {
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const float x = in && mine && k + 2 * d < a.K ? delta_ld(in, f32, row + 2 * (e + d)) : 0.f;
+                        const float y = in && mine && k + 2 * d + 1 < a.K ? delta_ld(in, f32, row + 2 * (e + d) + 1) : 0.f;
+                        S[e + d] = pk2(x, y);
+                    }
+                }
             }
         }
         // quarter 2 hf + g of the state as chunk c's operand, and kept as the state that enters it (backwards: whose gradient leaves it)
@@ -606,14 +628,35 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 *reinterpret_cast<uint4 *>(to + STATE_BYTES + ((p ^ (v & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
         }
+        const bool wide = (a.K & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
         if (out && mine)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 32; e += 4) {
                 const int k = 64 * hf + 2 * e;
-                float x, y;
-                up2(S[e], x, y);
-                if (k < a.K) delta_st(out, f32, row + 2 * e, x);
-                if (k + 1 < a.K) delta_st(out, f32, row + 2 * e + 1, y);
+                if (wide && k < a.K) {
+                    if (f32) {
+                        ulonglong2 *to = reinterpret_cast<ulonglong2 *>(static_cast<float *>(out) + row + 2 * e);
+                        to[0] = make_ulonglong2(S[e], S[e + 1]);
+                        to[1] = make_ulonglong2(S[e + 2], S[e + 3]);
+                    } else {
+                        uint32_t b2[4];
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            float x, y;
+                            up2(S[e + d], x, y);
+                            b2[d] = pack_bf16(x, y);
+                        }
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + row + 2 * e) = make_uint4(b2[0], b2[1], b2[2], b2[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        float x, y;
+                        up2(S[e + d], x, y);
+                        if (k + 2 * d < a.K) delta_st(out, f32, row + 2 * (e + d), x);
+                        if (k + 2 * d + 1 < a.K) delta_st(out, f32, row + 2 * (e + d) + 1, y);
+                    }
+                }
             }
         tc_fence_before();
     } else if (w < CH_CW + CH_EW) {
