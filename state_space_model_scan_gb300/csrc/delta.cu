@@ -88,7 +88,7 @@ Kept kept_plan(const ssd_delta_problem *p) {
 }
 struct Plan {
     size_t hdr, gates, sys, att, a, tiles, seg, dS, mu, part, kept, total;
-    int nseg, seglen;
+    int nseg, seg0, seglen;
 };
 Plan plan(const ssd_delta_problem *p, bool back, bool kept) {
     const size_t ch = (size_t)slots(p) * p->nheads, mat = ch * DQ * DQ * 4;
@@ -99,7 +99,7 @@ Plan plan(const ssd_delta_problem *p, bool back, bool kept) {
     w.hdr = take(HDR_WORDS * 4);
     if (tc) {
         w.tiles = take(back ? 0 : ch * dtc::OPS_BYTES);
-        dtc::delta_segments(nstates(p), p->nheads, (p->seqlen + DQ - 1) / DQ, &w.nseg, &w.seglen);
+        dtc::delta_segments(nstates(p), p->nheads, (p->seqlen + DQ - 1) / DQ, &w.nseg, &w.seg0, &w.seglen);
         w.seg = take(2 * (size_t)(w.nseg - 1) * nstates(p) * p->nheads * dtc::SEG_BYTES);
     } else {
         w.gates = take(ch * DGATES * 4);
@@ -139,7 +139,7 @@ DeltaArgs make(const ssd_delta_problem *p, const ssd_delta_args *f, const Plan &
     a.scale = p->scale;
     a.hdr = reinterpret_cast<int32_t *>(ws + w.hdr);
     a.tiles = ws + w.tiles;
-    a.nseg = w.nseg; a.seglen = w.seglen;
+    a.nseg = w.nseg; a.seg0 = w.seg0; a.seglen = w.seglen;
     a.segB = ws + w.seg;
     a.segM = ws + w.seg + (size_t)(w.nseg > 1 ? w.nseg - 1 : 0) * nstates(p) * p->nheads * dtc::SEG_BYTES;
     a.gates = reinterpret_cast<float *>(ws + w.gates);

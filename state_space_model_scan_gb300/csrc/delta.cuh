@@ -53,9 +53,10 @@ struct DeltaArgs {
     float *part;                // [2][nslots][H][64][K]: dq and dk of each value head, where heads share a group
     void *tiles;                // tensor-core path: operand images of every chunk and head, `both` for a backward too
     bool both, fresh;           // fresh: a backward's first launch clears the header
-    // tensor-core path: a chain of few heads is cut into nseg segments of seglen chunks; a first launch leaves, for all but the last,
-    // its end from a zero state [nseqs][H][nseg - 1][128][128] fp32 and what it makes of one (as two terms, 64 KB each)
-    int nseg, seglen;
+    // tensor-core path: a chain of few heads is cut into nseg segments (see delta_segments), the first of seg0 chunks, those between of
+    // seglen; a first launch leaves, for all but the last, the end from a zero state (the first's from its own) [nseqs][H][nseg - 1][128][128]
+    // fp32 and, for those between, what it makes of a state (as two terms, 64 KB each)
+    int nseg, seg0, seglen;
     void *segB, *segM;
 };
 

@@ -35,87 +35,123 @@ using namespace dtc;
 constexpr int PREP_NT = 128;
 constexpr int MLD = DELTA_ML;
 // K's and Q's rows; once their product is out, the system and scratch lie over them
-constexpr uint32_t P_A = 0, P_M = 0, P_T = 64 * MLD * 4, P_GATE = 4 * HALF, P_COLS = P_GATE + GATE_BYTES, P_MISC = P_COLS + DQ * 4, P_BYTES = P_MISC + 64 + 1024;
+constexpr int TLD = 40;         // of the scratch matrix: its columns are read four rows at a time, eight banks apart
+constexpr uint32_t P_A = 0, P_M = 0, P_T = 64 * MLD * 4, P_ATT = 3 * HALF, P_GATE = 4 * HALF, P_COLS = P_GATE + GATE_BYTES, P_MISC = P_COLS + DQ * 4, P_BYTES = P_MISC + 64 + 1024;
 
 // e^(G_i - G_j), as delta_decay, by the multi-function unit: off by 2^-22 and by 2^-24 of the exponent
 __device__ __forceinline__ float decay_of(float hi_i, float lo_i, float hi_j, float lo_j) {
     return ex2f(kLog2e * ((hi_i - hi_j) + (lo_i - lo_j)));
 }
-// X = (I + a B)^-1 a = a (I + B a)^-1 for a strictly lower triangular 64 x 64, B = diag(beta), in place (rows MLD apart), by PREP_NT
-// threads.  Both inverses that are needed are in it: (I + a B)^-1 = I - X B and (I + B a)^-1 = I - B X.  Blocks of 16 on the diagonal by
-// substitution, a thread a column; then twice the block below the diagonal of a pair, X21 = t - X22 B2 t with
-// t = a21 - a21 B1 X11, a thread four neighbouring columns of a row (T: 32 x 36 floats of scratch, for B2 t).  Blocks above the
-// diagonal: those in the pairs of 32 are set to zero, the other is neither read nor written.
-__device__ __forceinline__ void solve(float *M, float *T, const float *beta, int tid) {
-    if (tid < 64) {
-        const int o = tid / 16 * 16, j = tid & 15;
-        float x[16], xb[16];
+// D += A B for A 16 x 8 (rows), B 8 x 8, by a warp; fp32 entries of which the tensor core takes the leading 11 bits
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&x)[4], const uint32_t (&y)[2]) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(y[0]), "r"(y[1]));
+}
+// v as the sum of its leading 11 bits and the rest (exact)
+__device__ __forceinline__ void split_tf32(float v, uint32_t &hi, uint32_t &lo) {
+    hi = __float_as_uint(v) & 0xffffe000u;
+    lo = __float_as_uint(v - __uint_as_float(hi));
+}
+// acc = A diag(f) B for 16 rows of A (rows lda apart; f NULL: 1) and 8 COLS columns of B (rows MLD or TLD apart), inner length N: every
+// entry as two terms of 11 bits, three of the four products (off by 2^-20 of each).  At N = 8 there are eight rows, taken twice.
+template <int N, int COLS>
+__device__ __forceinline__ void small_product(float (&acc)[COLS][4], const float *A, const float *f, const float *B, int ldb, int lane) {
+    const int r = lane >> 2, c = lane & 3, r2 = N == 8 ? r : r + 8;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s = i > j ? M[(o + i) * MLD + o + j] : 0.f;
+    for (int t = 0; t < COLS; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
 #pragma unroll
-            for (int l = 0; l < i; l += 4) {
-                const float4 m = *reinterpret_cast<const float4 *>(M + (o + i) * MLD + o + l);
-                s = fmaf(-m.x, xb[l], s);
-                if (l + 1 < i) s = fmaf(-m.y, xb[l + 1], s);
-                if (l + 2 < i) s = fmaf(-m.z, xb[l + 2], s);
-                if (l + 3 < i) s = fmaf(-m.w, xb[l + 3], s);
-            }
-            x[i] = s;
-            xb[i] = beta[o + i] * s;
+    for (int l = 0; l < N; l += 8) {
+        float x[4] = {A[r * MLD + l + c], A[r2 * MLD + l + c], A[r * MLD + l + c + 4], A[r2 * MLD + l + c + 4]};
+        if (f != nullptr) {
+            const float f0 = f[l + c], f1 = f[l + c + 4];
+            x[0] *= f0; x[1] *= f0; x[2] *= f1; x[3] *= f1;
         }
-        __syncwarp();                                        // a block's sixteen threads are in one warp
+        uint32_t xh[4], xl[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) M[(o + i) * MLD + o + j] = x[i];
+        for (int e = 0; e < 4; ++e) split_tf32(x[e], xh[e], xl[e]);
+#pragma unroll
+        for (int t = 0; t < COLS; ++t) {
+            uint32_t yh[2], yl[2];
+            split_tf32(B[(l + c) * ldb + 8 * t + r], yh[0], yl[0]);
+            split_tf32(B[(l + c + 4) * ldb + 8 * t + r], yh[1], yl[1]);
+            mma_tf32(acc[t], xl, yh);
+            mma_tf32(acc[t], xh, yl);
+            mma_tf32(acc[t], xh, yh);
+        }
     }
-    {
-        const int o = tid / 64 * 32;
-        *reinterpret_cast<float4 *>(M + (o + tid % 64 / 4) * MLD + o + 16 + tid % 4 * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+}
+// The block X21 below the diagonal of a pair of N x N blocks, from a21 in its place, with t = a21 - a21 B1 X11:
+// X21 = t - X22 B2 t (T: scratch for B2 t).  At N = 8 a warp takes each of the four pairs, at 16 two each of two, at 32 four the one; a
+// warp 16 rows (at 8 eight).
+template <int N>
+__device__ __forceinline__ void join_pair(float *M, float *T, const float *beta, int w, int lane) {
+    constexpr int COLS = N == 32 ? 2 : 1, ROWS = N == 8 ? 1 : 2;
+    const int o = N == 8 ? w * 16 : N == 16 ? (w >> 1) * 32 : 0, i = N == 32 ? (w >> 1) * 16 : 0, j = N == 8 ? 0 : (w & 1) * (N / 2), r = lane >> 2, c = 2 * (lane & 3);
+    float *own = M + (o + N + i) * MLD + o + j, *scr = T + o / 2 * TLD, *t = scr + i * TLD + j, acc[COLS][4], d[COLS][4];
+    small_product<N, COLS>(acc, M + (o + N + i) * MLD + o, beta + o, M + o * MLD + o + j, MLD, lane);
+#pragma unroll
+    for (int k = 0; k < COLS; ++k)
+#pragma unroll
+        for (int e = 0; e < ROWS; ++e) {
+            const int row = r + 8 * e, col = 8 * k + c;
+            const float2 u = *reinterpret_cast<const float2 *>(own + row * MLD + col);
+            const float f = beta[o + N + i + row];
+            d[k][2 * e] = u.x - acc[k][2 * e];
+            d[k][2 * e + 1] = u.y - acc[k][2 * e + 1];
+            *reinterpret_cast<float2 *>(t + row * TLD + col) = make_float2(f * d[k][2 * e], f * d[k][2 * e + 1]);
+        }
+    if (N == 8) __syncwarp();
+    else __syncthreads();
+    small_product<N, COLS>(acc, M + (o + N + i) * MLD + o + N, nullptr, scr + j, TLD, lane);
+#pragma unroll
+    for (int k = 0; k < COLS; ++k)
+#pragma unroll
+        for (int e = 0; e < ROWS; ++e)
+            *reinterpret_cast<float2 *>(own + (r + 8 * e) * MLD + 8 * k + c) = make_float2(d[k][2 * e] - acc[k][2 * e], d[k][2 * e + 1] - acc[k][2 * e + 1]);
     __syncthreads();
+}
+// X = (I + a B)^-1 a = a (I + B a)^-1 for a strictly lower triangular 64 x 64, B = diag(beta), in place (rows MLD apart), by PREP_NT
+// threads.  Both inverses that are needed are in it: (I + a B)^-1 = I - X B and (I + B a)^-1 = I - B X.  A warp a block of 16 on the
+// diagonal: its two blocks of 8 by substitution, a thread a column, and what lies below them as a join; then twice the join of
+// a pair.  Those products are of 8, 16 and 32: too small for a tile of tcgen05, whose operands would have to be laid out anew for each.
+// By FMAs out of shared memory they were three quarters of the kernel's shared-memory traffic, which bounded it.  Blocks above the
+// diagonal: those in the pairs of 16 and 32 are set to zero, the other is neither read nor written.
+__device__ __forceinline__ void solve(float *M, float *T, const float *beta, int tid) {
+    const int w = tid >> 5, lane = tid & 31;
+    {
+        const int o = w * 16 + (lane & 8), j = lane & 7;
+        if (lane < 16) {
+            float x[8], xb[8];
 #pragma unroll
-    for (int n = 16; n <= 32; n *= 2) {
-        float4 t[2];                                         // this thread's elements of t (two of them at n = 32)
+            for (int i = 0; i < 8; ++i) {
+                float s = i > j ? M[(o + i) * MLD + o + j] : 0.f;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int k = 0; k < n / 16; ++k) {
-                const int it = tid + k * PREP_NT, per = n * n / 4, p = it / per, i = it % per / (n / 4), j = it % (n / 4) * 4, o = p * 2 * n;
-                f32x2 s0 = 0, s1 = 0;
-                const float *A = M + (o + n + i) * MLD + o + (half ? n : 0), *B = half ? T + p * n * 36 + j : M + o * MLD + o + j;
-                const int ldb = half ? 36 : MLD;
-#pragma unroll 2
-                for (int l = 0; l < n; l += 4) {
-                    float4 x = *reinterpret_cast<const float4 *>(A + l);
-                    if (!half) {
-                        const float4 f = *reinterpret_cast<const float4 *>(beta + o + l);
-                        x.x *= f.x; x.y *= f.y; x.z *= f.z; x.w *= f.w;
-                    }
-                    const float xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(B + (l + e) * ldb);
-                        const f32x2 xx = pk2(xs[e], xs[e]);
-                        s0 = fma2(xx, y.x, s0);
-                        s1 = fma2(xx, y.y, s1);
-                    }
+                for (int l = 0; l < i; l += 4) {
+                    const float4 m = *reinterpret_cast<const float4 *>(M + (o + i) * MLD + o + l);
+                    s = fmaf(-m.x, xb[l], s);
+                    if (l + 1 < i) s = fmaf(-m.y, xb[l + 1], s);
+                    if (l + 2 < i) s = fmaf(-m.z, xb[l + 2], s);
+                    if (l + 3 < i) s = fmaf(-m.w, xb[l + 3], s);
                 }
-                float4 r, *own = reinterpret_cast<float4 *>(M + (o + n + i) * MLD + o + j);
-                up2(s0, r.x, r.y);
-                up2(s1, r.z, r.w);
-                const float4 u = half ? t[k] : *own;
-                const float4 d = make_float4(u.x - r.x, u.y - r.y, u.z - r.z, u.w - r.w);
-                if (half) {
-                    *own = d;
-                } else {
-                    const float f = beta[o + n + i];
-                    t[k] = d;
-                    *reinterpret_cast<float4 *>(T + (p * n + i) * 36 + j) = make_float4(f * d.x, f * d.y, f * d.z, f * d.w);
-                }
+                x[i] = s;
+                xb[i] = beta[o + i] * s;
             }
-            __syncthreads();
+            __syncwarp(0xffffu);                             // a block's threads are in one warp
+#pragma unroll
+            for (int i = 0; i < 8; ++i) M[(o + i) * MLD + o + j] = x[i];
+        } else {                                             // zeros above: 8 x 8 of this warp's block, and half of a pair's 16 x 16
+            const int e = lane - 16, p = (w >> 1) * 32;
+            *reinterpret_cast<float4 *>(M + (w * 16 + e / 2) * MLD + w * 16 + 8 + e % 2 * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<float4 *>(M + (p + (w & 1) * 8 + k * 4 + e / 4) * MLD + p + 16 + e % 4 * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
+    __syncwarp();
+    join_pair<8>(M, T, beta, w, lane);
+    join_pair<16>(M, T, beta, w, lane);
+    join_pair<32>(M, T, beta, w, lane);
 }
 
 // a block a chunk and head
@@ -171,7 +207,6 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
         const float f = decay_of(gate[3 * DQ + e], gate[4 * DQ + e], gate[3 * DQ + j], gate[4 * DQ + j]);
         cols[j] = f;
     }
-    for (int e = tid; e < DGATES / 4; e += PREP_NT) reinterpret_cast<float4 *>(ops + GATES)[e] = reinterpret_cast<const float4 *>(gate)[e];
     ok = mbar_wait(bar + 1, 0) && ok;
     __syncthreads();
     if (!ok && tid == 0) set_status(a.hdr, SSD_ERR_DEVICE_TIMEOUT);
@@ -181,8 +216,8 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
     // (from the end of j's block on) and one of the column (to that end), each at most 1.
     const int i = tid & 63, ib = i >> 4, nb = 2 * (w & 1) + 2;
     const float ghi = gate[3 * DQ + i], glo = gate[4 * DQ + i];
-#pragma unroll
-    for (int jb = 0; jb < 4; ++jb) {
+#pragma unroll 1
+    for (int jb = 0; jb < 4; ++jb) {                         // (unrolled, this loop and the next cost 4 us of 56 by their fetches)
         float x[16];
         if (jb < nb) {
             tmem_ld16(tmem + ((uint32_t)w << 21) + 16 * jb, x);
@@ -222,25 +257,32 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
         } else {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-                *reinterpret_cast<uint4 *>(ops + ATT + i * 128 + (((2 * jb + q) ^ (i & 7)) << 4)) =
+                *reinterpret_cast<uint4 *>(sm + P_ATT + i * 128 + (((2 * jb + q) ^ (i & 7)) << 4)) =
                     make_uint4(pack_bf16(x[8 * q], x[8 * q + 1]), pack_bf16(x[8 * q + 2], x[8 * q + 3]), pack_bf16(x[8 * q + 4], x[8 * q + 5]),
                                pack_bf16(x[8 * q + 6], x[8 * q + 7]));
         }
     }
     tc_fence_before();
+    fence_proxy_async_smem();
     __syncthreads();
     if (w == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 64);
     }
+    if (tid == PREP_NT - 1) {                                // (of a warp that does not substitute)
+        bulk_store(ops + ATT, sm + P_ATT, MAT_BYTES);
+        bulk_store(ops + GATES, gate, GATE_BYTES);
+        bulk_commit();
+    }
+    __syncwarp();
     const float *beta = gate + 2 * DQ;
     solve(M, T, beta, tid);
-    // rows of the right operands, N index n, K index k: (I + a B)^-1; and of the transposed (I + B a)^-1
-    const int n = tid >> 1;
-#pragma unroll
+    // Rows of the right operands, N index n, K index k: (I + a B)^-1, eight threads a row, so that a warp's pieces are whole lines; and
+    // of the transposed (I + B a)^-1, where lanes are rows, so that what they read lies in different banks.
+#pragma unroll 1
     for (int q = 0; q < 4; ++q) {
         uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
-        const int k0 = (tid & 1) * 32 + q * 8;
+        const int n = q * 16 + (tid >> 3), k0 = (tid & 7) * 8;
         uint8_t *to = ops + n * 128 + (((k0 / 8) ^ (n & 7)) << 4);
         if (k0 / 16 <= n / 16)
 #pragma unroll
@@ -251,10 +293,15 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
             }
         *reinterpret_cast<uint4 *>(to + SYS_HI) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4 *>(to + SYS_LO) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        if (BOTH) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) hi[e] = lo[e] = 0u;
-            if (k0 / 16 >= n / 16)
+    }
+    if (BOTH) {
+        const int n = tid >> 1;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+            uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+            const int k0 = 16 * q + 8 * (tid & 1);           // (a sector of 32 bytes for two threads)
+            uint8_t *to = ops + n * 128 + (((k0 / 8) ^ (n & 7)) << 4);
+            if (q >= n / 16)
 #pragma unroll
                 for (int e = 0; e < 8; e += 2)
                     split2((k0 + e == n ? 1.f : 0.f) - beta[k0 + e] * M[(k0 + e) * MLD + n], (k0 + e + 1 == n ? 1.f : 0.f) - beta[k0 + e + 1] * M[(k0 + e + 1) * MLD + n],
@@ -263,6 +310,7 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
             *reinterpret_cast<uint4 *>(to + SYS_T + MAT_BYTES) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     }
+    if (tid == PREP_NT - 1) bulk_wait0();
 }
 
 // ---------------------------------------------------------------------------------------- the chain
@@ -348,8 +396,8 @@ __device__ __forceinline__ void ld_gates(f32x2 &g0, f32x2 &g1, const float *p) {
     g0 = v.x;
     g1 = v.y;
 }
-// KEEP: U, or mu, and the states are left for the gradients; OUT: o (backwards dV) is computed; ENDS: a segment's end from a zero state, or
-// its matrix, is left and nothing else
+// KEEP: U, or mu, and the states are left for the gradients; OUT: o (backwards dV) is computed; ENDS: the first launch of chains that
+// are cut into segments: the first segment as it is, of the others but the last the end from a zero state and the matrix, and nothing else
 template <bool BACK, bool KEEP, bool OUT, bool ENDS>
 __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __grid_constant__ DeltaMaps m) {
     after_previous();
@@ -357,15 +405,16 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
     uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     ChainBars *ms = reinterpret_cast<ChainBars *>(sm + CH_MISC);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    // unit: sequence and head; segment; of a segment's two, its end or (mat) what it makes of the state before it, S -> S M
+    // unit: sequence and head; segment; of a segment's two, its end or (mat) what it makes of the state before it, S -> S M.  The longest first.
     const int units = a.nseqs * a.H, unit = blockIdx.x % units, part = blockIdx.x / units, s = unit / a.H, h = unit % a.H, grp = h / (a.H / a.G);
-    const bool mat = ENDS && part >= a.nseg - 1;
-    const int seg = mat ? part - (a.nseg - 1) + 1 : part;
+    const bool mat = ENDS && part > a.nseg - 2;
+    const int seg = mat ? part - (a.nseg - 2) : ENDS ? part : a.nseg - 1 - part;
+    const bool run = !ENDS || seg == 0, keeps = KEEP && run, outs = OUT && run;
     if (BACK && a.fresh && (ENDS || a.nseg == 1) && blockIdx.x == 0 && tid < HDR_WORDS) a.hdr[tid] = 0;
     const DeltaSeq q = delta_seq(a, s);
-    const int all = (q.len + DQ - 1) / DQ, c0 = seg * a.seglen;            // chunks of the sequence; the segment's first step
-    if (ENDS ? c0 + a.seglen >= all : seg > 0 && c0 >= all) return;        // no segment follows; nothing in it
-    const int n = min(a.seglen, all - c0), joins = ENDS ? 0 : max(0, seg - 1);
+    const int all = (q.len + DQ - 1) / DQ, c0 = seg == 0 ? 0 : a.seg0 + (seg - 1) * a.seglen;   // chunks of the sequence; the segment's first step
+    if (seg > 0 && c0 + (ENDS ? a.seglen : 0) >= all) return;              // no segment follows; nothing in it
+    const int n = a.nseg > 1 && seg < a.nseg - 1 ? min(seg == 0 ? a.seg0 : a.seglen, all - c0) : all - c0, joins = ENDS ? 0 : max(0, seg - 1);
     if (tid == 0) {
         for (int b : {B_FULL0, B_FULL1}) mbar_init(&ms->bar[b], CH_LW);
         for (int b : {B_TMA0, B_TMA1, B_O0, B_O1, B_P, B_U, B_S, B_END, B_FO, B_FV, B_FS, B_JM0, B_JM1, B_JD}) mbar_init(&ms->bar[b], 1);
@@ -381,7 +430,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         prefetch_tmap(&m.k);
         prefetch_tmap(BACK ? &m.dO : &m.v);
         prefetch_tmap(&m.q);
-        if (OUT) prefetch_tmap(&m.out);
+        if (outs) prefetch_tmap(&m.out);
     }
     tc_fence_before();
     __syncthreads();
@@ -400,7 +449,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
     auto stage = [&](int c) { return sm + (c & 1) * ST_BYTES; };
     auto idx = [&](int c) { return BACK ? all - 1 - c0 - c : c0 + c; };    // the chunk of step c
     // Q and, backwards, dO are needed for the state's sake too
-    const bool outputs = BACK ? !mat : OUT, values = !mat;
+    const bool outputs = BACK ? !mat : outs, values = !mat;
     using C = Cols<BACK>;
 
     if (w < CH_CW) {
@@ -464,7 +513,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
             }
             tmem_wait_st();
             arrive(B_AS + g);
-            if (KEEP && keep) {
+            if (keeps && keep) {
                 if (g == 0 && c > 0) wait(B_FS, c - 1);
                 uint8_t *to = sm + CH_S + hf * (STATE_BYTES / 2) + v * 128;
 #pragma unroll
@@ -562,7 +611,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 if (!BACK) tmem_st8(at + C::W + i0, wb);
                 tmem_wait_st();
                 arrive(B_AW + g);
-                if (KEEP) {
+                if (keeps) {
                     if (g == 0 && c > 0) go = wait(B_FV, c - 1);
                     if (!go) break;
 #pragma unroll
@@ -577,7 +626,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                         arrive(B_WV);
                     }
                 }
-                if (BACK && OUT) {                           // dV: a whole chunk through a tile, as one copy; another by itself
+                if (BACK && outs) {                           // dV: a whole chunk through a tile, as one copy; another by itself
                     if (g == 0 && c > 0) go = wait(B_FO, c - 1);
                     if (!go) break;
                     if (m.has_out && q.len - ci * DQ >= DQ) {
@@ -606,9 +655,9 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 if (c + 1 < n) publish(c + 1, g, true);
             }
         }
-        void *out = ENDS || c0 + n < all ? nullptr : BACK ? a.dinit : a.final;
+        void *out = !run || c0 + n < all ? nullptr : BACK ? a.dinit : a.final;
         const bool f32 = BACK ? !a.dinit_bf16 : !a.final_bf16;
-        if (ENDS && !mat) {
+        if (ENDS && !mat && c0 + n < all) {
             float *to = const_cast<float *>(ends) + seg * (128 * 128);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
@@ -617,7 +666,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 up2(S[e + 1], x.z, x.w);
                 *reinterpret_cast<float4 *>(to + 2 * e) = x;
             }
-        } else if (ENDS) {
+        } else if (ENDS && mat) {
             uint8_t *to = static_cast<uint8_t *>(a.segM) + ((int64_t)unit * (a.nseg - 1) + seg) * SEG_BYTES + hf * (STATE_BYTES / 2) + v * 128;
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
@@ -691,7 +740,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 tmem_wait_st();
                 arrive(B_AF);
             }
-        } else if (!BACK && OUT) {
+        } else if (!BACK && outs) {
             float *eg = reinterpret_cast<float *>(sm + CH_EG) + (w & 3) * DQ;
             for (int c = 0; c < n; ++c) {                    // o = scale (e^G Q S + att W)
                 if (!full(c)) break;
@@ -790,7 +839,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
             arrive(B_FULL0 + (c & 1));
             // chunk c has been announced; chunk c - 1's products are done with its stage (and so is every lane): chunk c + 1
             if (c > 0 && c + 1 < n) {
-                if (!wait2(B_O0, c - 1) || (!BACK && OUT && !wait2(B_EG0, c - 1))) break;
+                if (!wait2(B_O0, c - 1) || (!BACK && outs && !wait2(B_EG0, c - 1))) break;
                 issue(c + 1);
             }
         }
@@ -800,7 +849,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
             uint8_t *vals = static_cast<uint8_t *>(BACK ? a.mu : a.U), *kept = static_cast<uint8_t *>(BACK ? a.dS : a.S);
             for (int c = 0; c < n; ++c) {
                 const int ci = idx(c);
-                if (KEEP) {
+                if (keeps) {
                     if (!wait(B_WS, c)) break;
                     bulk_store(kept + (((int64_t)q.slot0 + ci) * a.H + h) * STATE_BYTES, sm + CH_S, STATE_BYTES);
                     bulk_commit();
@@ -812,7 +861,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                     bulk_wait_read0();
                     mbar_arrive(&ms->bar[B_FV]);
                 }
-                if (OUT) {
+                if (outs) {
                     if (!wait2(B_WO0, c)) break;
                     if (m.has_out && q.len - ci * DQ >= DQ) {
                         tma_store_4d(&m.out, sm + CH_O, 0, h, q.t0 + ci * DQ, q.b);
@@ -853,7 +902,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                     for (int k = 0; k < 4; ++k)
                         umma_bf16(tmem + C::R(c), mnmaj(X, k, HALF), mnmaj(ops + ATT, k, HALF), idesc_bf16(128, 64, 1, 1), k > 0);
                 }
-                go = BACK || !OUT || c < 2 || wait2(B_WO0, c - 2);   // o of the chunk before last has been read
+                go = BACK || !outs || c < 2 || wait2(B_WO0, c - 2);   // o of the chunk before last has been read
                 // K S and Q S in one: their rows are the 128 rows of the right operand.  Each thread's first quarter
                 // while it still writes the second; so with the other products.
 #pragma unroll
@@ -913,7 +962,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 }
                 if (!go) break;
                 umma_commit(&ms->bar[B_S]);
-                if (!BACK && OUT)
+                if (!BACK && outs)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) umma_bf16_ta(tmem + C::P(c), tmem + C::W + 16 * k, kmaj(ops + ATT, k, 0), id64, k > 0);
                 umma_commit(&ms->bar[B_O0 + (c & 1)]);
@@ -1306,8 +1355,8 @@ cudaError_t launch_chain(const DeltaArgs &a, const DeltaMaps &m, int parts, cuda
 template <bool BACK, bool KEEP, bool OUT>
 cudaError_t chain(const DeltaArgs &a, const DeltaMaps &m, cudaStream_t st) {
     if (a.nseg > 1)
-        if (cudaError_t e = launch_chain<BACK, false, false, true>(a, m, 2 * a.nseg - 3, st); e != cudaSuccess) return e;
-    return launch_chain<BACK, KEEP, OUT, false>(a, m, a.nseg, st);
+        if (cudaError_t e = launch_chain<BACK, KEEP, OUT, true>(a, m, 2 * a.nseg - 3, st); e != cudaSuccess) return e;
+    return launch_chain<BACK, KEEP, OUT, false>(a, m, std::max(1, a.nseg - 1), st);
 }
 
 }  // namespace

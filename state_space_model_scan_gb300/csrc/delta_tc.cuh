@@ -4,6 +4,8 @@
 // 64 tokens x 128 features is two such images of 64 rows, 8 KB each (features 0..63, 64..127).
 #pragma once
 
+#include <algorithm>
+
 #include "delta.cuh"
 #include "tc_common.cuh"
 
@@ -25,22 +27,29 @@ constexpr uint32_t VAL_BYTES = DQ * 128 * 2;     // kept U, and mu: [64][128], p
 
 constexpr uint32_t SEG_BYTES = 128 * 128 * 4;    // of a segment: its end in fp32; its matrix as two states' images
 
-// Segments of the chains of nseqs x H sequences and heads, at most `chunks` long.  Cut into m, a chain's first launch takes 2 m - 3
-// blocks (every end but the last, every matrix but the first and last), the second m, each of chunks / m steps on kSMs SMs;
-// and joining the ends before a segment takes 0.8 of a step each.
-inline void delta_segments(int64_t nseqs, int64_t H, int64_t chunks, int *nseg, int *seglen) {
+// Segments of the chains of nseqs x H sequences and heads, at most `chunks` long: one of `first` chunks, nseg - 2 of `len`, one of the
+// rest.  Two launches: the first takes the first segment as it is and, of each one between, its end from a zero state and its
+// matrix; the second, which knows the state that every segment starts from, those and the last.  So the first segment
+// lasts as long as what goes on beside it on the other SMs, and the last one too; the blocks for those between come in
+// waves.  A block costs one step more than its chunks, joining the ends before a segment 0.8 each, the second launch eight.
+// (8192 tokens of 32 heads: 195 us of chains instead of 340 in one launch, or 260 in three equal segments; 2 x 2048 of 32: 104 cut, 102
+// in one, so it stays whole.)
+inline void delta_segments(int64_t nseqs, int64_t H, int64_t chunks, int *nseg, int *first, int *len) {
     const int64_t sms = 152, U = nseqs * H;
     *nseg = 1;
-    *seglen = (int)(chunks > 0 ? chunks : 1);
-    double best = (double)chunks * ((U + sms - 1) / sms);
-    if (3 * U > sms) return;
-    for (int64_t m = 3; m <= 32 && chunks / m >= 4; ++m) {
-        const int64_t len = (chunks + m - 1) / m;
-        const double t = (double)len * ((U * (2 * m - 3) + sms - 1) / sms + (U * m + sms - 1) / sms) + 0.8 * (m - 2) + 4;
+    *first = *len = 0;
+    double best = (double)chunks;
+    if (U >= sms) return;
+    for (int64_t k = 1; k <= 30; ++k) {
+        const int64_t w1 = (2 * k * U + sms - U - 1) / (sms - U), w2 = (k * U + sms - U - 1) / (sms - U), n = w1 + k + w2, s = (chunks + n - 1) / n;
+        const int64_t last = chunks - (w1 + k) * s;
+        if (s < 4 || last < 1) continue;
+        const double t = (double)w1 * (s + 1) + std::max<int64_t>(last, w2 * (s + 1)) + 0.8 * k + 8;
         if (t < best) {
             best = t;
-            *seglen = (int)len;
-            *nseg = (int)((chunks + len - 1) / len);
+            *nseg = (int)k + 2;
+            *first = (int)(w1 * s);
+            *len = (int)s;
         }
     }
 }
