@@ -422,44 +422,15 @@ def gated_delta_backward(q, k, v, g, beta, do, scale=None, initial_states=None, 
                                  _handle(stream))
 
 
-class GatedDeltaFunction(torch.autograd.Function):
-    """Autograd wrapper of the gated delta rule.  Where gradients are asked for, the forward keeps what the backward starts from
-    (ssd_delta_chunk_states_size; with keep_chunk_states=False the backward computes it again).  An unused output costs no gradient
-    of zeros.  A second differentiation is refused."""
-
-    @classmethod
-    def apply(cls, q, k, v, g, beta, initial_states=None, cu_seqlens=None, scale=None, keep_chunk_states=True):
-        inputs = (q, k, v, g, beta, initial_states)
-        keep = keep_chunk_states and torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)
-        return super().apply(*inputs, cu_seqlens, scale, keep)
+class GatedDeltaFunction:
+    """The gated delta rule in an autograd graph: o, final_states = GatedDeltaFunction.apply(...).  Where gradients are asked for, the
+    forward keeps what the backward starts from (ssd_delta_chunk_states_size: on tensor cores 90 KB per 64 tokens and value head;
+    with keep_chunk_states=False the backward computes it again).  Gradients go to q, k, v, g, beta and initial_states; an unused
+    final state costs no gradient of zeros.  A second differentiation is refused."""
 
     @staticmethod
-    def forward(ctx, q, k, v, g, beta, initial_states, cu_seqlens, scale, keep):
-        o, fin, *kept = _lib.fast().delta_fwd(q, k, v, g, beta, initial_states, cu_seqlens, scale, True, -1, keep, None)
-        ctx.save_for_backward(q, k, v, g, beta, initial_states, cu_seqlens, kept[0] if keep else None)
-        ctx.scale = scale
-        ctx.set_materialize_grads(False)
-        return o, fin
-
-    @staticmethod
-    def backward(ctx, do, dfin):
-        return (_once if torch.is_grad_enabled() else _delta_grads)(_delta_grads, ctx, do, dfin)
-
-
-def _delta_grads(_, ctx, do, dfin):
-    q, k, v, g, beta, init, cu, kept = ctx.saved_tensors
-    if do is None:
-        do = torch.zeros_like(v, memory_format=torch.contiguous_format)
-    elif do.stride(-1) != 1:
-        do = do.contiguous()
-    d = _lib.fast().delta_bwd(q, k, v, g, beta, init, cu, ctx.scale, do, None if dfin is None else dfin.contiguous(), kept, None, None)
-    return d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"], d.get("dinitial_states"), None, None, None
-
-
-@torch.autograd.function.once_differentiable
-def _once(f, *args):
-    """f's gradients where a graph of them is asked for: differentiating them again is refused.  (20 us a call, so not otherwise.)"""
-    return f(f, *args)
+    def apply(q, k, v, g, beta, initial_states=None, cu_seqlens=None, scale=None, keep_chunk_states=True):
+        return _lib.fast().delta_apply(q, k, v, g, beta, initial_states, cu_seqlens, scale, bool(keep_chunk_states))
 
 
 def gated_delta_step(state, q, k, v, g, beta, scale=None, state_indices=None, stream=None):
@@ -498,27 +469,10 @@ def qk_norm_backward(q, k, dq, dk, q_weight=None, k_weight=None, cos=None, sin=N
                               _handle(stream))
 
 
-class QKNormFunction(torch.autograd.Function):
-    """Autograd wrapper of the norm and rotation of queries and keys; it keeps its inputs alone.  cos, sin and positions get no
-    gradient.  A second differentiation is refused."""
-
-    @classmethod
-    def apply(cls, q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, mode="rms", interleaved=False, eps=1e-6):
-        return super().apply(q, k, q_weight, k_weight, cos, sin, positions, mode, interleaved, eps)
+class QKNormFunction:
+    """The norm and rotation of queries and keys in an autograd graph: q_out, k_out = QKNormFunction.apply(...).  It keeps its inputs
+    alone; gradients go to q, k and the weights.  A second differentiation is refused."""
 
     @staticmethod
-    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, mode, interleaved, eps):
-        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
-        ctx.how = how = _qk_mode(mode), bool(interleaved), eps
-        return _lib.fast().qk_fwd(q, k, q_weight, k_weight, cos, sin, positions, *how, None)
-
-    @staticmethod
-    def backward(ctx, dq, dk):
-        return (_once if torch.is_grad_enabled() else _qk_grads)(_qk_grads, ctx, dq, dk)
-
-
-def _qk_grads(_, ctx, dq, dk):
-    q, k, wq, wk, cos, sin, pos = ctx.saved_tensors
-    dq, dk = (t if t is None or t.stride(-1) == 1 else t.contiguous() for t in (dq, dk))
-    d = _lib.fast().qk_bwd(q, k, wq, wk, cos, sin, pos, *ctx.how, dq, dk, None, None)
-    return d["dq"], d.get("dk"), d.get("dq_weight"), d.get("dk_weight"), None, None, None, None, None, None
+    def apply(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, mode="rms", interleaved=False, eps=1e-6):
+        return _lib.fast().qk_apply(q, k, q_weight, k_weight, cos, sin, positions, _qk_mode(mode), bool(interleaved), eps)

@@ -9,12 +9,21 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <ATen/ops/zeros_like.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/saved_variable.h>
 
 #include <math.h>
 #include <stdarg.h>
 
+#include <array>
 #include <initializer_list>
+#include <memory>
+#include <optional>
 #include <string>
 
 #include "../../include/ssd.h"
@@ -450,9 +459,9 @@ struct Delta {
 };
 const char *const delta_names[7] = {"q", "k", "v", "g", "beta", "initial_states", "cu_seqlens"};
 
-// A float argument, or `other` where it is None.
-double number(PyObject *o, const char *name, double other) {
-    if (o == Py_None) return other;
+// A float argument; nothing where it is None.
+std::optional<double> number(PyObject *o, const char *name) {
+    if (o == Py_None) return std::nullopt;
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) {
         PyErr_Clear();
@@ -462,7 +471,7 @@ double number(PyObject *o, const char *name, double other) {
 }
 
 // q, k, v, g, beta, initial_states, cu_seqlens; scale: dstate^-0.5 where it is None
-Delta delta_inputs(const Tensor *const *t, PyObject *scale) {
+Delta delta_inputs(const Tensor *const *t, std::optional<double> scale) {
     const Tensor &q = *t[0], &k = *t[1], &v = *t[2], &g = *t[3], &beta = *t[4], &init = *t[5], &cu = *t[6];
     Delta s{};
     const int dev = s.dev = lead("v", v, 4), own = type_of(v);
@@ -480,70 +489,78 @@ Delta delta_inputs(const Tensor *const *t, PyObject *scale) {
     like("g", g, {s.B, s.L, s.H}, F32 | own, dev, 0);
     like("beta", beta, {s.B, s.L, s.H}, F32 | own, dev, 0);
     if (init.defined()) like("initial_states", init, {s.S, s.H, s.V, s.K}, F32 | BF16, dev, 4);
-    s.p = {s.B, s.L, s.H, s.G, s.V, s.K, cu.defined() ? s.S : 0, (float)number(scale, "scale", s.K > 0 ? 1.0 / sqrt((double)s.K) : 1.0), code(v)};
+    s.p = {s.B, s.L, s.H, s.G, s.V, s.K, cu.defined() ? s.S : 0, (float)scale.value_or(s.K > 0 ? 1.0 / sqrt((double)s.K) : 1.0), code(v)};
     s.f.q = desc(q, 1); s.f.k = desc(k, 1); s.f.v = desc(v, 1); s.f.g = desc(g, 0); s.f.beta = desc(beta, 0);
     s.f.initial_states = desc(init, 4);
     s.f.cu_seqlens = ptr_as<int32_t>(cu);
     return s;
 }
 
-// delta_fwd(the inputs, scale, return_final, state_dtype (-1: the initial states' or f32), keep, stream)
-PyObject *delta_fwd(PyObject *const *a) {
-    const Tensor *t[7];
-    for (int i = 0; i < 7; ++i) t[i] = &arg(a[i], delta_names[i], i >= 5);
-    Delta s = delta_inputs(t, a[7]);
+struct DeltaOut {
+    Tensor o, final, kept;
+};
+// state_dtype -1: the initial states' or f32
+DeltaOut delta_forward(const Tensor *const *t, std::optional<double> scale, bool want_final, long state_dtype, bool keep, PyObject *stream) {
+    Delta s = delta_inputs(t, scale);
     const Tensor &v = *t[2], &init = *t[5];
-    const bool want_final = a[8] == Py_True, keep = a[10] == Py_True;
-    const long sd = PyLong_AsLong(a[9]);
-    const Stream st(a[11], s.dev);
-    Tensor o = st.output({s.B, s.L, s.H, s.V}, v.scalar_type()), final, kept;
-    s.f.o = desc(o, 4);
+    const Stream st(stream, s.dev);
+    DeltaOut r;
+    r.o = st.output({s.B, s.L, s.H, s.V}, v.scalar_type());
+    s.f.o = desc(r.o, 4);
     if (want_final) {
-        const bool bf16 = sd < 0 ? init.defined() && init.scalar_type() == at::kBFloat16 : sd == SSD_BF16;
-        final = st.output({s.S, s.H, s.V, s.K}, bf16 ? at::kBFloat16 : at::kFloat);
-        s.f.final_states = desc(final, 4);
+        const bool bf16 = state_dtype < 0 ? init.defined() && init.scalar_type() == at::kBFloat16 : state_dtype == SSD_BF16;
+        r.final = st.output({s.S, s.H, s.V, s.K}, bf16 ? at::kBFloat16 : at::kFloat);
+        s.f.final_states = desc(r.final, 4);
     }
     if (keep) {
         size_t n = 0;
         check(lib.delta_states_size(&s.p, &n), "ssd_delta_chunk_states_size");
-        kept = st.output({(int64_t)n}, at::kByte);
-        s.f.chunk_states = kept.data_ptr();
+        r.kept = st.output({(int64_t)n}, at::kByte);
+        s.f.chunk_states = r.kept.data_ptr();
     }
     size_t n = 0;
     check(lib.delta_fwd_workspace_size(&s.p, &n), "ssd_delta_fwd_workspace_size");
     Tensor ws;
     if (n > 0) ws = st.empty({(int64_t)n}, at::kByte);
     check(lib.delta_fwd(&s.p, &s.f, ptr(ws), n, st.handle), "ssd_delta_fwd");
+    return r;
+}
+PyObject *wrap_or_none(const Tensor &t) { return t.defined() ? wrap(t) : Py_NewRef(Py_None); }
+template <int N>
+void read(PyObject *const *a, const char *const (&names)[N], int required, const Tensor *(&t)[N]) {
+    for (int i = 0; i < N; ++i) t[i] = &arg(a[i], names[i], i >= required);
+}
+// delta_fwd(the inputs, scale, return_final, state_dtype, keep, stream)
+PyObject *delta_fwd(PyObject *const *a) {
+    const Tensor *t[7];
+    read(a, delta_names, 5, t);
+    const bool keep = a[10] == Py_True;
+    const DeltaOut out = delta_forward(t, number(a[7], "scale"), a[8] == Py_True, PyLong_AsLong(a[9]), keep, a[11]);
     PyObject *r = PyTuple_New(keep ? 3 : 2);
     if (!r) throw Raised();
-    PyTuple_SET_ITEM(r, 0, wrap(o));
-    PyTuple_SET_ITEM(r, 1, want_final ? wrap(final) : Py_NewRef(Py_None));
-    if (keep) PyTuple_SET_ITEM(r, 2, wrap(kept));
+    PyTuple_SET_ITEM(r, 0, wrap(out.o));
+    PyTuple_SET_ITEM(r, 1, wrap_or_none(out.final));
+    if (keep) PyTuple_SET_ITEM(r, 2, wrap(out.kept));
     return r;
 }
 
-// A dict's tensors, allocated and described one by one.
-struct Grads {
+// The tensors that are there, by name.
+template <size_t N>
+PyObject *dict_of(const std::array<Tensor, N> &t, const char *const (&names)[N]) {
     PyObject *g = PyDict_New();
-    const Stream &st;
-    explicit Grads(const Stream &s) : st(s) {
-        if (!g) throw Raised();
-    }
-    ~Grads() { Py_XDECREF(g); }
-    Tensor out(const char *name, at::IntArrayRef shape, at::ScalarType type) {
-        Tensor v = st.output(shape, type);
-        PyObject *o = wrap(v);
-        const int rc = o ? PyDict_SetItemString(g, name, o) : -1;
+    if (!g) throw Raised();
+    for (size_t i = 0; i < N; ++i) {
+        if (!t[i].defined()) continue;
+        PyObject *o = wrap(t[i]);
+        const int rc = o ? PyDict_SetItemString(g, names[i], o) : -1;
         Py_XDECREF(o);
-        if (rc) throw Raised();
-        return v;
+        if (rc) {
+            Py_DECREF(g);
+            throw Raised();
+        }
     }
-    PyObject *take() {
-        PyObject *r = g;
-        g = nullptr;
-        return r;
-    }
-};
+    return g;
+}
 // The backward's workspace: from an object with get(bytes), or of its own.
 Tensor workspace_of(PyObject *o, size_t n, const Stream &st) {
     if (o == Py_None) return st.empty({(int64_t)(n < 256 ? 256 : n)}, at::kByte);
@@ -558,13 +575,11 @@ Tensor workspace_of(PyObject *o, size_t n, const Stream &st) {
     return ws;
 }
 
-// delta_bwd(the inputs, scale, do, dfinal_states, chunk_states, workspace, stream)
-PyObject *delta_bwd(PyObject *const *a) {
-    const Tensor *t[7];
-    for (int i = 0; i < 7; ++i) t[i] = &arg(a[i], delta_names[i], i >= 5);
-    Delta s = delta_inputs(t, a[7]);
+const char *const delta_grad_names[6] = {"dq", "dk", "dv", "dg", "dbeta", "dinitial_states"};
+std::array<Tensor, 6> delta_backward(const Tensor *const *t, std::optional<double> scale, const Tensor &dO, const Tensor &dfinal, const Tensor &kept,
+                                     PyObject *workspace, PyObject *stream) {
+    Delta s = delta_inputs(t, scale);
     const Tensor &v = *t[2], &g = *t[3], &beta = *t[4], &init = *t[5];
-    const Tensor &dO = arg(a[8], "do"), &dfinal = arg(a[9], "dfinal_states", true), &kept = arg(a[10], "chunk_states", true);
     like("do", dO, {s.B, s.L, s.H, s.V}, type_of(v), s.dev, 1);
     if (dfinal.defined()) like("dfinal_states", dfinal, {s.S, s.H, s.V, s.K}, F32 | BF16, s.dev, 4);
     if (kept.defined()) {
@@ -574,23 +589,127 @@ PyObject *delta_bwd(PyObject *const *a) {
         NEED(kept.nbytes() >= n, "chunk_states is smaller than %zu bytes", n);
         s.f.chunk_states = kept.data_ptr();
     }
-    const Stream st(a[12], s.dev);
+    const Stream st(stream, s.dev);
     ssd_delta_bwd_args b{};
     b.fwd = s.f;
     b.dO = desc(dO, 1);
     b.dfinal_states = desc(dfinal, 4);
-    Grads d(st);
-    b.dq = desc(d.out("dq", {s.B, s.L, s.G, s.K}, v.scalar_type()), 4);
-    b.dk = desc(d.out("dk", {s.B, s.L, s.G, s.K}, v.scalar_type()), 4);
-    b.dv = desc(d.out("dv", {s.B, s.L, s.H, s.V}, v.scalar_type()), 4);
-    b.dg = desc(d.out("dg", {s.B, s.L, s.H}, g.scalar_type()), 3);
-    b.dbeta = desc(d.out("dbeta", {s.B, s.L, s.H}, beta.scalar_type()), 3);
-    if (init.defined()) b.dinitial_states = desc(d.out("dinitial_states", {s.S, s.H, s.V, s.K}, init.scalar_type()), 4);
+    std::array<Tensor, 6> d = {st.output({s.B, s.L, s.G, s.K}, v.scalar_type()), st.output({s.B, s.L, s.G, s.K}, v.scalar_type()),
+                               st.output({s.B, s.L, s.H, s.V}, v.scalar_type()), st.output({s.B, s.L, s.H}, g.scalar_type()),
+                               st.output({s.B, s.L, s.H}, beta.scalar_type()), Tensor()};
+    if (init.defined()) d[5] = st.output({s.S, s.H, s.V, s.K}, init.scalar_type());
+    b.dq = desc(d[0], 4); b.dk = desc(d[1], 4); b.dv = desc(d[2], 4); b.dg = desc(d[3], 3); b.dbeta = desc(d[4], 3); b.dinitial_states = desc(d[5], 4);
     size_t n = 0;
     check(lib.delta_bwd_workspace_size(&s.p, kept.defined(), &n), "ssd_delta_bwd_workspace_size");
-    Tensor ws = workspace_of(a[11], n, st);
+    Tensor ws = workspace_of(workspace, n, st);
     check(lib.delta_bwd(&s.p, &b, ws.data_ptr(), ws.nbytes(), st.handle), "ssd_delta_bwd");
-    return d.take();
+    return d;
+}
+// delta_bwd(the inputs, scale, do, dfinal_states, chunk_states, workspace, stream)
+PyObject *delta_bwd(PyObject *const *a) {
+    const Tensor *t[7];
+    read(a, delta_names, 5, t);
+    return dict_of(delta_backward(t, number(a[7], "scale"), arg(a[8], "do"), arg(a[9], "dfinal_states", true), arg(a[10], "chunk_states", true), a[11], a[12]),
+                   delta_grad_names);
+}
+
+// ---- autograd: nodes of their own, since a Python function's way into the graph and back takes 80 us of host time a step
+namespace ag = torch::autograd;
+
+// What a node does under the interpreter's lock; a Python exception goes on as the engine carries those.
+template <typename F>
+auto locked(F f) {
+    struct Lock {
+        PyGILState_STATE s = PyGILState_Ensure();
+        ~Lock() { PyGILState_Release(s); }
+    } lock;
+    try {
+        return f();
+    } catch (const Raised &) {
+        python_error e;
+        e.persist();
+        throw std::move(e);
+    }
+}
+// A backward's gradients: where a graph of them is asked for, one that refuses to be differentiated.
+void refuse_second(ag::variable_list &d, ag::edge_list &&edges) {
+    std::shared_ptr<ag::Node> no(new ag::Error("the gradients of this operator cannot be differentiated again", std::move(edges)), ag::deleteNode);
+    for (Tensor &t : d)
+        if (t.defined()) ag::set_history(t, no);
+}
+// An output's gradient with unit stride in its last dimension
+Tensor unit(const Tensor &t) { return !t.defined() || t.stride(-1) == 1 ? t : t.contiguous(); }
+
+// An operator's node: its N inputs (and one tensor more) saved.
+template <size_t N>
+struct OpNode : ag::Node {
+    std::array<ag::SavedVariable, N> saved;
+    void save(const Tensor *const *t) {
+        for (size_t i = 0; i < N; ++i) saved[i] = ag::SavedVariable(*t[i], false);
+    }
+    void release_variables() override {
+        for (auto &v : saved) v.reset_data();
+    }
+    // f(inputs, gradients) -> gradients of the inputs, without a graph
+    template <typename F>
+    ag::variable_list run(ag::variable_list &&grads, F f) {
+        std::array<Tensor, N> in;
+        for (size_t i = 0; i < N; ++i) in[i] = saved[i].unpack();
+        const bool again = at::GradMode::is_enabled();
+        ag::variable_list d;
+        {
+            at::NoGradGuard off;
+            const Tensor *t[N];
+            for (size_t i = 0; i < N; ++i) t[i] = &in[i];
+            d = locked([&] { return f(t, grads); });
+        }
+        if (again) {
+            ag::edge_list edges = ag::collect_next_edges(ag::variable_list(in.begin(), in.end()), grads);
+            refuse_second(d, std::move(edges));
+        }
+        return d;
+    }
+};
+bool graph_wanted(const Tensor *const *t, int n) {
+    if (!at::GradMode::is_enabled()) return false;
+    for (int i = 0; i < n; ++i)
+        if (t[i]->defined() && t[i]->requires_grad()) return true;
+    return false;
+}
+
+struct GatedDelta : OpNode<8> {                            // the seven inputs, what the forward kept
+    std::optional<double> scale;
+    std::string name() const override { return "GatedDelta"; }
+    ag::variable_list apply(ag::variable_list &&grads) override {
+        return run(std::move(grads), [this](const Tensor *const *t, const ag::variable_list &g) {
+            const Tensor &v = *t[2];
+            const Tensor dO = g[0].defined() ? unit(g[0]) : at::zeros_like(v, at::MemoryFormat::Contiguous);
+            auto d = delta_backward(t, scale, dO, g[1].defined() ? g[1].contiguous() : g[1], *t[7], Py_None, Py_None);
+            return ag::variable_list(d.begin(), d.end());
+        });
+    }
+};
+// delta_apply(the inputs, scale, keep) -> o, final_states in a graph
+PyObject *delta_apply(PyObject *const *a) {
+    const Tensor *t[8];
+    for (int i = 0; i < 7; ++i) t[i] = &arg(a[i], delta_names[i], i >= 5);
+    const auto scale = number(a[7], "scale");
+    const bool graph = graph_wanted(t, 6);
+    const DeltaOut out = delta_forward(t, scale, true, -1, graph && a[8] == Py_True, Py_None);
+    if (graph) {
+        t[7] = &out.kept;
+        std::shared_ptr<GatedDelta> node(new GatedDelta(), ag::deleteNode);
+        node->scale = scale;
+        node->set_next_edges(ag::collect_next_edges(*t[0], *t[1], *t[2], *t[3], *t[4], *t[5]));
+        node->save(t);
+        ag::set_history(out.o, node);
+        ag::set_history(out.final, node);
+    }
+    PyObject *r = PyTuple_New(2);
+    if (!r) throw Raised();
+    PyTuple_SET_ITEM(r, 0, wrap(out.o));
+    PyTuple_SET_ITEM(r, 1, wrap(out.final));
+    return r;
 }
 
 // delta_step(state, q, k, v, g, beta, scale, state_indices, stream)
@@ -609,7 +728,7 @@ PyObject *delta_step(PyObject *const *a) {
     like("state", state, {slots, H, V, K}, F32 | BF16, dev, 3);
     if (idx.defined()) like("state_indices", idx, {n}, I32, dev, 1);
     else NEED(slots >= n, "the state pool has fewer slots than there are requests");
-    const double scale = number(a[6], "scale", K > 0 ? 1.0 / sqrt((double)K) : 1.0);
+    const double scale = number(a[6], "scale").value_or(K > 0 ? 1.0 / sqrt((double)K) : 1.0);
     const Stream st(a[8], dev);
     Tensor o = st.output(v.sizes(), v.scalar_type());
     const ssd_delta_step_problem p{n, slots, H, V, G, K, state.stride(0), q.stride(0), k.stride(0), v.stride(0), g.stride(0), beta.stride(0),
@@ -627,8 +746,14 @@ struct Qk {
     ssd_qk_args f;
 };
 const char *const qk_names[7] = {"q", "k", "q_weight", "k_weight", "cos", "sin", "positions"};
-// q, k, q_weight, k_weight, cos, sin, positions; mode, interleaved, eps
-Qk qk_inputs(const Tensor *const *t, PyObject *mode, PyObject *interleaved, PyObject *eps) {
+struct QkHow {
+    int32_t mode;
+    bool interleaved;
+    float eps;
+};
+QkHow qk_how(PyObject *const *a) { return {(int32_t)PyLong_AsLong(a[0]), a[1] == Py_True, (float)number(a[2], "eps").value_or(1e-6)}; }
+// q, k, q_weight, k_weight, cos, sin, positions
+Qk qk_inputs(const Tensor *const *t, const QkHow &how) {
     const Tensor &q = *t[0], &k = *t[1], &wq = *t[2], &wk = *t[3], &cos = *t[4], &sin = *t[5], &pos = *t[6];
     Qk s{};
     const int dev = s.dev = lead("q", q, 4), own = type_of(q);
@@ -656,58 +781,96 @@ Qk qk_inputs(const Tensor *const *t, PyObject *mode, PyObject *interleaved, PyOb
         NEED(rotary <= s.D, "the rotation is wider than the heads");
     }
     if (pos.defined()) like("positions", pos, {s.B, s.L}, I32, dev, 1);
-    s.p = {s.B, s.L, s.Hq, s.Hk, s.D, rotary, rows, pos.defined() ? pos.stride(0) : 0, (float)number(eps, "eps", 1e-6), code(q),
-           (int32_t)PyLong_AsLong(mode), interleaved == Py_True};
+    s.p = {s.B, s.L, s.Hq, s.Hk, s.D, rotary, rows, pos.defined() ? pos.stride(0) : 0, how.eps, code(q), how.mode, how.interleaved};
     s.f.q = desc(q, 1); s.f.k = desc(k, 1);
     s.f.q_weight = ptr_as<float>(wq); s.f.k_weight = ptr_as<float>(wk); s.f.cos = ptr_as<float>(cos); s.f.sin = ptr_as<float>(sin);
     s.f.positions = ptr_as<int32_t>(pos);
     return s;
 }
 
+std::array<Tensor, 2> qk_forward(const Tensor *const *t, const QkHow &how, PyObject *stream) {
+    Qk s = qk_inputs(t, how);
+    const Stream st(stream, s.dev);
+    std::array<Tensor, 2> out = {st.output({s.B, s.L, s.Hq, s.D}, t[0]->scalar_type()), Tensor()};
+    s.f.q_out = desc(out[0], 4);
+    if (t[1]->defined()) {
+        out[1] = st.output({s.B, s.L, s.Hk, s.D}, t[0]->scalar_type());
+        s.f.k_out = desc(out[1], 4);
+    }
+    check(lib.qk_fwd(&s.p, &s.f, st.handle), "ssd_qk_norm_fwd");
+    return out;
+}
+PyObject *pair_of(const std::array<Tensor, 2> &t) {
+    PyObject *r = PyTuple_New(2);
+    if (!r) throw Raised();
+    PyTuple_SET_ITEM(r, 0, wrap(t[0]));
+    PyTuple_SET_ITEM(r, 1, wrap_or_none(t[1]));
+    return r;
+}
 // qk_fwd(the inputs, mode, interleaved, eps, stream)
 PyObject *qk_fwd(PyObject *const *a) {
     const Tensor *t[7];
-    for (int i = 0; i < 7; ++i) t[i] = &arg(a[i], qk_names[i], i >= 1);
-    Qk s = qk_inputs(t, a[7], a[8], a[9]);
-    const Stream st(a[10], s.dev);
-    Tensor q = st.output({s.B, s.L, s.Hq, s.D}, t[0]->scalar_type()), k;
-    s.f.q_out = desc(q, 4);
-    if (t[1]->defined()) {
-        k = st.output({s.B, s.L, s.Hk, s.D}, t[0]->scalar_type());
-        s.f.k_out = desc(k, 4);
-    }
-    check(lib.qk_fwd(&s.p, &s.f, st.handle), "ssd_qk_norm_fwd");
-    PyObject *r = PyTuple_New(2);
-    if (!r) throw Raised();
-    PyTuple_SET_ITEM(r, 0, wrap(q));
-    PyTuple_SET_ITEM(r, 1, k.defined() ? wrap(k) : Py_NewRef(Py_None));
-    return r;
+    read(a, qk_names, 1, t);
+    return pair_of(qk_forward(t, qk_how(a + 7), a[10]));
 }
 
-// qk_bwd(the inputs, mode, interleaved, eps, dq_out, dk_out, workspace, stream)
-PyObject *qk_bwd(PyObject *const *a) {
-    const Tensor *t[7];
-    for (int i = 0; i < 7; ++i) t[i] = &arg(a[i], qk_names[i], i >= 1);
-    Qk s = qk_inputs(t, a[7], a[8], a[9]);
-    const Tensor &dq = arg(a[10], "dq"), &dk = arg(a[11], "dk", true);
+const char *const qk_grad_names[4] = {"dq", "dk", "dq_weight", "dk_weight"};
+std::array<Tensor, 4> qk_backward(const Tensor *const *t, const QkHow &how, const Tensor &dq, const Tensor &dk, PyObject *workspace, PyObject *stream) {
+    Qk s = qk_inputs(t, how);
     NEED(dk.defined() == t[1]->defined(), "dk is given where k is");
     like("dq", dq, {s.B, s.L, s.Hq, s.D}, type_of(*t[0]), s.dev, 1);
     if (dk.defined()) like("dk", dk, {s.B, s.L, s.Hk, s.D}, type_of(*t[0]), s.dev, 1);
-    const Stream st(a[13], s.dev);
+    const Stream st(stream, s.dev);
     ssd_qk_bwd_args b{};
     b.fwd = s.f;
     b.dq_out = desc(dq, 1); b.dk_out = desc(dk, 1);
-    Grads d(st);
-    b.dq = desc(d.out("dq", {s.B, s.L, s.Hq, s.D}, t[0]->scalar_type()), 4);
-    if (dk.defined()) b.dk = desc(d.out("dk", {s.B, s.L, s.Hk, s.D}, t[0]->scalar_type()), 4);
-    if (t[2]->defined()) b.dq_weight = ptr_as<float>(d.out("dq_weight", {s.D}, at::kFloat));
-    if (t[3]->defined()) b.dk_weight = ptr_as<float>(d.out("dk_weight", {s.D}, at::kFloat));
+    std::array<Tensor, 4> d = {st.output({s.B, s.L, s.Hq, s.D}, t[0]->scalar_type()), Tensor(), Tensor(), Tensor()};
+    if (dk.defined()) d[1] = st.output({s.B, s.L, s.Hk, s.D}, t[0]->scalar_type());
+    if (t[2]->defined()) d[2] = st.output({s.D}, at::kFloat);
+    if (t[3]->defined()) d[3] = st.output({s.D}, at::kFloat);
+    b.dq = desc(d[0], 4); b.dk = desc(d[1], 4);
+    b.dq_weight = ptr_as<float>(d[2]); b.dk_weight = ptr_as<float>(d[3]);
     size_t n = 0;
     check(lib.qk_bwd_workspace_size(&s.p, &n), "ssd_qk_norm_bwd_workspace_size");
     Tensor ws;
-    if (b.dq_weight || b.dk_weight) ws = workspace_of(a[12], n, st);
+    if (b.dq_weight || b.dk_weight) ws = workspace_of(workspace, n, st);
     check(lib.qk_bwd(&s.p, &b, ptr(ws), ws.defined() ? ws.nbytes() : 0, st.handle), "ssd_qk_norm_bwd");
-    return d.take();
+    return d;
+}
+// qk_bwd(the inputs, mode, interleaved, eps, dq_out, dk_out, workspace, stream)
+PyObject *qk_bwd(PyObject *const *a) {
+    const Tensor *t[7];
+    read(a, qk_names, 1, t);
+    return dict_of(qk_backward(t, qk_how(a + 7), arg(a[10], "dq"), arg(a[11], "dk", true), a[12], a[13]), qk_grad_names);
+}
+
+struct QKNorm : OpNode<7> {
+    QkHow how;
+    std::string name() const override { return "QKNorm"; }
+    ag::variable_list apply(ag::variable_list &&grads) override {
+        return run(std::move(grads), [this](const Tensor *const *t, const ag::variable_list &g) {
+            Tensor d[2];                                     // an output that nothing came of: zeros
+            for (int i = 0; i < 2; ++i)
+                if (t[i]->defined()) d[i] = g[i].defined() ? unit(g[i]) : at::zeros_like(*t[i], at::MemoryFormat::Contiguous);
+            auto r = qk_backward(t, how, d[0], d[1], Py_None, Py_None);
+            return ag::variable_list(r.begin(), r.end());
+        });
+    }
+};
+// qk_apply(the inputs, mode, interleaved, eps) -> q_out, k_out in a graph
+PyObject *qk_apply(PyObject *const *a) {
+    const Tensor *t[7];
+    read(a, qk_names, 1, t);
+    const QkHow how = qk_how(a + 7);
+    const auto out = qk_forward(t, how, Py_None);
+    if (graph_wanted(t, 4)) {
+        std::shared_ptr<QKNorm> node(new QKNorm(), ag::deleteNode);
+        node->how = how;
+        node->set_next_edges(ag::collect_next_edges(*t[0], *t[1], *t[2], *t[3]));
+        node->save(t);
+        for (const Tensor &o : out) ag::set_history(o, node);
+    }
+    return pair_of(out);
 }
 
 // init(SSDError, torch.OutOfMemoryError, addresses of the library's functions in Lib's order)
@@ -732,6 +895,8 @@ PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n) {
     try {
         return F(a);
     } catch (const Raised &) {
+    } catch (python_error &e) {                              // (of a hook on saved tensors)
+        e.restore();
     } catch (const c10::OutOfMemoryError &e) {
         PyErr_SetString(out_of_memory ? out_of_memory : PyExc_MemoryError, e.what_without_backtrace());
     } catch (const c10::Error &e) {
@@ -746,6 +911,7 @@ PyMethodDef methods[] = {ENTRY(step, 12),          ENTRY(conv1d_prompt, 9), ENTR
                          ENTRY(snapshot, 7),       ENTRY(selective_fwd, 14), ENTRY(selective_bwd, 15),
                          ENTRY(delta_fwd, 12),     ENTRY(delta_bwd, 13),    ENTRY(delta_step, 9),
                          ENTRY(qk_fwd, 11),        ENTRY(qk_bwd, 14),
+                         ENTRY(delta_apply, 9),    ENTRY(qk_apply, 10),
                          ENTRY(init, 2 + sizeof(Lib) / sizeof(void *)),      {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
