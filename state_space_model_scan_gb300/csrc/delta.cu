@@ -87,7 +87,7 @@ Kept kept_plan(const ssd_delta_problem *p) {
     return k;
 }
 struct Plan {
-    size_t hdr, gates, sys, att, a, tiles, seg, dS, mu, part, kept, total;
+    size_t hdr, gates, sys, att, a, tiles, seg, dS, mu, flow, part, kept, total;
     int nseg, seg0, seglen;
 };
 Plan plan(const ssd_delta_problem *p, bool back, bool kept) {
@@ -110,6 +110,7 @@ Plan plan(const ssd_delta_problem *p, bool back, bool kept) {
     if (back) {
         w.dS = take(ch * state_bytes(p));
         w.mu = take(ch * value_bytes(p));
+        w.flow = take(tc ? 0 : ch * delta_grad_shares(slots(p), p->nheads, p->dstate) * DELTA_FLOW * 4);
         w.part = take(!tc && p->nheads > p->ngroups ? 2 * ch * DQ * p->dstate * 4 : 0);
         w.kept = take(kept ? 0 : kept_plan(p).total);
     }
@@ -253,6 +254,7 @@ ssd_status ssd_delta_bwd(const ssd_delta_problem *p, const ssd_delta_bwd_args *b
     a.dinit = b->dinitial_states.ptr; a.dinit_bf16 = b->dinitial_states.dtype == SSD_BF16;
     a.dS = ws + w.dS;
     a.mu = ws + w.mu;
+    a.flow = reinterpret_cast<float *>(ws + w.flow);
     a.part = !on_tensor_cores(p) && p->nheads > p->ngroups ? reinterpret_cast<float *>(ws + w.part) : nullptr;
     return of_cuda(on_tensor_cores(p) && a.nslots > 0 ? delta_tc_bwd(a, maps(p, f, a, b, b->dv), st) : delta_simt_bwd(a, p->dtype == SSD_BF16, st));
 }

@@ -50,6 +50,7 @@ struct DeltaArgs {
     // state entering each chunk and U (kept by a training forward), gradient of the state leaving each chunk and mu: SIMT
     // [nslots][H][V][K] and [nslots][H][64][V] fp32, tensor-core path [nslots][H] operand images of 32 KB and [64][128] bf16
     void *S, *U, *dS, *mu;
+    float *flow;                // SIMT backward: [nslots][H][shares][DELTA_FLOW]: what dg is made of
     float *part;                // [2][nslots][H][64][K]: dq and dk of each value head, where heads share a group
     void *tiles;                // tensor-core path: operand images of every chunk and head, `both` for a backward too
     bool both, fresh;           // fresh: a backward's first launch clears the header
@@ -224,6 +225,15 @@ __device__ __forceinline__ void delta_invert(float *M, float *t, int tid) {
             __syncthreads();
         }
     }
+}
+
+// Into how many shares of its keys (slices of 32) a chunk's gradients are cut, so that the blocks fill the SMs; every share
+// computes the chunk's matrices again, a fifth of a block's work at 64 keys.
+constexpr int DELTA_FLOW = 3 * DQ + 1;
+constexpr int64_t kDeltaSMs = 152;
+inline int delta_grad_shares(int64_t nslots, int64_t H, int64_t K) {
+    const int64_t n = nslots * H, most = (K + 31) / 32, fit = n > 0 ? kDeltaSMs / n : 1;
+    return (int)(fit < 1 ? 1 : fit < most ? fit : most);
 }
 
 // delta_simt.cu: any type and size.  states: leave a.S and a.U (and no o, where a.o is NULL).

@@ -2,11 +2,11 @@
 // does not take (fp32 data among them, which is computed in fp32 throughout).
 //
 // Four kernels (formulas in delta.cuh): k_prep, a block a chunk and head: the triangular system's inverse and att;
-// k_chain, a block a sequence, head and 32 values, from chunk to chunk with its rows of the state in shared memory,
-// forwards (o, states, U) or backwards (mu, dS); k_grads, a block a chunk and head: everything else of the
-// gradients; k_share, the sum over the heads that share a group.  Products go through shared memory in slices of 32,
-// a thread a few rows and columns of the result.  Bound by the chain's shared-memory reads: one chunk of 64 tokens
-// at dstate 128 takes about 11 us, whatever the number of heads, until the card is full.
+// k_chain, a block a sequence, head and 8, 16 or 32 values, from chunk to chunk with its rows of the state in shared memory,
+// forwards (o, states, U) or backwards (mu, dS); k_grads, a block a chunk, head and share of the keys: everything else of the
+// gradients; k_finish, what is summed over those blocks.  Products go through shared memory in slices of 32,
+// a thread a few rows and columns of the result, and its reads are what bounds the chain: 75% of its cycles with 32 values.  A chunk of 64 tokens
+// at dstate 64 takes 6 us with 8 values a block, 11 with 32, whatever the number of heads, until the card is full.
 #include "delta.cuh"
 
 namespace ssd {
@@ -14,14 +14,13 @@ namespace ssd {
 namespace {
 
 constexpr int NT = 256;
-constexpr int VS = 32;              // values of a chain block
 constexpr int LD = 36;              // row stride of a slice of 32: rows of 16-byte pieces, four banks apart
 constexpr int MLD = DELTA_ML;
 
 // rows [0, 64) of a slice of 32 columns from column k0 of a chunk's rows (row stride `step` elements); zeros past the chunk and past n
-template <typename T>
+template <int N, typename T>
 __device__ __forceinline__ void load_slice(float *to, const T *p, int64_t step, int len, int k0, int n, int tid) {
-    for (int e = tid; e < 64 * 32; e += NT) {
+    for (int e = tid; e < 64 * 32; e += N) {
         const int i = e / 32, c = e % 32;
         to[i * LD + c] = i < len && k0 + c < n ? to_f(p[i * step + k0 + c]) : 0.f;
     }
@@ -30,7 +29,7 @@ template <typename T>
 __device__ __forceinline__ const T *rows_of(const void *p, const int64_t *s, const DeltaChunk &c, int h) {
     return static_cast<const T *>(p) + c.b * s[0] + c.t0 * s[1] + h * s[2];
 }
-// R x 2 of a product over a slice of n: rows 16 r + ty of A, columns 2 tx and 2 tx + 1 of B [n][ldb]
+// R x 2 of a product over a slice of n: rows 64 / R r + ty of A, columns 2 tx and 2 tx + 1 of B [n][ldb]
 template <int R>
 __device__ __forceinline__ void fma_slice(float (&acc)[R][2], const float *A, int lda, const float *B, int ldb, int n, int ty, int tx) {
 #pragma unroll 4
@@ -40,7 +39,7 @@ __device__ __forceinline__ void fma_slice(float (&acc)[R][2], const float *A, in
         for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const float2 *>(B + (l + e) * ldb + 2 * tx);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float4 x = *reinterpret_cast<const float4 *>(A + (16 * r + ty) * lda + l);
+            const float4 x = *reinterpret_cast<const float4 *>(A + (64 / R * r + ty) * lda + l);
             const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -58,22 +57,23 @@ __device__ __forceinline__ void fma_slice_t(float (&acc)[R][2], const float *A, 
         const float2 b = *reinterpret_cast<const float2 *>(B + l * ldb + 2 * tx);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float x = A[l * lda + 16 * r + ty];
+            const float x = A[l * lda + 64 / R * r + ty];
             acc[r][0] = fmaf(x, b.x, acc[r][0]);
             acc[r][1] = fmaf(x, b.y, acc[r][1]);
         }
     }
 }
-// x[r][s] += rows 16 r + ty of A times rows 16 s + tx of B, y of A2 (all [64][LD], a slice of 32)
-__device__ __forceinline__ void mul_rows(float (&x)[4][4], float (&y)[4][4], const float *A, const float *A2, const float *B, int ty, int tx) {
+// x[r][s] += rows 64 / R r + ty of A times rows 16 s + tx of B, y of A2 (all [64][LD], a slice of 32)
+template <int R>
+__device__ __forceinline__ void mul_rows(float (&x)[R][4], float (&y)[R][4], const float *A, const float *A2, const float *B, int ty, int tx) {
 #pragma unroll 2
     for (int l = 0; l < 32; l += 4) {
         float4 b[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) b[s] = *reinterpret_cast<const float4 *>(B + (16 * s + tx) * LD + l);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float4 u = *reinterpret_cast<const float4 *>(A + (16 * r + ty) * LD + l), v = *reinterpret_cast<const float4 *>(A2 + (16 * r + ty) * LD + l);
+        for (int r = 0; r < R; ++r) {
+            const float4 u = *reinterpret_cast<const float4 *>(A + (64 / R * r + ty) * LD + l), v = *reinterpret_cast<const float4 *>(A2 + (64 / R * r + ty) * LD + l);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 x[r][s] = fmaf(u.x, b[s].x, fmaf(u.y, b[s].y, fmaf(u.z, b[s].z, fmaf(u.w, b[s].w, x[r][s]))));
@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(NT) k_prep(const DeltaArgs a, const bool back)
         for (int s = 0; s < 4; ++s) kk[r][s] = qk[r][s] = 0.f;
     for (int k0 = 0; k0 < a.K; k0 += 32) {
         __syncthreads();
-        load_slice(Ks, k, a.ks[1], c.len, k0, a.K, tid);
-        load_slice(Qs, q, a.qs[1], c.len, k0, a.K, tid);
+        load_slice<NT>(Ks, k, a.ks[1], c.len, k0, a.K, tid);
+        load_slice<NT>(Qs, q, a.qs[1], c.len, k0, a.K, tid);
         __syncthreads();
         mul_rows(kk, qk, Ks, Qs, Ks, ty, tx);
     }
@@ -130,12 +130,16 @@ __global__ void __launch_bounds__(NT) k_prep(const DeltaArgs a, const bool back)
 
 // ---- the chain.  Shared memory, in floats: the state's rows [VS][KL]; Y, Z [64][XL] of this block's values; and one or two stages (two
 // where they fit) of what a chunk needs: K and Q [64][KL], V or dO [64][XL], the inverse and att [64][ML], the gates.
-constexpr int XL = VS + 4, ML = DELTA_ML;     // rows of 16-byte pieces, four banks apart
+// 16 threads for each of a block's VS values: two rows and two values a thread.
+constexpr int ML = DELTA_ML;                  // rows of 16-byte pieces, four banks apart; XL of VS values: an odd number of pieces
+constexpr int chain_threads(int VS) { return 16 * VS; }
+constexpr int chain_row(int VS) { return VS + 4; }
 struct ChainSizes {
     int KP, KL, stage, stages, bytes;
 };
-__host__ __device__ inline ChainSizes chain_sizes(int K) {
+__host__ __device__ inline ChainSizes chain_sizes(int K, int VS) {
     ChainSizes z;
+    const int XL = chain_row(VS);
     z.KP = (K + 3) / 4 * 4;
     z.KL = z.KP + (z.KP % 8 == 0 ? 4 : 8);     // an odd number of pieces
     z.stage = 2 * 64 * z.KL + 64 * XL + 2 * 64 * ML + DGATES;
@@ -151,40 +155,44 @@ __device__ __forceinline__ void copy_async1(float *to, const float *from, bool i
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(in ? 4 : 0) : "memory");
 }
 // rows [0, 64) x columns [c0, c0 + W), W a multiple of 4, of a token tensor of n columns, zeros past `len` rows and n.  fp32 in the background.
-template <typename T>
+template <int N, typename T>
 __device__ __forceinline__ void load_tile(float *to, int ld, const T *p, int64_t step, int len, int c0, int W, int n, bool vec, int tid) {
     if constexpr (sizeof(T) == 4) {
         if (vec) {
-            for (int e = tid; e < 64 * (W / 4); e += NT) {
+            for (int e = tid; e < 64 * (W / 4); e += N) {
                 const int i = e / (W / 4), c = e % (W / 4) * 4, left = i < len ? min(4, max(0, n - c0 - c)) : 0;
                 copy_async(to + i * ld + c, left > 0 ? p + i * step + c0 + c : p, left);
             }
         } else {
-            for (int e = tid; e < 64 * W; e += NT) {
+            for (int e = tid; e < 64 * W; e += N) {
                 const int i = e / W, c = e % W;
                 const bool in = i < len && c0 + c < n;
                 copy_async1(to + i * ld + c, in ? p + i * step + c0 + c : p, in);
             }
         }
     } else {
-        for (int e = tid; e < 64 * W; e += NT) {
+        for (int e = tid; e < 64 * W; e += N) {
             const int i = e / W, c = e % W;
             to[i * ld + c] = i < len && c0 + c < n ? to_f(p[i * step + c0 + c]) : 0.f;
         }
     }
 }
-// C[i][v] += sum over j <= i of A[i][j] B[j][v]: rows i = ig + 16 r, columns v = 2 vg, 2 vg + 1
-__device__ __forceinline__ void mul_lower(float (&C)[4][2], const float *A, const float *B, int ig, int vg) {
+// C[i][v] += sum over j <= i of A[i][j] B[j][v]: rows i = ig + 32 r, columns v = 2 vg, 2 vg + 1
+template <int XL>
+__device__ __forceinline__ void mul_lower(float (&C)[2][2], const float *A, const float *B, int ig, int vg) {
+    const int ib = ig / 16;                                 // (the same for a warp's threads)
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb) {
+        if (jb > 2 + ib) break;
 #pragma unroll
         for (int j = 16 * jb; j < 16 * jb + 16; j += 4) {
             float2 b[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const float2 *>(B + (j + e) * XL + 2 * vg);
 #pragma unroll
-            for (int r = jb; r < 4; ++r) {
-                const float4 x = *reinterpret_cast<const float4 *>(A + (ig + 16 * r) * ML + j);
+            for (int r = 0; r < 2; ++r) {
+                if (r == 0 && jb > ib) continue;
+                const float4 x = *reinterpret_cast<const float4 *>(A + (ig + 32 * r) * ML + j);
                 const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -195,33 +203,28 @@ __device__ __forceinline__ void mul_lower(float (&C)[4][2], const float *A, cons
         }
     }
 }
-// C[j][v] += sum over i >= j of A[i][j] B[i][v]: rows j = 4 ig + r
-__device__ __forceinline__ void mul_lower_t(float (&C)[4][2], const float *A, const float *B, int ig, int vg) {
+// C[j][v] += sum over i >= j of A[i][j] B[i][v]: rows j = 2 ig + r
+template <int XL>
+__device__ __forceinline__ void mul_lower_t(float (&C)[2][2], const float *A, const float *B, int ig, int vg) {
 #pragma unroll 8
-    for (int i = ig / 4 * 16; i < 64; ++i) {
-        const float4 x = *reinterpret_cast<const float4 *>(A + i * ML + 4 * ig);
+    for (int i = ig / 8 * 16; i < 64; ++i) {
+        const float2 x = *reinterpret_cast<const float2 *>(A + i * ML + 2 * ig);
         const float2 b = *reinterpret_cast<const float2 *>(B + i * XL + 2 * vg);
-        const float xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            C[r][0] = fmaf(xs[r], b.x, C[r][0]);
-            C[r][1] = fmaf(xs[r], b.y, C[r][1]);
-        }
+        C[0][0] = fmaf(x.x, b.x, C[0][0]);
+        C[0][1] = fmaf(x.x, b.y, C[0][1]);
+        C[1][0] = fmaf(x.y, b.x, C[1][0]);
+        C[1][1] = fmaf(x.y, b.y, C[1][1]);
     }
 }
 // D[v][k] += sum over i of W[i][v] K[i][k]: TV values from v0 on, four keys
-template <int TV>
+template <int TV, int XL>
 __device__ __forceinline__ void mul_state(float (&D)[TV][4], const float *W, const float *K, int KL) {
 #pragma unroll 8
     for (int i = 0; i < 64; ++i) {
         const float4 k = *reinterpret_cast<const float4 *>(K + i * KL);
         float w[TV];
 #pragma unroll
-        for (int e = 0; e < TV; e += 2) {
-            const float2 u = *reinterpret_cast<const float2 *>(W + i * XL + e);
-            w[e] = u.x;
-            w[e + 1] = u.y;
-        }
+        for (int e = 0; e < TV; ++e) w[e] = W[i * XL + e];
 #pragma unroll
         for (int e = 0; e < TV; ++e) {
             D[e][0] = fmaf(w[e], k.x, D[e][0]);
@@ -232,13 +235,13 @@ __device__ __forceinline__ void mul_state(float (&D)[TV][4], const float *W, con
     }
 }
 // S[v][k] = whole S + W^T K (+ Z^T Q), tiles of TV values x 4 keys
-template <int TV, bool BACK>
+template <int TV, int VS, bool BACK>
 __device__ __forceinline__ void update_state(float *S, const float *W, const float *Z, const float *K, const float *Q, float whole, int KP, int KL, int tid) {
-    for (int t = tid; t < VS / TV * (KP / 4); t += NT) {
+    for (int t = tid; t < VS / TV * (KP / 4); t += chain_threads(VS)) {
         const int v0 = t % (VS / TV) * TV, k0 = t / (VS / TV) * 4;
         float D[TV][4] = {};
-        mul_state<TV>(D, W + v0, K + k0, KL);
-        if (BACK) mul_state<TV>(D, Z + v0, Q + k0, KL);
+        mul_state<TV, chain_row(VS)>(D, W + v0, K + k0, KL);
+        if (BACK) mul_state<TV, chain_row(VS)>(D, Z + v0, Q + k0, KL);
 #pragma unroll
         for (int e = 0; e < TV; ++e) {
             float4 *p = reinterpret_cast<float4 *>(S + (v0 + e) * KL + k0);
@@ -248,14 +251,15 @@ __device__ __forceinline__ void update_state(float *S, const float *W, const flo
     }
 }
 
-template <typename T, bool BACK>
-__global__ void __launch_bounds__(NT) k_chain(const DeltaArgs a) {
+template <typename T, bool BACK, int VS>
+__global__ void __launch_bounds__(chain_threads(VS), 1) k_chain(const DeltaArgs a) {
+    constexpr int XL = chain_row(VS), N_ = chain_threads(VS);
     after_previous();
     extern __shared__ float sm[];
-    const ChainSizes z = chain_sizes(a.K);
+    const ChainSizes z = chain_sizes(a.K, VS);
     const int KP = z.KP, KL = z.KL;
     float *S = sm, *Y = S + VS * KL, *Z = Y + 64 * XL, *stages = Z + 64 * XL;
-    const int nv = (a.V + VS - 1) / VS, tid = threadIdx.x, ig = tid / 16, vg = tid % 16;
+    const int nv = (a.V + VS - 1) / VS, tid = threadIdx.x, ig = tid / (VS / 2), vg = tid % (VS / 2);
     const int v0 = blockIdx.x % nv * VS, h = blockIdx.x / nv % a.H, s = blockIdx.x / nv / a.H, grp = h / (a.H / a.G);
     const DeltaSeq q = delta_seq(a, s);
     const int64_t sat = ((int64_t)s * a.H + h) * a.V * a.K;
@@ -265,22 +269,22 @@ __global__ void __launch_bounds__(NT) k_chain(const DeltaArgs a) {
         const DeltaChunk c{q.b, q.t0 + ci * DQ, min(DQ, q.len - ci * DQ)};
         const int64_t ch = (int64_t)(q.slot0 + ci) * a.H + h;
         float *st = stages + (z.stages == 2 ? n & 1 : 0) * z.stage;
-        load_tile(st, KL, rows_of<T>(a.k, a.ks, c, grp), a.ks[1], c.len, 0, KP, a.K, a.vk, tid);
-        if (BACK || a.o) load_tile(st + 64 * KL, KL, rows_of<T>(a.q, a.qs, c, grp), a.qs[1], c.len, 0, KP, a.K, a.vq, tid);
-        if (BACK) load_tile(st + 128 * KL, XL, rows_of<T>(a.dO, a.dos, c, h), a.dos[1], c.len, v0, VS, a.V, a.vo, tid);
-        else load_tile(st + 128 * KL, XL, rows_of<T>(a.v, a.vs, c, h), a.vs[1], c.len, v0, VS, a.V, a.vv, tid);
+        load_tile<N_>(st, KL, rows_of<T>(a.k, a.ks, c, grp), a.ks[1], c.len, 0, KP, a.K, a.vk, tid);
+        if (BACK || a.o) load_tile<N_>(st + 64 * KL, KL, rows_of<T>(a.q, a.qs, c, grp), a.qs[1], c.len, 0, KP, a.K, a.vq, tid);
+        if (BACK) load_tile<N_>(st + 128 * KL, XL, rows_of<T>(a.dO, a.dos, c, h), a.dos[1], c.len, v0, VS, a.V, a.vo, tid);
+        else load_tile<N_>(st + 128 * KL, XL, rows_of<T>(a.v, a.vs, c, h), a.vs[1], c.len, v0, VS, a.V, a.vv, tid);
         float *M = st + 128 * KL + 64 * XL;
-        for (int e = tid; e < 64 * 16; e += NT) {
+        for (int e = tid; e < 64 * 16; e += N_) {
             copy_async(M + e / 16 * ML + e % 16 * 4, a.sys + ch * 4096 + e * 4, 4);
             copy_async(M + 64 * ML + e / 16 * ML + e % 16 * 4, a.att + ch * 4096 + e * 4, 4);
         }
-        for (int e = tid; e < DGATES / 4; e += NT) copy_async(M + 2 * 64 * ML + e * 4, a.gates + ch * DGATES + e * 4, 4);
+        for (int e = tid; e < DGATES / 4; e += N_) copy_async(M + 2 * 64 * ML + e * 4, a.gates + ch * DGATES + e * 4, 4);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (nch > 0) issue(0);
     const void *in = BACK ? a.dfinal : a.init;
     const bool in16 = BACK ? a.dfinal_bf16 : a.init_bf16;
-    for (int e = tid; e < VS * KP; e += NT) {
+    for (int e = tid; e < VS * KP; e += N_) {
         const int v = e / KP, k = e % KP;
         S[v * KL + k] = in && v0 + v < a.V && k < a.K ? delta_ld(in, !in16, sat + (int64_t)(v0 + v) * a.K + k) : 0.f;
     }
@@ -298,21 +302,21 @@ __global__ void __launch_bounds__(NT) k_chain(const DeltaArgs a) {
         __syncthreads();
         const float *Ks = stages + (z.stages == 2 ? n & 1 : 0) * z.stage, *Qs = Ks + 64 * KL, *Xs = Qs + 64 * KL, *Ms = Xs + 64 * XL, *Ma = Ms + 64 * ML, *gate = Ma + 64 * ML;
         if (kept)
-            for (int e = tid; e < VS * KP; e += NT) {
+            for (int e = tid; e < VS * KP; e += N_) {
                 const int v = e / KP, k = e % KP;
                 if (v0 + v < a.V && k < a.K) kept[(ch * a.V + v0 + v) * a.K + k] = S[v * KL + k];
             }
-        // P = K S^T and, forwards, Q S^T: rows ig + 16 r (backwards 4 ig + r), columns 2 vg, 2 vg + 1
-        float P[4][2] = {}, O[4][2] = {};
+        // P = K S^T and, forwards, Q S^T: rows ig + 32 r (backwards 2 ig + r), columns 2 vg, 2 vg + 1
+        float P[2][2] = {}, O[2][2] = {};
         const bool outs = !BACK && a.o;
-        auto rw = [&](int r) { return BACK ? 4 * ig + r : ig + 16 * r; };
+        auto rw = [&](int r) { return BACK ? 2 * ig + r : ig + 32 * r; };
 #pragma unroll 2
         for (int l = 0; l < KP; l += 4) {
             float4 b[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) b[e] = *reinterpret_cast<const float4 *>(S + (2 * vg + e) * KL + l);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int r = 0; r < 2; ++r) {
                 const float4 x = *reinterpret_cast<const float4 *>(Ks + rw(r) * KL + l);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) P[r][e] = fmaf(x.x, b[e].x, fmaf(x.y, b[e].y, fmaf(x.z, b[e].z, fmaf(x.w, b[e].w, P[r][e]))));
@@ -323,10 +327,10 @@ __global__ void __launch_bounds__(NT) k_chain(const DeltaArgs a) {
                 }
             }
         }
-        float N[4][2] = {};
-        if (BACK) mul_lower_t(N, Ma, Xs, ig, vg);           // N = scale att^T dO + e^(Gc - G) P
+        float N[2][2] = {};
+        if (BACK) mul_lower_t<XL>(N, Ma, Xs, ig, vg);           // N = scale att^T dO + e^(Gc - G) P
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < 2; ++r) {
             const int i = rw(r);
             float2 y;
             if (BACK) {
@@ -338,13 +342,13 @@ __global__ void __launch_bounds__(NT) k_chain(const DeltaArgs a) {
             *reinterpret_cast<float2 *>(Y + i * XL + 2 * vg) = y;
         }
         __syncthreads();
-        float U[4][2] = {};
-        if (BACK) mul_lower_t(U, Ms, Y, ig, vg);
-        else mul_lower(U, Ms, Y, ig, vg);
+        float U[2][2] = {};
+        if (BACK) mul_lower_t<XL>(U, Ms, Y, ig, vg);
+        else mul_lower<XL>(U, Ms, Y, ig, vg);
         __syncthreads();
         // W = beta U, or lam; what goes to the state: e^(Gc - G) W in Z, backwards -e^G lam in Y and scale e^G dO in Z
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < 2; ++r) {
             const int i = rw(r);
             if (vals)
 #pragma unroll
@@ -363,19 +367,19 @@ __global__ void __launch_bounds__(NT) k_chain(const DeltaArgs a) {
         __syncthreads();
         const float whole = gate[DQ - 1];
         if (outs) {
-            float A[4][2] = {};
-            mul_lower(A, Ma, Y, ig, vg);
+            float A[2][2] = {};
+            mul_lower<XL>(A, Ma, Y, ig, vg);
             T *op = static_cast<T *>(a.o) + c.b * a.os[0] + c.t0 * a.os[1] + h * a.os[2] + v0;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int i = ig + 16 * r, v = 2 * vg + e;
+                    const int i = ig + 32 * r, v = 2 * vg + e;
                     if (i < c.len && v0 + v < a.V) op[i * a.os[1] + v] = from_f<T>(a.scale * fmaf(gate[i], O[r][e], A[r][e]));
                 }
         }
-        if (KP > 64) update_state<4, BACK>(S, BACK ? Y : Z, Z, Ks, Qs, whole, KP, KL, tid);
-        else update_state<2, BACK>(S, BACK ? Y : Z, Z, Ks, Qs, whole, KP, KL, tid);
+        if (KP > 64) update_state<2, VS, BACK>(S, BACK ? Y : Z, Z, Ks, Qs, whole, KP, KL, tid);
+        else update_state<1, VS, BACK>(S, BACK ? Y : Z, Z, Ks, Qs, whole, KP, KL, tid);
         __syncthreads();
         if (z.stages == 1 && n + 1 < nch) issue(n + 1);
     }
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(NT) k_chain(const DeltaArgs a) {
     void *out = BACK ? a.dinit : a.final;
     const bool out16 = BACK ? a.dinit_bf16 : a.final_bf16;
     if (out)
-        for (int e = tid; e < VS * KP; e += NT) {
+        for (int e = tid; e < VS * KP; e += N_) {
             const int v = e / KP, k = e % KP;
             if (v0 + v < a.V && k < a.K) delta_st(out, !out16, sat + (int64_t)(v0 + v) * a.K + k, S[v * KL + k]);
         }
@@ -402,16 +406,19 @@ __device__ __forceinline__ float row16(float v) {                  // sum over t
     return v;
 }
 
-// ---- a chunk's gradients.  Shared memory: E + E^T and F (64 x 64), four slices, the gates, sums per row.
-constexpr int GRADS_FLOATS = 2 * 64 * MLD + 4 * 64 * LD + DGATES + 5 * 64 + 64 + 8;
+// ---- a chunk's gradients, a block a chunk, head and share of the keys (slices of 32, one after the other).  Shared memory: E + E^T and F
+// (64 x 64), four slices, the gates, sums per row.  What goes into dg is left for the last launch: of the first share what crosses each token
+// inside the chunk, of each share the sums of its keys, and its part of <dS', S>.
+constexpr int GRADS_FLOATS = 2 * 64 * MLD + 4 * 64 * LD + DGATES + 4 * 64 + 64 + 64 + NT / 32;
+constexpr int FLOW = DELTA_FLOW;        // floats left by a share: flow, X, R, <dS', S>
 
 template <typename T>
-__global__ void __launch_bounds__(NT) k_grads(const DeltaArgs a) {
+__global__ void __launch_bounds__(NT) k_grads(const DeltaArgs a, const int shares) {
     after_previous();
     extern __shared__ float sm[];
     float *E = sm, *F = E + 64 * MLD, *s0 = F + 64 * MLD, *s1 = s0 + 64 * LD, *s2 = s1 + 64 * LD, *s3 = s2 + 64 * LD;
-    float *gate = s3 + 64 * LD, *R = gate + DGATES, *X = R + 64, *flow = X + 64, *fg = flow + 64, *fd = fg + 64, *fl = fd + 64, *red = fl + 64;
-    const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, grp = h / (a.H / a.G), tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+    float *gate = s3 + 64 * LD, *R = gate + DGATES, *X = R + 64, *fg = X + 64, *fd = fg + 64, *fl = fd + 64, *red = fl + 64;
+    const int share = blockIdx.x % shares, h = blockIdx.x / shares % a.H, slot = blockIdx.x / shares / a.H, grp = h / (a.H / a.G), tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
     const DeltaChunk c = delta_chunk(a, slot);
     if (c.len == 0) return;
     const int64_t ch = (int64_t)slot * a.H + h;
@@ -438,10 +445,10 @@ __global__ void __launch_bounds__(NT) k_grads(const DeltaArgs a) {
         __syncthreads();
         load_plain(s0, U, 64, v0, a.V, beta, tid);
         load_plain(s1, mu, 64, v0, a.V, beta, tid);
-        load_slice(s2, dop, a.dos[1], c.len, v0, a.V, tid);
+        load_slice<NT>(s2, dop, a.dos[1], c.len, v0, a.V, tid);
         __syncthreads();
         T *dv = static_cast<T *>(a.dv) + c.b * a.dvs[0] + c.t0 * a.dvs[1] + h * a.dvs[2];
-        for (int e = tid; e < 64 * 32; e += NT) {
+        for (int e = tid; e < 64 * 32 && share == 0; e += NT) {
             const int i = e / 32, v = e % 32;
             if (i < c.len && v0 + v < a.V) dv[i * a.dvs[1] + v0 + v] = from_f<T>(s1[i * LD + v]);
         }
@@ -460,7 +467,7 @@ __global__ void __launch_bounds__(NT) k_grads(const DeltaArgs a) {
     for (int r = 0; r < 4; ++r) {
         db[r] = row16(db[r]);
         const int i = 16 * r + ty;
-        if (tx == 0 && i < c.len) delta_st(a.dbeta, a.beta_f32, c.b * a.dbs[0] + (int64_t)(c.t0 + i) * a.dbs[1] + h * a.dbs[2], db[r]);
+        if (share == 0 && tx == 0 && i < c.len) delta_st(a.dbeta, a.beta_f32, c.b * a.dbs[0] + (int64_t)(c.t0 + i) * a.dbs[1] + h * a.dbs[2], db[r]);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const int j = 16 * s + tx;
@@ -471,7 +478,9 @@ __global__ void __launch_bounds__(NT) k_grads(const DeltaArgs a) {
         }
     }
     // the slices' memory holds W meanwhile; then flow_t = sum over i >= t > j of W_ij
+    float *left = a.flow + (ch * shares + share) * FLOW;
     __syncthreads();
+    if (share == 0) {
     float *Wm = s0;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -490,7 +499,8 @@ __global__ void __launch_bounds__(NT) k_grads(const DeltaArgs a) {
     if (tid < 64) {
         float f = 0.f;
         for (int i = tid; i < 64; ++i) f += Wm[i * MLD + tid];
-        flow[tid] = f;
+        left[tid] = f;
+    }
     }
     __syncthreads();
     // E + E^T
@@ -501,12 +511,12 @@ __global__ void __launch_bounds__(NT) k_grads(const DeltaArgs a) {
     float SS = 0.f;
     T *dqp = static_cast<T *>(a.dq) + c.b * a.dqs[0] + c.t0 * a.dqs[1] + grp * a.dqs[2];
     T *dkp = static_cast<T *>(a.dk) + c.b * a.dks[0] + c.t0 * a.dks[1] + grp * a.dks[2];
-    for (int k0 = 0; k0 < a.K; k0 += 32) {
+    for (int k0 = 32 * share; k0 < a.K; k0 += 32 * shares) {
         float dq[4][2] = {}, kr[4][2] = {}, kw[4][2] = {};
         for (int v0 = 0; v0 < a.V; v0 += 32) {
             // scale e^G dO S, -e^G lam S
             __syncthreads();
-            load_slice(s0, dop, a.dos[1], c.len, v0, a.V, tid);
+            load_slice<NT>(s0, dop, a.dos[1], c.len, v0, a.V, tid);
             load_plain(s1, mu, 64, v0, a.V, fl, tid);
             for (int e = tid; e < 32 * 32; e += NT) {
                 const int v = e / 32, k = e % 32;
@@ -523,8 +533,8 @@ __global__ void __launch_bounds__(NT) k_grads(const DeltaArgs a) {
             fma_slice(kw, s3, LD, s2 + 32 * LD, LD, 32, ty, tx);
         }
         __syncthreads();
-        load_slice(s0, kp, a.ks[1], c.len, k0, a.K, tid);
-        load_slice(s1, qp, a.qs[1], c.len, k0, a.K, tid);
+        load_slice<NT>(s0, kp, a.ks[1], c.len, k0, a.K, tid);
+        load_slice<NT>(s1, qp, a.qs[1], c.len, k0, a.K, tid);
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -566,31 +576,53 @@ __global__ void __launch_bounds__(NT) k_grads(const DeltaArgs a) {
     SS = warp_sum(SS);
     if (tid % 32 == 0) red[tid / 32] = SS;
     __syncthreads();
-    if (tid == 0) {
-        float all = 0.f;
-        for (int w = 0; w < NT / 32; ++w) all += red[w];
-        all *= gate[DQ - 1];
-        float x = 0.f;
-        for (int t = 0; t < 64; ++t) {                               // what left the tokens before t, and what passes all
-            flow[t] += x + all;
-            x += X[t];
-        }
-        float y = 0.f;
-        for (int t = 63; t >= 0; --t) {
-            y += R[t];
-            flow[t] += y;
-        }
+    if (tid < 64) {
+        left[64 + tid] = X[tid];
+        left[128 + tid] = R[tid];
     }
-    __syncthreads();
-    if (tid < c.len) delta_st(a.dg, a.g_f32, c.b * a.dgs[0] + (int64_t)(c.t0 + tid) * a.dgs[1] + h * a.dgs[2], flow[tid]);
+    if (tid < 32) {
+        const float all = warp_sum(tid < NT / 32 ? red[tid] : 0.f);
+        if (tid == 0) left[192] = gate[DQ - 1] * all;
+    }
 }
 
-// dq and dk of a group: the sum over its heads, in their order
+// The last launch, a block a chunk and group: dq and dk, the sums over the group's heads in their order; and dg of each head by a warp,
+// lane l tokens 2l and 2l + 1: what crosses the token, what left the tokens before it, what passes all, what came from before it.
 template <typename T>
-__global__ void __launch_bounds__(NT) k_share(const DeltaArgs a) {
+__global__ void __launch_bounds__(NT) k_finish(const DeltaArgs a, const int shares) {
     after_previous();
-    const int slot = blockIdx.x / a.G, grp = blockIdx.x % a.G, per = a.H / a.G;
+    const int slot = blockIdx.x / a.G, grp = blockIdx.x % a.G, per = a.H / a.G, lane = threadIdx.x % 32;
     const DeltaChunk c = delta_chunk(a, slot);
+    if (c.len == 0) return;
+    for (int h = grp * per + threadIdx.x / 32; h < (grp + 1) * per; h += NT / 32) {
+        const float *left = a.flow + ((int64_t)slot * a.H + h) * shares * FLOW;
+        float x[2] = {}, r[2] = {}, all = 0.f;
+        for (int p = 0; p < shares; ++p) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                x[e] += left[p * FLOW + 64 + 2 * lane + e];
+                r[e] += left[p * FLOW + 128 + 2 * lane + e];
+            }
+            all += left[p * FLOW + 192];
+        }
+        float before = x[0] + x[1], after = r[0] + r[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float u = __shfl_up_sync(0xffffffffu, before, o), d = __shfl_down_sync(0xffffffffu, after, o);
+            if (lane >= o) before += u;
+            if (lane + o < 32) after += d;
+        }
+        before = __shfl_up_sync(0xffffffffu, before, 1);
+        after = __shfl_down_sync(0xffffffffu, after, 1);
+        if (lane == 0) before = 0.f;
+        if (lane == 31) after = 0.f;
+        after += r[1];
+        const float d[2] = {left[2 * lane] + before + all + (after + r[0]), left[2 * lane + 1] + (before + x[0]) + all + after};
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (2 * lane + e < c.len) delta_st(a.dg, a.g_f32, c.b * a.dgs[0] + (int64_t)(c.t0 + 2 * lane + e) * a.dgs[1] + h * a.dgs[2], d[e]);
+    }
+    if (a.part == nullptr) return;
     T *dqp = static_cast<T *>(a.dq) + c.b * a.dqs[0] + c.t0 * a.dqs[1] + grp * a.dqs[2];
     T *dkp = static_cast<T *>(a.dk) + c.b * a.dks[0] + c.t0 * a.dks[1] + grp * a.dks[2];
     const int64_t other = (int64_t)a.nslots * a.H * 64 * a.K;
@@ -607,12 +639,20 @@ __global__ void __launch_bounds__(NT) k_share(const DeltaArgs a) {
     }
 }
 
+template <typename T, bool BACK, int VS>
+cudaError_t launch_chain(const DeltaArgs &a, cudaStream_t st) {
+    static int set[64] = {};
+    const int bytes = chain_sizes(a.K, VS).bytes;
+    if (cudaError_t e = ensure_smem_attr(k_chain<T, BACK, VS>, bytes, set); e != cudaSuccess) return e;
+    return launch_early(k_chain<T, BACK, VS>, (unsigned)(a.nseqs * (int64_t)a.H * ((a.V + VS - 1) / VS)), chain_threads(VS), bytes, st, a);
+}
+// The fewest values a block whose blocks still have an SM each: a block is bound by its reads of shared memory, which go with
+// its values.  6 chunks of 9 sequences and heads of 96 x 64: 32 / 16 / 8 values 66 / 47 / 38 us; 8 chunks of 12 of 128 x 128:
+// 129 / 88 / 131 (192 blocks); of 20: 129 / 165 / 193; 32 chunks of 64: 966 / 1228 / 1720.
 template <typename T, bool BACK>
 cudaError_t chain(const DeltaArgs &a, cudaStream_t st) {
-    static int set[64] = {};
-    const int bytes = chain_sizes(a.K).bytes;
-    if (cudaError_t e = ensure_smem_attr(k_chain<T, BACK>, bytes, set); e != cudaSuccess) return e;
-    return launch_early(k_chain<T, BACK>, (unsigned)(a.nseqs * (int64_t)a.H * ((a.V + VS - 1) / VS)), NT, bytes, st, a);
+    auto fits = [&](int VS) { return a.nseqs * (int64_t)a.H * ((a.V + VS - 1) / VS) <= kDeltaSMs; };
+    return fits(8) ? launch_chain<T, BACK, 8>(a, st) : fits(16) ? launch_chain<T, BACK, 16>(a, st) : launch_chain<T, BACK, 32>(a, st);
 }
 
 template <typename T>
@@ -630,8 +670,9 @@ cudaError_t bwd(const DeltaArgs &a, cudaStream_t st) {
     static int set[64] = {};
     const int bytes = GRADS_FLOATS * (int)sizeof(float);
     if (cudaError_t e = ensure_smem_attr(k_grads<T>, bytes, set); e != cudaSuccess) return e;
-    if (cudaError_t e = launch_early(k_grads<T>, (unsigned)((int64_t)a.nslots * a.H), NT, bytes, st, a); e != cudaSuccess || a.part == nullptr) return e;
-    return launch_early(k_share<T>, (unsigned)((int64_t)a.nslots * a.G), NT, 0, st, a);
+    const int shares = delta_grad_shares(a.nslots, a.H, a.K);
+    if (cudaError_t e = launch_early(k_grads<T>, (unsigned)((int64_t)a.nslots * a.H * shares), NT, bytes, st, a, shares); e != cudaSuccess) return e;
+    return launch_early(k_finish<T>, (unsigned)((int64_t)a.nslots * a.G), NT, 0, st, a, shares);
 }
 
 }  // namespace

@@ -35,7 +35,7 @@ constexpr uint32_t SEG_BYTES = 128 * 128 * 4;    // of a segment: its end in fp3
 // (8192 tokens of 32 heads: 195 us of chains instead of 340 in one launch, or 260 in three equal segments; 2 x 2048 of 32: 104 cut, 102
 // in one, so it stays whole.)
 inline void delta_segments(int64_t nseqs, int64_t H, int64_t chunks, int *nseg, int *first, int *len) {
-    const int64_t sms = 152, U = nseqs * H;
+    const int64_t sms = kDeltaSMs, U = nseqs * H;
     *nseg = 1;
     *first = *len = 0;
     double best = (double)chunks;
