@@ -537,6 +537,8 @@ ssd_status ssd_conv1d_step(const ssd_conv_problem *prob, const void *u, int64_t 
  *                         each (nstate = batch, or nseqs with cu_seqlens)
  *   cu_seqlens     : int32 [nseqs + 1], device, batch 1.  Its contents are not validated: bad ones give
  *                    unspecified values, yet every access stays inside the tensors described here.
+ *                    Tokens before the first sequence and behind the last are not read; their rows of the
+ *                    outputs (o, or dq, dk, dv, dg, dbeta) are left as they were, or zeroed when zero_rest is set.
  * A sequence without tokens has final state = initial state (zero without one), and passes dfinal on to
  * dinitial.  headdim and dstate 1..256, else SSD_ERR_UNSUPPORTED.
  *
@@ -546,8 +548,10 @@ ssd_status ssd_conv1d_step(const ssd_conv_problem *prob, const void *u, int64_t 
  * are sums of products of bf16 operands (each rounded once, 2^-9), whatever type g, beta and their gradients have.
  *
  * chunk_states (optional): a device buffer of ssd_delta_chunk_states_size bytes, 256-byte aligned, into which the
- * forward writes what the backward of the same problem starts from instead of running the forward again.
- * Workspaces: device memory, 256-byte aligned, contents need not be initialised.  Gradients are summed
+ * forward writes what the backward of the same problem starts from instead of running the forward again (on the tensor
+ * cores states, values and matrices of every chunk, 90 KB for 64 tokens and head; else in fp32, at 128 x 128 98 KB).
+ * Workspaces: device memory, 256-byte aligned, contents need not be initialised; of one call at a time.  Waits inside the
+ * tensor-core kernels are bounded: after one has run out, ssd_query_status(workspace, ...) gives SSD_ERR_DEVICE_TIMEOUT.  Gradients are summed
  * in a fixed order (bitwise reproducible).
  */
 typedef struct {
@@ -560,6 +564,7 @@ typedef struct {
     ssd_tensor o, final_states;                                       /* final_states optional */
     const int32_t *cu_seqlens;
     void *chunk_states;
+    int32_t zero_rest;                                                /* with cu_seqlens: see above */
 } ssd_delta_args;
 typedef struct {
     ssd_delta_args fwd;                                               /* o and final_states are not looked at */

@@ -107,7 +107,7 @@ class DeltaProblem(ctypes.Structure):
 
 class DeltaArgs(ctypes.Structure):
     _fields_ = ([(n, Tensor) for n in ("q", "k", "v", "g", "beta", "initial_states", "o", "final_states")] +
-                [("cu_seqlens", ctypes.c_void_p), ("chunk_states", ctypes.c_void_p)])
+                [("cu_seqlens", ctypes.c_void_p), ("chunk_states", ctypes.c_void_p), ("zero_rest", ctypes.c_int32)])
 
 
 class DeltaBwdArgs(ctypes.Structure):

@@ -493,6 +493,7 @@ Delta delta_inputs(const Tensor *const *t, std::optional<double> scale) {
     s.f.q = desc(q, 1); s.f.k = desc(k, 1); s.f.v = desc(v, 1); s.f.g = desc(g, 0); s.f.beta = desc(beta, 0);
     s.f.initial_states = desc(init, 4);
     s.f.cu_seqlens = ptr_as<int32_t>(cu);
+    s.f.zero_rest = 1;                                      // (outputs are allocated here)
     return s;
 }
 

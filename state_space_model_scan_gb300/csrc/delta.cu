@@ -1,4 +1,6 @@
 // delta.cu -- the C entry points of the gated delta rule: validation, workspace, launches.
+#include <initializer_list>
+
 #include "delta_tc.cuh"
 
 using namespace ssd;
@@ -181,6 +183,46 @@ DeltaMaps maps(const ssd_delta_problem *p, const ssd_delta_args *f, const DeltaA
 cudaError_t run_fwd(const ssd_delta_problem *p, const ssd_delta_args *f, const DeltaArgs &a, const ssd_tensor &o, cudaStream_t st) {
     return on_tensor_cores(p) && a.nslots > 0 ? delta_tc_fwd(a, maps(p, f, a, nullptr, o), st) : delta_simt_fwd(a, p->dtype == SSD_BF16, st);
 }
+// ---- rows of tokens that lie in no sequence
+struct Rest {
+    struct {
+        void *p;
+        int64_t s[3];
+        int heads, inner, bytes;
+    } t[5];
+    int n, nseqs, seqlen;
+    const int32_t *cu;
+};
+__global__ void k_rest(const Rest a) {
+    after_previous();
+    const int first = min(max(a.cu[0], 0), a.seqlen), last = max(first, min(max(a.cu[a.nseqs], 0), a.seqlen));
+    const int rows = first + a.seqlen - last;
+    for (int k = 0; k < a.n; ++k) {
+        const auto &t = a.t[k];
+        for (int64_t e = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; e < (int64_t)rows * t.heads * t.inner; e += (int64_t)gridDim.x * blockDim.x) {
+            const int64_t r = e / ((int64_t)t.heads * t.inner), rest = e - r * t.heads * t.inner;
+            const int64_t at = (r < first ? r : last + r - first) * t.s[1] + rest / t.inner * t.s[2] + rest % t.inner;
+            if (t.bytes == 2) static_cast<uint16_t *>(t.p)[at] = 0;
+            else static_cast<float *>(t.p)[at] = 0.f;
+        }
+    }
+}
+ssd_status zero_rest(const ssd_delta_problem *p, const ssd_delta_args *f, std::initializer_list<const ssd_tensor *> tensors, cudaStream_t st) {
+    if (!f->zero_rest || f->cu_seqlens == nullptr || p->seqlen == 0) return SSD_OK;
+    Rest a{};
+    a.nseqs = (int)p->nseqs; a.seqlen = (int)p->seqlen; a.cu = f->cu_seqlens;
+    int k = 0;
+    for (const ssd_tensor *t : tensors) {                    // o, or dq, dk, dv, dg, dbeta
+        auto &to = a.t[a.n++];
+        to.p = t->ptr;
+        set3(to.s, *t);
+        to.heads = (int)(tensors.size() > 1 && k < 2 ? p->ngroups : p->nheads);
+        to.inner = (int)(k >= 3 ? 1 : tensors.size() > 1 && k < 2 ? p->dstate : p->headdim);
+        to.bytes = (int)esize(t->dtype);
+        ++k;
+    }
+    return launch_early(k_rest, 64u, 256u, 0, st, a) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
 ssd_status of_cuda(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
 
 }  // namespace
@@ -218,7 +260,8 @@ ssd_status ssd_delta_fwd(const ssd_delta_problem *p, const ssd_delta_args *f, vo
     a.final = f->final_states.ptr;
     a.final_bf16 = f->final_states.dtype == SSD_BF16;
     if (f->chunk_states) set_kept(a, p, f->chunk_states);
-    return of_cuda(run_fwd(p, f, a, f->o, (cudaStream_t)stream));
+    DELTA_TRY(of_cuda(run_fwd(p, f, a, f->o, (cudaStream_t)stream)));
+    return zero_rest(p, f, {&f->o}, (cudaStream_t)stream);
 }
 
 ssd_status ssd_delta_bwd(const ssd_delta_problem *p, const ssd_delta_bwd_args *b, void *workspace, size_t workspace_bytes, void *stream) {
@@ -256,7 +299,8 @@ ssd_status ssd_delta_bwd(const ssd_delta_problem *p, const ssd_delta_bwd_args *b
     a.mu = ws + w.mu;
     a.flow = reinterpret_cast<float *>(ws + w.flow);
     a.part = !on_tensor_cores(p) && p->nheads > p->ngroups ? reinterpret_cast<float *>(ws + w.part) : nullptr;
-    return of_cuda(on_tensor_cores(p) && a.nslots > 0 ? delta_tc_bwd(a, maps(p, f, a, b, b->dv), st) : delta_simt_bwd(a, p->dtype == SSD_BF16, st));
+    DELTA_TRY(of_cuda(on_tensor_cores(p) && a.nslots > 0 ? delta_tc_bwd(a, maps(p, f, a, b, b->dv), st) : delta_simt_bwd(a, p->dtype == SSD_BF16, st)));
+    return zero_rest(p, f, {&b->dq, &b->dk, &b->dv, &b->dg, &b->dbeta}, st);
 }
 
 }  // extern "C"

@@ -43,6 +43,7 @@ inline void delta_segments(int64_t nseqs, int64_t H, int64_t chunks, int *nseg, 
     for (int64_t k = 1; k <= 30; ++k) {
         const int64_t w1 = (2 * k * U + sms - U - 1) / (sms - U), w2 = (k * U + sms - U - 1) / (sms - U), n = w1 + k + w2, s = (chunks + n - 1) / n;
         const int64_t last = chunks - (w1 + k) * s;
+        if (w1 > 3) break;                                   // (ends and matrices are memory: 128 KB each)
         if (s < 4 || last < 1) continue;
         const double t = (double)w1 * (s + 1) + std::max<int64_t>(last, w2 * (s + 1)) + 0.8 * k + 8;
         if (t < best) {
