@@ -169,38 +169,53 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
     const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, grp = h / (a.H / a.G);
     const DeltaChunk c = delta_chunk(a, slot);
     if (c.len == 0) return;
-    if (w == 1) tmem_alloc(tm, 64);
-    if (tid == 0) {
-        mbar_init(bar, 1);
-        mbar_init(bar + 1, 1);
-        fence_mbar_init();
-        if (m.has_k || m.has_q) {
-            mbar_expect_tx(bar, (m.has_k + m.has_q) * TOK_BYTES);
-            if (m.has_k) tma_rows(sm + P_A, 2 * HALF, &m.k, bar, c, grp);
-            if (m.has_q) tma_rows(sm + P_A + HALF, 2 * HALF, &m.q, bar, c, grp);
-        }
-    }
-    __syncwarp();
-    if (w == 0) delta_gates(a, c, h, gate, lane);
-    if (!m.has_k) load_rows<PREP_NT>(sm + P_A, 2 * HALF, tok_rows(a.k, a.ks, c, grp), a.ks[1], c.len, a.K, tid);
-    if (!m.has_q) load_rows<PREP_NT>(sm + P_A + HALF, 2 * HALF, tok_rows(a.q, a.qs, c, grp), a.qs[1], c.len, a.K, tid);
-    __syncthreads();
+    // a whole chunk that comes by TMA needs nobody but one thread until its product is out, while another warp computes the gates
+    const bool quick = m.has_k && m.has_q && c.len == DQ;
+    const uint32_t base = smem_u32(sm + P_A);
+    auto product = [&] {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) umma_bf16(*tm, kmaj(base, k, 2 * HALF), kmaj(base, k, 2 * HALF), idesc_bf16(128, 64, 0, 0), k > 0);
+        umma_commit(bar + 1);
+    };
     bool ok = true;
-    if (m.has_k || m.has_q) {
-        ok = mbar_wait(bar, 0);
-        if (m.has_k && c.len < DQ) zero_rows<PREP_NT>(sm + P_A, 2 * HALF, c.len, tid);
-        if (m.has_q && c.len < DQ) zero_rows<PREP_NT>(sm + P_A + HALF, 2 * HALF, c.len, tid);
+    if (w == 0) {
+        tmem_alloc(tm, 64);
+        __syncwarp();
+        if (lane == 0) {
+            mbar_init(bar, 1);
+            mbar_init(bar + 1, 1);
+            fence_mbar_init();
+            if (m.has_k || m.has_q) {
+                mbar_expect_tx(bar, (m.has_k + m.has_q) * TOK_BYTES);
+                if (m.has_k) tma_rows(sm + P_A, 2 * HALF, &m.k, bar, c, grp);
+                if (m.has_q) tma_rows(sm + P_A + HALF, 2 * HALF, &m.q, bar, c, grp);
+            }
+            if (quick) {
+                ok = mbar_wait(bar, 0);
+                product();
+            }
+        }
+        __syncwarp();
+    } else if (w == 3) {
+        delta_gates(a, c, h, gate, lane);
     }
-    fence_proxy_async_smem();
+    if (!quick) {
+        if (!m.has_k) load_rows<PREP_NT>(sm + P_A, 2 * HALF, tok_rows(a.k, a.ks, c, grp), a.ks[1], c.len, a.K, tid);
+        if (!m.has_q) load_rows<PREP_NT>(sm + P_A + HALF, 2 * HALF, tok_rows(a.q, a.qs, c, grp), a.qs[1], c.len, a.K, tid);
+        __syncthreads();
+        if (m.has_k || m.has_q) {
+            ok = mbar_wait(bar, 0);
+            if (m.has_k && c.len < DQ) zero_rows<PREP_NT>(sm + P_A, 2 * HALF, c.len, tid);
+            if (m.has_q && c.len < DQ) zero_rows<PREP_NT>(sm + P_A + HALF, 2 * HALF, c.len, tid);
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0) product();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tm, base = smem_u32(sm + P_A);
-    if (tid == 0) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) umma_bf16(tmem, kmaj(base, k, 2 * HALF), kmaj(base, k, 2 * HALF), idesc_bf16(128, 64, 0, 0), k > 0);
-        umma_commit(bar + 1);
-    }
+    const uint32_t tmem = *tm;
     uint8_t *ops = static_cast<uint8_t *>(a.tiles) + ((int64_t)slot * a.H + h) * (BOTH ? OPS_BOTH : OPS_BYTES);
     if (tid >= 64) {                                         // (warps 2 and 3: while the product runs)
         const int j = tid - 64, e = j | 15;
@@ -265,11 +280,11 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
     tc_fence_before();
     fence_proxy_async_smem();
     __syncthreads();
-    if (w == 1) {
+    if (w == 0) {
         tc_fence_after();
         tmem_dealloc(tmem, 64);
     }
-    if (tid == PREP_NT - 1) {                                // (of a warp that does not substitute)
+    if (tid == PREP_NT - 1) {                                // (not of the warp that gives the tensor memory back)
         bulk_store(ops + ATT, sm + P_ATT, MAT_BYTES);
         bulk_store(ops + GATES, gate, GATE_BYTES);
         bulk_commit();
