@@ -2,7 +2,8 @@
 // the zero-extended part of 128).  Formulas in delta.cuh.
 //
 // Two kernels forwards.  k_prep, a block a chunk and head: K K^T and Q K^T in one product (K's rows and Q's rows as the 128
-// rows of A), the gates, the triangular system, its inverse (fp32, by blocks) and att, left as operand images.  k_chain, a block a sequence and head, walks the chunks.  It works on transposed matrices, so that the
+// rows of A), the gates, the triangular system, its inverse (fp32, by blocks) and att, left as operand images.  k_chain, a block a
+// sequence and head (or a segment of one), walks the chunks.  It works on transposed matrices, so that the
 // 128 TMEM lanes are the values: lane v holds row v of the state S [values][keys], and every product
 //
 //     P^T = S K^T   [v][i]        Y = V^T - e^G P^T     U^T = Y sys^T  [v][i]      S' = e^Gc S + (e^(Gc - G) beta U)^T K   [v][k]
@@ -12,13 +13,20 @@
 // little arithmetic and one tcgen05.st, and no shared memory is written.  The state stays in registers, in fp32.
 // What is carried (S, Y, e^(Gc - G) beta U, sys) enters a product as the sum of two bf16 values (2^-17), two or three products of
 // which the small ones are the cheaper price than tf32's single one of half the rate and 2^-11; what only leaves as bf16
-// (att, beta U in o) as one.
+// (att, beta U in o) as one: o is off by 2.6e-3, of which its own rounding is 1.7e-3 (beta U as two took 6% more time for 2.2e-3).
 // Backwards the same chain runs from the last chunk to the first, with dS in S's place and the transposed inverse in sys's: k_prep
 // leaves both for it, which come of one substitution, and nothing of the chunks is computed twice.
 //
-// Warps of a chain block: eight with two threads a lane, each half of the columns; four with one thread a lane for what is off
-// the chain; two that load the next chunk, one that stores; one thread that issues every product.  A product of 128 x 64 x 16 takes as long as one of 128 x 128 x 16 (64 cycles), so that K's and
+// Warps of a chain block: eight with two threads a lane, each half of the columns (four threads a lane were 13% slower: a thread's
+// second quarter is what runs beside the products of the first); four with one thread a lane for what is off
+// the chain; two that load the next chunk, one that stores; one thread that issues every product.  A product of 128 x 64 x 16 takes as
+// long as one of 128 x 128 x 16 (64 cycles), so that K's and
 // Q's rows, and both terms of sys, go as one right operand of 128 rows.  All waits are bounded.
+//
+// Bound by latency: a step of a chunk is three products in a row with arithmetic between them, about 2.6 us, of which the products are 40% and the
+// rest are splits, loads and stores of tensor memory at two warps a scheduler; the launch's first step comes 9 us late (tensor memory, maps, cold
+// code).  8192 tokens of 32 heads, 128 x 128: k_prep 50 us, chains 122 + 73 (34.6 GF, 204 MB: 18 and 30 us); 2 x 2048 tokens forwards
+// 31 + 102 us, backwards 105, k_grads 77 (294 MB, 3.8 TB/s).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -32,6 +40,7 @@ namespace {
 using namespace dtc;
 
 // ---------------------------------------------------------------------------------------- the chunk's matrices
+// Bound by instructions and by the waits between its steps, six blocks on an SM (shared memory): issue 61%, shared memory 63%.
 constexpr int PREP_NT = 128;
 constexpr int MLD = DELTA_ML;
 // K's and Q's rows; once their product is out, the system and scratch lie over them

