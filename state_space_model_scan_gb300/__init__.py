@@ -1,5 +1,6 @@
 """GB300 (sm_103a) state-space scans: the Mamba-2 SSD chunked scan, the selective scan with a decay rate per
-channel and state, and what serving them takes (single tokens, carried windows, 8-bit snapshots).
+channel and state, the gated delta rule with the norms of its queries and keys, and what serving them takes (single tokens,
+carried windows, 8-bit snapshots).
 
 The compute lives in libssd.so (C ABI, include/ssd.h); this package holds its
 thin ctypes binding (``_lib``) and the compiled one of the newer calls (``_binding``), convenience wrappers that allocate outputs and

@@ -451,10 +451,10 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
     }
     if (w == 0) tmem_alloc(&ms->tmem, 512);
     if (tid == CH_L0) {
-        prefetch_tmap(&m.k);
-        prefetch_tmap(BACK ? &m.dO : &m.v);
-        prefetch_tmap(&m.q);
-        if (outs) prefetch_tmap(&m.out);
+        if (m.has_k) prefetch_tmap(&m.k);
+        if (BACK ? m.has_dO : m.has_v) prefetch_tmap(BACK ? &m.dO : &m.v);
+        if (m.has_q) prefetch_tmap(&m.q);
+        if (outs && m.has_out) prefetch_tmap(&m.out);
     }
     tc_fence_before();
     __syncthreads();
