@@ -11,13 +11,16 @@
 // before the first is used, and the token's cosines and sines are loaded once for them.  What the shapes or addresses keep
 // from that goes feature by feature through shared memory.  The weights' gradients are summed in registers over a
 // block's tokens, then over its groups, then by a second launch over the blocks, each in a fixed order.
-// 8192 tokens x 40 heads of 128, bf16: 35.3 us for 172 MB (4.9 TB/s, 72% of a plain copy); backwards 4096 tokens 32 us for 129 MB and 5 for the weights' sums.
+// 8192 tokens x 40 heads of 128, bf16: 32.2 us for 172 MB (5.3 TB/s, 79% of a plain copy); backwards 4096 tokens 32 us for 129 MB and 5 for the weights' sums.
 #include "selective.cuh"
 
 namespace ssd {
 
 namespace {
 
+// Threads of a forward block: 7 blocks of 128 leave 72 registers a thread and start anew more evenly: 32.2 us where 3 of 256 took 35.8
+// (8192 tokens x 40 heads of 128; 6 of 128 34.0, 8 of 128, 64 registers, 36.8).
+constexpr int QK_FWD_NT = 128;
 constexpr int QK_NT = 256, QK_HB_MIN = 2, QK_MAXD = 512;
 constexpr int QK_BLOCKS = 3 * kSMs;     // of the backward: each leaves its share of the weights' gradients
 
@@ -187,11 +190,11 @@ __device__ __forceinline__ void qk_weight(f32x2 (&w)[V / 2], const float *p, boo
 
 // y = rstd (c w x + s w' x'), x' and w' the partners': their factors are the token's
 template <typename T, int V, bool INTER, int HB>
-__global__ void __launch_bounds__(QK_NT, V <= 8 ? 3 : 2) k_qk_fwd(const QkArgs a) {
+__global__ void __launch_bounds__(QK_FWD_NT, V <= 8 ? 7 : 4) k_qk_fwd(const QkArgs a) {
     after_previous();
     const bool keys = blockIdx.x >= a.blocks0;
     const QkSide &s = a.side[keys];
-    const int lane = threadIdx.x & 31, l = lane & (a.lpr - 1), gpb = QK_NT / a.lpr;
+    const int lane = threadIdx.x & 31, l = lane & (a.lpr - 1), gpb = QK_FWD_NT / a.lpr;
     const uint32_t item = (uint32_t)(blockIdx.x - (keys ? a.blocks0 : 0)) * gpb + threadIdx.x / a.lpr;
     const bool live = item < s.items;                        // (idle groups stay for the shuffles)
     const QkAt q = qk_at(a, s, live ? item : s.items - 1, HB);
@@ -478,7 +481,7 @@ QkArgs make(const ssd_qk_problem *p, const ssd_qk_args *f, const ssd_tensor &yq,
     }
     if (!vec) *V = 0;
     // Heads of an item: 128 bytes of them on the way to a lane (backwards 64 of x and of dy each) where that still fills the card, two where
-    // few tokens come.  8192 tokens x 40 heads of 128: 4 / 8 heads 39.2 / 35.3 us; backwards 4096 tokens 32.7 / 48.6.
+    // few tokens come.  8192 tokens x 40 heads of 128: 4 / 8 heads 39 / 32 us; backwards 4096 tokens 32.7 / 48.6.
     const int64_t lanes = tokens * (p->q_heads + p->k_heads) * p->dim / (*V ? *V : 16);
     const int many = (dyq != nullptr ? 64 : 128) / ((*V ? *V : 16) * (p->dtype == SSD_BF16 ? 2 : 4));
     *HB = *V && many > QK_HB_MIN && lanes / many >= 2 * kSMs * QK_NT ? many : QK_HB_MIN;
@@ -497,7 +500,7 @@ QkArgs make(const ssd_qk_problem *p, const ssd_qk_args *f, const ssd_tensor &yq,
     return a;
 }
 int blocks_for(const QkArgs &a, int side, int64_t most) {
-    const int64_t gpb = QK_NT / a.lpr, n = (a.side[side].items + gpb - 1) / gpb;
+    const int64_t gpb = (most == 0 ? QK_FWD_NT : QK_NT) / a.lpr, n = (a.side[side].items + gpb - 1) / gpb;   // most 0: forwards, a group an item
     if (most == 0) return (int)n;
     const uint64_t all = (uint64_t)a.side[0].items + a.side[1].items;   // blocks in proportion to the items
     const int64_t share = std::max<int64_t>(1, (int64_t)((uint64_t)most * a.side[side].items / all));
@@ -507,7 +510,7 @@ int blocks_for(const QkArgs &a, int side, int64_t most) {
 template <typename T, int V, bool INTER, int HB>
 cudaError_t launch(const QkArgs &a, bool back, cudaStream_t st) {
     const unsigned grid = (unsigned)(a.blocks0 + a.blocks1);
-    if (!back) return launch_early(k_qk_fwd<T, V, INTER, HB>, grid, QK_NT, 0, st, a);
+    if (!back) return launch_early(k_qk_fwd<T, V, INTER, HB>, grid, QK_FWD_NT, 0, st, a);
     return launch_early(k_qk_bwd<T, V, INTER, HB>, grid, QK_NT, 0, st, a);
 }
 template <typename T, int V>
