@@ -420,6 +420,54 @@ __device__ __forceinline__ void ld_gates(f32x2 &g0, f32x2 &g1, const float *p) {
     g0 = v.x;
     g1 = v.y;
 }
+// A state in shared memory, fp32: piece p (four keys) of row v lies at p ^ (v & 31), so that a thread's row and a warp's pieces of one row are
+// in different banks.  Rows w, w + 8, .. by a warp, from and to memory, where a row's pieces are neighbours.
+__device__ __forceinline__ float4 *state_piece(uint8_t *buf, int v, int p) { return reinterpret_cast<float4 *>(buf) + v * 32 + (p ^ (v & 31)); }
+__device__ __forceinline__ void state_rows(uint8_t *buf, const void *in, bool f32, int64_t at, int V, int K, int w, int lane) {
+    const bool wide = (K & 3) == 0 && (reinterpret_cast<uintptr_t>(in) & 15) == 0;   // (a head's rows start at a multiple of four elements)
+    const int k = 4 * lane;
+#pragma unroll 4
+    for (int r = w; r < 128; r += CH_CW) {
+        float x[4] = {};
+        if (r < V && k < K) {
+            const int64_t e = at + (int64_t)r * K + k;
+            if (wide && f32) {
+                const float4 u = *reinterpret_cast<const float4 *>(static_cast<const float *>(in) + e);
+                x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+            } else if (wide) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(in) + e);
+                x[0] = bf_lo(u.x); x[1] = bf_hi(u.x); x[2] = bf_lo(u.y); x[3] = bf_hi(u.y);
+            } else {
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    if (k + d < K) x[d] = delta_ld(in, f32, e + d);
+            }
+        }
+        *state_piece(buf, r, lane) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+}
+__device__ __forceinline__ void rows_state(uint8_t *buf, void *out, bool f32, int64_t at, int V, int K, int w, int lane) {
+    const bool wide = (K & 3) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    const int k = 4 * lane;
+#pragma unroll 4
+    for (int r = w; r < V; r += CH_CW) {
+        const float4 x = *state_piece(buf, r, lane);
+        const int64_t e = at + (int64_t)r * K + k;
+        if (k >= K) continue;
+        if (wide && f32) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(out) + e) = x;
+        } else if (wide) {
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(out) + e) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+        } else {
+            const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                if (k + d < K) delta_st(out, f32, e + d, y[d]);
+        }
+    }
+}
+// a barrier of the lanes' warps, where each of them comes by whatever has run out before
+__device__ __forceinline__ void lanes_meet() { asm volatile("bar.sync 1, %0;" ::"n"(CH_CW * 32) : "memory"); }
 // KEEP: U, or mu, and the states are left for the gradients; OUT: o (backwards dV) is computed; ENDS: the first launch of chains that
 // are cut into segments: the first segment as it is, of the others but the last the end from a zero state and the matrix, and nothing else
 template <bool BACK, bool KEEP, bool OUT, bool ENDS>
@@ -441,7 +489,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
     const int n = a.nseg > 1 && seg < a.nseg - 1 ? min(seg == 0 ? a.seg0 : a.seglen, all - c0) : all - c0, joins = ENDS ? 0 : max(0, seg - 1);
     if (tid == 0) {
         for (int b : {B_FULL0, B_FULL1}) mbar_init(&ms->bar[b], CH_LW);
-        for (int b : {B_TMA0, B_TMA1, B_O0, B_O1, B_P, B_U, B_S, B_END, B_FO, B_FV, B_FS, B_JM0, B_JM1, B_JD}) mbar_init(&ms->bar[b], 1);
+        for (int b : {B_O0, B_O1, B_P, B_U, B_S, B_END, B_FO, B_FV, B_FS, B_JM0, B_JM1, B_JD}) mbar_init(&ms->bar[b], 1);
         for (int b : {B_WV, B_WS}) mbar_init(&ms->bar[b], CH_CW);
         for (int b = B_AY; b < NB; ++b) mbar_init(&ms->bar[b], CH_CW);
         for (int b : {B_AF, B_EG0, B_EG1}) mbar_init(&ms->bar[b], CH_EW);
@@ -449,13 +497,41 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         ms->abort_ = 0;
         fence_mbar_init();
     }
-    if (w == 0) tmem_alloc(&ms->tmem, 512);
+    auto stage = [&](int c) { return sm + (c & 1) * ST_BYTES; };
+    auto idx = [&](int c) { return BACK ? all - 1 - c0 - c : c0 + c; };    // the chunk of step c
+    // Q and, backwards, dO are needed for the state's sake too
+    const bool outputs = BACK ? !mat : outs, values = !mat;
+    const CUtensorMap *mx = BACK ? &m.dO : &m.v;
+    const bool has_x = values && (BACK ? m.has_dO : m.has_v);
+    auto chunk = [&](int c) {
+        const int ci = idx(c);
+        return DeltaChunk{q.b, q.t0 + ci * DQ, min(DQ, q.len - ci * DQ)};
+    };
+    auto issue_copies = [&](int c) {                        // by one thread
+        const DeltaChunk k = chunk(c);
+        uint8_t *st = stage(c);
+        uint64_t *bar = &ms->bar[B_TMA0 + (c & 1)];
+        mbar_expect_tx(bar, OPS_BYTES + (m.has_k + has_x + (m.has_q && outputs)) * TOK_BYTES);
+        if (m.has_k) tma_rows(st + ST_KQ, 2 * HALF, &m.k, bar, k, grp);
+        if (has_x) tma_rows(st + ST_X, HALF, mx, bar, k, h);
+        const uint8_t *ops = static_cast<const uint8_t *>(a.tiles) + (((int64_t)q.slot0 + idx(c)) * a.H + h) * (a.both ? OPS_BOTH : OPS_BYTES);
+        if (BACK) {                                  // the other inverse in its place
+            bulk_load(st + ST_OPS, ops + SYS_T, 2 * MAT_BYTES, bar);
+            bulk_load(st + ST_OPS + ATT, ops + ATT, OPS_BYTES - ATT, bar);
+        } else {
+            bulk_load(st + ST_OPS, ops, OPS_BYTES, bar);
+        }
+        if (m.has_q && outputs) tma_rows(st + ST_KQ + HALF, 2 * HALF, &m.q, bar, k, grp);
+    };
+    // the first chunks' copies, before anything else is set up
     if (tid == CH_L0) {
-        if (m.has_k) prefetch_tmap(&m.k);
-        if (BACK ? m.has_dO : m.has_v) prefetch_tmap(BACK ? &m.dO : &m.v);
-        if (m.has_q) prefetch_tmap(&m.q);
+        for (int b : {B_TMA0, B_TMA1}) mbar_init(&ms->bar[b], 1);
+        fence_mbar_init();
+        if (joins == 0)
+            for (int c = 0; c < min(n, 2); ++c) issue_copies(c);
         if (outs && m.has_out) prefetch_tmap(&m.out);
     }
+    if (w == 0) tmem_alloc(&ms->tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -470,10 +546,6 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms->bar[b]);
     };
-    auto stage = [&](int c) { return sm + (c & 1) * ST_BYTES; };
-    auto idx = [&](int c) { return BACK ? all - 1 - c0 - c : c0 + c; };    // the chunk of step c
-    // Q and, backwards, dO are needed for the state's sake too
-    const bool outputs = BACK ? !mat : outs, values = !mat;
     using C = Cols<BACK>;
 
     if (w < CH_CW) {
@@ -482,12 +554,12 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         const uint32_t at = tmem + ((uint32_t)(w & 3) << 21);
         const bool mine = v < a.V;
         f32x2 S[32];                                         // row v, keys 64 hf ..
-        const int64_t row = (((int64_t)s * a.H + h) * a.V + v) * a.K + 64 * hf;
-        const float *ends = static_cast<const float *>(a.segB) + (int64_t)unit * (a.nseg - 1) * (128 * 128) + v * 128 + 64 * hf;
+        const int64_t row = ((int64_t)s * a.H + h) * a.V * a.K;
+        const float4 *ends = static_cast<const float4 *>(a.segB) + (int64_t)unit * (a.nseg - 1) * 4096 + 16 * hf * 128 + v;   // [piece of four keys][value]
         if (!ENDS && seg > 0) {
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-                const float4 x = *reinterpret_cast<const float4 *>(ends + 2 * e);
+                const float4 x = ends[e / 2 * 128];
                 S[e] = pk2(x.x, x.y);
                 S[e + 1] = pk2(x.z, x.w);
             }
@@ -496,29 +568,15 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
             for (int e = 0; e < 32; ++e) S[e] = pk2(mat && v == 64 * hf + 2 * e ? 1.f : 0.f, mat && v == 64 * hf + 2 * e + 1 ? 1.f : 0.f);
         } else {
             const void *in = BACK ? a.dfinal : a.init;
-            const bool f32 = BACK ? !a.dfinal_bf16 : !a.init_bf16;
-            const bool wide = (a.K & 7) == 0 && (reinterpret_cast<uintptr_t>(in) & 15) == 0;   // rows in pieces of 16 bytes
+            if (in) {                                        // (nothing else is there yet)
+                state_rows(sm + CH_O, in, BACK ? !a.dfinal_bf16 : !a.init_bf16, row, a.V, a.K, w, lane);
+                lanes_meet();
+            }
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {                // eight keys
-                const int k = 64 * hf + 2 * e;
-                if (in && mine && wide && k < a.K) {
-                    if (f32) {
-                        const ulonglong2 x = reinterpret_cast<const ulonglong2 *>(static_cast<const float *>(in) + row + 2 * e)[0];
-                        const ulonglong2 y = reinterpret_cast<const ulonglong2 *>(static_cast<const float *>(in) + row + 2 * e)[1];
-                        S[e] = x.x; S[e + 1] = x.y; S[e + 2] = y.x; S[e + 3] = y.y;
-                    } else {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(in) + row + 2 * e);
-                        S[e] = pk2(bf_lo(x.x), bf_hi(x.x)); S[e + 1] = pk2(bf_lo(x.y), bf_hi(x.y));
-                        S[e + 2] = pk2(bf_lo(x.z), bf_hi(x.z)); S[e + 3] = pk2(bf_lo(x.w), bf_hi(x.w));
-                    }
-                } else {
-#pragma unroll
-                    for (int d = 0; d < 4; ++d) {
-                        const float x = in && mine && k + 2 * d < a.K ? delta_ld(in, f32, row + 2 * (e + d)) : 0.f;
-                        const float y = in && mine && k + 2 * d + 1 < a.K ? delta_ld(in, f32, row + 2 * (e + d) + 1) : 0.f;
-                        S[e + d] = pk2(x, y);
-                    }
-                }
+            for (int e = 0; e < 32; e += 2) {
+                const float4 x = in ? *state_piece(sm + CH_O, v, 16 * hf + e / 2) : make_float4(0.f, 0.f, 0.f, 0.f);
+                S[e] = pk2(x.x, x.y);
+                S[e + 1] = pk2(x.z, x.w);
             }
         }
         // quarter 2 hf + g of the state as chunk c's operand, and kept as the state that enters it (backwards: whose gradient leaves it)
@@ -554,19 +612,22 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         for (int j = 0; j < joins; ++j) {
             publish(0, 0, false);
             publish(0, 1, false);
+            ends += 4096;
+            float4 y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = ends[e * 128];
             if (!(go = wait(B_JD, j))) break;
             tc_fence_after();
-            ends += 128 * 128;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 f32x2 x[8];
                 tmem_ld16x2(at + C::U + 64 * hf + 16 * g, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float4 y = *reinterpret_cast<const float4 *>(ends + 16 * g + 2 * e);
-                    S[8 * g + e] = add2(x[e], pk2(y.x, y.y));
-                    S[8 * g + e + 1] = add2(x[e + 1], pk2(y.z, y.w));
+                for (int e = 0; e < 4; ++e) {
+                    S[8 * g + 2 * e] = add2(x[2 * e], pk2(y[e].x, y[e].y));
+                    S[8 * g + 2 * e + 1] = add2(x[2 * e + 1], pk2(y[e].z, y[e].w));
+                    if (g < 3) y[e] = ends[(4 * g + 4 + e) * 128];
                 }
             }
         }
@@ -682,13 +743,13 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         void *out = !run || c0 + n < all ? nullptr : BACK ? a.dinit : a.final;
         const bool f32 = BACK ? !a.dinit_bf16 : !a.final_bf16;
         if (ENDS && !mat && c0 + n < all) {
-            float *to = const_cast<float *>(ends) + seg * (128 * 128);
+            float4 *to = const_cast<float4 *>(ends) + seg * 4096;
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
                 float4 x;
                 up2(S[e], x.x, x.y);
                 up2(S[e + 1], x.z, x.w);
-                *reinterpret_cast<float4 *>(to + 2 * e) = x;
+                to[e / 2 * 128] = x;
             }
         } else if (ENDS && mat) {
             uint8_t *to = static_cast<uint8_t *>(a.segM) + ((int64_t)unit * (a.nseg - 1) + seg) * SEG_BYTES + hf * (STATE_BYTES / 2) + v * 128;
@@ -701,36 +762,18 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 *reinterpret_cast<uint4 *>(to + STATE_BYTES + ((p ^ (v & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
         }
-        const bool wide = (a.K & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-        if (out && mine)
+        if (out) {                                           // (chunk n - 2 was the last with anything in that stage, and its products are done)
+            uint8_t *buf = stage(n);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                const int k = 64 * hf + 2 * e;
-                if (wide && k < a.K) {
-                    if (f32) {
-                        ulonglong2 *to = reinterpret_cast<ulonglong2 *>(static_cast<float *>(out) + row + 2 * e);
-                        to[0] = make_ulonglong2(S[e], S[e + 1]);
-                        to[1] = make_ulonglong2(S[e + 2], S[e + 3]);
-                    } else {
-                        uint32_t b2[4];
-#pragma unroll
-                        for (int d = 0; d < 4; ++d) {
-                            float x, y;
-                            up2(S[e + d], x, y);
-                            b2[d] = pack_bf16(x, y);
-                        }
-                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + row + 2 * e) = make_uint4(b2[0], b2[1], b2[2], b2[3]);
-                    }
-                } else {
-#pragma unroll
-                    for (int d = 0; d < 4; ++d) {
-                        float x, y;
-                        up2(S[e + d], x, y);
-                        if (k + 2 * d < a.K) delta_st(out, f32, row + 2 * (e + d), x);
-                        if (k + 2 * d + 1 < a.K) delta_st(out, f32, row + 2 * (e + d) + 1, y);
-                    }
-                }
+            for (int e = 0; e < 32; e += 2) {
+                float4 x;
+                up2(S[e], x.x, x.y);
+                up2(S[e + 1], x.z, x.w);
+                *state_piece(buf, v, 16 * hf + e / 2) = x;
             }
+            lanes_meet();
+            rows_state(buf, out, f32, row, a.V, a.K, w, lane);
+        }
         tc_fence_before();
     } else if (w < CH_CW + CH_EW) {
         // ------------------------------------------------------------ one thread a lane, off the chain
@@ -809,35 +852,19 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
     } else if (w < CH_CW + CH_EW + CH_LW) {
         // ------------------------------------------------------------ loads
         const int t = tid - CH_L0;
-        const CUtensorMap *mx = BACK ? &m.dO : &m.v;
-        const bool has_x = values && (BACK ? m.has_dO : m.has_v);
-        auto chunk = [&](int c) {
-            const int ci = idx(c);
-            return DeltaChunk{q.b, q.t0 + ci * DQ, min(DQ, q.len - ci * DQ)};
-        };
-        auto issue = [&](int c) {
+        auto issue_rows = [&](int c) {
             const DeltaChunk k = chunk(c);
             uint8_t *st = stage(c);
-            uint64_t *bar = &ms->bar[B_TMA0 + (c & 1)];
-            if (t == 0) {
-                mbar_expect_tx(bar, OPS_BYTES + (m.has_k + has_x + (m.has_q && outputs)) * TOK_BYTES);
-                if (m.has_k) tma_rows(st + ST_KQ, 2 * HALF, &m.k, bar, k, grp);
-                if (has_x) tma_rows(st + ST_X, HALF, mx, bar, k, h);
-                const uint8_t *ops = static_cast<const uint8_t *>(a.tiles) + (((int64_t)q.slot0 + idx(c)) * a.H + h) * (a.both ? OPS_BOTH : OPS_BYTES);
-                if (BACK) {                                  // the other inverse in its place
-                    bulk_load(st + ST_OPS, ops + SYS_T, 2 * MAT_BYTES, bar);
-                    bulk_load(st + ST_OPS + ATT, ops + ATT, OPS_BYTES - ATT, bar);
-                } else {
-                    bulk_load(st + ST_OPS, ops, OPS_BYTES, bar);
-                }
-                if (m.has_q && outputs) tma_rows(st + ST_KQ + HALF, 2 * HALF, &m.q, bar, k, grp);
-            }
             if (!m.has_k) load_rows<CH_L>(st + ST_KQ, 2 * HALF, tok_rows(a.k, a.ks, k, grp), a.ks[1], k.len, a.K, t);
             if (!has_x && values) {
                 if (BACK) load_rows<CH_L>(st + ST_X, HALF, tok_rows(a.dO, a.dos, k, h), a.dos[1], k.len, a.V, t);
                 else load_rows<CH_L>(st + ST_X, HALF, tok_rows(a.v, a.vs, k, h), a.vs[1], k.len, a.V, t);
             }
             if (!m.has_q && outputs) load_rows<CH_L>(st + ST_KQ + HALF, 2 * HALF, tok_rows(a.q, a.qs, k, grp), a.qs[1], k.len, a.K, t);
+        };
+        auto issue = [&](int c) {
+            if (t == 0) issue_copies(c);
+            issue_rows(c);
         };
         bool go = true;
         for (int j = 0; j < joins && go; ++j) {              // the matrices of the segments between, in either stage's memory in turn
@@ -850,8 +877,10 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         }
         if (joins > 1 && go) go = wait(B_JD, joins - 2);
         if (joins > 0 && go) go = wait(B_JD, joins - 1);
-        if (go && n > 0) issue(0);
-        if (go && n > 1) issue(1);
+        for (int c = 0; c < min(n, 2) && go; ++c) {
+            if (joins > 0 && t == 0) issue_copies(c);
+            issue_rows(c);
+        }
         for (int c = 0; c < n && go; ++c) {
             if (!wait2(B_TMA0, c)) break;
             if (const int len = chunk(c).len; len < DQ) {    // the next sequence's tokens
