@@ -612,10 +612,13 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         for (int j = 0; j < joins; ++j) {
             publish(0, 0, false);
             publish(0, 1, false);
-            ends += 4096;
-            float4 y[4];
+            ends += 4096;                                    // (the state is in tensor memory now: the next end takes its registers)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = ends[e * 128];
+            for (int e = 0; e < 32; e += 2) {
+                const float4 x = ends[e / 2 * 128];
+                S[e] = pk2(x.x, x.y);
+                S[e + 1] = pk2(x.z, x.w);
+            }
             if (!(go = wait(B_JD, j))) break;
             tc_fence_after();
 #pragma unroll
@@ -624,11 +627,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 tmem_ld16x2(at + C::U + 64 * hf + 16 * g, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    S[8 * g + 2 * e] = add2(x[2 * e], pk2(y[e].x, y[e].y));
-                    S[8 * g + 2 * e + 1] = add2(x[2 * e + 1], pk2(y[e].z, y[e].w));
-                    if (g < 3) y[e] = ends[(4 * g + 4 + e) * 128];
-                }
+                for (int e = 0; e < 8; ++e) S[8 * g + e] = add2(x[e], S[8 * g + e]);
             }
         }
         if (n > 0) {
