@@ -24,9 +24,9 @@
 // Q's rows, and both terms of sys, go as one right operand of 128 rows.  All waits are bounded.
 //
 // Bound by latency: a step of a chunk is three products in a row with arithmetic between them, about 2.6 us, of which the products are 40% and the
-// rest are splits, loads and stores of tensor memory at two warps a scheduler; the launch's first step comes 9 us late (tensor memory, maps, cold
-// code).  8192 tokens of 32 heads, 128 x 128: k_prep 50 us, chains 122 + 73 (34.6 GF, 204 MB: 18 and 30 us); 2 x 2048 tokens forwards
-// 31 + 102 us, backwards 105, k_grads 77 (294 MB, 3.8 TB/s).
+// rest are splits, loads and stores of tensor memory at two warps a scheduler; the launch's first step comes 7 us late (first
+// copies, tensor memory, cold code).  8192 tokens of 32 heads, 128 x 128: k_prep 50 us, chains 117 + 67 (34.6 GF, 204 MB: 18 and 30 us);
+// 2 x 2048 tokens forwards 31 + 96 us, backwards 102, k_grads 78 (294 MB, 3.8 TB/s).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -343,7 +343,7 @@ constexpr int CH_CW = 8, CH_EW = 4, CH_LW = 2, CH_NT = (CH_CW + CH_EW + CH_LW + 
 constexpr int CH_L = CH_LW * 32, CH_L0 = (CH_CW + CH_EW) * 32;
 // a stage: K and Q (two images of 128 rows: K's, Q's), V (backwards dO), operands
 constexpr uint32_t ST_KQ = 0, ST_X = 2 * TOK_BYTES, ST_OPS = 3 * TOK_BYTES, ST_BYTES = (ST_OPS + OPS_BYTES + 1023) / 1024 * 1024;
-// and what leaves by bulk copies: two tiles [64][128], plain, of o (backwards dV) and U (mu), the state's image; and a copy of e^G for each warp that computes o
+// and what leaves by bulk copies (and, before that, the state that comes in): two tiles [64][128], plain, of o (backwards dV) and U (mu), the state's image; and a copy of e^G for each warp that computes o
 constexpr uint32_t CH_O = 2 * ST_BYTES, CH_V = CH_O + VAL_BYTES, CH_S = CH_V + VAL_BYTES, CH_EG = CH_S + STATE_BYTES, CH_MISC = CH_EG + CH_EW * DQ * 4, CH_BYTES = CH_MISC + 256 + 1024;
 // TMEM columns.  A lane's columns of each belong to two threads, two of its quarters each, taken one after the other; a quarter of
 // an operand lies over the quarter that its thread has read, both terms one after the other.

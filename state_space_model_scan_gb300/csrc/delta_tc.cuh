@@ -32,8 +32,8 @@ constexpr uint32_t SEG_BYTES = 128 * 128 * 4;    // of a segment: its end in fp3
 // matrix; the second, which knows the state that every segment starts from, those and the last.  So the first segment
 // lasts as long as what goes on beside it on the other SMs, and the last one too; the blocks for those between come in
 // waves.  A block costs one step more than its chunks, joining the ends before a segment 0.8 each, the second launch eight.
-// (8192 tokens of 32 heads: 195 us of chains instead of 340 in one launch, or 260 in three equal segments; 2 x 2048 of 32: 104 cut, 102
-// in one, so it stays whole.)
+// (8192 tokens of 32 heads: 184 us of chains instead of 340 in one launch, or 260 in three equal segments; 2 x 2048 of 32 was 104 cut and
+// 102 in one, so it stays whole.)
 inline void delta_segments(int64_t nseqs, int64_t H, int64_t chunks, int *nseg, int *first, int *len) {
     const int64_t sms = kDeltaSMs, U = nseqs * H;
     *nseg = 1;

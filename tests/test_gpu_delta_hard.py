@@ -190,3 +190,41 @@ def test_rows_of_no_sequence_are_left_in_c():
     f.zero_rest = 1
     assert lib.ssd_delta_fwd(ctypes.byref(p), ctypes.byref(f), ctypes.c_void_p(ws.data_ptr()), n, st) == 0
     assert torch.equal(o, want["o"])
+
+
+@pytest.mark.parametrize("case", [(1, 65, 2, 6, 128, 128, BF16, BF16, None, BF16), (2, 64, 2, 4, 128, 128, BF16, F32, None, F32), (3, 70, 1, 4, 33, 57, BF16, BF16, None, F32),
+                                  (1, 150, 2, 8, 48, 96, BF16, F32, [150], None), (1, 129, 1, 6, 128, 72, BF16, F32, [1, 64, 64], BF16),
+                                  (1, 257, 1, 1, 64, 64, BF16, BF16, None, F32), (1, 9, 1, 40, 128, 128, BF16, F32, None, F32), (1, 1, 8, 264, 128, 64, BF16, BF16, None, F32),
+                                  (1, 300, 4, 12, 96, 48, BF16, BF16, [64, 0, 0, 235, 1], F32)])
+@pytest.mark.parametrize("kept", [True, False])
+def test_odd_sizes_of_more_heads(case, kept):
+    """The tensor-core path at the sizes of the oracle's cases, with the heads that it takes; tolerances as there."""
+    import test_gpu_delta as t
+    B, L, G, H, V, K, dtype, gd, lens, init = case
+    x = t.make(B, L, G, H, V, K, dtype, gd, lens and len(lens), init, train=True, seed=6)
+    cu = None if lens is None else t.packed(lens)
+    a = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    o, f, states = pkg.gated_delta_forward(*a, initial_states=x["init"], cu_seqlens=cu, state_dtype=F32, keep_chunk_states=True)
+    d = pkg.gated_delta_backward(*a, x["do"], initial_states=x["init"], dfinal_states=x["dfinal"], cu_seqlens=cu, chunk_states=states if kept else None)
+    w = t.want(x, K ** -0.5, None if cu is None else cu.tolist(), back=True)
+    assert t.rel(o, w["o"]) <= t.OUT[BF16] and t.rel(f, w["final"]) <= t.OUT[F32]
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert t.rel(d[n], w[n]) <= t.GRAD[BF16], n
+    if init is not None:
+        assert t.rel(d["dinitial_states"], w["dinit"]) <= t.GRAD[BF16]
+
+
+@pytest.mark.parametrize("L,H", [(1, 1), (1, 3), (2, 2), (7, 2), (20, 9), (64, 4), (5, 40)])
+def test_few_tokens_are_as_right_as_their_rounding(L, H):
+    """dg and dbeta of a few tokens are few numbers that may happen to be small: computed in fp32, each is off by its own rounding to
+    bf16 (at most 2^-8 of it), and by 2e-5 of the terms that it is summed from, here up to a hundred times the norm."""
+    import test_gpu_delta as t
+    for seed in range(6):
+        x = t.make(1, L, 1, H, 64, 64, BF16, BF16, None, F32 if seed % 2 else None, train=True, seed=seed)
+        a = [x[n] for n in ("q", "k", "v", "g", "beta")]
+        o, f, states = pkg.gated_delta_forward(*a, initial_states=x["init"], keep_chunk_states=True)
+        d = pkg.gated_delta_backward(*a, x["do"], initial_states=x["init"], dfinal_states=x["dfinal"], chunk_states=states)
+        w = t.want(x, 64 ** -0.5, back=True)
+        for n, v in (("o", o), *d.items()):
+            if n != "dinitial_states":
+                assert t.rel(v, w[n]) <= 2.0 ** -8 + 2e-3, n
