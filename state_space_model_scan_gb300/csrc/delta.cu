@@ -72,7 +72,8 @@ ssd_status check_inputs(const ssd_delta_problem *p, const ssd_delta_args *a) {
 // The tensor-core path takes bf16 data of up to 128 values and keys; fp32 data is computed in fp32, and so are calls of few tokens and
 // heads: dg and dbeta are sums over a head's values and keys, and where there are only a few of them that happen to be small, the
 // roundings of bf16 operands do not average out.  (In 220 calls of 1 to 30000 tokens and heads dbeta or dg was off by more than 5e-3, up
-// to 1.3e-2, in three, of 3, 7 x 2 and 9; in fp32 by 2e-3, their own rounding.  One chunk takes some 20 us in fp32, 14 on the tensor cores.)
+// to 1.3e-2, in three, of 3, 7 x 2 and 9; in fp32 by 2e-3, their own rounding.  One chunk takes 22 to 27 us in fp32, 14 on the
+// tensor cores.)
 constexpr int64_t kFewTokens = 256;
 bool on_tensor_cores(const ssd_delta_problem *p) {
     return p->dtype == SSD_BF16 && p->headdim <= 128 && p->dstate <= 128 && p->batch * p->seqlen * p->nheads > kFewTokens;
