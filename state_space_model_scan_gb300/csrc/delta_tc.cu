@@ -335,6 +335,7 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
         }
     }
     if (tid == PREP_NT - 1) bulk_wait0();
+    if (tid == 0 && !ok && (m.has_k || m.has_q)) mbar_wait(bar, 0);   // (no copy is on its way when the block ends)
 }
 
 // ---------------------------------------------------------------------------------------- the chain
@@ -866,8 +867,10 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
             issue_rows(c);
         };
         bool go = true;
+        int matrices = 0, sent = joins == 0 ? min(n, 2) : 0, seen = 0;   // copies on their way, and those that have come
         for (int j = 0; j < joins && go; ++j) {              // the matrices of the segments between, in either stage's memory in turn
             if (j > 1 && !(go = wait(B_JD, j - 2))) break;
+            matrices = j + 1;
             if (t == 0) {
                 uint64_t *bar = &ms->bar[B_JM0 + (j & 1)];
                 mbar_expect_tx(bar, SEG_BYTES);
@@ -878,10 +881,12 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         if (joins > 0 && go) go = wait(B_JD, joins - 1);
         for (int c = 0; c < min(n, 2) && go; ++c) {
             if (joins > 0 && t == 0) issue_copies(c);
+            sent = c + 1;
             issue_rows(c);
         }
         for (int c = 0; c < n && go; ++c) {
             if (!wait2(B_TMA0, c)) break;
+            seen = c + 1;
             if (const int len = chunk(c).len; len < DQ) {    // the next sequence's tokens
                 if (m.has_k) zero_rows<CH_L>(stage(c) + ST_KQ, 2 * HALF, len, t);
                 if (has_x) zero_rows<CH_L>(stage(c) + ST_X, HALF, len, t);
@@ -893,7 +898,12 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
             if (c > 0 && c + 1 < n) {
                 if (!wait2(B_O0, c - 1) || (!BACK && outs && !wait2(B_EG0, c - 1))) break;
                 issue(c + 1);
+                sent = c + 2;
             }
+        }
+        if (t == 0 && *ab) {                                 // a wait has run out: no copy is on its way when the block ends
+            for (int j = max(0, matrices - 2); j < matrices; ++j) mbar_wait(&ms->bar[B_JM0 + (j & 1)], (j >> 1) & 1);
+            for (int c = seen; c < sent; ++c) mbar_wait(&ms->bar[B_TMA0 + (c & 1)], (c >> 1) & 1);
         }
     } else if (w == CH_CW + CH_EW + CH_LW) {
         // ------------------------------------------------------------ tiles that leave
@@ -1171,8 +1181,8 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
         f += pr + (px - xs) + warp_sum(other);
         if (tid < was.len) delta_st(a.dg, a.g_f32, was.b * a.dgs[0] + (int64_t)(was.t0 + tid) * a.dgs[1] + was_h * a.dgs[2], f);
     };
-    int it = 0;
-    for (int nu = 0; unit < units; ++nu) {
+    int it = 0, nu = 0;
+    for (; unit < units; ++nu) {
         const int grp = unit % a.G;
         const int next = find(unit + gridDim.x, c2);
         uint8_t *kqt = sm + G_KQ + (nu & 1) * 4 * HALF;
@@ -1383,7 +1393,11 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
         c = c2;
     }
     if (w < 2) write_dg(~it & 1);
-    if (!ok && tid == 0) set_status(a.hdr, SSD_ERR_DEVICE_TIMEOUT);
+    if (!ok && tid == 0) {                                   // (no copy is on its way when the block ends)
+        set_status(a.hdr, SSD_ERR_DEVICE_TIMEOUT);
+        mbar_wait(bar + L_KQ, (nu - 1) & 1);
+        mbar_wait(bar + L_HEAD, (it - 1) & 1);
+    }
     bulk_wait0();
     __syncthreads();
     if (w == 0) {
