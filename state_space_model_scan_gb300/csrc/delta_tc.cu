@@ -579,6 +579,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 S[e] = pk2(x.x, x.y);
                 S[e + 1] = pk2(x.z, x.w);
             }
+            if (in) lanes_meet();                            // (the tile of kept states lies over rows that other warps read)
         }
         // quarter 2 hf + g of the state as chunk c's operand, and kept as the state that enters it (backwards: whose gradient leaves it)
         auto publish = [&](int c, int g, bool keep) {

@@ -1,0 +1,46 @@
+"""The gated delta rule's tensor-core kernels where one part of a block works in memory that another part has used: states that come in,
+joins of segments, tiles that leave.  What orders them is in the kernels; here the calls that need it are made often, at the sizes and
+addresses that reach it, and compared bit for bit with one another, or with the oracle (tolerances of test_gpu_delta.py)."""
+import pytest
+import torch
+
+import state_space_model_scan_gb300 as pkg
+import test_gpu_delta as t
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+NAMES = ("q", "k", "v", "g", "beta")
+
+
+def step(x, cu=None):
+    """One training step, with what the forward kept and without."""
+    a = [x[n] for n in NAMES]
+    o, f, kept = pkg.gated_delta_forward(*a, initial_states=x["init"], cu_seqlens=cu, state_dtype=F32, keep_chunk_states=True)
+    rest = dict(initial_states=x["init"], dfinal_states=x["dfinal"], cu_seqlens=cu)
+    d, d2 = pkg.gated_delta_backward(*a, x["do"], chunk_states=kept, **rest), pkg.gated_delta_backward(*a, x["do"], **rest)
+    assert all(torch.equal(d[n], d2[n]) for n in d)
+    return dict(o=o, f=f, **d)
+
+
+def check(got, x, cu=None):
+    w = t.want(x, x["q"].shape[-1] ** -0.5, None if cu is None else cu.tolist(), back=True)
+    assert t.rel(got["o"], w["o"]) <= t.OUT[BF16] and t.rel(got["f"], w["final"]) <= t.OUT[F32]
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert t.rel(got[n], w[n]) <= t.GRAD[BF16], n
+    if x["init"] is not None:
+        assert t.rel(got["dinitial_states"], w["dinit"]) <= t.GRAD[BF16]
+
+
+@pytest.mark.parametrize("init", [F32, BF16])
+@pytest.mark.parametrize("V,K", [(128, 128), (128, 64), (72, 128)])
+def test_states_that_come_in_are_read_before_states_are_kept(V, K, init):
+    """A step from given states, to given gradients of the final ones, in a full card (160 chains): their rows pass through the memory
+    from which the kept states leave.  The first state that is kept is the one that came in."""
+    x = t.make(4, 70, 40, 40, V, K, BF16, F32, None, init, train=True)
+    first = step(x)
+    for h in (0, 17, 39):                                    # (the oracle goes token by token)
+        y = {n: v[:1, :, h:h + 1] if n not in ("init", "dfinal") else v[:1, h:h + 1] for n, v in x.items()}
+        check({n: v[:1, :, h:h + 1] if n not in ("f", "dinitial_states") else v[:1, h:h + 1] for n, v in first.items()}, y)
+    for _ in range(30):
+        again = step(x)
+        assert all(torch.equal(first[n], again[n]) for n in first)
