@@ -361,8 +361,8 @@ struct Cols {
 };
 // Barriers.  A wait tells the completions of a barrier apart by their parity: nothing completes twice before every waiter has seen the
 // first, because a waiter's own next step is needed for the second; where that is two steps off there is one barrier
-// for even chunks and one for odd.
-enum { B_FULL0, B_FULL1, B_TMA0, B_TMA1, B_O0, B_O1, B_WO0, B_WO1, B_EG0, B_EG1, B_P, B_U, B_S, B_END, B_AF, B_WV, B_WS, B_FO, B_FV, B_FS, B_JM0, B_JM1, B_JD,
+// for even chunks (or joins) and one for odd.
+enum { B_FULL0, B_FULL1, B_TMA0, B_TMA1, B_O0, B_O1, B_WO0, B_WO1, B_EG0, B_EG1, B_P, B_U, B_S, B_END, B_AF, B_WV, B_WS, B_FO, B_FV, B_FS, B_JM0, B_JM1, B_JD0, B_JD1,
        B_AY, B_AW = B_AY + 2, B_AS = B_AW + 2, NB = B_AS + 2 };   // (one for each thread's first quarter, one for its second)
 
 // a column of 16 tokens of one value, two to a register, into a plain tile
@@ -387,6 +387,7 @@ struct ChainBars {
     uint32_t tmem;
     int abort_;
 };
+static_assert(sizeof(ChainBars) <= 256, "the barriers' place in shared memory");
 
 __device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
     const int n = a.nseg > 1 && seg < a.nseg - 1 ? min(seg == 0 ? a.seg0 : a.seglen, all - c0) : all - c0, joins = ENDS ? 0 : max(0, seg - 1);
     if (tid == 0) {
         for (int b : {B_FULL0, B_FULL1}) mbar_init(&ms->bar[b], CH_LW);
-        for (int b : {B_O0, B_O1, B_P, B_U, B_S, B_END, B_FO, B_FV, B_FS, B_JM0, B_JM1, B_JD}) mbar_init(&ms->bar[b], 1);
+        for (int b : {B_O0, B_O1, B_P, B_U, B_S, B_END, B_FO, B_FV, B_FS, B_JM0, B_JM1, B_JD0, B_JD1}) mbar_init(&ms->bar[b], 1);
         for (int b : {B_WV, B_WS}) mbar_init(&ms->bar[b], CH_CW);
         for (int b = B_AY; b < NB; ++b) mbar_init(&ms->bar[b], CH_CW);
         for (int b : {B_AF, B_EG0, B_EG1}) mbar_init(&ms->bar[b], CH_EW);
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 S[e] = pk2(x.x, x.y);
                 S[e + 1] = pk2(x.z, x.w);
             }
-            if (!(go = wait(B_JD, j))) break;
+            if (!(go = wait2(B_JD0, j))) break;
             tc_fence_after();
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -870,7 +871,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
         bool go = true;
         int matrices = 0, sent = joins == 0 ? min(n, 2) : 0, seen = 0;   // copies on their way, and those that have come
         for (int j = 0; j < joins && go; ++j) {              // the matrices of the segments between, in either stage's memory in turn
-            if (j > 1 && !(go = wait(B_JD, j - 2))) break;
+            if (j > 1 && !(go = wait2(B_JD0, j - 2))) break;
             matrices = j + 1;
             if (t == 0) {
                 uint64_t *bar = &ms->bar[B_JM0 + (j & 1)];
@@ -878,8 +879,8 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 bulk_load(stage(j), static_cast<const uint8_t *>(a.segM) + ((int64_t)unit * (a.nseg - 1) + 1 + j) * SEG_BYTES, SEG_BYTES, bar);
             }
         }
-        if (joins > 1 && go) go = wait(B_JD, joins - 2);
-        if (joins > 0 && go) go = wait(B_JD, joins - 1);
+        if (joins > 1 && go) go = wait2(B_JD0, joins - 2);
+        if (joins > 0 && go) go = wait2(B_JD0, joins - 1);
         for (int c = 0; c < min(n, 2) && go; ++c) {
             if (joins > 0 && t == 0) issue_copies(c);
             sent = c + 1;
@@ -954,7 +955,7 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                     umma_bf16_ta(tmem + C::U, A + 8, mnmaj(M, k, STATE_BYTES / 2), id128t, 1);
                     umma_bf16_ta(tmem + C::U, A, mnmaj(M + STATE_BYTES, k, STATE_BYTES / 2), id128t, 1);
                 }
-                umma_commit(&ms->bar[B_JD]);
+                umma_commit(&ms->bar[B_JD0 + (j & 1)]);
             }
             for (int c = 0; c < n && go; ++c) {
                 const uint32_t st = s0 + (c & 1) * ST_BYTES, K = st + ST_KQ, Q = K + HALF, X = st + ST_X, ops = st + ST_OPS;

@@ -44,3 +44,27 @@ def test_states_that_come_in_are_read_before_states_are_kept(V, K, init):
     for _ in range(30):
         again = step(x)
         assert all(torch.equal(first[n], again[n]) for n in first)
+
+
+def odd_rows(x, names=("q", "k", "v", "do")):
+    """The same values in rows that start at odd elements, which no tensor map describes."""
+    def odd(v):
+        w = torch.full((*v.shape[:2], v[0, 0].numel() + 3), float("nan"), dtype=v.dtype, device="cuda")
+        w[..., 1:-2] = v.flatten(2)
+        return w[..., 1:-2].unflatten(2, v.shape[2:])
+    return {n: odd(v) if n in names else v for n, v in x.items()}
+
+
+@pytest.mark.parametrize("B,H,L,lens,V,K", [(1, 2, 64 * 33, None, 128, 128), (1, 2, 64 * 33 - 7, None, 72, 48), (2, 2, 64 * 30 + 1, None, 64, 128),
+                                            (1, 3, 2176, [1700, 0, 64, 1, 411], 128, 40), (1, 1, 64 * 40, None, 33, 57)])
+def test_segments_of_smaller_heads_and_odd_rows(B, H, L, lens, V, K):
+    """Chains in up to eleven segments, the last with up to nine joins before it, of states that are a part of 128 x 128."""
+    x = t.make(B, L, 1, H, V, K, BF16, F32, lens and len(lens), F32, seed=3, train=True)
+    x["g"] *= 0.02                                           # the past matters across segments
+    cu = None if lens is None else t.packed(lens)
+    first = step(x, cu)
+    check(first, x, cu)
+    for y in (x, odd_rows(x), odd_rows(x, ("k", "do"))):
+        for _ in range(5):
+            again = step(y, cu)
+            assert all(torch.equal(first[n], again[n]) for n in first)
