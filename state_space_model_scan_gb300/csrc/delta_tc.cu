@@ -1117,7 +1117,6 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
     auto issue_kq = [&](const DeltaChunk &k, int grp, uint8_t *kq) {
         if (one && (w == 11 || w == 14)) {
             const bool has = w == 11 ? m.has_k : m.has_q;
-            bulk_wait_read0();                               // (the chunk before this one has left that tile: the same thread sent it)
             mbar_expect_tx(bar + L_KQ, has ? TOK_BYTES : 0);
             if (has) tma_rows(w == 11 ? kq : kq + HALF, 2 * HALF, w == 11 ? &m.k : &m.q, bar + L_KQ, k, grp);
         }
@@ -1302,6 +1301,7 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
             fence_proxy_async_smem();
             tc_fence_before();
             ok = mbar_wait(bar + L_D2, it & 1) && ok;
+            if (one && (w == 11 || w == 14)) bulk_wait_read0();   // the chunk before this one has left its tile, which may be filled anew now by all threads
             __syncthreads();
             tc_fence_after();
             if (tid == 15 * 32) {
