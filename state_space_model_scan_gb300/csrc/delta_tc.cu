@@ -290,6 +290,7 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
     fence_proxy_async_smem();
     __syncthreads();
     if (w == 0) {
+        if (!ok) mbar_wait(bar + 1, 0);                      // (nor is the product)
         tc_fence_after();
         tmem_dealloc(tmem, 64);
     }
@@ -1108,6 +1109,7 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
     if (w == 0) tmem_alloc(tm, 512);
     if (tid == 0) {
         for (int i = 0; i < 5; ++i) mbar_init(bar + i, i == L_KQ ? 2 : i == L_HEAD ? 5 : 1);
+        tm[1] = 0;
         fence_mbar_init();
     }
     for (int e = tid; e < (int)HALF / 16; e += GR_NT) reinterpret_cast<uint4 *>(sm + G_Z)[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -1148,7 +1150,9 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
     };
     issue_kq(c, unit % a.G, sm + G_KQ);
     issue(c, unit / a.G, unit % a.G * per);
-    bool ok = true;
+    // After a wait has run out the block leaves both loops at the next head's start.  (The word beside the tensor memory's address is written
+    // before one barrier and read behind it, by all threads alike; a barrier that gathers it, and waits that look at it, took 12 us of 78 more.)
+    bool ok = true, left = false;
     const uint32_t base = smem_u32(sm), A = base + G_A, U = base + G_U, S = base + G_S, dS = base + G_DS, EF = base + G_EF, Z = base + G_Z;
     const int row = (w & 3) * 32 + lane, i = row & 63, qu = w >> 2, j0 = 16 * qu;
     const bool qside = row >= 64;
@@ -1206,9 +1210,12 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
             }
             fence_proxy_async_smem();
             tc_fence_before();
+            if (!ok) tm[1] = 1;
             __syncthreads();
             tc_fence_after();
-            tmem = *tm;
+            const uint2 words = *reinterpret_cast<const uint2 *>(tm);
+            tmem = words.x;
+            if ((left = words.y != 0)) break;
             if (tid == 15 * 32) {
                 if (r == 0)
 #pragma unroll
@@ -1369,6 +1376,7 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
             was_h = h;
             was_whole = whole;
         }
+        if (left) break;
         // dK's and dQ's rows: a whole chunk through K's and Q's tile, which nothing reads any more, as one copy
         uint32_t out[16];
 #pragma unroll
@@ -1395,16 +1403,16 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
         c = c2;
     }
     if (w < 2) write_dg(~it & 1);
-    if (!ok && tid == 0) {                                   // (no copy is on its way when the block ends)
-        set_status(a.hdr, SSD_ERR_DEVICE_TIMEOUT);
-        mbar_wait(bar + L_KQ, (nu - 1) & 1);
-        mbar_wait(bar + L_HEAD, (it - 1) & 1);
-    }
     bulk_wait0();
-    __syncthreads();
+    if (__syncthreads_or(!ok) && w == 0) {                   // no copy and no product is on its way when the block ends
+        if (lane == 0) set_status(a.hdr, SSD_ERR_DEVICE_TIMEOUT);
+        mbar_wait(bar + L_KQ, (left ? nu : nu - 1) & 1);
+        mbar_wait(bar + L_HEAD, (left ? it : it - 1) & 1);
+        if (it > 0) mbar_wait(bar + L_D4, (it - 1) & 1);
+    }
     if (w == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(*tm, 512);
     }
 }
 
