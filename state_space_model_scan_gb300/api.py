@@ -427,7 +427,7 @@ class GatedDeltaFunction:
     """The gated delta rule in an autograd graph: o, final_states = GatedDeltaFunction.apply(...).  Where gradients are asked for, the
     forward keeps what the backward starts from (ssd_delta_chunk_states_size: on tensor cores 90 KB per 64 tokens and value head;
     with keep_chunk_states=False the backward computes it again).  Gradients go to q, k, v, g, beta and initial_states; an unused
-    final state costs no gradient of zeros.  A second differentiation is refused."""
+    final state costs no gradient of zeros.  A second differentiation is refused, and so is a forward-mode one."""
 
     @staticmethod
     def apply(q, k, v, g, beta, initial_states=None, cu_seqlens=None, scale=None, keep_chunk_states=True):
@@ -472,7 +472,7 @@ def qk_norm_backward(q, k, dq, dk, q_weight=None, k_weight=None, cos=None, sin=N
 
 class QKNormFunction:
     """The norm and rotation of queries and keys in an autograd graph: q_out, k_out = QKNormFunction.apply(...).  It keeps its inputs
-    alone; gradients go to q, k and the weights.  A second differentiation is refused."""
+    alone; gradients go to q, k and the weights.  A second differentiation is refused, and so is a forward-mode one."""
 
     @staticmethod
     def apply(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, mode="rms", interleaved=False, eps=1e-6):

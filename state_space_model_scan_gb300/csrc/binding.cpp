@@ -9,6 +9,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/core/AutogradState.h>
 #include <ATen/ops/zeros_like.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/function.h>
@@ -641,6 +642,13 @@ void refuse_second(ag::variable_list &d, ag::edge_list &&edges) {
 // An output's gradient with unit stride in its last dimension
 Tensor unit(const Tensor &t) { return !t.defined() || t.stride(-1) == 1 ? t : t.contiguous(); }
 
+// No operator here has a forward-mode derivative: a tensor that carries a tangent is refused, where an output without one would be wrong in
+// silence.
+void refuse_tangent(const Tensor &t, const char *name) {
+    if (t.defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+        fail(PyExc_NotImplementedError, "%s carries a tangent: this operator has no forward-mode derivative", name);
+}
+
 // An operator's node: its N inputs (and one tensor more) saved.
 template <size_t N>
 struct OpNode : ag::Node {
@@ -662,7 +670,10 @@ struct OpNode : ag::Node {
             at::NoGradGuard off;
             const Tensor *t[N];
             for (size_t i = 0; i < N; ++i) t[i] = &in[i];
-            d = locked([&] { return f(t, grads); });
+            d = locked([&] {
+                for (const Tensor &g : grads) refuse_tangent(g, "an output's gradient");
+                return f(t, grads);
+            });
         }
         if (again) {
             ag::edge_list edges = ag::collect_next_edges(ag::variable_list(in.begin(), in.end()), grads);
@@ -693,7 +704,10 @@ struct GatedDelta : OpNode<8> {                            // the seven inputs, 
 // delta_apply(the inputs, scale, keep) -> o, final_states in a graph
 PyObject *delta_apply(PyObject *const *a) {
     const Tensor *t[8];
-    for (int i = 0; i < 7; ++i) t[i] = &arg(a[i], delta_names[i], i >= 5);
+    for (int i = 0; i < 7; ++i) {
+        t[i] = &arg(a[i], delta_names[i], i >= 5);
+        refuse_tangent(*t[i], delta_names[i]);
+    }
     const auto scale = number(a[7], "scale");
     const bool graph = graph_wanted(t, 6);
     const DeltaOut out = delta_forward(t, scale, true, -1, graph && a[8] == Py_True, Py_None);
@@ -862,6 +876,7 @@ struct QKNorm : OpNode<7> {
 PyObject *qk_apply(PyObject *const *a) {
     const Tensor *t[7];
     read(a, qk_names, 1, t);
+    for (int i = 0; i < 7; ++i) refuse_tangent(*t[i], qk_names[i]);
     const QkHow how = qk_how(a + 7);
     const auto out = qk_forward(t, how, Py_None);
     if (graph_wanted(t, 4)) {
