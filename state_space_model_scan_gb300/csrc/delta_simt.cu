@@ -261,6 +261,7 @@ __global__ void __launch_bounds__(chain_threads(VS), 1) k_chain(const DeltaArgs 
     float *S = sm, *Y = S + VS * KL, *Z = Y + 64 * XL, *stages = Z + 64 * XL;
     const int nv = (a.V + VS - 1) / VS, tid = threadIdx.x, ig = tid / (VS / 2), vg = tid % (VS / 2);
     const int v0 = blockIdx.x % nv * VS, h = blockIdx.x / nv % a.H, s = blockIdx.x / nv / a.H, grp = h / (a.H / a.G);
+    if (a.nslots == 0 && blockIdx.x == 0 && tid < HDR_WORDS) a.hdr[tid] = 0;   // (of a call without tokens this is the first launch)
     const DeltaSeq q = delta_seq(a, s);
     const int64_t sat = ((int64_t)s * a.H + h) * a.V * a.K;
     const int nch = (q.len + DQ - 1) / DQ;

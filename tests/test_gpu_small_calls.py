@@ -1,0 +1,46 @@
+"""Calls with nothing in them: no tokens, no heads of keys."""
+import ctypes
+
+import pytest
+import torch
+
+import state_space_model_scan_gb300 as pkg
+from state_space_model_scan_gb300 import _lib
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_call_without_tokens_leaves_a_status(dtype, packed):
+    """The workspace's contents need not be initialised, and its status is that of the call."""
+    z = lambda *s, t=dtype: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+    S = 3 if packed else 2
+    a = [z(1 if packed else 2, 0, 1, 64), z(1 if packed else 2, 0, 1, 64), z(1 if packed else 2, 0, 2, 64), z(1 if packed else 2, 0, 2, t=F32), z(1 if packed else 2, 0, 2, t=F32)]
+    init = torch.randn(S, 2, 64, 64, device="cuda")
+    cu = torch.zeros(S + 1, dtype=torch.int32, device="cuda") if packed else None
+    ws = torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda")
+
+    class Same:
+        def get(self, n):
+            assert n <= ws.numel()
+            return ws
+    d = pkg.gated_delta_backward(*a, a[2], initial_states=init, dfinal_states=init, cu_seqlens=cu, workspace=Same())
+    assert torch.equal(d["dinitial_states"], init)
+    assert _lib.query_status(ws) == _lib.SSD_OK
+    # the forward through C, whose workspace Python allocates by itself
+    ws.fill_(7)
+    p = _lib.DeltaProblem(1 if packed else 2, 0, 2, 1, 64, 64, S if packed else 0, 0.125, _lib.SSD_BF16 if dtype == BF16 else _lib.SSD_F32)
+    f, out = _lib.DeltaArgs(), torch.empty_like(init)
+    for name, t in (("initial_states", init), ("final_states", out)):
+        d = _lib.Tensor()
+        d.ptr, d.dtype = t.data_ptr(), _lib.SSD_F32
+        for i, s in enumerate(t.stride()):
+            d.stride[i] = s
+        setattr(f, name, d)
+    if packed:
+        f.cu_seqlens = cu.data_ptr()
+    st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert _lib.load().ssd_delta_fwd(ctypes.byref(p), ctypes.byref(f), ctypes.c_void_p(ws.data_ptr()), ctypes.c_size_t(ws.numel()), st) == 0
+    assert torch.equal(out, init) and _lib.query_status(ws) == _lib.SSD_OK
