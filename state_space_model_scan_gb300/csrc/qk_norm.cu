@@ -570,7 +570,7 @@ ssd_status ssd_qk_norm_bwd(const ssd_qk_problem *p, const ssd_qk_bwd_args *b, vo
     if (b == nullptr) return SSD_ERR_INVALID_ARGUMENT;
     const ssd_qk_args *f = &b->fwd;
     if (ssd_status s = check(p, f); s != SSD_OK) return s;
-    float *dw[2] = {f->q_weight ? b->dq_weight : nullptr, f->k_weight && p->k_heads > 0 ? b->dk_weight : nullptr};
+    float *dw[2] = {f->q_weight ? b->dq_weight : nullptr, f->k_weight ? b->dk_weight : nullptr};   // (without heads of keys theirs is zero)
     if ((f->q_weight && !dw[0]) || (f->k_weight && p->k_heads > 0 && !dw[1])) return SSD_ERR_INVALID_ARGUMENT;
     if (!al(dw[0], 4) || !al(dw[1], 4)) return SSD_ERR_MISALIGNED;
     cudaStream_t st = (cudaStream_t)stream;

@@ -44,3 +44,20 @@ def test_a_call_without_tokens_leaves_a_status(dtype, packed):
     st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     assert _lib.load().ssd_delta_fwd(ctypes.byref(p), ctypes.byref(f), ctypes.c_void_p(ws.data_ptr()), ctypes.c_size_t(ws.numel()), st) == 0
     assert torch.equal(out, init) and _lib.query_status(ws) == _lib.SSD_OK
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dim", [64, 40, 7])
+def test_weights_of_no_key_heads_have_gradients_of_zero(dtype, dim):
+    q, k = torch.randn(2, 9, 3, dim, device="cuda").to(dtype), torch.empty(2, 9, 0, dim, device="cuda", dtype=dtype)
+    w = 1 + torch.rand(2, dim, device="cuda")
+    dq = torch.randn_like(q)
+    want = pkg.qk_norm_backward(q, None, dq, None, w[0])
+    for _ in range(4):
+        full = torch.full((dim,), float("nan"), device="cuda")             # what is allocated next holds NaN
+        del full
+        got = pkg.qk_norm_backward(q, k, dq, k, w[0], w[1])
+        assert torch.equal(got["dq"], want["dq"]) and torch.equal(got["dq_weight"], want["dq_weight"])
+        assert not got["dk_weight"].any() and got["dk"].shape == k.shape
+    got = pkg.qk_norm_backward(q, k, dq, k, None, w[1])                    # the keys' weights alone
+    assert torch.equal(got["dq"], pkg.qk_norm_backward(q, None, dq, None)["dq"]) and not got["dk_weight"].any()
