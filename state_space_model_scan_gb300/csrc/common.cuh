@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "../../include/ssd.h"
 
 namespace ssd {
@@ -113,9 +115,14 @@ inline cudaError_t ensure_smem_attr(K kernel, int bytes, int *set_bytes /* [64] 
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (set_bytes[dev & 63] >= bytes) return cudaSuccess;
+    int *set = &set_bytes[dev & 63];
+    if (__atomic_load_n(set, __ATOMIC_ACQUIRE) >= bytes) return cudaSuccess;
+    // one thread at a time: of two that ask for different sizes the larger stays
+    static std::mutex m;
+    const std::lock_guard<std::mutex> one(m);
+    if (*set >= bytes) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) set_bytes[dev & 63] = bytes;
+    if (e == cudaSuccess) __atomic_store_n(set, bytes, __ATOMIC_RELEASE);
     return e;
 }
 

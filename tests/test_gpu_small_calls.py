@@ -1,5 +1,8 @@
-"""Calls with nothing in them: no tokens, no heads of keys."""
+"""Calls with nothing in them, no tokens, no heads of keys, and calls that several threads make for the first time."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -61,3 +64,41 @@ def test_weights_of_no_key_heads_have_gradients_of_zero(dtype, dim):
         assert not got["dk_weight"].any() and got["dk"].shape == k.shape
     got = pkg.qk_norm_backward(q, k, dq, k, None, w[1])                    # the keys' weights alone
     assert torch.equal(got["dq"], pkg.qk_norm_backward(q, None, dq, None)["dq"]) and not got["dk_weight"].any()
+
+
+FIRST = r"""
+import sys, threading
+import torch
+import state_space_model_scan_gb300 as pkg
+
+def one(K, back):
+    r = lambda *s: torch.rand(*s, device="cuda") / 16
+    x = [r(1, 2, 1, K), r(1, 2, 1, K), r(1, 2, H, 32), -r(1, 2, H), r(1, 2, H)]
+    gate.wait()
+    return pkg.gated_delta_backward(*x, x[2]) if back else pkg.gated_delta_forward(*x)
+
+torch.zeros(1, device="cuda")
+for H in (2, 64, 200):                         # 8, 16 or 32 values a block
+    for back in (False, True):
+        sizes, errors = [8, 256, 40, 200, 100, 256, 8, 256], []
+        gate = threading.Barrier(len(sizes))
+        def work(K):
+            try:
+                one(K, back)
+            except Exception as e:
+                errors.append(e)
+        ts = [threading.Thread(target=work, args=(K,)) for K in sizes]
+        [t.start() for t in ts]
+        [t.join() for t in ts]
+        torch.cuda.synchronize()
+        if errors:
+            sys.exit("refused: %r" % errors)
+"""
+
+
+def test_threads_that_launch_a_kernel_for_the_first_time():
+    """Eight threads, each with another size of the keys, and so of the shared memory that the same kernel is launched with."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for _ in range(3):
+        r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0, r.stderr[-2000:]
