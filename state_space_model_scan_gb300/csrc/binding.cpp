@@ -24,6 +24,7 @@
 #include <array>
 #include <initializer_list>
 #include <memory>
+#include <mutex>
 #include <optional>
 #include <string>
 
@@ -657,13 +658,17 @@ struct OpNode : ag::Node {
         for (size_t i = 0; i < N; ++i) saved[i] = ag::SavedVariable(*t[i], false);
     }
     void release_variables() override {
+        const std::lock_guard<std::mutex> one(mutex_);       // (two threads may go through one graph)
         for (auto &v : saved) v.reset_data();
     }
     // f(inputs, gradients) -> gradients of the inputs, without a graph
     template <typename F>
     ag::variable_list run(ag::variable_list &&grads, F f) {
         std::array<Tensor, N> in;
-        for (size_t i = 0; i < N; ++i) in[i] = saved[i].unpack();
+        {
+            const std::lock_guard<std::mutex> one(mutex_);
+            for (size_t i = 0; i < N; ++i) in[i] = saved[i].unpack();
+        }
         const bool again = at::GradMode::is_enabled();
         ag::variable_list d;
         {
