@@ -1,14 +1,18 @@
-"""The autograd nodes of the gated delta rule, on its tensor-core path (more than 256 tokens x heads), and of the norm of queries and keys,
-where one graph is gone through by several threads."""
+"""The autograd node of the gated delta rule on its tensor-core path (more than 256 tokens x heads; test_gpu_delta_autograd.py's calls are
+smaller and run in fp32), and the norm of queries and keys beside it: threads, streams, retained graphs, hooks, checkpoints, strided
+gradients, one graph in several threads.  Bit for bit as the calls without a graph, or as one another."""
 import threading
 
 import pytest
 import torch
+import torch.utils.checkpoint
 
 import state_space_model_scan_gb300 as pkg
+from state_space_model_scan_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
+NAMES = ("dq", "dk", "dv", "dg", "dbeta", "dinitial_states")
 
 
 def leaves(seed=0, L=200, H=4, V=64, K=128):
@@ -37,6 +41,68 @@ def total(out):
     return sum(o.float().sum() for o in out)
 
 
+def test_these_calls_take_the_tensor_cores():
+    """What is kept says which path a call takes: states, values and matrices of a chunk and head (4 of each here) in bf16, 90 KB, or
+    states and values in fp32."""
+    import ctypes
+    for L, H, tc in ((200, 4, True), (65, 4, True), (64, 4, False), (70, 2, False)):
+        n = ctypes.c_size_t()
+        p = _lib.DeltaProblem(1, L, H, 2, 64, 128, 0, 0.1, _lib.SSD_BF16)
+        assert _lib.load().ssd_delta_chunk_states_size(ctypes.byref(p), ctypes.byref(n)) == 0
+        chunks = -(-L // 64) * H
+        assert (n.value // chunks > 65536) == tc and (tc or n.value == chunks * (64 * 128 + 64 * 64) * 4)
+
+
+def test_a_graph_gives_what_the_calls_give():
+    x = leaves()
+    out = pkg.GatedDeltaFunction.apply(*x)
+    w = [torch.randn_like(o) for o in out]
+    got = torch.autograd.grad(out, x, w, retain_graph=True)
+    a = [t.detach() for t in x]
+    d = pkg.gated_delta_backward(*a[:5], w[0], initial_states=a[5], dfinal_states=w[1])
+    assert same(got, [d[n] for n in NAMES]) and same(got, torch.autograd.grad(out, x, w))
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(out, x, w)
+    again = torch.autograd.grad(pkg.GatedDeltaFunction.apply(*x, None, None, False), x, w)
+    assert same(got, again)
+
+
+def test_strided_and_expanded_gradients():
+    x = leaves()
+    out = pkg.GatedDeltaFunction.apply(*x)
+    for w in ([torch.randn(*o.shape[:-1], 2 * o.shape[-1], device="cuda").to(o.dtype)[..., ::2] for o in out],
+              [torch.randn(*o.shape[:-1], o.shape[-1] + 3, device="cuda").to(o.dtype)[..., 1:-2] for o in out],
+              [torch.ones((), dtype=o.dtype, device="cuda").expand_as(o) for o in out]):
+        a = torch.autograd.grad(out, x, w, retain_graph=True)
+        assert same(a, torch.autograd.grad(out, x, [t.contiguous() for t in w], retain_graph=True))
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_threads_and_streams(op):
+    """Eight threads, each with its own stream, inputs and size (tensor maps are encoded by all of them at once)."""
+    f, make = OPS[op]
+    xs = [make(i, 130 + 30 * i) if op == "delta" else make(i) for i in range(8)]
+    want = [torch.autograd.grad(total(f.apply(*x)), x) for x in xs]
+    torch.cuda.synchronize()
+    got, errors = [None] * len(xs), []
+
+    def work(i):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(8):
+                    got[i] = torch.autograd.grad(total(f.apply(*xs[i])), xs[i])
+            st.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(len(xs))]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert not errors
+    assert all(same(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("retain", [True, False])
 @pytest.mark.parametrize("op", OPS)
 def test_one_graph_in_several_threads(op, retain):
@@ -61,3 +127,13 @@ def test_one_graph_in_several_threads(op, retain):
         torch.cuda.synchronize()
         assert all(same(g, want) for g in got) and len(got) + len(errors) == 4
         assert len(got) == 4 if retain else all("second time" in str(e) or "freed" in str(e) for e in errors)
+
+
+def test_saved_tensor_hooks_and_checkpoints():
+    x = leaves()
+    f = pkg.GatedDeltaFunction.apply
+    want = torch.autograd.grad(total(f(*x)), x)
+    with torch.autograd.graph.save_on_cpu():
+        out = f(*x)
+    assert same(want, torch.autograd.grad(total(out), x))
+    assert same(want, torch.autograd.grad(total(torch.utils.checkpoint.checkpoint(f, *x, use_reentrant=False)), x))
