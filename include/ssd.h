@@ -540,7 +540,9 @@ ssd_status ssd_conv1d_step(const ssd_conv_problem *prob, const void *u, int64_t 
  *                    Tokens before the first sequence and behind the last are not read; their rows of the
  *                    outputs (o, or dq, dk, dv, dg, dbeta) are left as they were, or zeroed when zero_rest is set.
  * A sequence without tokens has final state = initial state (zero without one), and passes dfinal on to
- * dinitial.  headdim and dstate 1..256, else SSD_ERR_UNSUPPORTED.
+ * dinitial.  A token that is not finite makes not only its sequence's later outputs of its head (group) not finite, but those of up to 63
+ * tokens before it, too: of all that lie in its chunk of 64.  Padding inside a batch row holds finite values, or lies outside
+ * cu_seqlens.  headdim and dstate 1..256, else SSD_ERR_UNSUPPORTED.
  *
  * It is computed in chunks of 64 tokens.  f32 data, and calls of up to 256 tokens times heads: fp32 arithmetic throughout.
  * Other bf16 data with headdim and dstate up to 128: tensor cores with fp32 accumulation; what is carried from chunk to chunk goes into them as the

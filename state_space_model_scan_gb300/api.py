@@ -406,7 +406,8 @@ def gated_delta_forward(q, k, v, g, beta, scale=None, initial_states=None, cu_se
     q, k: [batch, seqlen, ngroups, dstate]; v, o: [batch, seqlen, nheads, headdim], q's type; head h reads group
     h // (nheads // ngroups); g (log decay, at most 0), beta: [batch, seqlen, nheads] float32 or v's type; scale: dstate ** -0.5
     by default; initial_states: [S, nheads, headdim, dstate] float32 or bfloat16; cu_seqlens: int32 [S + 1] (batch 1), tokens before the
-    first sequence and behind the last are padding: never read, and zeros in the outputs and gradients.  Keys are expected
+    first sequence and behind the last are padding: never read, and zeros in the outputs and gradients (padding inside a row of a batch
+    holds finite values: one that is not reaches every token of its chunk of 64).  Keys are expected
     at unit length (qk_norm_forward(mode="l2")).  state_dtype: of the final states (default: that of
     initial_states, else float32).  keep_chunk_states: also return the buffer that gated_delta_backward(chunk_states=...)
     starts from."""

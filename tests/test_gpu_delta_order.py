@@ -82,3 +82,23 @@ def test_tiles_of_gradients_have_left_before_they_are_filled_anew(names):
     for _ in range(10):
         again = step(y)
         assert all(torch.equal(first[n], again[n]) for n in first)
+
+
+@pytest.mark.parametrize("B,L,H,V,K,dtype,at", [(2, 200, 4, 128, 128, BF16, 100), (2, 200, 4, 64, 72, BF16, 64), (1, 64 * 30, 2, 128, 128, BF16, 64 * 20 + 63),
+                                                (2, 140, 2, 40, 24, F32, 100), (1, 130, 2, 200, 40, BF16, 129)])
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "beta"])
+def test_a_token_that_is_not_finite_reaches_its_chunk_and_what_follows(B, L, H, V, K, dtype, at, name):
+    """Tokens of earlier chunks, other heads and other rows stay as they are, bit for bit."""
+    x = t.make(B, L, 2, H, V, K, dtype, F32, None, F32)
+    a = [x[n] for n in NAMES]
+    o, f = pkg.gated_delta_forward(*a, initial_states=x["init"])
+    y = {n: v.clone() for n, v in x.items()}
+    y[name][0, at, 0] = float("nan")
+    o2, f2 = pkg.gated_delta_forward(*[y[n] for n in NAMES], initial_states=y["init"])
+    own = H // 2 if name in ("q", "k") else 1                # heads of the first group
+    assert torch.equal(o2[0, :at // 64 * 64], o[0, :at // 64 * 64])
+    assert torch.equal(o2[0, :, own:], o[0, :, own:]) and torch.equal(f2[0, own:], f[0, own:])
+    assert torch.equal(o2[1:], o[1:]) and torch.equal(f2[1:], f[1:])
+    assert not torch.isfinite(o2[0, at, 0]).all()
+    if name != "q":                                          # (a query is read and not kept)
+        assert not torch.isfinite(o2[0, at:, 0]).any(-1).any() and not torch.isfinite(f2[0, 0]).all()
