@@ -765,7 +765,10 @@ __global__ void __launch_bounds__(CH_NT, 1) k_chain(const DeltaArgs a, const __g
                 *reinterpret_cast<uint4 *>(to + STATE_BYTES + ((p ^ (v & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
         }
-        if (out) {                                           // (chunk n - 2 was the last with anything in that stage, and its products are done)
+        if (out) {
+            // Chunk n - 2 was the last with anything in that stage, and its products are done.  Its gates, which the warps of o may still have to copy, lie
+            // behind the state.
+            static_assert(128 * 128 * 4 <= ST_OPS + GATES, "the state is staged in front of a stage's gates");
             uint8_t *buf = stage(n);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
