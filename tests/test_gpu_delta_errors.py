@@ -1,0 +1,34 @@
+"""How far bf16 outputs and gradients of the gated delta rule's tensor-core path are from the float64 oracle: no more than the roundings that
+they are documented to go through.
+
+A rounding to bf16 is off by at most half a step, uniformly, 2^-8 / sqrt(3) = 2.26e-3 in the mean square of values at the lower end of
+a power of two (less above it).  n of them, of random sign, one after another or beside one another: sqrt(n) times that.
+  o:   att, beta U, the output itself                                          3   3.91e-3
+  dv:  att, the gradient itself (what is carried is held to 2^-17)             2   3.20e-3
+  dq:  U and F, or the kept state; the gradient itself                         3   3.91e-3
+  dk:  mu, U and E, or F's two, or a kept state and U; the gradient itself     4   4.52e-3
+States go as the sum of two bf16 values: 2e-5, as in test_gpu_delta.py."""
+import pytest
+import torch
+
+import state_space_model_scan_gb300 as pkg
+import test_gpu_delta as t
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+BOUND = dict(o=3.91e-3, f=2e-5, dv=3.20e-3, dq=3.91e-3, dk=4.52e-3)
+
+
+@pytest.mark.parametrize("kept", [True, False])
+@pytest.mark.parametrize("B,L,G,H,V,K,lens", [(1, 320, 4, 8, 128, 128, None), (2, 256, 3, 3, 128, 64, None), (1, 500, 2, 4, 64, 128, [129, 1, 0, 370]),
+                                              (1, 1408, 1, 2, 128, 128, None)])
+def test_errors_are_those_of_the_roundings(B, L, G, H, V, K, lens, kept):
+    x = t.make(B, L, G, H, V, K, BF16, F32, lens and len(lens), F32, seed=8, train=True)
+    cu = None if lens is None else t.packed(lens)
+    a = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    o, f, states = pkg.gated_delta_forward(*a, initial_states=x["init"], cu_seqlens=cu, keep_chunk_states=True)
+    d = pkg.gated_delta_backward(*a, x["do"], initial_states=x["init"], dfinal_states=x["dfinal"], cu_seqlens=cu, chunk_states=states if kept else None)
+    w = t.want(x, K ** -0.5, None if cu is None else cu.tolist(), back=True)
+    got = dict(d, o=o, f=f)
+    off = {n: t.rel(got[n], w["final" if n == "f" else n]) for n in BOUND}
+    assert all(off[n] <= BOUND[n] for n in BOUND), off
