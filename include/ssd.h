@@ -544,8 +544,8 @@ ssd_status ssd_conv1d_step(const ssd_conv_problem *prob, const void *u, int64_t 
  * tokens before it, too: of all that lie in its chunk of 64.  Padding inside a batch row holds finite values, or lies outside
  * cu_seqlens.  headdim and dstate 1..256, else SSD_ERR_UNSUPPORTED.
  *
- * It is computed in chunks of 64 tokens.  f32 data, and calls of up to 256 tokens times heads: fp32 arithmetic throughout.
- * Other bf16 data with headdim and dstate up to 128: tensor cores with fp32 accumulation; what is carried from chunk to chunk goes into them as the
+ * It is computed in chunks of 64 tokens.  f32 data, calls of up to 256 tokens times heads, and dstate below 8: fp32 arithmetic
+ * throughout.  Other bf16 data with headdim and dstate up to 128: tensor cores with fp32 accumulation; what is carried from chunk to chunk goes into them as the
  * sum of two bf16 values (2^-17), so that states are right to fp32's measure (about 1e-5); outputs and gradients
  * are sums of products of bf16 operands (each rounded once, 2^-9), whatever type g, beta and their gradients have.
  *

@@ -73,10 +73,13 @@ ssd_status check_inputs(const ssd_delta_problem *p, const ssd_delta_args *a) {
 // heads: dg and dbeta are sums over a head's values and keys, and where there are only a few of them that happen to be small, the
 // roundings of bf16 operands do not average out.  (In 220 calls of 1 to 30000 tokens and heads dbeta or dg was off by more than 5e-3, up
 // to 1.3e-2, in three, of 3, 7 x 2 and 9; in fp32 by 2e-3, their own rounding.  One chunk takes 22 to 27 us in fp32, 14 on the
-// tensor cores.)
-constexpr int64_t kFewTokens = 256;
+// tensor cores.)  And so are keys of fewer than eight features: what one token has taken up the next ones take back for the most part, the
+// sums of att W cancel, and their operands' roundings do not (o, dq and dg of 640 tokens, one feature: off by 1.0e-2, 1.1e-2, 1.3e-2; four:
+// 5.9e-3; eight: 4.3e-3, 4.5e-3, 4.0e-3; from 64 on 2.8e-3).  8192 tokens of 32 heads x 128 values, four features, forward and backward: 1204
+// and 2082 us on the tensor cores, whose tiles no tensor map fills then, 1109 and 2860 in fp32; eight features 234 and 646, and 815 and 2391.
+constexpr int64_t kFewTokens = 256, kFewKeys = 8;
 bool on_tensor_cores(const ssd_delta_problem *p) {
-    return p->dtype == SSD_BF16 && p->headdim <= 128 && p->dstate <= 128 && p->batch * p->seqlen * p->nheads > kFewTokens;
+    return p->dtype == SSD_BF16 && p->headdim <= 128 && p->dstate <= 128 && p->dstate >= kFewKeys && p->batch * p->seqlen * p->nheads > kFewTokens;
 }
 
 // What the forward keeps and the backward starts from: the state that enters each chunk, U, and on the tensor cores the chunks'

@@ -32,3 +32,20 @@ def test_errors_are_those_of_the_roundings(B, L, G, H, V, K, lens, kept):
     got = dict(d, o=o, f=f)
     off = {n: t.rel(got[n], w["final" if n == "f" else n]) for n in BOUND}
     assert all(off[n] <= BOUND[n] for n in BOUND), off
+
+
+@pytest.mark.parametrize("K", [1, 2, 3, 5, 7, 8])
+@pytest.mark.parametrize("B,L,G,H,V,lens", [(1, 640, 4, 4, 64, None), (3, 65, 1, 3, 1, None), (1, 129, 3, 6, 128, [27, 13, 57, 6, 11, 8, 7])])
+def test_few_features_of_the_keys(B, L, G, H, V, lens, K):
+    """Keys that point the same way take back what the one before has written: outputs and gradients are differences.  The bounds are
+    those of all sizes (test_gpu_delta.py)."""
+    x = t.make(B, L, G, H, V, K, BF16, F32, lens and len(lens), F32, seed=3, train=True)
+    cu = None if lens is None else t.packed(lens)
+    a = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    o, f, states = pkg.gated_delta_forward(*a, initial_states=x["init"], cu_seqlens=cu, keep_chunk_states=True)
+    d = pkg.gated_delta_backward(*a, x["do"], initial_states=x["init"], dfinal_states=x["dfinal"], cu_seqlens=cu, chunk_states=states)
+    w = t.want(x, K ** -0.5, None if cu is None else cu.tolist(), back=True)
+    assert t.rel(o, w["o"]) <= t.OUT[BF16] and t.rel(f, w["final"]) <= t.OUT[F32]
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert t.rel(d[n], w[n]) <= t.GRAD[BF16], n
+    assert t.rel(d["dinitial_states"], w["dinit"]) <= t.GRAD[BF16]
