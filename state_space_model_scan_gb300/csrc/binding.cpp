@@ -616,7 +616,7 @@ PyObject *delta_bwd(PyObject *const *a) {
                    delta_grad_names);
 }
 
-// ---- autograd: nodes of their own, since a Python function's way into the graph and back takes 80 us of host time a step
+// ---- autograd: nodes of their own, since a Python function's way into the graph and back takes 20 to 50 us of host time more a step
 namespace ag = torch::autograd;
 
 // What a node does under the interpreter's lock; a Python exception goes on as the engine carries those.

@@ -13,7 +13,9 @@
 // little arithmetic and one tcgen05.st, and no shared memory is written.  The state stays in registers, in fp32.
 // What is carried (S, Y, e^(Gc - G) beta U, sys) enters a product as the sum of two bf16 values (2^-17), two or three products of
 // which the small ones are the cheaper price than tf32's single one of half the rate and 2^-11; what only leaves as bf16
-// (att, beta U in o) as one: o is off by 2.6e-3, of which its own rounding is 1.7e-3 (beta U as two took 6% more time for 2.2e-3).
+// (att, beta U in o) as one: o is off by 2.6e-3, of which its own rounding is 1.7e-3 (beta U as two took 6% more time for 2.2e-3).  Where keys point
+// much the same way and little is forgotten, a token's U takes back what the ones before have written, att W is a sum that cancels, and those
+// roundings count for more: 5.8e-3 at a mean cosine of 0.5, 8.9e-3 at 0.95 (by arithmetic in 64 bits: 6e-3 with beta U or att as two, 1.7e-3 with both).
 // Backwards the same chain runs from the last chunk to the first, with dS in S's place and the transposed inverse in sys's: k_prep
 // leaves both for it, which come of one substitution, and nothing of the chunks is computed twice.
 //
@@ -26,7 +28,7 @@
 // Bound by latency: a step of a chunk is three products in a row with arithmetic between them, about 2.6 us, of which the products are 40% and the
 // rest are splits, loads and stores of tensor memory at two warps a scheduler; the launch's first step comes 7 us late (first
 // copies, tensor memory, cold code).  8192 tokens of 32 heads, 128 x 128: k_prep 50 us, chains 117 + 67 (34.6 GF, 204 MB: 18 and 30 us);
-// 2 x 2048 tokens forwards 31 + 96 us, backwards 102, k_grads 78 (294 MB, 3.8 TB/s).
+// 2 x 2048 tokens forwards 31 + 96 us, backwards 102, k_grads 80 (294 MB, 3.7 TB/s).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
