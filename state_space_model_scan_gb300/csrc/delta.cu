@@ -69,15 +69,17 @@ ssd_status check_inputs(const ssd_delta_problem *p, const ssd_delta_args *a) {
     return SSD_OK;
 }
 
-// The tensor-core path takes bf16 data of up to 128 values and keys; fp32 data is computed in fp32, and so are calls of few tokens and
-// heads: dg and dbeta are sums over a head's values and keys, and where there are only a few of them that happen to be small, the
-// roundings of bf16 operands do not average out.  (In 220 calls of 1 to 30000 tokens and heads dbeta or dg was off by more than 5e-3, up
-// to 1.3e-2, in three, of 3, 7 x 2 and 9; in fp32 by 2e-3, their own rounding.  The border lies well above those: of 425 calls of 1 to
-// 60000 none was off by more than 4.0e-3 then.  A chunk of 128 x 128 on either side of it, forwards, and forwards and backwards: one head 29 and
-// 100 us in fp32, 32 heads 37 and 115, on the tensor cores 17 and 41.)  And so are keys of fewer than eight features: what one token has taken up the next ones take back for the most part, the
-// sums of att W cancel, and their operands' roundings do not (o, dq and dg of 640 tokens, one feature: off by 1.0e-2, 1.1e-2, 1.3e-2; four:
-// 5.9e-3; eight: 4.3e-3, 4.5e-3, 4.0e-3; from 64 on 2.8e-3).  8192 tokens of 32 heads x 128 values, four features, forward and backward: 1204
-// and 2082 us on the tensor cores, whose tiles no tensor map fills then, 1109 and 2860 in fp32; eight features 234 and 646, and 815 and 2391.
+// The tensor-core path takes bf16 data of up to 128 values and keys; fp32 data is computed in fp32, and so are
+// - calls of few tokens and heads: dg and dbeta are sums over a head's values and keys, and where there are only a few of them that happen
+//   to be small, the roundings of bf16 operands do not average out.  (In 220 calls of 1 to 30000 tokens and heads dbeta or dg was off by
+//   more than 5e-3, up to 1.3e-2, in three, of 3, 7 x 2 and 9; in fp32 by 2e-3, their own rounding.  The border lies well above those: of
+//   425 calls of 1 to 60000 none was off by more than 4.0e-3 then.  A chunk of 128 x 128 on either side of it, forwards, and forwards and
+//   backwards: one head 29 and 100 us in fp32, 32 heads 37 and 115, on the tensor cores 17 and 41.)
+// - keys of fewer than eight features: what one token has taken up the next ones take back for the most part, the sums of att W cancel,
+//   and their operands' roundings do not.  (o, dq and dg of 640 tokens, one feature: off by 1.0e-2, 1.1e-2, 1.3e-2; four: 5.9e-3, 5.9e-3,
+//   5.3e-3; eight: 4.3e-3, 4.5e-3, 4.0e-3; from 64 on 2.8e-3.  8192 tokens of 32 heads x 128 values, four features, forward, and backward with
+//   its forward: 1204 and 2082 us on the tensor cores, where no tensor map fills the tiles, 1109 and 2860 in fp32; eight features 234 and
+//   646 on the tensor cores, 815 and 2391 as fp32 data.)
 constexpr int64_t kFewTokens = 256, kFewKeys = 8;
 bool on_tensor_cores(const ssd_delta_problem *p) {
     return p->dtype == SSD_BF16 && p->headdim <= 128 && p->dstate <= 128 && p->dstate >= kFewKeys && p->batch * p->seqlen * p->nheads > kFewTokens;

@@ -292,7 +292,8 @@ __global__ void __launch_bounds__(PREP_NT, 6) k_prep(const DeltaArgs a, const __
     fence_proxy_async_smem();
     __syncthreads();
     if (w == 0) {
-        if (!ok) mbar_wait(bar + 1, 0);                      // (nor is the product)
+        if (!ok) mbar_wait(bar + 1, 0);                      // the product is not on its way when the tensor memory is given up
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 64);
     }
@@ -1156,7 +1157,7 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
     issue_kq(c, unit % a.G, sm + G_KQ);
     issue(c, unit / a.G, unit % a.G * per);
     // After a wait has run out the block leaves both loops at the next head's start.  (The word beside the tensor memory's address is written
-    // before one barrier and read behind it, by all threads alike; a barrier that gathers it, and waits that look at it, took 12 us of 78 more.)
+    // before one barrier and read behind it, by all threads alike: 80 us where none left took 78, and a barrier that gathers it with waits that look at it 90.)
     bool ok = true, left = false;
     const uint32_t base = smem_u32(sm), A = base + G_A, U = base + G_U, S = base + G_S, dS = base + G_DS, EF = base + G_EF, Z = base + G_Z;
     const int row = (w & 3) * 32 + lane, i = row & 63, qu = w >> 2, j0 = 16 * qu;
@@ -1414,6 +1415,7 @@ __global__ void __launch_bounds__(GR_NT, 1) k_grads(const DeltaArgs a, const __g
         mbar_wait(bar + L_KQ, (left ? nu : nu - 1) & 1);
         mbar_wait(bar + L_HEAD, (left ? it : it - 1) & 1);
         if (it > 0) mbar_wait(bar + L_D4, (it - 1) & 1);
+        __syncwarp();
     }
     if (w == 0) {
         tc_fence_after();
