@@ -137,3 +137,34 @@ def test_saved_tensor_hooks_and_checkpoints():
         out = f(*x)
     assert same(want, torch.autograd.grad(total(out), x))
     assert same(want, torch.autograd.grad(total(torch.utils.checkpoint.checkpoint(f, *x, use_reentrant=False)), x))
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_a_captured_step_through_autograd(op):
+    """Forward and backward captured into a CUDA graph and replayed on new values; meanwhile an eager graph of other leaves lives."""
+    f, make = OPS[op]
+    x, y = make(1), make(2)
+    other = f.apply(*make(3))
+    want = []
+    for src in (x, y):
+        out = f.apply(*src)
+        want.append(([o.detach() for o in out], torch.autograd.grad(total(out), src)))
+        del out
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(total(f.apply(*x)), x)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = f.apply(*x)
+        d = torch.autograd.grad(total(out), x)
+    for src, (o, g) in ((y, want[1]), (make(1), want[0])):
+        with torch.no_grad():
+            for s, t in zip(x, src):
+                s.copy_(t)
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert same([t.detach() for t in out], o) and same(d, g)
+    assert all(torch.isfinite(t).all() for t in other)
